@@ -69,6 +69,7 @@ typedef enum {
 #define PA_DEV_TIMEOUT   0x8u  /* a pipeline wait gave up after its time limit */
 #define PA_DEV_BAD_Q     0x10u /* a q value outside the fp16 range (|q| >= 65520 or NaN) */
 #define PA_DEV_BAD_POS   0x20u /* kv_store_norm_rope: a position outside the rotation table */
+#define PA_DEV_NO_BLOCKS 0x40u /* build_block_tables: the free list ran out */
 
 /* Flags of pa_paged_attention / pa_paged_attention_ex. */
 #define PA_ATTN_NON_CAUSAL   0x1u  /* every query of a sequence sees all of its seq_len keys */
@@ -340,6 +341,161 @@ pa_status pa_paged_attention_f8v4(const void *q, const void *k_cache, const void
 pa_status pa_merge_attn_states(const void *out_a, const float *lse_a, const void *out_b,
                                const float *lse_b, void *out, float *lse, int64_t num_rows,
                                int32_t head_dim, void *stream);
+
+/*
+ * build_block_tables -- a serving step's block table, slot map, positions and
+ * length arrays, formed on the device from its request lengths: what
+ * pa_kv_store (slot_mapping), pa_kv_store_norm_rope (positions) and
+ * pa_paged_attention (cu_seqlens_q, seq_lens, block_table) take, with no
+ * host round trip.
+ * Passage: "attention_impl.py" (the metadata of a forward pass: slot_mapping,
+ * block_table, query_start_loc, seq_lens); the pages build it on the host.
+ *
+ * Sequence s has context_lens[s] tokens in the cache (c), whose pages row
+ * source_rows[s] of source_table holds, and query_lens[s] new ones (q):
+ *   seq_lens[s]     = c + q
+ *   cu_seqlens_q[s] = sum of q before s;  cu_seqlens_q[num_seqs] = their sum
+ *   block_table[s][p], p < ceil(c / bs):  the source row's entry p
+ *   block_table[s][p], ceil(c / bs) <= p < ceil((c + q) / bs): a new page, the
+ *                     next entry of free_blocks from *free_head on, in order of
+ *                     s, then p
+ *   positions[cu + i] = c + i, slot_mapping[cu + i] = the slot of that position
+ * Rows of slot_mapping behind the last token get -1 (a padding row of the
+ * stores), of positions 0.  Entries of block_table past ceil((c + q) / bs)
+ * are left as they were.
+ *
+ *   source_table  int32 [num_source_rows][source_table_stride].
+ *   source_rows   int32 [num_seqs] or NULL: row s.  Several sequences may name
+ *                 one row (samples forked off one prompt).
+ *   shared_lens   int32 [num_seqs] or NULL: how many leading tokens of s stand
+ *                 in pages that other sequences read too.  Where the first new
+ *                 token would go into such a page (c % bs != 0, q > 0 and
+ *                 shared_lens[s] > c - c % bs), s gets a new page in its place
+ *                 and copy_pairs[s] = (old, new): copy it with pa_copy_blocks
+ *                 before the store.  Needs copy_pairs.
+ *   free_blocks   int32 [num_free] page ids, dealt in order; free_head int32
+ *                 device word, the first entry not dealt yet (NULL: 0);
+ *                 *next_free = the next one after this call (NULL: not wanted).
+ *   block_table   int32 [num_seqs][block_table_stride] (written).  It may be
+ *                 source_table itself (same stride, source_rows NULL): then
+ *                 only new entries are written.
+ *   positions     int64 [num_tokens] or NULL; slot_mapping int64 [num_tokens].
+ *   num_tokens    rows of slot_mapping: at least the sum of q (host bound).
+ *   copy_pairs    int32 [num_seqs][2] or NULL; (-1, -1) where nothing is to copy.
+ * Apart from that one case no output may overlap an input or another output
+ * (PA_ERR_INVALID_ARG); keep two words for free_head / next_free and two
+ * arrays for context_lens / seq_lens and swap them from step to step.
+ * Device checks (status): a negative length, a q above num_tokens or a source
+ * row out of range with c > 0 (PA_DEV_BAD_SEQ: that sequence counts as
+ * empty, or without old pages); more tokens than num_tokens (PA_DEV_BAD_SEQ:
+ * the rest is not written); a page past block_table_stride, a token whose old
+ * page or a free entry outside [0, num_blocks) (PA_DEV_BAD_BLOCK: slot -1); the
+ * free list used up (PA_DEV_NO_BLOCKS: entry and slots -1, *next_free still
+ * counts the pages wanted).  With num_seqs == 0 every row is padding and no
+ * page is dealt.  block_size 16 or 32; at most 2^25 sequences, tokens and table
+ * columns.  Asynchronous.
+ */
+pa_status pa_build_block_tables(const int32_t *context_lens, const int32_t *query_lens,
+                                int32_t num_seqs, const int32_t *source_table,
+                                int32_t source_table_stride, int32_t num_source_rows,
+                                const int32_t *source_rows, const int32_t *shared_lens,
+                                const int32_t *free_blocks, int32_t num_free,
+                                const int32_t *free_head, int32_t num_blocks, int32_t block_size,
+                                int32_t *block_table, int32_t block_table_stride,
+                                int32_t *cu_seqlens_q, int32_t *seq_lens, int64_t *slot_mapping,
+                                int64_t *positions, int32_t num_tokens, int32_t *copy_pairs,
+                                int32_t *next_free, uint32_t *status, void *stream);
+
+/*
+ * copy_blocks -- whole blocks of a q8 cache (all its kv heads, codes and
+ * scales) copied to other blocks of it: the pages that a fork made private
+ * (copy_pairs of pa_build_block_tables), or pages moved together.
+ *
+ *   copy_pairs  int32 [num_pairs][2], 8-byte aligned: (source, destination)
+ *               block ids.  A pair with a negative id, or with equal ids, is
+ *               skipped; an id past num_blocks is flagged PA_DEV_BAD_BLOCK and
+ *               its pair skipped.  One source may go to several destinations;
+ *               a block that is the destination of two pairs, or of one pair
+ *               and the source of another, has undefined contents afterwards.
+ * num_pairs == 0 is a no-op.  Asynchronous.
+ */
+pa_status pa_copy_blocks(const int32_t *copy_pairs, int32_t num_pairs, int32_t num_kv_heads,
+                         int32_t head_dim, void *k_cache, void *k_scale, void *v_cache,
+                         void *v_scale, int32_t num_blocks, int32_t block_size, uint32_t *status,
+                         void *stream);
+
+/* The same for a cache in the fp8 / 4-bit format. */
+pa_status pa_copy_blocks_f8v4(const int32_t *copy_pairs, int32_t num_pairs, int32_t num_kv_heads,
+                              int32_t head_dim, void *k_cache, void *v_cache, void *v_scale,
+                              void *v_zero, int32_t num_blocks, int32_t block_size,
+                              uint32_t *status, void *stream);
+
+/*
+ * Bytes of workspace pa_paged_attention_shared_prefix uses for these bounds:
+ * 256 bytes of header (the status word at offset 0) plus an fp32 triple of
+ * head_dim + 2 for every query row (num_tokens * num_q_heads) and key segment.
+ * 256 for sizes out of range.
+ */
+size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t max_query_len, int32_t max_prefix_len,
+                                       int32_t max_suffix_len);
+
+/*
+ * paged_attention_shared_prefix -- causal attention over the q8 cache for a
+ * batch whose sequences stand in groups that share a prefix; the prefix is
+ * read and multiplied once for all queries of its group.
+ * Passage: "shared/attention_kit.py" (`_attend_with_prefix`: the cached prefix
+ * in a pass of its own, merged by LSE), over the batch of
+ * "triton_turboquant_unified_attention.py".  The result is that of
+ * pa_paged_attention_ex (causal, no window) over the same batch.
+ *
+ *   cu_groups     int32 [num_groups + 1]: group g owns sequences
+ *                 [cu_groups[g], cu_groups[g + 1]); cu_groups[0] = 0,
+ *                 non-decreasing, cu_groups[num_groups] = num_seqs.
+ *   prefix_lens   int32 [num_groups]: the first prefix_lens[g] keys of every
+ *                 sequence of g are the same, and are read through the
+ *                 block-table row of the group's first sequence.  Any length
+ *                 from 0 (nothing shared) to seq_len - q_len of each of its
+ *                 sequences; it need not end with a page.  A sequence on its
+ *                 own is a group of one.
+ *   max_query_len, max_prefix_len, max_suffix_len
+ *                 host bounds of q_len, of prefix_lens and of seq_len - prefix
+ *                 (never synced): they size the key segments and choose kernels;
+ *                 any positive value (max_prefix_len: not negative) gives
+ *                 correct results.
+ *   workspace     device buffer, 16-byte aligned, its first 4 bytes the status
+ *                 word (zero it once).  pa_shared_prefix_workspace_size bytes;
+ *                 a smaller one takes fewer key segments, down to 256 bytes +
+ *                 two triples per query row (less: PA_ERR_INVALID_ARG).  Calls
+ *                 that may overlap on the GPU need workspaces of their own.
+ *   flags         0.
+ * Other arguments as pa_paged_attention_ex.  A sequence whose seq_len - q_len
+ * is below its prefix, that no group holds, or whose metadata is out of range
+ * is not written and flagged PA_DEV_BAD_SEQ; rows of tokens no sequence owns
+ * are not written.  Numerics as pa_paged_attention_ex; the parts are joined in
+ * fp32.  Asynchronous.
+ */
+pa_status pa_paged_attention_shared_prefix(
+    const void *q, const void *k_cache, const void *k_scale, const void *v_cache,
+    const void *v_scale, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, const int32_t *cu_groups,
+    const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs, int32_t num_tokens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+    int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
+    float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
+    size_t workspace_bytes, uint32_t flags, void *stream);
+
+/* The same over the fp8 / 4-bit format. */
+pa_status pa_paged_attention_shared_prefix_f8v4(
+    const void *q, const void *k_cache, const void *v_cache, const void *v_scale,
+    const void *v_zero, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, const int32_t *cu_groups,
+    const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs, int32_t num_tokens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+    int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
+    float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
+    size_t workspace_bytes, uint32_t flags, void *stream);
 
 /*
  * Synchronizes `stream`, reads the device status word at `status` (a kv_store

@@ -6,7 +6,10 @@ the q8 format (int8 codes, one fp16 scale per token, kv head and 32 channels)
 and scatters them into a block-paged cache; ``paged_attention`` runs unified
 causal prefill + decode over that cache and returns bf16 output and fp32 LSE;
 ``merge_attn_states`` merges two such results over disjoint key sets by their
-LSEs.
+LSEs.  For batches whose requests share prompts, ``build_block_tables`` forms
+a step's tables and slot map on the device, ``copy_blocks`` fills the pages a
+fork made private, and ``paged_attention_shared_prefix`` computes each shared
+prefix once.
 
 Importing the package does not load the CUDA library; the first call does, and
 fails loudly if it has not been built.
@@ -15,7 +18,9 @@ from __future__ import annotations
 
 __all__ = ["kv_store", "kv_store_norm_rope", "kv_store_f8v4", "paged_attention",
            "paged_attention_f8v4", "paged_attention_noalloc", "merge_attn_states",
-           "workspace_size", "check_status",
+           "build_block_tables", "BlockTables", "copy_blocks", "copy_blocks_f8v4",
+           "paged_attention_shared_prefix", "paged_attention_shared_prefix_f8v4",
+           "shared_prefix_workspace_size", "workspace_size", "check_status",
            "auto_num_splits", "Status", "PagedAttentionError", "library_path"]
 
 

@@ -11,6 +11,7 @@ import ctypes
 import enum
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -35,6 +36,7 @@ DEV_BAD_SEQ = 0x4
 DEV_TIMEOUT = 0x8
 DEV_BAD_Q = 0x10
 DEV_BAD_POS = 0x20
+DEV_NO_BLOCKS = 0x40
 
 ATTN_NON_CAUSAL = 0x1
 ATTN_TEST_TIMEOUT = 0x80000000
@@ -94,6 +96,18 @@ def load():
         lib.pa_paged_attention_noalloc.restype = ctypes.c_int
         lib.pa_merge_attn_states.argtypes = [P, P, P, P, P, P, i64, i32, P]
         lib.pa_merge_attn_states.restype = ctypes.c_int
+        lib.pa_build_block_tables.argtypes = [P, P, i32, P, i32, i32, P, P, P, i32, P, i32, i32, P,
+                                              i32, P, P, P, P, i32, P, P, P, P]
+        lib.pa_build_block_tables.restype = ctypes.c_int
+        for fn in (lib.pa_copy_blocks, lib.pa_copy_blocks_f8v4):
+            fn.argtypes = [P, i32, i32, i32, P, P, P, P, i32, i32, P, P]
+            fn.restype = ctypes.c_int
+        lib.pa_shared_prefix_workspace_size.argtypes = [i32] * 9
+        lib.pa_shared_prefix_workspace_size.restype = ctypes.c_size_t
+        for fn in (lib.pa_paged_attention_shared_prefix, lib.pa_paged_attention_shared_prefix_f8v4):
+            fn.argtypes = [P] * 8 + [i32, P, P] + [i32] * 11 + [
+                ctypes.c_float, P, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
+            fn.restype = ctypes.c_int
         lib.pa_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.pa_check_status.restype = ctypes.c_int
         lib.pa_status_string.argtypes = [ctypes.c_int]
@@ -483,6 +497,275 @@ def merge_attn_states(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=Non
                                          _ptr(out), _ptr(lse), rows, d, _stream(stream, device))
     _raise_if(st)
     return (out, lse) if return_lse else out
+
+
+# The calls of a serving step are made once a step or a layer on small batches
+# too, where the host's share counts: their bindings look each attribute up
+# once and enter the tensors' device only when another one is current.
+
+def _call(fn, device, *args):
+    """fn(*args), with `device` current."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        _raise_if(st)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _handle(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _check_i32(device, **tensors):
+    """Contiguous int32 CUDA tensors on `device` (None passes)."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{name} must be int32")
+        if t.device != device:
+            raise ValueError(f"all tensors must be CUDA tensors on one device: {name} on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+class BlockTables(NamedTuple):
+    """What build_block_tables returns: the arrays the stores and the
+    attention of this step take, the pages to copy before the store, and the
+    free list's next entry."""
+    block_table: torch.Tensor    # int32 [S, columns]
+    cu_seqlens_q: torch.Tensor   # int32 [S + 1]
+    seq_lens: torch.Tensor       # int32 [S]
+    slot_mapping: torch.Tensor   # int64 [num_tokens], -1 on padding rows
+    positions: torch.Tensor      # int64 [num_tokens]
+    copy_pairs: torch.Tensor     # int32 [S, 2], -1 where nothing is to copy
+    next_free: torch.Tensor      # int32 [1]
+
+
+def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_blocks: int,
+                       block_size: int, num_tokens: int, source_rows=None, shared_lens=None,
+                       free_head=None, out=None, status=None, stream=None) -> BlockTables:
+    """A step's block table, slot map, positions and lengths from its request
+    lengths, on the device (pa_build_block_tables).
+
+    ``context_lens`` / ``query_lens`` int32 [S]: tokens in the cache and new
+    ones; ``source_table`` int32 [R, columns]: the pages held so far, at row
+    ``source_rows[s]`` (int32 [S]; None: row s).  New pages come from
+    ``free_blocks`` (int32) from entry ``free_head`` (int32 [1]; None: 0) on.
+    ``shared_lens`` int32 [S]: leading tokens in pages that others read too; a
+    sequence about to write into such a page gets a private one, and
+    ``copy_pairs`` names the copy to make (copy_blocks).  ``num_tokens``: rows
+    of the slot map (host bound of the new tokens; the rest is padding).
+    ``out``: a BlockTables (or tuple in its order) to write into; its
+    ``block_table`` may be ``source_table`` itself (source_rows None), the
+    only allowed overlap.  ``status``: optional int32 CUDA tensor, zeroed."""
+    if not context_lens.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    device = context_lens.device
+    s = context_lens.shape[0]
+    if context_lens.dim() != 1 or query_lens.shape != (s,):
+        raise ValueError("context_lens and query_lens must be [S]")
+    if source_table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("source_table must be [R, columns] and free_blocks [num_free]")
+    if num_tokens < 0:
+        raise ValueError("num_tokens < 0")
+    if out is None:
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
+        out = (torch.full((s, source_table.shape[1]), -1, dtype=torch.int32, device=device),
+               new(s + 1, torch.int32), new(s, torch.int32), new(num_tokens, torch.int64),
+               new(num_tokens, torch.int64), new((s, 2), torch.int32), new(1, torch.int32))
+    out = BlockTables(*out)
+    table, cu, lens, slots, pos, pairs, nxt = out
+    _check_i32(device, context_lens=context_lens, query_lens=query_lens, source_table=source_table,
+               source_rows=source_rows, shared_lens=shared_lens, free_blocks=free_blocks,
+               free_head=free_head, block_table=table, cu_seqlens_q=cu, seq_lens=lens,
+               copy_pairs=pairs, next_free=nxt, status=status)
+    for name, t in (("slot_mapping", slots), ("positions", pos)):
+        if t is None and name == "positions":
+            continue
+        if t.dtype is not torch.int64 or t.device != device or t.shape != (num_tokens,) \
+                or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous int64 CUDA tensor [num_tokens]")
+    if table.dim() != 2 or table.shape[0] != s:
+        raise ValueError("block_table must be [S, columns]")
+    if cu.shape != (s + 1,) or lens.shape != (s,) or (pairs is not None and pairs.shape != (s, 2)):
+        raise ValueError("cu_seqlens_q [S + 1], seq_lens [S] and copy_pairs [S, 2] are wanted")
+    for name, t in (("source_rows", source_rows), ("shared_lens", shared_lens)):
+        if t is not None and t.shape != (s,):
+            raise ValueError(f"{name} must be [S]")
+    for name, t in (("free_head", free_head), ("next_free", nxt), ("status", status)):
+        if t is not None and t.numel() < 1:
+            raise ValueError(f"{name} must hold a value")
+    _call(load().pa_build_block_tables, device, context_lens.data_ptr(), query_lens.data_ptr(), s,
+          source_table.data_ptr(), source_table.shape[1], source_table.shape[0],
+          _addr(source_rows), _addr(shared_lens), free_blocks.data_ptr(), free_blocks.shape[0],
+          _addr(free_head), num_blocks, block_size, table.data_ptr(), table.shape[1],
+          cu.data_ptr(), lens.data_ptr(), slots.data_ptr(), _addr(pos), num_tokens, _addr(pairs),
+          _addr(nxt), _addr(status), _handle(stream, device))
+    return out
+
+
+def _copy_args(copy_pairs, status, arrays):
+    if not copy_pairs.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    device = copy_pairs.device
+    _check_i32(device, copy_pairs=copy_pairs, status=status)
+    if copy_pairs.dim() != 2 or copy_pairs.shape[1] != 2:
+        raise ValueError("copy_pairs must be [N, 2]")
+    for t in arrays:
+        if t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("caches must be contiguous")
+    return device
+
+
+def copy_blocks(copy_pairs, k_cache, k_scale, v_cache, v_scale, status=None, stream=None) -> None:
+    """Copy whole blocks of a q8 cache to other blocks of it
+    (pa_copy_blocks): ``copy_pairs`` int32 [N, 2] of (source, destination),
+    pairs with a negative id skipped.  Destinations must be distinct and no
+    pair's source."""
+    device = _copy_args(copy_pairs, status, (k_cache, k_scale, v_cache, v_scale))
+    if k_cache.dtype is not torch.int8 or v_cache.dtype is not torch.int8:
+        raise TypeError("caches must be int8")
+    _check16("k_scale", k_scale)
+    _check16("v_scale", v_scale)
+    _check_cache_shapes(k_cache, k_scale, v_cache, v_scale)
+    nb, hk, bs, d = k_cache.shape
+    _call(load().pa_copy_blocks, device, copy_pairs.data_ptr(), copy_pairs.shape[0], hk, d,
+          k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), nb, bs,
+          _addr(status), _handle(stream, device))
+
+
+def copy_blocks_f8v4(copy_pairs, k_cache, v_cache, v_scale, v_zero, status=None,
+                     stream=None) -> None:
+    """copy_blocks over the fp8 / 4-bit format (pa_copy_blocks_f8v4)."""
+    device = _copy_args(copy_pairs, status, (k_cache, v_cache, v_scale, v_zero))
+    _check_f8v4_shapes(k_cache, v_cache, v_scale, v_zero)
+    nb, hk, bs, d = k_cache.shape
+    _call(load().pa_copy_blocks_f8v4, device, copy_pairs.data_ptr(), copy_pairs.shape[0], hk, d,
+          k_cache.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), v_zero.data_ptr(), nb, bs,
+          _addr(status), _handle(stream, device))
+
+
+def shared_prefix_workspace_size(num_seqs: int, num_tokens: int, num_groups: int,
+                                 num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                 max_query_len: int, max_prefix_len: int,
+                                 max_suffix_len: int) -> int:
+    """Bytes of workspace paged_attention_shared_prefix uses for these bounds."""
+    return int(load().pa_shared_prefix_workspace_size(
+        num_seqs, num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim, max_query_len,
+        max_prefix_len, max_suffix_len))
+
+
+def _shared_prefix(fn, q, k_cache, four, hk, nb, bs, cu_seqlens_q, seq_lens, block_table,
+                   cu_groups, prefix_lens, max_query_len, max_prefix_len, max_suffix_len,
+                   softmax_scale, sinks, out, lse, workspace, stream, return_lse):
+    if not q.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    device = q.device
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        raise TypeError("q must be a contiguous bf16 tensor [T, Hq, D]")
+    t, hq, d = q.shape
+    if k_cache.shape[3] != d:
+        raise ValueError("cache shape mismatch")
+    for x in four:
+        if x.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {x.device}")
+        if not x.is_contiguous():
+            raise ValueError("caches must be contiguous")
+    _check_i32(device, cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens, cu_groups=cu_groups,
+               prefix_lens=prefix_lens)
+    if block_table.dtype is not torch.int32 or block_table.device != device:
+        raise TypeError(f"block_table must be an int32 CUDA tensor on {device}")
+    s, g = seq_lens.shape[0], prefix_lens.shape[0]
+    if block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be [S, max_blocks] with unit column stride")
+    if cu_seqlens_q.shape != (s + 1,) or block_table.shape[0] != s or cu_groups.shape != (g + 1,):
+        raise ValueError("cu_seqlens_q [S + 1], block_table [S, ...] and cu_groups [G + 1] are wanted")
+    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.shape != (hq,)
+                              or sinks.device != device or not sinks.is_contiguous()):
+        raise TypeError("sinks must be a contiguous fp32 CUDA tensor [num_q_heads]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype is not torch.bfloat16 or out.device != device \
+            or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 CUDA tensor shaped like q")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((t, hq), dtype=torch.float32, device=device)
+    elif lse.shape != (t, hq) or lse.dtype is not torch.float32 or lse.device != device \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 CUDA tensor [T, Hq]")
+    lib = load()
+    if workspace is None:
+        need = lib.pa_shared_prefix_workspace_size(s, t, g, hq, hk, d, max_query_len,
+                                                   max_prefix_len, max_suffix_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace[:4].zero_()
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    _call(fn(lib), device, q.data_ptr(), k_cache.data_ptr(), four[1].data_ptr(),
+          four[2].data_ptr(), four[3].data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+          block_table.data_ptr(), block_table.stride(0), cu_groups.data_ptr(),
+          prefix_lens.data_ptr(), g, s, t, hq, hk, d, nb, bs, max_query_len, max_prefix_len,
+          max_suffix_len, d ** -0.5 if softmax_scale is None else softmax_scale, _addr(sinks),
+          out.data_ptr(), _addr(lse), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), 0, _handle(stream, device))
+    return (out, lse) if return_lse else out
+
+
+def paged_attention_shared_prefix(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens,
+                                  block_table, cu_groups, prefix_lens, max_query_len: int,
+                                  max_prefix_len: int, max_suffix_len: int,
+                                  softmax_scale: float | None = None, sinks=None, out=None,
+                                  lse=None, workspace=None, stream=None, return_lse: bool = True):
+    """Causal paged attention of a batch whose groups of sequences share a
+    prefix, the prefix computed once per group
+    (pa_paged_attention_shared_prefix): the result of paged_attention.
+
+    ``cu_groups`` int32 [G + 1]: group g owns sequences cu_groups[g] ..
+    cu_groups[g + 1] - 1; ``prefix_lens`` int32 [G]: its first keys, the same
+    for all of them, read through the first sequence's row of ``block_table``
+    (0: nothing shared; at most seq_len - q_len of each).  ``max_*``: host
+    bounds of the query lengths, the prefixes and the keys past them.
+    ``workspace``: uint8 CUDA tensor of ``shared_prefix_workspace_size``
+    bytes, its first 4 bytes zero (the device status word); allocated when
+    omitted.  Other arguments and results as paged_attention."""
+    if k_cache.dtype is not torch.int8 or v_cache.dtype is not torch.int8:
+        raise TypeError("caches must be int8")
+    _check16("k_scale", k_scale)
+    _check16("v_scale", v_scale)
+    _check_cache_shapes(k_cache, k_scale, v_cache, v_scale)
+    nb, hk, bs, _ = k_cache.shape
+    return _shared_prefix(lambda lib: lib.pa_paged_attention_shared_prefix, q, k_cache,
+                          (k_cache, k_scale, v_cache, v_scale), hk, nb, bs, cu_seqlens_q, seq_lens,
+                          block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
+                          max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
+                          return_lse)
+
+
+def paged_attention_shared_prefix_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q,
+                                       seq_lens, block_table, cu_groups, prefix_lens,
+                                       max_query_len: int, max_prefix_len: int,
+                                       max_suffix_len: int, softmax_scale: float | None = None,
+                                       sinks=None, out=None, lse=None, workspace=None, stream=None,
+                                       return_lse: bool = True):
+    """paged_attention_shared_prefix over the fp8 / 4-bit format
+    (pa_paged_attention_shared_prefix_f8v4)."""
+    _check_f8v4_shapes(k_cache, v_cache, v_scale, v_zero)
+    nb, hk, bs, _ = k_cache.shape
+    return _shared_prefix(lambda lib: lib.pa_paged_attention_shared_prefix_f8v4, q, k_cache,
+                          (k_cache, v_cache, v_scale, v_zero), hk, nb, bs, cu_seqlens_q, seq_lens,
+                          block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
+                          max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
+                          return_lse)
 
 
 def check_status(status_tensor, stream=None) -> int:

@@ -2,10 +2,12 @@
 // declared, with its contract, in include/paq8.h.
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "launch.h"
 #include "merge.h"
+#include "serving.h"
 
 
 namespace {
@@ -404,6 +406,287 @@ const char *pa_status_string(pa_status s) {
 }
 
 const char *pa_last_error(void) { return g_last_error; }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Calls of a serving step whose sequences share prefixes.
+namespace {
+
+// Whether [a, a + an) and [b, b + bn) (bytes) share an address.
+bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an > 0 && bn > 0 && x < y + static_cast<uintptr_t>(bn) &&
+         y < x + static_cast<uintptr_t>(an);
+}
+
+bool misaligned(uintptr_t mask, std::initializer_list<const void *> ps) {
+  uintptr_t all = 0;
+  for (const void *p : ps) all |= reinterpret_cast<uintptr_t>(p);
+  return (all & mask) != 0;
+}
+
+pa_status copy_blocks(paq8::BlockCopy &p, const int32_t *copy_pairs, int32_t num_pairs,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                      int32_t block_size, void *const (&base)[4], const int64_t (&row_bytes)[4],
+                      uint32_t *status, void *stream) {
+  if (num_pairs < 0) return fail(PA_ERR_INVALID_ARG, "num_pairs < 0");
+  if (num_pairs == 0) return PA_OK;
+  if (!copy_pairs || !base[0] || !base[1] || !base[2] || !base[3])
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (num_kv_heads <= 0 || num_blocks <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_kv_heads and num_blocks must be positive");
+  if (!supported_dim(head_dim)) return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  if (!supported_bs(block_size)) return fail(PA_ERR_UNSUPPORTED, "block_size must be 16 or 32");
+  if (static_cast<int64_t>(num_blocks) * num_kv_heads * head_dim >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * head_dim must be < 2^31");
+  if (!aligned16(base[0]) || !aligned16(base[1]) || !aligned16(base[2]) || !aligned16(base[3]))
+    return fail(PA_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  if (misaligned(7, {copy_pairs})) return fail(PA_ERR_INVALID_ARG, "copy_pairs must be 8-byte aligned");
+  if (misaligned(3, {status})) return fail(PA_ERR_INVALID_ARG, "status must be 4-byte aligned");
+  p.pairs = copy_pairs;
+  p.num_pairs = num_pairs;
+  p.num_blocks = num_blocks;
+  int64_t bytes = 0;
+  for (int i = 0; i < 4; ++i) {
+    p.base[i] = static_cast<uint8_t *>(base[i]);
+    p.bytes[i] = row_bytes[i] * num_kv_heads;
+    bytes += p.bytes[i];
+  }
+  // a thread block takes 16 KB of one pair
+  if ((bytes / 16384 + 1) * num_pairs >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "too many bytes in one call: split the pairs");
+  p.status = status;
+  cudaError_t e = paq8::launch_copy_blocks(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+// Sizes of a shared-prefix call that both its workspace size and its launch
+// need; false: out of range.
+bool shared_sizes_ok(int32_t num_seqs, int32_t num_tokens, int32_t num_groups, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, int32_t max_query_len,
+                     int32_t max_prefix_len, int32_t max_suffix_len) {
+  return num_seqs > 0 && num_tokens > 0 && num_groups > 0 && num_q_heads > 0 &&
+         num_kv_heads > 0 && num_q_heads % num_kv_heads == 0 &&
+         num_q_heads / num_kv_heads <= 16 && supported_dim(head_dim) && max_query_len > 0 &&
+         max_prefix_len >= 0 && max_suffix_len > 0 && max_prefix_len <= 0x7fffffff - 4096 &&
+         max_suffix_len <= 0x7fffffff - 4096;
+}
+
+size_t shared_bytes(int32_t num_tokens, int32_t num_q_heads, int32_t head_dim, int32_t splits) {
+  return 256 + static_cast<size_t>(num_tokens) * num_q_heads * splits * (head_dim + 2) *
+                   sizeof(float);
+}
+
+pa_status shared_prefix(paq8::SharedLaunch &L, void *workspace, size_t workspace_bytes,
+                        uint32_t flags, void *stream) {
+  if (flags) return fail(PA_ERR_INVALID_ARG, "unknown flag bits");
+  if (L.num_seqs < 0 || L.num_tokens < 0 || L.num_groups < 0)
+    return fail(PA_ERR_INVALID_ARG, "negative size");
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "null workspace");
+  if (L.num_seqs == 0 || L.num_tokens == 0) return PA_OK;
+  if (!L.q || !L.k_cache || !L.k_scale || !L.v_cache || !L.v_scale || (L.f8v4 && !L.v_zero) ||
+      !L.cu || !L.seq_lens || !L.block_table || !L.cu_groups || !L.prefix_lens || !L.out)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (L.num_groups == 0) return fail(PA_ERR_INVALID_ARG, "num_groups must be positive");
+  if (L.hq <= 0 || L.hk <= 0 || L.hq % L.hk)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (L.hq / L.hk > 16) return fail(PA_ERR_UNSUPPORTED, "more than 16 q heads per kv head");
+  if (!supported_dim(L.d)) return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  if (!supported_bs(L.bs)) return fail(PA_ERR_UNSUPPORTED, "block_size must be 16 or 32");
+  if (L.num_blocks <= 0 || L.bt_stride <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_blocks and block_table_stride must be positive");
+  if (static_cast<int64_t>(L.num_blocks) * L.hk * L.d >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * head_dim must be < 2^31");
+  if (L.hk > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 kv heads");
+  if (!shared_sizes_ok(L.num_seqs, L.num_tokens, L.num_groups, L.hq, L.hk, L.d, L.max_query_len,
+                       L.max_prefix_len, L.max_suffix_len))
+    return fail(PA_ERR_INVALID_ARG,
+                "max_query_len and max_suffix_len must be positive, max_prefix_len not negative");
+  if (misaligned(15, {L.q, L.out, L.k_cache, L.v_cache, L.k_scale, L.v_scale, L.v_zero, workspace}))
+    return fail(PA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned(3, {L.lse, L.sinks, L.cu, L.seq_lens, L.block_table, L.cu_groups, L.prefix_lens}))
+    return fail(PA_ERR_INVALID_ARG, "lse, sinks and the int32 arrays must be 4-byte aligned");
+  paq8::SharedSplits n = paq8::shared_splits(L.num_seqs, L.num_tokens, L.num_groups, L.hq, L.hk,
+                                             L.d, L.max_query_len, L.max_prefix_len,
+                                             L.max_suffix_len);
+  // a smaller workspace takes fewer segments, down to one each
+  while (workspace_bytes < shared_bytes(L.num_tokens, L.hq, L.d, n.prefix + n.suffix) &&
+         n.prefix + n.suffix > 2) {
+    if (n.prefix >= n.suffix) --n.prefix;
+    else --n.suffix;
+  }
+  if (workspace_bytes < shared_bytes(L.num_tokens, L.hq, L.d, n.prefix + n.suffix))
+    return fail(PA_ERR_INVALID_ARG, "workspace too small: two fp32 triples for every query row");
+  L.prefix_splits = n.prefix;
+  L.suffix_splits = n.suffix;
+  L.workspace = static_cast<uint8_t *>(workspace);
+  cudaError_t e = paq8::launch_shared_prefix(L, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_build_block_tables(const int32_t *context_lens, const int32_t *query_lens,
+                                int32_t num_seqs, const int32_t *source_table,
+                                int32_t source_table_stride, int32_t num_source_rows,
+                                const int32_t *source_rows, const int32_t *shared_lens,
+                                const int32_t *free_blocks, int32_t num_free,
+                                const int32_t *free_head, int32_t num_blocks, int32_t block_size,
+                                int32_t *block_table, int32_t block_table_stride,
+                                int32_t *cu_seqlens_q, int32_t *seq_lens, int64_t *slot_mapping,
+                                int64_t *positions, int32_t num_tokens, int32_t *copy_pairs,
+                                int32_t *next_free, uint32_t *status, void *stream) {
+  g_last_error[0] = '\0';
+  if (num_seqs < 0 || num_tokens < 0 || num_free < 0 || num_source_rows < 0)
+    return fail(PA_ERR_INVALID_ARG, "negative size");
+  // no sequence: every row is padding, cu_seqlens_q[0] = 0, no page is dealt
+  if ((num_seqs > 0 && (!context_lens || !query_lens || !source_table || !block_table || !seq_lens)) ||
+      !cu_seqlens_q || (num_tokens > 0 && !slot_mapping) || (num_free > 0 && !free_blocks))
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (shared_lens && !copy_pairs)
+    return fail(PA_ERR_INVALID_ARG, "shared_lens needs copy_pairs: the private pages must be filled");
+  if (!supported_bs(block_size)) return fail(PA_ERR_UNSUPPORTED, "block_size must be 16 or 32");
+  if (num_blocks <= 0 || source_table_stride <= 0 || block_table_stride <= 0 ||
+      (num_source_rows == 0 && num_seqs > 0))
+    return fail(PA_ERR_INVALID_ARG, "num_blocks, num_source_rows and the table strides must be positive");
+  if (!source_rows && num_source_rows < num_seqs)
+    return fail(PA_ERR_INVALID_ARG, "fewer source rows than sequences, and no source_rows");
+  if (misaligned(3, {context_lens, query_lens, source_table, source_rows, shared_lens, free_blocks,
+                     free_head, block_table, cu_seqlens_q, seq_lens, copy_pairs, next_free, status}))
+    return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if (misaligned(7, {slot_mapping, positions}))
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping and positions must be 8-byte aligned");
+  if (num_seqs > (1 << 25) || num_tokens > (1 << 25) || block_table_stride > (1 << 25))
+    return fail(PA_ERR_UNSUPPORTED, "more than 2^25 sequences, tokens or table columns");
+  // every output apart from every input and every other output; the table may
+  // be the source table itself, row for row
+  const int64_t S = num_seqs, T = num_tokens;
+  const bool in_place = block_table == source_table && block_table_stride == source_table_stride &&
+                        !source_rows;
+  struct Span {
+    const void *p;
+    int64_t n;
+  };
+  const Span outs[] = {{block_table, 4 * S * block_table_stride}, {cu_seqlens_q, 4 * (S + 1)},
+                       {seq_lens, 4 * S}, {slot_mapping, 8 * T}, {positions, 8 * T},
+                       {copy_pairs, 8 * S}, {next_free, 4}};
+  const Span ins[] = {{in_place ? nullptr : source_table,
+                       4 * static_cast<int64_t>(num_source_rows) * source_table_stride},
+                      {context_lens, 4 * S}, {query_lens, 4 * S}, {source_rows, 4 * S},
+                      {shared_lens, 4 * S}, {free_blocks, 4 * static_cast<int64_t>(num_free)},
+                      {free_head, 4}};
+  for (const Span &o : outs) {
+    for (const Span &i : ins)
+      if (overlap(o.p, o.n, i.p, i.n))
+        return fail(PA_ERR_INVALID_ARG, "an output overlaps an input (only block_table may be source_table)");
+    for (const Span &q : outs)
+      if (&q != &o && overlap(o.p, o.n, q.p, q.n))
+        return fail(PA_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  paq8::BlockTables p;
+  p.context_lens = context_lens;
+  p.query_lens = query_lens;
+  p.num_seqs = num_seqs;
+  p.source_table = source_table;
+  p.source_stride = source_table_stride;
+  p.num_source_rows = num_source_rows;
+  p.source_rows = source_rows;
+  p.shared_lens = shared_lens;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.free_head = free_head;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.block_table = block_table;
+  p.table_stride = block_table_stride;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.num_tokens = num_tokens;
+  p.copy_pairs = copy_pairs;
+  p.next_free = next_free;
+  p.status = status;
+  cudaError_t e = paq8::launch_build_block_tables(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+pa_status pa_copy_blocks(const int32_t *copy_pairs, int32_t num_pairs, int32_t num_kv_heads,
+                         int32_t head_dim, void *k_cache, void *k_scale, void *v_cache,
+                         void *v_scale, int32_t num_blocks, int32_t block_size, uint32_t *status,
+                         void *stream) {
+  g_last_error[0] = '\0';
+  const int64_t codes = static_cast<int64_t>(block_size) * head_dim;
+  paq8::BlockCopy p;
+  return copy_blocks(p, copy_pairs, num_pairs, num_kv_heads, head_dim, num_blocks, block_size,
+                     {k_cache, k_scale, v_cache, v_scale}, {codes, codes / 16, codes, codes / 16},
+                     status, stream);
+}
+
+pa_status pa_copy_blocks_f8v4(const int32_t *copy_pairs, int32_t num_pairs, int32_t num_kv_heads,
+                              int32_t head_dim, void *k_cache, void *v_cache, void *v_scale,
+                              void *v_zero, int32_t num_blocks, int32_t block_size,
+                              uint32_t *status, void *stream) {
+  g_last_error[0] = '\0';
+  const int64_t codes = static_cast<int64_t>(block_size) * head_dim;
+  paq8::BlockCopy p;
+  return copy_blocks(p, copy_pairs, num_pairs, num_kv_heads, head_dim, num_blocks, block_size,
+                     {k_cache, v_cache, v_scale, v_zero},
+                     {codes, codes / 2, int64_t{2} * block_size, int64_t{2} * block_size}, status,
+                     stream);
+}
+
+size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t max_query_len, int32_t max_prefix_len,
+                                       int32_t max_suffix_len) {
+  if (!shared_sizes_ok(num_seqs, num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim,
+                       max_query_len, max_prefix_len, max_suffix_len))
+    return 256;
+  const paq8::SharedSplits n =
+      paq8::shared_splits(num_seqs, num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim,
+                          max_query_len, max_prefix_len, max_suffix_len);
+  return shared_bytes(num_tokens, num_q_heads, head_dim, n.prefix + n.suffix);
+}
+
+pa_status pa_paged_attention_shared_prefix(
+    const void *q, const void *k_cache, const void *k_scale, const void *v_cache,
+    const void *v_scale, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, const int32_t *cu_groups,
+    const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs, int32_t num_tokens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+    int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
+    float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
+    size_t workspace_bytes, uint32_t flags, void *stream) {
+  g_last_error[0] = '\0';
+  paq8::SharedLaunch L = {q, k_cache, k_scale, v_cache, v_scale, nullptr, cu_seqlens_q, seq_lens,
+                          block_table, cu_groups, prefix_lens, block_table_stride, num_seqs,
+                          num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim, num_blocks,
+                          block_size, max_query_len, max_prefix_len, max_suffix_len, 1, 1,
+                          softmax_scale, sinks, out, lse, nullptr, false};
+  return shared_prefix(L, workspace, workspace_bytes, flags, stream);
+}
+
+pa_status pa_paged_attention_shared_prefix_f8v4(
+    const void *q, const void *k_cache, const void *v_cache, const void *v_scale,
+    const void *v_zero, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, const int32_t *cu_groups,
+    const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs, int32_t num_tokens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+    int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
+    float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
+    size_t workspace_bytes, uint32_t flags, void *stream) {
+  g_last_error[0] = '\0';
+  paq8::SharedLaunch L = {q, k_cache, v_zero, v_cache, v_scale, v_zero, cu_seqlens_q, seq_lens,
+                          block_table, cu_groups, prefix_lens, block_table_stride, num_seqs,
+                          num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim, num_blocks,
+                          block_size, max_query_len, max_prefix_len, max_suffix_len, 1, 1,
+                          softmax_scale, sinks, out, lse, nullptr, true};
+  return shared_prefix(L, workspace, workspace_bytes, flags, stream);
+}
 
 }  // extern "C"
 

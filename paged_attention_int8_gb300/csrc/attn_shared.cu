@@ -1,0 +1,536 @@
+// Attention of a batch whose groups of sequences share a prefix: the row-tile
+// kernel on warp MMAs, the join of the segments, and the dispatch.
+// attn_shared.cuh states the decomposition.
+//
+// shared_mma_kernel: one item segment per block -- 64 / qpk query tokens x the
+// qpk q heads of one kv head, up to 64 rows -- in the form of the generic
+// attention kernel (attn_prefill.cu): warp 4 stages each 64-key tile's pages
+// through a 4-deep mbarrier ring (16-byte cp.async copies); warps 0-3 take the
+// rows in groups of 16 (R groups; the 4/R warps that share a group alternate
+// tiles with private softmax states, merged at the end).  q8: QK^T on the
+// exact integer codes (fp16) per 32-channel group, scaled by the group's fp16
+// K scale in fp32; PV multiplies P (fp16) by V' = code * scale (fp16, one
+// rounding).  fp8 / 4-bit: one QK accumulation of the exact keys, V' = idx *
+// scale + zero in one fp16 FMA.  Sums, maxima and accumulators are fp32.
+// A prefix of P keys costs ceil(rows / 64) reads of its pages (L2 serves all
+// but the first), not one per sequence.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn_shared.cuh"
+
+namespace paq8 {
+
+constexpr int kTile = kSegTile;
+constexpr int kRowTile = 64;  // rows of one block of shared_mma_kernel
+
+template <int D, int BS, bool F8>
+struct SharedMmaCfg {
+  using L = std::conditional_t<F8, StageF8V4<D, BS, kTile>, StageLayout<D, BS, kTile>>;
+  static constexpr int G = D / 32;
+  static constexpr int kQBytes = 4 * G * 2 * 32 * 16;  // fragment-ordered q, 4 row groups
+  static constexpr int kQOff = kStages * L::kBytes;
+  static constexpr int kBarOff = kQOff + kQBytes;
+  static constexpr int kSmemBytes = kBarOff + 2 * kStages * 8 + 1024;  // + alignment slack
+  // merge area (inside the stages) per partner warp: m0 m1 l0 l1 + O
+  static constexpr int kMergeFields = 4 + 4 * 4 * G;
+  static_assert(3 * kMergeFields * 32 * 4 <= kStages * L::kBytes, "merge area");
+};
+
+template <int D, int BS, bool F8>
+__global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_constant__ SharedArgs s) {
+  using C = SharedMmaCfg<D, BS, F8>;
+  using L = typename C::L;
+  constexpr int G = C::G;
+  const AttnArgs &a = s.a;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (smem_base - smem_u32(smem_raw));
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int h = blockIdx.y;  // kv head
+
+  // ---- which rows, which keys: prefix items first, segment-major
+  SharedWork w;
+  const int n_prefix = s.n_pblocks * s.ns_p;
+  const int bx = static_cast<int>(blockIdx.x);
+  if (bx < n_prefix) {
+    if (!prefix_work(s, bx % s.n_pblocks, bx / s.n_pblocks, a.block_q, lane, bx == 0, w)) return;
+  } else {
+    const int r = bx - n_prefix;
+    if (!suffix_work(s, r % s.n_sblocks, r / s.n_sblocks, a.block_q, lane, w)) return;
+  }
+  const int kv_begin = w.kv_begin, kv_end = w.kv_end;
+  const int n_rows = w.n_tok * a.qpk;
+  const int tile_lo = kv_begin / kTile;
+  const int n_iter = (kv_end + kTile - 1) / kTile - tile_lo;
+  const int R = n_rows <= 16 ? 1 : (n_rows <= 32 ? 2 : 4);
+  const int KG = kConsumerWarps / R;
+
+  const uint32_t bar_full = smem_base + C::kBarOff;
+  const uint32_t bar_empty = bar_full + kStages * 8;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_full + 8 * i, 32);  // one arrival per producer lane
+      mbar_init(bar_empty + 8 * i, R);  // a tile is consumed by the R warps of one key group
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == kConsumerWarps) {
+    if constexpr (F8)
+      produce_f8v4<L, BS, kStages>(a, smem_base, bar_full, bar_empty, w.row, h, tile_lo, n_iter,
+                                   kv_begin, kv_end, lane);
+    else
+      produce_tiles_lsu<L, BS>(a, smem_base, bar_full, bar_empty, w.row, h, tile_lo, n_iter,
+                               kv_begin, kv_end, lane);
+    return;
+  }
+
+  // ================================================================== consumers
+  const int rg = warp % R;
+  const int kg = warp / R;
+  const int g = lane >> 2;
+  const int t = lane & 3;
+  const uint32_t q_frag = smem_base + C::kQOff;
+
+  // q -> fp16 A fragments in MMA order: [row group][group][k-step][lane] x 16 B.
+  // Channel order inside a k-step: cols 2t, 2t+1 <- 32gq + 8t + 4s + {0,1},
+  // cols 2t+8, 2t+9 <- 32gq + 8t + 4s + {2,3}; K rows use the same order.
+  if (warp < R) {
+    bool bad_q = false;
+#pragma unroll
+    for (int gq = 0; gq < G; ++gq) {
+      uint32_t f[2][4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int idx = warp * 16 + g + 8 * half;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (idx < n_rows) {
+          const int tq = idx / a.qpk;
+          const int hh = h * a.qpk + idx % a.qpk;
+          const uint16_t *src = a.q + (static_cast<int64_t>(w.q0 + tq) * a.hq + hh) * D +
+                                gq * 32 + t * 8;
+          v = *reinterpret_cast<const uint4 *>(src);
+        }
+        f[0][half] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
+        f[0][2 + half] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
+        f[1][half] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));
+        f[1][2 + half] = pack_half2(bf16_lo(v.w), bf16_hi(v.w));
+        bad_q |= half2_nonfinite(f[0][half]) || half2_nonfinite(f[0][2 + half]) ||
+                 half2_nonfinite(f[1][half]) || half2_nonfinite(f[1][2 + half]);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        sts128(q_frag + (((warp * G + gq) * 2 + s) * 32 + lane) * 16,
+               make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]));
+    }
+    // q values beyond the fp16 range (|q| >= 65520) would give inf scores
+    if (__any_sync(0xffffffffu, bad_q) && lane == 0)
+      flag_status(a.status, PA_DEV_BAD_Q);
+  }
+  named_barrier(1, kConsumerWarps * 32);
+
+  // last visible keys of rows g and g + 8; padding rows copy the
+  // block's last row so their arithmetic stays finite
+  int lim[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int idx = rg * 16 + g + 8 * half;
+    lim[half] = min(kv_end - 1, idx < n_rows ? w.limit0 + (idx / a.qpk) * w.limit_step : kv_end - 1);
+  }
+  int min_lim = min(lim[0], lim[1]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
+
+  // key (within its 16-key block) of score column n of an even / odd n-tile
+  const int kc0 = perm16(2 * t), kc1 = perm16(2 * t + 1);  // even n-tile, cols 2t, 2t+1
+  const int kr_even = perm16(g), kr_odd = perm16(8 + g);    // K rows this lane loads
+
+  float m_run[2] = {-INFINITY, -INFINITY};  // running max, log2 units
+  float l_run[2] = {0.0f, 0.0f};            // this lane's share of the expsum
+  float o_acc[4 * G][4];                    // n-tile (gq, j): channels 32gq + 8j + 2t + {0,1}
+#pragma unroll
+  for (int i = 0; i < 4 * G; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o_acc[i][e] = 0.0f;
+
+  bool timed_out = false;
+  for (int it = kg; it < n_iter; it += KG) {
+    const int stage = it % kStages;
+    if (!mbar_wait(bar_full + 8 * stage, (it / kStages) & 1, a.wait_limit_ns)) {
+      timed_out = true;
+      break;
+    }
+    const uint32_t st = smem_base + stage * L::kBytes;
+    const int key0 = (tile_lo + it) * kTile;
+
+    // ---------------- S = q k^T, exact codes, per-group scale
+    float sc[8][4];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
+#pragma unroll
+    for (int gq = 0; gq < G; ++gq) {
+      const uint4 qa0 = lds128(q_frag + (((rg * G + gq) * 2 + 0) * 32 + lane) * 16);
+      const uint4 qa1 = lds128(q_frag + (((rg * G + gq) * 2 + 1) * 32 + lane) * 16);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const int kb16 = (nt >> 1) * 16;
+        const uint2 kw = lds64(st + L::k_off(kb16 + ((nt & 1) ? kr_odd : kr_even), gq * 32 + t * 8));
+        if constexpr (F8) {  // e4m3 bytes (0,1) -> k 2t, 2t+1; (2,3) -> k 2t+8, 2t+9
+          mma_f16_16816(sc[nt], qa0.x, qa0.y, qa0.z, qa0.w, e4m3x2_to_half2(kw.x),
+                        e4m3x2_to_half2(kw.x >> 16));
+          mma_f16_16816(sc[nt], qa1.x, qa1.y, qa1.z, qa1.w, e4m3x2_to_half2(kw.y),
+                        e4m3x2_to_half2(kw.y >> 16));
+        } else {
+          uint32_t b0, b1, b2, b3;
+          codes4_to_half2(kw.x, b0, b1);
+          codes4_to_half2(kw.y, b2, b3);
+          float sg[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_f16_16816(sg, qa0.x, qa0.y, qa0.z, qa0.w, b0, b1);
+          mma_f16_16816(sg, qa1.x, qa1.y, qa1.z, qa1.w, b2, b3);
+          const int off = (nt & 1) ? 2 : 0;  // odd n-tiles hold keys 4t+2, 4t+3
+          const float s0 = __half2float(__ushort_as_half(lds16(st + L::ks_off(kb16 + kc0 + off, gq))));
+          const float s1 = __half2float(__ushort_as_half(lds16(st + L::ks_off(kb16 + kc1 + off, gq))));
+          sc[nt][0] = fmaf(sg[0], s0, sc[nt][0]);
+          sc[nt][1] = fmaf(sg[1], s1, sc[nt][1]);
+          sc[nt][2] = fmaf(sg[2], s0, sc[nt][2]);
+          sc[nt][3] = fmaf(sg[3], s1, sc[nt][3]);
+        }
+      }
+    }
+
+    // ---------------- mask, online softmax (log2 domain)
+    const bool need_mask = key0 + kTile - 1 > min_lim || key0 < kv_begin;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = sc[nt][e] * a.scale_log2;
+        if (need_mask) {
+          const int key = key0 + (nt >> 1) * 16 + ((e & 1) ? kc1 : kc0) + ((nt & 1) ? 2 : 0);
+          if (key > lim[e >> 1] || key < kv_begin) v = -INFINITY;
+        }
+        sc[nt][e] = v;
+        mx[e >> 1] = fmaxf(mx[e >> 1], v);
+      }
+    float alpha[2], mu[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      const float mn = fmaxf(m_run[r], mx[r]);
+      mu[r] = mn == -INFINITY ? 0.0f : mn;
+      alpha[r] = fast_exp2(m_run[r] - mu[r]);
+      m_run[r] = mn;
+      l_run[r] *= alpha[r];
+    }
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = fast_exp2(sc[nt][e] - mu[e >> 1]);
+        sc[nt][e] = p;
+        l_run[e >> 1] += p;
+      }
+#pragma unroll
+    for (int i = 0; i < 4 * G; ++i) {
+      o_acc[i][0] *= alpha[0];
+      o_acc[i][1] *= alpha[0];
+      o_acc[i][2] *= alpha[1];
+      o_acc[i][3] *= alpha[1];
+    }
+
+    // ---------------- O += P V', V' = code * scale in fp16 from channel-major pages
+    const bool tail = key0 + kTile > kv_end || key0 < kv_begin;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const uint32_t pa0 = pack_half2(sc[2 * kk][0], sc[2 * kk][1]);
+      const uint32_t pa1 = pack_half2(sc[2 * kk][2], sc[2 * kk][3]);
+      const uint32_t pa2 = pack_half2(sc[2 * kk + 1][0], sc[2 * kk + 1][1]);
+      const uint32_t pa3 = pack_half2(sc[2 * kk + 1][2], sc[2 * kk + 1][3]);
+      if constexpr (F8) {
+        // the 4 keys 4t .. 4t+3 of this 16-key block: their scales and zeros
+        // (zeroed outside [kv_begin, kv_end): stale bytes may sit there)
+        uint2 vsc = lds64(st + L::vs_off(kk * 16 + 4 * t));
+        uint2 vzr = lds64(st + L::vz_off(kk * 16 + 4 * t));
+        if (tail) {
+          const int k = key0 + kk * 16 + 4 * t;
+          const auto in = [&](int x) { return x >= kv_begin && x < kv_end; };
+          const uint32_t mx = (in(k) ? 0x0000ffffu : 0u) | (in(k + 1) ? 0xffff0000u : 0u);
+          const uint32_t my = (in(k + 2) ? 0x0000ffffu : 0u) | (in(k + 3) ? 0xffff0000u : 0u);
+          vsc.x &= mx;
+          vzr.x &= mx;
+          vsc.y &= my;
+          vzr.y &= my;
+        }
+#pragma unroll
+        for (int c8 = 0; c8 < D / 8; ++c8) {
+          const uint32_t w = lds16(st + L::v_off(c8 * 8 + g, kk * 16 + 4 * t));
+          uint32_t b0, b1;
+          nibbles4_to_half2(w, b0, b1);  // keys 4t, 4t+1 | 4t+2, 4t+3
+          mma_f16_16816(o_acc[c8], pa0, pa1, pa2, pa3, hfma2_u32(b0, vsc.x, vzr.x),
+                        hfma2_u32(b1, vsc.y, vzr.y));
+        }
+      } else {
+#pragma unroll
+        for (int gq = 0; gq < G; ++gq) {
+          const uint2 vsc = v_scales4<L>(st, kk * 16 + 4 * t, gq, tail, key0, kv_begin, kv_end);
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const uint32_t w = lds32(st + L::v_off(gq * 32 + jj * 8 + g, kk * 16 + 4 * t));
+            uint32_t b0, b1;
+            codes4_to_half2(w, b0, b1);  // keys 4t, 4t+1 -> k 2t, 2t+1; 4t+2, 4t+3 -> k 2t+8, 2t+9
+            mma_f16_16816(o_acc[gq * 4 + jj], pa0, pa1, pa2, pa3, hmul2_u32(b0, vsc.x),
+                          hmul2_u32(b1, vsc.y));
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty + 8 * stage);
+  }
+  if (timed_out && lane == 0) flag_status(a.status, PA_DEV_TIMEOUT);
+
+  // row expsums: sum the 4 lanes of a row
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+    l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+  }
+
+  // ---------------- merge the KG warps of a row group (field-major, no conflicts)
+  if (KG > 1) {
+    named_barrier(1, kConsumerWarps * 32);  // every stage consumed: reuse them
+    float *mbuf = reinterpret_cast<float *>(smem);
+    if (kg > 0) {
+      float *dst = mbuf + (warp - R) * C::kMergeFields * 32 + lane;
+      dst[0 * 32] = m_run[0];
+      dst[1 * 32] = m_run[1];
+      dst[2 * 32] = l_run[0];
+      dst[3 * 32] = l_run[1];
+#pragma unroll
+      for (int i = 0; i < 4 * G; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[(4 + i * 4 + e) * 32] = o_acc[i][e];
+    }
+    named_barrier(1, kConsumerWarps * 32);
+    if (kg > 0) return;
+    for (int k = 1; k < KG; ++k) {
+      const float *src = mbuf + (rg + k * R - R) * C::kMergeFields * 32 + lane;
+      float wa[2], wb[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float mo = src[r * 32];
+        const float lo = src[(2 + r) * 32];
+        const float mn = fmaxf(m_run[r], mo);
+        const float muv = mn == -INFINITY ? 0.0f : mn;
+        wa[r] = fast_exp2(m_run[r] - muv);
+        wb[r] = fast_exp2(mo - muv);
+        m_run[r] = mn;
+        l_run[r] = l_run[r] * wa[r] + lo * wb[r];
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * G; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o_acc[i][e] = o_acc[i][e] * wa[e >> 1] + src[(4 + i * 4 + e) * 32] * wb[e >> 1];
+    }
+  }
+
+  // ---------------- write this segment's triples
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int idx = rg * 16 + g + 8 * half;
+    if (idx >= n_rows) continue;
+    const int64_t at = triple_at(s, w.q0 + idx / a.qpk, h * a.qpk + idx % a.qpk, w.slot);
+    float *dst = a.part_acc + at * D;
+#pragma unroll
+    for (int i = 0; i < 4 * G; ++i)
+      *reinterpret_cast<float2 *>(dst + (i >> 2) * 32 + (i & 3) * 8 + 2 * t) =
+          make_float2(o_acc[i][2 * half], o_acc[i][2 * half + 1]);
+    if (t == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(m_run[half], l_run[half]);
+  }
+}
+
+// The join: one warp per (query token, q head), all segment triples of the row
+// and its sink merged to bf16 output and fp32 LSE.  Bound by its reads (D + 2
+// floats a segment, mostly L2 hits).
+template <int D>
+__global__ void __launch_bounds__(128) shared_join_kernel(const __grid_constant__ SharedArgs s) {
+  constexpr int V = D / 32;  // channels per lane
+  const AttnArgs &a = s.a;
+  const int lane = threadIdx.x & 31;
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (gw >= static_cast<int64_t>(a.num_tokens) * a.hq) return;
+  const int tok = static_cast<int>(gw / a.hq);
+  const int hh = static_cast<int>(gw % a.hq);
+  const int seq = find_seq(a.cu_seqlens_q, a.num_seqs, 1, tok, lane);
+  const int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1];
+  if (c0 < 0 || tok < c0 || tok >= c1 || c1 > a.num_tokens) return;  // a row no sequence owns
+  const int P = prefix_of(s, seq, lane);
+  const int ctx = a.seq_lens[seq] - (c1 - c0);
+  if (P < 0 || ctx < P) return;  // flagged by the suffix item
+  const int n_p = shared_segments(0, P, s.seg_p, s.ns_p);
+  const int n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
+  const int n = n_p + n_s;
+  const int64_t base = gw * (s.ns_p + s.ns_s);
+  // segment k of the row: its slot (prefix slots first, unused ones skipped)
+  auto slot = [&](int k) { return k < n_p ? k : s.ns_p + k - n_p; };
+  float M = a.sinks ? sink_log2(a, hh) : -INFINITY;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float m = k0 + lane < n ? a.part_ml[(base + slot(k0 + lane)) * 2] : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    M = fmaxf(M, m);
+  }
+  const float mu = M == -INFINITY ? 0.0f : M;
+  float total = a.sinks && lane == 0 ? fast_exp2(sink_log2(a, hh) - mu) : 0.0f;
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float wk = 0.0f;
+    if (k0 + lane < n) {
+      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (base + slot(k0 + lane)) * 2);
+      wk = fast_exp2(ml.x - mu);
+      total = fmaf(wk, ml.y, total);
+    }
+    const int end = min(32, n - k0);
+#pragma unroll 8
+    for (int k = 0; k < end; ++k) {
+      const float wv = __shfl_sync(0xffffffffu, wk, k);
+      const float *src = a.part_acc + (base + slot(k0 + k)) * D + lane * V;
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        const float2 x = *reinterpret_cast<const float2 *>(src + v);
+        acc[v] = fmaf(wv, x.x, acc[v]);
+        acc[v + 1] = fmaf(wv, x.y, acc[v + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const float inv = 1.0f / total;
+  uint16_t *dst = a.out + gw * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2)
+    *reinterpret_cast<uint32_t *>(dst + v) = pack_bf162(acc[v] * inv, acc[v + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[gw] = (M + log2f(total)) * kLn2;
+}
+
+// ---------------------------------------------------------------------- host
+
+SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_groups, int32_t hq,
+                           int32_t hk, int32_t d, int32_t max_query_len, int32_t max_prefix_len,
+                           int32_t max_suffix_len) {
+  (void)max_query_len;
+  const int qpk = hq / hk;
+  const int block_q = std::max(1, kRowTile / qpk);
+  const int64_t rows_blocks = std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q);
+  // two resident blocks per SM (one at D = 256), at least 4 tiles a segment
+  const int64_t slots = d == 256 ? 152 : 304;
+  auto pick = [&](int64_t units, int len) {
+    const int64_t tiles = (len + kTile - 1) / kTile;
+    const int64_t n = std::min((slots + units - 1) / std::max<int64_t>(1, units), (tiles + 3) / 4);
+    return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(n, 64)));
+  };
+  SharedSplits r;
+  r.prefix = pick(rows_blocks * hk, max_prefix_len);
+  r.suffix = pick(static_cast<int64_t>(num_seqs) * hk, max_suffix_len);
+  return r;
+}
+
+template <int D, int BS, bool F8>
+static cudaError_t launch_shared_mma_t(const SharedArgs &s, cudaStream_t stream) {
+  using C = SharedMmaCfg<D, BS, F8>;
+  static DeviceOnce configured;
+  cudaError_t e = configured.get(nullptr, [](int, int *) {
+    return cudaFuncSetAttribute(shared_mma_kernel<D, BS, F8>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p +
+                     static_cast<int64_t>(s.n_sblocks) * s.ns_s;
+  if (gx > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s.a.hk));
+  shared_mma_kernel<D, BS, F8><<<grid, kThreads, C::kSmemBytes, stream>>>(s);
+  return cudaGetLastError();
+}
+
+static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8v4,
+                                     cudaStream_t stream) {
+#define PAQ8_SHARED_CASE(DD, BB)                                          \
+  if (d == DD && bs == BB)                                                \
+    return f8v4 ? launch_shared_mma_t<DD, BB, true>(s, stream)            \
+                : launch_shared_mma_t<DD, BB, false>(s, stream);
+  PAQ8_SHARED_CASE(64, 16)
+  PAQ8_SHARED_CASE(64, 32)
+  PAQ8_SHARED_CASE(128, 16)
+  PAQ8_SHARED_CASE(128, 32)
+  PAQ8_SHARED_CASE(256, 16)
+  PAQ8_SHARED_CASE(256, 32)
+#undef PAQ8_SHARED_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
+  SharedArgs s{};
+  AttnArgs &a = s.a;
+  a.q = static_cast<const uint16_t *>(L.q);
+  a.cu_seqlens_q = L.cu;
+  a.seq_lens = L.seq_lens;
+  a.block_table = L.block_table;
+  a.k_cache = static_cast<const int8_t *>(L.k_cache);
+  a.v_cache = static_cast<const int8_t *>(L.v_cache);
+  a.k_scale = static_cast<const uint16_t *>(L.k_scale);
+  a.v_scale = static_cast<const uint16_t *>(L.v_scale);
+  a.v_zero = static_cast<const uint16_t *>(L.v_zero);
+  a.out = static_cast<uint16_t *>(L.out);
+  a.lse = L.lse;
+  a.status = reinterpret_cast<uint32_t *>(L.workspace);
+  a.num_seqs = L.num_seqs;
+  a.num_tokens = L.num_tokens;
+  a.hq = L.hq;
+  a.hk = L.hk;
+  a.qpk = L.hq / L.hk;
+  a.num_blocks = L.num_blocks;
+  a.bt_stride = L.bt_stride;
+  a.scale_log2 = L.softmax_scale * kLog2e;
+  a.causal = 1;
+  a.sinks = L.sinks;
+  a.wait_limit_ns = kWaitLimitNs;
+  const int64_t triples = static_cast<int64_t>(L.num_tokens) * L.hq *
+                          (L.prefix_splits + L.suffix_splits);
+  a.part_acc = reinterpret_cast<float *>(L.workspace + 256);
+  a.part_ml = a.part_acc + triples * L.d;
+  s.cu_groups = L.cu_groups;
+  s.prefix_lens = L.prefix_lens;
+  s.num_groups = L.num_groups;
+  s.ns_p = L.prefix_splits;
+  s.ns_s = L.suffix_splits;
+  auto seg = [](int len, int ns) { return std::max(1, ((len + kTile - 1) / kTile + ns - 1) / ns); };
+  s.seg_p = seg(L.max_prefix_len, s.ns_p);
+  s.seg_s = seg(L.max_suffix_len + kTile, s.ns_s);  // a suffix may start inside a tile
+  a.block_q = std::max(1, kRowTile / a.qpk);
+  s.n_pblocks = L.num_tokens / a.block_q + L.num_groups;
+  s.n_sblocks = L.num_tokens / a.block_q + L.num_seqs;
+  cudaError_t e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(L.num_tokens) * L.hq;
+  const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
+  switch (L.d) {
+    case 64: shared_join_kernel<64><<<blocks, 128, 0, stream>>>(s); break;
+    case 128: shared_join_kernel<128><<<blocks, 128, 0, stream>>>(s); break;
+    case 256: shared_join_kernel<256><<<blocks, 128, 0, stream>>>(s); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace paq8
