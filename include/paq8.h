@@ -459,11 +459,13 @@ size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int
  *                 from 0 (nothing shared) to seq_len - q_len of each of its
  *                 sequences; it need not end with a page.  A sequence on its
  *                 own is a group of one.
- *   max_query_len, max_prefix_len, max_suffix_len
- *                 host bounds of q_len, of prefix_lens and of seq_len - prefix
- *                 (never synced): they size the key segments and choose kernels;
- *                 any positive value (max_prefix_len: not negative) gives
- *                 correct results.
+ *   max_query_len host upper bound on every q_len (never synced); a sequence
+ *                 with more query tokens may be left unprocessed and flagged
+ *                 PA_DEV_BAD_SEQ.
+ *   max_prefix_len, max_suffix_len
+ *                 host hints of the longest prefix and of the longest seq_len -
+ *                 prefix: they size the key segments; any positive value
+ *                 (max_prefix_len: not negative) gives correct results.
  *   workspace     device buffer, 16-byte aligned, its first 4 bytes the status
  *                 word (zero it once).  pa_shared_prefix_workspace_size bytes;
  *                 a smaller one takes fewer key segments, down to 256 bytes +

@@ -733,8 +733,10 @@ def paged_attention_shared_prefix(q, k_cache, k_scale, v_cache, v_scale, cu_seql
     ``cu_groups`` int32 [G + 1]: group g owns sequences cu_groups[g] ..
     cu_groups[g + 1] - 1; ``prefix_lens`` int32 [G]: its first keys, the same
     for all of them, read through the first sequence's row of ``block_table``
-    (0: nothing shared; at most seq_len - q_len of each).  ``max_*``: host
-    bounds of the query lengths, the prefixes and the keys past them.
+    (0: nothing shared; at most seq_len - q_len of each).
+    ``max_query_len``: a host bound of the query lengths; ``max_prefix_len``
+    and ``max_suffix_len``: hints of the longest prefix and of the most keys
+    past one.
     ``workspace``: uint8 CUDA tensor of ``shared_prefix_workspace_size``
     bytes, its first 4 bytes zero (the device status word); allocated when
     omitted.  Other arguments and results as paged_attention."""

@@ -21,6 +21,11 @@
 
 namespace paq8 {
 
+cudaError_t launch_shared_rows(const SharedArgs &s, int d, int bs, bool f8v4, cudaStream_t stream);
+cudaError_t launch_shared_tc(const SharedArgs &s, const CUtensorMap &tk, const CUtensorMap &tv,
+                             int d, int bs, bool f8v4, cudaStream_t stream);
+int shared_tc_rows(int d);
+
 constexpr int kTile = kSegTile;
 constexpr int kRowTile = 64;  // rows of one block of shared_mma_kernel
 
@@ -56,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
   const int n_prefix = s.n_pblocks * s.ns_p;
   const int bx = static_cast<int>(blockIdx.x);
   if (bx < n_prefix) {
-    if (!prefix_work(s, bx % s.n_pblocks, bx / s.n_pblocks, a.block_q, lane, bx == 0, w)) return;
+    if (!prefix_work(s, bx % s.n_pblocks, bx / s.n_pblocks, a.block_q, lane, w)) return;
   } else {
     const int r = bx - n_prefix;
     if (!suffix_work(s, r % s.n_sblocks, r / s.n_sblocks, a.block_q, lane, w)) return;
@@ -375,7 +380,8 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const __grid_constant_
   if (c0 < 0 || tok < c0 || tok >= c1 || c1 > a.num_tokens) return;  // a row no sequence owns
   const int P = prefix_of(s, seq, lane);
   const int ctx = a.seq_lens[seq] - (c1 - c0);
-  if (P < 0 || ctx < P) return;  // flagged by the suffix item
+  // flagged by the suffix item
+  if (P < 0 || ctx < P || rows_of(s, c1 - c0) > s.max_rows) return;
   const int n_p = shared_segments(0, P, s.seg_p, s.ns_p);
   const int n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
   const int n = n_p + n_s;
@@ -426,23 +432,52 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const __grid_constant_
 
 // ---------------------------------------------------------------------- host
 
+// Whether the prefix items go to the tensor-core kernel: its blocks hold 256
+// rows and convert a tile for them all, the warp-MMA kernel's hold 64.
+static bool prefix_on_tc(int32_t num_tokens, int32_t num_groups, int32_t qpk, int32_t d) {
+  return shared_tc_rows(d) > 0 &&
+         static_cast<int64_t>(num_tokens) * qpk >= int64_t{32} * num_groups;
+}
+
 SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_groups, int32_t hq,
                            int32_t hk, int32_t d, int32_t max_query_len, int32_t max_prefix_len,
                            int32_t max_suffix_len) {
   (void)max_query_len;
   const int qpk = hq / hk;
-  const int block_q = std::max(1, kRowTile / qpk);
-  const int64_t rows_blocks = std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q);
-  // two resident blocks per SM (one at D = 256), at least 4 tiles a segment
-  const int64_t slots = d == 256 ? 152 : 304;
-  auto pick = [&](int64_t units, int len) {
-    const int64_t tiles = (len + kTile - 1) / kTile;
-    const int64_t n = std::min((slots + units - 1) / std::max<int64_t>(1, units), (tiles + 3) / 4);
-    return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(n, 64)));
-  };
   SharedSplits r;
-  r.prefix = pick(rows_blocks * hk, max_prefix_len);
-  r.suffix = pick(static_cast<int64_t>(num_seqs) * hk, max_suffix_len);
+  {
+    // prefix: the count of segments that ends soonest, in units of a tile's
+    // time: whole waves of blocks of (tiles + the block's fixed cost), plus
+    // the join's traffic (a triple is written and read once more per segment)
+    const bool tc = prefix_on_tc(num_tokens, num_groups, qpk, d);
+    const int rows = tc ? shared_tc_rows(d) : kRowTile;
+    const int64_t block_q = std::max(1, rows / qpk);
+    const int64_t units =
+        std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q) * hk;
+    const int64_t slots = tc || d == 256 ? 152 : 304;  // resident blocks
+    const int64_t tiles = std::max(1, (max_prefix_len + kTile - 1) / kTile);
+    const double fixed = 4.0, join = static_cast<double>(num_tokens) * hq * (d + 2) * 8 / 6.6e6;
+    double best = 0;
+    r.prefix = 1;
+    for (int n = 1; n <= 64 && n <= tiles; ++n) {
+      const double waves = static_cast<double>((units * n + slots - 1) / slots);
+      const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + fixed) + join * n;
+      if (n == 1 || cost < best) {
+        best = cost;
+        r.prefix = n;
+      }
+    }
+  }
+  {
+    // suffix: ~1024 keys a segment (the decode kernel's measured best), more
+    // segments only while blocks are too few to fill the GPU four to an SM
+    const int64_t units = static_cast<int64_t>(num_seqs) * hk;
+    const int64_t tiles = (max_suffix_len + kTile - 1) / kTile;
+    int64_t n = std::max<int64_t>((max_suffix_len + 1023) / 1024,
+                                  std::min((608 + units - 1) / units, (tiles + 3) / 4));
+    n = std::min(n, std::max<int64_t>(1, 8192 / units));
+    r.suffix = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(n, 64)));
+  }
   return r;
 }
 
@@ -477,6 +512,33 @@ static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8
   PAQ8_SHARED_CASE(256, 32)
 #undef PAQ8_SHARED_CASE
   return cudaErrorInvalidValue;
+}
+
+// 2-D byte map of page rows: `rows` rows of `row_bytes`, boxes of box_y whole
+// rows (row_bytes <= 128).
+static bool encode_page_map(CUtensorMap *map, const void *base, int64_t rows, int row_bytes,
+                            int box_y, CUtensorMapSwizzle swizzle) {
+  typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const EncodeTiled fn = []() -> EncodeTiled {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_y)};
+  const cuuint32_t step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+            step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
@@ -517,11 +579,36 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   auto seg = [](int len, int ns) { return std::max(1, ((len + kTile - 1) / kTile + ns - 1) / ns); };
   s.seg_p = seg(L.max_prefix_len, s.ns_p);
   s.seg_s = seg(L.max_suffix_len + kTile, s.ns_s);  // a suffix may start inside a tile
-  a.block_q = std::max(1, kRowTile / a.qpk);
-  s.n_pblocks = L.num_tokens / a.block_q + L.num_groups;
-  s.n_sblocks = L.num_tokens / a.block_q + L.num_seqs;
-  cudaError_t e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream);
-  if (e != cudaSuccess) return e;
+  // Who takes what: the prefix goes to the tensor-core kernel or the row-tile
+  // kernel (prefix_on_tc), a suffix of up to kFewRows rows to the rows kernel,
+  // of more to the row-tile kernel.
+  const bool tc = prefix_on_tc(L.num_tokens, L.num_groups, a.qpk, L.d);
+  const bool few = a.qpk <= kFewRows;
+  const bool many = static_cast<int64_t>(L.max_query_len) * a.qpk > kFewRows;
+  s.few_rows = few ? kFewRows : 0;
+  s.max_rows = many ? 0x7fffffff : kFewRows;
+  cudaError_t e = cudaSuccess;
+  if (tc) {
+    CUtensorMap tk = {}, tv = {};
+    const int64_t pages = static_cast<int64_t>(L.num_blocks) * L.hk;
+    if (!encode_page_map(&tk, L.k_cache, pages * L.bs, L.d, L.bs,
+                         L.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        (!L.f8v4 && !encode_page_map(&tv, L.v_cache, pages * L.d, L.bs, L.d,
+                                     L.bs == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                : CU_TENSOR_MAP_SWIZZLE_NONE)))
+      return cudaErrorInvalidValue;
+    SharedArgs p = s;
+    p.a.block_q = shared_tc_rows(L.d) / a.qpk;
+    p.n_pblocks = L.num_tokens / p.a.block_q + L.num_groups;
+    if ((e = launch_shared_tc(p, tk, tv, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+  }
+  if (few && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+  if (!tc || many) {
+    a.block_q = std::max(1, kRowTile / a.qpk);
+    s.n_pblocks = tc ? 0 : L.num_tokens / a.block_q + L.num_groups;
+    s.n_sblocks = many ? L.num_tokens / a.block_q + L.num_seqs : 0;
+    if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+  }
   const int64_t rows = static_cast<int64_t>(L.num_tokens) * L.hq;
   const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
   switch (L.d) {

@@ -25,6 +25,7 @@
 namespace paq8 {
 
 constexpr int kSegTile = 64;  // keys per tile of the segment rule, for every kernel
+constexpr int kFewRows = 8;   // rows per kv head that the rows kernel takes
 
 struct SharedArgs {
   AttnArgs a;  // q, caches, tables, partials (part_acc, part_ml), status, scale, sinks
@@ -34,6 +35,8 @@ struct SharedArgs {
   int32_t ns_p, ns_s;          // prefix and suffix segments: triples of a row
   int32_t seg_p, seg_s;        // 64-key tiles per segment
   int32_t n_pblocks, n_sblocks;  // row blocks of the prefix and suffix items in the grid
+  int32_t few_rows;            // suffixes of at most this many rows are the rows kernel's
+  int32_t max_rows;            // no suffix kernel takes more rows than this
 };
 
 // Warp-cooperative search: the last i in [0, n) with key(i) <= target, key
@@ -67,6 +70,11 @@ __device__ __forceinline__ int prefix_of(const SharedArgs &s, int seq, int lane)
   return s.prefix_lens[g];
 }
 
+// Query rows per kv head of a sequence of q_len tokens (saturating).
+__device__ __forceinline__ int rows_of(const SharedArgs &s, int q_len) {
+  return q_len > (1 << 26) ? 1 << 30 : q_len * s.a.qpk;
+}
+
 // Segments of keys [begin, end): the rule every kernel and the join share.
 __device__ __forceinline__ int shared_segments(int begin, int end, int seg_tiles, int ns) {
   return end <= begin ? 0 : segments_of(begin, end, kSegTile, seg_tiles, ns);
@@ -97,7 +105,7 @@ __device__ __forceinline__ bool segment_keys(int begin, int end, int seg_tiles, 
 // Prefix item: row block `blk` (block_q tokens of one group), segment sigma.
 // Executed by whole warps; false: nothing to do.
 __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int blk, int sigma, int block_q,
-                                            int lane, bool first, SharedWork &w) {
+                                            int lane, SharedWork &w) {
   const AttnArgs &a = s.a;
   const int g = find_last(s.num_groups, blk, lane, [&](int i) {
     const int t = group_token(s, i);
@@ -106,7 +114,7 @@ __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int blk, int si
   const int c0 = group_token(s, g), c1 = group_token(s, g + 1);
   const int P = s.prefix_lens[g];
   if (c0 < 0 || c1 > a.num_tokens || c0 > c1 || P < 0) {
-    if (first && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
     return false;
   }
   const int tok0 = (blk - (c0 / block_q + g)) * block_q;
@@ -130,6 +138,7 @@ __device__ __forceinline__ bool suffix_work(const SharedArgs &s, int blk, int si
   const int first = block_q == 1 ? c0 : c0 / block_q + seq;
   const int tok0 = (blk - first) * block_q;
   if (tok0 < 0 || tok0 >= c1 - c0) return false;
+  if (rows_of(s, c1 - c0) <= s.few_rows) return false;
   const int seq_len = a.seq_lens[seq], ctx = seq_len - (c1 - c0);
   const int P = prefix_of(s, seq, lane);
   if (c0 < 0 || c1 > a.num_tokens || P < 0 || ctx < P) {

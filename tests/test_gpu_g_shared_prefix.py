@@ -65,8 +65,8 @@ def test_segments(cuda_device, fmt, d, bs, squeeze):
     S.check(b, *b.call(workspace=ws))
 
 
-# the bounds are hints for prefix, suffix and query lengths alike
-@pytest.mark.parametrize("bounds", [(1, 0, 1), (1, 64, 64), (999, 99999, 99999), (3, 1, 100000)])
+# the bounds of the prefixes and suffixes are hints, that of the query lengths an upper bound
+@pytest.mark.parametrize("bounds", [(6, 0, 1), (6, 64, 64), (999, 99999, 99999), (7, 1, 100000)])
 def test_bounds_are_hints(cuda_device, bounds):
     b = S.make(5, cuda_device, "q8", 8, 2, 128, 16, [(700, [(1, 300), (6, 80), (1, 2)]),
                                                      (5, [(1, 900)])])
@@ -136,6 +136,22 @@ def test_rows_of_bad_sequences_stay(cuda_device):
             assert torch.isfinite(out[0].float()).all()
             assert (lse[0].double().cpu() - ref[1][0]).abs().max() < 1e-3
     S.check(b, *b.call(), ref=ref)
+
+
+def test_query_longer_than_its_bound_is_flagged(cuda_device):
+    b = S.make(15, cuda_device, "q8", 8, 2, 128, 16, [(40, [(1, 5), (6, 9), (2, 4)])])
+    ref = S.reference(b)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device=cuda_device)
+    out = torch.full_like(b.q, float("nan"))
+    lse = torch.full(b.q.shape[:2], float("nan"), device=cuda_device)
+    _lib.paged_attention_shared_prefix(b.q, *b.cache, b.cu, b.lens, b.table, b.groups, b.prefixes,
+                                       2, 40, 9, out=out, lse=lse, workspace=ws)
+    with pytest.raises(_lib.PagedAttentionError) as err:
+        _lib.check_status(ws)
+    assert err.value.bits == _lib.DEV_BAD_SEQ
+    assert torch.isnan(out[1:7].float()).all() and torch.isnan(lse[1:7]).all()
+    for rows in ([0], [7, 8]):
+        assert (lse[rows].double().cpu() - ref[1][rows]).abs().max() < 1e-3
 
 
 def test_q_outside_fp16_is_flagged(cuda_device):
