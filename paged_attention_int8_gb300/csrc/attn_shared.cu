@@ -55,13 +55,15 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int h = blockIdx.y;  // kv head
+  launch_dependents();
+  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1};
 
   // ---- which rows, which keys: prefix items first, segment-major
   SharedWork w;
   const int n_prefix = s.n_pblocks * s.ns_p;
   const int bx = static_cast<int>(blockIdx.x);
   if (bx < n_prefix) {
-    if (!prefix_work(s, bx % s.n_pblocks, bx / s.n_pblocks, a.block_q, lane, w)) return;
+    if (!prefix_work(s, bx, a.block_q, lane, w)) return;
   } else {
     const int r = bx - n_prefix;
     if (!suffix_work(s, r % s.n_sblocks, r / s.n_sblocks, a.block_q, lane, w)) return;
@@ -353,81 +355,138 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
   for (int half = 0; half < 2; ++half) {
     const int idx = rg * 16 + g + 8 * half;
     if (idx >= n_rows) continue;
-    const int64_t at = triple_at(s, w.q0 + idx / a.qpk, h * a.qpk + idx % a.qpk, w.slot);
-    float *dst = a.part_acc + at * D;
+    const int64_t r = static_cast<int64_t>(w.q0) * a.qpk + idx, step = rows_total(s) * 4;
+    float *dst = acc_at<D>(s, w.slot, h) + (t >> 1) * step + r * 4 + (t & 1) * 2;
 #pragma unroll
-    for (int i = 0; i < 4 * G; ++i)
-      *reinterpret_cast<float2 *>(dst + (i >> 2) * 32 + (i & 3) * 8 + 2 * t) =
+    for (int i = 0; i < 4 * G; ++i)  // channels 8i + 2t, + 1
+      *reinterpret_cast<float2 *>(dst + 2 * i * step) =
           make_float2(o_acc[i][2 * half], o_acc[i][2 * half + 1]);
-    if (t == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(m_run[half], l_run[half]);
+    if (t == 0)
+      *reinterpret_cast<float2 *>(a.part_ml + (ml_at(s, w.slot, h) + r) * 2) =
+          make_float2(m_run[half], l_run[half]);
   }
 }
 
-// The join: one warp per (query token, q head), all segment triples of the row
-// and its sink merged to bf16 output and fp32 LSE.  Bound by its reads (D + 2
-// floats a segment, mostly L2 hits).
+// The join: all segment triples of a row (query token x q head) and its sink
+// merged to bf16 output and fp32 LSE.  One warp per two consecutive rows of a
+// kv head: lane l reads 4 channels (l / 2, + 16, ...) of row l % 2, so that a
+// pair of lanes takes a whole sector.  Bound by its reads (D + 2 floats a
+// segment, L2 hits); launched beside the last kernel, it looks up the rows'
+// sequences and waits.
 template <int D>
 __global__ void __launch_bounds__(128) shared_join_kernel(const __grid_constant__ SharedArgs s) {
-  constexpr int V = D / 32;  // channels per lane
+  constexpr int V = D / 64;  // 4-channel pieces per lane
+  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
   const AttnArgs &a = s.a;
   const int lane = threadIdx.x & 31;
+  const int odd = lane & 1;
+  const int64_t rows = rows_total(s);
+  const int64_t pairs = (rows + 1) / 2;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (gw >= static_cast<int64_t>(a.num_tokens) * a.hq) return;
-  const int tok = static_cast<int>(gw / a.hq);
-  const int hh = static_cast<int>(gw % a.hq);
-  const int seq = find_seq(a.cu_seqlens_q, a.num_seqs, 1, tok, lane);
-  const int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1];
-  if (c0 < 0 || tok < c0 || tok >= c1 || c1 > a.num_tokens) return;  // a row no sequence owns
-  const int P = prefix_of(s, seq, lane);
-  const int ctx = a.seq_lens[seq] - (c1 - c0);
-  // flagged by the suffix item
-  if (P < 0 || ctx < P || rows_of(s, c1 - c0) > s.max_rows) return;
-  const int n_p = shared_segments(0, P, s.seg_p, s.ns_p);
-  const int n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
-  const int n = n_p + n_s;
-  const int64_t base = gw * (s.ns_p + s.ns_s);
-  // segment k of the row: its slot (prefix slots first, unused ones skipped)
+  if (gw >= pairs * a.hk) return;
+  const int h = static_cast<int>(gw / pairs);
+  const int64_t row0 = gw % pairs * 2, row = row0 + odd;
+  // this lane's row: its token, q head, and how many segments hold its keys
+  int n_p = 0, n_s = 0;
+  const int tok0 = static_cast<int>(row0 / a.qpk), tok1 = static_cast<int>((row0 + 1) / a.qpk);
+  const int tok = odd ? tok1 : tok0;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int tk = i ? tok1 : tok0;
+    if (i && (tok1 == tok0 || tok1 >= a.num_tokens)) break;
+    const int seq = find_seq(a.cu_seqlens_q, a.num_seqs, 1, tk, lane);
+    const int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1];
+    if (c0 < 0 || tk < c0 || tk >= c1 || c1 > a.num_tokens) continue;  // a row no sequence owns
+    const int P = prefix_of(s, seq, lane);
+    const int ctx = a.seq_lens[seq] - (c1 - c0);
+    // flagged by the suffix item
+    if (P < 0 || ctx < P || rows_of(s, c1 - c0) > s.max_rows) continue;
+    if (tk == tok) {
+      n_p = shared_segments(0, P, s.seg_p, s.ns_p);
+      n_s = shared_segments(P, ctx + tk - c0 + 1, s.seg_s, s.ns_s);
+    }
+  }
+  const bool own = row < rows && n_s > 0;  // a row that is written
+  const int hh = h * a.qpk + static_cast<int>(row % a.qpk);
+  const int n = own ? n_p + n_s : 0;
+  const int n_max = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
+  if (n_max == 0) return;
+  const float sink = a.sinks && own ? sink_log2(a, hh) : -INFINITY;
+  // segment k of the row: its slot (the prefix's first, unused ones skipped)
   auto slot = [&](int k) { return k < n_p ? k : s.ns_p + k - n_p; };
-  float M = a.sinks ? sink_log2(a, hh) : -INFINITY;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float m = k0 + lane < n ? a.part_ml[(base + slot(k0 + lane)) * 2] : -INFINITY;
+  auto triple_ml = [&](int k) {
+    return *reinterpret_cast<const float2 *>(a.part_ml + (ml_at(s, slot(k), h) + row) * 2);
+  };
+  wait_for_predecessor();  // the triples
+  const int k_lane = lane >> 1;
+  float M = sink;
+  float total = sink > -INFINITY && k_lane == 0 ? 1.0f : 0.0f;  // this lane's share, scaled to M
+  float4 acc[V];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    M = fmaxf(M, m);
-  }
-  const float mu = M == -INFINITY ? 0.0f : M;
-  float total = a.sinks && lane == 0 ? fast_exp2(sink_log2(a, hh) - mu) : 0.0f;
-  float acc[V];
+  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // 16 segments a round, one per lane pair for the weights; the accumulators
+  // kBatch segments at a time, all their loads in flight together
+  constexpr int kBatch = V == 4 ? 4 : 8;
+  for (int k0 = 0; k0 < n_max; k0 += 16) {
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (k0 + k_lane < n) ml = triple_ml(k0 + k_lane);
+    float4 x[kBatch][V];
+    auto load = [&](int k1) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float wk = 0.0f;
-    if (k0 + lane < n) {
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (base + slot(k0 + lane)) * 2);
-      wk = fast_exp2(ml.x - mu);
-      total = fmaf(wk, ml.y, total);
-    }
-    const int end = min(32, n - k0);
-#pragma unroll 8
-    for (int k = 0; k < end; ++k) {
-      const float wv = __shfl_sync(0xffffffffu, wk, k);
-      const float *src = a.part_acc + (base + slot(k0 + k)) * D + lane * V;
+      for (int i = 0; i < kBatch; ++i) {
+        const bool in = k1 + i < n;
+        const float *src = acc_at<D>(s, slot(in ? k1 + i : 0), h) + (k_lane * rows + row) * 4;
 #pragma unroll
-      for (int v = 0; v < V; v += 2) {
-        const float2 x = *reinterpret_cast<const float2 *>(src + v);
-        acc[v] = fmaf(wv, x.x, acc[v]);
-        acc[v + 1] = fmaf(wv, x.y, acc[v + 1]);
+        for (int v = 0; v < V; ++v)
+          x[i][v] = in ? *reinterpret_cast<const float4 *>(src + v * 16 * rows * 4)
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+    };
+    load(k0);
+    float m = ml.x;
+#pragma unroll
+    for (int o = 2; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(M, m);
+    const float mu = m == -INFINITY ? 0.0f : m;
+    const float f = fast_exp2(M - mu);
+    M = m;
+    const float wk = fast_exp2(ml.x - mu);
+    total = fmaf(total, f, wk * ml.y);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      acc[v].x *= f;
+      acc[v].y *= f;
+      acc[v].z *= f;
+      acc[v].w *= f;
+    }
+#pragma unroll
+    for (int b = 0; b < 16 / kBatch; ++b) {
+      if (k0 + b * kBatch >= n_max) break;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wk, 2 * (b * kBatch + i) + odd);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          acc[v].x = fmaf(w, x[i][v].x, acc[v].x);
+          acc[v].y = fmaf(w, x[i][v].y, acc[v].y);
+          acc[v].z = fmaf(w, x[i][v].z, acc[v].z);
+          acc[v].w = fmaf(w, x[i][v].w, acc[v].w);
+        }
+      }
+      if (b + 1 < 16 / kBatch) load(k0 + (b + 1) * kBatch);
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  for (int o = 2; o < 32; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (!own) return;
   const float inv = 1.0f / total;
-  uint16_t *dst = a.out + gw * D + lane * V;
+  const int64_t at = static_cast<int64_t>(tok) * a.hq + hh;
 #pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<uint32_t *>(dst + v) = pack_bf162(acc[v] * inv, acc[v + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[gw] = (M + log2f(total)) * kLn2;
+  for (int v = 0; v < V; ++v)
+    *reinterpret_cast<uint2 *>(a.out + at * D + v * 64 + k_lane * 4) =
+        make_uint2(pack_bf162(acc[v].x * inv, acc[v].y * inv),
+                   pack_bf162(acc[v].z * inv, acc[v].w * inv));
+  if (k_lane == 0 && a.lse) a.lse[at] = (M + log2f(total)) * kLn2;
 }
 
 // ---------------------------------------------------------------------- host
@@ -482,7 +541,7 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
 }
 
 template <int D, int BS, bool F8>
-static cudaError_t launch_shared_mma_t(const SharedArgs &s, cudaStream_t stream) {
+static cudaError_t launch_shared_mma_t(const SharedArgs &s, bool beside, cudaStream_t stream) {
   using C = SharedMmaCfg<D, BS, F8>;
   static DeviceOnce configured;
   cudaError_t e = configured.get(nullptr, [](int, int *) {
@@ -494,16 +553,15 @@ static cudaError_t launch_shared_mma_t(const SharedArgs &s, cudaStream_t stream)
                      static_cast<int64_t>(s.n_sblocks) * s.ns_s;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s.a.hk));
-  shared_mma_kernel<D, BS, F8><<<grid, kThreads, C::kSmemBytes, stream>>>(s);
-  return cudaGetLastError();
+  return launch_kernel(shared_mma_kernel<D, BS, F8>, grid, kThreads, C::kSmemBytes, stream, beside, s);
 }
 
-static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8v4,
+static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8v4, bool beside,
                                      cudaStream_t stream) {
 #define PAQ8_SHARED_CASE(DD, BB)                                          \
   if (d == DD && bs == BB)                                                \
-    return f8v4 ? launch_shared_mma_t<DD, BB, true>(s, stream)            \
-                : launch_shared_mma_t<DD, BB, false>(s, stream);
+    return f8v4 ? launch_shared_mma_t<DD, BB, true>(s, beside, stream)    \
+                : launch_shared_mma_t<DD, BB, false>(s, beside, stream);
   PAQ8_SHARED_CASE(64, 16)
   PAQ8_SHARED_CASE(64, 32)
   PAQ8_SHARED_CASE(128, 16)
@@ -599,25 +657,26 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
       return cudaErrorInvalidValue;
     SharedArgs p = s;
     p.a.block_q = shared_tc_rows(L.d) / a.qpk;
-    p.n_pblocks = L.num_tokens / p.a.block_q + L.num_groups;
+    p.n_pblocks = prefix_blocks(L.num_tokens, L.num_groups, p.a.block_q);
     if ((e = launch_shared_tc(p, tk, tv, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   }
-  if (few && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   if (!tc || many) {
     a.block_q = std::max(1, kRowTile / a.qpk);
-    s.n_pblocks = tc ? 0 : L.num_tokens / a.block_q + L.num_groups;
+    s.n_pblocks = tc ? 0 : prefix_blocks(L.num_tokens, L.num_groups, a.block_q);
     s.n_sblocks = many ? L.num_tokens / a.block_q + L.num_seqs : 0;
-    if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+    if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, tc, stream)) != cudaSuccess) return e;
   }
-  const int64_t rows = static_cast<int64_t>(L.num_tokens) * L.hq;
-  const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
+  if (few && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+  const int64_t warps = (static_cast<int64_t>(L.num_tokens) * a.qpk + 1) / 2 * L.hk;
+  const int64_t blocks = (warps + 3) / 4;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
   switch (L.d) {
-    case 64: shared_join_kernel<64><<<blocks, 128, 0, stream>>>(s); break;
-    case 128: shared_join_kernel<128><<<blocks, 128, 0, stream>>>(s); break;
-    case 256: shared_join_kernel<256><<<blocks, 128, 0, stream>>>(s); break;
-    default: return cudaErrorInvalidValue;
+    case 64: return launch_kernel(shared_join_kernel<64>, grid, 128, 0, stream, true, s);
+    case 128: return launch_kernel(shared_join_kernel<128>, grid, 128, 0, stream, true, s);
+    case 256: return launch_kernel(shared_join_kernel<256>, grid, 128, 0, stream, true, s);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace paq8

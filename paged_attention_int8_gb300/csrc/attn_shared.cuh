@@ -102,23 +102,53 @@ __device__ __forceinline__ bool segment_keys(int begin, int end, int seg_tiles, 
   return w.kv_begin < w.kv_end;
 }
 
-// Prefix item: row block `blk` (block_q tokens of one group), segment sigma.
-// Executed by whole warps; false: nothing to do.
-__device__ __forceinline__ bool prefix_work(const SharedArgs &s, int blk, int sigma, int block_q,
-                                            int lane, SharedWork &w) {
+// Prefix item `item` of the grid: a row block (block_q tokens of one group) and
+// a segment, segment-major.  Up to 32 groups are counted exactly (one lane
+// each), so that the grid's unused items stand at its end; more are found by
+// search over the key first_token / block_q + g, which leaves gaps.  Executed
+// by whole warps; false: nothing to do.
+__device__ __forceinline__ bool prefix_work(const SharedArgs &s, int item, int block_q, int lane,
+                                            SharedWork &w) {
   const AttnArgs &a = s.a;
-  const int g = find_last(s.num_groups, blk, lane, [&](int i) {
-    const int t = group_token(s, i);
-    return t == 0x7fffffff ? t : t / block_q + i;
-  });
-  const int c0 = group_token(s, g), c1 = group_token(s, g + 1);
-  const int P = s.prefix_lens[g];
-  if (c0 < 0 || c1 > a.num_tokens || c0 > c1 || P < 0) {
-    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
-    return false;
+  int g, tok0, sigma, c0, c1;
+  if (s.num_groups <= 32) {
+    int b0 = 0, b1 = 0;
+    if (lane < s.num_groups) {
+      b0 = group_token(s, lane);
+      b1 = group_token(s, lane + 1);
+    }
+    const int mine = b0 >= 0 && b1 <= a.num_tokens && b0 < b1 ? (b1 - b0 + block_q - 1) / block_q : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
+    if (total == 0 || item >= total * s.ns_p) return false;
+    const int blk = item % total;
+    sigma = item / total;
+    const unsigned past = __ballot_sync(0xffffffffu, upto > blk);
+    g = __ffs(past) - 1;
+    c0 = __shfl_sync(0xffffffffu, b0, g);
+    c1 = __shfl_sync(0xffffffffu, b1, g);
+    tok0 = (blk - __shfl_sync(0xffffffffu, upto - mine, g)) * block_q;
+  } else {
+    const int blk = item % s.n_pblocks;
+    sigma = item / s.n_pblocks;
+    if (sigma >= s.ns_p) return false;
+    g = find_last(s.num_groups, blk, lane, [&](int i) {
+      const int t = group_token(s, i);
+      return t == 0x7fffffff ? t : t / block_q + i;
+    });
+    c0 = group_token(s, g);
+    c1 = group_token(s, g + 1);
+    if (c0 < 0 || c1 > a.num_tokens) return false;  // the suffix items flag it
+    tok0 = (blk - (c0 / block_q + g)) * block_q;
+    if (tok0 < 0 || tok0 >= c1 - c0) return false;
   }
-  const int tok0 = (blk - (c0 / block_q + g)) * block_q;
-  if (tok0 < 0 || tok0 >= c1 - c0 || P == 0) return false;
+  const int P = s.prefix_lens[g];
+  if (P <= 0) return false;
   w.row = s.cu_groups[g];
   w.q0 = c0 + tok0;
   w.n_tok = min(block_q, c1 - c0 - tok0);
@@ -127,6 +157,13 @@ __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int blk, int si
   w.limit0 = w.kv_end - 1;
   w.limit_step = 0;
   return true;
+}
+
+// Row blocks of all groups at most: the items of one prefix segment.
+inline int prefix_blocks(int num_tokens, int num_groups, int block_q) {
+  return num_groups <= 32
+             ? static_cast<int>((num_tokens + static_cast<int64_t>(num_groups) * (block_q - 1)) / block_q)
+             : num_tokens / block_q + num_groups;
 }
 
 // Suffix item: row block `blk` (block_q tokens of one sequence), segment sigma.
@@ -155,9 +192,64 @@ __device__ __forceinline__ bool suffix_work(const SharedArgs &s, int blk, int si
   return true;
 }
 
-// Triple of row (token, q head), segment slot k.
-__device__ __forceinline__ int64_t triple_at(const SharedArgs &s, int token, int hh, int k) {
-  return (static_cast<int64_t>(token) * s.a.hq + hh) * (s.ns_p + s.ns_s) + k;
+// Where triples stand.  A row of kv head h is token * qpk + (q head - h * qpk),
+// so the rows of a block are consecutive; acc is [slot][h][D / 4][row][4], which
+// a block of any kernel writes (and the join reads) in whole sectors, and
+// (m, l) is [slot][h][row].
+__device__ __forceinline__ int64_t rows_total(const SharedArgs &s) {
+  return static_cast<int64_t>(s.a.num_tokens) * s.a.qpk;
+}
+// First row of slot k, head h in (m, l) pairs.
+__device__ __forceinline__ int64_t ml_at(const SharedArgs &s, int k, int h) {
+  return (static_cast<int64_t>(k) * s.a.hk + h) * rows_total(s);
+}
+// acc of slot k, head h: channel c of row r at + (c / 4) * rows_total * 4 + r * 4 + c % 4.
+template <int D>
+__device__ __forceinline__ float *acc_at(const SharedArgs &s, int k, int h) {
+  return s.a.part_acc + ml_at(s, k, h) * D;
+}
+
+// Programmatic launches.  The call's kernels work on disjoint triples, so each
+// is launched while its predecessor runs (launch_dependents at a block's start)
+// and fills the SMs beside it.  The last block of such a kernel waits for the
+// predecessor before it ends, so that a kernel's end implies the end of all
+// before it, which is what the join waits for.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// In a block of the grid's last one: whichever way a thread leaves, it waits.
+struct LastBlockWaits {
+  bool last;
+  __device__ ~LastBlockWaits() {
+    if (last) wait_for_predecessor();
+  }
+};
+
+// Launch attribute of a kernel that may start beside its predecessor.
+struct BesidePredecessor {
+  cudaLaunchAttribute attr[1];
+  BesidePredecessor() {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+};
+
+template <class... P, class... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                          cudaStream_t stream, bool beside, const A &...args) {
+  BesidePredecessor b;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = b.attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace paq8

@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
   const int seq = rest % a.num_seqs;
   const int sigma = rest / a.num_seqs;
 
+  launch_dependents();
+  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
   const int q_start = a.cu_seqlens_q[seq];
   const int q_len = a.cu_seqlens_q[seq + 1] - q_start;
   const int n_rows = rows_of(sa, q_len);
@@ -383,14 +385,16 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
   for (int c = 0; c < 2; ++c) {
     const int row = 2 * t + c;
     if (row >= n_rows) continue;
-    const int64_t at = triple_at(sa, q_start + row / a.qpk, h * a.qpk + row % a.qpk, sa.ns_p + sigma);
-    float *dst = a.part_acc + at * D;
+    const int64_t r = static_cast<int64_t>(q_start) * a.qpk + row, step = rows_total(sa) * 4;
+    float *dst = acc_at<D>(sa, sa.ns_p + sigma, h) + (g >> 2) * step + r * 4 + (g & 3);
 #pragma unroll
     for (int cm = 0; cm < Cfg::kCm; ++cm) {
-      dst[cm * 16 + g] = o[cm][c];
-      dst[cm * 16 + g + 8] = o[cm][2 + c];
+      dst[(cm * 4) * step] = o[cm][c];
+      dst[(cm * 4 + 2) * step] = o[cm][2 + c];
     }
-    if (g == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(m_run[c], l_run[c]);
+    if (g == 0)
+      *reinterpret_cast<float2 *>(a.part_ml + (ml_at(sa, sa.ns_p + sigma, h) + r) * 2) =
+          make_float2(m_run[c], l_run[c]);
   }
 }
 
@@ -405,8 +409,8 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(s.a.num_seqs) * s.ns_s * s.a.hk;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  shared_rows_kernel<D, BS, F8><<<static_cast<unsigned>(grid), kThreads, Cfg::kSmem, stream>>>(s);
-  return cudaGetLastError();
+  return launch_kernel(shared_rows_kernel<D, BS, F8>, dim3(static_cast<unsigned>(grid)), kThreads,
+                       Cfg::kSmem, stream, true, s);
 }
 
 cudaError_t launch_shared_rows(const SharedArgs &s, int d, int bs, bool f8v4, cudaStream_t stream) {

@@ -67,7 +67,8 @@ enum : int {
 };
 
 template <int D, int BS, bool F8>
-__global__ void __launch_bounds__(512, 1)
+// at most 96 registers, so that a block of the rows kernel fits beside it
+__global__ void __maxnreg__(96)
     shared_tc_kernel(const __grid_constant__ SharedArgs sa, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v) {
   using C = SharedTcCfg<D, BS, F8>;
@@ -79,15 +80,29 @@ __global__ void __launch_bounds__(512, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
+  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(sa.a.hk));
 
+  launch_dependents();
   SharedWork w;
-  const int bx = static_cast<int>(blockIdx.x);
-  if (!prefix_work(sa, bx % sa.n_pblocks, bx / sa.n_pblocks, a.block_q, lane, w)) return;
+  if (!prefix_work(sa, static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk)), a.block_q, lane, w))
+    return;
   const int n_rows = w.n_tok * a.qpk;
   const int kv_begin = w.kv_begin, kv_end = w.kv_end;  // kv_begin starts a tile
   const int t0 = kv_begin / C::kTile;
   const int nt = (kv_end + C::kTile - 1) / C::kTile - t0;
+  // the softmax warps' q rows, one per thread: in flight during the set-up
+  const bool softmax_warp = warp >= 6 && warp < 14;
+  const int q_row = ((warp - 6) >> 2) * 128 + (warp & 3) * 32 + lane;
+  uint4 qv[D / 8];
+  if (softmax_warp) {
+    const bool valid = q_row < n_rows;
+    const int tq = valid ? q_row / a.qpk : 0;
+    const uint16_t *src =
+        a.q + (static_cast<int64_t>(w.q0 + tq) * a.hq + h * a.qpk + (valid ? q_row % a.qpk : 0)) * D;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+      qv[c] = valid ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+  }
   // half 1 holds no valid row when the block is short: it is then skipped
   const int halves = n_rows > 128 ? 2 : 1;
 
@@ -363,20 +378,16 @@ __global__ void __launch_bounds__(512, 1)
     const int row = hf * 128 + lrow;
     const uint32_t t_lane = tmem + hf * C::kHalfCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const bool valid = row < n_rows;
-    const int tq = valid ? row / a.qpk : 0;
-    const int hh = h * a.qpk + (valid ? row % a.qpk : 0);
     const float sl2 = a.scale_log2;
     // q row -> fp16 pairs in this lane's q columns (the QK MMA's A operand)
     {
-      const uint16_t *src = a.q + (static_cast<int64_t>(w.q0 + tq) * a.hq + hh) * D;
       bool bad_q = false;
-#pragma unroll 1
+#pragma unroll
       for (int cb = 0; cb < D / 64; ++cb) {
         uint32_t qw[32];
 #pragma unroll
         for (int c16 = 0; c16 < 8; ++c16) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (valid) v = *reinterpret_cast<const uint4 *>(src + cb * 64 + c16 * 8);
+          const uint4 v = qv[cb * 8 + c16];
           qw[4 * c16 + 0] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
           qw[4 * c16 + 1] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
           qw[4 * c16 + 2] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));
@@ -489,8 +500,8 @@ __global__ void __launch_bounds__(512, 1)
       // ---- epilogue: the row's triple
       if (ok && mbar_wait(bar(kBarPvDone + hf), 0)) {
         tc::fence_after();
-        const int64_t at = triple_at(sa, w.q0 + tq, hh, w.slot);
-        float *dst = a.part_acc + at * D;
+        const int64_t r = static_cast<int64_t>(w.q0) * a.qpk + row, step = rows_total(sa) * 4;
+        float *dst = acc_at<D>(sa, w.slot, h) + r * 4;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t orr[32];
@@ -499,11 +510,13 @@ __global__ void __launch_bounds__(512, 1)
           if (valid) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4 *>(dst + cb * 32 + i) =
+              *reinterpret_cast<uint4 *>(dst + (cb * 8 + i / 4) * step) =
                   make_uint4(orr[i], orr[i + 1], orr[i + 2], orr[i + 3]);
           }
         }
-        if (valid) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(m_used, l);
+        if (valid)
+          *reinterpret_cast<float2 *>(a.part_ml + (ml_at(sa, w.slot, h) + r) * 2) =
+              make_float2(m_used, l);
       } else {
         ok = false;
       }
@@ -529,11 +542,11 @@ static cudaError_t launch_shared_tc_t(const SharedArgs &s, const CUtensorMap &tk
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p;
+  const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p * s.a.hk;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s.a.hk));
-  shared_tc_kernel<D, BS, F8><<<grid, C::kWarps * 32, C::kSmem, stream>>>(s, tk, tv);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(gx));
+  return launch_kernel(shared_tc_kernel<D, BS, F8>, grid, C::kWarps * 32, C::kSmem, stream, false, s, tk,
+                       tv);
 }
 
 // Rows of one block, 0 where the kernel does not take the head size.

@@ -27,7 +27,7 @@ namespace paq8 {
 namespace {
 
 constexpr int kWarps = 8;          // sequences per block
-constexpr int kTokenChunk = 1024;  // tokens of a sequence per block
+constexpr int kTokenChunk = 256;   // tokens of a sequence per block
 constexpr int kPageChunk = 1024;   // pages of a sequence per block
 
 struct SeqPlan {
@@ -159,19 +159,35 @@ __global__ void __launch_bounds__(kWarps * 32) block_tables_kernel(const BlockTa
     const bool in_place = dst == src;
     const int split = max(pl, min(ph, me.first));  // old entries end here
     if (!in_place) {
-      const int n = split - pl;
-      const bool wide = ((reinterpret_cast<uintptr_t>(dst + pl) |
-                          reinterpret_cast<uintptr_t>(src + pl)) & 15u) == 0;
-      if (wide && row_ok && split <= p.source_stride) {
-        const int4 *a = reinterpret_cast<const int4 *>(src + pl);
-        int4 *b = reinterpret_cast<int4 *>(dst + pl);
-#pragma unroll 8
-        for (int i = lane; i < n / 4; i += 32) b[i] = a[i];
-        for (int i = (n & ~3) + lane; i < n; i += 32) dst[pl + i] = src[pl + i];
-      } else {
-#pragma unroll 8
-        for (int i = lane; i < n; i += 32) dst[pl + i] = old_entry(pl + i);
+      // entries that the source row has, a batch of loads ahead of their stores
+      const int have = row_ok ? max(pl, min(split, p.source_stride)) : pl;
+      const int n = have - pl;
+      constexpr int kBatch = 8;
+      int i = lane;
+      if (((reinterpret_cast<uintptr_t>(dst + pl) | reinterpret_cast<uintptr_t>(src + pl)) & 15u) == 0) {
+        const int4 *from = reinterpret_cast<const int4 *>(src + pl);
+        int4 *to = reinterpret_cast<int4 *>(dst + pl);
+        for (; i < n / 4; i += 32 * kBatch) {
+          int4 v[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (i + 32 * j < n / 4) v[j] = from[i + 32 * j];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (i + 32 * j < n / 4) to[i + 32 * j] = v[j];
+        }
+        i = (n & ~3) + lane;
       }
+      for (; i < n; i += 32 * kBatch) {
+        int v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (i + 32 * j < n) v[j] = src[pl + i + 32 * j];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (i + 32 * j < n) dst[pl + i + 32 * j] = v[j];
+      }
+      for (int page = have + lane; page < split; page += 32) dst[page] = -1;
     }
     for (int page = split + lane; page < ph; page += 32) dst[page] = new_entry(page);
 
