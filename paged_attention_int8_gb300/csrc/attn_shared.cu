@@ -397,10 +397,13 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const __grid_constant_
     const int seq = find_seq(a.cu_seqlens_q, a.num_seqs, 1, tk, lane);
     const int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1];
     if (c0 < 0 || tk < c0 || tk >= c1 || c1 > a.num_tokens) continue;  // a row no sequence owns
-    const int P = prefix_of(s, seq, lane);
+    int g = 0;
+    const int P = prefix_of(s, seq, lane, &g);
     const int ctx = a.seq_lens[seq] - (c1 - c0);
     // flagged by the suffix item
     if (P < 0 || ctx < P || rows_of(s, c1 - c0) > s.max_rows) continue;
+    const int g0 = group_token(s, g), g1 = group_token(s, g + 1);
+    if (g0 < 0 || g0 > tk || tk >= g1 || g1 > a.num_tokens) continue;  // its prefix was not taken
     if (tk == tok) {
       n_p = shared_segments(0, P, s.seg_p, s.ns_p);
       n_s = shared_segments(P, ctx + tk - c0 + 1, s.seg_s, s.ns_s);

@@ -64,8 +64,10 @@ __device__ __forceinline__ int group_token(const SharedArgs &s, int g) {
 
 // The prefix length that sequence seq shares, -1 when no group holds it or
 // the group's entries are out of range.
-__device__ __forceinline__ int prefix_of(const SharedArgs &s, int seq, int lane) {
+__device__ __forceinline__ int prefix_of(const SharedArgs &s, int seq, int lane,
+                                         int *group = nullptr) {
   const int g = find_last(s.num_groups, seq, lane, [&](int i) { return s.cu_groups[i]; });
+  if (group) *group = g;
   if (s.cu_groups[g] > seq || s.cu_groups[g + 1] <= seq) return -1;
   return s.prefix_lens[g];
 }

@@ -4,13 +4,18 @@
 // of the decode kernel (attn_decode.cu): keys in the MMA's M dimension, rows in
 // its N dimension,
 //   S^T[16 keys x 8 rows] = K[16 x 16 ch] . Q^T[16 ch x 8],
-//   O^T[16 ch x 8 rows] += V^T[16 ch x 16 keys] . P^T[16 keys x 8],
-// four consumer warps on the 16-key blocks of each 64-key tile (32-key tiles
-// at D = 256, pairs of warps on alternate tiles) with private softmax states
-// merged at the end, one producer warp copying pages with 16-byte cp.async
-// into a 3-stage ring (4 at D = 256). Each row has its own causal limit, taken
-// on edge tiles only. HBM bound: 2 (D + D / 16) bytes a key and kv head (q8),
-// D + D / 2 + 4 (fp8 / 4-bit); each block leaves one fp32 triple per row.
+//   O^T[16 ch x 8 rows] += V^T[16 ch x 16 keys] . P^T[16 keys x 8].
+// Each row has its own causal limit, taken on edge blocks only.  HBM bound:
+// 2 (D + D / 16) bytes a key and kv head (q8), D + D / 2 + 4 (fp8 / 4-bit).
+//
+// Four warps share a segment's 16-key blocks round robin, each on its own: it
+// copies its blocks with 16-byte cp.async into a private 3-stage ring and reads
+// them back, so that no warp waits for another until the four softmax states
+// are merged at the end (one fp32 triple per row).  No producer warp, because
+// four warps of at most 128 registers fit beside a block of the tensor-core
+// kernel (its 16 warps leave 4096 registers of each SM sub-partition, one warp's;
+// a fifth warp would double up on one): the prefix, bound by the tensor core, and
+// the suffixes, bound by HBM, then share every SM from the start.
 #include <type_traits>
 
 #include "attn_shared.cuh"
@@ -45,31 +50,107 @@ __device__ __forceinline__ void load_key_scales(uint32_t addr, float (&f)[G]) {
   }
 }
 
-template <int D, int BS, bool F8>
-struct SharedRowsCfg {
-  static constexpr int kTile = D == 256 ? 32 : 64;
-  using L = std::conditional_t<F8, StageF8V4<D, BS, kTile>, StageLayout<D, BS, kTile>>;
-  static constexpr int kMt = kTile / 16;   // 16-key blocks per tile
-  static constexpr int kWpt = kMt < kConsumerWarps ? kMt : kConsumerWarps;  // warps per tile
-  static constexpr int kKg = kConsumerWarps / kWpt;  // tile groups (alternate tiles)
-  static constexpr int kCm = D / 16;       // 16-channel blocks of the output
+// One stage: a block of 16 keys.
+//   K  [16][D] codes, rows of 128 bytes (D = 64: of 64, D = 256: two halves)
+//   V  [D][16] codes (fp8 / 4-bit: [D][8], two keys a byte)
+//   scales: K [16][G], V [G][16] fp16 (fp8 / 4-bit: scale [16], zero [16])
+template <int D, bool F8>
+struct RowsStage {
   static constexpr int G = D / 32;
-  static constexpr int kSt = D == 256 ? 4 : 3;          // ring stages
-  static constexpr int kMinBlocks = D == 256 ? 2 : 4;   // blocks per SM
-  static constexpr int kSmem = kSt * L::kBytes + 2 * kSt * 8 + 1024;
+  static constexpr int kVOff = 16 * D;
+  static constexpr int kVBytes = F8 ? 8 * D : 16 * D;
+  static constexpr int kKsOff = kVOff + kVBytes;        // fp8 / 4-bit: V scales
+  static constexpr int kVsOff = kKsOff + (F8 ? 32 : 32 * G);  // fp8 / 4-bit: V zeros
+  static constexpr int kBytes = (kVsOff + (F8 ? 32 : 32 * G) + 127) / 128 * 128;
+  // Byte b of key row r.  A lane of the MMA fragment (g, t) reads 8 bytes at 8t
+  // of key perm16(g): the 16-byte pieces of a row are permuted so that the four
+  // rows of a phase (0, 1, 4, 5 or 8, 9, 12, 13; 2 more for the second half)
+  // stand in different banks.
+  __device__ static __forceinline__ uint32_t k_off(int r, int b) {
+    if constexpr (D >= 128) {
+      const int i = (r & 1) | ((r >> 2) << 1);
+      const int off = r * 128 + (b & 127);
+      return (b >> 7) * (16 * 128) + (off ^ ((((i & 3) << 1) | (i >> 2)) << 4));
+    } else {
+      const int off = r * 64 + b;
+      return off ^ (((r >> 2) & 1) << 5);
+    }
+  }
 };
 
 template <int D, int BS, bool F8>
-__global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks)
+struct SharedRowsCfg {
+  using L = RowsStage<D, F8>;
+  static constexpr int kWarps = 4;
+  static constexpr int kSt = 3;
+  static constexpr int kCm = D / 16;                    // 16-channel blocks of the output
+  static constexpr int G = D / 32;
+  static constexpr int kMinBlocks = D == 256 ? 2 : 4;   // blocks per SM
+  static constexpr int kRing = kWarps * kSt * L::kBytes;
+  static constexpr int kMerge = (kWarps - 1) * 32 * (4 + 4 * kCm) * 4;
+  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
+};
+
+// This lane's share of the copy of 16-key block `half` (of BS / 16) of page
+// `page` (block id * hk + kv head) into the stage at `st`.
+template <int D, int BS, bool F8>
+__device__ __forceinline__ void copy_rows_block(const AttnArgs &a, uint32_t st, int64_t page, int half,
+                                                int lane) {
+  using L = RowsStage<D, F8>;
+  constexpr int G = D / 32;
+  const uint8_t *k = reinterpret_cast<const uint8_t *>(a.k_cache) + page * (BS * D) + half * (16 * D);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int c = lane + 32 * i;
+    cp_async16(st + L::k_off(c / (D / 16), (c % (D / 16)) * 16), k + c * 16);
+  }
+  const uint8_t *v = reinterpret_cast<const uint8_t *>(a.v_cache);
+  if constexpr (!F8) {
+    v += page * (BS * D) + half * 16;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int c = lane + 32 * i;  // channel
+      cp_async16(st + L::kVOff + c * 16, v + c * BS);
+    }
+    // 2 G pieces of K scales, then 2 G of V scales (G rows of BS)
+    const uint8_t *ks = reinterpret_cast<const uint8_t *>(a.k_scale) + page * (BS * G * 2) + half * (32 * G);
+    const uint8_t *vs = reinterpret_cast<const uint8_t *>(a.v_scale) + page * (BS * G * 2) + half * 32;
+    if (lane < 4 * G) {
+      const int c = lane < 2 * G ? lane : lane - 2 * G;
+      cp_async16(st + (lane < 2 * G ? L::kKsOff : L::kVsOff) + c * 16,
+                 lane < 2 * G ? ks + c * 16 : vs + (c >> 1) * (BS * 2) + (c & 1) * 16);
+    }
+  } else {
+    v += page * (BS * D / 2) + half * 8;
+    if constexpr (BS == 16) {
+#pragma unroll
+      for (int i = 0; i < (D / 2 + 31) / 32; ++i) {
+        const int c = lane + 32 * i;  // two channels
+        if (D / 2 >= 32 || c < D / 2) cp_async16(st + L::kVOff + c * 16, v + c * 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int c = lane + 32 * i;
+        cp_async_8(st + L::kVOff + c * 8, v + c * (BS / 2));
+      }
+    }
+    if (lane < 4) {
+      const uint8_t *s = reinterpret_cast<const uint8_t *>(lane < 2 ? a.v_scale : a.v_zero);
+      cp_async16(st + (lane < 2 ? L::kKsOff : L::kVsOff) + (lane & 1) * 16,
+                 s + page * (BS * 2) + half * 32 + (lane & 1) * 16);
+    }
+  }
+}
+
+template <int D, int BS, bool F8>
+__global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
     shared_rows_kernel(const __grid_constant__ SharedArgs sa) {
   using Cfg = SharedRowsCfg<D, BS, F8>;
   using L = typename Cfg::L;
   constexpr int G = Cfg::G;
-  constexpr int kTile = Cfg::kTile;
-  constexpr int kWpt = Cfg::kWpt;
-  constexpr int kKg = Cfg::kKg;
-  constexpr int kStages = Cfg::kSt;
-  static_assert(kStages % kKg == 0, "a stage always feeds the same tile group");
+  constexpr int kWarps = Cfg::kWarps;
+  constexpr int kSt = Cfg::kSt;
   const AttnArgs &a = sa.a;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -105,32 +186,35 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
   SharedWork w;
   if (!segment_keys(P, seq_len, sa.seg_s, sa.ns_s, sigma, w)) return;
   const int kv_begin = w.kv_begin, kv_end = w.kv_end;
-  const int tile_lo = kv_begin / kTile;
-  const int n_iter = (kv_end + kTile - 1) / kTile - tile_lo;
-
-  constexpr int kMergeBytes = 3 * 32 * (4 + 4 * Cfg::kCm) * 4;
-  constexpr int kRingBytes = kStages * L::kBytes;
-  static_assert(kMergeBytes <= kRingBytes, "merge area fits in the ring");
-  const uint32_t bar_full = smem_base + kRingBytes;
-  const uint32_t bar_empty = bar_full + kStages * 8;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar_full + 8 * i, 32);    // one arrival per producer lane
-      mbar_init(bar_empty + 8 * i, kWpt);  // every warp of the tile group reads it
+  // this warp's 16-key blocks: b0, b0 + 4, ...
+  const int b0 = kv_begin / 16 + warp;
+  const int n_blk = max(0, ((kv_end + 15) / 16 - b0 + kWarps - 1) / kWarps);
+  const uint32_t ring = smem_base + warp * (kSt * L::kBytes);
+  const int32_t *bt_row = a.block_table + static_cast<int64_t>(seq) * a.bt_stride;
+  int held = -1;  // block id of this lane's block: number (i / 32) * 32 + lane of this warp's
+  // block ids of the warp's blocks i .. i + 31 (-1: a bad entry, flagged and masked by no copy)
+  auto load_ids = [&](int i) {
+    held = -1;
+    if (i + lane < n_blk) {
+      const int lp = static_cast<int>((static_cast<int64_t>(b0) + kWarps * (i + lane)) / (BS / 16));
+      const int b = lp < a.bt_stride ? bt_row[lp] : -1;
+      if (b >= 0 && b < a.num_blocks) held = b;
+      else flag_status(a.status, PA_DEV_BAD_BLOCK);
     }
-    fence_barrier_init();
-  }
-  __syncthreads();
-
-  if (warp == kConsumerWarps) {
-    if constexpr (F8)
-      produce_f8v4<L, BS, kStages>(a, smem_base, bar_full, bar_empty, seq, h, tile_lo, n_iter,
-                                   kv_begin, kv_end, lane);
-    else
-      produce_tiles_lsu<L, BS, kStages>(a, smem_base, bar_full, bar_empty, seq, h, tile_lo,
-                                        n_iter, kv_begin, kv_end, lane);
-    return;
-  }
+  };
+  // block i's copy into its stage, one commit group per block
+  auto issue = [&](int i) {
+    if (i < n_blk) {
+      if ((i & 31) == 0) load_ids(i);
+      const int id = __shfl_sync(0xffffffffu, held, i & 31);
+      if (id >= 0)
+        copy_rows_block<D, BS, F8>(a, ring + (i % kSt) * L::kBytes, static_cast<int64_t>(id) * a.hk + h,
+                                   BS == 32 ? (b0 + kWarps * i) & 1 : 0, lane);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kSt - 1; ++i) issue(i);
 
   const int g = lane >> 2;
   const int t = lane & 3;
@@ -174,23 +258,16 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
 
-  // Warp w takes the 16-key block mt = w % kWpt of every tile of its tile
-  // group (w / kWpt): all warps read every stage, so the whole ring is in
-  // flight for each of them.
-  const int my_mt = warp % kWpt;
-  const int kg = warp / kWpt;
-  bool timed_out = false;
-  for (int it = kg; it < n_iter; it += kKg) {
-    const int stage = it % kStages;
-    if (!mbar_wait(bar_full + 8 * stage, (it / kStages) & 1, a.wait_limit_ns)) {
-      timed_out = true;
-      break;
-    }
-    const uint32_t st = smem_base + stage * L::kBytes;
-    const int key0 = (tile_lo + it) * kTile + my_mt * 16;  // first key of this warp's block
+#pragma unroll 1
+  for (int i = 0; i < n_blk; ++i) {
+    cp_async_wait<kSt - 2>();
+    __syncwarp();  // block i has landed for every lane, block i - 1 is read by every lane
+    issue(i + kSt - 1);
+    const uint32_t st = ring + (i % kSt) * L::kBytes;
+    const int key0 = (b0 + kWarps * i) * 16;
     // keys outside [kv_begin, kv_end) in this block: masked, V zeroed (stale
     // bytes may sit there); keys past a row's own limit masked.  Formed on edge
-    // tiles only.
+    // blocks only.
     const bool tail = key0 + 16 > all_end || key0 < kv_begin;
     uint2 vmask = make_uint2(0xffffffffu, 0xffffffffu);
     if (tail) {
@@ -204,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
     // keys exact in one accumulation
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     {
-      const int k0 = my_mt * 16 + r0, k1 = my_mt * 16 + r1;
+      const int k0 = r0, k1 = r1;
       if constexpr (F8) {
 #pragma unroll
         for (int gq = 0; gq < G; ++gq) {
@@ -220,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
         }
       } else {
         float ks0[G], ks1[G];
-        load_key_scales<G>(st + L::ks_off(k0, 0), ks0);
-        load_key_scales<G>(st + L::ks_off(k1, 0), ks1);
+        load_key_scales<G>(st + L::kKsOff + k0 * G * 2, ks0);
+        load_key_scales<G>(st + L::kKsOff + k1 * G * 2, ks1);
 #pragma unroll
         for (int gq = 0; gq < G; ++gq) {
           const uint2 c0 = lds64(st + L::k_off(k0, gq * 32 + t * 8));
@@ -290,16 +367,16 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
     // ---------------- O^T += V'^T P^T, V' = code * scale (fp8 / 4-bit: idx * scale
     // + zero) in fp16
     if constexpr (F8) {
-      uint2 vsc = lds64(st + L::vs_off(my_mt * 16 + 4 * t));
-      uint2 vzr = lds64(st + L::vz_off(my_mt * 16 + 4 * t));
+      uint2 vsc = lds64(st + L::kKsOff + 8 * t);
+      uint2 vzr = lds64(st + L::kVsOff + 8 * t);
       vsc.x &= vmask.x;
       vsc.y &= vmask.y;
       vzr.x &= vmask.x;
       vzr.y &= vmask.y;
 #pragma unroll
       for (int cm = 0; cm < Cfg::kCm; ++cm) {
-        const uint32_t w0 = lds16(st + L::v_off(cm * 16 + g, my_mt * 16 + 4 * t));
-        const uint32_t w1 = lds16(st + L::v_off(cm * 16 + g + 8, my_mt * 16 + 4 * t));
+        const uint32_t w0 = lds16(st + L::kVOff + (cm * 16 + g) * 8 + 2 * t);
+        const uint32_t w1 = lds16(st + L::kVOff + (cm * 16 + g + 8) * 8 + 2 * t);
         uint32_t a0, a2, a1, a3;
         nibbles4_to_half2(w0, a0, a2);  // channel g: keys 4t, 4t+1 | 4t+2, 4t+3
         nibbles4_to_half2(w1, a1, a3);  // channel g + 8
@@ -312,14 +389,14 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
     } else {
 #pragma unroll
       for (int gv = 0; gv < G; ++gv) {
-        uint2 vsc = lds64(st + L::vs_off(my_mt * 16 + 4 * t, gv));
+        uint2 vsc = lds64(st + L::kVsOff + (gv * 16 + 4 * t) * 2);
         vsc.x &= vmask.x;
         vsc.y &= vmask.y;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int cm = gv * 2 + half;
-          const uint32_t w0 = lds32(st + L::v_off(cm * 16 + g, my_mt * 16 + 4 * t));
-          const uint32_t w1 = lds32(st + L::v_off(cm * 16 + g + 8, my_mt * 16 + 4 * t));
+          const uint32_t w0 = lds32(st + L::kVOff + (cm * 16 + g) * 16 + 4 * t);
+          const uint32_t w1 = lds32(st + L::kVOff + (cm * 16 + g + 8) * 16 + 4 * t);
           uint32_t a0, a2, a1, a3;
           codes4_to_half2(w0, a0, a2);  // channel g: keys 4t..4t+1 | 4t+2..4t+3
           codes4_to_half2(w1, a1, a3);  // channel g + 8
@@ -331,10 +408,7 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * stage);
   }
-  if (timed_out && lane == 0) flag_status(a.status, PA_DEV_TIMEOUT);
 
   // expsum of each row: sum over the 8 lanes that share t
 #pragma unroll
@@ -344,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
 
   // ---------------- merge the 4 warps (field-major through shared memory)
   constexpr int kFields = 4 + 4 * Cfg::kCm;
-  named_barrier(1, kConsumerWarps * 32);  // every stage consumed: reuse the ring
+  cp_async_wait<0>();
+  __syncthreads();  // every block consumed: reuse the rings
   if (warp > 0) {
     float *dst = smem_f + (warp - 1) * kFields * 32 + lane;
     dst[0] = m_run[0];
@@ -356,10 +431,10 @@ __global__ void __launch_bounds__(kThreads, SharedRowsCfg<D, BS, F8>::kMinBlocks
 #pragma unroll
       for (int e = 0; e < 4; ++e) dst[(4 + i * 4 + e) * 32] = o[i][e];
   }
-  named_barrier(1, kConsumerWarps * 32);
+  __syncthreads();
   if (warp > 0) return;
 #pragma unroll 1
-  for (int k = 0; k < kConsumerWarps - 1; ++k) {
+  for (int k = 0; k < kWarps - 1; ++k) {
     const float *src = smem_f + k * kFields * 32 + lane;
     float wa[2], wb[2];
 #pragma unroll
@@ -403,13 +478,17 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
   using Cfg = SharedRowsCfg<D, BS, F8>;
   static DeviceOnce configured;
   cudaError_t e = configured.get(nullptr, [](int, int *) {
-    return cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    cudaError_t r = cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    // the tensor-core kernel's carveout, so that blocks of both are resident together
+    return r != cudaSuccess ? r
+                            : cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8>,
+                                                   cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(s.a.num_seqs) * s.ns_s * s.a.hk;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_kernel(shared_rows_kernel<D, BS, F8>, dim3(static_cast<unsigned>(grid)), kThreads,
+  return launch_kernel(shared_rows_kernel<D, BS, F8>, dim3(static_cast<unsigned>(grid)), 128,
                        Cfg::kSmem, stream, true, s);
 }
 

@@ -78,7 +78,7 @@ __global__ void __maxnreg__(96)
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (smem_base - smem_u32(smem_raw));
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(sa.a.hk));
 
@@ -150,62 +150,64 @@ __global__ void __maxnreg__(96)
                                    bar(kBarStEmpty), w.row, h, t0, nt, kv_begin, kv_end, lane);
   } else if (warp == 1) {
     // ============================================================ MMA issuer
-    // The whole warp runs this loop (uniform values, no divergence); the
-    // elected lane issues every MMA and commit.
-    const uint32_t leader = tc::elect_one();
-    constexpr uint32_t id_qk = tc::idesc_f16(128, 64);
-    constexpr uint32_t id_qk_neg = id_qk | (1u << 14);  // negate B: K_lo is stored as -lo
-    constexpr uint32_t id_pv = tc::idesc_f16(128, D);
-    auto wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity)); };
-    // O(half) += P(i, half) V'(i): A = P from the half's S/P columns
-    auto issue_pv = [&](int i, int hf) -> bool {
-      const int b = i & 1;
-      if (hf == 0 && !wait(kBarVFull + b, (i >> 1) & 1)) return false;
-      if (!wait(kBarPFull + hf, i & 1)) return false;
-      tc::fence_after();
-      const uint64_t v_desc = tc::desc_sw128(smem_base + C::kVOff + b * C::kVBytes);
-      const uint32_t base = tmem + hf * C::kHalfCols;
-#pragma unroll
-      for (int ks = 0; ks < C::kTile / 16; ++ks)  // +32 bytes of K per step
-        tc::mma_f16_ts_by(leader, base + C::kOCol, base + ks * 8, v_desc + 2 * ks, id_pv,
-                          (i > 0 || ks > 0) ? 1u : 0u);
-      return true;
-    };
-    // S(half) = q K_hi(j)^T - q (-K_lo(j))^T: A = q from the half's TMEM columns
-    auto issue_qk = [&](int j, int hf) {
-      const uint64_t k_desc = tc::desc_sw128(smem_base + C::kKOff + (j & 1) * C::kKSlot);
-      const uint32_t base = tmem + hf * C::kHalfCols;
-#pragma unroll
-      for (int part = 0; part < (F8 ? 1 : 2); ++part)  // F8: exact keys, no K_lo part
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t koff = part * C::kKBytes + (ks >> 2) * (64 * 128) + (ks & 3) * 32;
-          tc::mma_f16_ts_by(leader, base, base + C::kQCol + ks * 8, k_desc + (koff >> 4),
-                            part ? id_qk_neg : id_qk, (part > 0 || ks > 0) ? 1u : 0u);
-        }
-      tc::commit_by(leader, bar(kBarSFull + hf));
-    };
-    ok = wait(kBarQFull, 0);
-    tc::fence_after();
-    for (int j = 0; ok && j < nt; ++j) {
-      const int b = j & 1;
-      for (int hf = 0; hf < halves; ++hf) {
-        // the half's S/P buffer is free once PV(j - 1) is issued: MMAs from
-        // this warp execute in order
-        if (j >= 1 && !issue_pv(j - 1, hf)) { ok = false; break; }
-        if (hf == 0 && !wait(kBarKFull + b, (j >> 1) & 1)) { ok = false; break; }
+    // One elected lane runs the whole loop: under `elect` the compiler knows that
+    // one thread is there and an MMA costs 5 instructions (18 under a predicate
+    // or a branch on an earlier election, so that the issue, not the tensor core,
+    // set the pace: 148 us against 138 on 128 requests and 32768 keys).
+    if (tc::elect_one()) {
+      constexpr uint32_t id_qk = tc::idesc_f16(128, 64);
+      constexpr uint32_t id_qk_neg = id_qk | (1u << 14);  // negate B: K_lo is stored as -lo
+      constexpr uint32_t id_pv = tc::idesc_f16(128, D);
+      // O(half) += P(i, half) V'(i): A = P from the half's S/P columns
+      auto issue_pv = [&](int i, int hf) -> bool {
+        const int b = i & 1;
+        if (hf == 0 && !mbar_wait(bar(kBarVFull + b), (i >> 1) & 1)) return false;
+        if (!mbar_wait(bar(kBarPFull + hf), i & 1)) return false;
         tc::fence_after();
-        issue_qk(j, hf);
+        const uint64_t v_desc = tc::desc_sw128(smem_base + C::kVOff + b * C::kVBytes);
+        const uint32_t base = tmem + hf * C::kHalfCols;
+#pragma unroll
+        for (int ks = 0; ks < C::kTile / 16; ++ks)  // +32 bytes of K per step
+          tc::mma_f16_ts(base + C::kOCol, base + ks * 8, v_desc + 2 * ks, id_pv,
+                         (i > 0 || ks > 0) ? 1u : 0u);
+        return true;
+      };
+      // S(half) = q K_hi(j)^T - q (-K_lo(j))^T: A = q from the half's TMEM columns
+      auto issue_qk = [&](int j, int hf) {
+        const uint64_t k_desc = tc::desc_sw128(smem_base + C::kKOff + (j & 1) * C::kKSlot);
+        const uint32_t base = tmem + hf * C::kHalfCols;
+#pragma unroll
+        for (int part = 0; part < (F8 ? 1 : 2); ++part)  // F8: exact keys, no K_lo part
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t koff = part * C::kKBytes + (ks >> 2) * (64 * 128) + (ks & 3) * 32;
+            tc::mma_f16_ts(base, base + C::kQCol + ks * 8, k_desc + (koff >> 4),
+                           part ? id_qk_neg : id_qk, (part > 0 || ks > 0) ? 1u : 0u);
+          }
+        tc::commit(bar(kBarSFull + hf));
+      };
+      ok = mbar_wait(bar(kBarQFull), 0);
+      tc::fence_after();
+      for (int j = 0; ok && j < nt; ++j) {
+        const int b = j & 1;
+        for (int hf = 0; hf < halves; ++hf) {
+          // the half's S/P buffer is free once PV(j - 1) is issued: MMAs from
+          // this thread execute in order
+          if (j >= 1 && !issue_pv(j - 1, hf)) { ok = false; break; }
+          if (hf == 0 && !mbar_wait(bar(kBarKFull + b), (j >> 1) & 1)) { ok = false; break; }
+          tc::fence_after();
+          issue_qk(j, hf);
+        }
+        if (!ok) break;
+        tc::commit(bar(kBarKEmpty + b));
+        if (j >= 1) tc::commit(bar(kBarVEmpty + (b ^ 1)));
       }
-      if (!ok) break;
-      tc::commit_by(leader, bar(kBarKEmpty + b));
-      if (j >= 1) tc::commit_by(leader, bar(kBarVEmpty + (b ^ 1)));
+      for (int hf = 0; ok && hf < halves; ++hf) {
+        if (!issue_pv(nt - 1, hf)) { ok = false; break; }
+        tc::commit(bar(kBarPvDone + hf));
+      }
     }
-    for (int hf = 0; ok && hf < halves; ++hf) {
-      if (!issue_pv(nt - 1, hf)) { ok = false; break; }
-      tc::commit_by(leader, bar(kBarPvDone + hf));
-    }
-    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);
   } else if (warp < 6 || warp >= 14) {
     // ============================================================ dequant
     // warps 0, 2, 3, 14: K (hi and lo parts), thread = one key row, D/2 channels
@@ -538,8 +540,12 @@ static cudaError_t launch_shared_tc_t(const SharedArgs &s, const CUtensorMap &tk
   using C = SharedTcCfg<D, BS, F8>;
   static DeviceOnce configured;
   cudaError_t e = configured.get(nullptr, [](int, int *) {
-    return cudaFuncSetAttribute(shared_tc_kernel<D, BS, F8>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t r = cudaFuncSetAttribute(shared_tc_kernel<D, BS, F8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    // all of the SM's shared memory, so that a block of the rows kernel fits beside
+    return r != cudaSuccess ? r
+                            : cudaFuncSetAttribute(shared_tc_kernel<D, BS, F8>,
+                                                   cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != cudaSuccess) return e;
   const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p * s.a.hk;

@@ -65,6 +65,40 @@ def test_segments(cuda_device, fmt, d, bs, squeeze):
     S.check(b, *b.call(workspace=ws))
 
 
+# many groups: shares of several short prefixes each, last rows that fill less
+# than half a block, more groups than a warp has lanes, prefixes of no key
+@pytest.mark.parametrize("fmt,hq,hk,d,bs", [("q8", 16, 1, 64, 16), ("q8", 16, 4, 128, 32),
+                                            ("f8v4", 16, 2, 128, 16), ("q8", 14, 2, 64, 32)])
+@pytest.mark.parametrize("n_groups", [2, 31, 33, 70])
+def test_many_groups(cuda_device, fmt, hq, hk, d, bs, n_groups):
+    sizes = [(7 * i) % 9 + 5 for i in range(n_groups)]
+    sizes[0] = 40
+    groups = [((37 * i) % 230 if i % 5 else 0, [(1, 1 + (3 * j + i) % 4) for j in range(n)])
+              for i, n in enumerate(sizes)]
+    b = S.make(n_groups, cuda_device, fmt, hq, hk, d, bs, groups)
+    ref = S.reference(b)
+    S.check(b, *b.call(), ref=ref)
+    # one segment each
+    ws = torch.zeros(256 + b.q.shape[0] * b.hq * 2 * (d + 2) * 4, dtype=torch.uint8,
+                     device=cuda_device)
+    S.check(b, *b.call(workspace=ws), ref=ref)
+
+
+# one group of several row blocks over a prefix of many tiles, its last block
+# part full; every block's share crosses units
+@pytest.mark.parametrize("fmt,d,n,prefix", [("q8", 128, 150, 1700), ("q8", 64, 90, 2500),
+                                            ("f8v4", 128, 129, 1100)])
+def test_shares_cross_units(cuda_device, fmt, d, n, prefix):
+    b = S.make(n, cuda_device, fmt, 8, 2, d, 16, [(prefix, [(1, 1 + i % 3) for i in range(n)])])
+    ref = S.reference(b)
+    S.check(b, *b.call(), ref=ref)
+    full = _lib.shared_prefix_workspace_size(n, n, 1, 8, 2, d, *b.bounds)
+    triple = n * 8 * (d + 2) * 4
+    for slots in (2, 3, 4):  # fewer and fewer segments
+        ws = torch.zeros(min(full, 256 + slots * triple), dtype=torch.uint8, device=cuda_device)
+        S.check(b, *b.call(workspace=ws), ref=ref)
+
+
 # the bounds of the prefixes and suffixes are hints, that of the query lengths an upper bound
 @pytest.mark.parametrize("bounds", [(6, 0, 1), (6, 64, 64), (999, 99999, 99999), (7, 1, 100000)])
 def test_bounds_are_hints(cuda_device, bounds):
