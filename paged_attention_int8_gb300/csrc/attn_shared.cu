@@ -368,128 +368,119 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
 }
 
 // The join: all segment triples of a row (query token x q head) and its sink
-// merged to bf16 output and fp32 LSE.  One warp per two consecutive rows of a
-// kv head: lane l reads 4 channels (l / 2, + 16, ...) of row l % 2, so that a
-// pair of lanes takes a whole sector.  Bound by its reads (D + 2 floats a
-// segment, L2 hits); launched beside the last kernel, it looks up the rows'
-// sequences and waits.
+// merged to bf16 output and fp32 LSE.  One warp per 8 consecutive rows of a kv
+// head and 16 channels: lane l reads 4 channels (l / 8) of row l % 8, so that
+// eight lanes take a whole 128-byte line of a segment, and every segment's load
+// is in flight at once (8 a batch).  Bound by its reads (D + 2 floats a row and
+// segment, L2 hits); with 32-byte pieces, two rows of all channels a warp, it
+// took 15 us where it now takes 5 (64 requests, 21 segments).  Launched beside
+// the last kernel: it looks up its rows' sequences and then waits.
 template <int D>
-__global__ void __launch_bounds__(128) shared_join_kernel(const __grid_constant__ SharedArgs s) {
-  constexpr int V = D / 64;  // 4-channel pieces per lane
-  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedArgs s) {
+  constexpr int kCb = D / 16;  // channel blocks of a row
   const AttnArgs &a = s.a;
+  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
   const int lane = threadIdx.x & 31;
-  const int odd = lane & 1;
   const int64_t rows = rows_total(s);
-  const int64_t pairs = (rows + 1) / 2;
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (gw >= pairs * a.hk) return;
-  const int h = static_cast<int>(gw / pairs);
-  const int64_t row0 = gw % pairs * 2, row = row0 + odd;
+  const int64_t groups = (rows + 7) / 8;
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (gw >= groups * a.hk * kCb) return;
+  const int cb = static_cast<int>(gw % kCb);
+  const int h = static_cast<int>(gw / kCb / groups);
+  const int64_t row = gw / kCb % groups * 8 + (lane & 7);
+  const int piece = lane >> 3;  // 4 channels of the 16; segments piece + 4 j of a round
+
   // this lane's row: its token, q head, and how many segments hold its keys
   int n_p = 0, n_s = 0;
-  const int tok0 = static_cast<int>(row0 / a.qpk), tok1 = static_cast<int>((row0 + 1) / a.qpk);
-  const int tok = odd ? tok1 : tok0;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    const int tk = i ? tok1 : tok0;
-    if (i && (tok1 == tok0 || tok1 >= a.num_tokens)) break;
-    const int seq = find_seq(a.cu_seqlens_q, a.num_seqs, 1, tk, lane);
+  const int tok = static_cast<int>(row / a.qpk);
+  const int hh = h * a.qpk + static_cast<int>(row % a.qpk);
+  if (row < rows) {
+    // a batch of single tokens: sequence = token; a search otherwise
+    int seq = tok < a.num_seqs ? tok : a.num_seqs - 1;
+    if (a.cu_seqlens_q[seq] > tok || a.cu_seqlens_q[seq + 1] <= tok)
+      seq = last_at_most(a.cu_seqlens_q, a.num_seqs, tok);
     const int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1];
-    if (c0 < 0 || tk < c0 || tk >= c1 || c1 > a.num_tokens) continue;  // a row no sequence owns
-    int g = 0;
-    const int P = prefix_of(s, seq, lane, &g);
-    const int ctx = a.seq_lens[seq] - (c1 - c0);
-    // flagged by the suffix item
-    if (P < 0 || ctx < P || rows_of(s, c1 - c0) > s.max_rows) continue;
-    const int g0 = group_token(s, g), g1 = group_token(s, g + 1);
-    if (g0 < 0 || g0 > tk || tk >= g1 || g1 > a.num_tokens) continue;  // its prefix was not taken
-    if (tk == tok) {
-      n_p = shared_segments(0, P, s.seg_p, s.ns_p);
-      n_s = shared_segments(P, ctx + tk - c0 + 1, s.seg_s, s.ns_s);
+    const int g = last_at_most(s.cu_groups, s.num_groups, seq);
+    if (c0 >= 0 && tok >= c0 && tok < c1 && c1 <= a.num_tokens &&  // else: a row no sequence owns
+        s.cu_groups[g] <= seq && s.cu_groups[g + 1] > seq && rows_of(s, c1 - c0) <= s.max_rows) {
+      const int P = s.prefix_lens[g];
+      const int ctx = a.seq_lens[seq] - (c1 - c0);
+      const int g0 = group_token(s, g), g1 = group_token(s, g + 1);
+      // else: flagged by the suffix item, or its prefix was not taken
+      if (P >= 0 && ctx >= P && g0 >= 0 && g0 <= tok && tok < g1 && g1 <= a.num_tokens) {
+        n_p = shared_segments(0, P, s.seg_p, s.ns_p);
+        n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
+      }
     }
   }
-  const bool own = row < rows && n_s > 0;  // a row that is written
-  const int hh = h * a.qpk + static_cast<int>(row % a.qpk);
-  const int n = own ? n_p + n_s : 0;
-  const int n_max = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
+  const int n = n_s > 0 ? n_p + n_s : 0;  // 0: a row that is not written
+  const int n_max = __reduce_max_sync(0xffffffffu, n);
   if (n_max == 0) return;
-  const float sink = a.sinks && own ? sink_log2(a, hh) : -INFINITY;
+  const float sink = a.sinks && n > 0 ? sink_log2(a, hh) : -INFINITY;
   // segment k of the row: its slot (the prefix's first, unused ones skipped)
   auto slot = [&](int k) { return k < n_p ? k : s.ns_p + k - n_p; };
-  auto triple_ml = [&](int k) {
-    return *reinterpret_cast<const float2 *>(a.part_ml + (ml_at(s, slot(k), h) + row) * 2);
-  };
   wait_for_predecessor();  // the triples
-  const int k_lane = lane >> 1;
   float M = sink;
-  float total = sink > -INFINITY && k_lane == 0 ? 1.0f : 0.0f;  // this lane's share, scaled to M
-  float4 acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  // 16 segments a round, one per lane pair for the weights; the accumulators
-  // kBatch segments at a time, all their loads in flight together
-  constexpr int kBatch = V == 4 ? 4 : 8;
+  float total = sink > -INFINITY && piece == 0 ? 1.0f : 0.0f;  // this lane's share, scaled to M
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int64_t at = (static_cast<int64_t>(cb * 4 + piece) * rows + row) * 4;
   for (int k0 = 0; k0 < n_max; k0 += 16) {
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (k0 + k_lane < n) ml = triple_ml(k0 + k_lane);
-    float4 x[kBatch][V];
+    constexpr int kBatch = 8;
+    float4 x[kBatch];
     auto load = [&](int k1) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const bool in = k1 + i < n;
-        const float *src = acc_at<D>(s, slot(in ? k1 + i : 0), h) + (k_lane * rows + row) * 4;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          x[i][v] = in ? *reinterpret_cast<const float4 *>(src + v * 16 * rows * 4)
-                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+      for (int i = 0; i < kBatch; ++i)
+        x[i] = k1 + i < n ? *reinterpret_cast<const float4 *>(acc_at<D>(s, slot(k1 + i), h) + at)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
-    load(k0);
-    float m = ml.x;
+    float2 ml[4];
 #pragma unroll
-    for (int o = 2; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = fmaxf(M, m);
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + piece + 4 * j;
+      ml[j] = k < n ? *reinterpret_cast<const float2 *>(a.part_ml + (ml_at(s, slot(k), h) + row) * 2)
+                    : make_float2(-INFINITY, 0.0f);
+    }
+    load(k0);
+    float m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = fmaxf(M, fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)));
     const float mu = m == -INFINITY ? 0.0f : m;
     const float f = fast_exp2(M - mu);
     M = m;
-    const float wk = fast_exp2(ml.x - mu);
-    total = fmaf(total, f, wk * ml.y);
+    float w[4];
+    total *= f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      acc[v].x *= f;
-      acc[v].y *= f;
-      acc[v].z *= f;
-      acc[v].w *= f;
+    for (int j = 0; j < 4; ++j) {
+      w[j] = fast_exp2(ml[j].x - mu);
+      total = fmaf(w[j], ml[j].y, total);
     }
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
 #pragma unroll
     for (int b = 0; b < 16 / kBatch; ++b) {
       if (k0 + b * kBatch >= n_max) break;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float w = __shfl_sync(0xffffffffu, wk, 2 * (b * kBatch + i) + odd);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          acc[v].x = fmaf(w, x[i][v].x, acc[v].x);
-          acc[v].y = fmaf(w, x[i][v].y, acc[v].y);
-          acc[v].z = fmaf(w, x[i][v].z, acc[v].z);
-          acc[v].w = fmaf(w, x[i][v].w, acc[v].w);
-        }
+        const int k = b * kBatch + i;
+        const float wk = __shfl_sync(0xffffffffu, w[k >> 2], (k & 3) * 8 + (lane & 7));
+        acc.x = fmaf(wk, x[i].x, acc.x);
+        acc.y = fmaf(wk, x[i].y, acc.y);
+        acc.z = fmaf(wk, x[i].z, acc.z);
+        acc.w = fmaf(wk, x[i].w, acc.w);
       }
       if (b + 1 < 16 / kBatch) load(k0 + (b + 1) * kBatch);
     }
   }
-#pragma unroll
-  for (int o = 2; o < 32; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (!own) return;
+  total += __shfl_xor_sync(0xffffffffu, total, 8);
+  total += __shfl_xor_sync(0xffffffffu, total, 16);
+  if (n == 0) return;
   const float inv = 1.0f / total;
-  const int64_t at = static_cast<int64_t>(tok) * a.hq + hh;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    *reinterpret_cast<uint2 *>(a.out + at * D + v * 64 + k_lane * 4) =
-        make_uint2(pack_bf162(acc[v].x * inv, acc[v].y * inv),
-                   pack_bf162(acc[v].z * inv, acc[v].w * inv));
-  if (k_lane == 0 && a.lse) a.lse[at] = (M + log2f(total)) * kLn2;
+  const int64_t to = static_cast<int64_t>(tok) * a.hq + hh;
+  *reinterpret_cast<uint2 *>(a.out + to * D + cb * 16 + piece * 4) =
+      make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
+  if (cb == 0 && piece == 0 && a.lse) a.lse[to] = (M + log2f(total)) * kLn2;
 }
 
 // ---------------------------------------------------------------------- host
@@ -670,14 +661,14 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
     if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, tc, stream)) != cudaSuccess) return e;
   }
   if (few && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
-  const int64_t warps = (static_cast<int64_t>(L.num_tokens) * a.qpk + 1) / 2 * L.hk;
-  const int64_t blocks = (warps + 3) / 4;
+  const int64_t warps = (static_cast<int64_t>(L.num_tokens) * a.qpk + 7) / 8 * L.hk * (L.d / 16);
+  const int64_t blocks = (warps + 7) / 8;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
   switch (L.d) {
-    case 64: return launch_kernel(shared_join_kernel<64>, grid, 128, 0, stream, true, s);
-    case 128: return launch_kernel(shared_join_kernel<128>, grid, 128, 0, stream, true, s);
-    case 256: return launch_kernel(shared_join_kernel<256>, grid, 128, 0, stream, true, s);
+    case 64: return launch_kernel(shared_join_kernel<64>, grid, 256, 0, stream, true, s);
+    case 128: return launch_kernel(shared_join_kernel<128>, grid, 256, 0, stream, true, s);
+    case 256: return launch_kernel(shared_join_kernel<256>, grid, 256, 0, stream, true, s);
   }
   return cudaErrorInvalidValue;
 }

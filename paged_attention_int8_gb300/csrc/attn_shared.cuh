@@ -56,6 +56,17 @@ __device__ __forceinline__ int find_last(int n, int target, int lane, K &&key) {
   return lo;
 }
 
+// The last i in [0, n) with v[i] <= target (0 if there is none), by one thread.
+__device__ __forceinline__ int last_at_most(const int32_t *v, int n, int target) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= target) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // First query token of group g (cu_seqlens_q of its first sequence).
 __device__ __forceinline__ int group_token(const SharedArgs &s, int g) {
   const int q = s.cu_groups[g];
