@@ -27,5 +27,6 @@ __all__ = ["kv_store", "kv_store_norm_rope", "kv_store_f8v4", "paged_attention",
 def __getattr__(name):
     if name in __all__:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # found at once from now on
+        return value
     raise AttributeError(name)

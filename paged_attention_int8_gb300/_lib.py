@@ -500,37 +500,35 @@ def merge_attn_states(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=Non
 
 
 # The calls of a serving step are made once a step or a layer on small batches
-# too, where the host's share counts: their bindings look each attribute up
-# once and enter the tensors' device only when another one is current.
+# too, where the host's share counts (a tensor attribute costs about 0.1 us, a
+# torch.cuda.Stream object 2): their bindings look each attribute up once, compare
+# device numbers, and enter the tensors' device only when another one is current.
 
-def _call(fn, device, *args):
-    """fn(*args), with `device` current."""
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args)
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream), with device number `dev` current."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args)
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
     if st:
         _raise_if(st)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _handle(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-def _check_i32(device, **tensors):
-    """Contiguous int32 CUDA tensors on `device` (None passes)."""
+def _refuse(dev, dtypes, **tensors):
+    """Raise for the tensors (None passes) that a quick check turned down: each
+    must be a contiguous tensor of one of `dtypes` on device number `dev`."""
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.dtype is not torch.int32:
-            raise TypeError(f"{name} must be int32")
-        if t.device != device:
+        if not t.is_cuda or t.get_device() != dev:
             raise ValueError(f"all tensors must be CUDA tensors on one device: {name} on {t.device}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
@@ -565,65 +563,105 @@ def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_
     ``out``: a BlockTables (or tuple in its order) to write into; its
     ``block_table`` may be ``source_table`` itself (source_rows None), the
     only allowed overlap.  ``status``: optional int32 CUDA tensor, zeroed."""
-    if not context_lens.is_cuda:
+    dev = context_lens.get_device()
+    if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    device = context_lens.device
-    s = context_lens.shape[0]
-    if context_lens.dim() != 1 or query_lens.shape != (s,):
-        raise ValueError("context_lens and query_lens must be [S]")
-    if source_table.dim() != 2 or free_blocks.dim() != 1:
-        raise ValueError("source_table must be [R, columns] and free_blocks [num_free]")
+    s = context_lens.numel()
+    rows, columns = source_table.shape
     if num_tokens < 0:
         raise ValueError("num_tokens < 0")
     if out is None:
+        device = context_lens.device
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
-        out = (torch.full((s, source_table.shape[1]), -1, dtype=torch.int32, device=device),
-               new(s + 1, torch.int32), new(s, torch.int32), new(num_tokens, torch.int64),
-               new(num_tokens, torch.int64), new((s, 2), torch.int32), new(1, torch.int32))
-    out = BlockTables(*out)
+        out = (torch.full((s, columns), -1, dtype=_I32, device=device), new(s + 1, _I32),
+               new(s, _I32), new(num_tokens, torch.int64), new(num_tokens, torch.int64),
+               new((s, 2), _I32), new(1, _I32))
+    if type(out) is not BlockTables:
+        out = BlockTables._make(out)
     table, cu, lens, slots, pos, pairs, nxt = out
-    _check_i32(device, context_lens=context_lens, query_lens=query_lens, source_table=source_table,
-               source_rows=source_rows, shared_lens=shared_lens, free_blocks=free_blocks,
-               free_head=free_head, block_table=table, cu_seqlens_q=cu, seq_lens=lens,
-               copy_pairs=pairs, next_free=nxt, status=status)
-    for name, t in (("slot_mapping", slots), ("positions", pos)):
-        if t is None and name == "positions":
+    for t in (context_lens, query_lens, source_table, free_blocks, table, cu, lens, source_rows,
+              shared_lens, free_head, pairs, nxt, status):
+        if t is not None and (t.dtype is not _I32 or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _refuse(dev, (_I32,), context_lens=context_lens, query_lens=query_lens,
+                    source_table=source_table, free_blocks=free_blocks, block_table=table,
+                    cu_seqlens_q=cu, seq_lens=lens, source_rows=source_rows,
+                    shared_lens=shared_lens, free_head=free_head, copy_pairs=pairs, next_free=nxt,
+                    status=status)
+    for t in (slots, pos):
+        if t is None and t is pos:
             continue
-        if t.dtype is not torch.int64 or t.device != device or t.shape != (num_tokens,) \
-                or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous int64 CUDA tensor [num_tokens]")
+        if t.dtype is not torch.int64 or t.get_device() != dev or not t.is_contiguous():
+            _refuse(dev, (torch.int64,), slot_mapping=slots, positions=pos)
+        if t.numel() != num_tokens:
+            raise ValueError("slot_mapping and positions must be [num_tokens]")
     if table.dim() != 2 or table.shape[0] != s:
         raise ValueError("block_table must be [S, columns]")
-    if cu.shape != (s + 1,) or lens.shape != (s,) or (pairs is not None and pairs.shape != (s, 2)):
-        raise ValueError("cu_seqlens_q [S + 1], seq_lens [S] and copy_pairs [S, 2] are wanted")
-    for name, t in (("source_rows", source_rows), ("shared_lens", shared_lens)):
-        if t is not None and t.shape != (s,):
-            raise ValueError(f"{name} must be [S]")
-    for name, t in (("free_head", free_head), ("next_free", nxt), ("status", status)):
+    if cu.numel() != s + 1 or lens.numel() != s or query_lens.numel() != s \
+            or (pairs is not None and pairs.numel() != 2 * s) \
+            or (source_rows is not None and source_rows.numel() != s) \
+            or (shared_lens is not None and shared_lens.numel() != s):
+        raise ValueError("query_lens, seq_lens, source_rows and shared_lens [S], cu_seqlens_q "
+                         "[S + 1] and copy_pairs [S, 2] are wanted")
+    for t in (free_head, nxt, status):
         if t is not None and t.numel() < 1:
-            raise ValueError(f"{name} must hold a value")
-    _call(load().pa_build_block_tables, device, context_lens.data_ptr(), query_lens.data_ptr(), s,
-          source_table.data_ptr(), source_table.shape[1], source_table.shape[0],
-          _addr(source_rows), _addr(shared_lens), free_blocks.data_ptr(), free_blocks.shape[0],
-          _addr(free_head), num_blocks, block_size, table.data_ptr(), table.shape[1],
-          cu.data_ptr(), lens.data_ptr(), slots.data_ptr(), _addr(pos), num_tokens, _addr(pairs),
-          _addr(nxt), _addr(status), _handle(stream, device))
+            raise ValueError("free_head, next_free and status must hold a value")
+    _call((_lib or load()).pa_build_block_tables, dev, stream, context_lens.data_ptr(),
+          query_lens.data_ptr(), s, source_table.data_ptr(), columns, rows,
+          None if source_rows is None else source_rows.data_ptr(),
+          None if shared_lens is None else shared_lens.data_ptr(), free_blocks.data_ptr(),
+          free_blocks.numel(), None if free_head is None else free_head.data_ptr(), num_blocks,
+          block_size, table.data_ptr(), table.shape[1], cu.data_ptr(), lens.data_ptr(),
+          slots.data_ptr(), None if pos is None else pos.data_ptr(), num_tokens,
+          None if pairs is None else pairs.data_ptr(), None if nxt is None else nxt.data_ptr(),
+          None if status is None else status.data_ptr())
     return out
 
 
-def _copy_args(copy_pairs, status, arrays):
-    if not copy_pairs.is_cuda:
+_Q8 = (torch.int8, torch.float16, torch.int16)
+
+
+def _q8_cache(dev, k_cache, k_scale, v_cache, v_scale):
+    """Checks a q8 cache on device number `dev`; (num_blocks, Hk, bs, D)."""
+    nb, hk, bs, d = k_cache.shape
+    for t in (k_cache, k_scale, v_cache, v_scale):
+        if t.get_device() != dev or not t.is_contiguous():
+            _refuse(dev, _Q8, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale)
+    if k_cache.dtype is not torch.int8 or v_cache.dtype is not torch.int8:
+        raise TypeError("caches must be int8")
+    if k_scale.element_size() != 2 or v_scale.element_size() != 2:
+        raise TypeError("k_scale and v_scale must hold 16-bit elements (fp16 scales)")
+    g = d // 32
+    if k_scale.shape != (nb, hk, bs, g) or v_cache.shape != (nb, hk, d, bs) \
+            or v_scale.shape != (nb, hk, g, bs):
+        _check_cache_shapes(k_cache, k_scale, v_cache, v_scale)
+    return nb, hk, bs, d
+
+
+def _f8v4_cache(dev, k_cache, v_cache, v_scale, v_zero):
+    """The same for a cache in the fp8 / 4-bit format."""
+    _check_f8v4_shapes(k_cache, v_cache, v_scale, v_zero)
+    for t in (k_cache, v_cache, v_scale, v_zero):
+        if t.get_device() != dev:
+            raise ValueError(f"all tensors must be CUDA tensors on one device: a cache on {t.device}")
+    return k_cache.shape
+
+
+def _copy(fn, check, copy_pairs, cache, status, stream):
+    dev = copy_pairs.get_device()
+    if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    device = copy_pairs.device
-    _check_i32(device, copy_pairs=copy_pairs, status=status)
+    for t in (copy_pairs, status):
+        if t is not None and (t.dtype is not _I32 or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _refuse(dev, (_I32,), copy_pairs=copy_pairs, status=status)
     if copy_pairs.dim() != 2 or copy_pairs.shape[1] != 2:
         raise ValueError("copy_pairs must be [N, 2]")
-    for t in arrays:
-        if t.device != device:
-            raise ValueError(f"tensors on different devices: {device} and {t.device}")
-        if not t.is_contiguous():
-            raise ValueError("caches must be contiguous")
-    return device
+    nb, hk, bs, d = check(dev, *cache)
+    a, b, c, e = cache
+    _call(fn, dev, stream, copy_pairs.data_ptr(), copy_pairs.shape[0], hk, d, a.data_ptr(),
+          b.data_ptr(), c.data_ptr(), e.data_ptr(), nb, bs,
+          None if status is None else status.data_ptr())
 
 
 def copy_blocks(copy_pairs, k_cache, k_scale, v_cache, v_scale, status=None, stream=None) -> None:
@@ -631,27 +669,15 @@ def copy_blocks(copy_pairs, k_cache, k_scale, v_cache, v_scale, status=None, str
     (pa_copy_blocks): ``copy_pairs`` int32 [N, 2] of (source, destination),
     pairs with a negative id skipped.  Destinations must be distinct and no
     pair's source."""
-    device = _copy_args(copy_pairs, status, (k_cache, k_scale, v_cache, v_scale))
-    if k_cache.dtype is not torch.int8 or v_cache.dtype is not torch.int8:
-        raise TypeError("caches must be int8")
-    _check16("k_scale", k_scale)
-    _check16("v_scale", v_scale)
-    _check_cache_shapes(k_cache, k_scale, v_cache, v_scale)
-    nb, hk, bs, d = k_cache.shape
-    _call(load().pa_copy_blocks, device, copy_pairs.data_ptr(), copy_pairs.shape[0], hk, d,
-          k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), nb, bs,
-          _addr(status), _handle(stream, device))
+    _copy((_lib or load()).pa_copy_blocks, _q8_cache, copy_pairs,
+          (k_cache, k_scale, v_cache, v_scale), status, stream)
 
 
 def copy_blocks_f8v4(copy_pairs, k_cache, v_cache, v_scale, v_zero, status=None,
                      stream=None) -> None:
     """copy_blocks over the fp8 / 4-bit format (pa_copy_blocks_f8v4)."""
-    device = _copy_args(copy_pairs, status, (k_cache, v_cache, v_scale, v_zero))
-    _check_f8v4_shapes(k_cache, v_cache, v_scale, v_zero)
-    nb, hk, bs, d = k_cache.shape
-    _call(load().pa_copy_blocks_f8v4, device, copy_pairs.data_ptr(), copy_pairs.shape[0], hk, d,
-          k_cache.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), v_zero.data_ptr(), nb, bs,
-          _addr(status), _handle(stream, device))
+    _copy((_lib or load()).pa_copy_blocks_f8v4, _f8v4_cache, copy_pairs,
+          (k_cache, v_cache, v_scale, v_zero), status, stream)
 
 
 def shared_prefix_workspace_size(num_seqs: int, num_tokens: int, num_groups: int,
@@ -664,60 +690,66 @@ def shared_prefix_workspace_size(num_seqs: int, num_tokens: int, num_groups: int
         max_prefix_len, max_suffix_len))
 
 
-def _shared_prefix(fn, q, k_cache, four, hk, nb, bs, cu_seqlens_q, seq_lens, block_table,
-                   cu_groups, prefix_lens, max_query_len, max_prefix_len, max_suffix_len,
-                   softmax_scale, sinks, out, lse, workspace, stream, return_lse):
-    if not q.is_cuda:
+def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_groups,
+                   prefix_lens, max_query_len, max_prefix_len, max_suffix_len, softmax_scale,
+                   sinks, out, lse, workspace, stream, return_lse):
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    device = q.device
-    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+    nb, hk, bs, dc = check(dev, *cache)
+    if q.dtype is not _BF16 or not q.is_contiguous():
         raise TypeError("q must be a contiguous bf16 tensor [T, Hq, D]")
     t, hq, d = q.shape
-    if k_cache.shape[3] != d:
+    if dc != d:
         raise ValueError("cache shape mismatch")
-    for x in four:
-        if x.device != device:
-            raise ValueError(f"tensors on different devices: {device} and {x.device}")
-        if not x.is_contiguous():
-            raise ValueError("caches must be contiguous")
-    _check_i32(device, cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens, cu_groups=cu_groups,
-               prefix_lens=prefix_lens)
-    if block_table.dtype is not torch.int32 or block_table.device != device:
-        raise TypeError(f"block_table must be an int32 CUDA tensor on {device}")
-    s, g = seq_lens.shape[0], prefix_lens.shape[0]
-    if block_table.dim() != 2 or block_table.stride(1) != 1:
+    for x in (cu_seqlens_q, seq_lens, cu_groups, prefix_lens):
+        if x.dtype is not _I32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens,
+                    cu_groups=cu_groups, prefix_lens=prefix_lens)
+    s, g = seq_lens.numel(), prefix_lens.numel()
+    rows, _ = block_table.shape
+    if block_table.dtype is not _I32 or block_table.get_device() != dev:
+        raise TypeError("block_table must be an int32 CUDA tensor on q's device")
+    if block_table.stride(1) != 1:
         raise ValueError("block_table must be [S, max_blocks] with unit column stride")
-    if cu_seqlens_q.shape != (s + 1,) or block_table.shape[0] != s or cu_groups.shape != (g + 1,):
+    if cu_seqlens_q.numel() != s + 1 or rows != s or cu_groups.numel() != g + 1:
         raise ValueError("cu_seqlens_q [S + 1], block_table [S, ...] and cu_groups [G + 1] are wanted")
-    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.shape != (hq,)
-                              or sinks.device != device or not sinks.is_contiguous()):
-        raise TypeError("sinks must be a contiguous fp32 CUDA tensor [num_q_heads]")
+    if sinks is not None:
+        if sinks.dtype is not _F32 or sinks.get_device() != dev or not sinks.is_contiguous():
+            _refuse(dev, (_F32,), sinks=sinks)
+        if sinks.numel() != hq:
+            raise ValueError("sinks must be [num_q_heads]")
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype is not torch.bfloat16 or out.device != device \
-            or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 CUDA tensor shaped like q")
+    else:
+        if out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
+            _refuse(dev, (_BF16,), out=out)
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
     if lse is None:
         if return_lse:
-            lse = torch.empty((t, hq), dtype=torch.float32, device=device)
-    elif lse.shape != (t, hq) or lse.dtype is not torch.float32 or lse.device != device \
-            or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 CUDA tensor [T, Hq]")
-    lib = load()
+            lse = torch.empty((t, hq), dtype=_F32, device=q.device)
+    else:
+        if lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
+            _refuse(dev, (_F32,), lse=lse)
+        if lse.shape != (t, hq):
+            raise ValueError("lse must be [T, Hq]")
     if workspace is None:
-        need = lib.pa_shared_prefix_workspace_size(s, t, g, hq, hk, d, max_query_len,
-                                                   max_prefix_len, max_suffix_len)
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        need = load().pa_shared_prefix_workspace_size(s, t, g, hq, hk, d, max_query_len,
+                                                      max_prefix_len, max_suffix_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         workspace[:4].zero_()
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-    _call(fn(lib), device, q.data_ptr(), k_cache.data_ptr(), four[1].data_ptr(),
-          four[2].data_ptr(), four[3].data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-          block_table.data_ptr(), block_table.stride(0), cu_groups.data_ptr(),
-          prefix_lens.data_ptr(), g, s, t, hq, hk, d, nb, bs, max_query_len, max_prefix_len,
-          max_suffix_len, d ** -0.5 if softmax_scale is None else softmax_scale, _addr(sinks),
-          out.data_ptr(), _addr(lse), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), 0, _handle(stream, device))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+    a, b, c, e = cache
+    _call(fn, dev, stream, q.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), e.data_ptr(),
+          cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+          block_table.stride(0), cu_groups.data_ptr(), prefix_lens.data_ptr(), g, s, t, hq, hk, d,
+          nb, bs, max_query_len, max_prefix_len, max_suffix_len,
+          d ** -0.5 if softmax_scale is None else softmax_scale,
+          None if sinks is None else sinks.data_ptr(), out.data_ptr(),
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), 0)
     return (out, lse) if return_lse else out
 
 
@@ -740,14 +772,8 @@ def paged_attention_shared_prefix(q, k_cache, k_scale, v_cache, v_scale, cu_seql
     ``workspace``: uint8 CUDA tensor of ``shared_prefix_workspace_size``
     bytes, its first 4 bytes zero (the device status word); allocated when
     omitted.  Other arguments and results as paged_attention."""
-    if k_cache.dtype is not torch.int8 or v_cache.dtype is not torch.int8:
-        raise TypeError("caches must be int8")
-    _check16("k_scale", k_scale)
-    _check16("v_scale", v_scale)
-    _check_cache_shapes(k_cache, k_scale, v_cache, v_scale)
-    nb, hk, bs, _ = k_cache.shape
-    return _shared_prefix(lambda lib: lib.pa_paged_attention_shared_prefix, q, k_cache,
-                          (k_cache, k_scale, v_cache, v_scale), hk, nb, bs, cu_seqlens_q, seq_lens,
+    return _shared_prefix((_lib or load()).pa_paged_attention_shared_prefix, _q8_cache, q,
+                          (k_cache, k_scale, v_cache, v_scale), cu_seqlens_q, seq_lens,
                           block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
                           max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
                           return_lse)
@@ -761,10 +787,8 @@ def paged_attention_shared_prefix_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_
                                        return_lse: bool = True):
     """paged_attention_shared_prefix over the fp8 / 4-bit format
     (pa_paged_attention_shared_prefix_f8v4)."""
-    _check_f8v4_shapes(k_cache, v_cache, v_scale, v_zero)
-    nb, hk, bs, _ = k_cache.shape
-    return _shared_prefix(lambda lib: lib.pa_paged_attention_shared_prefix_f8v4, q, k_cache,
-                          (k_cache, v_cache, v_scale, v_zero), hk, nb, bs, cu_seqlens_q, seq_lens,
+    return _shared_prefix((_lib or load()).pa_paged_attention_shared_prefix_f8v4, _f8v4_cache, q,
+                          (k_cache, v_cache, v_scale, v_zero), cu_seqlens_q, seq_lens,
                           block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
                           max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
                           return_lse)

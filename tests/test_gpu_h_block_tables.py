@@ -329,3 +329,59 @@ def test_fork_and_decode(cuda_device, fmt, hq, hk, d, bs):
         t, source, source_rows, shared = t2, t2.block_table, None, None
         ctx = [c + 1 for c in ctx]
     assert _lib.check_status(status) == 0
+
+
+# --------------------------------------------------------- the bindings' checks
+
+def test_bindings_refuse_what_the_calls_cannot_take(cuda_device):
+    """Types, layouts and shapes, each refused before anything is launched."""
+    H.ensure_built()
+    dev = cuda_device
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    good = dict(context_lens=i32(2), query_lens=i32(2), source_table=i32(2, 4), free_blocks=i32(3),
+                num_blocks=4, block_size=16, num_tokens=2)
+    _lib.build_block_tables(**good)
+    for bad in (dict(query_lens=i32(3)), dict(context_lens=i32(2).long()),
+                dict(source_table=i32(4, 4)[:, ::2]), dict(source_table=i32(8)),
+                dict(free_blocks=i32(3).cpu()), dict(source_rows=i32(1)), dict(shared_lens=i32(5)),
+                dict(free_head=i32(0)), dict(num_tokens=-1), dict(query_lens=i32(4)[::2])):
+        with pytest.raises((TypeError, ValueError)):
+            _lib.build_block_tables(**{**good, **bad})
+    out = list(_lib.build_block_tables(**good))
+    for at, t in ((0, i32(3, 4)), (1, i32(2)), (2, i32(2).long()), (3, i32(2)), (3, i32(3).long()),
+                  (5, i32(2, 3)), (6, i32(0))):
+        with pytest.raises((TypeError, ValueError)):
+            _lib.build_block_tables(**good, out=out[:at] + [t] + out[at + 1:])
+    with pytest.raises(_lib.PagedAttentionError):  # next_free over free_head
+        head = i32(1)
+        _lib.build_block_tables(**good, free_head=head, out=out[:6] + [head])
+    cache = inputs.empty_cache(4, 2, 16, 64, device=dev)
+    pairs = i32(1, 2)
+    _lib.copy_blocks(pairs, *cache)
+    for args in ((pairs.long(), *cache), (i32(2), *cache), (pairs, cache[0].float(), *cache[1:]),
+                 (pairs, cache[0], cache[1], cache[0], cache[3]), (pairs, cache[0].cpu(), *cache[1:]),
+                 (pairs, cache[0].transpose(1, 2), *cache[1:]),
+                 (pairs, cache[0], cache[1].float(), *cache[2:])):
+        with pytest.raises((TypeError, ValueError)):
+            _lib.copy_blocks(*args)
+    b = S.make(1, dev, "q8", 4, 2, 64, 16, [(20, [(1, 5)])])
+    args = dict(q=b.q, k_cache=b.cache[0], k_scale=b.cache[1], v_cache=b.cache[2],
+                v_scale=b.cache[3], cu_seqlens_q=b.cu, seq_lens=b.lens, block_table=b.table,
+                cu_groups=b.groups, prefix_lens=b.prefixes, max_query_len=1, max_prefix_len=20,
+                max_suffix_len=5)
+    _lib.paged_attention_shared_prefix(**args)
+    for bad in (dict(q=b.q.float()), dict(q=b.q.cpu()), dict(seq_lens=b.lens.long()),
+                dict(block_table=b.table.long()), dict(cu_groups=b.groups[:1]),
+                dict(cu_seqlens_q=b.cu[:1]), dict(sinks=torch.zeros(3, device=dev)),
+                dict(sinks=torch.zeros(4, device=dev).half()), dict(out=b.q.float()),
+                dict(lse=torch.zeros((1, 3), device=dev)), dict(q=b.q[:, :, :32].contiguous()),
+                dict(workspace=torch.zeros(64, dtype=torch.uint8)),
+                dict(block_table=b.table.t().contiguous().t())):
+        if "block_table" in bad and bad["block_table"].dtype == torch.int32 \
+                and bad["block_table"].stride(1) == 1:
+            continue
+        with pytest.raises((TypeError, ValueError)):
+            _lib.paged_attention_shared_prefix(**{**args, **bad})
+    with pytest.raises(_lib.PagedAttentionError):  # too small for two triples a row
+        _lib.paged_attention_shared_prefix(**args, workspace=torch.zeros(
+            512, dtype=torch.uint8, device=dev))
