@@ -495,7 +495,6 @@ static bool prefix_on_tc(int32_t num_tokens, int32_t num_groups, int32_t qpk, in
 SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_groups, int32_t hq,
                            int32_t hk, int32_t d, int32_t max_query_len, int32_t max_prefix_len,
                            int32_t max_suffix_len) {
-  (void)max_query_len;
   const int qpk = hq / hk;
   SharedSplits r;
   {
@@ -524,7 +523,8 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   {
     // suffix: ~1024 keys a segment (the decode kernel's measured best), more
     // segments only while blocks are too few to fill the GPU four to an SM
-    const int64_t units = static_cast<int64_t>(num_seqs) * hk;
+    const int64_t most = std::min<int64_t>(static_cast<int64_t>(max_query_len) * qpk, kFewRows);
+    const int64_t units = static_cast<int64_t>(num_seqs) * hk * ((most + 15) / 16);
     const int64_t tiles = (max_suffix_len + kTile - 1) / kTile;
     int64_t n = std::max<int64_t>((max_suffix_len + 1023) / 1024,
                                   std::min((608 + units - 1) / units, (tiles + 3) / 4));
@@ -566,8 +566,8 @@ static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8
   return cudaErrorInvalidValue;
 }
 
-// 2-D byte map of page rows: `rows` rows of `row_bytes`, boxes of box_y whole
-// rows (row_bytes <= 128).
+// 2-D byte map of page rows: `rows` rows of `row_bytes`, boxes of box_y rows of
+// up to 128 bytes.
 static bool encode_page_map(CUtensorMap *map, const void *base, int64_t rows, int row_bytes,
                             int box_y, CUtensorMapSwizzle swizzle) {
   typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -586,7 +586,8 @@ static bool encode_page_map(CUtensorMap *map, const void *base, int64_t rows, in
   if (!fn) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_y)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(std::min(row_bytes, 128)),
+                             static_cast<cuuint32_t>(box_y)};
   const cuuint32_t step[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
             step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -635,16 +636,16 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   // kernel (prefix_on_tc), a suffix of up to kFewRows rows to the rows kernel,
   // of more to the row-tile kernel.
   const bool tc = prefix_on_tc(L.num_tokens, L.num_groups, a.qpk, L.d);
-  const bool few = a.qpk <= kFewRows;
-  const bool many = static_cast<int64_t>(L.max_query_len) * a.qpk > kFewRows;
-  s.few_rows = few ? kFewRows : 0;
-  s.max_rows = many ? 0x7fffffff : kFewRows;
+  const int64_t most = static_cast<int64_t>(L.max_query_len) * a.qpk;  // rows of a sequence
+  const bool many = most > kFewRows;
+  s.few_rows = static_cast<int32_t>(std::min<int64_t>(most, kFewRows));
+  s.max_rows = many ? 0x7fffffff : s.few_rows;
   cudaError_t e = cudaSuccess;
   if (tc) {
     CUtensorMap tk = {}, tv = {};
     const int64_t pages = static_cast<int64_t>(L.num_blocks) * L.hk;
     if (!encode_page_map(&tk, L.k_cache, pages * L.bs, L.d, L.bs,
-                         L.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+                         L.d >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
         (!L.f8v4 && !encode_page_map(&tv, L.v_cache, pages * L.d, L.bs, L.d,
                                      L.bs == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE)))
@@ -660,7 +661,7 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
     s.n_sblocks = many ? L.num_tokens / a.block_q + L.num_seqs : 0;
     if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, tc, stream)) != cudaSuccess) return e;
   }
-  if (few && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+  if ((e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   const int64_t warps = (static_cast<int64_t>(L.num_tokens) * a.qpk + 7) / 8 * L.hk * (L.d / 16);
   const int64_t blocks = (warps + 7) / 8;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;

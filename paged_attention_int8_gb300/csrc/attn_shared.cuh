@@ -25,7 +25,7 @@
 namespace paq8 {
 
 constexpr int kSegTile = 64;  // keys per tile of the segment rule, for every kernel
-constexpr int kFewRows = 8;   // rows per kv head that the rows kernel takes
+constexpr int kFewRows = 32;  // rows per kv head that the rows kernel takes
 
 struct SharedArgs {
   AttnArgs a;  // q, caches, tables, partials (part_acc, part_ml), status, scale, sinks
@@ -37,6 +37,7 @@ struct SharedArgs {
   int32_t n_pblocks, n_sblocks;  // row blocks of the prefix and suffix items in the grid
   int32_t few_rows;            // suffixes of at most this many rows are the rows kernel's
   int32_t max_rows;            // no suffix kernel takes more rows than this
+  int32_t row_passes;          // rows kernel: passes over the keys that cover them
 };
 
 // Warp-cooperative search: the last i in [0, n) with key(i) <= target, key

@@ -1,10 +1,13 @@
-// Attention over a shared prefix: the suffix of sequences with at most 8 query
-// rows per kv head (query tokens x q heads; a decode token of up to 8 heads, a
-// few draft tokens of fewer), one key segment per block, in the swap-AB form
+// Attention over a shared prefix: the suffix of sequences with at most 32 query
+// rows per kv head (query tokens x q heads: a decode token, a few draft tokens
+// verified together), one key segment per block, in the swap-AB form
 // of the decode kernel (attn_decode.cu): keys in the MMA's M dimension, rows in
 // its N dimension,
 //   S^T[16 keys x 8 rows] = K[16 x 16 ch] . Q^T[16 ch x 8],
-//   O^T[16 ch x 8 rows] += V^T[16 ch x 16 keys] . P^T[16 keys x 8].
+//   O^T[16 ch x 8 rows] += V^T[16 ch x 16 keys] . P^T[16 keys x 8],
+// NT tiles of 8 rows (1, 2 or 4, by the bound of the query lengths) off every
+// converted key and value: the conversions, not the MMAs, are most of a block's
+// instructions.  More rows than 8 NT take several passes (D = 256).
 // Each row has its own causal limit, taken on edge blocks only.  HBM bound:
 // 2 (D + D / 16) bytes a key and kv head (q8), D + D / 2 + 4 (fp8 / 4-bit).
 //
@@ -78,16 +81,18 @@ struct RowsStage {
   }
 };
 
-template <int D, int BS, bool F8>
+template <int D, int BS, bool F8, int NT>
 struct SharedRowsCfg {
   using L = RowsStage<D, F8>;
   static constexpr int kWarps = 4;
   static constexpr int kSt = 3;
   static constexpr int kCm = D / 16;                    // 16-channel blocks of the output
   static constexpr int G = D / 32;
-  static constexpr int kMinBlocks = D == 256 ? 2 : 4;   // blocks per SM
+  // blocks per SM: 128 registers a thread (one block beside the tensor-core
+  // kernel, four alone) where that costs a few spills at most
+  static constexpr int kMinBlocks = D == 256 ? 2 : (NT == 4 ? 3 : 4);
   static constexpr int kRing = kWarps * kSt * L::kBytes;
-  static constexpr int kMerge = (kWarps - 1) * 32 * (4 + 4 * kCm) * 4;
+  static constexpr int kMerge = kWarps * 32 * NT * (4 + 4 * kCm) * 4;
   static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
 };
 
@@ -143,10 +148,10 @@ __device__ __forceinline__ void copy_rows_block(const AttnArgs &a, uint32_t st, 
   }
 }
 
-template <int D, int BS, bool F8>
-__global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
+template <int D, int BS, bool F8, int NT>
+__global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
     shared_rows_kernel(const __grid_constant__ SharedArgs sa) {
-  using Cfg = SharedRowsCfg<D, BS, F8>;
+  using Cfg = SharedRowsCfg<D, BS, F8, NT>;
   using L = typename Cfg::L;
   constexpr int G = Cfg::G;
   constexpr int kWarps = Cfg::kWarps;
@@ -163,16 +168,17 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.hk));
   const int rest = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk));
   const int seq = rest % a.num_seqs;
-  const int sigma = rest / a.num_seqs;
+  const int row0 = rest / a.num_seqs % sa.row_passes * (8 * NT);
+  const int sigma = rest / a.num_seqs / sa.row_passes;
 
   launch_dependents();
   const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
   const int q_start = a.cu_seqlens_q[seq];
   const int q_len = a.cu_seqlens_q[seq + 1] - q_start;
-  const int n_rows = rows_of(sa, q_len);
+  const int all_rows = rows_of(sa, q_len);
   if (q_len <= 0) return;
-  if (n_rows > kFewRows) {  // shared_mma_kernel's, where it runs
-    if (n_rows > sa.max_rows && sigma == 0 && h == 0 && threadIdx.x == 0)
+  if (all_rows > sa.few_rows) {  // shared_mma_kernel's, where it runs
+    if (all_rows > sa.max_rows && sigma == 0 && row0 == 0 && h == 0 && threadIdx.x == 0)
       flag_status(a.status, PA_DEV_BAD_SEQ);  // max_query_len was below a q_len
     return;
   }
@@ -180,9 +186,11 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
   const int ctx = seq_len - q_len;
   const int P = prefix_of(sa, seq, lane);
   if (q_start < 0 || q_start + q_len > a.num_tokens || P < 0 || ctx < P) {
-    if (threadIdx.x == 0 && sigma == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+    if (threadIdx.x == 0 && sigma == 0 && row0 == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
     return;
   }
+  const int n_rows = min(8 * NT, all_rows - row0);  // of this pass
+  if (n_rows <= 0) return;
   SharedWork w;
   if (!segment_keys(P, seq_len, sa.seg_s, sa.ns_s, sigma, w)) return;
   const int kv_begin = w.kv_begin, kv_end = w.kv_end;
@@ -219,44 +227,49 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
   const int g = lane >> 2;
   const int t = lane & 3;
 
-  // Q^T as the B operand: lane (g, t) holds row g, channels 32gq + 8t + 4s +
-  // {0,1} (k = 2t, 2t+1) and + {2,3} (k = 2t+8, 2t+9) for k-step s.
-  uint32_t qb[G][2][2];
-  {
-    const int row = g < n_rows ? g : 0;
-    const bool hv = g < n_rows;
+  // Q^T as the B operand: of row tile nt, lane (g, t) holds row 8 nt + g, channels
+  // 32gq + 8t + 4s + {0,1} (k = 2t, 2t+1) and + {2,3} (k = 2t+8, 2t+9) for k-step s.
+  uint32_t qb[NT][G][2][2];
+  bool bad_q = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const bool hv = 8 * nt + g < n_rows;
+    const int row = row0 + (hv ? 8 * nt + g : 0);
     const uint16_t *src = a.q + (static_cast<int64_t>(q_start + row / a.qpk) * a.hq + h * a.qpk +
                                  row % a.qpk) * D + t * 8;
-    bool bad_q = false;
 #pragma unroll
     for (int gq = 0; gq < G; ++gq) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (hv) v = *reinterpret_cast<const uint4 *>(src + gq * 32);
-      qb[gq][0][0] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
-      qb[gq][0][1] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
-      qb[gq][1][0] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));
-      qb[gq][1][1] = pack_half2(bf16_lo(v.w), bf16_hi(v.w));
-      bad_q |= half2_nonfinite(qb[gq][0][0]) || half2_nonfinite(qb[gq][0][1]) ||
-               half2_nonfinite(qb[gq][1][0]) || half2_nonfinite(qb[gq][1][1]);
+      qb[nt][gq][0][0] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
+      qb[nt][gq][0][1] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
+      qb[nt][gq][1][0] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));
+      qb[nt][gq][1][1] = pack_half2(bf16_lo(v.w), bf16_hi(v.w));
+      bad_q |= half2_nonfinite(qb[nt][gq][0][0]) || half2_nonfinite(qb[nt][gq][0][1]) ||
+               half2_nonfinite(qb[nt][gq][1][0]) || half2_nonfinite(qb[nt][gq][1][1]);
     }
-    // q values beyond the fp16 range (|q| >= 65520) would give inf scores
-    if (__any_sync(0xffffffffu, bad_q) && warp == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_Q);
   }
+  // q values beyond the fp16 range (|q| >= 65520) would give inf scores
+  if (__any_sync(0xffffffffu, bad_q) && warp == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_Q);
   const int r0 = perm16(g);      // key (within a 16-key block) of score row g
   const int r1 = perm16(g + 8);  // ... of score row g + 8
-  // last visible keys of this lane's two rows, and the first key past the
-  // block that every row sees
-  const int lim0 = min(kv_end - 1, ctx + min(2 * t, n_rows - 1) / a.qpk);
-  const int lim1 = min(kv_end - 1, ctx + min(2 * t + 1, n_rows - 1) / a.qpk);
-  const int all_end = min(kv_end, ctx + 1);
+  // last visible key of a row of this pass
+  auto limit = [&](int row) {
+    return min(kv_end - 1, ctx + (row0 + min(row, n_rows - 1)) / a.qpk);
+  };
+  const int all_end = min(kv_end, limit(0) + 1);  // the first key past those every row sees
 
-  float m_run[2] = {-INFINITY, -INFINITY};  // rows 2t, 2t+1 (log2 units)
-  float l_run[2] = {0.0f, 0.0f};            // this lane's share of the expsum
-  float o[Cfg::kCm][4];                     // O^T: channels (g, g+8) x rows (2t, 2t+1)
+  float m_run[NT][2], l_run[NT][2];  // rows 8 nt + 2t, + 1: max (log2 units), this lane's expsum
+  float o[NT][Cfg::kCm][4];          // O^T: channels (g, g+8) x rows (2t, 2t+1)
 #pragma unroll
-  for (int i = 0; i < Cfg::kCm; ++i)
+  for (int nt = 0; nt < NT; ++nt) {
+    m_run[nt][0] = m_run[nt][1] = -INFINITY;
+    l_run[nt][0] = l_run[nt][1] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    for (int i = 0; i < Cfg::kCm; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
+  }
 
 #pragma unroll 1
   for (int i = 0; i < n_blk; ++i) {
@@ -279,90 +292,101 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
 
     // ---------------- S^T = K Q^T: q8 with exact codes, scaled per group; fp8
     // keys exact in one accumulation
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    {
-      const int k0 = r0, k1 = r1;
-      if constexpr (F8) {
+    float s[NT][4];
 #pragma unroll
-        for (int gq = 0; gq < G; ++gq) {
-          const uint2 c0 = lds64(st + L::k_off(k0, gq * 32 + t * 8));
-          const uint2 c1 = lds64(st + L::k_off(k1, gq * 32 + t * 8));
-          // bytes (0,1) -> k 2t, 2t+1; (2,3) -> k 2t+8, 2t+9, as codes4_to_half2
-          const uint32_t a00 = e4m3x2_to_half2(c0.x), a02 = e4m3x2_to_half2(c0.x >> 16);
-          const uint32_t a01 = e4m3x2_to_half2(c1.x), a03 = e4m3x2_to_half2(c1.x >> 16);
-          const uint32_t a10 = e4m3x2_to_half2(c0.y), a12 = e4m3x2_to_half2(c0.y >> 16);
-          const uint32_t a11 = e4m3x2_to_half2(c1.y), a13 = e4m3x2_to_half2(c1.y >> 16);
-          mma_f16_16816(s, a00, a01, a02, a03, qb[gq][0][0], qb[gq][0][1]);
-          mma_f16_16816(s, a10, a11, a12, a13, qb[gq][1][0], qb[gq][1][1]);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+    if constexpr (F8) {
+#pragma unroll
+      for (int gq = 0; gq < G; ++gq) {
+        const uint2 c0 = lds64(st + L::k_off(r0, gq * 32 + t * 8));
+        const uint2 c1 = lds64(st + L::k_off(r1, gq * 32 + t * 8));
+        // bytes (0,1) -> k 2t, 2t+1; (2,3) -> k 2t+8, 2t+9, as codes4_to_half2
+        const uint32_t a00 = e4m3x2_to_half2(c0.x), a02 = e4m3x2_to_half2(c0.x >> 16);
+        const uint32_t a01 = e4m3x2_to_half2(c1.x), a03 = e4m3x2_to_half2(c1.x >> 16);
+        const uint32_t a10 = e4m3x2_to_half2(c0.y), a12 = e4m3x2_to_half2(c0.y >> 16);
+        const uint32_t a11 = e4m3x2_to_half2(c1.y), a13 = e4m3x2_to_half2(c1.y >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16_16816(s[nt], a00, a01, a02, a03, qb[nt][gq][0][0], qb[nt][gq][0][1]);
+          mma_f16_16816(s[nt], a10, a11, a12, a13, qb[nt][gq][1][0], qb[nt][gq][1][1]);
         }
-      } else {
-        float ks0[G], ks1[G];
-        load_key_scales<G>(st + L::kKsOff + k0 * G * 2, ks0);
-        load_key_scales<G>(st + L::kKsOff + k1 * G * 2, ks1);
+      }
+    } else {
+      float ks0[G], ks1[G];
+      load_key_scales<G>(st + L::kKsOff + r0 * G * 2, ks0);
+      load_key_scales<G>(st + L::kKsOff + r1 * G * 2, ks1);
 #pragma unroll
-        for (int gq = 0; gq < G; ++gq) {
-          const uint2 c0 = lds64(st + L::k_off(k0, gq * 32 + t * 8));
-          const uint2 c1 = lds64(st + L::k_off(k1, gq * 32 + t * 8));
-          uint32_t a00, a02, a01, a03, a10, a12, a11, a13;
-          codes4_to_half2(c0.x, a00, a02);  // row g, k-step 0: (k 2t,2t+1), (k 2t+8,2t+9)
-          codes4_to_half2(c1.x, a01, a03);  // row g+8
-          codes4_to_half2(c0.y, a10, a12);  // k-step 1
-          codes4_to_half2(c1.y, a11, a13);
+      for (int gq = 0; gq < G; ++gq) {
+        const uint2 c0 = lds64(st + L::k_off(r0, gq * 32 + t * 8));
+        const uint2 c1 = lds64(st + L::k_off(r1, gq * 32 + t * 8));
+        uint32_t a00, a02, a01, a03, a10, a12, a11, a13;
+        codes4_to_half2(c0.x, a00, a02);  // row g, k-step 0: (k 2t,2t+1), (k 2t+8,2t+9)
+        codes4_to_half2(c1.x, a01, a03);  // row g+8
+        codes4_to_half2(c0.y, a10, a12);  // k-step 1
+        codes4_to_half2(c1.y, a11, a13);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
           float sg[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_f16_16816(sg, a00, a01, a02, a03, qb[gq][0][0], qb[gq][0][1]);
-          mma_f16_16816(sg, a10, a11, a12, a13, qb[gq][1][0], qb[gq][1][1]);
-          s[0] = fmaf(sg[0], ks0[gq], s[0]);
-          s[1] = fmaf(sg[1], ks0[gq], s[1]);
-          s[2] = fmaf(sg[2], ks1[gq], s[2]);
-          s[3] = fmaf(sg[3], ks1[gq], s[3]);
+          mma_f16_16816(sg, a00, a01, a02, a03, qb[nt][gq][0][0], qb[nt][gq][0][1]);
+          mma_f16_16816(sg, a10, a11, a12, a13, qb[nt][gq][1][0], qb[nt][gq][1][1]);
+          s[nt][0] = fmaf(sg[0], ks0[gq], s[nt][0]);
+          s[nt][1] = fmaf(sg[1], ks0[gq], s[nt][1]);
+          s[nt][2] = fmaf(sg[2], ks1[gq], s[nt][2]);
+          s[nt][3] = fmaf(sg[3], ks1[gq], s[nt][3]);
         }
       }
     }
 
-    // ---------------- mask the tail, online softmax over keys (rows)
-    float mx[2] = {-INFINITY, -INFINITY};
+    // ---------------- mask the edges, online softmax over keys (rows of S^T)
+    uint32_t pb[NT][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = s[e] * a.scale_log2;
-      if (tail) {
-        const int k = key0 + (e < 2 ? r0 : r1);
-        if (k < kv_begin || k > ((e & 1) ? lim1 : lim0)) v = -INFINITY;
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = s[nt][e] * a.scale_log2;
+        if (tail) {
+          const int k = key0 + (e < 2 ? r0 : r1);
+          if (k < kv_begin || k > limit(8 * nt + 2 * t + (e & 1))) v = -INFINITY;
+        }
+        s[nt][e] = v;
+        mx[e & 1] = fmaxf(mx[e & 1], v);
       }
-      s[e] = v;
-      mx[e & 1] = fmaxf(mx[e & 1], v);
-    }
-    float alpha[2], mu[2];
-    bool grew = false;
+      float alpha[2], mu[2];
+      bool grew = false;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
-        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
-      const float mn = fmaxf(m_run[c], mx[c]);
-      grew |= mn != m_run[c];
-      mu[c] = mn == -INFINITY ? 0.0f : mn;
-      alpha[c] = fast_exp2(m_run[c] - mu[c]);
-      m_run[c] = mn;
-    }
-    float p[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = fast_exp2(s[e] - mu[e & 1]);
-    const uint32_t pb0 = movmatrix_trans(pack_half2(p[0], p[1]));  // keys 0..7 -> k 2t, 2t+1
-    const uint32_t pb1 = movmatrix_trans(pack_half2(p[2], p[3]));  // keys 8..15 -> k 2t+8, 2t+9
-    // rescale only when some row's running max moved (alpha == 1 otherwise)
-    if (__any_sync(0xffffffffu, grew)) {
-      l_run[0] *= alpha[0];
-      l_run[1] *= alpha[1];
-#pragma unroll
-      for (int i = 0; i < Cfg::kCm; ++i) {
-        o[i][0] *= alpha[0];
-        o[i][1] *= alpha[1];
-        o[i][2] *= alpha[0];
-        o[i][3] *= alpha[1];
+        for (int off = 4; off < 32; off <<= 1)
+          mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
+        const float mn = fmaxf(m_run[nt][c], mx[c]);
+        grew |= mn != m_run[nt][c];
+        mu[c] = mn == -INFINITY ? 0.0f : mn;
+        alpha[c] = fast_exp2(m_run[nt][c] - mu[c]);
+        m_run[nt][c] = mn;
       }
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = fast_exp2(s[nt][e] - mu[e & 1]);
+      pb[nt][0] = movmatrix_trans(pack_half2(p[0], p[1]));  // keys 0..7 -> k 2t, 2t+1
+      pb[nt][1] = movmatrix_trans(pack_half2(p[2], p[3]));  // keys 8..15 -> k 2t+8, 2t+9
+      // rescale only when some row's running max moved (alpha == 1 otherwise)
+      if (__any_sync(0xffffffffu, grew)) {
+        l_run[nt][0] *= alpha[0];
+        l_run[nt][1] *= alpha[1];
+#pragma unroll
+        for (int i = 0; i < Cfg::kCm; ++i) {
+          o[nt][i][0] *= alpha[0];
+          o[nt][i][1] *= alpha[1];
+          o[nt][i][2] *= alpha[0];
+          o[nt][i][3] *= alpha[1];
+        }
+      }
+      l_run[nt][0] += p[0] + p[2];
+      l_run[nt][1] += p[1] + p[3];
     }
-    l_run[0] += p[0] + p[2];
-    l_run[1] += p[1] + p[3];
 
     // ---------------- O^T += V'^T P^T, V' = code * scale (fp8 / 4-bit: idx * scale
     // + zero) in fp16
@@ -384,7 +408,9 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
         a2 = hfma2_u32(a2, vsc.y, vzr.y);
         a1 = hfma2_u32(a1, vsc.x, vzr.x);
         a3 = hfma2_u32(a3, vsc.y, vzr.y);
-        mma_f16_16816(o[cm], a0, a1, a2, a3, pb0, pb1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16_16816(o[nt][cm], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
       }
     } else {
 #pragma unroll
@@ -404,7 +430,9 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
           a2 = hmul2_u32(a2, vsc.y);
           a1 = hmul2_u32(a1, vsc.x);
           a3 = hmul2_u32(a3, vsc.y);
-          mma_f16_16816(o[cm], a0, a1, a2, a3, pb0, pb1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16_16816(o[nt][cm], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
         }
       }
     }
@@ -412,91 +440,119 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8>::kMinBlocks)
 
   // expsum of each row: sum over the 8 lanes that share t
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) l_run[c] += __shfl_xor_sync(0xffffffffu, l_run[c], off);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+        l_run[nt][c] += __shfl_xor_sync(0xffffffffu, l_run[nt][c], off);
 
-  // ---------------- merge the 4 warps (field-major through shared memory)
+  // ---------------- merge the 4 warps through shared memory (field-major), each
+  // warp taking a quarter of the channels of every row, and write the triples
   constexpr int kFields = 4 + 4 * Cfg::kCm;
+  constexpr int kMine = Cfg::kCm / kWarps;  // 16-channel blocks a warp merges
   cp_async_wait<0>();
   __syncthreads();  // every block consumed: reuse the rings
-  if (warp > 0) {
-    float *dst = smem_f + (warp - 1) * kFields * 32 + lane;
-    dst[0] = m_run[0];
-    dst[32] = m_run[1];
-    dst[64] = l_run[0];
-    dst[96] = l_run[1];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float *dst = smem_f + (warp * NT + nt) * kFields * 32 + lane;
+    dst[0] = m_run[nt][0];
+    dst[32] = m_run[nt][1];
+    dst[64] = l_run[nt][0];
+    dst[96] = l_run[nt][1];
 #pragma unroll
     for (int i = 0; i < Cfg::kCm; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dst[(4 + i * 4 + e) * 32] = o[i][e];
+      for (int e = 0; e < 4; ++e) dst[(4 + i * 4 + e) * 32] = o[nt][i][e];
   }
   __syncthreads();
-  if (warp > 0) return;
+  const int64_t step = rows_total(sa) * 4;
 #pragma unroll 1
-  for (int k = 0; k < kWarps - 1; ++k) {
-    const float *src = smem_f + k * kFields * 32 + lane;
-    float wa[2], wb[2];
+  for (int nt = 0; nt < NT && 8 * nt < n_rows; ++nt) {
+    const float *src = smem_f + nt * kFields * 32 + lane;
+    constexpr int kNext = NT * kFields * 32;  // the next warp's
+    float m[2], l[2], wt[kWarps][2], sum[kMine][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const float mo = src[c * 32];
-      const float mn = fmaxf(m_run[c], mo);
-      const float muv = mn == -INFINITY ? 0.0f : mn;
-      wa[c] = fast_exp2(m_run[c] - muv);
-      wb[c] = fast_exp2(mo - muv);
-      m_run[c] = mn;
-      l_run[c] = l_run[c] * wa[c] + src[(2 + c) * 32] * wb[c];
+      m[c] = fmaxf(fmaxf(src[c * 32], src[kNext + c * 32]),
+                   fmaxf(src[2 * kNext + c * 32], src[3 * kNext + c * 32]));
+      const float mu = m[c] == -INFINITY ? 0.0f : m[c];
+      l[c] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        wt[k][c] = fast_exp2(src[k * kNext + c * 32] - mu);
+        l[c] = fmaf(wt[k][c], src[k * kNext + (2 + c) * 32], l[c]);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < Cfg::kCm; ++i)
+    for (int i = 0; i < kMine; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[i][e] = o[i][e] * wa[e & 1] + src[(4 + i * 4 + e) * 32] * wb[e & 1];
-  }
-
-  // ---------------- write the triples: lane (g, t) holds channels cm*16 + g (+8)
-  // of rows 2t, 2t+1
+      for (int e = 0; e < 4; ++e) {
+        sum[i][e] = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int row = 2 * t + c;
-    if (row >= n_rows) continue;
-    const int64_t r = static_cast<int64_t>(q_start) * a.qpk + row, step = rows_total(sa) * 4;
-    float *dst = acc_at<D>(sa, sa.ns_p + sigma, h) + (g >> 2) * step + r * 4 + (g & 3);
+        for (int k = 0; k < kWarps; ++k)
+          sum[i][e] = fmaf(wt[k][e & 1], src[k * kNext + (4 + (warp * kMine + i) * 4 + e) * 32], sum[i][e]);
+      }
+    // lane (g, t) holds channels cm*16 + g (+8) of rows 8 nt + 2t, + 1
 #pragma unroll
-    for (int cm = 0; cm < Cfg::kCm; ++cm) {
-      dst[(cm * 4) * step] = o[cm][c];
-      dst[(cm * 4 + 2) * step] = o[cm][2 + c];
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * nt + 2 * t + c;
+      if (row >= n_rows) continue;
+      const int64_t r = static_cast<int64_t>(q_start) * a.qpk + row0 + row;
+      float *dst = acc_at<D>(sa, sa.ns_p + sigma, h) + (warp * kMine * 4 + (g >> 2)) * step + r * 4 + (g & 3);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        dst[(i * 4) * step] = sum[i][c];
+        dst[(i * 4 + 2) * step] = sum[i][2 + c];
+      }
+      if (warp == 0 && g == 0)
+        *reinterpret_cast<float2 *>(a.part_ml + (ml_at(sa, sa.ns_p + sigma, h) + r) * 2) =
+            make_float2(m[c], l[c]);
     }
-    if (g == 0)
-      *reinterpret_cast<float2 *>(a.part_ml + (ml_at(sa, sa.ns_p + sigma, h) + r) * 2) =
-          make_float2(m_run[c], l_run[c]);
   }
 }
 
-template <int D, int BS, bool F8>
+template <int D, int BS, bool F8, int NT>
 static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream) {
-  using Cfg = SharedRowsCfg<D, BS, F8>;
+  using Cfg = SharedRowsCfg<D, BS, F8, NT>;
   static DeviceOnce configured;
   cudaError_t e = configured.get(nullptr, [](int, int *) {
-    cudaError_t r = cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8>,
+    cudaError_t r = cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     // the tensor-core kernel's carveout, so that blocks of both are resident together
     return r != cudaSuccess ? r
-                            : cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8>,
+                            : cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8, NT>,
                                                    cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   });
   if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(s.a.num_seqs) * s.ns_s * s.a.hk;
+  SharedArgs p = s;
+  p.row_passes = (s.few_rows + 8 * NT - 1) / (8 * NT);
+  const int64_t grid = static_cast<int64_t>(s.a.num_seqs) * s.ns_s * s.a.hk * p.row_passes;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_kernel(shared_rows_kernel<D, BS, F8>, dim3(static_cast<unsigned>(grid)), 128,
-                       Cfg::kSmem, stream, true, s);
+  return launch_kernel(shared_rows_kernel<D, BS, F8, NT>, dim3(static_cast<unsigned>(grid)), 128,
+                       Cfg::kSmem, stream, true, p);
+}
+
+template <int D, int BS>
+static cudaError_t launch_shared_rows_d(const SharedArgs &s, bool f8v4, cudaStream_t stream) {
+  // row tiles a pass: as many as the rows need and the registers hold (4 at
+  // D = 128 ran two blocks an SM and none beside the tensor-core kernel: 48
+  // requests of up to 20 rows took 67 us, two passes of 2 tiles 56)
+  if (s.few_rows <= 8)
+    return f8v4 ? launch_shared_rows_t<D, BS, true, 1>(s, stream)
+                : launch_shared_rows_t<D, BS, false, 1>(s, stream);
+  if (s.few_rows <= 16 || D != 64)
+    return f8v4 ? launch_shared_rows_t<D, BS, true, 2>(s, stream)
+                : launch_shared_rows_t<D, BS, false, 2>(s, stream);
+  if constexpr (D == 64)
+    return f8v4 ? launch_shared_rows_t<D, BS, true, 4>(s, stream)
+                : launch_shared_rows_t<D, BS, false, 4>(s, stream);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_shared_rows(const SharedArgs &s, int d, int bs, bool f8v4, cudaStream_t stream) {
-#define PAQ8_SHARED_CASE(DD, BB)                                           \
-  if (d == DD && bs == BB)                                                 \
-    return f8v4 ? launch_shared_rows_t<DD, BB, true>(s, stream)            \
-                : launch_shared_rows_t<DD, BB, false>(s, stream);
+#define PAQ8_SHARED_CASE(DD, BB) \
+  if (d == DD && bs == BB) return launch_shared_rows_d<DD, BB>(s, f8v4, stream);
   PAQ8_SHARED_CASE(64, 16)
   PAQ8_SHARED_CASE(64, 32)
   PAQ8_SHARED_CASE(128, 16)

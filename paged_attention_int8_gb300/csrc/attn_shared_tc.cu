@@ -556,7 +556,10 @@ static cudaError_t launch_shared_tc_t(const SharedArgs &s, const CUtensorMap &tk
 }
 
 // Rows of one block, 0 where the kernel does not take the head size.
-int shared_tc_rows(int d) { return d == 64 || d == 128 ? 256 : 0; }
+int shared_tc_rows(int d) { return d == 64 || d == 128 ? 256 : d == 256 ? 128 : 0; }
+
+cudaError_t launch_shared_tc256(const SharedArgs &s, const CUtensorMap &tk, const CUtensorMap &tv, int bs,
+                                bool f8v4, cudaStream_t stream);  // attn_shared_tc256.cu
 
 cudaError_t launch_shared_tc(const SharedArgs &s, const CUtensorMap &tk, const CUtensorMap &tv,
                              int d, int bs, bool f8v4, cudaStream_t stream) {
@@ -568,6 +571,7 @@ cudaError_t launch_shared_tc(const SharedArgs &s, const CUtensorMap &tk, const C
   PAQ8_TC_CASE(64, 32)
   PAQ8_TC_CASE(128, 16)
   PAQ8_TC_CASE(128, 32)
+  if (d == 256) return launch_shared_tc256(s, tk, tv, bs, f8v4, stream);
 #undef PAQ8_TC_CASE
   return cudaErrorInvalidValue;
 }

@@ -68,7 +68,8 @@ def test_segments(cuda_device, fmt, d, bs, squeeze):
 # many groups: shares of several short prefixes each, last rows that fill less
 # than half a block, more groups than a warp has lanes, prefixes of no key
 @pytest.mark.parametrize("fmt,hq,hk,d,bs", [("q8", 16, 1, 64, 16), ("q8", 16, 4, 128, 32),
-                                            ("f8v4", 16, 2, 128, 16), ("q8", 14, 2, 64, 32)])
+                                            ("f8v4", 16, 2, 128, 16), ("q8", 14, 2, 64, 32),
+                                            ("q8", 16, 2, 256, 16), ("f8v4", 8, 1, 256, 32)])
 @pytest.mark.parametrize("n_groups", [2, 31, 33, 70])
 def test_many_groups(cuda_device, fmt, hq, hk, d, bs, n_groups):
     sizes = [(7 * i) % 9 + 5 for i in range(n_groups)]
@@ -87,7 +88,8 @@ def test_many_groups(cuda_device, fmt, hq, hk, d, bs, n_groups):
 # one group of several row blocks over a prefix of many tiles, its last block
 # part full; every block's share crosses units
 @pytest.mark.parametrize("fmt,d,n,prefix", [("q8", 128, 150, 1700), ("q8", 64, 90, 2500),
-                                            ("f8v4", 128, 129, 1100)])
+                                            ("f8v4", 128, 129, 1100), ("q8", 256, 70, 1500),
+                                               ("f8v4", 256, 33, 900), ("q8", 256, 32, 4100)])
 def test_shares_cross_units(cuda_device, fmt, d, n, prefix):
     b = S.make(n, cuda_device, fmt, 8, 2, d, 16, [(prefix, [(1, 1 + i % 3) for i in range(n)])])
     ref = S.reference(b)
