@@ -13,8 +13,10 @@
 // Operand buffers: three 32 KB slots that hold the key parts hi(0), lo(0), hi(1),
 // ... in turn, each freed when its own MMAs are done, and one value slot; pages
 // are staged by TMA in rings of their own for keys and for values.
-// Warps: 5 producer, 1 MMA issuer; keys 0, 2, 3, 6; values 4, 7, 12, 13; softmax
-// 8 - 11 (one per TMEM lane quarter).  fp8 / 4-bit: keys are exact in one part.
+// Warps: 5 producer, 1 MMA issuer; keys 0, 2, 3, 6, 14 - 17; values 4, 7, 12, 13;
+// softmax 8 - 11 (one per TMEM lane quarter).  fp8 / 4-bit: keys are exact in one
+// part.  Eight key warps in one pass over both parts: four warps, a pass a part,
+// took 3100 cycles a tile and set the pace.
 #include <type_traits>
 
 #include "attn_shared.cuh"
@@ -29,8 +31,9 @@ constexpr int kD = 256;
 template <int BS, bool F8>
 struct Tc256Cfg {
   static constexpr int kTile = 64;
-  static constexpr int kSt = 2;  // staging stages of each ring
-  static constexpr int kWarps = 14;
+  static constexpr int kStK = 3, kStV = 2;  // staging stages of the rings
+  static constexpr int kWarps = 18;
+  static constexpr int kKWarps = 8;
   static constexpr int kParts = F8 ? 1 : 2;  // key parts: hi, lo
   static constexpr int G = kD / 32;
   static constexpr int kPages = kTile / BS;
@@ -44,8 +47,8 @@ struct Tc256Cfg {
   static constexpr int kPartOff = 0;
   static constexpr int kVOff = 3 * kPartBytes;
   static constexpr int kStKOff = kVOff + kVBytes;
-  static constexpr int kStVOff = kStKOff + kSt * kKStage;
-  static constexpr int kBarOff = (kStVOff + kSt * kVStage + 1023) / 1024 * 1024;
+  static constexpr int kStVOff = kStKOff + kStK * kKStage;
+  static constexpr int kBarOff = (kStVOff + kStV * kVStage + 1023) / 1024 * 1024;
   static constexpr int kSmem = kBarOff + 256 + 1024;
   static constexpr uint32_t kOCol = 0, kQCol = 256, kSCol = 384;
   static constexpr float kMaxTileSum = 32768.0f;  // bound on a tile's P sum (so on every P)
@@ -54,23 +57,24 @@ struct Tc256Cfg {
 
 // barriers (8 bytes each, from kBarOff)
 enum : int {
-  kStKFull = 0,    // [2] producer -> K dequant (tx bytes)
-  kStKEmpty = 2,   // [2] K dequant -> producer (4 warps)
-  kStVFull = 4,    // [2] producer -> V dequant
-  kStVEmpty = 6,   // [2] V dequant -> producer (4 warps)
-  kPartFull = 8,   // [3] K dequant -> MMA (4 warps)
-  kPartEmpty = 11, // [3] commit after the part's MMAs -> K dequant
-  kVFull = 14,     // V dequant -> MMA (4 warps)
-  kPvDone = 15,    // commit after PV -> V dequant, softmax
-  kSFull = 16,     // [2] commit after QK -> softmax
-  kPFull = 18,     // [2] softmax (P in TMEM) -> MMA (4 warps)
-  kQFull = 20,     // softmax (q in TMEM) -> MMA (4 warps)
-  kAllDone = 21,   // commit after the last PV -> softmax (PvDone may be two phases off there)
-  kBars = 22
+  kStKFull = 0,    // [3] producer -> K dequant (tx bytes)
+  kStKEmpty = 3,   // [3] K dequant -> producer (8 warps)
+  kStVFull = 6,    // [2] producer -> V dequant
+  kStVEmpty = 8,   // [2] V dequant -> producer (4 warps)
+  kPartFull = 10,  // [3] K dequant -> MMA (8 warps)
+  kPartEmpty = 13, // [3] commit after the part's MMAs -> K dequant
+  kVFull = 16,     // V dequant -> MMA (4 warps)
+  kPvDone = 17,    // commit after PV -> V dequant, softmax
+  kSFull = 18,     // [2] commit after QK -> softmax
+  kPFull = 20,     // [2] softmax (P in TMEM) -> MMA (4 warps)
+  kQFull = 22,     // softmax (q in TMEM) -> MMA (4 warps)
+  kAllDone = 23,   // commit after the last PV -> softmax (PvDone may be two phases off there)
+  kBars = 24
 };
 
 template <int BS, bool F8>
-__global__ void __launch_bounds__(448, 1)
+// 18 warps, five on two of the SM sub-partitions: 96 registers at most
+__global__ void __maxnreg__(96)
     shared_tc256_kernel(const __grid_constant__ SharedArgs sa, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v) {
   using C = Tc256Cfg<BS, F8>;
@@ -100,15 +104,15 @@ __global__ void __launch_bounds__(448, 1)
   const uint32_t tmem_slot = bars + 8 * kBars;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kStKFull + i), 1);
-      mbar_init(bar(kStKEmpty + i), 4);
       mbar_init(bar(kStVFull + i), 1);
       mbar_init(bar(kStVEmpty + i), 4);
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kPFull + i), 4);
     }
     for (int i = 0; i < 3; ++i) {
-      mbar_init(bar(kPartFull + i), 4);
+      mbar_init(bar(kStKFull + i), 1);
+      mbar_init(bar(kStKEmpty + i), C::kKWarps);
+      mbar_init(bar(kPartFull + i), C::kKWarps);
       mbar_init(bar(kPartEmpty + i), 1);
     }
     mbar_init(bar(kVFull), 4);
@@ -136,12 +140,10 @@ __global__ void __launch_bounds__(448, 1)
     const int32_t *bt_row = a.block_table + static_cast<int64_t>(w.row) * a.bt_stride;
     int page_base = -(1 << 30), my_blk = -1;
     for (int j = 0; ok && j < nt; ++j) {
-      const int sb = j & 1;
-      if (j >= 2) {
+      const int kb = j % C::kStK, vb = j % C::kStV;
+      if (j >= C::kStK) {
         int there = 1;
-        if (lane == 0)
-          there = mbar_wait(bar(kStKEmpty + sb), ((j >> 1) - 1) & 1) &&
-                  mbar_wait(bar(kStVEmpty + sb), ((j >> 1) - 1) & 1);
+        if (lane == 0) there = mbar_wait(bar(kStKEmpty + kb), (j / C::kStK - 1) & 1);
         if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
       }
       const int lp0 = (t0 + j) * C::kPages;
@@ -163,11 +165,8 @@ __global__ void __launch_bounds__(448, 1)
         nvalid += blk[p] >= 0;
       }
       if (lane == 0) {
-        const uint32_t sk = smem_base + C::kStKOff + sb * C::kKStage;
-        const uint32_t sv = smem_base + C::kStVOff + sb * C::kVStage;
-        constexpr uint32_t kVPage = F8 ? D * BS / 2 : D * BS;
-        mbar_arrive_expect_tx(bar(kStKFull + sb), nvalid * (BS * D + (F8 ? 0 : BS * G * 2)));
-        mbar_arrive_expect_tx(bar(kStVFull + sb), nvalid * (kVPage + (F8 ? 4 * BS : BS * G * 2)));
+        const uint32_t sk = smem_base + C::kStKOff + kb * C::kKStage;
+        mbar_arrive_expect_tx(bar(kStKFull + kb), nvalid * (BS * D + (F8 ? 0 : BS * G * 2)));
 #pragma unroll
         for (int p = 0; p < C::kPages; ++p) {
           if (blk[p] < 0) continue;
@@ -175,19 +174,35 @@ __global__ void __launch_bounds__(448, 1)
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub)
             tma_load_2d(sk + sub * (C::kTile * 128) + p * (BS * 128), &tmap_k, sub * 128,
-                        static_cast<int32_t>(page * BS), bar(kStKFull + sb));
+                        static_cast<int32_t>(page * BS), bar(kStKFull + kb));
+          if constexpr (!F8)
+            bulk_load(sk + C::kTile * D + p * (BS * G * 2), a.k_scale + page * BS * G, BS * G * 2,
+                      bar(kStKFull + kb));
+        }
+      }
+      if (j >= C::kStV) {
+        int there = 1;
+        if (lane == 0) there = mbar_wait(bar(kStVEmpty + vb), (j / C::kStV - 1) & 1);
+        if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
+      }
+      if (lane == 0) {
+        const uint32_t sv = smem_base + C::kStVOff + vb * C::kVStage;
+        constexpr uint32_t kVPage = F8 ? D * BS / 2 : D * BS;
+        mbar_arrive_expect_tx(bar(kStVFull + vb), nvalid * (kVPage + (F8 ? 4 * BS : BS * G * 2)));
+#pragma unroll
+        for (int p = 0; p < C::kPages; ++p) {
+          if (blk[p] < 0) continue;
+          const int64_t page = static_cast<int64_t>(blk[p]) * a.hk + h;
           if constexpr (F8) {
             bulk_load(sv + p * kVPage, reinterpret_cast<const uint8_t *>(a.v_cache) + page * kVPage, kVPage,
-                      bar(kStVFull + sb));
-            bulk_load(sv + C::kVCodes + p * (BS * 2), a.v_scale + page * BS, BS * 2, bar(kStVFull + sb));
+                      bar(kStVFull + vb));
+            bulk_load(sv + C::kVCodes + p * (BS * 2), a.v_scale + page * BS, BS * 2, bar(kStVFull + vb));
             bulk_load(sv + C::kVCodes + C::kTile * 2 + p * (BS * 2), a.v_zero + page * BS, BS * 2,
-                      bar(kStVFull + sb));
+                      bar(kStVFull + vb));
           } else {
-            bulk_load(sk + C::kTile * D + p * (BS * G * 2), a.k_scale + page * BS * G, BS * G * 2,
-                      bar(kStKFull + sb));
-            tma_load_2d(sv + p * kVPage, &tmap_v, 0, static_cast<int32_t>(page * D), bar(kStVFull + sb));
+            tma_load_2d(sv + p * kVPage, &tmap_v, 0, static_cast<int32_t>(page * D), bar(kStVFull + vb));
             bulk_load(sv + C::kVCodes + p * (BS * G * 2), a.v_scale + page * BS * G, BS * G * 2,
-                      bar(kStVFull + sb));
+                      bar(kStVFull + vb));
           }
         }
       }
@@ -249,64 +264,80 @@ __global__ void __launch_bounds__(448, 1)
       if (ok) tc::commit(bar(kAllDone));
     }
     ok = __all_sync(0xffffffffu, ok);
-  } else if (warp == 0 || warp == 2 || warp == 3 || warp == 6) {
+  } else if (warp == 0 || warp == 2 || warp == 3 || warp == 6 || warp >= 14) {
     // ============================================================ K dequant
-    // thread = one key row, 128 channels; the parts one after the other
-    const int t = (warp == 6 ? 3 : warp == 0 ? 0 : warp - 1) * 32 + lane;
+    // thread = one key row, 64 channels (two scale groups), both parts in one pass:
+    // the slots of tile j are free once the hi MMAs of tile j - 1 are done
+    const int t = (warp >= 14 ? warp - 10 : warp == 6 ? 3 : warp == 0 ? 0 : warp - 1) * 32 + lane;
     const int r = t & 63;
-    const int c0 = (t >> 6) * 128;
+    const int c0 = (t >> 6) * 64;
     uint32_t slot = 0, phase = 1;  // of the next part: the first round's slots are free
+    auto step = [&]() {
+      if (++slot == 3) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
-      const int sb = j & 1;
-      if (!mbar_wait(bar(kStKFull + sb), (j >> 1) & 1)) { ok = false; break; }
-      const uint32_t st = smem_base + C::kStKOff + sb * C::kKStage;
+      const int kb = j % C::kStK;
+      uint32_t part[2];
+      part[0] = slot;
+      if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
+      step();
+      if constexpr (!F8) {
+        part[1] = slot;
+        if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
+        step();
+      }
+      if (!mbar_wait(bar(kStKFull + kb), (j / C::kStK) & 1)) { ok = false; break; }
+      const uint32_t st = smem_base + C::kStKOff + kb * C::kKStage;
+      const uint32_t hi_dst = smem_base + C::kPartOff + part[0] * C::kPartBytes;
+      const uint32_t lo_dst = F8 ? 0u : smem_base + C::kPartOff + part[F8 ? 0 : 1] * C::kPartBytes;
       // keys at and past the prefix's end may hold stale bytes: converted as zeros
       const bool dead = (t0 + j) * C::kTile + r >= kv_end;
-#pragma unroll 1
-      for (int part = 0; part < C::kParts; ++part) {
-        if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
-        const uint32_t kdst = smem_base + C::kPartOff + slot * C::kPartBytes;
-#pragma unroll 2
-        for (int c = c0; c < c0 + 128; c += 16) {
-          const uint4 codes = lds128(st + L::k_off(r, c));
-          const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-          uint32_t out[8];
-          if constexpr (F8) {
+      const uint32_t scales = F8 || dead ? 0u : lds32(st + C::kTile * D + (r * G + c0 / 32) * 2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              out[2 * i] = dead ? 0u : e4m3x2_to_half2(cw[i]);
-              out[2 * i + 1] = dead ? 0u : e4m3x2_to_half2(cw[i] >> 16);
-            }
-          } else {
-            const uint32_t sbits = lds16(st + C::kTile * D + (r * G + c / 32) * 2);
-            const uint32_t s2 = dead ? 0u : (sbits | (sbits << 16));
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 16 * i;
+        const uint4 codes = lds128(st + L::k_off(r, c));
+        const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+        uint32_t hw[8], lw[8];
+        if constexpr (F8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t lo, hi;
-              codes4_to_half2(cw[i], lo, hi);
-              // hi part fp16(code * s); second part code * (-s) + hi = -lo, exact
-              out[2 * i] = hmul2_u32(lo, s2);
-              out[2 * i + 1] = hmul2_u32(hi, s2);
-              if (part) {
-                out[2 * i] = hfma2_u32(lo, s2 ^ 0x80008000u, out[2 * i]);
-                out[2 * i + 1] = hfma2_u32(hi, s2 ^ 0x80008000u, out[2 * i + 1]);
-              }
-            }
+          for (int k = 0; k < 4; ++k) {
+            hw[2 * k] = dead ? 0u : e4m3x2_to_half2(cw[k]);
+            hw[2 * k + 1] = dead ? 0u : e4m3x2_to_half2(cw[k] >> 16);
           }
-          sts128(kdst + tc::sw128_chunk(r, c / 8, 64), make_uint4(out[0], out[1], out[2], out[3]));
-          sts128(kdst + tc::sw128_chunk(r, c / 8 + 1, 64), make_uint4(out[4], out[5], out[6], out[7]));
+        } else {
+          const uint32_t s2 = __byte_perm(scales, 0u, i < 2 ? 0x1010 : 0x3232);
+          const uint32_t ns2 = s2 ^ 0x80008000u;  // -scale
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t lo, hi;
+            codes4_to_half2(cw[k], lo, hi);
+            // hi part fp16(code * s); second part code * (-s) + hi = -lo, exact
+            hw[2 * k] = hmul2_u32(lo, s2);
+            hw[2 * k + 1] = hmul2_u32(hi, s2);
+            lw[2 * k] = hfma2_u32(lo, ns2, hw[2 * k]);
+            lw[2 * k + 1] = hfma2_u32(hi, ns2, hw[2 * k + 1]);
+          }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPartFull + slot));
-        if (++slot == 3) {
-          slot = 0;
-          phase ^= 1;
+        const uint32_t o0 = tc::sw128_chunk(r, c / 8, 64), o1 = tc::sw128_chunk(r, c / 8 + 1, 64);
+        sts128(hi_dst + o0, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+        sts128(hi_dst + o1, make_uint4(hw[4], hw[5], hw[6], hw[7]));
+        if constexpr (!F8) {
+          sts128(lo_dst + o0, make_uint4(lw[0], lw[1], lw[2], lw[3]));
+          sts128(lo_dst + o1, make_uint4(lw[4], lw[5], lw[6], lw[7]));
         }
       }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(bar(kStKEmpty + sb));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kPartFull + part[0]));
+        if constexpr (!F8) mbar_arrive(bar(kPartFull + part[1]));
+        mbar_arrive(bar(kStKEmpty + kb));
+      }
     }
   } else if (warp == 4 || warp == 7 || warp >= 12) {
     // ============================================================ V dequant
@@ -323,7 +354,7 @@ __global__ void __launch_bounds__(448, 1)
       const uint32_t vrow = smem_base + C::kVOff;
       const int key0 = (t0 + j) * C::kTile;
       const bool tail = key0 + C::kTile > kv_end;
-#pragma unroll 1
+#pragma unroll 2
       for (int key = 0; key < C::kTile; key += 16) {
         uint32_t sc[8], zr[8];
         {
