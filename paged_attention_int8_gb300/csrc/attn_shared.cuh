@@ -78,6 +78,19 @@ __device__ __forceinline__ int group_token(const SharedArgs &s, int g) {
 // the group's entries are out of range.
 __device__ __forceinline__ int prefix_of(const SharedArgs &s, int seq, int lane,
                                          int *group = nullptr) {
+  if (s.num_groups <= 32) {  // a lane a group: one round of loads
+    int first = 0x7fffffff, end = 0, len = 0;
+    if (lane < s.num_groups) {
+      first = s.cu_groups[lane];
+      end = s.cu_groups[lane + 1];
+      len = s.prefix_lens[lane];
+    }
+    const unsigned ball = __ballot_sync(0xffffffffu, first <= seq);
+    const int g = ball ? 31 - __clz(ball) : 0;
+    if (group) *group = g;
+    if (__shfl_sync(0xffffffffu, first, g) > seq || __shfl_sync(0xffffffffu, end, g) <= seq) return -1;
+    return __shfl_sync(0xffffffffu, len, g);
+  }
   const int g = find_last(s.num_groups, seq, lane, [&](int i) { return s.cu_groups[i]; });
   if (group) *group = g;
   if (s.cu_groups[g] > seq || s.cu_groups[g + 1] <= seq) return -1;
@@ -124,10 +137,12 @@ __device__ __forceinline__ bool segment_keys(int begin, int end, int seg_tiles, 
 __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int item, int block_q, int lane,
                                             SharedWork &w) {
   const AttnArgs &a = s.a;
-  int g, tok0, sigma, c0, c1;
+  int g, tok0, sigma, c0, c1, P;
   if (s.num_groups <= 32) {
-    int b0 = 0, b1 = 0;
+    int b0 = 0, b1 = 0, first = 0, len = 0;
     if (lane < s.num_groups) {
+      len = s.prefix_lens[lane];
+      first = s.cu_groups[lane];
       b0 = group_token(s, lane);
       b1 = group_token(s, lane + 1);
     }
@@ -146,6 +161,8 @@ __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int item, int b
     g = __ffs(past) - 1;
     c0 = __shfl_sync(0xffffffffu, b0, g);
     c1 = __shfl_sync(0xffffffffu, b1, g);
+    w.row = __shfl_sync(0xffffffffu, first, g);
+    P = __shfl_sync(0xffffffffu, len, g);
     tok0 = (blk - __shfl_sync(0xffffffffu, upto - mine, g)) * block_q;
   } else {
     const int blk = item % s.n_pblocks;
@@ -160,10 +177,10 @@ __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int item, int b
     if (c0 < 0 || c1 > a.num_tokens) return false;  // the suffix items flag it
     tok0 = (blk - (c0 / block_q + g)) * block_q;
     if (tok0 < 0 || tok0 >= c1 - c0) return false;
+    w.row = s.cu_groups[g];
+    P = s.prefix_lens[g];
   }
-  const int P = s.prefix_lens[g];
   if (P <= 0) return false;
-  w.row = s.cu_groups[g];
   w.q0 = c0 + tok0;
   w.n_tok = min(block_q, c1 - c0 - tok0);
   w.slot = sigma;
@@ -221,6 +238,32 @@ __device__ __forceinline__ int64_t ml_at(const SharedArgs &s, int k, int h) {
 template <int D>
 __device__ __forceinline__ float *acc_at(const SharedArgs &s, int k, int h) {
   return s.a.part_acc + ml_at(s, k, h) * D;
+}
+
+// q rows r0 .. r0 + 31 of a block (row r: q head h qpk + r % qpk of query token
+// q0 + r / qpk; rows at and past n_rows are left out) to shared memory at dst, by
+// one warp: whole lines, all in flight, and no registers held.  A lane that reads
+// its own row from global memory touches a line per piece: the 4096 lookups of a
+// block's rows took 4 us.  Pieces of 16 bytes stand swizzled for reads by row.
+template <int D>
+__device__ __forceinline__ uint32_t q_piece(uint32_t dst, int r, int piece) {
+  return dst + r * (2 * D) + ((piece * 16) ^ ((r & 7) << 4));
+}
+template <int D>
+__device__ __forceinline__ void copy_q_rows(const AttnArgs &a, uint32_t dst, int q0, int h, int r0,
+                                            int n_rows, int lane) {
+  constexpr int kPieces = D / 8, kStep = 32 / kPieces;
+  const int magic = (65536 + a.qpk - 1) / a.qpk;  // r / qpk = r magic / 65536 for r < 256, qpk <= 16
+  const uint16_t *base = a.q + (static_cast<int64_t>(q0) * a.hq + h * a.qpk) * D + lane % kPieces * 8;
+#pragma unroll 8
+  for (int i = 0; i < 32; i += kStep) {
+    const int r = i + lane / kPieces;
+    const int tok = ((r0 + r) * magic) >> 16;
+    if (r0 + r < n_rows)
+      cp_async16(q_piece<D>(dst, r, lane % kPieces),
+                 base + (static_cast<int64_t>(tok) * (a.hq - a.qpk) + r0 + r) * D);
+  }
+  cp_async_commit();
 }
 
 // Programmatic launches.  The call's kernels work on disjoint triples, so each

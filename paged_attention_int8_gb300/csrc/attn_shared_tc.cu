@@ -48,6 +48,7 @@ struct SharedTcCfg {
   static constexpr float kMaxTileSum = 32768.0f;  // bound on a tile's P sum (so on every P)
   static_assert(D == 64 || D == 128, "the tcgen05 kernel handles D = 64, 128");
   static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kKSlot + 2 * kVBytes >= kRows * 2 * D, "q rows in K slot 1 and the V slots");
   static_assert(kSt <= 4, "staging barriers");
 };
 
@@ -83,6 +84,10 @@ __global__ void __maxnreg__(96)
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(sa.a.hk));
 
   launch_dependents();
+  if (threadIdx.x == 5 * 32) {
+    prefetch_tensormap(&tmap_k);
+    if constexpr (!F8) prefetch_tensormap(&tmap_v);
+  }
   SharedWork w;
   if (!prefix_work(sa, static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk)), a.block_q, lane, w))
     return;
@@ -90,19 +95,11 @@ __global__ void __maxnreg__(96)
   const int kv_begin = w.kv_begin, kv_end = w.kv_end;  // kv_begin starts a tile
   const int t0 = kv_begin / C::kTile;
   const int nt = (kv_end + C::kTile - 1) / C::kTile - t0;
-  // the softmax warps' q rows, one per thread: in flight during the set-up
-  const bool softmax_warp = warp >= 6 && warp < 14;
-  const int q_row = ((warp - 6) >> 2) * 128 + (warp & 3) * 32 + lane;
-  uint4 qv[D / 8];
-  if (softmax_warp) {
-    const bool valid = q_row < n_rows;
-    const int tq = valid ? q_row / a.qpk : 0;
-    const uint16_t *src =
-        a.q + (static_cast<int64_t>(w.q0 + tq) * a.hq + h * a.qpk + (valid ? q_row % a.qpk : 0)) * D;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      qv[c] = valid ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-  }
+  // the softmax warps' 32 rows of q each, in flight during the set-up: they stand
+  // in K slot 1 and the V slots until they are in TMEM
+  const int row0 = ((warp - 6) >> 2) * 128 + (warp & 3) * 32;
+  const uint32_t q_smem = smem_base + C::kKOff + C::kKSlot + row0 * (2 * D);
+  if (warp >= 6 && warp < 14) copy_q_rows<D>(a, q_smem, w.q0, h, row0, n_rows, lane);
   // half 1 holds no valid row when the block is short: it is then skipped
   const int halves = n_rows > 128 ? 2 : 1;
 
@@ -137,10 +134,6 @@ __global__ void __maxnreg__(96)
 
   if (warp == 5) {
     // ============================================================ producer
-    if (lane == 0) {
-      prefetch_tensormap(&tmap_k);
-      if constexpr (!F8) prefetch_tensormap(&tmap_v);
-    }
     if constexpr (F8)
       produce_tiles_f8v4_tma<L, BS, C::kSt>(a, &tmap_k, smem_base, bar(kBarStFull),
                                             bar(kBarStEmpty), w.row, h, t0, nt, kv_begin, kv_end,
@@ -223,6 +216,8 @@ __global__ void __maxnreg__(96)
       const int key0 = (t0 + j) * C::kTile;
       // keys at and past kv_end may hold stale bytes: converted as zeros
       const bool tail = key0 + C::kTile > kv_end;
+      // K slot 1 and the V slots hold q until it is in TMEM
+      if (j == (k_side ? 1 : 0) && !mbar_wait(bar(kBarQFull), 0)) { ok = false; break; }
       if (k_side) {
         if (j >= 2 && !mbar_wait(bar(kBarKEmpty + b), ((j - 2) >> 1) & 1)) { ok = false; break; }
         const uint32_t kdst = smem_base + C::kKOff + b * C::kKSlot;
@@ -376,20 +371,21 @@ __global__ void __maxnreg__(96)
     // ============================================================ softmax
     const int hf = (warp - 6) >> 2;  // which 128-row half
     const int quarter = warp & 3;    // TMEM lanes this warp may access
-    const int lrow = quarter * 32 + lane;
-    const int row = hf * 128 + lrow;
+    const int row = row0 + lane;
     const uint32_t t_lane = tmem + hf * C::kHalfCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const bool valid = row < n_rows;
     const float sl2 = a.scale_log2;
     // q row -> fp16 pairs in this lane's q columns (the QK MMA's A operand)
     {
       bool bad_q = false;
+      cp_async_wait<0>();
+      __syncwarp();
 #pragma unroll
       for (int cb = 0; cb < D / 64; ++cb) {
         uint32_t qw[32];
 #pragma unroll
         for (int c16 = 0; c16 < 8; ++c16) {
-          const uint4 v = qv[cb * 8 + c16];
+          const uint4 v = valid ? lds128(q_piece<D>(q_smem, lane, cb * 8 + c16)) : make_uint4(0u, 0u, 0u, 0u);
           qw[4 * c16 + 0] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
           qw[4 * c16 + 1] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
           qw[4 * c16 + 2] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));

@@ -13,7 +13,7 @@
 // Operand buffers: three 32 KB slots that hold the key parts hi(0), lo(0), hi(1),
 // ... in turn, each freed when its own MMAs are done, and one value slot; pages
 // are staged by TMA in rings of their own for keys and for values.
-// Warps: 5 producer, 1 MMA issuer; keys 0, 2, 3, 6, 14 - 17; values 4, 7, 12, 13;
+// Warps: 5 and 18 producers, 1 MMA issuer; keys 0, 2, 3, 6, 14 - 17; values 4, 7, 12, 13;
 // softmax 8 - 11 (one per TMEM lane quarter).  fp8 / 4-bit: keys are exact in one
 // part.  Eight key warps in one pass over both parts: four warps, a pass a part,
 // took 3100 cycles a tile and set the pace.
@@ -32,7 +32,7 @@ template <int BS, bool F8>
 struct Tc256Cfg {
   static constexpr int kTile = 64;
   static constexpr int kStK = 3, kStV = 2;  // staging stages of the rings
-  static constexpr int kWarps = 18;
+  static constexpr int kWarps = 19;
   static constexpr int kKWarps = 8;
   static constexpr int kParts = F8 ? 1 : 2;  // key parts: hi, lo
   static constexpr int G = kD / 32;
@@ -73,7 +73,7 @@ enum : int {
 };
 
 template <int BS, bool F8>
-// 18 warps, five on two of the SM sub-partitions: 96 registers at most
+// 19 warps, five on three of the SM sub-partitions: 96 registers at most
 __global__ void __maxnreg__(96)
     shared_tc256_kernel(const __grid_constant__ SharedArgs sa, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v) {
@@ -91,10 +91,19 @@ __global__ void __maxnreg__(96)
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(sa.a.hk));
 
   launch_dependents();
+  if (threadIdx.x == 5 * 32) prefetch_tensormap(&tmap_k);
+  if constexpr (!F8) {
+    if (threadIdx.x == 18 * 32) prefetch_tensormap(&tmap_v);
+  }
   SharedWork w;
   if (!prefix_work(sa, static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk)), a.block_q, lane, w))
     return;
   const int n_rows = w.n_tok * a.qpk;
+  // the softmax warps' 32 rows of q each, in flight during the set-up: they stand
+  // in part slot 2 and the value slot until they are in TMEM
+  const int row0 = (warp & 3) * 32;
+  const uint32_t q_smem = smem_base + C::kPartOff + 2 * C::kPartBytes + row0 * (2 * D);
+  if (warp >= 8 && warp < 12) copy_q_rows<D>(a, q_smem, w.q0, h, row0, n_rows, lane);
   const int kv_end = w.kv_end;  // kv_begin starts a tile
   const int t0 = w.kv_begin / C::kTile;
   const int nt = (kv_end + C::kTile - 1) / C::kTile - t0;
@@ -128,22 +137,23 @@ __global__ void __maxnreg__(96)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kBarOff + 8 * kBars);
   bool ok = true;
 
-  if (warp == 5) {
-    // ============================================================ producer
+  if (warp == 5 || warp == 18) {
+    // ============================================================ producers
+    // One warp stages the keys, one the values: the values' ring is the shorter one
+    // and follows PV, and one warp in order for both held the keys back to it.
     // Block-table entries are read 32 pages at a time, one per lane; pages at or
     // past the prefix's end are not staged.
-    if (lane == 0) {
-      prefetch_tensormap(&tmap_k);
-      if constexpr (!F8) prefetch_tensormap(&tmap_v);
-    }
+    const bool keys = warp == 5;
+    const int n_st = keys ? C::kStK : C::kStV;
+    const int full0 = keys ? kStKFull : kStVFull, empty0 = keys ? kStKEmpty : kStVEmpty;
     const int n_pages = (kv_end + BS - 1) / BS;
     const int32_t *bt_row = a.block_table + static_cast<int64_t>(w.row) * a.bt_stride;
     int page_base = -(1 << 30), my_blk = -1;
+    int st = 0, phase = 1;  // stage of the ring and the parity of its being empty
     for (int j = 0; ok && j < nt; ++j) {
-      const int kb = j % C::kStK, vb = j % C::kStV;
-      if (j >= C::kStK) {
+      if (j >= n_st) {
         int there = 1;
-        if (lane == 0) there = mbar_wait(bar(kStKEmpty + kb), (j / C::kStK - 1) & 1);
+        if (lane == 0) there = mbar_wait(bar(empty0 + st), phase);
         if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
       }
       const int lp0 = (t0 + j) * C::kPages;
@@ -164,9 +174,9 @@ __global__ void __maxnreg__(96)
         blk[p] = __shfl_sync(0xffffffffu, my_blk, lp0 + p - page_base);
         nvalid += blk[p] >= 0;
       }
-      if (lane == 0) {
-        const uint32_t sk = smem_base + C::kStKOff + kb * C::kKStage;
-        mbar_arrive_expect_tx(bar(kStKFull + kb), nvalid * (BS * D + (F8 ? 0 : BS * G * 2)));
+      if (lane == 0 && keys) {
+        const uint32_t sk = smem_base + C::kStKOff + st * C::kKStage;
+        mbar_arrive_expect_tx(bar(full0 + st), nvalid * (BS * D + (F8 ? 0 : BS * G * 2)));
 #pragma unroll
         for (int p = 0; p < C::kPages; ++p) {
           if (blk[p] < 0) continue;
@@ -174,37 +184,35 @@ __global__ void __maxnreg__(96)
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub)
             tma_load_2d(sk + sub * (C::kTile * 128) + p * (BS * 128), &tmap_k, sub * 128,
-                        static_cast<int32_t>(page * BS), bar(kStKFull + kb));
+                        static_cast<int32_t>(page * BS), bar(full0 + st));
           if constexpr (!F8)
             bulk_load(sk + C::kTile * D + p * (BS * G * 2), a.k_scale + page * BS * G, BS * G * 2,
-                      bar(kStKFull + kb));
+                      bar(full0 + st));
         }
-      }
-      if (j >= C::kStV) {
-        int there = 1;
-        if (lane == 0) there = mbar_wait(bar(kStVEmpty + vb), (j / C::kStV - 1) & 1);
-        if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
-      }
-      if (lane == 0) {
-        const uint32_t sv = smem_base + C::kStVOff + vb * C::kVStage;
+      } else if (lane == 0) {
+        const uint32_t sv = smem_base + C::kStVOff + st * C::kVStage;
         constexpr uint32_t kVPage = F8 ? D * BS / 2 : D * BS;
-        mbar_arrive_expect_tx(bar(kStVFull + vb), nvalid * (kVPage + (F8 ? 4 * BS : BS * G * 2)));
+        mbar_arrive_expect_tx(bar(full0 + st), nvalid * (kVPage + (F8 ? 4 * BS : BS * G * 2)));
 #pragma unroll
         for (int p = 0; p < C::kPages; ++p) {
           if (blk[p] < 0) continue;
           const int64_t page = static_cast<int64_t>(blk[p]) * a.hk + h;
           if constexpr (F8) {
             bulk_load(sv + p * kVPage, reinterpret_cast<const uint8_t *>(a.v_cache) + page * kVPage, kVPage,
-                      bar(kStVFull + vb));
-            bulk_load(sv + C::kVCodes + p * (BS * 2), a.v_scale + page * BS, BS * 2, bar(kStVFull + vb));
+                      bar(full0 + st));
+            bulk_load(sv + C::kVCodes + p * (BS * 2), a.v_scale + page * BS, BS * 2, bar(full0 + st));
             bulk_load(sv + C::kVCodes + C::kTile * 2 + p * (BS * 2), a.v_zero + page * BS, BS * 2,
-                      bar(kStVFull + vb));
+                      bar(full0 + st));
           } else {
-            tma_load_2d(sv + p * kVPage, &tmap_v, 0, static_cast<int32_t>(page * D), bar(kStVFull + vb));
+            tma_load_2d(sv + p * kVPage, &tmap_v, 0, static_cast<int32_t>(page * D), bar(full0 + st));
             bulk_load(sv + C::kVCodes + p * (BS * G * 2), a.v_scale + page * BS * G, BS * G * 2,
-                      bar(kStVFull + vb));
+                      bar(full0 + st));
           }
         }
+      }
+      if (++st == n_st) {
+        st = 0;
+        phase ^= 1;
       }
       __syncwarp();
     }
@@ -264,7 +272,7 @@ __global__ void __maxnreg__(96)
       if (ok) tc::commit(bar(kAllDone));
     }
     ok = __all_sync(0xffffffffu, ok);
-  } else if (warp == 0 || warp == 2 || warp == 3 || warp == 6 || warp >= 14) {
+  } else if (warp == 0 || warp == 2 || warp == 3 || warp == 6 || (warp >= 14 && warp < 18)) {
     // ============================================================ K dequant
     // thread = one key row, 64 channels (two scale groups), both parts in one pass:
     // the slots of tile j are free once the hi MMAs of tile j - 1 are done
@@ -281,6 +289,7 @@ __global__ void __maxnreg__(96)
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int kb = j % C::kStK;
+      if (j == 1 && !mbar_wait(bar(kQFull), 0)) { ok = false; break; }  // q is out of slot 2
       uint32_t part[2];
       part[0] = slot;
       if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
@@ -339,7 +348,7 @@ __global__ void __maxnreg__(96)
         mbar_arrive(bar(kStKEmpty + kb));
       }
     }
-  } else if (warp == 4 || warp == 7 || warp >= 12) {
+  } else if (warp == 4 || warp == 7 || warp == 12 || warp == 13) {
     // ============================================================ V dequant
     // thread = two channel rows of one scale group, all 64 keys
     const int t = (warp == 4 ? 0 : warp == 7 ? 1 : warp - 10) * 32 + lane;
@@ -349,7 +358,8 @@ __global__ void __maxnreg__(96)
     for (int j = 0; j < nt; ++j) {
       const int sb = j & 1;
       if (!mbar_wait(bar(kStVFull + sb), (j >> 1) & 1)) { ok = false; break; }
-      if (j >= 1 && !mbar_wait(bar(kPvDone), (j - 1) & 1)) { ok = false; break; }
+      // the slot is free once q is in TMEM, then with each PV
+      if (!mbar_wait(bar(j >= 1 ? kPvDone : kQFull), j >= 1 ? (j - 1) & 1 : 0)) { ok = false; break; }
       const uint32_t st = smem_base + C::kStVOff + sb * C::kVStage;
       const uint32_t vrow = smem_base + C::kVOff;
       const int key0 = (t0 + j) * C::kTile;
@@ -417,32 +427,24 @@ __global__ void __maxnreg__(96)
   } else {
     // ============================================================ softmax
     const int quarter = warp & 3;  // TMEM lanes this warp may access
-    const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const bool valid = row < n_rows;
+    const bool valid = row0 + lane < n_rows;
     const float sl2 = a.scale_log2;
     // q row -> fp16 pairs in this lane's q columns (the QK MMA's A operand)
     {
-      const int tq = valid ? row / a.qpk : 0;
-      const uint16_t *src =
-          a.q + (static_cast<int64_t>(w.q0 + tq) * a.hq + h * a.qpk + (valid ? row % a.qpk : 0)) * D;
       bool bad_q = false;
+      cp_async_wait<0>();
+      __syncwarp();
 #pragma unroll 1
       for (int cb = 0; cb < D / 64; ++cb) {
-        uint4 qv[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) qv[c] = *reinterpret_cast<const uint4 *>(src + cb * 64 + 8 * c);
-        }
         uint32_t qw[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          qw[4 * c + 0] = pack_half2(bf16_lo(qv[c].x), bf16_hi(qv[c].x));
-          qw[4 * c + 1] = pack_half2(bf16_lo(qv[c].y), bf16_hi(qv[c].y));
-          qw[4 * c + 2] = pack_half2(bf16_lo(qv[c].z), bf16_hi(qv[c].z));
-          qw[4 * c + 3] = pack_half2(bf16_lo(qv[c].w), bf16_hi(qv[c].w));
+          const uint4 v = valid ? lds128(q_piece<D>(q_smem, lane, cb * 8 + c)) : make_uint4(0u, 0u, 0u, 0u);
+          qw[4 * c + 0] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
+          qw[4 * c + 1] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
+          qw[4 * c + 2] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));
+          qw[4 * c + 3] = pack_half2(bf16_lo(v.w), bf16_hi(v.w));
           bad_q |= half2_nonfinite(qw[4 * c]) || half2_nonfinite(qw[4 * c + 1]) ||
                    half2_nonfinite(qw[4 * c + 2]) || half2_nonfinite(qw[4 * c + 3]);
         }
@@ -553,7 +555,7 @@ __global__ void __maxnreg__(96)
     // ---- epilogue: the row's triple
     if (ok && __all_sync(0xffffffffu, mbar_wait(bar(kAllDone), 0))) {
       tc::fence_after();
-      const int64_t r = static_cast<int64_t>(w.q0) * a.qpk + row, step = rows_total(sa) * 4;
+      const int64_t r = static_cast<int64_t>(w.q0) * a.qpk + row0 + lane, step = rows_total(sa) * 4;
       float *dst = acc_at<D>(sa, w.slot, h) + r * 4;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
