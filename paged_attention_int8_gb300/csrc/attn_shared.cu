@@ -497,10 +497,27 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
                            int32_t max_suffix_len) {
   const int qpk = hq / hk;
   SharedSplits r;
+  // suffixes: blocks of a segment (16 rows in the rows kernel, 64 in the row-tile
+  // kernel), tiles of the longest
+  const int64_t most = static_cast<int64_t>(max_query_len) * qpk;
+  const bool few = most <= kFewRows;
+  const int64_t sunits = static_cast<int64_t>(num_seqs) * hk *
+                         (few ? (most + 15) / 16 : (most + kRowTile - 1) / kRowTile);
+  const int64_t stiles = (static_cast<int64_t>(max_suffix_len) + kTile - 1) / kTile;
   {
-    // prefix: the count of segments that ends soonest, in units of a tile's
-    // time: whole waves of blocks of (tiles + the block's fixed cost), plus
-    // the join's traffic (a triple is written and read once more per segment)
+    // prefix: the count of segments that ends soonest, in units of a tile's time,
+    // of a model fitted to 47 batches x 20 counts each (all D, both formats, 1 - 128
+    // sequences, 1 - 5 groups): on average it is 3.3 % above the best count's time
+    // (2.6 % on 26 others), where whole waves of the prefix's blocks by themselves
+    // were 8.4 % above it.
+    //  - A block takes its tiles and 5 more (set-up, first loads, triples).
+    //  - The suffixes (half of the longest on average, and 4 tiles of set-up; a tile
+    //    is 0.3 of a prefix tile, 3 in the row-tile kernel) run beside it, on the SMs
+    //    that the prefix's blocks leave and a little on theirs.  So a prefix of few,
+    //    long blocks on half of the SMs beats one on all of them: 64 requests, 8192
+    //    keys, 8 segments 41 us, 19 segments 52.
+    //  - Several groups: their lengths differ, and waves overlap.
+    //  - The join reads a triple a segment, 16 in flight at a time.
     const bool tc = prefix_on_tc(num_tokens, num_groups, qpk, d);
     const int rows = tc ? shared_tc_rows(d) : kRowTile;
     const int64_t block_q = std::max(1, rows / qpk);
@@ -508,12 +525,20 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
         std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q) * hk;
     const int64_t slots = tc || d == 256 ? 152 : 304;  // resident blocks
     const int64_t tiles = std::max(1, (max_prefix_len + kTile - 1) / kTile);
-    const double fixed = 4.0, join = static_cast<double>(num_tokens) * hq * (d + 2) * 8 / 6.6e6;
+    const double join = static_cast<double>(num_tokens) * hq * (d + 2) * 8 / 1.65e6;
+    const double suffix =
+        (few ? 0.3 : 3.0) * static_cast<double>(sunits) * (0.5 * static_cast<double>(stiles) + 4.0);
+    const double held = !tc ? 0.5 : d == 256 ? 1.0 : 0.9;  // share of an SM a prefix block takes
     double best = 0;
     r.prefix = 1;
     for (int n = 1; n <= 64 && n <= tiles; ++n) {
-      const double waves = static_cast<double>((units * n + slots - 1) / slots);
-      const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + fixed) + join * n;
+      const double blocks = static_cast<double>(units * n);
+      const double waves = num_groups == 1 ? static_cast<double>((units * n + slots - 1) / slots)
+                                           : std::max(1.0, 0.9 * blocks / static_cast<double>(slots));
+      const double block = static_cast<double>((tiles + n - 1) / n) + 5.0;
+      const double cost =
+          std::max(waves * block, (blocks * block * held + suffix) / static_cast<double>(slots)) +
+          join * n + 1.5 * ((n + 15) / 16);
       if (n == 1 || cost < best) {
         best = cost;
         r.prefix = n;
@@ -521,14 +546,14 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
     }
   }
   {
-    // suffix: ~1024 keys a segment (the decode kernel's measured best), more
-    // segments only while blocks are too few to fill the GPU four to an SM
-    const int64_t most = std::min<int64_t>(static_cast<int64_t>(max_query_len) * qpk, kFewRows);
-    const int64_t units = static_cast<int64_t>(num_seqs) * hk * ((most + 15) / 16);
-    const int64_t tiles = (max_suffix_len + kTile - 1) / kTile;
-    int64_t n = std::max<int64_t>((max_suffix_len + 1023) / 1024,
-                                  std::min((608 + units - 1) / units, (tiles + 3) / 4));
-    n = std::min(n, std::max<int64_t>(1, 8192 / units));
+    // suffix: ~1024 keys a segment (the decode kernel's measured best), more only
+    // while blocks are too few to fill the GPU, four of the rows kernel to an SM, of
+    // 4 tiles at least; two of the row-tile kernel, a tile at least (2 x 40 tokens of
+    // 16 rows behind 1284 keys of D = 256: 7 segments 35 us, 3 45)
+    const int64_t full = few ? 608 : 304, cap = few ? (stiles + 3) / 4 : stiles + 1;
+    int64_t n = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + 1023) / 1024,
+                                  std::min((full + sunits - 1) / sunits, cap));
+    n = std::min(n, std::max<int64_t>(1, 8192 / sunits));
     r.suffix = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(n, 64)));
   }
   return r;
