@@ -371,29 +371,32 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
 // merged to bf16 output and fp32 LSE.  One warp per 8 consecutive rows of a kv
 // head and 16 channels: lane l reads 4 channels (l / 8) of row l % 8, so that
 // eight lanes take a whole 128-byte line of a segment, and every segment's load
-// is in flight at once (8 a batch).  Bound by its reads (D + 2 floats a row and
+// is in flight at once (8 a batch); where there are more warps than fit at once, a
+// warp takes several channel blocks in turn.  Bound by its reads (D + 2 floats a row and
 // segment, L2 hits); with 32-byte pieces, two rows of all channels a warp, it
 // took 15 us where it now takes 5 (64 requests, 21 segments).  Launched beside
 // the last kernel: it looks up its rows' sequences and then waits.
 template <int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ SharedArgs s) {
-  constexpr int kCb = D / 16;  // channel blocks of a row
+__global__ void __launch_bounds__(256, 3)
+    shared_join_kernel(const __grid_constant__ SharedArgs s, int cpw_log2) {
+  constexpr int kCbLog2 = D == 64 ? 2 : D == 128 ? 3 : 4;  // D / 16 channel blocks of a row
   const AttnArgs &a = s.a;
-  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
+  const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1};
   const int lane = threadIdx.x & 31;
-  const int64_t rows = rows_total(s);
-  const int64_t groups = (rows + 7) / 8;
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (gw >= groups * a.hk * kCb) return;
-  const int cb = static_cast<int>(gw % kCb);
-  const int h = static_cast<int>(gw / kCb / groups);
-  const int64_t row = gw / kCb % groups * 8 + (lane & 7);
+  // rows fit 32 bits: their output alone takes 128 bytes a row
+  const uint32_t rows = static_cast<uint32_t>(rows_total(s));
+  const uint32_t gw = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int slices_log2 = kCbLog2 - cpw_log2;
+  if ((gw >> slices_log2) >= (rows + 7) / 8) return;
+  const int cb0 = static_cast<int>(gw & ((1u << slices_log2) - 1u)) << cpw_log2;
+  const int h = static_cast<int>(blockIdx.y);
+  const uint32_t row = (gw >> slices_log2) * 8 + (lane & 7);
   const int piece = lane >> 3;  // 4 channels of the 16; segments piece + 4 j of a round
 
   // this lane's row: its token, q head, and how many segments hold its keys
   int n_p = 0, n_s = 0;
-  const int tok = static_cast<int>(row / a.qpk);
-  const int hh = h * a.qpk + static_cast<int>(row % a.qpk);
+  const int tok = static_cast<int>(row / static_cast<uint32_t>(a.qpk));
+  const int hh = h * a.qpk + static_cast<int>(row % static_cast<uint32_t>(a.qpk));
   if (row < rows) {
     // a batch of single tokens: sequence = token; a search otherwise
     int seq = tok < a.num_seqs ? tok : a.num_seqs - 1;
@@ -420,67 +423,71 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   // segment k of the row: its slot (the prefix's first, unused ones skipped)
   auto slot = [&](int k) { return k < n_p ? k : s.ns_p + k - n_p; };
   wait_for_predecessor();  // the triples
-  float M = sink;
-  float total = sink > -INFINITY && piece == 0 ? 1.0f : 0.0f;  // this lane's share, scaled to M
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const int64_t at = (static_cast<int64_t>(cb * 4 + piece) * rows + row) * 4;
-  for (int k0 = 0; k0 < n_max; k0 += 16) {
-    constexpr int kBatch = 8;
-    float4 x[kBatch];
-    auto load = [&](int k1) {
+#pragma unroll 1
+  for (int cb = cb0; cb < cb0 + (1 << cpw_log2); ++cb) {
+    float M = sink;
+    float total = sink > -INFINITY && piece == 0 ? 1.0f : 0.0f;  // this lane's share, scaled to M
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int64_t at = (static_cast<int64_t>(cb * 4 + piece) * rows + row) * 4;
+    for (int k0 = 0; k0 < n_max; k0 += 16) {
+      constexpr int kBatch = 8;
+      float4 x[kBatch];
+      auto load = [&](int k1) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        x[i] = k1 + i < n ? *reinterpret_cast<const float4 *>(acc_at<D>(s, slot(k1 + i), h) + at)
-                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    };
-    float2 ml[4];
+        for (int i = 0; i < kBatch; ++i)
+          x[i] = k1 + i < n ? *reinterpret_cast<const float4 *>(acc_at<D>(s, slot(k1 + i), h) + at)
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      };
+      float2 ml[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = k0 + piece + 4 * j;
-      ml[j] = k < n ? *reinterpret_cast<const float2 *>(a.part_ml + (ml_at(s, slot(k), h) + row) * 2)
-                    : make_float2(-INFINITY, 0.0f);
-    }
-    load(k0);
-    float m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-    m = fmaxf(M, fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)));
-    const float mu = m == -INFINITY ? 0.0f : m;
-    const float f = fast_exp2(M - mu);
-    M = m;
-    float w[4];
-    total *= f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = fast_exp2(ml[j].x - mu);
-      total = fmaf(w[j], ml[j].y, total);
-    }
-    acc.x *= f;
-    acc.y *= f;
-    acc.z *= f;
-    acc.w *= f;
-#pragma unroll
-    for (int b = 0; b < 16 / kBatch; ++b) {
-      if (k0 + b * kBatch >= n_max) break;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int k = b * kBatch + i;
-        const float wk = __shfl_sync(0xffffffffu, w[k >> 2], (k & 3) * 8 + (lane & 7));
-        acc.x = fmaf(wk, x[i].x, acc.x);
-        acc.y = fmaf(wk, x[i].y, acc.y);
-        acc.z = fmaf(wk, x[i].z, acc.z);
-        acc.w = fmaf(wk, x[i].w, acc.w);
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + piece + 4 * j;
+        ml[j] = k < n ? *reinterpret_cast<const float2 *>(a.part_ml + (ml_at(s, slot(k), h) + row) * 2)
+                      : make_float2(-INFINITY, 0.0f);
       }
-      if (b + 1 < 16 / kBatch) load(k0 + (b + 1) * kBatch);
+      load(k0);
+      float m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(M, fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)));
+      const float mu = m == -INFINITY ? 0.0f : m;
+      const float f = fast_exp2(M - mu);
+      M = m;
+      float w[4];
+      total *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = fast_exp2(ml[j].x - mu);
+        total = fmaf(w[j], ml[j].y, total);
+      }
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int b = 0; b < 16 / kBatch; ++b) {
+        if (k0 + b * kBatch >= n_max) break;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int k = b * kBatch + i;
+          const float wk = __shfl_sync(0xffffffffu, w[k >> 2], (k & 3) * 8 + (lane & 7));
+          acc.x = fmaf(wk, x[i].x, acc.x);
+          acc.y = fmaf(wk, x[i].y, acc.y);
+          acc.z = fmaf(wk, x[i].z, acc.z);
+          acc.w = fmaf(wk, x[i].w, acc.w);
+        }
+        if (b + 1 < 16 / kBatch) load(k0 + (b + 1) * kBatch);
+      }
+    }
+    total += __shfl_xor_sync(0xffffffffu, total, 8);
+    total += __shfl_xor_sync(0xffffffffu, total, 16);
+    if (n > 0) {
+      const float inv = 1.0f / total;
+      const int64_t to = static_cast<int64_t>(tok) * a.hq + hh;
+      *reinterpret_cast<uint2 *>(a.out + to * D + cb * 16 + piece * 4) =
+          make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
+      if (cb == 0 && piece == 0 && a.lse) a.lse[to] = (M + log2f(total)) * kLn2;
     }
   }
-  total += __shfl_xor_sync(0xffffffffu, total, 8);
-  total += __shfl_xor_sync(0xffffffffu, total, 16);
-  if (n == 0) return;
-  const float inv = 1.0f / total;
-  const int64_t to = static_cast<int64_t>(tok) * a.hq + hh;
-  *reinterpret_cast<uint2 *>(a.out + to * D + cb * 16 + piece * 4) =
-      make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
-  if (cb == 0 && piece == 0 && a.lse) a.lse[to] = (M + log2f(total)) * kLn2;
 }
 
 // ---------------------------------------------------------------------- host
@@ -546,12 +553,14 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
     }
   }
   {
-    // suffix: ~1024 keys a segment (the decode kernel's measured best), more only
-    // while blocks are too few to fill the GPU, four of the rows kernel to an SM, of
+    // suffix: ~1024 keys a segment (the decode kernel's measured best; 2048 where one
+    // segment each fills the GPU, 128 requests of up to 2048 keys behind 32768: 218 us
+    // against 228), more only while blocks are too few to fill the GPU, four of the rows kernel to an SM, of
     // 4 tiles at least; two of the row-tile kernel, a tile at least (2 x 40 tokens of
     // 16 rows behind 1284 keys of D = 256: 7 segments 35 us, 3 45)
     const int64_t full = few ? 608 : 304, cap = few ? (stiles + 3) / 4 : stiles + 1;
-    int64_t n = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + 1023) / 1024,
+    const int64_t keys = sunits >= full ? 2048 : 1024;
+    int64_t n = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + keys - 1) / keys,
                                   std::min((full + sunits - 1) / sunits, cap));
     n = std::min(n, std::max<int64_t>(1, 8192 / sunits));
     r.suffix = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(n, 64)));
@@ -687,14 +696,18 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
     if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, tc, stream)) != cudaSuccess) return e;
   }
   if ((e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
-  const int64_t warps = (static_cast<int64_t>(L.num_tokens) * a.qpk + 7) / 8 * L.hk * (L.d / 16);
-  const int64_t blocks = (warps + 7) / 8;
+  // channel blocks a warp takes in turn: one while all blocks are resident at once
+  // (three an SM), so that a row's look-ups are not repeated behind a first wave
+  const int64_t groups = (static_cast<int64_t>(L.num_tokens) * a.qpk + 7) / 8;
+  int cb_log2 = L.d == 64 ? 2 : L.d == 128 ? 3 : 4, cpw_log2 = 0;
+  while (cpw_log2 < cb_log2 && (groups << (cb_log2 - cpw_log2)) * L.hk > 3 * 8 * 152) ++cpw_log2;
+  const int64_t blocks = ((groups << (cb_log2 - cpw_log2)) + 7) / 8;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(L.hk));
   switch (L.d) {
-    case 64: return launch_kernel(shared_join_kernel<64>, grid, 256, 0, stream, true, s);
-    case 128: return launch_kernel(shared_join_kernel<128>, grid, 256, 0, stream, true, s);
-    case 256: return launch_kernel(shared_join_kernel<256>, grid, 256, 0, stream, true, s);
+    case 64: return launch_kernel(shared_join_kernel<64>, grid, 256, 0, stream, true, s, cpw_log2);
+    case 128: return launch_kernel(shared_join_kernel<128>, grid, 256, 0, stream, true, s, cpw_log2);
+    case 256: return launch_kernel(shared_join_kernel<256>, grid, 256, 0, stream, true, s, cpw_log2);
   }
   return cudaErrorInvalidValue;
 }

@@ -25,6 +25,8 @@
 
 namespace paq8 {
 
+constexpr float kMaxP = 32768.0f;  // bound on P, inside fp16
+
 // The G fp16 K scales of one key row (contiguous) as floats.
 template <int G>
 __device__ __forceinline__ void load_key_scales(uint32_t addr, float (&f)[G]) {
@@ -259,11 +261,16 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
   };
   const int all_end = min(kv_end, limit(0) + 1);  // the first key past those every row sees
 
-  float m_run[NT][2], l_run[NT][2];  // rows 8 nt + 2t, + 1: max (log2 units), this lane's expsum
+  // rows 8 nt + 2t, + 1: the max O and l are scaled to (log2 units), the same with 0
+  // for -inf, this lane's expsum
+  float m_run[NT][2], mu[NT][2], l_run[NT][2];
+  bool started[NT];  // both rows have a max
   float o[NT][Cfg::kCm][4];          // O^T: channels (g, g+8) x rows (2t, 2t+1)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m_run[nt][0] = m_run[nt][1] = -INFINITY;
+    mu[nt][0] = mu[nt][1] = 0.0f;
+    started[nt] = false;
     l_run[nt][0] = l_run[nt][1] = 0.0f;
 #pragma unroll
     for (int i = 0; i < Cfg::kCm; ++i)
@@ -341,41 +348,43 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
 
     // ---------------- mask the edges, online softmax over keys (rows of S^T)
     uint32_t pb[NT][2];
+    const float mul = tail ? 1.0f : a.scale_log2;  // an edge block's scores are scaled as they are masked
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx[2] = {-INFINITY, -INFINITY};
+      if (tail) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v = s[nt][e] * a.scale_log2;
-        if (tail) {
+        for (int e = 0; e < 4; ++e) {
           const int k = key0 + (e < 2 ? r0 : r1);
-          if (k < kv_begin || k > limit(8 * nt + 2 * t + (e & 1))) v = -INFINITY;
+          s[nt][e] = k < kv_begin || k > limit(8 * nt + 2 * t + (e & 1)) ? -INFINITY
+                                                                         : s[nt][e] * a.scale_log2;
         }
-        s[nt][e] = v;
-        mx[e & 1] = fmaxf(mx[e & 1], v);
       }
-      float alpha[2], mu[2];
-      bool grew = false;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
-          mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
-        const float mn = fmaxf(m_run[nt][c], mx[c]);
-        grew |= mn != m_run[nt][c];
-        mu[c] = mn == -INFINITY ? 0.0f : mn;
-        alpha[c] = fast_exp2(m_run[nt][c] - mu[c]);
-        m_run[nt][c] = mn;
-      }
+      // P = 2^(s scale - m).  m is the largest score of the row's first block with a
+      // visible key; it moves, and O and l with it, only when a P would pass 2^15
+      // (inside fp16): no row maximum is taken on the common path.
       float p[4];
+      auto exps = [&]() {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = fast_exp2(s[nt][e] - mu[e & 1]);
-      pb[nt][0] = movmatrix_trans(pack_half2(p[0], p[1]));  // keys 0..7 -> k 2t, 2t+1
-      pb[nt][1] = movmatrix_trans(pack_half2(p[2], p[3]));  // keys 8..15 -> k 2t+8, 2t+9
-      // rescale only when some row's running max moved (alpha == 1 otherwise)
-      if (__any_sync(0xffffffffu, grew)) {
-        l_run[nt][0] *= alpha[0];
-        l_run[nt][1] *= alpha[1];
+        for (int e = 0; e < 4; ++e) p[e] = fast_exp2(fmaf(s[nt][e], mul, -mu[nt][e & 1]));
+      };
+      exps();
+      const bool fits = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) <= kMaxP;
+      if (!__all_sync(0xffffffffu, fits && started[nt])) {
+        float mx[2], alpha[2];
+        started[nt] = true;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mx[c] = fmaxf(s[nt][c] * mul, s[nt][2 + c] * mul);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
+          const float mn = fmaxf(m_run[nt][c], mx[c]);
+          started[nt] &= mn > -INFINITY;
+          mu[nt][c] = mn == -INFINITY ? 0.0f : mn;
+          alpha[c] = fast_exp2(m_run[nt][c] - mu[nt][c]);
+          m_run[nt][c] = mn;
+          l_run[nt][c] *= alpha[c];
+        }
 #pragma unroll
         for (int i = 0; i < Cfg::kCm; ++i) {
           o[nt][i][0] *= alpha[0];
@@ -383,7 +392,10 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
           o[nt][i][2] *= alpha[0];
           o[nt][i][3] *= alpha[1];
         }
+        exps();
       }
+      pb[nt][0] = movmatrix_trans(pack_half2(p[0], p[1]));  // keys 0..7 -> k 2t, 2t+1
+      pb[nt][1] = movmatrix_trans(pack_half2(p[2], p[3]));  // keys 8..15 -> k 2t+8, 2t+9
       l_run[nt][0] += p[0] + p[2];
       l_run[nt][1] += p[1] + p[3];
     }
