@@ -513,16 +513,16 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   const int64_t stiles = (static_cast<int64_t>(max_suffix_len) + kTile - 1) / kTile;
   {
     // prefix: the count of segments that ends soonest, in units of a tile's time,
-    // of a model fitted to 47 batches x 20 counts each (all D, both formats, 1 - 128
-    // sequences, 1 - 5 groups): on average it is 3.3 % above the best count's time
-    // (2.6 % on 26 others), where whole waves of the prefix's blocks by themselves
-    // were 8.4 % above it.
-    //  - A block takes its tiles and 5 more (set-up, first loads, triples).
-    //  - The suffixes (half of the longest on average, and 4 tiles of set-up; a tile
-    //    is 0.3 of a prefix tile, 3 in the row-tile kernel) run beside it, on the SMs
-    //    that the prefix's blocks leave and a little on theirs.  So a prefix of few,
-    //    long blocks on half of the SMs beats one on all of them: 64 requests, 8192
-    //    keys, 8 segments 41 us, 19 segments 52.
+    // of a model fitted to 68 batches x 20 counts each (all D, both formats, 1 - 128
+    // sequences, 1 - 5 groups): on average it is 3.5 % above the best count's time;
+    // whole waves of the prefix's blocks by themselves were 8.4 % above it.
+    //  - A block takes its tiles and 8 more (set-up, first loads, triples; row-tile
+    //    kernel: 6).
+    //  - The suffixes (half of the longest on average, and 5 tiles of set-up; a tile
+    //    is 0.35 of a prefix tile, 3 in the row-tile kernel) run on the SMs that the
+    //    prefix's blocks leave.  So a prefix of few, long blocks on half of the SMs
+    //    beats one on all of them: 64 requests, 8192 keys, 8 segments 39 us, 19
+    //    segments 50.
     //  - Several groups: their lengths differ, and waves overlap.
     //  - The join reads a triple a segment, 16 in flight at a time.
     const bool tc = prefix_on_tc(num_tokens, num_groups, qpk, d);
@@ -532,17 +532,17 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
         std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q) * hk;
     const int64_t slots = tc || d == 256 ? 152 : 304;  // resident blocks
     const int64_t tiles = std::max(1, (max_prefix_len + kTile - 1) / kTile);
-    const double join = static_cast<double>(num_tokens) * hq * (d + 2) * 8 / 1.65e6;
+    const double join = static_cast<double>(num_tokens) * hq * (d + 2) * 8 / 2.2e6;
     const double suffix =
-        (few ? 0.3 : 3.0) * static_cast<double>(sunits) * (0.5 * static_cast<double>(stiles) + 4.0);
-    const double held = !tc ? 0.5 : d == 256 ? 1.0 : 0.9;  // share of an SM a prefix block takes
+        (few ? 0.35 : 3.0) * static_cast<double>(sunits) * (0.5 * static_cast<double>(stiles) + 5.0);
+    const double held = tc ? 1.0 : 0.5;  // share of an SM a prefix block takes
     double best = 0;
     r.prefix = 1;
     for (int n = 1; n <= 64 && n <= tiles; ++n) {
       const double blocks = static_cast<double>(units * n);
       const double waves = num_groups == 1 ? static_cast<double>((units * n + slots - 1) / slots)
                                            : std::max(1.0, 0.9 * blocks / static_cast<double>(slots));
-      const double block = static_cast<double>((tiles + n - 1) / n) + 5.0;
+      const double block = static_cast<double>((tiles + n - 1) / n) + (tc ? 8.0 : 6.0);
       const double cost =
           std::max(waves * block, (blocks * block * held + suffix) / static_cast<double>(slots)) +
           join * n + 1.5 * ((n + 15) / 16);

@@ -7,18 +7,15 @@
 //   O^T[16 ch x 8 rows] += V^T[16 ch x 16 keys] . P^T[16 keys x 8],
 // NT tiles of 8 rows (1, 2 or 4, by the bound of the query lengths) off every
 // converted key and value: the conversions, not the MMAs, are most of a block's
-// instructions.  More rows than 8 NT take several passes (D = 256).
+// instructions.  More rows than 8 NT take several passes.
 // Each row has its own causal limit, taken on edge blocks only.  HBM bound:
 // 2 (D + D / 16) bytes a key and kv head (q8), D + D / 2 + 4 (fp8 / 4-bit).
 //
 // Four warps share a segment's 16-key blocks round robin, each on its own: it
 // copies its blocks with 16-byte cp.async into a private 3-stage ring and reads
 // them back, so that no warp waits for another until the four softmax states
-// are merged at the end (one fp32 triple per row).  No producer warp, because
-// four warps of at most 128 registers fit beside a block of the tensor-core
-// kernel (its 16 warps leave 4096 registers of each SM sub-partition, one warp's;
-// a fifth warp would double up on one): the prefix, bound by the tensor core, and
-// the suffixes, bound by HBM, then share every SM from the start.
+// are merged at the end (one fp32 triple per row); four blocks of four warps and
+// 128 registers hold an SM.
 #include <type_traits>
 
 #include "attn_shared.cuh"
@@ -90,9 +87,9 @@ struct SharedRowsCfg {
   static constexpr int kSt = 3;
   static constexpr int kCm = D / 16;                    // 16-channel blocks of the output
   static constexpr int G = D / 32;
-  // blocks per SM: 128 registers a thread (one block beside the tensor-core
-  // kernel, four alone) where that costs a few spills at most
-  static constexpr int kMinBlocks = D == 256 ? 2 : (NT == 4 ? 3 : 4);
+  // blocks per SM: 128 registers a thread (four blocks) where that costs a few
+  // spills at most
+  static constexpr int kMinBlocks = D == 256 || (D == 128 && NT == 4) ? 2 : NT == 4 ? 3 : 4;
   static constexpr int kRing = kWarps * kSt * L::kBytes;
   static constexpr int kMerge = kWarps * 32 * NT * (4 + 4 * kCm) * 4;
   static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
@@ -531,7 +528,7 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
   cudaError_t e = configured.get(nullptr, [](int, int *) {
     cudaError_t r = cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8, NT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    // the tensor-core kernel's carveout, so that blocks of both are resident together
+    // all of the SM's shared memory, for four blocks
     return r != cudaSuccess ? r
                             : cudaFuncSetAttribute(shared_rows_kernel<D, BS, F8, NT>,
                                                    cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -547,16 +544,17 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
 
 template <int D, int BS>
 static cudaError_t launch_shared_rows_d(const SharedArgs &s, bool f8v4, cudaStream_t stream) {
-  // row tiles a pass: as many as the rows need and the registers hold (4 at
-  // D = 128 ran two blocks an SM and none beside the tensor-core kernel: 48
-  // requests of up to 20 rows took 67 us, two passes of 2 tiles 56)
+  // row tiles a pass: as many as the rows need and the registers hold.  At D = 128
+  // 4 tiles leave two blocks an SM: 48 requests of up to 32 rows and 2000 keys take
+  // 82 us (fp8 / 4-bit) and 90 (q8), two passes of 2 tiles 101 and 116; of up to 24
+  // rows and 700 keys, where the fourth tile stays empty, 68 and 76 against 60 and 66.
   if (s.few_rows <= 8)
     return f8v4 ? launch_shared_rows_t<D, BS, true, 1>(s, stream)
                 : launch_shared_rows_t<D, BS, false, 1>(s, stream);
-  if (s.few_rows <= 16 || D != 64)
+  if (s.few_rows <= 16 || D == 256 || (D == 128 && s.few_rows <= 24))
     return f8v4 ? launch_shared_rows_t<D, BS, true, 2>(s, stream)
                 : launch_shared_rows_t<D, BS, false, 2>(s, stream);
-  if constexpr (D == 64)
+  if constexpr (D != 256)
     return f8v4 ? launch_shared_rows_t<D, BS, true, 4>(s, stream)
                 : launch_shared_rows_t<D, BS, false, 4>(s, stream);
   return cudaErrorInvalidValue;

@@ -25,6 +25,13 @@
 
 namespace paq8 {
 
+// Every block asks for all of an SM's shared memory, so that no block of the rows
+// kernel comes beside it: with one a tile took 2700 cycles (fp8 / 4-bit, 16 rows:
+// 4500), alone it takes 2000, and the rows run better on the SMs that a prefix cut
+// into fewer segments leaves (4 groups of 96 requests: 42 us against 47; draft
+// batches 58 against 62; 128 requests on 32768 keys 200 against 210).
+constexpr int kSmemOfSm = 232448;
+
 template <int D, int BS, bool F8>
 struct SharedTcCfg {
   static constexpr int kTile = 64;
@@ -47,7 +54,7 @@ struct SharedTcCfg {
   static constexpr uint32_t kOCol = 128;
   static constexpr float kMaxTileSum = 32768.0f;  // bound on a tile's P sum (so on every P)
   static_assert(D == 64 || D == 128, "the tcgen05 kernel handles D = 64, 128");
-  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSmem <= kSmemOfSm, "shared memory");
   static_assert(kKSlot + 2 * kVBytes >= kRows * 2 * D, "q rows in K slot 1 and the V slots");
   static_assert(kSt <= 4, "staging barriers");
 };
@@ -68,8 +75,7 @@ enum : int {
 };
 
 template <int D, int BS, bool F8>
-// at most 96 registers, so that a block of the rows kernel fits beside it
-__global__ void __maxnreg__(96)
+__global__ void __launch_bounds__(512, 1)
     shared_tc_kernel(const __grid_constant__ SharedArgs sa, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v) {
   using C = SharedTcCfg<D, BS, F8>;
@@ -536,19 +542,15 @@ static cudaError_t launch_shared_tc_t(const SharedArgs &s, const CUtensorMap &tk
   using C = SharedTcCfg<D, BS, F8>;
   static DeviceOnce configured;
   cudaError_t e = configured.get(nullptr, [](int, int *) {
-    cudaError_t r = cudaFuncSetAttribute(shared_tc_kernel<D, BS, F8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    // all of the SM's shared memory, so that a block of the rows kernel fits beside
-    return r != cudaSuccess ? r
-                            : cudaFuncSetAttribute(shared_tc_kernel<D, BS, F8>,
-                                                   cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    return cudaFuncSetAttribute(shared_tc_kernel<D, BS, F8>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOfSm);
   });
   if (e != cudaSuccess) return e;
   const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p * s.a.hk;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(gx));
-  return launch_kernel(shared_tc_kernel<D, BS, F8>, grid, C::kWarps * 32, C::kSmem, stream, false, s, tk,
-                       tv);
+  return launch_kernel(shared_tc_kernel<D, BS, F8>, grid, C::kWarps * 32, kSmemOfSm, stream, false, s,
+                       tk, tv);
 }
 
 // Rows of one block, 0 where the kernel does not take the head size.
