@@ -453,7 +453,7 @@ pa_status copy_blocks(paq8::BlockCopy &p, const int32_t *copy_pairs, int32_t num
     p.bytes[i] = row_bytes[i] * num_kv_heads;
     bytes += p.bytes[i];
   }
-  // a thread block takes 16 KB of one pair
+  // 2^31 pieces of 16 KB are more than any list of pairs of one cache can mean
   if ((bytes / 16384 + 1) * num_pairs >= (int64_t{1} << 31))
     return fail(PA_ERR_UNSUPPORTED, "too many bytes in one call: split the pairs");
   p.status = status;
