@@ -393,56 +393,82 @@ __global__ void __launch_bounds__(256, 3)
   const uint32_t row = (gw >> slices_log2) * 8 + (lane & 7);
   const int piece = lane >> 3;  // 4 channels of the 16; segments piece + 4 j of a round
 
-  // this lane's row: its token, q head, and how many segments hold its keys
+  // this lane's row: its token, q head, and how many segments hold its keys.  Few
+  // groups are read by a lane each, beside the row's own entries: the blocks that
+  // come last start when the kernel before has ended, and wait for each round.
+  const bool few = s.num_groups < 32;
+  int first = 0x7fffffff, len = 0;
+  if (few && lane <= s.num_groups) {
+    first = s.cu_groups[lane];
+    if (lane < s.num_groups) len = s.prefix_lens[lane];
+  }
   int n_p = 0, n_s = 0;
-  const int tok = static_cast<int>(row / static_cast<uint32_t>(a.qpk));
+  const int tok = static_cast<int>(min(row, rows - 1) / static_cast<uint32_t>(a.qpk));
   const int hh = h * a.qpk + static_cast<int>(row % static_cast<uint32_t>(a.qpk));
-  if (row < rows) {
-    // a batch of single tokens: sequence = token; a search otherwise
-    int seq = tok < a.num_seqs ? tok : a.num_seqs - 1;
-    if (a.cu_seqlens_q[seq] > tok || a.cu_seqlens_q[seq + 1] <= tok)
-      seq = last_at_most(a.cu_seqlens_q, a.num_seqs, tok);
-    const int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1];
-    const int g = last_at_most(s.cu_groups, s.num_groups, seq);
-    if (c0 >= 0 && tok >= c0 && tok < c1 && c1 <= a.num_tokens &&  // else: a row no sequence owns
-        s.cu_groups[g] <= seq && s.cu_groups[g + 1] > seq && rows_of(s, c1 - c0) <= s.max_rows) {
-      const int P = s.prefix_lens[g];
-      const int ctx = a.seq_lens[seq] - (c1 - c0);
-      const int g0 = group_token(s, g), g1 = group_token(s, g + 1);
-      // else: flagged by the suffix item, or its prefix was not taken
-      if (P >= 0 && ctx >= P && g0 >= 0 && g0 <= tok && tok < g1 && g1 <= a.num_tokens) {
-        n_p = shared_segments(0, P, s.seg_p, s.ns_p);
-        n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
-      }
+  // a batch of single tokens: sequence = token; a search otherwise
+  int seq = min(tok, a.num_seqs - 1);
+  int c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1], seq_len = a.seq_lens[seq];
+  const int token = few && first >= 0 && first <= a.num_seqs ? a.cu_seqlens_q[first] : 0x7fffffff;
+  if (c0 > tok || c1 <= tok) {
+    seq = last_at_most(a.cu_seqlens_q, a.num_seqs, tok);
+    c0 = a.cu_seqlens_q[seq], c1 = a.cu_seqlens_q[seq + 1], seq_len = a.seq_lens[seq];
+  }
+  // the row's group: its first sequence, that of the next, its prefix, its tokens
+  int s0, s1, P, g0, g1;
+  if (few) {
+    int g = 0;
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+      const int v = __shfl_sync(0xffffffffu, first, (g + step) & 31);
+      if (g + step < s.num_groups && v <= seq) g += step;
     }
+    s0 = __shfl_sync(0xffffffffu, first, g), s1 = __shfl_sync(0xffffffffu, first, g + 1);
+    P = __shfl_sync(0xffffffffu, len, g);
+    g0 = __shfl_sync(0xffffffffu, token, g), g1 = __shfl_sync(0xffffffffu, token, g + 1);
+  } else {
+    const int g = last_at_most(s.cu_groups, s.num_groups, seq);
+    s0 = s.cu_groups[g], s1 = s.cu_groups[g + 1], P = s.prefix_lens[g];
+    g0 = group_token(s, g), g1 = group_token(s, g + 1);
+  }
+  const int ctx = seq_len - (c1 - c0);
+  // else: a row no sequence owns, one flagged by its suffix item, or one whose
+  // prefix was not taken
+  if (row < rows && c0 >= 0 && tok >= c0 && tok < c1 && c1 <= a.num_tokens && s0 <= seq && s1 > seq &&
+      rows_of(s, c1 - c0) <= s.max_rows && P >= 0 && ctx >= P && g0 >= 0 && g0 <= tok && tok < g1 &&
+      g1 <= a.num_tokens) {
+    n_p = shared_segments(0, P, s.seg_p, s.ns_p);
+    n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
   }
   const int n = n_s > 0 ? n_p + n_s : 0;  // 0: a row that is not written
   const int n_max = __reduce_max_sync(0xffffffffu, n);
   if (n_max == 0) return;
   const float sink = a.sinks && n > 0 ? sink_log2(a, hh) : -INFINITY;
-  // segment k of the row: its slot (the prefix's first, unused ones skipped)
-  auto slot = [&](int k) { return k < n_p ? k : s.ns_p + k - n_p; };
+  // segment k of the row: its slot k, past the prefix's the unused ones skipped
+  const int64_t per_slot = static_cast<int64_t>(a.hk) * rows;  // (m, l) pairs; D floats of acc each
+  const int64_t skip = (s.ns_p - n_p) * per_slot;
+  const float *ml_row = a.part_ml + (ml_at(s, 0, h) + row) * 2;
   wait_for_predecessor();  // the triples
 #pragma unroll 1
   for (int cb = cb0; cb < cb0 + (1 << cpw_log2); ++cb) {
     float M = sink;
     float total = sink > -INFINITY && piece == 0 ? 1.0f : 0.0f;  // this lane's share, scaled to M
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int64_t at = (static_cast<int64_t>(cb * 4 + piece) * rows + row) * 4;
+    const float *acc_row = acc_at<D>(s, 0, h) + (static_cast<int64_t>(cb * 4 + piece) * rows + row) * 4;
     for (int k0 = 0; k0 < n_max; k0 += 16) {
       constexpr int kBatch = 8;
       float4 x[kBatch];
       auto load = [&](int k1) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-          x[i] = k1 + i < n ? *reinterpret_cast<const float4 *>(acc_at<D>(s, slot(k1 + i), h) + at)
+          x[i] = k1 + i < n ? *reinterpret_cast<const float4 *>(acc_row + (k1 + i) * (per_slot * D) +
+                                                                (k1 + i < n_p ? 0 : skip * D))
                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       };
       float2 ml[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = k0 + piece + 4 * j;
-        ml[j] = k < n ? *reinterpret_cast<const float2 *>(a.part_ml + (ml_at(s, slot(k), h) + row) * 2)
+        ml[j] = k < n ? *reinterpret_cast<const float2 *>(ml_row + (k * per_slot + (k < n_p ? 0 : skip)) * 2)
                       : make_float2(-INFINITY, 0.0f);
       }
       load(k0);

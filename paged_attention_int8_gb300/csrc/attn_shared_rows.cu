@@ -172,8 +172,11 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
 
   launch_dependents();
   const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1};
-  const int q_start = a.cu_seqlens_q[seq];
-  const int q_len = a.cu_seqlens_q[seq + 1] - q_start;
+  // one round of loads before any of them is looked at
+  const int q_start = a.cu_seqlens_q[seq], q_end = a.cu_seqlens_q[seq + 1];
+  const int seq_len = a.seq_lens[seq];
+  const int P = prefix_of(sa, seq, lane);
+  const int q_len = q_end - q_start;
   const int all_rows = rows_of(sa, q_len);
   if (q_len <= 0) return;
   if (all_rows > sa.few_rows) {  // shared_mma_kernel's, where it runs
@@ -181,9 +184,7 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
       flag_status(a.status, PA_DEV_BAD_SEQ);  // max_query_len was below a q_len
     return;
   }
-  const int seq_len = a.seq_lens[seq];
   const int ctx = seq_len - q_len;
-  const int P = prefix_of(sa, seq, lane);
   if (q_start < 0 || q_start + q_len > a.num_tokens || P < 0 || ctx < P) {
     if (threadIdx.x == 0 && sigma == 0 && row0 == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
     return;
