@@ -7,6 +7,7 @@ is no fallback: if the library is missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import enum
 import os
@@ -519,6 +520,17 @@ def _call(fn, dev, stream, *args):
         _raise_if(st)
 
 
+def _allocating(stream):
+    """Context in which a call's omitted results and workspace are allocated: on
+    the stream that it runs on, so that neither their first bytes nor their
+    reuse after the last reference is gone are out of its order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _refuse(dev, dtypes, **tensors):
     """Raise for the tensors (None passes) that a quick check turned down: each
     must be a contiguous tensor of one of `dtypes` on device number `dev`."""
@@ -573,9 +585,10 @@ def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_
     if out is None:
         device = context_lens.device
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
-        out = (torch.full((s, columns), -1, dtype=_I32, device=device), new(s + 1, _I32),
-               new(s, _I32), new(num_tokens, torch.int64), new(num_tokens, torch.int64),
-               new((s, 2), _I32), new(1, _I32))
+        with _allocating(stream):
+            out = (torch.full((s, columns), -1, dtype=_I32, device=device), new(s + 1, _I32),
+                   new(s, _I32), new(num_tokens, torch.int64), new(num_tokens, torch.int64),
+                   new((s, 2), _I32), new(1, _I32))
     if type(out) is not BlockTables:
         out = BlockTables._make(out)
     table, cu, lens, slots, pos, pairs, nxt = out
@@ -720,7 +733,8 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
         if sinks.numel() != hq:
             raise ValueError("sinks must be [num_q_heads]")
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating(stream):
+            out = torch.empty_like(q)
     else:
         if out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
             _refuse(dev, (_BF16,), out=out)
@@ -728,7 +742,8 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
             raise ValueError("out must be shaped like q")
     if lse is None:
         if return_lse:
-            lse = torch.empty((t, hq), dtype=_F32, device=q.device)
+            with _allocating(stream):
+                lse = torch.empty((t, hq), dtype=_F32, device=q.device)
     else:
         if lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
             _refuse(dev, (_F32,), lse=lse)
@@ -737,8 +752,9 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
     if workspace is None:
         need = load().pa_shared_prefix_workspace_size(s, t, g, hq, hk, d, max_query_len,
                                                       max_prefix_len, max_suffix_len)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        workspace[:4].zero_()
+        with _allocating(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace[:4].zero_()
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
     a, b, c, e = cache

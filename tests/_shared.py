@@ -165,8 +165,8 @@ def reference(b, scale=None):
                     w = torch.exp(x - z)
                     out[t, h], lse[t, h] = w @ vv, z
                     A[t, h] = w @ vv.abs()
-                    B[t, h] = (kk.abs() @ q[t, h].abs()).max() * scale
-                    Q[t, h] = q[t, h].abs().sum() * scale
+                    B[t, h] = (kk.abs() @ q[t, h].abs()).max() * abs(scale)
+                    Q[t, h] = q[t, h].abs().sum() * abs(scale)
                     N[t, h], V[t, h] = n, vv.abs().max()
                 t += 1
     return out, lse, A, B, Q, N, V

@@ -1,0 +1,179 @@
+"""The serving calls where an index, an order or a stream could go wrong: offsets
+past 32 bits, work that wraps around the grid, graphs, streams, odd scales."""
+import pytest
+import torch
+
+from paged_attention_int8_gb300 import _lib, inputs
+from tests import _harness as H
+from tests import _shared as S
+
+pytestmark = pytest.mark.gpu
+
+
+# rows of 9 - 16, 17 - 24 and 25 - 32 a sequence, several segments, scores that grow
+# along the keys (the running offset moves) and that shrink
+@pytest.mark.parametrize("fmt", ["q8", "f8v4"])
+@pytest.mark.parametrize("hq,hk,d,bs,q_len", [(8, 1, 128, 16, 2), (8, 1, 128, 32, 3), (8, 1, 128, 16, 4),
+                                              (8, 1, 128, 32, 4), (16, 2, 64, 16, 4), (8, 1, 256, 16, 4),
+                                              (5, 1, 128, 16, 6), (16, 1, 64, 32, 2)])
+@pytest.mark.parametrize("q_scale", [1.0, 10.0])
+def test_row_tiles(cuda_device, fmt, hq, hk, d, bs, q_len, q_scale):
+    b = S.make(hq + q_len, cuda_device, fmt, hq, hk, d, bs,
+               [(70, [(q_len, 900), (1, 1), (q_len - 1, 333)]), (9, [(q_len, q_len)])],
+               q_scale=q_scale, k_bias=2.0)
+    S.check(b, *b.call())
+
+
+@pytest.mark.parametrize("n_groups", [30, 31, 32, 33])
+def test_groups_about_a_warp(cuda_device, n_groups):
+    groups = [(11 * i % 97, [(1, 1 + i % 70)] * (1 + i % 3)) for i in range(n_groups)]
+    b = S.make(n_groups, cuda_device, "q8", 4, 1, 64, 16, groups)
+    S.check(b, *b.call())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.0, -0.07])
+def test_scales_of_zero_and_below(cuda_device, d, scale):
+    """Masked keys stay masked under a scale that is not positive."""
+    b = S.make(d, cuda_device, "q8", 8, 2, d, 16, [(75, [(1, 1), (1, 70), (3, 9), (20, 31)]),
+                                                  (40, [(1, 5)] * 20)])
+    S.check(b, *b.call(softmax_scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8v4"])
+def test_pages_past_four_gigabytes(cuda_device, fmt):
+    """Pages at the end of a cache whose K alone takes more than 2^32 bytes."""
+    hk, d, bs = 2, 128, 16
+    b = S.make(3, cuda_device, fmt, 16, hk, d, bs, [(100, [(1, 40)] * 9), (30, [(2, 9)])])
+    ref = S.reference(b)
+    blocks = (1 << 20) + (1 << 17)
+    shapes = (inputs.cache_shapes if fmt == "q8" else inputs.cache_shapes_f8v4)(blocks, hk, bs, d)
+    big = [torch.empty(s, dtype=t.dtype, device=cuda_device) for s, t in zip(shapes, b.cache)]
+    assert big[0].numel() > 1 << 32
+    first = blocks - b.blocks
+    for t, x in zip(big, b.cache):
+        t[first:] = x
+    small, b.cache = b.cache, big
+    table = b.table.clone()
+    b.table = torch.where(table >= 0, table + first, table)
+    S.check(b, *b.call(), ref=ref)
+    # the copy: from the far end to the near one and back to other far blocks
+    copy = _lib.copy_blocks if fmt == "q8" else _lib.copy_blocks_f8v4
+    pairs = torch.tensor([[first + i, i] for i in range(b.blocks)], dtype=torch.int32,
+                         device=cuda_device)
+    copy(pairs, *big)
+    far = torch.tensor([[i, first - b.blocks + i] for i in range(b.blocks)], dtype=torch.int32,
+                       device=cuda_device)
+    copy(far, *big)
+    for t, x in zip(big, small):
+        assert torch.equal(t[:b.blocks], x) and torch.equal(t[first - b.blocks:first], x)
+
+
+def _filled(blocks, hk, d, bs, device, seed):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randint(-100, 100, s, generator=g, dtype=torch.int8).to(device) if i % 2 == 0
+            else torch.randint(0, 9999, s, generator=g, dtype=torch.int16).to(device)
+            for i, s in enumerate(inputs.cache_shapes(blocks, hk, bs, d))]
+
+
+# more parts than a grid takes 32 times over; parts that end inside each array;
+# blocks of many parts; a hole in every few pairs
+@pytest.mark.parametrize("pairs,hk,d,bs", [(30000, 1, 64, 16), (9000, 2, 128, 16), (5, 64, 256, 32),
+                                           (1, 13, 256, 32), (700, 7, 64, 32)])
+def test_copies_of_all_sizes(cuda_device, pairs, hk, d, bs):
+    H.ensure_built()
+    blocks = 2 * pairs + 1
+    cache = _filled(blocks, hk, d, bs, cuda_device, pairs)
+    order = torch.randperm(blocks, generator=torch.Generator().manual_seed(5)).to(cuda_device)
+    p = torch.stack([order[:pairs], order[pairs:2 * pairs]], 1).to(torch.int32)
+    if pairs > 9:
+        p[3::7, 0] = -1
+        p[5::11, 1] = p[5::11, 0]
+    want = [t.clone() for t in cache]
+    real = (p[:, 0] >= 0) & (p[:, 0] != p[:, 1])
+    for t in want:
+        t[p[real, 1].long()] = t[p[real, 0].long()]
+    _lib.copy_blocks(p, *cache)
+    for t, w in zip(cache, want):
+        assert torch.equal(t, w)
+
+
+def test_copy_captured_and_replayed_with_other_pairs(cuda_device):
+    H.ensure_built()
+    cache = _filled(40, 2, 128, 16, cuda_device, 1)
+    pairs = torch.full((6, 2), -1, dtype=torch.int32, device=cuda_device)
+    _lib.copy_blocks(pairs, *cache)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _lib.copy_blocks(pairs, *cache)
+    for step in range(3):
+        pairs.copy_(torch.tensor([[step, 10 + step], [-1, 4], [step, 20 + step], [30, 30], [7, 35],
+                                  [8, 36 + step]]))
+        want = [t.clone() for t in cache]
+        for a, b in pairs.tolist():
+            if a >= 0:
+                for w in want:
+                    w[b] = w[a]
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, w in zip(cache, want):
+            assert torch.equal(t, w)
+
+
+@pytest.mark.parametrize("fmt,d,hq,hk,q_len", [("q8", 256, 16, 2, 1), ("f8v4", 128, 8, 1, 4),
+                                               ("q8", 64, 16, 1, 3), ("q8", 128, 4, 4, 40)])
+def test_two_graphs_that_share_a_workspace(cuda_device, fmt, d, hq, hk, q_len):
+    """Each of two captured calls, replayed in turn on one stream, leaves its own result."""
+    a = S.make(1, cuda_device, fmt, hq, hk, d, 16, [(300, [(q_len, 50 + i) for i in range(6)])])
+    b = S.make(2, cuda_device, fmt, hq, hk, d, 16, [(90, [(q_len, 41)] * 2), (5, [(q_len, 200)])])
+    ws = torch.zeros(max(_lib.shared_prefix_workspace_size(
+        len(x.seq_lens), x.q.shape[0], len(x.prefix), hq, hk, d, *x.bounds) for x in (a, b)),
+        dtype=torch.uint8, device=cuda_device)
+    fn = (_lib.paged_attention_shared_prefix if fmt == "q8"
+          else _lib.paged_attention_shared_prefix_f8v4)
+    runs = []
+    for x in (a, b):
+        out, lse = torch.empty_like(x.q), torch.empty(x.q.shape[:2], device=cuda_device)
+
+        def call(x=x, out=out, lse=lse):
+            fn(x.q, *x.cache, x.cu, x.lens, x.table, x.groups, x.prefixes, *x.bounds, out=out,
+               lse=lse, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((x, S.reference(x), graph, out, lse))
+    for x, ref, graph, out, lse in (*runs, *reversed(runs)):
+        out.fill_(float("nan")), lse.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert _lib.check_status(ws) == 0
+        S.check(x, out, lse, ref=ref)
+
+
+def test_omitted_results_belong_to_the_calls_stream(cuda_device):
+    """Results and workspace that a call allocates for another stream than the
+    current one are not handed out again before that stream has used them."""
+    b = S.make(51, cuda_device, "q8", 8, 2, 128, 16, [(400, [(1, 60)] * 20)])
+    want = b.call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    ctx, one, free = i32([5, 40]), i32([1, 1]), torch.arange(30, dtype=torch.int32, device=cuda_device)
+    source = i32([[7, -1, -1, -1], [8, 9, 10, -1]])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = _lib.paged_attention_shared_prefix(b.q, *b.cache, b.cu, b.lens, b.table, b.groups,
+                                             b.prefixes, *b.bounds, stream=side)
+    tables = _lib.build_block_tables(ctx, one, source, free, 30, 16, 2, stream=side)
+    need = _lib.shared_prefix_workspace_size(20, 20, 1, 8, 2, 128, *b.bounds)
+    for _ in range(4):  # what the current stream allocates meanwhile, overwritten
+        other = [torch.full((need,), 0xFF, dtype=torch.uint8, device=cuda_device) for _ in range(3)]
+        del other
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert tables.block_table.tolist() == [[7, -1, -1, -1], [8, 9, 10, -1]]
+    assert tables.slot_mapping.tolist() == [7 * 16 + 5, 10 * 16 + 8]
