@@ -9,14 +9,18 @@
 // half of shared memory.  So instead of two halves the pipeline alternates the
 // S buffers of one: QK(j + 1) runs while the softmax works on S(j), then PV(j).
 //   tensor core, a tile: 2 x 16 MMAs of N = 64 and 4 of N = 256, 1536 cycles;
-//   softmax, one row per thread, hidden behind QK(j + 1) and PV(j - 1).
+//   softmax, one row per thread, hidden behind QK(j + 1) and PV(j - 1);
+//   shared memory: 34 KB staged, read and turned into 96 KB of operands that the
+//   MMAs read once, 2060 cycles at 128 bytes each.
+// A tile takes 2650 cycles: bound by shared memory and the conversions.
 // Operand buffers: three 32 KB slots that hold the key parts hi(0), lo(0), hi(1),
 // ... in turn, each freed when its own MMAs are done, and one value slot; pages
-// are staged by TMA in rings of their own for keys and for values.
+// are staged by TMA in rings of their own for keys (2) and for values (3).
 // Warps: 5 and 18 producers, 1 MMA issuer; keys 0, 2, 3, 6, 14 - 17; values 4, 7, 12, 13;
 // softmax 8 - 11 (one per TMEM lane quarter).  fp8 / 4-bit: keys are exact in one
-// part.  Eight key warps in one pass over both parts: four warps, a pass a part,
-// took 3100 cycles a tile and set the pace.
+// part.  What a converter can do before its slot is free it does (the keys' codes
+// and half of the values in registers): waiting first took 3200 cycles a tile, with
+// four key warps 4300.
 #include <type_traits>
 
 #include "attn_shared.cuh"
@@ -31,7 +35,7 @@ constexpr int kD = 256;
 template <int BS, bool F8>
 struct Tc256Cfg {
   static constexpr int kTile = 64;
-  static constexpr int kStK = 3, kStV = 2;  // staging stages of the rings
+  static constexpr int kStK = 2, kStV = 3;  // staging stages of the rings
   static constexpr int kWarps = 19;
   static constexpr int kKWarps = 8;
   static constexpr int kParts = F8 ? 1 : 2;  // key parts: hi, lo
@@ -57,10 +61,10 @@ struct Tc256Cfg {
 
 // barriers (8 bytes each, from kBarOff)
 enum : int {
-  kStKFull = 0,    // [3] producer -> K dequant (tx bytes)
-  kStKEmpty = 3,   // [3] K dequant -> producer (8 warps)
-  kStVFull = 6,    // [2] producer -> V dequant
-  kStVEmpty = 8,   // [2] V dequant -> producer (4 warps)
+  kStKFull = 0,    // [2] producer -> K dequant (tx bytes)
+  kStKEmpty = 2,   // [2] K dequant -> producer (8 warps)
+  kStVFull = 4,    // [3] producer -> V dequant
+  kStVEmpty = 7,   // [3] V dequant -> producer (4 warps)
   kPartFull = 10,  // [3] K dequant -> MMA (8 warps)
   kPartEmpty = 13, // [3] commit after the part's MMAs -> K dequant
   kVFull = 16,     // V dequant -> MMA (4 warps)
@@ -112,17 +116,21 @@ __global__ void __maxnreg__(96)
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const uint32_t tmem_slot = bars + 8 * kBars;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kStVFull + i), 1);
-      mbar_init(bar(kStVEmpty + i), 4);
-      mbar_init(bar(kSFull + i), 1);
-      mbar_init(bar(kPFull + i), 4);
-    }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < C::kStK; ++i) {
       mbar_init(bar(kStKFull + i), 1);
       mbar_init(bar(kStKEmpty + i), C::kKWarps);
+    }
+    for (int i = 0; i < C::kStV; ++i) {
+      mbar_init(bar(kStVFull + i), 1);
+      mbar_init(bar(kStVEmpty + i), 4);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(bar(kPartFull + i), C::kKWarps);
       mbar_init(bar(kPartEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kPFull + i), 4);
     }
     mbar_init(bar(kVFull), 4);
     mbar_init(bar(kPvDone), 1);
@@ -274,98 +282,88 @@ __global__ void __maxnreg__(96)
     ok = __all_sync(0xffffffffu, ok);
   } else if (warp == 0 || warp == 2 || warp == 3 || warp == 6 || (warp >= 14 && warp < 18)) {
     // ============================================================ K dequant
-    // thread = one key row, 64 channels (two scale groups), both parts in one pass:
-    // the slots of tile j are free once the hi MMAs of tile j - 1 are done
+    // thread = one key row, 64 channels (two scale groups).  The codes are held in
+    // registers: the hi part goes into a slot while the tensor core still reads both
+    // parts of the tile before, the lo part into the next slot that it lets go.
     const int t = (warp >= 14 ? warp - 10 : warp == 6 ? 3 : warp == 0 ? 0 : warp - 1) * 32 + lane;
     const int r = t & 63;
     const int c0 = (t >> 6) * 64;
     uint32_t slot = 0, phase = 1;  // of the next part: the first round's slots are free
-    auto step = [&]() {
-      if (++slot == 3) {
-        slot = 0;
-        phase ^= 1;
-      }
-    };
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int kb = j % C::kStK;
       if (j == 1 && !mbar_wait(bar(kQFull), 0)) { ok = false; break; }  // q is out of slot 2
-      uint32_t part[2];
-      part[0] = slot;
-      if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
-      step();
-      if constexpr (!F8) {
-        part[1] = slot;
-        if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
-        step();
-      }
       if (!mbar_wait(bar(kStKFull + kb), (j / C::kStK) & 1)) { ok = false; break; }
       const uint32_t st = smem_base + C::kStKOff + kb * C::kKStage;
-      const uint32_t hi_dst = smem_base + C::kPartOff + part[0] * C::kPartBytes;
-      const uint32_t lo_dst = F8 ? 0u : smem_base + C::kPartOff + part[F8 ? 0 : 1] * C::kPartBytes;
       // keys at and past the prefix's end may hold stale bytes: converted as zeros
       const bool dead = (t0 + j) * C::kTile + r >= kv_end;
       const uint32_t scales = F8 || dead ? 0u : lds32(st + C::kTile * D + (r * G + c0 / 32) * 2);
+      uint4 codes[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 16 * i;
-        const uint4 codes = lds128(st + L::k_off(r, c));
-        const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-        uint32_t hw[8], lw[8];
-        if constexpr (F8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            hw[2 * k] = dead ? 0u : e4m3x2_to_half2(cw[k]);
-            hw[2 * k + 1] = dead ? 0u : e4m3x2_to_half2(cw[k] >> 16);
-          }
-        } else {
-          const uint32_t s2 = __byte_perm(scales, 0u, i < 2 ? 0x1010 : 0x3232);
-          const uint32_t ns2 = s2 ^ 0x80008000u;  // -scale
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t lo, hi;
-            codes4_to_half2(cw[k], lo, hi);
-            // hi part fp16(code * s); second part code * (-s) + hi = -lo, exact
-            hw[2 * k] = hmul2_u32(lo, s2);
-            hw[2 * k + 1] = hmul2_u32(hi, s2);
-            lw[2 * k] = hfma2_u32(lo, ns2, hw[2 * k]);
-            lw[2 * k + 1] = hfma2_u32(hi, ns2, hw[2 * k + 1]);
-          }
-        }
-        const uint32_t o0 = tc::sw128_chunk(r, c / 8, 64), o1 = tc::sw128_chunk(r, c / 8 + 1, 64);
-        sts128(hi_dst + o0, make_uint4(hw[0], hw[1], hw[2], hw[3]));
-        sts128(hi_dst + o1, make_uint4(hw[4], hw[5], hw[6], hw[7]));
-        if constexpr (!F8) {
-          sts128(lo_dst + o0, make_uint4(lw[0], lw[1], lw[2], lw[3]));
-          sts128(lo_dst + o1, make_uint4(lw[4], lw[5], lw[6], lw[7]));
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (int i = 0; i < 4; ++i) codes[i] = lds128(st + L::k_off(r, c0 + 16 * i));
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(kPartFull + part[0]));
-        if constexpr (!F8) mbar_arrive(bar(kPartFull + part[1]));
-        mbar_arrive(bar(kStKEmpty + kb));
+      if (lane == 0) mbar_arrive(bar(kStKEmpty + kb));
+#pragma unroll 1
+      for (int part = 0; part < C::kParts; ++part) {
+        if (!mbar_wait(bar(kPartEmpty + slot), phase)) { ok = false; break; }
+        const uint32_t dst = smem_base + C::kPartOff + slot * C::kPartBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + 16 * i;
+          const uint32_t cw[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+          uint32_t o[8];
+          if constexpr (F8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = dead ? 0u : e4m3x2_to_half2(cw[k]);
+              o[2 * k + 1] = dead ? 0u : e4m3x2_to_half2(cw[k] >> 16);
+            }
+          } else {
+            const uint32_t s2 = __byte_perm(scales, 0u, i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t lo, hi;
+              codes4_to_half2(cw[k], lo, hi);
+              // hi part fp16(code * s); second part code * (-s) + hi = -lo, exact
+              o[2 * k] = hmul2_u32(lo, s2);
+              o[2 * k + 1] = hmul2_u32(hi, s2);
+              if (part) {
+                o[2 * k] = hfma2_u32(lo, s2 ^ 0x80008000u, o[2 * k]);
+                o[2 * k + 1] = hfma2_u32(hi, s2 ^ 0x80008000u, o[2 * k + 1]);
+              }
+            }
+          }
+          sts128(dst + tc::sw128_chunk(r, c / 8, 64), make_uint4(o[0], o[1], o[2], o[3]));
+          sts128(dst + tc::sw128_chunk(r, c / 8 + 1, 64), make_uint4(o[4], o[5], o[6], o[7]));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPartFull + slot));
+        if (++slot == 3) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
+      if (!ok) break;
     }
   } else if (warp == 4 || warp == 7 || warp == 12 || warp == 13) {
     // ============================================================ V dequant
-    // thread = two channel rows of one scale group, all 64 keys
+    // thread = two channel rows of one scale group, all 64 keys.  The slot is single:
+    // the first 32 keys are converted while the tensor core still reads the values of
+    // the tile before, and wait in registers.
     const int t = (warp == 4 ? 0 : warp == 7 ? 1 : warp - 10) * 32 + lane;
     const int ch[2] = {(t >> 4) * 32 + (t & 15), (t >> 4) * 32 + (t & 15) + 16};
     const int g = t >> 4;
+    const uint32_t vrow = smem_base + C::kVOff;
+    int sb = 0, st_phase = 0;
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
-      const int sb = j & 1;
-      if (!mbar_wait(bar(kStVFull + sb), (j >> 1) & 1)) { ok = false; break; }
-      // the slot is free once q is in TMEM, then with each PV
-      if (!mbar_wait(bar(j >= 1 ? kPvDone : kQFull), j >= 1 ? (j - 1) & 1 : 0)) { ok = false; break; }
+      if (!mbar_wait(bar(kStVFull + sb), st_phase)) { ok = false; break; }
       const uint32_t st = smem_base + C::kStVOff + sb * C::kVStage;
-      const uint32_t vrow = smem_base + C::kVOff;
       const int key0 = (t0 + j) * C::kTile;
       const bool tail = key0 + C::kTile > kv_end;
-#pragma unroll 2
-      for (int key = 0; key < C::kTile; key += 16) {
+      // 16 keys from `key` on of both rows, as fp16 pairs
+      auto convert = [&](int key, uint32_t (&o)[2][8]) {
         uint32_t sc[8], zr[8];
         {
           // the 16 keys' scales (of this channel group; fp8 / 4-bit: of the key)
@@ -391,7 +389,6 @@ __global__ void __maxnreg__(96)
         }
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
-          uint32_t o[8];
           if constexpr (F8) {
             const uint2 nb = lds64(st + (key / BS) * (D * BS / 2) + ch[rr] * (BS / 2) + (key % BS) / 2);
             const uint32_t nw[4] = {nb.x, nb.x >> 16, nb.y, nb.y >> 16};
@@ -399,8 +396,8 @@ __global__ void __maxnreg__(96)
             for (int i = 0; i < 4; ++i) {
               uint32_t lo, hi;
               nibbles4_to_half2(nw[i], lo, hi);
-              o[2 * i] = hfma2_u32(lo, sc[2 * i], zr[2 * i]);
-              o[2 * i + 1] = hfma2_u32(hi, sc[2 * i + 1], zr[2 * i + 1]);
+              o[rr][2 * i] = hfma2_u32(lo, sc[2 * i], zr[2 * i]);
+              o[rr][2 * i + 1] = hfma2_u32(hi, sc[2 * i + 1], zr[2 * i + 1]);
             }
           } else {
             const uint4 codes = lds128(st + L::v_off(ch[rr], key) - L::kVOff);
@@ -409,19 +406,42 @@ __global__ void __maxnreg__(96)
             for (int i = 0; i < 4; ++i) {
               uint32_t lo, hi;
               codes4_to_half2(cw[i], lo, hi);
-              o[2 * i] = hmul2_u32(lo, sc[2 * i]);
-              o[2 * i + 1] = hmul2_u32(hi, sc[2 * i + 1]);
+              o[rr][2 * i] = hmul2_u32(lo, sc[2 * i]);
+              o[rr][2 * i + 1] = hmul2_u32(hi, sc[2 * i + 1]);
             }
           }
-          sts128(vrow + tc::sw128_chunk(ch[rr], key / 8, D), make_uint4(o[0], o[1], o[2], o[3]));
-          sts128(vrow + tc::sw128_chunk(ch[rr], key / 8 + 1, D), make_uint4(o[4], o[5], o[6], o[7]));
         }
+      };
+      auto put = [&](int key, const uint32_t (&o)[2][8]) {
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+          sts128(vrow + tc::sw128_chunk(ch[rr], key / 8, D), make_uint4(o[rr][0], o[rr][1], o[rr][2], o[rr][3]));
+          sts128(vrow + tc::sw128_chunk(ch[rr], key / 8 + 1, D),
+                 make_uint4(o[rr][4], o[rr][5], o[rr][6], o[rr][7]));
+        }
+      };
+      uint32_t early[2][2][8];
+      convert(0, early[0]);
+      convert(16, early[1]);
+      // the slot is free once q is in TMEM, then with each PV
+      if (!mbar_wait(bar(j >= 1 ? kPvDone : kQFull), j >= 1 ? (j - 1) & 1 : 0)) { ok = false; break; }
+      put(0, early[0]);
+      put(16, early[1]);
+#pragma unroll
+      for (int key = 32; key < C::kTile; key += 16) {
+        uint32_t o[2][8];
+        convert(key, o);
+        put(key, o);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(kVFull));
         mbar_arrive(bar(kStVEmpty + sb));
+      }
+      if (++sb == C::kStV) {
+        sb = 0;
+        st_phase ^= 1;
       }
     }
   } else {
