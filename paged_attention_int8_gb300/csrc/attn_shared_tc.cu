@@ -6,7 +6,7 @@
 // so only the last tile of a prefix is masked.  The pipeline is the one of the
 // causal kernel (attn_prefill_tc.cu), whose measurements chose it: two 128-row
 // halves share every converted K/V tile, both MMA A operands (q, P) live in
-// TMEM, and warp 5 stages pages by TMA (4-stage ring), warps 0, 2, 3, 14 turn
+// TMEM, and warp 5 stages pages by TMA (6-stage ring), warps 0, 2, 3, 14 turn
 // keys into fp16 hi and lo parts (q8: k = code * scale is exact as hi + lo; fp8
 // keys are exact in one part), warps 4 and 15 turn values into fp16, warp 1
 // issues the MMAs of the two halves alternately, and warps 6-13 run one row
@@ -37,8 +37,9 @@ struct SharedTcCfg {
   static constexpr int kTile = 64;
   static constexpr int kHalves = 2;
   static constexpr int kRows = 128 * kHalves;
-  static constexpr int kSt = 4;  // int8 staging stages (TMA)
+  static constexpr int kSt = 6;  // staging stages (TMA)
   static constexpr int kWarps = 16;
+  static constexpr int kKWarps = F8 ? 2 : 4, kVWarps = F8 ? 4 : 2;  // converters
   using L = std::conditional_t<F8, StageF8V4<D, BS, kTile>, StageLayout<D, BS, kTile>>;
   static constexpr int kKBytes = kTile * D * 2;  // one of K_hi, K_lo: [D/64][64 keys][128 B]
   static constexpr int kKSlot = 2 * kKBytes;     // K ring slot: hi then lo
@@ -56,22 +57,21 @@ struct SharedTcCfg {
   static_assert(D == 64 || D == 128, "the tcgen05 kernel handles D = 64, 128");
   static_assert(kSmem <= kSmemOfSm, "shared memory");
   static_assert(kKSlot + 2 * kVBytes >= kRows * 2 * D, "q rows in K slot 1 and the V slots");
-  static_assert(kSt <= 4, "staging barriers");
 };
 
 // barrier indices (8 bytes each, from kBarOff)
 enum : int {
-  kBarStFull = 0,    // [4] producer -> dequant (tx bytes)
-  kBarStEmpty = 4,   // [4] dequant -> producer (6 warps)
-  kBarKFull = 8,     // [2] K dequant -> MMA (4 warps)
-  kBarKEmpty = 10,   // [2] commit after both halves' QK -> K dequant
-  kBarVFull = 12,    // [2] V dequant -> MMA (2 warps)
-  kBarVEmpty = 14,   // [2] commit after both halves' PV -> V dequant
-  kBarSFull = 16,    // [half] commit after QK -> softmax of the half
-  kBarPFull = 18,    // [half] softmax (P in TMEM) -> MMA (4 warps)
-  kBarPvDone = 20,   // [half] commit after the last PV -> epilogue
-  kBarQFull = 22,    // softmax (q written to TMEM) -> MMA (8 warps)
-  kNumBars = 23
+  kBarStFull = 0,    // [6] producer -> dequant (tx bytes)
+  kBarStEmpty = 6,   // [6] dequant -> producer (6 warps)
+  kBarKFull = 12,    // [2] K dequant -> MMA (kKWarps)
+  kBarKEmpty = 14,   // [2] commit after both halves' QK -> K dequant
+  kBarVFull = 16,    // [2] V dequant -> MMA (kVWarps)
+  kBarVEmpty = 18,   // [2] commit after both halves' PV -> V dequant
+  kBarSFull = 20,    // [half] commit after QK -> softmax of the half
+  kBarPFull = 22,    // [half] softmax (P in TMEM) -> MMA (4 warps)
+  kBarPvDone = 24,   // [half] commit after the last PV -> epilogue
+  kBarQFull = 26,    // softmax (q written to TMEM) -> MMA (8 warps)
+  kNumBars = 27
 };
 
 template <int D, int BS, bool F8>
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(512, 1)
   if (!prefix_work(sa, static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk)), a.block_q, lane, w))
     return;
   const int n_rows = w.n_tok * a.qpk;
-  const int kv_begin = w.kv_begin, kv_end = w.kv_end;  // kv_begin starts a tile
-  const int t0 = kv_begin / C::kTile;
+  const int kv_end = w.kv_end;  // kv_begin starts a tile
+  const int t0 = w.kv_begin / C::kTile;
   const int nt = (kv_end + C::kTile - 1) / C::kTile - t0;
   // the softmax warps' 32 rows of q each, in flight during the set-up: they stand
   // in K slot 1 and the V slots until they are in TMEM
@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(bar(kBarStEmpty + s), 6);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(kBarKFull + s), 4);
+      mbar_init(bar(kBarKFull + s), C::kKWarps);
       mbar_init(bar(kBarKEmpty + s), 1);
-      mbar_init(bar(kBarVFull + s), 2);
+      mbar_init(bar(kBarVFull + s), C::kVWarps);
       mbar_init(bar(kBarVEmpty + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -140,13 +140,66 @@ __global__ void __launch_bounds__(512, 1)
 
   if (warp == 5) {
     // ============================================================ producer
-    if constexpr (F8)
-      produce_tiles_f8v4_tma<L, BS, C::kSt>(a, &tmap_k, smem_base, bar(kBarStFull),
-                                            bar(kBarStEmpty), w.row, h, t0, nt, kv_begin, kv_end,
-                                            lane);
-    else
-      produce_tiles<L, BS, C::kSt>(a, &tmap_k, &tmap_v, smem_base, bar(kBarStFull),
-                                   bar(kBarStEmpty), w.row, h, t0, nt, kv_begin, kv_end, lane);
+    // A lane per page and array issues that array's copy: one lane for all of them
+    // took longer over the small copies of fp8 / 4-bit scales than a tile's MMAs.
+    // Block-table entries are read 32 pages at a time; pages at or past the prefix's
+    // end are not staged.
+    const int n_pages = (kv_end + BS - 1) / BS;
+    const int32_t *bt_row = a.block_table + static_cast<int64_t>(w.row) * a.bt_stride;
+    const int my_page = lane >> 2, what = lane & 3;
+    constexpr uint32_t kPageTx = F8 ? BS * D + BS * D / 2 + 4 * BS : 2 * BS * D + 4 * BS * (D / 32);
+    int page_base = -(1 << 30), my_blk = -1;
+    int stage = 0, phase = 1;  // of the ring; the parity of its being empty
+    for (int j = 0; ok && j < nt; ++j) {
+      if (j >= C::kSt) {
+        int there = 1;
+        if (lane == 0) there = mbar_wait(bar(kBarStEmpty + stage), phase);
+        if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
+      }
+      const int lp0 = (t0 + j) * L::kPages;
+      if (lp0 - page_base >= 32) {
+        page_base = lp0;
+        const int lp = page_base + lane;
+        my_blk = -1;
+        if (lp < n_pages) {
+          const int b = lp < a.bt_stride ? bt_row[lp] : -1;
+          if (b >= 0 && b < a.num_blocks) my_blk = b;
+          else flag_status(a.status, PA_DEV_BAD_BLOCK);
+        }
+      }
+      const int blk = __shfl_sync(0xffffffffu, my_blk, lp0 + min(my_page, L::kPages - 1) - page_base);
+      const bool mine = my_page < L::kPages && blk >= 0;
+      const uint32_t full = bar(kBarStFull + stage);
+      const int n_valid = __popc(__ballot_sync(0xffffffffu, mine && what == 0));
+      if (lane == 0) mbar_arrive_expect_tx(full, n_valid * kPageTx);
+      __syncwarp();
+      if (mine) {
+        const int64_t page = static_cast<int64_t>(blk) * a.hk + h;
+        const uint32_t st = smem_base + stage * L::kBytes;
+        if (what == 0)
+          tma_load_2d(st + my_page * (BS * L::kRowBytes), &tmap_k, 0, static_cast<int32_t>(page * BS), full);
+        if constexpr (F8) {
+          if (what == 1)
+            bulk_load(st + L::kVOff + my_page * (D * BS / 2),
+                      reinterpret_cast<const uint8_t *>(a.v_cache) + page * (D * BS / 2), D * BS / 2, full);
+          if (what == 2) bulk_load(st + L::kVsOff + my_page * (BS * 2), a.v_scale + page * BS, BS * 2, full);
+          if (what == 3) bulk_load(st + L::kVzOff + my_page * (BS * 2), a.v_zero + page * BS, BS * 2, full);
+        } else {
+          constexpr int G = D / 32;
+          if (what == 1)
+            tma_load_2d(st + L::kVOff + my_page * (D * BS), &tmap_v, 0, static_cast<int32_t>(page * D), full);
+          if (what == 2)
+            bulk_load(st + L::kKsOff + my_page * (BS * G * 2), a.k_scale + page * BS * G, BS * G * 2, full);
+          if (what == 3)
+            bulk_load(st + L::kVsOff + my_page * (BS * G * 2), a.v_scale + page * BS * G, BS * G * 2, full);
+        }
+      }
+      if (++stage == C::kSt) {
+        stage = 0;
+        phase ^= 1;
+      }
+      __syncwarp();
+    }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
     // One elected lane runs the whole loop: under `elect` the compiler knows that
@@ -209,11 +262,17 @@ __global__ void __launch_bounds__(512, 1)
     ok = __all_sync(0xffffffffu, ok);
   } else if (warp < 6 || warp >= 14) {
     // ============================================================ dequant
-    // warps 0, 2, 3, 14: K (hi and lo parts), thread = one key row, D/2 channels
-    // warps 4, 15: V', thread = D / 64 channel rows of one scale group, all 64 keys
-    const bool k_side = warp != 4 && warp != 15;
-    const int t = (k_side ? (warp == 14 ? 3 : warp == 0 ? 0 : warp - 1) : (warp == 4 ? 0 : 1)) * 32 +
-                  lane;  // K: 0..127, V: 0..63
+    // q8: warps 0, 2, 3, 14: K (hi and lo parts), thread = one key row, D/2 channels;
+    // warps 4, 15: V', thread = D / 64 channel rows of one scale group, all 64 keys.
+    // fp8 / 4-bit, whose keys take a third of the work and whose values more: warps
+    // 0, 2: K, thread = one key row; warps 4, 15, 3, 14: V', 32 keys a thread (two V'
+    // warps took 1960 cycles a tile and set the pace).
+    const bool k_side = F8 ? warp == 0 || warp == 2 : warp != 4 && warp != 15;
+    const int t = (k_side ? (warp == 14 ? 3 : warp == 0 ? 0 : warp - 1)
+                          : (warp == 4 ? 0 : warp == 15 ? 1 : warp == 3 ? 2 : 3)) * 32 +
+                  lane;  // K: 0 .. 32 kKWarps - 1, V: 0 .. 32 kVWarps - 1
+    constexpr int kChannels = 64 * D / (32 * C::kKWarps);  // of a K thread
+    constexpr int kKeys = 64 * 64 / (32 * C::kVWarps);     // of a V' thread
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int sb = j % C::kSt, b = j & 1;
@@ -228,12 +287,12 @@ __global__ void __launch_bounds__(512, 1)
         if (j >= 2 && !mbar_wait(bar(kBarKEmpty + b), ((j - 2) >> 1) & 1)) { ok = false; break; }
         const uint32_t kdst = smem_base + C::kKOff + b * C::kKSlot;
         const int r = t & 63;
-        const int c0 = (t >> 6) * (D / 2);
+        const int c0 = (t >> 6) * kChannels;
         const bool dead = tail && key0 + r >= kv_end;
         if constexpr (F8) {
           // e4m3 -> fp16 exactly; a row outside the visible keys becomes zeros
 #pragma unroll
-          for (int c = c0; c < c0 + D / 2; c += 16) {
+          for (int c = c0; c < c0 + kChannels; c += 16) {
             const uint4 codes = dead ? make_uint4(0u, 0u, 0u, 0u) : lds128(st + L::k_off(r, c));
             const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
             uint32_t hw[8];
@@ -248,7 +307,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         } else {
 #pragma unroll
-        for (int c = c0; c < c0 + D / 2; c += 16) {
+        for (int c = c0; c < c0 + kChannels; c += 16) {
           const uint4 codes = lds128(st + L::k_off(r, c));
           const uint32_t sbits = lds16(st + L::ks_off(r, c / 32));
           const uint32_t s2 = dead ? 0u : (sbits | (sbits << 16));
@@ -292,14 +351,15 @@ __global__ void __launch_bounds__(512, 1)
         constexpr int R = D / 64;
         int ch[R];
         if constexpr (R == 2) {
-          ch[0] = (t >> 4) * 32 + (t & 15);
+          ch[0] = ((t & 63) >> 4) * 32 + (t & 15);
           ch[1] = ch[0] + 16;
         } else {
-          ch[0] = t;
+          ch[0] = t & 63;
         }
+        const int key_lo = (t >> 6) * kKeys;
         if constexpr (F8) {
 #pragma unroll
-          for (int key = 0; key < C::kTile; key += 16) {  // 16 keys: 8 bytes per channel row
+          for (int key = key_lo; key < key_lo + kKeys; key += 16) {  // 16 keys: 8 bytes per channel row
             // the keys' scales and zeros, fp16 pairs (keys 2i, 2i+1); zero
             // outside the visible keys (stale bytes may sit there)
             const uint4 s01 = lds128(st + L::vs_off(key)), s23 = lds128(st + L::vs_off(key + 8));
