@@ -175,46 +175,43 @@ __global__ void __maxnreg__(96)
           else flag_status(a.status, PA_DEV_BAD_BLOCK);
         }
       }
-      int blk[C::kPages];
-      int nvalid = 0;
-#pragma unroll
-      for (int p = 0; p < C::kPages; ++p) {
-        blk[p] = __shfl_sync(0xffffffffu, my_blk, lp0 + p - page_base);
-        nvalid += blk[p] >= 0;
-      }
-      if (lane == 0 && keys) {
-        const uint32_t sk = smem_base + C::kStKOff + st * C::kKStage;
-        mbar_arrive_expect_tx(bar(full0 + st), nvalid * (BS * D + (F8 ? 0 : BS * G * 2)));
-#pragma unroll
-        for (int p = 0; p < C::kPages; ++p) {
-          if (blk[p] < 0) continue;
-          const int64_t page = static_cast<int64_t>(blk[p]) * a.hk + h;
-#pragma unroll
-          for (int sub = 0; sub < 2; ++sub)
-            tma_load_2d(sk + sub * (C::kTile * 128) + p * (BS * 128), &tmap_k, sub * 128,
-                        static_cast<int32_t>(page * BS), bar(full0 + st));
-          if constexpr (!F8)
-            bulk_load(sk + C::kTile * D + p * (BS * G * 2), a.k_scale + page * BS * G, BS * G * 2,
-                      bar(full0 + st));
-        }
-      } else if (lane == 0) {
-        const uint32_t sv = smem_base + C::kStVOff + st * C::kVStage;
-        constexpr uint32_t kVPage = F8 ? D * BS / 2 : D * BS;
-        mbar_arrive_expect_tx(bar(full0 + st), nvalid * (kVPage + (F8 ? 4 * BS : BS * G * 2)));
-#pragma unroll
-        for (int p = 0; p < C::kPages; ++p) {
-          if (blk[p] < 0) continue;
-          const int64_t page = static_cast<int64_t>(blk[p]) * a.hk + h;
+      // a lane per page and copy: keys two boxes and scales, values codes, scales, zeros
+      const int my_page = lane >> 2, what = lane & 3;
+      const int blk = __shfl_sync(0xffffffffu, my_blk, lp0 + min(my_page, C::kPages - 1) - page_base);
+      const bool mine = my_page < C::kPages && blk >= 0;
+      const int n_valid = __popc(__ballot_sync(0xffffffffu, mine && what == 0));
+      constexpr uint32_t kVPage = F8 ? D * BS / 2 : D * BS;
+      const uint32_t full = bar(full0 + st);
+      if (lane == 0)
+        mbar_arrive_expect_tx(full, n_valid * (keys ? BS * D + (F8 ? 0 : BS * G * 2)
+                                                    : kVPage + (F8 ? 4 * BS : BS * G * 2)));
+      __syncwarp();
+      if (mine) {
+        const int64_t page = static_cast<int64_t>(blk) * a.hk + h;
+        if (keys) {
+          const uint32_t sk = smem_base + C::kStKOff + st * C::kKStage;
+          if (what < 2)
+            tma_load_2d(sk + what * (C::kTile * 128) + my_page * (BS * 128), &tmap_k, what * 128,
+                        static_cast<int32_t>(page * BS), full);
+          if constexpr (!F8) {
+            if (what == 2)
+              bulk_load(sk + C::kTile * D + my_page * (BS * G * 2), a.k_scale + page * BS * G, BS * G * 2, full);
+          }
+        } else {
+          const uint32_t sv = smem_base + C::kStVOff + st * C::kVStage;
           if constexpr (F8) {
-            bulk_load(sv + p * kVPage, reinterpret_cast<const uint8_t *>(a.v_cache) + page * kVPage, kVPage,
-                      bar(full0 + st));
-            bulk_load(sv + C::kVCodes + p * (BS * 2), a.v_scale + page * BS, BS * 2, bar(full0 + st));
-            bulk_load(sv + C::kVCodes + C::kTile * 2 + p * (BS * 2), a.v_zero + page * BS, BS * 2,
-                      bar(full0 + st));
+            if (what == 0)
+              bulk_load(sv + my_page * kVPage, reinterpret_cast<const uint8_t *>(a.v_cache) + page * kVPage,
+                        kVPage, full);
+            if (what == 1)
+              bulk_load(sv + C::kVCodes + my_page * (BS * 2), a.v_scale + page * BS, BS * 2, full);
+            if (what == 2)
+              bulk_load(sv + C::kVCodes + C::kTile * 2 + my_page * (BS * 2), a.v_zero + page * BS, BS * 2, full);
           } else {
-            tma_load_2d(sv + p * kVPage, &tmap_v, 0, static_cast<int32_t>(page * D), bar(full0 + st));
-            bulk_load(sv + C::kVCodes + p * (BS * G * 2), a.v_scale + page * BS * G, BS * G * 2,
-                      bar(full0 + st));
+            if (what == 0)
+              tma_load_2d(sv + my_page * kVPage, &tmap_v, 0, static_cast<int32_t>(page * D), full);
+            if (what == 1)
+              bulk_load(sv + C::kVCodes + my_page * (BS * G * 2), a.v_scale + page * BS * G, BS * G * 2, full);
           }
         }
       }
