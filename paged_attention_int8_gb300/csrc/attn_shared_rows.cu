@@ -24,6 +24,14 @@ namespace paq8 {
 
 constexpr float kMaxP = 32768.0f;  // bound on P, inside fp16
 
+// Four 8 x 16-byte matrices; lane l gives the address of row l % 8 of matrix l / 8 and
+// gets bytes 4 (l % 4) .. + 3 of row l / 4 of each.
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr));
+}
+
 // The G fp16 K scales of one key row (contiguous) as floats.
 template <int G>
 __device__ __forceinline__ void load_key_scales(uint32_t addr, float (&f)[G]) {
@@ -64,10 +72,9 @@ struct RowsStage {
   static constexpr int kKsOff = kVOff + kVBytes;        // fp8 / 4-bit: V scales
   static constexpr int kVsOff = kKsOff + (F8 ? 32 : 32 * G);  // fp8 / 4-bit: V zeros
   static constexpr int kBytes = (kVsOff + (F8 ? 32 : 32 * G) + 127) / 128 * 128;
-  // Byte b of key row r.  A lane of the MMA fragment (g, t) reads 8 bytes at 8t
-  // of key perm16(g): the 16-byte pieces of a row are permuted so that the four
-  // rows of a phase (0, 1, 4, 5 or 8, 9, 12, 13; 2 more for the second half)
-  // stand in different banks.
+  // Byte b of key row r.  A matrix of the MMA fragments' loads is one 16-byte piece
+  // of the eight rows perm16(0 .. 7) (0, 1, 4, 5, 8, 9, 12, 13) or of those 2 on: the
+  // pieces of a row are permuted so that these stand in different banks.
   __device__ static __forceinline__ uint32_t k_off(int r, int b) {
     if constexpr (D >= 128) {
       const int i = (r & 1) | ((r >> 2) << 1);
@@ -75,7 +82,7 @@ struct RowsStage {
       return (b >> 7) * (16 * 128) + (off ^ ((((i & 3) << 1) | (i >> 2)) << 4));
     } else {
       const int off = r * 64 + b;
-      return off ^ (((r >> 2) & 1) << 5);
+      return off ^ (((r >> 2) & 1) << 5) ^ (((r >> 3) & 1) << 4);
     }
   }
 };
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
   const int t = lane & 3;
 
   // Q^T as the B operand: of row tile nt, lane (g, t) holds row 8 nt + g, channels
-  // 32gq + 8t + 4s + {0,1} (k = 2t, 2t+1) and + {2,3} (k = 2t+8, 2t+9) for k-step s.
+  // 32gq + 16s + 4t + {0,1} (k = 2t, 2t+1) and + {2,3} (k = 2t+8, 2t+9) for k-step s.
   uint32_t qb[NT][G][2][2];
   bool bad_q = false;
 #pragma unroll
@@ -236,15 +243,18 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
     const bool hv = 8 * nt + g < n_rows;
     const int row = row0 + (hv ? 8 * nt + g : 0);
     const uint16_t *src = a.q + (static_cast<int64_t>(q_start + row / a.qpk) * a.hq + h * a.qpk +
-                                 row % a.qpk) * D + t * 8;
+                                 row % a.qpk) * D + t * 4;
 #pragma unroll
     for (int gq = 0; gq < G; ++gq) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (hv) v = *reinterpret_cast<const uint4 *>(src + gq * 32);
-      qb[nt][gq][0][0] = pack_half2(bf16_lo(v.x), bf16_hi(v.x));
-      qb[nt][gq][0][1] = pack_half2(bf16_lo(v.y), bf16_hi(v.y));
-      qb[nt][gq][1][0] = pack_half2(bf16_lo(v.z), bf16_hi(v.z));
-      qb[nt][gq][1][1] = pack_half2(bf16_lo(v.w), bf16_hi(v.w));
+      uint2 v[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+      if (hv) {
+        v[0] = *reinterpret_cast<const uint2 *>(src + gq * 32);
+        v[1] = *reinterpret_cast<const uint2 *>(src + gq * 32 + 16);
+      }
+      qb[nt][gq][0][0] = pack_half2(bf16_lo(v[0].x), bf16_hi(v[0].x));
+      qb[nt][gq][0][1] = pack_half2(bf16_lo(v[0].y), bf16_hi(v[0].y));
+      qb[nt][gq][1][0] = pack_half2(bf16_lo(v[1].x), bf16_hi(v[1].x));
+      qb[nt][gq][1][1] = pack_half2(bf16_lo(v[1].y), bf16_hi(v[1].y));
       bad_q |= half2_nonfinite(qb[nt][gq][0][0]) || half2_nonfinite(qb[nt][gq][0][1]) ||
                half2_nonfinite(qb[nt][gq][1][0]) || half2_nonfinite(qb[nt][gq][1][1]);
     }
@@ -253,6 +263,11 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
   if (__any_sync(0xffffffffu, bad_q) && warp == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_Q);
   const int r0 = perm16(g);      // key (within a 16-key block) of score row g
   const int r1 = perm16(g + 8);  // ... of score row g + 8
+  // where this lane's rows of the K matrices stand in a stage: score rows 0 - 7 and
+  // 8 - 15 of a group's first 16 channels, then of its others (group gq: ^ 32 gq in
+  // each 128 bytes); of the V matrices: channels 8m .. 8m + 7, 16 keys each
+  const uint32_t k_lane = L::k_off(perm16((lane & 7) + (lane & 8)), lane & 16);
+  const uint32_t v_lane = L::kVOff + lane * 16;
   // last visible key of a row of this pass
   auto limit = [&](int row) {
     return min(kv_end - 1, ctx + (row0 + min(row, n_rows - 1)) / a.qpk);
@@ -305,13 +320,13 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
     if constexpr (F8) {
 #pragma unroll
       for (int gq = 0; gq < G; ++gq) {
-        const uint2 c0 = lds64(st + L::k_off(r0, gq * 32 + t * 8));
-        const uint2 c1 = lds64(st + L::k_off(r1, gq * 32 + t * 8));
+        uint32_t c[4];  // k-step 0: rows g, g + 8; k-step 1
+        ldmatrix4(st + ((k_lane + (gq >> 2) * (16 * 128)) ^ ((gq & 3) * 32)), c);
         // bytes (0,1) -> k 2t, 2t+1; (2,3) -> k 2t+8, 2t+9, as codes4_to_half2
-        const uint32_t a00 = e4m3x2_to_half2(c0.x), a02 = e4m3x2_to_half2(c0.x >> 16);
-        const uint32_t a01 = e4m3x2_to_half2(c1.x), a03 = e4m3x2_to_half2(c1.x >> 16);
-        const uint32_t a10 = e4m3x2_to_half2(c0.y), a12 = e4m3x2_to_half2(c0.y >> 16);
-        const uint32_t a11 = e4m3x2_to_half2(c1.y), a13 = e4m3x2_to_half2(c1.y >> 16);
+        const uint32_t a00 = e4m3x2_to_half2(c[0]), a02 = e4m3x2_to_half2(c[0] >> 16);
+        const uint32_t a01 = e4m3x2_to_half2(c[1]), a03 = e4m3x2_to_half2(c[1] >> 16);
+        const uint32_t a10 = e4m3x2_to_half2(c[2]), a12 = e4m3x2_to_half2(c[2] >> 16);
+        const uint32_t a11 = e4m3x2_to_half2(c[3]), a13 = e4m3x2_to_half2(c[3] >> 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16_16816(s[nt], a00, a01, a02, a03, qb[nt][gq][0][0], qb[nt][gq][0][1]);
@@ -324,13 +339,13 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
       load_key_scales<G>(st + L::kKsOff + r1 * G * 2, ks1);
 #pragma unroll
       for (int gq = 0; gq < G; ++gq) {
-        const uint2 c0 = lds64(st + L::k_off(r0, gq * 32 + t * 8));
-        const uint2 c1 = lds64(st + L::k_off(r1, gq * 32 + t * 8));
+        uint32_t c[4];
+        ldmatrix4(st + ((k_lane + (gq >> 2) * (16 * 128)) ^ ((gq & 3) * 32)), c);
         uint32_t a00, a02, a01, a03, a10, a12, a11, a13;
-        codes4_to_half2(c0.x, a00, a02);  // row g, k-step 0: (k 2t,2t+1), (k 2t+8,2t+9)
-        codes4_to_half2(c1.x, a01, a03);  // row g+8
-        codes4_to_half2(c0.y, a10, a12);  // k-step 1
-        codes4_to_half2(c1.y, a11, a13);
+        codes4_to_half2(c[0], a00, a02);  // row g, k-step 0: (k 2t,2t+1), (k 2t+8,2t+9)
+        codes4_to_half2(c[1], a01, a03);  // row g+8
+        codes4_to_half2(c[2], a10, a12);  // k-step 1
+        codes4_to_half2(c[3], a11, a13);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float sg[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -428,14 +443,14 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
         uint2 vsc = lds64(st + L::kVsOff + (gv * 16 + 4 * t) * 2);
         vsc.x &= vmask.x;
         vsc.y &= vmask.y;
+        uint32_t c[4];  // the group's 32 channels, 8 a matrix: keys 4t .. 4t + 3 of channel g
+        ldmatrix4(st + v_lane + gv * (32 * 16), c);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int cm = gv * 2 + half;
-          const uint32_t w0 = lds32(st + L::kVOff + (cm * 16 + g) * 16 + 4 * t);
-          const uint32_t w1 = lds32(st + L::kVOff + (cm * 16 + g + 8) * 16 + 4 * t);
           uint32_t a0, a2, a1, a3;
-          codes4_to_half2(w0, a0, a2);  // channel g: keys 4t..4t+1 | 4t+2..4t+3
-          codes4_to_half2(w1, a1, a3);  // channel g + 8
+          codes4_to_half2(c[2 * half], a0, a2);      // channel g: keys 4t..4t+1 | 4t+2..4t+3
+          codes4_to_half2(c[2 * half + 1], a1, a3);  // channel g + 8
           a0 = hmul2_u32(a0, vsc.x);
           a2 = hmul2_u32(a2, vsc.y);
           a1 = hmul2_u32(a1, vsc.x);
