@@ -540,7 +540,7 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   {
     // prefix: the count of segments that ends soonest, in units of a tile's time,
     // of a model fitted to 68 batches x 20 counts each (all D, both formats, 1 - 128
-    // sequences, 1 - 5 groups): on average it is 3.5 % above the best count's time;
+    // sequences, 1 - 5 groups): on average it is 2.8 % above the best count's time;
     // whole waves of the prefix's blocks by themselves were 8.4 % above it.
     //  - A block takes its tiles and 8 more (set-up, first loads, triples; row-tile
     //    kernel: 6).
@@ -581,10 +581,12 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   {
     // suffix: ~1024 keys a segment (the decode kernel's measured best; 2048 where one
     // segment each fills the GPU, 128 requests of up to 2048 keys behind 32768: 218 us
-    // against 228), more only while blocks are too few to fill the GPU, four of the rows kernel to an SM, of
-    // 4 tiles at least; two of the row-tile kernel, a tile at least (2 x 40 tokens of
-    // 16 rows behind 1284 keys of D = 256: 7 segments 35 us, 3 45)
-    const int64_t full = few ? 608 : 304, cap = few ? (stiles + 3) / 4 : stiles + 1;
+    // against 228), more only while blocks are too few to fill the GPU: four of the
+    // rows kernel to an SM, of 4 tiles at least; one at D = 256 (two fit, and the
+    // prefix holds most SMs: 32 requests behind 16384 keys, a segment each 43 us, two
+    // 47); one of the row-tile kernel, a tile at least (2 x 40 tokens of 4 rows behind
+    // 1284 keys of D = 256: 7 segments 35 us, 3 45).
+    const int64_t full = few && d != 256 ? 608 : 152, cap = few ? (stiles + 3) / 4 : stiles + 1;
     const int64_t keys = sunits >= full ? 2048 : 1024;
     int64_t n = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + keys - 1) / keys,
                                   std::min((full + sunits - 1) / sunits, cap));
