@@ -475,7 +475,8 @@ size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int
  * Other arguments as pa_paged_attention_ex.  A sequence whose seq_len - q_len
  * is below its prefix, that no group holds, or whose metadata is out of range
  * is not written and flagged PA_DEV_BAD_SEQ; rows of tokens no sequence owns
- * are not written.  Numerics as pa_paged_attention_ex; the parts are joined in
+ * are not written.  Keys past the table's columns are flagged PA_DEV_BAD_BLOCK
+ * and left out.  Numerics as pa_paged_attention_ex; the parts are joined in
  * fp32.  Asynchronous.
  */
 pa_status pa_paged_attention_shared_prefix(

@@ -436,8 +436,9 @@ __global__ void __launch_bounds__(256, 3)
   if (row < rows && c0 >= 0 && tok >= c0 && tok < c1 && c1 <= a.num_tokens && s0 <= seq && s1 > seq &&
       rows_of(s, c1 - c0) <= s.max_rows && P >= 0 && ctx >= P && g0 >= 0 && g0 <= tok && tok < g1 &&
       g1 <= a.num_tokens) {
+    P = min(P, s.capacity);
     n_p = shared_segments(0, P, s.seg_p, s.ns_p);
-    n_s = shared_segments(P, ctx + tok - c0 + 1, s.seg_s, s.ns_s);
+    n_s = shared_segments(P, min(ctx + tok - c0 + 1, s.capacity), s.seg_s, s.ns_s);
   }
   const int n = n_s > 0 ? n_p + n_s : 0;  // 0: a row that is not written
   const int n_max = __reduce_max_sync(0xffffffffu, n);
@@ -689,6 +690,7 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   s.cu_groups = L.cu_groups;
   s.prefix_lens = L.prefix_lens;
   s.num_groups = L.num_groups;
+  s.capacity = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(L.bt_stride) * L.bs, 0x7fffffff - 4096));
   s.ns_p = L.prefix_splits;
   s.ns_s = L.suffix_splits;
   auto seg = [](int len, int ns) { return std::max(1, ((len + kTile - 1) / kTile + ns - 1) / ns); };

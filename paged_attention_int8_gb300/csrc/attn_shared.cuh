@@ -38,6 +38,7 @@ struct SharedArgs {
   int32_t few_rows;            // suffixes of at most this many rows are the rows kernel's
   int32_t max_rows;            // no suffix kernel takes more rows than this
   int32_t row_passes;          // rows kernel: passes over the keys that cover them
+  int32_t capacity;            // keys a row of the block table holds: no more are walked
 };
 
 // Warp-cooperative search: the last i in [0, n) with key(i) <= target, key
@@ -74,8 +75,8 @@ __device__ __forceinline__ int group_token(const SharedArgs &s, int g) {
   return q < 0 || q > s.a.num_seqs ? 0x7fffffff : s.a.cu_seqlens_q[q];
 }
 
-// The prefix length that sequence seq shares, -1 when no group holds it or
-// the group's entries are out of range.
+// The prefix length that sequence seq shares (what a table row holds at most), -1
+// when no group holds it or the group's entries are out of range.
 __device__ __forceinline__ int prefix_of(const SharedArgs &s, int seq, int lane,
                                          int *group = nullptr) {
   if (s.num_groups <= 32) {  // a lane a group: one round of loads
@@ -89,12 +90,12 @@ __device__ __forceinline__ int prefix_of(const SharedArgs &s, int seq, int lane,
     const int g = ball ? 31 - __clz(ball) : 0;
     if (group) *group = g;
     if (__shfl_sync(0xffffffffu, first, g) > seq || __shfl_sync(0xffffffffu, end, g) <= seq) return -1;
-    return __shfl_sync(0xffffffffu, len, g);
+    return min(__shfl_sync(0xffffffffu, len, g), s.capacity);
   }
   const int g = find_last(s.num_groups, seq, lane, [&](int i) { return s.cu_groups[i]; });
   if (group) *group = g;
   if (s.cu_groups[g] > seq || s.cu_groups[g + 1] <= seq) return -1;
-  return s.prefix_lens[g];
+  return min(s.prefix_lens[g], s.capacity);
 }
 
 // Query rows per kv head of a sequence of q_len tokens (saturating).
@@ -180,7 +181,11 @@ __device__ __forceinline__ bool prefix_work(const SharedArgs &s, int item, int b
     w.row = s.cu_groups[g];
     P = s.prefix_lens[g];
   }
-  if (P <= 0) return false;
+  if (P <= 0 || w.row >= a.num_seqs) return false;
+  if (P > s.capacity) {  // pages past the table's columns: flagged and left out
+    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_BLOCK);
+    P = s.capacity;
+  }
   w.q0 = c0 + tok0;
   w.n_tok = min(block_q, c1 - c0 - tok0);
   w.slot = sigma;
@@ -217,7 +222,9 @@ __device__ __forceinline__ bool suffix_work(const SharedArgs &s, int blk, int si
   w.q0 = c0 + tok0;
   w.n_tok = min(block_q, c1 - c0 - tok0);
   w.slot = s.ns_p + sigma;
-  if (!segment_keys(P, ctx + tok0 + w.n_tok, s.seg_s, s.ns_s, sigma, w)) return false;
+  const int end = ctx + tok0 + w.n_tok;
+  if (end > s.capacity && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_BLOCK);
+  if (!segment_keys(P, min(end, s.capacity), s.seg_s, s.ns_s, sigma, w)) return false;
   w.limit0 = ctx + tok0;
   w.limit_step = 1;
   return true;

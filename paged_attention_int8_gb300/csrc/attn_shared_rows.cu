@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
   const int n_rows = min(8 * NT, all_rows - row0);  // of this pass
   if (n_rows <= 0) return;
   SharedWork w;
-  if (!segment_keys(P, seq_len, sa.seg_s, sa.ns_s, sigma, w)) return;
+  if (seq_len > sa.capacity && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_BLOCK);
+  if (!segment_keys(P, min(seq_len, sa.capacity), sa.seg_s, sa.ns_s, sigma, w)) return;
   const int kv_begin = w.kv_begin, kv_end = w.kv_end;
   // this warp's 16-key blocks: b0, b0 + 4, ...
   const int b0 = kv_begin / 16 + warp;

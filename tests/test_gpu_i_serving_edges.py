@@ -177,3 +177,53 @@ def test_omitted_results_belong_to_the_calls_stream(cuda_device):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert tables.block_table.tolist() == [[7, -1, -1, -1], [8, 9, 10, -1]]
     assert tables.slot_mapping.tolist() == [7 * 16 + 5, 10 * 16 + 8]
+
+
+@pytest.mark.parametrize("fmt,hq,hk,d,q_len", [("q8", 8, 2, 128, 1), ("q8", 8, 2, 256, 1),
+                                               ("f8v4", 2, 2, 64, 3), ("q8", 16, 1, 128, 9)])
+@pytest.mark.parametrize("n", [2, 24])
+def test_lengths_past_the_table_end_there(cuda_device, fmt, hq, hk, d, q_len, n):
+    """Lengths that no table row can hold (the largest int32): flagged, walked no
+    further than the table's columns, and the other group's rows right."""
+    b = S.make(61, cuda_device, fmt, hq, hk, d, 16, [(90, [(q_len, 33)] * n), (40, [(q_len, 30)] * n)])
+    ref = S.reference(b)
+    fn = (_lib.paged_attention_shared_prefix if fmt == "q8"
+          else _lib.paged_attention_shared_prefix_f8v4)
+    lens, prefixes = b.lens.clone(), b.prefixes.clone()
+    lens[n:] = 2 ** 31 - 1
+    good = n * q_len
+    for prefix in (40, 2 ** 31 - 100):
+        prefixes[1] = prefix
+        ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device)
+        out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=cuda_device)
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        fn(b.q, *b.cache, b.cu, lens, b.table, b.groups, prefixes, *b.bounds, out=out, lse=lse,
+           workspace=ws)
+        end.record()
+        with pytest.raises(_lib.PagedAttentionError) as err:
+            _lib.check_status(ws)
+        assert err.value.bits == _lib.DEV_BAD_BLOCK
+        assert start.elapsed_time(end) < 50  # ms; 2^31 keys would take seconds
+        # fp32 sums; bf16 rounds |out| < 4 by 2^-7 at most, fp16 P and V' by 2^-10 of it
+        assert (lse[:good].double().cpu() - ref[1][:good]).abs().max() < 1e-3
+        assert (out[:good].double().cpu() - ref[0][:good]).abs().max() < 2e-2
+
+
+def test_groups_that_name_no_sequence(cuda_device):
+    """Group bounds out of order and past the batch: nothing out of range is read,
+    the rows no group holds stay."""
+    b = S.make(63, cuda_device, "q8", 8, 2, 128, 16, [(64, [(1, 20)] * 20), (32, [(1, 9)] * 20)])
+    for groups in ([0, 40, 0], [40, 0, 40], [0, 41, 40], [-1, 20, 40], [0, 2 ** 31 - 1, 40]):
+        ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device)
+        out = torch.full_like(b.q, float("nan"))
+        bad = torch.tensor(groups, dtype=torch.int32, device=cuda_device)
+        cu = b.cu.clone()
+        cu[-1] = 39
+        _lib.paged_attention_shared_prefix(b.q, *b.cache, cu, b.lens, b.table, bad, b.prefixes,
+                                           *b.bounds, out=out, workspace=ws)
+        try:
+            _lib.check_status(ws)
+        except _lib.PagedAttentionError as err:
+            assert err.bits & ~(_lib.DEV_BAD_SEQ | _lib.DEV_BAD_BLOCK) == 0
+        assert torch.isnan(out[39].float()).all()
