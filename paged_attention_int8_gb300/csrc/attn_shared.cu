@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int h = blockIdx.y;  // kv head
+  if (s.first) wait_for_predecessor();
   launch_dependents();
   const LastBlockWaits at_end{blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1};
 
@@ -598,7 +599,7 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
 }
 
 template <int D, int BS, bool F8>
-static cudaError_t launch_shared_mma_t(const SharedArgs &s, bool beside, cudaStream_t stream) {
+static cudaError_t launch_shared_mma_t(const SharedArgs &s, cudaStream_t stream) {
   using C = SharedMmaCfg<D, BS, F8>;
   static DeviceOnce configured;
   cudaError_t e = configured.get(nullptr, [](int, int *) {
@@ -610,15 +611,15 @@ static cudaError_t launch_shared_mma_t(const SharedArgs &s, bool beside, cudaStr
                      static_cast<int64_t>(s.n_sblocks) * s.ns_s;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(s.a.hk));
-  return launch_kernel(shared_mma_kernel<D, BS, F8>, grid, kThreads, C::kSmemBytes, stream, beside, s);
+  return launch_kernel(shared_mma_kernel<D, BS, F8>, grid, kThreads, C::kSmemBytes, stream, s);
 }
 
-static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8v4, bool beside,
+static cudaError_t launch_shared_mma(const SharedArgs &s, int d, int bs, bool f8v4,
                                      cudaStream_t stream) {
 #define PAQ8_SHARED_CASE(DD, BB)                                          \
   if (d == DD && bs == BB)                                                \
-    return f8v4 ? launch_shared_mma_t<DD, BB, true>(s, beside, stream)    \
-                : launch_shared_mma_t<DD, BB, false>(s, beside, stream);
+    return f8v4 ? launch_shared_mma_t<DD, BB, true>(s, stream)            \
+                : launch_shared_mma_t<DD, BB, false>(s, stream);
   PAQ8_SHARED_CASE(64, 16)
   PAQ8_SHARED_CASE(64, 32)
   PAQ8_SHARED_CASE(128, 16)
@@ -723,7 +724,8 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
     a.block_q = std::max(1, kRowTile / a.qpk);
     s.n_pblocks = tc ? 0 : prefix_blocks(L.num_tokens, L.num_groups, a.block_q);
     s.n_sblocks = many ? L.num_tokens / a.block_q + L.num_seqs : 0;
-    if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, tc, stream)) != cudaSuccess) return e;
+    s.first = !tc;
+    if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   }
   if ((e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   // channel blocks a warp takes in turn: one while all blocks are resident at once
@@ -735,9 +737,9 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(L.hk));
   switch (L.d) {
-    case 64: return launch_kernel(shared_join_kernel<64>, grid, 256, 0, stream, true, s, cpw_log2);
-    case 128: return launch_kernel(shared_join_kernel<128>, grid, 256, 0, stream, true, s, cpw_log2);
-    case 256: return launch_kernel(shared_join_kernel<256>, grid, 256, 0, stream, true, s, cpw_log2);
+    case 64: return launch_kernel(shared_join_kernel<64>, grid, 256, 0, stream, s, cpw_log2);
+    case 128: return launch_kernel(shared_join_kernel<128>, grid, 256, 0, stream, s, cpw_log2);
+    case 256: return launch_kernel(shared_join_kernel<256>, grid, 256, 0, stream, s, cpw_log2);
   }
   return cudaErrorInvalidValue;
 }

@@ -20,6 +20,7 @@
 #include "attn_common.cuh"
 #include "attn_f8v4.cuh"
 #include "launch.h"
+#include "programmatic.cuh"
 #include "serving.h"
 
 namespace paq8 {
@@ -39,6 +40,7 @@ struct SharedArgs {
   int32_t max_rows;            // no suffix kernel takes more rows than this
   int32_t row_passes;          // rows kernel: passes over the keys that cover them
   int32_t capacity;            // keys a row of the block table holds: no more are walked
+  int32_t first;               // row-tile kernel: it is the call's first
 };
 
 // Warp-cooperative search: the last i in [0, n) with key(i) <= target, key
@@ -271,49 +273,6 @@ __device__ __forceinline__ void copy_q_rows(const AttnArgs &a, uint32_t dst, int
                  base + (static_cast<int64_t>(tok) * (a.hq - a.qpk) + r0 + r) * D);
   }
   cp_async_commit();
-}
-
-// Programmatic launches.  The call's kernels work on disjoint triples, so each
-// is launched while its predecessor runs (launch_dependents at a block's start)
-// and fills the SMs beside it.  The last block of such a kernel waits for the
-// predecessor before it ends, so that a kernel's end implies the end of all
-// before it, which is what the join waits for.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_predecessor() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// In a block of the grid's last one: whichever way a thread leaves, it waits.
-struct LastBlockWaits {
-  bool last;
-  __device__ ~LastBlockWaits() {
-    if (last) wait_for_predecessor();
-  }
-};
-
-// Launch attribute of a kernel that may start beside its predecessor.
-struct BesidePredecessor {
-  cudaLaunchAttribute attr[1];
-  BesidePredecessor() {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  }
-};
-
-template <class... P, class... A>
-cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
-                          cudaStream_t stream, bool beside, const A &...args) {
-  BesidePredecessor b;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = b.attr;
-  cfg.numAttrs = beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace paq8

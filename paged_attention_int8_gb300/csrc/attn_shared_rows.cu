@@ -556,7 +556,7 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
   const int64_t grid = static_cast<int64_t>(s.a.num_seqs) * s.ns_s * s.a.hk * p.row_passes;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_kernel(shared_rows_kernel<D, BS, F8, NT>, dim3(static_cast<unsigned>(grid)), 128,
-                       Cfg::kSmem, stream, true, p);
+                       Cfg::kSmem, stream, p);
 }
 
 template <int D, int BS>

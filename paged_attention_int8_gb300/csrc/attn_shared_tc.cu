@@ -89,11 +89,12 @@ __global__ void __launch_bounds__(512, 1)
   const int lane = threadIdx.x & 31;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(sa.a.hk));
 
-  launch_dependents();
   if (threadIdx.x == 5 * 32) {
     prefetch_tensormap(&tmap_k);
     if constexpr (!F8) prefetch_tensormap(&tmap_v);
   }
+  wait_for_predecessor();
+  launch_dependents();
   SharedWork w;
   if (!prefix_work(sa, static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk)), a.block_q, lane, w))
     return;
@@ -609,7 +610,7 @@ static cudaError_t launch_shared_tc_t(const SharedArgs &s, const CUtensorMap &tk
   const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p * s.a.hk;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(gx));
-  return launch_kernel(shared_tc_kernel<D, BS, F8>, grid, C::kWarps * 32, kSmemOfSm, stream, false, s,
+  return launch_kernel(shared_tc_kernel<D, BS, F8>, grid, C::kWarps * 32, kSmemOfSm, stream, s,
                        tk, tv);
 }
 

@@ -94,11 +94,12 @@ __global__ void __maxnreg__(96)
   const int lane = threadIdx.x & 31;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(sa.a.hk));
 
-  launch_dependents();
   if (threadIdx.x == 5 * 32) prefetch_tensormap(&tmap_k);
   if constexpr (!F8) {
     if (threadIdx.x == 18 * 32) prefetch_tensormap(&tmap_v);
   }
+  wait_for_predecessor();
+  launch_dependents();
   SharedWork w;
   if (!prefix_work(sa, static_cast<int>(blockIdx.x / static_cast<unsigned>(a.hk)), a.block_q, lane, w))
     return;
@@ -615,7 +616,7 @@ cudaError_t launch_shared_tc256_t(const SharedArgs &s, const CUtensorMap &tk, co
   const int64_t gx = static_cast<int64_t>(s.n_pblocks) * s.ns_p * s.a.hk;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_kernel(shared_tc256_kernel<BS, F8>, dim3(static_cast<unsigned>(gx)), C::kWarps * 32,
-                       C::kSmem, stream, false, s, tk, tv);
+                       C::kSmem, stream, s, tk, tv);
 }
 
 }  // namespace

@@ -20,6 +20,7 @@
 // and takes no sum.
 #include "common.cuh"
 #include "launch.h"
+#include "programmatic.cuh"
 #include "serving.h"
 
 namespace paq8 {
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_tables_kernel(const BlockTa
   const int chunk = static_cast<int>(blockIdx.y);
   const bool active = s < p.num_seqs;
 
+  wait_for_predecessor();  // the lengths, and every reader of what is written here
   SeqPlan me = {0, 0, 0, 0, false, true};
   if (active) me = plan_of(p, s);
   const int n_new = me.end - me.first;  // 0 when q == 0: end == held == first
@@ -236,8 +238,7 @@ cudaError_t launch_build_block_tables(const BlockTables &p, cudaStream_t stream)
   const int tc = (p.num_tokens + kTokenChunk - 1) / kTokenChunk;
   const int pc = (p.table_stride + kPageChunk - 1) / kPageChunk;
   const unsigned y = static_cast<unsigned>(tc > pc ? tc : pc);  // at most 2^15: the sizes are checked
-  block_tables_kernel<<<dim3(x, y), kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(block_tables_kernel, dim3(x, y), kWarps * 32, 0, stream, p);
 }
 
 }  // namespace paq8

@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "programmatic.cuh"
 #include "serving.h"
 
 namespace paq8 {
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(32) copy_blocks_kernel(const BlockCopy p, int 
     fence_barrier_init();
   }
   __syncwarp();
+  wait_for_predecessor();  // the pairs, and the blocks themselves
   bool ok = true;
   int n = 0;  // parts whose read was issued; all of this is lane 0's
   // part i has landed: write it
@@ -125,9 +127,8 @@ cudaError_t launch_copy_blocks(const BlockCopy &p, cudaStream_t stream) {
     return cudaFuncSetAttribute(copy_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCopy);
   });
   if (e != cudaSuccess) return e;
-  copy_blocks_kernel<<<static_cast<unsigned>(grid), 32, kSmemCopy, stream>>>(
-      p, static_cast<int>(parts), static_cast<int>(part_bytes));
-  return cudaGetLastError();
+  return launch_kernel(copy_blocks_kernel, dim3(static_cast<unsigned>(grid)), 32, kSmemCopy, stream, p,
+                       static_cast<int>(parts), static_cast<int>(part_bytes));
 }
 
 }  // namespace paq8

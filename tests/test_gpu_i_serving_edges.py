@@ -227,3 +227,158 @@ def test_groups_that_name_no_sequence(cuda_device):
         except _lib.PagedAttentionError as err:
             assert err.bits & ~(_lib.DEV_BAD_SEQ | _lib.DEV_BAD_BLOCK) == 0
         assert torch.isnan(out[39].float()).all()
+
+
+@pytest.mark.parametrize("fmt,d,hq,hk,n,q_len", [("q8", 128, 8, 1, 20, 1), ("q8", 256, 16, 2, 12, 1),
+                                                 ("f8v4", 64, 4, 2, 3, 1), ("q8", 128, 8, 2, 3, 20),
+                                                 ("q8", 128, 4, 2, 2, 1)])
+@pytest.mark.parametrize("before", ["nothing", "memset", "copy", "kernel", "branches", "call"])
+def test_reads_what_was_written_just_before(cuda_device, fmt, d, hq, hk, n, q_len, before):
+    """The call's kernels start only after the work before it on the stream: its
+    inputs become right right before it, by every kind of work that can stand there,
+    eagerly and in a captured graph."""
+    b = S.make(71, cuda_device, fmt, hq, hk, d, 16, [(200, [(q_len, 50)] * n)])
+    ref = S.reference(b)
+    fn = (_lib.paged_attention_shared_prefix if fmt == "q8"
+          else _lib.paged_attention_shared_prefix_f8v4)
+    q, cu, lens, groups, prefixes = (torch.empty_like(t) for t in (b.q, b.cu, b.lens, b.groups,
+                                                                   b.prefixes))
+    pairs = list(zip((q, cu, lens, groups, prefixes), (b.q, b.cu, b.lens, b.groups, b.prefixes)))
+    out, lse = torch.empty_like(b.q), torch.empty(b.q.shape[:2], device=cuda_device)
+    ws = torch.zeros(_lib.shared_prefix_workspace_size(n, b.q.shape[0], 1, hq, hk, d, *b.bounds),
+                     dtype=torch.uint8, device=cuda_device)
+    side = torch.cuda.Stream()
+    other = torch.empty(1 << 24, device=cuda_device)
+
+    def call(x=q):
+        fn(x, *b.cache, cu, lens, b.table, groups, prefixes, *b.bounds, out=out, lse=lse,
+           workspace=ws)
+
+    def run():
+        other.fill_(1.0)
+        for t, x in pairs:
+            t.copy_(x)
+        if before == "memset":
+            lse.view(torch.uint8).zero_()
+        elif before == "kernel":
+            for t, x in pairs:
+                torch.add(x, 0, out=t)
+        elif before == "branches":
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                other.mul_(2.0)
+                q.copy_(b.q)
+            cu.copy_(b.cu)
+            main.wait_stream(side)
+        elif before == "call":
+            call(torch.zeros_like(q))
+        call()
+
+    def spoil():
+        for t, _ in pairs:
+            t.zero_()
+        out.fill_(float("nan")), lse.fill_(float("nan"))
+
+    def verify():
+        torch.cuda.synchronize()
+        assert _lib.check_status(ws) == 0
+        S.check(b, out, lse, ref=ref)
+
+    if before != "nothing":
+        for _ in range(3):
+            spoil()
+            torch.cuda.synchronize()
+            run()
+            verify()
+    for t, x in pairs:
+        t.copy_(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call() if before == "nothing" else run()
+    for _ in range(3):
+        if before != "nothing":
+            spoil()
+        torch.cuda.synchronize()
+        graph.replay()
+        verify()
+
+
+@pytest.mark.parametrize("before", ["memset", "copy", "kernel", "branches", "call"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_tables_and_copies_follow_what_was_before(cuda_device, before, captured):
+    """The same of the single-kernel calls: tables from lengths written just before,
+    then a copy by the pairs they made, from blocks written just before."""
+    H.ensure_built()
+    dev = cuda_device
+    n, columns, bs = 40, 300, 16
+    ctx_good = torch.arange(n, dtype=torch.int32, device=dev) * 101 + 7
+    one, free = torch.ones(n, dtype=torch.int32, device=dev), torch.arange(5000, 5100, dtype=torch.int32,
+                                                                           device=dev)
+    source = torch.arange(n * columns, dtype=torch.int32, device=dev).view(n, columns) % 4000
+    blocks = 6000
+    cache = _filled(blocks, 1, 64, bs, dev, 9)
+    fresh = [t.clone() for t in cache]
+    ctx = torch.zeros_like(ctx_good)
+    side = torch.cuda.Stream()
+    other = torch.empty(1 << 24, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    t = _lib.build_block_tables(ctx, one, source, free, blocks, bs, n,
+                                source_rows=torch.arange(n, dtype=torch.int32, device=dev),
+                                shared_lens=ctx_good)
+    rows = torch.arange(n, dtype=torch.int32, device=dev)
+
+    def run():
+        other.fill_(1.0)
+        ctx.copy_(ctx_good)
+        for x, y in zip(cache, fresh):
+            x.copy_(y)
+        if before == "memset":
+            t.copy_pairs.zero_()
+        elif before == "kernel":
+            torch.add(ctx_good, 0, out=ctx)
+        elif before == "branches":
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                other.mul_(2.0)
+                ctx.copy_(ctx_good)
+            main.wait_stream(side)
+        elif before == "call":
+            _lib.copy_blocks(t.copy_pairs, *cache)
+            for x, y in zip(cache, fresh):
+                x.copy_(y)
+        _lib.build_block_tables(ctx, one, source, free, blocks, bs, n, source_rows=rows,
+                                shared_lens=ctx_good, out=t, status=status)
+        _lib.copy_blocks(t.copy_pairs, *cache, status=status)
+
+    # on the host: every sequence's last page is shared and partly filled, or full
+    c = ctx_good.tolist()
+    dealt, pairs = 5000, []
+    for s in range(n):
+        pairs.append([int(source[s, c[s] // bs]), dealt] if c[s] % bs else [-1, -1])
+        dealt += 1
+    want = [x.clone() for x in fresh]
+    for a, b in pairs:
+        if a >= 0:
+            for x, y in zip(want, fresh):
+                x[b] = y[a]
+    run()
+    torch.cuda.synchronize()
+    graph = None
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(4):
+        ctx.zero_(), t.copy_pairs.fill_(-1)
+        for x in cache:
+            x.zero_()
+        torch.cuda.synchronize()
+        graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        assert _lib.check_status(status) == 0
+        assert t.copy_pairs.tolist() == pairs and t.seq_lens.tolist() == [x + 1 for x in c]
+        for x, y in zip(cache, want):
+            assert torch.equal(x, y)
