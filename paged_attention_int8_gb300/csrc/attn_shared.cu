@@ -699,11 +699,19 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   s.seg_s = seg(L.max_suffix_len + kTile, s.ns_s);  // a suffix may start inside a tile
   // Who takes what: the prefix goes to the tensor-core kernel or the row-tile
   // kernel (prefix_on_tc), a suffix of up to kFewRows rows to the rows kernel,
-  // of more to the row-tile kernel.
+  // of more to the row-tile kernel.  Where that one takes the prefix and the
+  // suffixes are little, it takes them all: a launch less (3.4 us of a call whose
+  // host side is longer than its 8 - 12 us on the GPU).  On the GPU, one kernel
+  // against two: 7.7 us and 8.3 (4 sequences, 37 own keys, 2 kv heads of 64), 11.6
+  // and 12.7 (8 of 128), 16.8 and 22.7 (8 of 256); with 1000 own keys 11.1 and 9.8,
+  // 26 and 15, 39 and 24.
   const bool tc = prefix_on_tc(L.num_tokens, L.num_groups, a.qpk, L.d);
+  const int64_t little = L.d == 64 ? 256 : 64;  // (sequence, kv head, tile of keys)
+  const bool one = !tc && static_cast<int64_t>(L.num_seqs) * L.hk *
+                              ((static_cast<int64_t>(L.max_suffix_len) + kTile - 1) / kTile) <= little;
   const int64_t most = static_cast<int64_t>(L.max_query_len) * a.qpk;  // rows of a sequence
-  const bool many = most > kFewRows;
-  s.few_rows = static_cast<int32_t>(std::min<int64_t>(most, kFewRows));
+  const bool many = one || most > kFewRows;
+  s.few_rows = one ? 0 : static_cast<int32_t>(std::min<int64_t>(most, kFewRows));
   s.max_rows = many ? 0x7fffffff : s.few_rows;
   cudaError_t e = cudaSuccess;
   if (tc) {
@@ -727,7 +735,7 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
     s.first = !tc;
     if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   }
-  if ((e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
+  if (!one && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   // channel blocks a warp takes in turn: one while all blocks are resident at once
   // (three an SM), so that a row's look-ups are not repeated behind a first wave
   const int64_t groups = (static_cast<int64_t>(L.num_tokens) * a.qpk + 7) / 8;

@@ -6,9 +6,10 @@
 // 13 KB.  A thread block is one warp with two parts in shared memory: bulk copies
 // bring one in while the part before it goes out, five thread blocks an SM, and no
 // thread holds data.  8191 blocks of 24.5 KB (fp8 / 4-bit, 8 kv heads of 128
-// channels) take 65 us, 6.3 TB/s read and written; 16-byte loads and stores of 256
-// threads took 86 (launched plainly, as the next two: the rest 68).  More in flight is no faster: 12 KB parts, two read ahead in a
-// ring of four, four an SM, 72 us; 8 KB, four ahead of six, 78.
+// channels) take 65 us, 6.3 TB/s read and written (68 when the launch does not
+// overlap the work before; so measured, 16-byte loads and stores of 256 threads took
+// 86, and more in flight is no faster: 12 KB parts, two read ahead in a ring of four,
+// four thread blocks an SM, 72; 8 KB, four ahead of six, 78).
 #include <algorithm>
 
 #include "common.cuh"
