@@ -372,13 +372,13 @@ __global__ void __launch_bounds__(kThreads) shared_mma_kernel(const __grid_const
 // merged to bf16 output and fp32 LSE.  One warp per 8 consecutive rows of a kv
 // head and 16 channels: lane l reads 4 channels (l / 8) of row l % 8, so that
 // eight lanes take a whole 128-byte line of a segment, and every segment's load
-// is in flight at once (8 a batch); where there are more warps than fit at once, a
-// warp takes several channel blocks in turn.  Bound by its reads (D + 2 floats a row and
+// is in flight at once (8 or 4 a batch); where there are more warps than fit at once,
+// a warp takes several channel blocks in turn.  Bound by its reads (D + 2 floats a row and
 // segment, L2 hits); with 32-byte pieces, two rows of all channels a warp, it
 // took 15 us where it now takes 5 (64 requests, 21 segments).  Launched beside
 // the last kernel: it looks up its rows' sequences and then waits.
-template <int D>
-__global__ void __launch_bounds__(256, 3)
+template <int D, int kBatch>
+__global__ void __launch_bounds__(256, kBatch == 8 ? 3 : 4)
     shared_join_kernel(const __grid_constant__ SharedArgs s, int cpw_log2) {
   constexpr int kCbLog2 = D == 64 ? 2 : D == 128 ? 3 : 4;  // D / 16 channel blocks of a row
   const AttnArgs &a = s.a;
@@ -457,7 +457,6 @@ __global__ void __launch_bounds__(256, 3)
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float *acc_row = acc_at<D>(s, 0, h) + (static_cast<int64_t>(cb * 4 + piece) * rows + row) * 4;
     for (int k0 = 0; k0 < n_max; k0 += 16) {
-      constexpr int kBatch = 8;
       float4 x[kBatch];
       auto load = [&](int k1) {
 #pragma unroll
@@ -736,18 +735,29 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
     if ((e = launch_shared_mma(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
   }
   if (!one && (e = launch_shared_rows(s, L.d, L.bs, L.f8v4, stream)) != cudaSuccess) return e;
-  // channel blocks a warp takes in turn: one while all blocks are resident at once
-  // (three an SM), so that a row's look-ups are not repeated behind a first wave
+  // All blocks resident at once, so that a row's look-ups are not repeated behind a
+  // first wave: eight loads in flight a lane and three blocks an SM where each warp
+  // can take one channel block so, else four loads, four blocks an SM, and several
+  // channel blocks in turn (128 requests of 64 q heads 196 us against 199; the other
+  // way round 32 requests of 256-channel heads 42.7 against 41.2)
   const int64_t groups = (static_cast<int64_t>(L.num_tokens) * a.qpk + 7) / 8;
-  int cb_log2 = L.d == 64 ? 2 : L.d == 128 ? 3 : 4, cpw_log2 = 0;
-  while (cpw_log2 < cb_log2 && (groups << (cb_log2 - cpw_log2)) * L.hk > 3 * 8 * 152) ++cpw_log2;
+  const int cb_log2 = L.d == 64 ? 2 : L.d == 128 ? 3 : 4;
+  const bool eight = (groups << cb_log2) * L.hk <= 3 * 8 * 152;
+  int cpw_log2 = 0;
+  while (!eight && cpw_log2 < cb_log2 && (groups << (cb_log2 - cpw_log2)) * L.hk > 4 * 8 * 152) ++cpw_log2;
   const int64_t blocks = ((groups << (cb_log2 - cpw_log2)) + 7) / 8;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(L.hk));
   switch (L.d) {
-    case 64: return launch_kernel(shared_join_kernel<64>, grid, 256, 0, stream, s, cpw_log2);
-    case 128: return launch_kernel(shared_join_kernel<128>, grid, 256, 0, stream, s, cpw_log2);
-    case 256: return launch_kernel(shared_join_kernel<256>, grid, 256, 0, stream, s, cpw_log2);
+    case 64:
+      return launch_kernel(eight ? shared_join_kernel<64, 8> : shared_join_kernel<64, 4>, grid, 256, 0, stream,
+                           s, cpw_log2);
+    case 128:
+      return launch_kernel(eight ? shared_join_kernel<128, 8> : shared_join_kernel<128, 4>, grid, 256, 0,
+                           stream, s, cpw_log2);
+    case 256:
+      return launch_kernel(eight ? shared_join_kernel<256, 8> : shared_join_kernel<256, 4>, grid, 256, 0,
+                           stream, s, cpw_log2);
   }
   return cudaErrorInvalidValue;
 }

@@ -382,3 +382,12 @@ def test_tables_and_copies_follow_what_was_before(cuda_device, before, captured)
         assert t.copy_pairs.tolist() == pairs and t.seq_lens.tolist() == [x + 1 for x in c]
         for x, y in zip(cache, want):
             assert torch.equal(x, y)
+
+
+# so many rows that a warp of the join takes two, four or more channel blocks in turn
+@pytest.mark.parametrize("fmt,hq,hk,d,n,pad", [("q8", 64, 8, 128, 100, 0), ("f8v4", 64, 4, 128, 200, 3),
+                                               ("q8", 32, 8, 256, 170, 1), ("q8", 16, 16, 64, 701, 5)])
+def test_many_rows_to_join(cuda_device, fmt, hq, hk, d, n, pad):
+    b = S.make(n, cuda_device, fmt, hq, hk, d, 16,
+               [(30, [(1, 1 + i % 5) for i in range(n - 7)]), (17, [(1, 2)] * 7)], pad_rows=pad)
+    S.check(b, *b.call())
