@@ -10,8 +10,9 @@
 //   suffix: the query tokens of one sequence x keys [P, seq_len), causal.
 // Each item's keys are cut into segments of whole 64-key tiles, and each
 // segment leaves one triple per row (a row = query token x q head):
-//   m = max_j s_j (log2 units), l = sum_j 2^(s_j - m), acc = sum_j 2^(s_j - m) v_j,
-// which the join kernel (attn_shared.cu) merges:
+//   m (log2 units), l = sum_j 2^(s_j - m), acc = sum_j 2^(s_j - m) v_j,
+// m one of the scores s_j, at most 15 below the largest (so that every 2^(s_j - m)
+// is inside fp16), which the join kernel (attn_shared.cu) merges:
 //   M = max m_k, w_k = 2^(m_k - M), out = sum w_k acc_k / sum w_k l_k,
 //   lse = (M + log2 sum w_k l_k) ln 2,
 // a sink joining as one more term with no value.  Triples are fp32.
