@@ -5,17 +5,17 @@
 // its N dimension,
 //   S^T[16 keys x 8 rows] = K[16 x 16 ch] . Q^T[16 ch x 8],
 //   O^T[16 ch x 8 rows] += V^T[16 ch x 16 keys] . P^T[16 keys x 8],
-// NT tiles of 8 rows (1, 2 or 4, by the bound of the query lengths) off every
-// converted key and value: the conversions, not the MMAs, are most of a block's
-// instructions.  More rows than 8 NT take several passes.
+// NT tiles of 8 rows (1 or 2, by the bound of the query lengths) off every converted
+// key and value: the conversions, not the MMAs, are most of a block's instructions.
+// More rows than 8 NT take several passes.
 // Each row has its own causal limit, taken on edge blocks only.  HBM bound:
 // 2 (D + D / 16) bytes a key and kv head (q8), D + D / 2 + 4 (fp8 / 4-bit).
 //
 // Four warps share a segment's 16-key blocks round robin, each on its own: it
 // copies its blocks with 16-byte cp.async into a private 3-stage ring and reads
 // them back, so that no warp waits for another until the four softmax states
-// are merged at the end (one fp32 triple per row); four blocks of four warps and
-// 128 registers hold an SM.
+// are merged at the end (one fp32 triple per row); four blocks of 128 registers a
+// thread hold an SM at D = 64, 128 and one row tile.
 #include <type_traits>
 
 #include "attn_shared.cuh"
@@ -94,9 +94,9 @@ struct SharedRowsCfg {
   static constexpr int kSt = 3;
   static constexpr int kCm = D / 16;                    // 16-channel blocks of the output
   static constexpr int G = D / 32;
-  // blocks per SM: 128 registers a thread (four blocks) where that costs a few
-  // spills at most
-  static constexpr int kMinBlocks = D == 256 || (D == 128 && NT == 4) ? 2 : NT == 4 ? 3 : 4;
+  // blocks per SM: as many as the registers hold without spills (48 requests of up to
+  // 20 rows and 2000 keys, D = 128: three blocks 60 us, four with 144 bytes spilled 95)
+  static constexpr int kMinBlocks = D == 256 ? 2 : (D == 128 && NT == 2) ? 3 : 4;
   static constexpr int kRing = kWarps * kSt * L::kBytes;
   static constexpr int kMerge = kWarps * 32 * NT * (4 + 4 * kCm) * 4;
   static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
@@ -561,19 +561,16 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
 
 template <int D, int BS>
 static cudaError_t launch_shared_rows_d(const SharedArgs &s, bool f8v4, cudaStream_t stream) {
-  // row tiles a pass: as many as the rows need and the registers hold.  At D = 128
-  // 4 tiles leave two blocks an SM: 48 requests of up to 32 rows and 2000 keys take
-  // 82 us (fp8 / 4-bit) and 90 (q8), two passes of 2 tiles 101 and 116; of up to 24
-  // rows and 700 keys, where the fourth tile stays empty, 68 and 76 against 60 and 66.
-  if (s.few_rows <= 8)
+  // row tiles a pass: two where the registers hold them without spills.  D = 128, 48
+  // requests of up to 32 rows and 2000 keys: two passes of two 69 us (q8) and 62
+  // (fp8 / 4-bit), one of four 83 and 75; D = 64, of 32 rows 46 and 45, one of four 56
+  // and 51; D = 256, of 12 rows: two passes of one 64 and 64, one of two 73 and 69.
+  if (D == 256 || s.few_rows <= 8)
     return f8v4 ? launch_shared_rows_t<D, BS, true, 1>(s, stream)
                 : launch_shared_rows_t<D, BS, false, 1>(s, stream);
-  if (s.few_rows <= 16 || D == 256 || (D == 128 && s.few_rows <= 24))
+  if constexpr (D != 256)
     return f8v4 ? launch_shared_rows_t<D, BS, true, 2>(s, stream)
                 : launch_shared_rows_t<D, BS, false, 2>(s, stream);
-  if constexpr (D != 256)
-    return f8v4 ? launch_shared_rows_t<D, BS, true, 4>(s, stream)
-                : launch_shared_rows_t<D, BS, false, 4>(s, stream);
   return cudaErrorInvalidValue;
 }
 
