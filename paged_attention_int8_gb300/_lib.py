@@ -302,6 +302,22 @@ def kv_store_f8v4(key, value, slot_mapping, k_cache, v_cache, v_scale, v_zero, s
     _raise_if(st)
 
 
+def _table_layout(block_table):
+    """Rows, columns and row stride of a block table [S, max_blocks].  The strides
+    of a dimension of size one mean nothing: a single row counts as contiguous."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [S, max_blocks]")
+    rows, columns = block_table.shape
+    row, column = block_table.stride()
+    if column != 1 and columns > 1:
+        raise ValueError("block_table must be [S, max_blocks] with unit column stride")
+    if rows <= 1:
+        return rows, columns, columns
+    if row < columns:
+        raise ValueError("the rows of block_table overlap")
+    return rows, columns, row
+
+
 def paged_attention_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q, seq_lens,
                          block_table, max_query_len: int, max_seq_len: int,
                          softmax_scale: float | None = None, num_splits: int = 0, out=None,
@@ -319,14 +335,13 @@ def paged_attention_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q, seq
                     ("block_table", block_table)):
         if t.dtype != torch.int32:
             raise TypeError(f"{name} must be int32")
-    if block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise ValueError("block_table must be [S, max_blocks] with unit column stride")
+    rows, _, table_stride = _table_layout(block_table)
     T, hq, d = q.shape
     num_blocks, hk, bs, d2 = k_cache.shape
     if d2 != d:
         raise ValueError("cache shape mismatch")
     S = seq_lens.shape[0]
-    if cu_seqlens_q.shape != (S + 1,) or block_table.shape[0] != S:
+    if cu_seqlens_q.shape != (S + 1,) or rows != S:
         raise ValueError("metadata shapes disagree with seq_lens")
     if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (hq,)):
         raise TypeError("sinks must be an fp32 tensor [num_q_heads]")
@@ -344,7 +359,7 @@ def paged_attention_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q, seq
     with torch.cuda.device(device):
         st = lib.pa_paged_attention_f8v4(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(v_scale), _ptr(v_zero),
-            _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(block_table), block_table.stride(0), S, T,
+            _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(block_table), table_stride, S, T,
             hq, hk, d, num_blocks, bs, int(max_query_len), int(max_seq_len),
             float(softmax_scale), int(num_splits), _ptr(sinks), int(sliding_window), _ptr(out),
             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), flags,
@@ -381,7 +396,7 @@ def paged_attention(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
     least ``workspace_size(S, Hq, D, num_splits)`` bytes whose first 4 bytes
     are zero (the device status word); allocated zeroed when omitted."""
     device = _check_cuda(q, workspace, sinks)
-    T, hq, d, num_blocks, hk, bs, S, softmax_scale, out, lse = _attention_args(
+    T, hq, d, num_blocks, hk, bs, S, table_stride, softmax_scale, out, lse = _attention_args(
         q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
         softmax_scale, out, lse, return_lse)
     if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (hq,)
@@ -395,7 +410,7 @@ def paged_attention(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
     with torch.cuda.device(device):
         st = lib.pa_paged_attention_ex(
             _ptr(q), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
-            _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(block_table), block_table.stride(0), S, T,
+            _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(block_table), table_stride, S, T,
             hq, hk, d, num_blocks, bs, int(max_query_len), int(max_seq_len),
             float(softmax_scale), int(num_splits), _ptr(sinks), int(sliding_window), _ptr(out),
             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), flags,
@@ -415,7 +430,7 @@ def paged_attention_noalloc(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q,
     call's device status bits.  ``out`` / ``lse``, when omitted, are
     allocated here by PyTorch (the library itself allocates nothing)."""
     device = _check_cuda(q, status)
-    T, hq, d, num_blocks, hk, bs, S, softmax_scale, out, lse = _attention_args(
+    T, hq, d, num_blocks, hk, bs, S, table_stride, softmax_scale, out, lse = _attention_args(
         q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
         softmax_scale, out, lse, return_lse)
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
@@ -423,7 +438,7 @@ def paged_attention_noalloc(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q,
     with torch.cuda.device(device):
         st = load().pa_paged_attention_noalloc(
             _ptr(q), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
-            _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(block_table), block_table.stride(0), S, T,
+            _ptr(cu_seqlens_q), _ptr(seq_lens), _ptr(block_table), table_stride, S, T,
             hq, hk, d, num_blocks, bs, int(max_query_len), int(max_seq_len),
             float(softmax_scale), int(num_splits), _ptr(out), _ptr(lse), _ptr(status),
             _stream(stream, device))
@@ -445,8 +460,7 @@ def _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
             raise TypeError(f"{name} must be int32")
     if not (cu_seqlens_q.is_contiguous() and seq_lens.is_contiguous()):
         raise ValueError("cu_seqlens_q and seq_lens must be contiguous")
-    if block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise ValueError("block_table must be [S, max_blocks] with unit column stride")
+    rows, _, table_stride = _table_layout(block_table)
     _check16("k_scale", k_scale)
     _check16("v_scale", v_scale)
     T, hq, d = q.shape
@@ -455,7 +469,7 @@ def _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
         raise ValueError("cache shape mismatch")
     _check_cache_shapes(k_cache, k_scale, v_cache, v_scale)
     S = seq_lens.shape[0]
-    if cu_seqlens_q.shape != (S + 1,) or block_table.shape[0] != S:
+    if cu_seqlens_q.shape != (S + 1,) or rows != S:
         raise ValueError("metadata shapes disagree with seq_lens")
     if softmax_scale is None:
         softmax_scale = d ** -0.5
@@ -463,7 +477,7 @@ def _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-    return T, hq, d, num_blocks, hk, bs, S, softmax_scale, out, lse
+    return T, hq, d, num_blocks, hk, bs, S, table_stride, softmax_scale, out, lse
 
 
 def merge_attn_states(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None,
@@ -720,11 +734,9 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
             _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens,
                     cu_groups=cu_groups, prefix_lens=prefix_lens)
     s, g = seq_lens.numel(), prefix_lens.numel()
-    rows, _ = block_table.shape
     if block_table.dtype is not _I32 or block_table.get_device() != dev:
         raise TypeError("block_table must be an int32 CUDA tensor on q's device")
-    if block_table.stride(1) != 1:
-        raise ValueError("block_table must be [S, max_blocks] with unit column stride")
+    rows, _, table_stride = _table_layout(block_table)
     if cu_seqlens_q.numel() != s + 1 or rows != s or cu_groups.numel() != g + 1:
         raise ValueError("cu_seqlens_q [S + 1], block_table [S, ...] and cu_groups [G + 1] are wanted")
     if sinks is not None:
@@ -760,7 +772,7 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
     a, b, c, e = cache
     _call(fn, dev, stream, q.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), e.data_ptr(),
           cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-          block_table.stride(0), cu_groups.data_ptr(), prefix_lens.data_ptr(), g, s, t, hq, hk, d,
+          table_stride, cu_groups.data_ptr(), prefix_lens.data_ptr(), g, s, t, hq, hk, d,
           nb, bs, max_query_len, max_prefix_len, max_suffix_len,
           d ** -0.5 if softmax_scale is None else softmax_scale,
           None if sinks is None else sinks.data_ptr(), out.data_ptr(),

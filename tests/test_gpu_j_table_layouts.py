@@ -1,0 +1,63 @@
+"""Block tables in the layouts that a caller's tensors take: one row of any strides,
+one column, a slice of a wider table."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from paged_attention_int8_gb300 import _lib
+from tests import _shared as S
+
+pytestmark = pytest.mark.gpu
+
+
+def _calls(b):
+    """Every attention binding of the batch's format over its table."""
+    longest = max(b.seq_lens)
+    if b.fmt == "q8":
+        yield lambda: _lib.paged_attention(b.q, *b.cache, b.cu, b.lens, b.table, max(b.q_lens),
+                                           longest)
+        yield lambda: _lib.paged_attention_noalloc(b.q, *b.cache, b.cu, b.lens, b.table,
+                                                   max(b.q_lens), longest)
+    else:
+        yield lambda: _lib.paged_attention_f8v4(b.q, *b.cache, b.cu, b.lens, b.table,
+                                                max(b.q_lens), longest)
+    yield b.call
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8v4"])
+def test_one_row_of_any_strides(cuda_device, fmt):
+    """A table of one row made by a transpose: torch gives its rows a stride of one
+    and calls it contiguous."""
+    b = S.make(81, cuda_device, fmt, 8, 2, 128, 16, [(70, [(1, 45)])])
+    ref = S.reference(b)
+    column = b.table.reshape(-1, 1).contiguous()
+    b.table = column.t()
+    assert b.table.stride() == (1, 1) and b.table.shape[1] > 1 and b.table.is_contiguous()
+    for call in _calls(b):
+        S.check(b, *call(), ref=ref)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8v4"])
+def test_one_column_of_any_strides(cuda_device, fmt):
+    """Short sequences, a page each, their column taken from a transposed row."""
+    b = S.make(82, cuda_device, fmt, 8, 2, 128, 16, [(0, [(1, 9), (1, 16), (1, 3)])], columns=0)
+    ref = S.reference(b)
+    assert b.table.shape[1] == 1
+    b.table = b.table.reshape(1, -1).contiguous().t()
+    assert b.table.stride() == (1, 3)
+    for call in _calls(b):
+        S.check(b, *call(), ref=ref)
+
+
+def test_tables_that_are_refused(cuda_device):
+    b = S.make(83, cuda_device, "q8", 8, 2, 128, 16, [(20, [(1, 5), (1, 30)])])
+    good = b.table
+    for table in (good.t().contiguous().t(),             # the columns apart
+                  good[:1].expand(2, -1),                # one row for both
+                  good.as_strided((2, good.shape[1]), (1, 1)),
+                  good.reshape(-1)):
+        b.table = table
+        for call in _calls(b):
+            with pytest.raises(ValueError):
+                call()
