@@ -475,9 +475,9 @@ size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int
  * Other arguments as pa_paged_attention_ex.  A sequence whose seq_len - q_len
  * is below its prefix, that no group holds, or whose metadata is out of range
  * is not written and flagged PA_DEV_BAD_SEQ; rows of tokens no sequence owns
- * are not written.  Keys past the table's columns are flagged PA_DEV_BAD_BLOCK
- * and left out.  Numerics as pa_paged_attention_ex; the parts are joined in
- * fp32.  Asynchronous.
+ * are not written.  Keys past the table's columns (block_table_stride of them)
+ * are flagged PA_DEV_BAD_BLOCK and left out.  Numerics as pa_paged_attention_ex;
+ * the parts are joined in fp32.  Asynchronous.
  */
 pa_status pa_paged_attention_shared_prefix(
     const void *q, const void *k_cache, const void *k_scale, const void *v_cache,
@@ -499,6 +499,31 @@ pa_status pa_paged_attention_shared_prefix_f8v4(
     int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
     float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
     size_t workspace_bytes, uint32_t flags, void *stream);
+
+/*
+ * The two over a block table whose rows are longer than the columns that belong
+ * to it (the first pages of a wider table): rows block_table_stride apart, of
+ * which block_table_columns entries are read.
+ */
+pa_status pa_paged_attention_shared_prefix_view(
+    const void *q, const void *k_cache, const void *k_scale, const void *v_cache,
+    const void *v_scale, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, int32_t block_table_columns,
+    const int32_t *cu_groups, const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs,
+    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t num_blocks, int32_t block_size, int32_t max_query_len, int32_t max_prefix_len,
+    int32_t max_suffix_len, float softmax_scale, const float *sinks, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, uint32_t flags, void *stream);
+
+pa_status pa_paged_attention_shared_prefix_f8v4_view(
+    const void *q, const void *k_cache, const void *v_cache, const void *v_scale,
+    const void *v_zero, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, int32_t block_table_columns,
+    const int32_t *cu_groups, const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs,
+    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t num_blocks, int32_t block_size, int32_t max_query_len, int32_t max_prefix_len,
+    int32_t max_suffix_len, float softmax_scale, const float *sinks, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, uint32_t flags, void *stream);
 
 /*
  * Synchronizes `stream`, reads the device status word at `status` (a kv_store

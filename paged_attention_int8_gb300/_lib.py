@@ -105,8 +105,11 @@ def load():
             fn.restype = ctypes.c_int
         lib.pa_shared_prefix_workspace_size.argtypes = [i32] * 9
         lib.pa_shared_prefix_workspace_size.restype = ctypes.c_size_t
-        for fn in (lib.pa_paged_attention_shared_prefix, lib.pa_paged_attention_shared_prefix_f8v4):
-            fn.argtypes = [P] * 8 + [i32, P, P] + [i32] * 11 + [
+        for fn, table in ((lib.pa_paged_attention_shared_prefix, [i32]),
+                          (lib.pa_paged_attention_shared_prefix_f8v4, [i32]),
+                          (lib.pa_paged_attention_shared_prefix_view, [i32, i32]),
+                          (lib.pa_paged_attention_shared_prefix_f8v4_view, [i32, i32])):
+            fn.argtypes = [P] * 8 + table + [P, P] + [i32] * 11 + [
                 ctypes.c_float, P, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
             fn.restype = ctypes.c_int
         lib.pa_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
@@ -736,7 +739,7 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
     s, g = seq_lens.numel(), prefix_lens.numel()
     if block_table.dtype is not _I32 or block_table.get_device() != dev:
         raise TypeError("block_table must be an int32 CUDA tensor on q's device")
-    rows, _, table_stride = _table_layout(block_table)
+    rows, columns, table_stride = _table_layout(block_table)
     if cu_seqlens_q.numel() != s + 1 or rows != s or cu_groups.numel() != g + 1:
         raise ValueError("cu_seqlens_q [S + 1], block_table [S, ...] and cu_groups [G + 1] are wanted")
     if sinks is not None:
@@ -772,7 +775,7 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
     a, b, c, e = cache
     _call(fn, dev, stream, q.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), e.data_ptr(),
           cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-          table_stride, cu_groups.data_ptr(), prefix_lens.data_ptr(), g, s, t, hq, hk, d,
+          table_stride, columns, cu_groups.data_ptr(), prefix_lens.data_ptr(), g, s, t, hq, hk, d,
           nb, bs, max_query_len, max_prefix_len, max_suffix_len,
           d ** -0.5 if softmax_scale is None else softmax_scale,
           None if sinks is None else sinks.data_ptr(), out.data_ptr(),
@@ -800,7 +803,7 @@ def paged_attention_shared_prefix(q, k_cache, k_scale, v_cache, v_scale, cu_seql
     ``workspace``: uint8 CUDA tensor of ``shared_prefix_workspace_size``
     bytes, its first 4 bytes zero (the device status word); allocated when
     omitted.  Other arguments and results as paged_attention."""
-    return _shared_prefix((_lib or load()).pa_paged_attention_shared_prefix, _q8_cache, q,
+    return _shared_prefix((_lib or load()).pa_paged_attention_shared_prefix_view, _q8_cache, q,
                           (k_cache, k_scale, v_cache, v_scale), cu_seqlens_q, seq_lens,
                           block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
                           max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
@@ -815,8 +818,8 @@ def paged_attention_shared_prefix_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_
                                        return_lse: bool = True):
     """paged_attention_shared_prefix over the fp8 / 4-bit format
     (pa_paged_attention_shared_prefix_f8v4)."""
-    return _shared_prefix((_lib or load()).pa_paged_attention_shared_prefix_f8v4, _f8v4_cache, q,
-                          (k_cache, v_cache, v_scale, v_zero), cu_seqlens_q, seq_lens,
+    return _shared_prefix((_lib or load()).pa_paged_attention_shared_prefix_f8v4_view,
+                          _f8v4_cache, q, (k_cache, v_cache, v_scale, v_zero), cu_seqlens_q, seq_lens,
                           block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
                           max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
                           return_lse)

@@ -494,8 +494,9 @@ pa_status shared_prefix(paq8::SharedLaunch &L, void *workspace, size_t workspace
   if (L.hq / L.hk > 16) return fail(PA_ERR_UNSUPPORTED, "more than 16 q heads per kv head");
   if (!supported_dim(L.d)) return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
   if (!supported_bs(L.bs)) return fail(PA_ERR_UNSUPPORTED, "block_size must be 16 or 32");
-  if (L.num_blocks <= 0 || L.bt_stride <= 0)
-    return fail(PA_ERR_INVALID_ARG, "num_blocks and block_table_stride must be positive");
+  if (L.num_blocks <= 0 || L.bt_cols <= 0 || L.bt_stride < L.bt_cols)
+    return fail(PA_ERR_INVALID_ARG, "num_blocks and the block table's columns must be positive, its "
+                                    "row stride no less than them");
   if (static_cast<int64_t>(L.num_blocks) * L.hk * L.d >= (int64_t{1} << 31))
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * head_dim must be < 2^31");
   if (L.hk > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 kv heads");
@@ -652,6 +653,44 @@ size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int
   return shared_bytes(num_tokens, num_q_heads, head_dim, n.prefix + n.suffix);
 }
 
+pa_status pa_paged_attention_shared_prefix_view(
+    const void *q, const void *k_cache, const void *k_scale, const void *v_cache,
+    const void *v_scale, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, int32_t block_table_columns,
+    const int32_t *cu_groups, const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs,
+    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t num_blocks, int32_t block_size, int32_t max_query_len, int32_t max_prefix_len,
+    int32_t max_suffix_len, float softmax_scale, const float *sinks, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, uint32_t flags, void *stream) {
+  g_last_error[0] = '\0';
+  paq8::SharedLaunch L = {q, k_cache, k_scale, v_cache, v_scale, nullptr, cu_seqlens_q, seq_lens,
+                          block_table, cu_groups, prefix_lens, block_table_stride,
+                          block_table_columns, num_seqs, num_tokens, num_groups, num_q_heads,
+                          num_kv_heads, head_dim, num_blocks, block_size, max_query_len,
+                          max_prefix_len, max_suffix_len, 1, 1, softmax_scale, sinks, out, lse,
+                          nullptr, false};
+  return shared_prefix(L, workspace, workspace_bytes, flags, stream);
+}
+
+pa_status pa_paged_attention_shared_prefix_f8v4_view(
+    const void *q, const void *k_cache, const void *v_cache, const void *v_scale,
+    const void *v_zero, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+    const int32_t *block_table, int32_t block_table_stride, int32_t block_table_columns,
+    const int32_t *cu_groups, const int32_t *prefix_lens, int32_t num_groups, int32_t num_seqs,
+    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t num_blocks, int32_t block_size, int32_t max_query_len, int32_t max_prefix_len,
+    int32_t max_suffix_len, float softmax_scale, const float *sinks, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, uint32_t flags, void *stream) {
+  g_last_error[0] = '\0';
+  paq8::SharedLaunch L = {q, k_cache, v_zero, v_cache, v_scale, v_zero, cu_seqlens_q, seq_lens,
+                          block_table, cu_groups, prefix_lens, block_table_stride,
+                          block_table_columns, num_seqs, num_tokens, num_groups, num_q_heads,
+                          num_kv_heads, head_dim, num_blocks, block_size, max_query_len,
+                          max_prefix_len, max_suffix_len, 1, 1, softmax_scale, sinks, out, lse,
+                          nullptr, true};
+  return shared_prefix(L, workspace, workspace_bytes, flags, stream);
+}
+
 pa_status pa_paged_attention_shared_prefix(
     const void *q, const void *k_cache, const void *k_scale, const void *v_cache,
     const void *v_scale, const int32_t *cu_seqlens_q, const int32_t *seq_lens,
@@ -661,13 +700,11 @@ pa_status pa_paged_attention_shared_prefix(
     int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
     float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
     size_t workspace_bytes, uint32_t flags, void *stream) {
-  g_last_error[0] = '\0';
-  paq8::SharedLaunch L = {q, k_cache, k_scale, v_cache, v_scale, nullptr, cu_seqlens_q, seq_lens,
-                          block_table, cu_groups, prefix_lens, block_table_stride, num_seqs,
-                          num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim, num_blocks,
-                          block_size, max_query_len, max_prefix_len, max_suffix_len, 1, 1,
-                          softmax_scale, sinks, out, lse, nullptr, false};
-  return shared_prefix(L, workspace, workspace_bytes, flags, stream);
+  return pa_paged_attention_shared_prefix_view(
+      q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table, block_table_stride,
+      block_table_stride, cu_groups, prefix_lens, num_groups, num_seqs, num_tokens, num_q_heads,
+      num_kv_heads, head_dim, num_blocks, block_size, max_query_len, max_prefix_len,
+      max_suffix_len, softmax_scale, sinks, out, lse, workspace, workspace_bytes, flags, stream);
 }
 
 pa_status pa_paged_attention_shared_prefix_f8v4(
@@ -679,13 +716,11 @@ pa_status pa_paged_attention_shared_prefix_f8v4(
     int32_t block_size, int32_t max_query_len, int32_t max_prefix_len, int32_t max_suffix_len,
     float softmax_scale, const float *sinks, void *out, float *lse, void *workspace,
     size_t workspace_bytes, uint32_t flags, void *stream) {
-  g_last_error[0] = '\0';
-  paq8::SharedLaunch L = {q, k_cache, v_zero, v_cache, v_scale, v_zero, cu_seqlens_q, seq_lens,
-                          block_table, cu_groups, prefix_lens, block_table_stride, num_seqs,
-                          num_tokens, num_groups, num_q_heads, num_kv_heads, head_dim, num_blocks,
-                          block_size, max_query_len, max_prefix_len, max_suffix_len, 1, 1,
-                          softmax_scale, sinks, out, lse, nullptr, true};
-  return shared_prefix(L, workspace, workspace_bytes, flags, stream);
+  return pa_paged_attention_shared_prefix_f8v4_view(
+      q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q, seq_lens, block_table, block_table_stride,
+      block_table_stride, cu_groups, prefix_lens, num_groups, num_seqs, num_tokens, num_q_heads,
+      num_kv_heads, head_dim, num_blocks, block_size, max_query_len, max_prefix_len,
+      max_suffix_len, softmax_scale, sinks, out, lse, workspace, workspace_bytes, flags, stream);
 }
 
 }  // extern "C"

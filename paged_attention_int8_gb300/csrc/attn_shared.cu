@@ -679,6 +679,7 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   a.qpk = L.hq / L.hk;
   a.num_blocks = L.num_blocks;
   a.bt_stride = L.bt_stride;
+  a.bt_cols = L.bt_cols;
   a.scale_log2 = L.softmax_scale * kLog2e;
   a.causal = 1;
   a.sinks = L.sinks;
@@ -690,7 +691,7 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   s.cu_groups = L.cu_groups;
   s.prefix_lens = L.prefix_lens;
   s.num_groups = L.num_groups;
-  s.capacity = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(L.bt_stride) * L.bs, 0x7fffffff - 4096));
+  s.capacity = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(L.bt_cols) * L.bs, 0x7fffffff - 4096));
   s.ns_p = L.prefix_splits;
   s.ns_s = L.suffix_splits;
   auto seg = [](int len, int ns) { return std::max(1, ((len + kTile - 1) / kTile + ns - 1) / ns); };

@@ -45,7 +45,7 @@ cudaError_t launch_copy_blocks(const BlockCopy &p, cudaStream_t stream);
 struct SharedLaunch {
   const void *q, *k_cache, *k_scale, *v_cache, *v_scale, *v_zero;
   const int32_t *cu, *seq_lens, *block_table, *cu_groups, *prefix_lens;
-  int32_t bt_stride, num_seqs, num_tokens, num_groups, hq, hk, d, num_blocks, bs;
+  int32_t bt_stride, bt_cols, num_seqs, num_tokens, num_groups, hq, hk, d, num_blocks, bs;
   int32_t max_query_len, max_prefix_len, max_suffix_len;
   int32_t prefix_splits, suffix_splits;
   float softmax_scale;

@@ -61,3 +61,33 @@ def test_tables_that_are_refused(cuda_device):
         for call in _calls(b):
             with pytest.raises(ValueError):
                 call()
+
+
+@pytest.mark.parametrize("fmt,d,hq,hk,n,q_len", [("q8", 128, 8, 2, 3, 1), ("q8", 256, 16, 2, 12, 1),
+                                                 ("f8v4", 64, 4, 2, 3, 3), ("q8", 128, 16, 1, 20, 2),
+                                                 ("q8", 128, 8, 2, 3, 20)])
+def test_slice_of_a_wider_table(cuda_device, fmt, d, hq, hk, n, q_len):
+    """The columns of a slice end where the slice does: keys past them are flagged and
+    left out, though the wider table has entries there; the other rows are right."""
+    b = S.make(84, cuda_device, fmt, hq, hk, d, 16, [(40, [(q_len, 30)] * n)], columns=0)
+    ref = S.reference(b)
+    columns = b.table.shape[1]
+    wide = torch.zeros((n, columns + 9), dtype=torch.int32, device=cuda_device)
+    wide[:, 4:4 + columns] = b.table
+    b.table = wide[:, 4:4 + columns]
+    S.check(b, *b.call(), ref=ref)
+    lens = b.lens.clone()
+    lens[1] = (columns + 3) * 16
+    fn = (_lib.paged_attention_shared_prefix if fmt == "q8"
+          else _lib.paged_attention_shared_prefix_f8v4)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_device)
+    out = torch.full_like(b.q, float("nan"))
+    lse = torch.full(b.q.shape[:2], float("nan"), device=cuda_device)
+    fn(b.q, *b.cache, b.cu, lens, b.table, b.groups, b.prefixes, *b.bounds, out=out, lse=lse,
+       workspace=ws)
+    with pytest.raises(_lib.PagedAttentionError) as err:
+        _lib.check_status(ws)
+    assert err.value.bits == _lib.DEV_BAD_BLOCK
+    for t in (out, lse):  # the over-long sequence: any row, for the comparison of the others
+        t[q_len:2 * q_len] = ref[0 if t is out else 1][q_len:2 * q_len].to(t)
+    S.check(b, out, lse, ref=ref)

@@ -1,9 +1,17 @@
 """Argument checks of the attention and serving calls on the edges of their sizes and
 layouts, without a GPU."""
+import ctypes
+
 import pytest
 import torch
 
-from paged_attention_int8_gb300 import _lib
+from paged_attention_int8_gb300 import _lib, build as pkg_build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pkg_build.build()
+    return _lib.load()
 
 
 def test_table_layouts():
@@ -17,3 +25,17 @@ def test_table_layouts():
     for bad in (t.t(), t[:1].expand(3, -1), t[:, ::2], t.as_strided((2, 8), (4, 1)), t[0]):
         with pytest.raises(ValueError):
             layout(bad)
+
+
+VIEW = dict(q=16, kc=16, ks=16, vc=16, vs=16, cu=16, sl=16, bt=16, bts=8, cols=5, groups=16,
+            prefix=16, G=1, S=2, T=2, hq=8, hk=2, d=128, nb=16, bs=16, mq=1, mp=100, ms=10,
+            scale=ctypes.c_float(0.1), sinks=None, out=16, lse=16, ws=16, wsb=1 << 20, flags=0,
+            stream=None)
+
+
+@pytest.mark.parametrize("kw", [dict(cols=0), dict(cols=-3), dict(cols=9), dict(bts=4), dict(bts=0)])
+def test_views_whose_columns_do_not_fit_their_rows(lib, kw):
+    for fn in (lib.pa_paged_attention_shared_prefix_view,
+               lib.pa_paged_attention_shared_prefix_f8v4_view):
+        assert fn(*{**VIEW, **kw}.values()) == _lib.Status.INVALID_ARG
+        assert "columns" in lib.pa_last_error().decode()
