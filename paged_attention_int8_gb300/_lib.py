@@ -321,6 +321,17 @@ def _table_layout(block_table):
     return rows, columns, row
 
 
+def _table_in_bounds(block_table, rows, stride, stream):
+    """The table, and its row stride, of a call whose kernels look up to `stride`
+    entries into each row: where the last row of a view (one that starts past the
+    first column) would pass the end of its memory, whole rows of its own."""
+    if (block_table.storage_offset() + rows * stride) * 4 <= block_table.untyped_storage().nbytes():
+        return block_table, stride
+    with _allocating(stream):
+        block_table = block_table.contiguous()
+    return block_table, block_table.shape[1]
+
+
 def paged_attention_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q, seq_lens,
                          block_table, max_query_len: int, max_seq_len: int,
                          softmax_scale: float | None = None, num_splits: int = 0, out=None,
@@ -338,7 +349,9 @@ def paged_attention_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_seqlens_q, seq
                     ("block_table", block_table)):
         if t.dtype != torch.int32:
             raise TypeError(f"{name} must be int32")
-    rows, _, table_stride = _table_layout(block_table)
+    rows, columns, table_stride = _table_layout(block_table)
+    if table_stride > columns:
+        block_table, table_stride = _table_in_bounds(block_table, rows, table_stride, stream)
     T, hq, d = q.shape
     num_blocks, hk, bs, d2 = k_cache.shape
     if d2 != d:
@@ -399,9 +412,9 @@ def paged_attention(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
     least ``workspace_size(S, Hq, D, num_splits)`` bytes whose first 4 bytes
     are zero (the device status word); allocated zeroed when omitted."""
     device = _check_cuda(q, workspace, sinks)
-    T, hq, d, num_blocks, hk, bs, S, table_stride, softmax_scale, out, lse = _attention_args(
-        q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
-        softmax_scale, out, lse, return_lse)
+    (T, hq, d, num_blocks, hk, bs, S, block_table, table_stride, softmax_scale, out,
+     lse) = _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens,
+                            block_table, softmax_scale, out, lse, return_lse, stream)
     if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (hq,)
                               or not sinks.is_contiguous()):
         raise TypeError("sinks must be a contiguous fp32 tensor [num_q_heads]")
@@ -433,9 +446,9 @@ def paged_attention_noalloc(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q,
     call's device status bits.  ``out`` / ``lse``, when omitted, are
     allocated here by PyTorch (the library itself allocates nothing)."""
     device = _check_cuda(q, status)
-    T, hq, d, num_blocks, hk, bs, S, table_stride, softmax_scale, out, lse = _attention_args(
-        q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
-        softmax_scale, out, lse, return_lse)
+    (T, hq, d, num_blocks, hk, bs, S, block_table, table_stride, softmax_scale, out,
+     lse) = _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens,
+                            block_table, softmax_scale, out, lse, return_lse, stream)
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise TypeError("status must be an int32 tensor")
     with torch.cuda.device(device):
@@ -450,7 +463,7 @@ def paged_attention_noalloc(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q,
 
 
 def _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens,
-                    block_table, softmax_scale, out, lse, return_lse):
+                    block_table, softmax_scale, out, lse, return_lse, stream):
     """Shared checks of the attention entry points; allocates out / lse when
     omitted."""
     _check_cuda(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
@@ -463,7 +476,9 @@ def _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
             raise TypeError(f"{name} must be int32")
     if not (cu_seqlens_q.is_contiguous() and seq_lens.is_contiguous()):
         raise ValueError("cu_seqlens_q and seq_lens must be contiguous")
-    rows, _, table_stride = _table_layout(block_table)
+    rows, columns, table_stride = _table_layout(block_table)
+    if table_stride > columns:
+        block_table, table_stride = _table_in_bounds(block_table, rows, table_stride, stream)
     _check16("k_scale", k_scale)
     _check16("v_scale", v_scale)
     T, hq, d = q.shape
@@ -480,7 +495,8 @@ def _attention_args(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_len
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-    return T, hq, d, num_blocks, hk, bs, S, table_stride, softmax_scale, out, lse
+    return (T, hq, d, num_blocks, hk, bs, S, block_table, table_stride, softmax_scale, out,
+            lse)
 
 
 def merge_attn_states(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=None,

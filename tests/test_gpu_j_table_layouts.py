@@ -91,3 +91,22 @@ def test_slice_of_a_wider_table(cuda_device, fmt, d, hq, hk, n, q_len):
     for t in (out, lse):  # the over-long sequence: any row, for the comparison of the others
         t[q_len:2 * q_len] = ref[0 if t is out else 1][q_len:2 * q_len].to(t)
     S.check(b, out, lse, ref=ref)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8v4"])
+def test_last_columns_of_a_wider_table(cuda_device, fmt):
+    """A slice whose last row ends with the memory, on the current stream and on
+    another."""
+    b = S.make(85, cuda_device, fmt, 8, 2, 128, 16, [(40, [(1, 30), (1, 9), (1, 33)])], columns=0)
+    ref = S.reference(b)
+    wide = torch.zeros((3, b.table.shape[1] + 9), dtype=torch.int32, device=cuda_device)
+    wide[:, 9:] = b.table
+    b.table = wide[:, 9:]
+    for call in _calls(b):
+        S.check(b, *call(), ref=ref)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call = _lib.paged_attention if fmt == "q8" else _lib.paged_attention_f8v4
+    out, lse = call(b.q, *b.cache, b.cu, b.lens, b.table, 1, max(b.seq_lens), stream=side)
+    side.synchronize()
+    S.check(b, out, lse, ref=ref)

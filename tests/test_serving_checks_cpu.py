@@ -39,3 +39,16 @@ def test_views_whose_columns_do_not_fit_their_rows(lib, kw):
                lib.pa_paged_attention_shared_prefix_f8v4_view):
         assert fn(*{**VIEW, **kw}.values()) == _lib.Status.INVALID_ARG
         assert "columns" in lib.pa_last_error().decode()
+
+
+def test_rows_that_would_pass_the_end_of_their_memory():
+    """The entries that a call may look up in a view of a wider table all stand in its
+    memory: the view's own, or a copy's."""
+    wide = torch.arange(24, dtype=torch.int32).reshape(3, 8)
+    for view, copied in ((wide[:, :5], False), (wide[:2, 3:], False), (wide[:, 3:], True),
+                         (wide[1:, 7:], True), (wide[1:2], False)):
+        rows, columns, stride = _lib._table_layout(view)
+        got, got_stride = _lib._table_in_bounds(view, rows, stride, None)
+        assert torch.equal(got, view) and (got.data_ptr() != view.data_ptr()) == copied
+        assert got_stride == (columns if copied else stride)
+        assert got.storage_offset() + rows * got_stride <= got.untyped_storage().nbytes() // 4
