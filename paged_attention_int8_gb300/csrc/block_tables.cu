@@ -13,11 +13,11 @@
 //
 // A block takes 8 sequences (one warp each) and one chunk of their tokens and
 // pages (grid y), so that a long prompt or a wide table row is spread over
-// blocks.  The sums over earlier sequences are formed by every block that
-// needs them, straight from the lengths (12 bytes a sequence, L2 resident):
-// one launch, no scan across blocks, no order that could change results.  A
-// block whose chunk holds neither tokens nor new pages copies old entries only
-// and takes no sum.
+// blocks; every grid-y-th chunk where one each would be more than kMaxBlocks.
+// The sums over earlier sequences are formed by every block that needs them,
+// straight from the lengths (12 bytes a sequence, L2 resident): one launch, no
+// scan across blocks, no order that could change results.  A block whose chunk
+// holds neither tokens nor new pages copies old entries only and takes no sum.
 #include "common.cuh"
 #include "launch.h"
 #include "programmatic.cuh"
@@ -30,6 +30,7 @@ namespace {
 constexpr int kWarps = 8;          // sequences per block
 constexpr int kTokenChunk = 256;   // tokens of a sequence per block
 constexpr int kPageChunk = 1024;   // pages of a sequence per block
+constexpr int kMaxBlocks = 65535;  // about; grid y has no more rows
 
 struct SeqPlan {
   int ctx, q, first, end;  // pages [first, end) are new
@@ -62,19 +63,20 @@ __global__ void __launch_bounds__(kWarps * 32) block_tables_kernel(const BlockTa
   const int s0 = static_cast<int>(blockIdx.x) * kWarps;
   const int s = s0 + warp;
   const bool last_x = blockIdx.x == gridDim.x - 1;
-  const int chunk = static_cast<int>(blockIdx.y);
+  const int y = static_cast<int>(blockIdx.y), dy = static_cast<int>(gridDim.y);
   const bool active = s < p.num_seqs;
 
   wait_for_predecessor();  // the lengths, and every reader of what is written here
   SeqPlan me = {0, 0, 0, 0, false, true};
   if (active) me = plan_of(p, s);
   const int n_new = me.end - me.first;  // 0 when q == 0: end == held == first
-  const int64_t tok_lo = static_cast<int64_t>(chunk) * kTokenChunk;
-  const int64_t page_lo = static_cast<int64_t>(chunk) * kPageChunk;
+  // chunks of this sequence's tokens and table entries; the block's are y, y + dy, ...
+  const int n_chunks = max(1, max((me.q + kTokenChunk - 1) / kTokenChunk,
+                                  (min(me.end, p.table_stride) + kPageChunk - 1) / kPageChunk));
   // the sums are needed for the heads of the arrays (chunk 0), for tokens and
-  // new pages of this chunk, and for the padding rows behind the last token
-  const bool need = chunk == 0 || last_x || tok_lo < me.q ||
-                    (page_lo < me.end && page_lo + kPageChunk > me.first);
+  // new pages of a chunk, and for the padding rows behind the last token
+  const bool need = y == 0 || last_x || y * kTokenChunk < me.q || y + dy < n_chunks ||
+                    (y * kPageChunk < me.end && (y + 1) * kPageChunk > me.first);
   int64_t before_q = 0, before_n = 0;
   int64_t total_q = 0, total_n = 0;
   if (__syncthreads_or(need)) {
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_tables_kernel(const BlockTa
       return b;
     };
 
-    if (chunk == 0 && lane == 0) {
+    if (y == 0 && lane == 0) {
       p.cu_seqlens_q[s] = clamp_i32(before_q);
       p.seq_lens[s] = me.ctx + me.q;
       if (me.end > p.table_stride) bad |= PA_DEV_BAD_BLOCK;
@@ -142,85 +144,90 @@ __global__ void __launch_bounds__(kWarps * 32) block_tables_kernel(const BlockTa
     // the pair comes from the block that owns the private page's entry (it is
     // replaced below, in place perhaps: read here before)
     const int pair_chunk = me.cow ? min(me.first, p.table_stride - 1) / kPageChunk : 0;
-    if (p.copy_pairs && chunk == pair_chunk && lane == 0) {
-      int from = -1, to = -1;
-      if (me.cow) {
-        from = old_entry(me.first);
-        to = me.first < p.table_stride ? new_entry(me.first) : -1;
-        if (from < 0 || from >= p.num_blocks) bad |= bad_old;
-        if (from < 0 || from >= p.num_blocks || to < 0) from = to = -1;
+    for (int chunk = y; chunk < n_chunks; chunk += dy) {
+      const int64_t tok_lo = static_cast<int64_t>(chunk) * kTokenChunk;
+      const int64_t page_lo = static_cast<int64_t>(chunk) * kPageChunk;
+      if (p.copy_pairs && chunk == pair_chunk && lane == 0) {
+        int from = -1, to = -1;
+        if (me.cow) {
+          from = old_entry(me.first);
+          to = me.first < p.table_stride ? new_entry(me.first) : -1;
+          if (from < 0 || from >= p.num_blocks) bad |= bad_old;
+          if (from < 0 || from >= p.num_blocks || to < 0) from = to = -1;
+        }
+        p.copy_pairs[2 * s] = from;
+        p.copy_pairs[2 * s + 1] = to;
       }
-      p.copy_pairs[2 * s] = from;
-      p.copy_pairs[2 * s + 1] = to;
-    }
-    __syncwarp();
+      __syncwarp();
 
-    // ---- table entries of this chunk
-    const int pl = static_cast<int>(min(page_lo, static_cast<int64_t>(me.end)));
-    const int ph = min(min(me.end, pl + kPageChunk), p.table_stride);
-    const bool in_place = dst == src;
-    const int split = max(pl, min(ph, me.first));  // old entries end here
-    if (!in_place) {
-      // entries that the source row has, a batch of loads ahead of their stores
-      const int have = row_ok ? max(pl, min(split, p.source_stride)) : pl;
-      const int n = have - pl;
-      constexpr int kBatch = 8;
-      int i = lane;
-      if (((reinterpret_cast<uintptr_t>(dst + pl) | reinterpret_cast<uintptr_t>(src + pl)) & 15u) == 0) {
-        const int4 *from = reinterpret_cast<const int4 *>(src + pl);
-        int4 *to = reinterpret_cast<int4 *>(dst + pl);
-        for (; i < n / 4; i += 32 * kBatch) {
-          int4 v[kBatch];
+      // ---- table entries of this chunk
+      const int pl = static_cast<int>(min(page_lo, static_cast<int64_t>(me.end)));
+      const int ph = min(min(me.end, pl + kPageChunk), p.table_stride);
+      const bool in_place = dst == src;
+      const int split = max(pl, min(ph, me.first));  // old entries end here
+      if (!in_place) {
+        // entries that the source row has, a batch of loads ahead of their stores
+        const int have = row_ok ? max(pl, min(split, p.source_stride)) : pl;
+        const int n = have - pl;
+        constexpr int kBatch = 8;
+        int i = lane;
+        if (((reinterpret_cast<uintptr_t>(dst + pl) | reinterpret_cast<uintptr_t>(src + pl)) & 15u) == 0) {
+          const int4 *from = reinterpret_cast<const int4 *>(src + pl);
+          int4 *to = reinterpret_cast<int4 *>(dst + pl);
+          for (; i < n / 4; i += 32 * kBatch) {
+            int4 v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+              if (i + 32 * j < n / 4) v[j] = from[i + 32 * j];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+              if (i + 32 * j < n / 4) to[i + 32 * j] = v[j];
+          }
+          i = (n & ~3) + lane;
+        }
+        for (; i < n; i += 32 * kBatch) {
+          int v[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j)
-            if (i + 32 * j < n / 4) v[j] = from[i + 32 * j];
+            if (i + 32 * j < n) v[j] = src[pl + i + 32 * j];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j)
-            if (i + 32 * j < n / 4) to[i + 32 * j] = v[j];
+            if (i + 32 * j < n) dst[pl + i + 32 * j] = v[j];
         }
-        i = (n & ~3) + lane;
+        for (int page = have + lane; page < split; page += 32) dst[page] = -1;
       }
-      for (; i < n; i += 32 * kBatch) {
-        int v[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (i + 32 * j < n) v[j] = src[pl + i + 32 * j];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (i + 32 * j < n) dst[pl + i + 32 * j] = v[j];
-      }
-      for (int page = have + lane; page < split; page += 32) dst[page] = -1;
-    }
-    for (int page = split + lane; page < ph; page += 32) dst[page] = new_entry(page);
+      for (int page = split + lane; page < ph; page += 32) dst[page] = new_entry(page);
 
-    // ---- slots and positions of this chunk
-    const int th = static_cast<int>(min(static_cast<int64_t>(me.q), tok_lo + kTokenChunk));
-    for (int i = static_cast<int>(min(tok_lo, static_cast<int64_t>(th))) + lane; i < th; i += 32) {
-      const int64_t t = before_q + i;
-      if (t >= p.num_tokens) break;  // flagged above
-      const int x = me.ctx + i;
-      const int page = x / p.block_size;
-      int b = -1;
-      if (page < p.table_stride) {
-        b = page < me.first ? old_entry(page) : new_entry(page);
-        if (page < me.first && (b < 0 || b >= p.num_blocks)) {
-          bad |= bad_old;
-          b = -1;
+      // ---- slots and positions of this chunk
+      const int th = static_cast<int>(min(static_cast<int64_t>(me.q), tok_lo + kTokenChunk));
+      for (int i = static_cast<int>(min(tok_lo, static_cast<int64_t>(th))) + lane; i < th; i += 32) {
+        const int64_t t = before_q + i;
+        if (t >= p.num_tokens) break;  // flagged above
+        const int x = me.ctx + i;
+        const int page = x / p.block_size;
+        int b = -1;
+        if (page < p.table_stride) {
+          b = page < me.first ? old_entry(page) : new_entry(page);
+          if (page < me.first && (b < 0 || b >= p.num_blocks)) {
+            bad |= bad_old;
+            b = -1;
+          }
         }
+        p.slot_mapping[t] =
+            b < 0 ? -1 : static_cast<int64_t>(b) * p.block_size + (x - page * p.block_size);
+        if (p.positions) p.positions[t] = x;
       }
-      p.slot_mapping[t] =
-          b < 0 ? -1 : static_cast<int64_t>(b) * p.block_size + (x - page * p.block_size);
-      if (p.positions) p.positions[t] = x;
     }
   }
   if (last_x) {
-    if (chunk == 0 && threadIdx.x == 0) {
+    if (y == 0 && threadIdx.x == 0) {
       p.cu_seqlens_q[p.num_seqs] = clamp_i32(total_q);
       if (p.next_free) *p.next_free = head < 0 ? head : clamp_i32(head + total_n);
     }
     // padding rows behind the last token: no slot, position 0
-    const int64_t hi = min(static_cast<int64_t>(p.num_tokens), total_q + tok_lo + kTokenChunk);
-    for (int64_t t = total_q + tok_lo + threadIdx.x; t < hi; t += kWarps * 32) {
+    static_assert(kTokenChunk == kWarps * 32, "a thread a row");
+    for (int64_t t = total_q + static_cast<int64_t>(y) * kTokenChunk + threadIdx.x; t < p.num_tokens;
+         t += static_cast<int64_t>(dy) * kTokenChunk) {
       p.slot_mapping[t] = -1;
       if (p.positions) p.positions[t] = 0;
     }
@@ -237,8 +244,10 @@ cudaError_t launch_build_block_tables(const BlockTables &p, cudaStream_t stream)
   // chunks that cover every token of one sequence and every page of one row
   const int tc = (p.num_tokens + kTokenChunk - 1) / kTokenChunk;
   const int pc = (p.table_stride + kPageChunk - 1) / kPageChunk;
-  const unsigned y = static_cast<unsigned>(tc > pc ? tc : pc);  // at most 2^15: the sizes are checked
-  return launch_kernel(block_tables_kernel, dim3(x, y), kWarps * 32, 0, stream, p);
+  const unsigned chunks = static_cast<unsigned>(tc > pc ? tc : pc);
+  const unsigned most = x < kMaxBlocks ? kMaxBlocks / x : 1;
+  const dim3 grid(x, chunks < most ? chunks : most);
+  return launch_kernel(block_tables_kernel, grid, kWarps * 32, 0, stream, p);
 }
 
 }  // namespace paq8

@@ -1,0 +1,75 @@
+"""build_block_tables at the ends of its sizes: as many tokens as it takes, many
+sequences beside long ones."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from paged_attention_int8_gb300 import _lib
+from tests import _harness as H
+
+pytestmark = pytest.mark.gpu
+
+MOST_TOKENS = 1 << 25
+
+
+def test_as_many_padding_rows_as_it_takes(cuda_device):
+    H.ensure_built()
+    e = lambda *s: torch.empty(s, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    got = _lib.build_block_tables(e(0), e(0), e(1, 4), e(0), 3, 16, MOST_TOKENS)
+    assert bool((got.slot_mapping == -1).all()) and bool((got.positions == 0).all())
+
+
+def _plain(ctx, q, source, rows, free, bs, tokens):
+    """The definition, in numpy: table (-1 where nothing is written), cu, slots, positions."""
+    n, columns = len(ctx), source.shape[1]
+    held, end = -(-ctx // bs), -(-(ctx + q) // bs)
+    cu = np.concatenate([[0], np.cumsum(q)])
+    at = np.concatenate([[0], np.cumsum(end - held)])
+    table = np.full((n, columns), -1, np.int64)
+    slots, pos = np.full(tokens, -1, np.int64), np.zeros(tokens, np.int64)
+    for s in range(n):
+        table[s, :held[s]] = source[rows[s], :held[s]]
+        table[s, held[s]:end[s]] = free[at[s]:at[s + 1]]
+        x = np.arange(ctx[s], ctx[s] + q[s])
+        slots[cu[s]:cu[s + 1]] = table[s, x // bs] * bs + x % bs
+        pos[cu[s]:cu[s + 1]] = x
+    return table, cu, slots, pos, at[n]
+
+
+@pytest.mark.parametrize("n,columns,long_q,pad", [
+    (1, (1 << 25) // 16, (1 << 25) - 700, 300),  # one prompt as long as it may be
+    (3000, 9000, 90000, 40000),                  # more chunks than a row of blocks has
+    (70000, 40, 500, 11),                        # many sequences
+])
+def test_many_tokens_and_sequences(cuda_device, n, columns, long_q, pad):
+    H.ensure_built()
+    rng = np.random.default_rng(n)
+    bs = 16
+    ctx = rng.integers(0, 30, n) if n > 1 else np.array([399])
+    q = rng.integers(0, 3, n)
+    q[n // 2] = long_q
+    if n > 1:
+        q[n - 1] = 7
+        ctx[1] = bs * columns - 40  # a row of many held pages
+    held = -(-ctx // bs)
+    source = np.full((n, columns), -1, np.int64)
+    source[np.arange(columns) < held[:, None]] = np.arange(held.sum())
+    new = int((-(-(ctx + q) // bs) - held).sum())
+    blocks = int(held.sum()) + new
+    assert blocks * bs < 2 ** 31
+    free = held.sum() + rng.permutation(new)
+    rows = rng.permutation(n)
+    tokens = int(q.sum()) + pad
+    assert tokens <= MOST_TOKENS
+    source[rows] = source.copy()  # the pages of s at row rows[s]
+    want = _plain(ctx, q, source, rows, free, bs, tokens)
+    i32 = lambda v: torch.from_numpy(np.ascontiguousarray(v).astype(np.int32)).to(cuda_device)  # noqa: E731
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    got = _lib.build_block_tables(i32(ctx), i32(q), i32(source), i32(free), blocks, bs, tokens,
+                                  source_rows=i32(rows), status=status)
+    assert _lib.check_status(status) == 0
+    for t, w in zip((got.block_table, got.cu_seqlens_q, got.slot_mapping, got.positions), want):
+        assert torch.equal(t.cpu().to(torch.int64), torch.from_numpy(w))
+    assert got.next_free.tolist() == [want[4]]
