@@ -392,8 +392,8 @@ pa_status pa_merge_attn_states(const void *out_a, const float *lse_a, const void
  * page or a free entry outside [0, num_blocks) (PA_DEV_BAD_BLOCK: slot -1); the
  * free list used up (PA_DEV_NO_BLOCKS: entry and slots -1, *next_free still
  * counts the pages wanted).  With num_seqs == 0 every row is padding and no
- * page is dealt.  block_size 16 or 32; at most 2^25 sequences, tokens and table
- * columns.  Asynchronous.
+ * page is dealt.  block_size 16 or 32; at most 2^18 sequences (the time grows with
+ * their square) and 2^25 tokens and table columns.  Asynchronous.
  */
 pa_status pa_build_block_tables(const int32_t *context_lens, const int32_t *query_lens,
                                 int32_t num_seqs, const int32_t *source_table,

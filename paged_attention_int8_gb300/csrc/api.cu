@@ -560,8 +560,11 @@ pa_status pa_build_block_tables(const int32_t *context_lens, const int32_t *quer
     return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   if (misaligned(7, {slot_mapping, positions}))
     return fail(PA_ERR_INVALID_ARG, "slot_mapping and positions must be 8-byte aligned");
-  if (num_seqs > (1 << 25) || num_tokens > (1 << 25) || block_table_stride > (1 << 25))
-    return fail(PA_ERR_UNSUPPORTED, "more than 2^25 sequences, tokens or table columns");
+  // every block adds up the lengths before its own: the reads grow with num_seqs^2
+  // (some 10 ms of them at 2^18 sequences, minutes at 2^25)
+  if (num_seqs > (1 << 18)) return fail(PA_ERR_UNSUPPORTED, "more than 2^18 sequences");
+  if (num_tokens > (1 << 25) || block_table_stride > (1 << 25))
+    return fail(PA_ERR_UNSUPPORTED, "more than 2^25 tokens or table columns");
   // every output apart from every input and every other output; the table may
   // be the source table itself, row for row
   const int64_t S = num_seqs, T = num_tokens;

@@ -73,3 +73,37 @@ def test_many_tokens_and_sequences(cuda_device, n, columns, long_q, pad):
     for t, w in zip((got.block_table, got.cu_seqlens_q, got.slot_mapping, got.positions), want):
         assert torch.equal(t.cpu().to(torch.int64), torch.from_numpy(w))
     assert got.next_free.tolist() == [want[4]]
+
+
+def test_as_many_sequences_as_it_takes(cuda_device):
+    """2^18 sequences: right, and in milliseconds."""
+    H.ensure_built()
+    n, bs = 1 << 18, 16
+    i = torch.arange(n, device=cuda_device)
+    ctx, q = (i % 33).int(), (i % 3).int()
+    source = (3 * i[:, None] + torch.arange(3, device=cuda_device)).int()
+    held, end = (ctx + bs - 1) // bs, (ctx + q + bs - 1) // bs
+    new = torch.where(q > 0, end - held, 0)
+    free = 3 * n + torch.arange(int(new.sum()), device=cuda_device, dtype=torch.int32)
+    tokens = int(q.sum())
+    args = (ctx, q, source, free, 4 * n, bs, tokens)
+    got = _lib.build_block_tables(*args)
+    cu = torch.cumsum(q, 0, dtype=torch.int32)
+    assert torch.equal(got.cu_seqlens_q[1:], cu) and torch.equal(got.seq_lens, ctx + q)
+    assert got.next_free.tolist() == [free.numel()]
+    at = (torch.cumsum(new, 0) - new)[:, None] + torch.arange(3, device=cuda_device) - held[:, None]
+    page = torch.arange(3, device=cuda_device)[None]
+    fresh = free[at.clamp(0, free.numel() - 1)]
+    table = torch.where(page < held[:, None], source, fresh)
+    table = torch.where(page < end[:, None], table, torch.full_like(table, -1))
+    assert torch.equal(got.block_table, table)
+    seq = torch.repeat_interleave(i, q.long())
+    x = ctx[seq].long() + torch.arange(tokens, device=cuda_device) - (cu - q)[seq].long()
+    assert torch.equal(got.positions, x)
+    assert torch.equal(got.slot_mapping, table[seq, x // bs].long() * bs + x % bs)
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    _lib.build_block_tables(*args, out=got)
+    stop.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(stop) < 100  # ms

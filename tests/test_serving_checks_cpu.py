@@ -52,3 +52,17 @@ def test_rows_that_would_pass_the_end_of_their_memory():
         assert torch.equal(got, view) and (got.data_ptr() != view.data_ptr()) == copied
         assert got_stride == (columns if copied else stride)
         assert got.storage_offset() + rows * got_stride <= got.untyped_storage().nbytes() // 4
+
+
+def test_block_tables_of_too_many_sequences(lib):
+    """The sums over earlier sequences are formed by every block: refused where they
+    would keep the GPU for seconds and more."""
+    far = 1 << 40
+    args = dict(ctx=far, q=2 * far, S=(1 << 18) + 1, src=3 * far, sstride=8, rows=1 << 19,
+                source_rows=None, shared=None, free=4 * far, num_free=9, head=5 * far, nb=10,
+                bs=16, table=6 * far, stride=8, cu=7 * far, lens=8 * far, slots=9 * far,
+                pos=10 * far, T=4, pairs=11 * far, next=12 * far, status=13 * far, stream=None)
+    for n in ((1 << 18) + 1, 1 << 25, (1 << 31) - 1):
+        args.update(S=n, rows=n)
+        assert lib.pa_build_block_tables(*args.values()) == _lib.Status.UNSUPPORTED
+        assert "sequences" in lib.pa_last_error().decode()
