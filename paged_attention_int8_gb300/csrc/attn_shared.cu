@@ -432,14 +432,17 @@ __global__ void __launch_bounds__(256, kBatch == 8 ? 3 : 4)
     g0 = group_token(s, g), g1 = group_token(s, g + 1);
   }
   const int ctx = seq_len - (c1 - c0);
-  // else: a row no sequence owns, one flagged by its suffix item, or one whose
-  // prefix was not taken
-  if (row < rows && c0 >= 0 && tok >= c0 && tok < c1 && c1 <= a.num_tokens && s0 <= seq && s1 > seq &&
-      rows_of(s, c1 - c0) <= s.max_rows && P >= 0 && ctx >= P && g0 >= 0 && g0 <= tok && tok < g1 &&
-      g1 <= a.num_tokens) {
-    P = min(P, s.capacity);
-    n_p = shared_segments(0, P, s.seg_p, s.ns_p);
-    n_s = shared_segments(P, min(ctx + tok - c0 + 1, s.capacity), s.seg_s, s.ns_s);
+  P = min(P, s.capacity);
+  if (row < rows && c0 >= 0 && tok >= c0 && tok < c1) {  // else: a row no sequence owns
+    if (c1 <= a.num_tokens && s0 <= seq && s1 > seq && rows_of(s, c1 - c0) <= s.max_rows && P >= 0 &&
+        ctx >= P && g0 >= 0 && g0 <= tok && tok < g1 && g1 <= a.num_tokens) {
+      n_p = shared_segments(0, P, s.seg_p, s.ns_p);
+      n_s = shared_segments(P, min(ctx + tok - c0 + 1, s.capacity), s.seg_s, s.ns_s);
+    } else {
+      // its prefix or its suffix was not taken (bounds of its group out of the batch are
+      // seen by the prefix items, its own entries by the suffix items): not written
+      flag_status(a.status, PA_DEV_BAD_SEQ);
+    }
   }
   const int n = n_s > 0 ? n_p + n_s : 0;  // 0: a row that is not written
   const int n_max = __reduce_max_sync(0xffffffffu, n);
