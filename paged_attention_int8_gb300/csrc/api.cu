@@ -473,9 +473,11 @@ bool shared_sizes_ok(int32_t num_seqs, int32_t num_tokens, int32_t num_groups, i
          max_suffix_len <= 0x7fffffff - 4096;
 }
 
+// Saturating: rows that no memory holds ask for all of it.
 size_t shared_bytes(int32_t num_tokens, int32_t num_q_heads, int32_t head_dim, int32_t splits) {
-  return 256 + static_cast<size_t>(num_tokens) * num_q_heads * splits * (head_dim + 2) *
-                   sizeof(float);
+  const size_t rows = static_cast<size_t>(num_tokens) * num_q_heads;
+  const size_t row_bytes = static_cast<size_t>(splits) * (head_dim + 2) * sizeof(float);
+  return rows > (SIZE_MAX - 256) / row_bytes ? SIZE_MAX : 256 + rows * row_bytes;
 }
 
 pa_status shared_prefix(paq8::SharedLaunch &L, void *workspace, size_t workspace_bytes,
@@ -500,6 +502,8 @@ pa_status shared_prefix(paq8::SharedLaunch &L, void *workspace, size_t workspace
   if (static_cast<int64_t>(L.num_blocks) * L.hk * L.d >= (int64_t{1} << 31))
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * num_kv_heads * head_dim must be < 2^31");
   if (L.hk > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 kv heads");
+  if (static_cast<int64_t>(L.num_tokens) + L.num_seqs + L.num_groups >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "num_tokens + num_seqs + num_groups must be < 2^31");
   if (!shared_sizes_ok(L.num_seqs, L.num_tokens, L.num_groups, L.hq, L.hk, L.d, L.max_query_len,
                        L.max_prefix_len, L.max_suffix_len))
     return fail(PA_ERR_INVALID_ARG,

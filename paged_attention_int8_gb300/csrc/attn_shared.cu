@@ -529,6 +529,13 @@ static bool prefix_on_tc(int32_t num_tokens, int32_t num_groups, int32_t qpk, in
          static_cast<int64_t>(num_tokens) * qpk >= int64_t{32} * num_groups;
 }
 
+// a * b * c of sizes below 2^31, at most 2^40: no count of segments goes by more.
+static int64_t blocks_of(int64_t a, int64_t b, int64_t c) {
+  constexpr int64_t kMost = int64_t{1} << 40;
+  const int64_t ab = a * b;
+  return ab > kMost / c ? kMost : ab * c;
+}
+
 SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_groups, int32_t hq,
                            int32_t hk, int32_t d, int32_t max_query_len, int32_t max_prefix_len,
                            int32_t max_suffix_len) {
@@ -538,8 +545,8 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   // kernel), tiles of the longest
   const int64_t most = static_cast<int64_t>(max_query_len) * qpk;
   const bool few = most <= kFewRows;
-  const int64_t sunits = static_cast<int64_t>(num_seqs) * hk *
-                         (few ? (most + 15) / 16 : (most + kRowTile - 1) / kRowTile);
+  const int64_t sunits =
+      blocks_of(num_seqs, hk, few ? (most + 15) / 16 : (most + kRowTile - 1) / kRowTile);
   const int64_t stiles = (static_cast<int64_t>(max_suffix_len) + kTile - 1) / kTile;
   {
     // prefix: the count of segments that ends soonest, in units of a tile's time,
@@ -559,7 +566,7 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
     const int rows = tc ? shared_tc_rows(d) : kRowTile;
     const int64_t block_q = std::max(1, rows / qpk);
     const int64_t units =
-        std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q) * hk;
+        blocks_of(std::max<int64_t>(num_groups, (num_tokens + block_q - 1) / block_q), hk, 1);
     const int64_t slots = tc || d == 256 ? 152 : 304;  // resident blocks
     const int64_t tiles = std::max(1, (max_prefix_len + kTile - 1) / kTile);
     const double join = static_cast<double>(num_tokens) * hq * (d + 2) * 8 / 2.2e6;

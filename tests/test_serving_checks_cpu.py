@@ -66,3 +66,21 @@ def test_block_tables_of_too_many_sequences(lib):
         args.update(S=n, rows=n)
         assert lib.pa_build_block_tables(*args.values()) == _lib.Status.UNSUPPORTED
         assert "sequences" in lib.pa_last_error().decode()
+
+
+def test_sizes_that_no_product_holds(lib):
+    """Sizes each in range whose products pass 64 bits: an answer, not a division by
+    zero, and no size that wrapped around."""
+    most = (1 << 31) - 1
+    size = _lib.shared_prefix_workspace_size
+    for args in ((1 << 30, most, 1, 1 << 19, 1 << 15, 64, most, 5, 5),
+                 (1 << 30, most, 1, 1 << 30, 1 << 30, 64, 1 << 10, 5, 5),
+                 (most, most, most, 16, 1, 256, most, most - 4096, most - 4096)):
+        _, t, _, hq, _, d, *_ = args
+        two = 256 + 2 * t * hq * (d + 2) * 4  # two triples a row, or all that a size_t holds
+        assert size(*args) >= min(two, (1 << 64) - 1)
+    for big in (dict(T=most), dict(S=most), dict(G=most), dict(S=1 << 30, T=1 << 30)):
+        args = {**VIEW, **big, "mq": most, "hq": 1 << 19, "hk": 1 << 15}
+        for fn in (lib.pa_paged_attention_shared_prefix_view,
+                   lib.pa_paged_attention_shared_prefix_f8v4_view):
+            assert fn(*args.values()) in (_lib.Status.UNSUPPORTED, _lib.Status.INVALID_ARG)
