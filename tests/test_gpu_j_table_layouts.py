@@ -2,6 +2,8 @@
 one column, a slice of a wider table."""
 from __future__ import annotations
 
+from dataclasses import replace
+
 import pytest
 import torch
 
@@ -98,15 +100,19 @@ def test_last_columns_of_a_wider_table(cuda_device, fmt):
     """A slice whose last row ends with the memory, on the current stream and on
     another."""
     b = S.make(85, cuda_device, fmt, 8, 2, 128, 16, [(40, [(1, 30), (1, 9), (1, 33)])], columns=0)
+    # the pages of one group differ where the prefix ends inside one: each row by itself
     ref = S.reference(b)
+    own = S.reference(replace(b, prefix=[0]))
     wide = torch.zeros((3, b.table.shape[1] + 9), dtype=torch.int32, device=cuda_device)
     wide[:, 9:] = b.table
     b.table = wide[:, 9:]
-    for call in _calls(b):
-        S.check(b, *call(), ref=ref)
+    *paged, shared = _calls(b)
+    S.check(b, *shared(), ref=ref)
+    for call in paged:
+        S.check(b, *call(), ref=own)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     call = _lib.paged_attention if fmt == "q8" else _lib.paged_attention_f8v4
     out, lse = call(b.q, *b.cache, b.cu, b.lens, b.table, 1, max(b.seq_lens), stream=side)
     side.synchronize()
-    S.check(b, out, lse, ref=ref)
+    S.check(b, out, lse, ref=own)
