@@ -541,12 +541,12 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
                            int32_t max_suffix_len) {
   const int qpk = hq / hk;
   SharedSplits r;
-  // suffixes: blocks of a segment (16 rows in the rows kernel, 64 in the row-tile
+  // suffixes: blocks of a segment (8 or 16 rows in the rows kernel, 64 in the row-tile
   // kernel), tiles of the longest
   const int64_t most = static_cast<int64_t>(max_query_len) * qpk;
   const bool few = most <= kFewRows;
-  const int64_t sunits =
-      blocks_of(num_seqs, hk, few ? (most + 15) / 16 : (most + kRowTile - 1) / kRowTile);
+  const int64_t tile = few ? rows_per_pass(d, most) : kRowTile;
+  const int64_t sunits = blocks_of(num_seqs, hk, (most + tile - 1) / tile);
   const int64_t stiles = (static_cast<int64_t>(max_suffix_len) + kTile - 1) / kTile;
   {
     // prefix: the count of segments that ends soonest, in units of a tile's time,
@@ -593,14 +593,18 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
     // suffix: ~1024 keys a segment (the decode kernel's measured best; 2048 where one
     // segment each fills the GPU, 128 requests of up to 2048 keys behind 32768: 218 us
     // against 228), more only while blocks are too few to fill the GPU: four of the
-    // rows kernel to an SM, of 4 tiles at least; one at D = 256 (two fit, and the
-    // prefix holds most SMs: 32 requests behind 16384 keys, a segment each 43 us, two
-    // 47); one of the row-tile kernel, a tile at least (2 x 40 tokens of 4 rows behind
-    // 1284 keys of D = 256: 7 segments 35 us, 3 45).
-    const int64_t full = few && d != 256 ? 608 : 152, cap = few ? (stiles + 3) / 4 : stiles + 1;
+    // rows kernel to an SM, of 4 tiles at least; two at D = 256, where whole rounds of
+    // them are taken, no part of one (32 requests behind 16384 keys, a segment each 43
+    // us, two 46; 16 of 24 rows and up to 2048 keys behind 4096: two 26.5, three 23;
+    // 64 of 16 rows and 2000 keys behind 8192: one 62, two 58); one of the row-tile
+    // kernel, a tile at least (2 x 40 tokens of 4 rows behind 1284 keys of D = 256:
+    // 7 segments 35 us, 3 45).
+    const int64_t full = !few ? 152 : d == 256 ? 304 : 608;
+    const int64_t cap = few ? (stiles + 3) / 4 : stiles + 1;
+    const int64_t rounds = few && d == 256 ? full / sunits : (full + sunits - 1) / sunits;
     const int64_t keys = sunits >= full ? 2048 : 1024;
     int64_t n = std::max<int64_t>((static_cast<int64_t>(max_suffix_len) + keys - 1) / keys,
-                                  std::min((full + sunits - 1) / sunits, cap));
+                                  std::min(rounds, cap));
     n = std::min(n, std::max<int64_t>(1, 8192 / sunits));
     r.suffix = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(n, 64)));
   }

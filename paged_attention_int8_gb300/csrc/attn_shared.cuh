@@ -205,6 +205,13 @@ inline int prefix_blocks(int num_tokens, int num_groups, int block_q) {
              : num_tokens / block_q + num_groups;
 }
 
+// Rows that the rows kernel takes a pass over the keys, for sequences of at most `most`
+// rows: two 8-row tiles where the registers hold them without spills.  D = 128, 48
+// requests of up to 32 rows and 2000 keys: two passes of two 69 us (q8) and 62 (fp8 /
+// 4-bit), one of four 83 and 75; D = 64, of 32 rows 46 and 45, one of four 56 and 51;
+// D = 256, of 12 rows: two passes of one 64 and 64, one of two 73 and 69.
+inline int rows_per_pass(int d, int64_t most) { return d == 256 || most <= 8 ? 8 : 16; }
+
 // Suffix item: row block `blk` (block_q tokens of one sequence), segment sigma.
 __device__ __forceinline__ bool suffix_work(const SharedArgs &s, int blk, int sigma, int block_q,
                                             int lane, SharedWork &w) {

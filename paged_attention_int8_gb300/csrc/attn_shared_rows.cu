@@ -561,11 +561,7 @@ static cudaError_t launch_shared_rows_t(const SharedArgs &s, cudaStream_t stream
 
 template <int D, int BS>
 static cudaError_t launch_shared_rows_d(const SharedArgs &s, bool f8v4, cudaStream_t stream) {
-  // row tiles a pass: two where the registers hold them without spills.  D = 128, 48
-  // requests of up to 32 rows and 2000 keys: two passes of two 69 us (q8) and 62
-  // (fp8 / 4-bit), one of four 83 and 75; D = 64, of 32 rows 46 and 45, one of four 56
-  // and 51; D = 256, of 12 rows: two passes of one 64 and 64, one of two 73 and 69.
-  if (D == 256 || s.few_rows <= 8)
+  if (rows_per_pass(D, s.few_rows) == 8)
     return f8v4 ? launch_shared_rows_t<D, BS, true, 1>(s, stream)
                 : launch_shared_rows_t<D, BS, false, 1>(s, stream);
   if constexpr (D != 256)

@@ -84,3 +84,12 @@ def test_sizes_that_no_product_holds(lib):
         for fn in (lib.pa_paged_attention_shared_prefix_view,
                    lib.pa_paged_attention_shared_prefix_f8v4_view):
             assert fn(*args.values()) in (_lib.Status.UNSUPPORTED, _lib.Status.INVALID_ARG)
+
+
+@pytest.mark.parametrize("n", [3, 16, 40])
+def test_segments_follow_the_rows_of_a_pass(lib, n):
+    """Heads of 256 channels take 8 rows a pass: a sequence of 16 rows fills as many
+    blocks as two of 8, and has its keys cut into as many segments."""
+    size = _lib.shared_prefix_workspace_size
+    tokens = 4 * n
+    assert size(n, tokens, 1, 8, 2, 256, 4, 0, 4096) == size(2 * n, tokens, 1, 8, 2, 256, 2, 0, 4096)
