@@ -71,7 +71,8 @@ enum : int {
   kBarPFull = 22,    // [half] softmax (P in TMEM) -> MMA (4 warps)
   kBarPvDone = 24,   // [half] commit after the last PV -> epilogue
   kBarQFull = 26,    // softmax (q written to TMEM) -> MMA (8 warps)
-  kNumBars = 27
+  kBarIdle = 27,     // commit after the last MMA issued -> MMA issuer
+  kNumBars = 28
 };
 
 template <int D, int BS, bool F8>
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(bar(kBarPvDone + s), 1);
     }
     mbar_init(bar(kBarQFull), 8);
+    mbar_init(bar(kBarIdle), 1);
     fence_barrier_init();
   }
   if (warp == 1) tc::alloc(tmem_slot, C::kTmemCols);
@@ -151,7 +153,8 @@ __global__ void __launch_bounds__(512, 1)
     constexpr uint32_t kPageTx = F8 ? BS * D + BS * D / 2 + 4 * BS : 2 * BS * D + 4 * BS * (D / 32);
     int page_base = -(1 << 30), my_blk = -1;
     int stage = 0, phase = 1;  // of the ring; the parity of its being empty
-    for (int j = 0; ok && j < nt; ++j) {
+    int j = 0;
+    for (; ok && j < nt; ++j) {
       if (j >= C::kSt) {
         int there = 1;
         if (lane == 0) there = mbar_wait(bar(kBarStEmpty + stage), phase);
@@ -201,6 +204,9 @@ __global__ void __launch_bounds__(512, 1)
       }
       __syncwarp();
     }
+    // the block holds its shared memory until its copies have landed, whoever gave up
+    for (int i = max(0, j - C::kSt); lane == 0 && i < j; ++i)
+      ok &= mbar_wait(bar(kBarStFull + i % C::kSt), (i / C::kSt) & 1);
   } else if (warp == 1) {
     // ============================================================ MMA issuer
     // One elected lane runs the whole loop: under `elect` the compiler knows that
@@ -259,6 +265,9 @@ __global__ void __launch_bounds__(512, 1)
         if (!issue_pv(nt - 1, hf)) { ok = false; break; }
         tc::commit(bar(kBarPvDone + hf));
       }
+      // and its TMEM until its MMAs are done
+      tc::commit(bar(kBarIdle));
+      ok &= mbar_wait(bar(kBarIdle), 0);
     }
     ok = __all_sync(0xffffffffu, ok);
   } else if (warp < 6 || warp >= 14) {

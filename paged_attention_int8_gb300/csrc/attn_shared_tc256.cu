@@ -73,7 +73,8 @@ enum : int {
   kPFull = 20,     // [2] softmax (P in TMEM) -> MMA (4 warps)
   kQFull = 22,     // softmax (q in TMEM) -> MMA (4 warps)
   kAllDone = 23,   // commit after the last PV -> softmax (PvDone may be two phases off there)
-  kBars = 24
+  kIdle = 24,      // commit after the last MMA issued -> MMA issuer
+  kBars = 25
 };
 
 template <int BS, bool F8>
@@ -137,6 +138,7 @@ __global__ void __maxnreg__(96)
     mbar_init(bar(kPvDone), 1);
     mbar_init(bar(kQFull), 4);
     mbar_init(bar(kAllDone), 1);
+    mbar_init(bar(kIdle), 1);
     fence_barrier_init();
   }
   if (warp == 1) tc::alloc(tmem_slot, 512);
@@ -159,7 +161,8 @@ __global__ void __maxnreg__(96)
     const int32_t *bt_row = a.block_table + static_cast<int64_t>(w.row) * a.bt_stride;
     int page_base = -(1 << 30), my_blk = -1;
     int st = 0, phase = 1;  // stage of the ring and the parity of its being empty
-    for (int j = 0; ok && j < nt; ++j) {
+    int j = 0;
+    for (; ok && j < nt; ++j) {
       if (j >= n_st) {
         int there = 1;
         if (lane == 0) there = mbar_wait(bar(empty0 + st), phase);
@@ -222,6 +225,9 @@ __global__ void __maxnreg__(96)
       }
       __syncwarp();
     }
+    // the block holds its shared memory until its copies have landed, whoever gave up
+    for (int i = max(0, j - n_st); lane == 0 && i < j; ++i)
+      ok &= mbar_wait(bar(full0 + i % n_st), (i / n_st) & 1);
   } else if (warp == 1) {
     // ============================================================ MMA issuer
     // one elected lane (attn_shared_tc.cu)
@@ -276,6 +282,9 @@ __global__ void __maxnreg__(96)
         tc::commit(bar(kPvDone));
       }
       if (ok) tc::commit(bar(kAllDone));
+      // the block holds its TMEM until its MMAs are done
+      tc::commit(bar(kIdle));
+      ok &= mbar_wait(bar(kIdle), 0);
     }
     ok = __all_sync(0xffffffffu, ok);
   } else if (warp == 0 || warp == 2 || warp == 3 || warp == 6 || (warp >= 14 && warp < 18)) {

@@ -111,6 +111,10 @@ __global__ void __launch_bounds__(32) copy_blocks_kernel(const BlockCopy p, int 
   }
   if (lane == 0) {
     for (int i = max(0, n - kAhead); ok && i < n; ++i) ok = put(i);
+    // a wait ran out: the parts being read may still land, and shared memory is theirs
+    // until they do (or another wait as long runs out)
+    for (int i = max(0, n - kAhead); !ok && i < n; ++i)
+      mbar_wait(smem_u32(full + i % kRing), (i / kRing) & 1);
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok) flag_status(p.status, PA_DEV_TIMEOUT);
   }
