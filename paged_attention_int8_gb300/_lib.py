@@ -605,7 +605,8 @@ def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_
     sequence about to write into such a page gets a private one, and
     ``copy_pairs`` names the copy to make (copy_blocks).  ``num_tokens``: rows
     of the slot map (host bound of the new tokens; the rest is padding).
-    ``out``: a BlockTables (or tuple in its order) to write into; its
+    ``out``: a BlockTables (or tuple in its order) to write into, None where
+    ``positions``, ``copy_pairs`` or ``next_free`` are not wanted; its
     ``block_table`` may be ``source_table`` itself (source_rows None), the
     only allowed overlap.  ``status``: optional int32 CUDA tensor, zeroed."""
     dev = context_lens.get_device()
@@ -625,6 +626,8 @@ def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_
     if type(out) is not BlockTables:
         out = BlockTables._make(out)
     table, cu, lens, slots, pos, pairs, nxt = out
+    if table is None or cu is None or lens is None or slots is None:
+        raise ValueError("block_table, cu_seqlens_q, seq_lens and slot_mapping are always written")
     for t in (context_lens, query_lens, source_table, free_blocks, table, cu, lens, source_rows,
               shared_lens, free_head, pairs, nxt, status):
         if t is not None and (t.dtype is not _I32 or t.get_device() != dev
@@ -635,7 +638,7 @@ def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_
                     shared_lens=shared_lens, free_head=free_head, copy_pairs=pairs, next_free=nxt,
                     status=status)
     for t in (slots, pos):
-        if t is None and t is pos:
+        if t is None:
             continue
         if t.dtype is not torch.int64 or t.get_device() != dev or not t.is_contiguous():
             _refuse(dev, (torch.int64,), slot_mapping=slots, positions=pos)

@@ -107,3 +107,30 @@ def test_as_many_sequences_as_it_takes(cuda_device):
     stop.record()
     torch.cuda.synchronize()
     assert start.elapsed_time(stop) < 100  # ms
+
+
+def test_results_that_are_not_wanted(cuda_device):
+    """positions, copy_pairs and next_free may be None; the others are refused so."""
+    H.ensure_built()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    args = (i32(3, 20), i32(1, 2), i32(7, -1, 8, 9).view(2, 2), i32(4, 5), 10, 16, 3)
+    want = _lib.build_block_tables(*args)
+    for at in range(7):
+        out = [torch.full_like(t, -1) for t in want]
+        out[at] = None
+        if at in (0, 1, 2, 3):
+            with pytest.raises(ValueError):
+                _lib.build_block_tables(*args, out=out)
+        else:
+            got = _lib.build_block_tables(*args, out=out)
+            assert got[at] is None
+            for t, w in zip(got, want):
+                assert t is None or torch.equal(t, w)
+    # two at once
+    for at in ((3, 4), (4, 5, 6)):
+        out = [None if i in at else torch.full_like(t, -1) for i, t in enumerate(want)]
+        if at[0] == 3:
+            with pytest.raises(ValueError):
+                _lib.build_block_tables(*args, out=out)
+        else:
+            assert torch.equal(_lib.build_block_tables(*args, out=out)[3], want[3])
