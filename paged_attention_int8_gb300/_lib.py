@@ -327,7 +327,7 @@ def _table_in_bounds(block_table, rows, stride, stream):
     first column) would pass the end of its memory, whole rows of its own."""
     if (block_table.storage_offset() + rows * stride) * 4 <= block_table.untyped_storage().nbytes():
         return block_table, stride
-    with _allocating(stream):
+    with _allocating(stream, block_table.get_device()):
         block_table = block_table.contiguous()
     return block_table, block_table.shape[1]
 
@@ -553,14 +553,14 @@ def _call(fn, dev, stream, *args):
         _raise_if(st)
 
 
-def _allocating(stream):
-    """Context in which a call's omitted results and workspace are allocated: on
-    the stream that it runs on, so that neither their first bytes nor their
-    reuse after the last reference is gone are out of its order."""
+def _allocating(stream, dev):
+    """Context in which a call's omitted results and workspace are allocated on
+    device number `dev`: on the stream that it runs on, so that neither their first
+    bytes nor their reuse after the last reference is gone are out of its order."""
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
     return torch.cuda.stream(stream)
 
 
@@ -619,7 +619,7 @@ def build_block_tables(context_lens, query_lens, source_table, free_blocks, num_
     if out is None:
         device = context_lens.device
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
-        with _allocating(stream):
+        with _allocating(stream, dev):
             out = (torch.full((s, columns), -1, dtype=_I32, device=device), new(s + 1, _I32),
                    new(s, _I32), new(num_tokens, torch.int64), new(num_tokens, torch.int64),
                    new((s, 2), _I32), new(1, _I32))
@@ -767,7 +767,7 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
         if sinks.numel() != hq:
             raise ValueError("sinks must be [num_q_heads]")
     if out is None:
-        with _allocating(stream):
+        with _allocating(stream, dev):
             out = torch.empty_like(q)
     else:
         if out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
@@ -776,7 +776,7 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
             raise ValueError("out must be shaped like q")
     if lse is None:
         if return_lse:
-            with _allocating(stream):
+            with _allocating(stream, dev):
                 lse = torch.empty((t, hq), dtype=_F32, device=q.device)
     else:
         if lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
@@ -786,7 +786,7 @@ def _shared_prefix(fn, check, q, cache, cu_seqlens_q, seq_lens, block_table, cu_
     if workspace is None:
         need = load().pa_shared_prefix_workspace_size(s, t, g, hq, hk, d, max_query_len,
                                                       max_prefix_len, max_suffix_len)
-        with _allocating(stream):
+        with _allocating(stream, dev):
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             workspace[:4].zero_()
     elif workspace.get_device() != dev or not workspace.is_contiguous():

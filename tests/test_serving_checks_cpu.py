@@ -93,3 +93,16 @@ def test_segments_follow_the_rows_of_a_pass(lib, n):
     size = _lib.shared_prefix_workspace_size
     tokens = 4 * n
     assert size(n, tokens, 1, 8, 2, 256, 4, 0, 4096) == size(2 * n, tokens, 1, 8, 2, 256, 2, 0, 4096)
+
+
+def test_streams_of_other_libraries_belong_to_the_tensors_device(monkeypatch):
+    """An object with a stream's handle: its memory comes from the device that the
+    tensors are on, whichever is current."""
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: made.append((h, device)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    _lib._allocating(type("Stream", (), {"cuda_stream": 0x1230})(), 3)
+    assert made == [(0x1230, 3)]
+    with _lib._allocating(None, 3):
+        pass
+    assert len(made) == 1
