@@ -461,7 +461,9 @@ size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int
  *                 own is a group of one.
  *   max_query_len host upper bound on every q_len (never synced); a sequence
  *                 with more query tokens may be left unprocessed and flagged
- *                 PA_DEV_BAD_SEQ.
+ *                 PA_DEV_BAD_SEQ.  It sizes the key segments too, as if every
+ *                 query were so long: a call for the single tokens and one
+ *                 for the long queries beside them is the faster way.
  *   max_prefix_len, max_suffix_len
  *                 host hints of the longest prefix and of the longest seq_len -
  *                 prefix: they size the key segments; any positive value
@@ -476,8 +478,12 @@ size_t pa_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_tokens, int
  * is below its prefix, that no group holds, or whose metadata is out of range
  * is not written and flagged PA_DEV_BAD_SEQ; rows of tokens no sequence owns
  * are not written.  Keys past the table's columns (block_table_stride of them)
- * are flagged PA_DEV_BAD_BLOCK and left out.  Numerics as pa_paged_attention_ex;
- * the parts are joined in fp32.  Asynchronous.
+ * are flagged PA_DEV_BAD_BLOCK and left out; an entry outside [0, num_blocks) is
+ * flagged so too, and the rows that see its keys are written with undefined
+ * values (a prefix's: all rows of its group).  Numerics as
+ * pa_paged_attention_ex; the q8 keys of a prefix with 32 rows or more are taken
+ * as two fp16 parts, exact for |k| <= 65504.  The parts are joined in fp32.
+ * Asynchronous.
  */
 pa_status pa_paged_attention_shared_prefix(
     const void *q, const void *k_cache, const void *k_scale, const void *v_cache,

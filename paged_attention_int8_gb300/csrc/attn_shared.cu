@@ -542,7 +542,10 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   const int qpk = hq / hk;
   SharedSplits r;
   // suffixes: blocks of a segment (8 or 16 rows in the rows kernel, 64 in the row-tile
-  // kernel), tiles of the longest
+  // kernel), tiles of the longest.  Every sequence is taken for as long as the longest
+  // query: one long query among many short ones leaves the prefix and the suffixes of
+  // all too few segments (63 tokens and a query of 9 behind 8192 keys 142 us, 64
+  // tokens 41).
   const int64_t most = static_cast<int64_t>(max_query_len) * qpk;
   const bool few = most <= kFewRows;
   const int64_t tile = few ? rows_per_pass(d, most) : kRowTile;
@@ -551,8 +554,10 @@ SharedSplits shared_splits(int32_t num_seqs, int32_t num_tokens, int32_t num_gro
   {
     // prefix: the count of segments that ends soonest, in units of a tile's time,
     // of a model fitted to 68 batches x 20 counts each (all D, both formats, 1 - 128
-    // sequences, 1 - 5 groups): on average it is 2.8 % above the best count's time;
-    // whole waves of the prefix's blocks by themselves were 8.4 % above it.
+    // sequences, 1 - 5 groups): on average it was 2.8 % above the best count's time;
+    // whole waves of the prefix's blocks by themselves were 8.4 % above it.  The kernels
+    // have become faster since: 12 batches at D = 256 are now 5 % above their best on
+    // average, 25 % at worst (8 requests of up to 1500 own keys behind 4096).
     //  - A block takes its tiles and 8 more (set-up, first loads, triples; row-tile
     //    kernel: 6).
     //  - The suffixes (half of the longest on average, and 5 tiles of set-up; a tile

@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
   const uint32_t ring = smem_base + warp * (kSt * L::kBytes);
   const int32_t *bt_row = a.block_table + static_cast<int64_t>(seq) * a.bt_stride;
   int held = -1;  // block id of this lane's block: number (i / 32) * 32 + lane of this warp's
-  // block ids of the warp's blocks i .. i + 31 (-1: a bad entry, flagged and masked by no copy)
+  // block ids of the warp's blocks i .. i + 31; -1: a bad entry, flagged and not copied.  Its
+  // keys are what stood in the stage before, and the rows that see them undefined.
   auto load_ids = [&](int i) {
     held = -1;
     if (i + lane < n_blk) {

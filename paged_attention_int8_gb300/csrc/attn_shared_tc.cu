@@ -317,34 +317,34 @@ __global__ void __launch_bounds__(512, 1)
           }
         } else {
 #pragma unroll
-        for (int c = c0; c < c0 + kChannels; c += 16) {
-          const uint4 codes = lds128(st + L::k_off(r, c));
-          const uint32_t sbits = lds16(st + L::ks_off(r, c / 32));
-          const uint32_t s2 = dead ? 0u : (sbits | (sbits << 16));
-          const uint32_t ns2 = s2 ^ 0x80008000u;  // -scale
-          uint32_t hw[8], lw[8];
-          const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+          for (int c = c0; c < c0 + kChannels; c += 16) {
+            const uint4 codes = lds128(st + L::k_off(r, c));
+            const uint32_t sbits = lds16(st + L::ks_off(r, c / 32));
+            const uint32_t s2 = dead ? 0u : (sbits | (sbits << 16));
+            const uint32_t ns2 = s2 ^ 0x80008000u;  // -scale
+            uint32_t hw[8], lw[8];
+            const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t lo, hi;
-            codes4_to_half2(cw[i], lo, hi);
-            // hi = fp16(code * s); lw = code * (-s) + hi = -lo (one rounding, exact);
-            // the QK MMA of the lo part negates B, so it adds q . lo
-            hw[2 * i] = hmul2_u32(lo, s2);
-            hw[2 * i + 1] = hmul2_u32(hi, s2);
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(lw[2 * i]) : "r"(lo), "r"(ns2), "r"(hw[2 * i]));
-            asm("fma.rn.f16x2 %0, %1, %2, %3;"
-                : "=r"(lw[2 * i + 1])
-                : "r"(hi), "r"(ns2), "r"(hw[2 * i + 1]));
+            for (int i = 0; i < 4; ++i) {
+              uint32_t lo, hi;
+              codes4_to_half2(cw[i], lo, hi);
+              // hi = fp16(code * s); lw = code * (-s) + hi = -lo (one rounding, exact);
+              // the QK MMA of the lo part negates B, so it adds q . lo
+              hw[2 * i] = hmul2_u32(lo, s2);
+              hw[2 * i + 1] = hmul2_u32(hi, s2);
+              asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(lw[2 * i]) : "r"(lo), "r"(ns2), "r"(hw[2 * i]));
+              asm("fma.rn.f16x2 %0, %1, %2, %3;"
+                  : "=r"(lw[2 * i + 1])
+                  : "r"(hi), "r"(ns2), "r"(hw[2 * i + 1]));
+            }
+            const int c16 = c / 8;
+            sts128(kdst + tc::sw128_chunk(r, c16, 64), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+            sts128(kdst + tc::sw128_chunk(r, c16 + 1, 64), make_uint4(hw[4], hw[5], hw[6], hw[7]));
+            sts128(kdst + C::kKBytes + tc::sw128_chunk(r, c16, 64),
+                   make_uint4(lw[0], lw[1], lw[2], lw[3]));
+            sts128(kdst + C::kKBytes + tc::sw128_chunk(r, c16 + 1, 64),
+                   make_uint4(lw[4], lw[5], lw[6], lw[7]));
           }
-          const int c16 = c / 8;
-          sts128(kdst + tc::sw128_chunk(r, c16, 64), make_uint4(hw[0], hw[1], hw[2], hw[3]));
-          sts128(kdst + tc::sw128_chunk(r, c16 + 1, 64), make_uint4(hw[4], hw[5], hw[6], hw[7]));
-          sts128(kdst + C::kKBytes + tc::sw128_chunk(r, c16, 64),
-                 make_uint4(lw[0], lw[1], lw[2], lw[3]));
-          sts128(kdst + C::kKBytes + tc::sw128_chunk(r, c16 + 1, 64),
-                 make_uint4(lw[4], lw[5], lw[6], lw[7]));
-        }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -403,37 +403,37 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
         } else {
-        const int g = ch[0] / 32;
+          const int g = ch[0] / 32;
 #pragma unroll
-        for (int key = 0; key < C::kTile; key += 16) {  // 16 keys: one 16-byte load
-          const uint4 s01 = lds128(st + L::vs_off(key, g));
-          const uint4 s23 = lds128(st + L::vs_off(key + 8, g));
-          uint32_t sc[8] = {s01.x, s01.y, s01.z, s01.w, s23.x, s23.y, s23.z, s23.w};
-          if (tail) {
+          for (int key = 0; key < C::kTile; key += 16) {  // 16 keys: one 16-byte load
+            const uint4 s01 = lds128(st + L::vs_off(key, g));
+            const uint4 s23 = lds128(st + L::vs_off(key + 8, g));
+            uint32_t sc[8] = {s01.x, s01.y, s01.z, s01.w, s23.x, s23.y, s23.z, s23.w};
+            if (tail) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int k0 = key0 + key + 2 * i;
-              if (k0 >= kv_end) sc[i] &= 0xffff0000u;
-              if (k0 + 1 >= kv_end) sc[i] &= 0x0000ffffu;
+              for (int i = 0; i < 8; ++i) {
+                const int k0 = key0 + key + 2 * i;
+                if (k0 >= kv_end) sc[i] &= 0xffff0000u;
+                if (k0 + 1 >= kv_end) sc[i] &= 0x0000ffffu;
+              }
+            }
+#pragma unroll
+            for (int rr = 0; rr < R; ++rr) {
+              const uint4 codes = lds128(st + L::v_off(ch[rr], key));
+              uint32_t o[8];
+              const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t lo, hi;
+                codes4_to_half2(cw[i], lo, hi);
+                o[2 * i] = hmul2_u32(lo, sc[2 * i]);
+                o[2 * i + 1] = hmul2_u32(hi, sc[2 * i + 1]);
+              }
+              sts128(vrow + tc::sw128_chunk(ch[rr], key / 8, D), make_uint4(o[0], o[1], o[2], o[3]));
+              sts128(vrow + tc::sw128_chunk(ch[rr], key / 8 + 1, D),
+                     make_uint4(o[4], o[5], o[6], o[7]));
             }
           }
-#pragma unroll
-          for (int rr = 0; rr < R; ++rr) {
-            const uint4 codes = lds128(st + L::v_off(ch[rr], key));
-            uint32_t o[8];
-            const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t lo, hi;
-              codes4_to_half2(cw[i], lo, hi);
-              o[2 * i] = hmul2_u32(lo, sc[2 * i]);
-              o[2 * i + 1] = hmul2_u32(hi, sc[2 * i + 1]);
-            }
-            sts128(vrow + tc::sw128_chunk(ch[rr], key / 8, D), make_uint4(o[0], o[1], o[2], o[3]));
-            sts128(vrow + tc::sw128_chunk(ch[rr], key / 8 + 1, D),
-                   make_uint4(o[4], o[5], o[6], o[7]));
-          }
-        }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
