@@ -201,7 +201,7 @@ cudaError_t launch_paged_attention(const AttnLaunch &L, cudaStream_t stream) {
   a.hk = L.hk;
   a.qpk = L.hq / L.hk;
   a.num_blocks = L.num_blocks;
-  a.bt_stride = a.bt_cols = L.bt_stride;
+  a.bt_stride = L.bt_stride;
   a.num_splits = L.num_splits;
   a.scale_log2 = L.softmax_scale * kLog2e;
   a.causal = L.causal ? 1 : 0;

@@ -17,7 +17,7 @@ struct AttnArgs {
   const uint16_t *q;            // [T, Hq, D] bf16
   const int32_t *cu_seqlens_q;  // [S+1]
   const int32_t *seq_lens;      // [S]
-  const int32_t *block_table;   // [S, bt_cols], rows bt_stride apart
+  const int32_t *block_table;   // [S, bt_stride]
   const int8_t *k_cache;        // [nb, Hk, bs, D] int8
   const int8_t *v_cache;        // [nb, Hk, D, bs] int8
   const uint16_t *k_scale;      // [nb, Hk, bs, G] fp16
@@ -28,7 +28,7 @@ struct AttnArgs {
   float *part_acc;              // [S, Hq, NS, D]
   float *part_ml;               // [S, Hq, NS, 2]  (max in log2 units, expsum)
   uint32_t *status;
-  int32_t num_seqs, num_tokens, hq, hk, qpk, num_blocks, bt_stride, bt_cols;
+  int32_t num_seqs, num_tokens, hq, hk, qpk, num_blocks, bt_stride;
   int32_t block_q;              // tokens per q-block (prefill kernel)
   int32_t n_qblocks;            // grid.x entries that are q-blocks (prefill kernel)
   int32_t num_splits;           // segments of single-token sequences
@@ -211,7 +211,7 @@ __device__ __forceinline__ void produce_tiles(const AttnArgs &a, const CUtensorM
       const int lp = page_base + lane;
       my_blk = -1;
       if (lp < n_pages && (lp + 1) * BS > kv_begin) {
-        const int b = lp < a.bt_cols ? bt_row[lp] : -1;
+        const int b = lp < a.bt_stride ? bt_row[lp] : -1;
         if (b >= 0 && b < a.num_blocks) my_blk = b;
         else flag_status(a.status, PA_DEV_BAD_BLOCK);
       }
@@ -319,7 +319,7 @@ __device__ __forceinline__ bool produce_tiles_lsu(const AttnArgs &a, uint32_t sm
       const int lp = page_base + lane;
       my_blk = -1;
       if (lp < n_pages && (lp + 1) * BS > kv_begin) {
-        const int b = lp < a.bt_cols ? bt_row[lp] : -1;
+        const int b = lp < a.bt_stride ? bt_row[lp] : -1;
         if (b >= 0 && b < a.num_blocks) my_blk = b;
         else flag_status(a.status, PA_DEV_BAD_BLOCK);
       }

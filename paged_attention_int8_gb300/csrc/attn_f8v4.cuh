@@ -90,7 +90,7 @@ __device__ __forceinline__ void produce_f8v4(const AttnArgs &a, uint32_t smem_ba
       const int lp = page_base + lane;
       my_blk = -1;
       if (lp < n_pages && (lp + 1) * BS > kv_begin) {
-        const int b = lp < a.bt_cols ? bt_row[lp] : -1;
+        const int b = lp < a.bt_stride ? bt_row[lp] : -1;
         if (b >= 0 && b < a.num_blocks) my_blk = b;
         else flag_status(a.status, PA_DEV_BAD_BLOCK);
       }
@@ -157,7 +157,7 @@ __device__ __forceinline__ void produce_tiles_f8v4_tma(const AttnArgs &a, const 
       const int lp = page_base + lane;
       my_blk = -1;
       if (lp < n_pages && (lp + 1) * BS > kv_begin) {
-        const int b = lp < a.bt_cols ? bt_row[lp] : -1;
+        const int b = lp < a.bt_stride ? bt_row[lp] : -1;
         if (b >= 0 && b < a.num_blocks) my_blk = b;
         else flag_status(a.status, PA_DEV_BAD_BLOCK);
       }

@@ -698,7 +698,6 @@ cudaError_t launch_shared_prefix(const SharedLaunch &L, cudaStream_t stream) {
   a.qpk = L.hq / L.hk;
   a.num_blocks = L.num_blocks;
   a.bt_stride = L.bt_stride;
-  a.bt_cols = L.bt_cols;
   a.scale_log2 = L.softmax_scale * kLog2e;
   a.causal = 1;
   a.sinks = L.sinks;

@@ -48,7 +48,8 @@ struct SharedArgs {
   int32_t few_rows;            // suffixes of at most this many rows are the rows kernel's
   int32_t max_rows;            // no suffix kernel takes more rows than this
   int32_t row_passes;          // rows kernel: passes over the keys that cover them
-  int32_t capacity;            // keys a row of the block table holds: no more are walked
+  int32_t capacity;            // keys that the columns of a table row hold: none past them is walked,
+                               // so that no look-up passes the columns, whatever the row stride
   int32_t first;               // row-tile kernel: it is the call's first
 };
 

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(128, SharedRowsCfg<D, BS, F8, NT>::kMinBlocks)
     held = -1;
     if (i + lane < n_blk) {
       const int lp = static_cast<int>((static_cast<int64_t>(b0) + kWarps * (i + lane)) / (BS / 16));
-      const int b = lp < a.bt_cols ? bt_row[lp] : -1;
+      const int b = lp < a.bt_stride ? bt_row[lp] : -1;
       if (b >= 0 && b < a.num_blocks) held = b;
       else flag_status(a.status, PA_DEV_BAD_BLOCK);
     }

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(512, 1)
         const int lp = page_base + lane;
         my_blk = -1;
         if (lp < n_pages) {
-          const int b = lp < a.bt_cols ? bt_row[lp] : -1;
+          const int b = lp < a.bt_stride ? bt_row[lp] : -1;
           if (b >= 0 && b < a.num_blocks) my_blk = b;
           else flag_status(a.status, PA_DEV_BAD_BLOCK);
         }
