@@ -532,6 +532,122 @@ pa_status pa_paged_attention_shared_prefix_f8v4_view(
     void *workspace, size_t workspace_bytes, uint32_t flags, void *stream);
 
 /*
+ * The 4-bit cache format: keys and values as codes 0 .. 15 with one fp16 scale and
+ * one fp16 zero per (token, kv head, group of 32 consecutive channels); per key and
+ * kv head 2 * (D / 2 + D / 8) bytes (160 at D = 128, q8's are 272).  This library's
+ * own format; the pages show 4-bit values alone (f8v4 above).
+ *     lo, hi = min, max of the group's 32 values (fp32)
+ *     s      = max((hi - lo) * fp32(1 / 15), 1e-8)             (fp32)
+ *     code   = clamp(round_half_away((x - lo) / s), 0, 15)     (fp32 divide)
+ *     scale  = fp16(s), zero = fp16(lo);   x' = code * scale + zero
+ * Caches (head-major pages, G = D / 32 groups):
+ *     k_cache : uint8 [num_blocks][num_kv_heads][block_size][D / 2]
+ *     k_scale : fp16  [num_blocks][num_kv_heads][2][block_size][G]  scales, zeros
+ *     v_cache : uint8 [num_blocks][num_kv_heads][block_size][D / 2]
+ *     v_scale : fp16  [num_blocks][num_kv_heads][2][G][block_size]  scales, zeros
+ * The codes of a row stand in the order in which the attention's lanes read them, two
+ * to a byte, the lower nibble first: channel 32 g + c is nibble
+ *     ((c / 8) * G + g) * 8 + c % 8   of a key row,
+ *     ((c / 4) * G + g) * 4 + c % 4   of a value row.
+ * All base pointers 16-byte aligned; num_blocks * num_kv_heads * D below 2^31.
+ */
+
+/*
+ * kv_store in the 4-bit format.  Arguments as pa_kv_store.  Every token writes bytes
+ * of its own.  Values beyond +-65504, or whose range is, leave the fp16 of scale and
+ * zero (infinities).  num_tokens * num_kv_heads * head_dim below 2^34.  Asynchronous.
+ */
+pa_status pa_kv_store_q4(const void *key, int64_t key_token_stride,
+                         const void *value, int64_t value_token_stride,
+                         const int64_t *slot_mapping, int32_t num_tokens,
+                         int32_t num_kv_heads, int32_t head_dim,
+                         void *k_cache, void *k_scale, void *v_cache, void *v_scale,
+                         int32_t num_blocks, int32_t block_size,
+                         uint32_t *status, void *stream);
+
+/*
+ * kv_load -- pages of a q8 cache read back as packed bf16 K/V rows: the cached
+ * prefix that the next chunk of a prompt attends to (pa_prompt_attention), or
+ * rows on their way into another format or another cache.
+ *
+ *   key, value     bf16 rows [num_rows][num_kv_heads][head_dim] (written), token
+ *                  strides in elements as pa_kv_store's.
+ *   cu_seqlens_k   int32 [num_seqs + 1], non-decreasing, cu[S] <= num_rows: key j of
+ *                  sequence s goes to row cu[s] + j.
+ *   load_lens      int32 [num_seqs]: how many keys of s are loaded, from its first
+ *                  on, 0 .. cu[s + 1] - cu[s]; NULL: all cu[s + 1] - cu[s].  The
+ *                  other rows are left as they were (the new rows of a chunk).
+ *   block_table    int32: rows block_table_stride apart, of which
+ *                  block_table_columns entries are read.
+ * Each value is code * scale (+ zero) in fp32, rounded once to bf16.  Device checks
+ * (status, or NULL): rows out of range or a bad load_lens (PA_DEV_BAD_SEQ, the
+ * sequence is not loaded); an entry outside [0, num_blocks) or past the table's
+ * columns (PA_DEV_BAD_BLOCK, the rows of that page are not written).
+ * num_seqs == 0 or num_rows == 0 is a no-op.  Asynchronous.
+ */
+pa_status pa_kv_load(void *key, int64_t key_token_stride, void *value, int64_t value_token_stride,
+                     const int32_t *cu_seqlens_k, const int32_t *load_lens, int32_t num_seqs,
+                     int32_t num_rows, const int32_t *block_table, int32_t block_table_stride,
+                     int32_t block_table_columns, int32_t num_kv_heads, int32_t head_dim,
+                     const void *k_cache, const void *k_scale, const void *v_cache,
+                     const void *v_scale, int32_t num_blocks, int32_t block_size,
+                     uint32_t *status, void *stream);
+
+/* The same from a cache in the fp8 / 4-bit format. */
+pa_status pa_kv_load_f8v4(void *key, int64_t key_token_stride, void *value,
+                          int64_t value_token_stride, const int32_t *cu_seqlens_k,
+                          const int32_t *load_lens, int32_t num_seqs, int32_t num_rows,
+                          const int32_t *block_table, int32_t block_table_stride,
+                          int32_t block_table_columns, int32_t num_kv_heads, int32_t head_dim,
+                          const void *k_cache, const void *v_cache, const void *v_scale,
+                          const void *v_zero, int32_t num_blocks, int32_t block_size,
+                          uint32_t *status, void *stream);
+
+/* The same from a cache in the 4-bit format. */
+pa_status pa_kv_load_q4(void *key, int64_t key_token_stride, void *value,
+                        int64_t value_token_stride, const int32_t *cu_seqlens_k,
+                        const int32_t *load_lens, int32_t num_seqs, int32_t num_rows,
+                        const int32_t *block_table, int32_t block_table_stride,
+                        int32_t block_table_columns, int32_t num_kv_heads, int32_t head_dim,
+                        const void *k_cache, const void *k_scale, const void *v_cache,
+                        const void *v_scale, int32_t num_blocks, int32_t block_size,
+                        uint32_t *status, void *stream);
+
+/*
+ * paged_attention over the 4-bit format: as pa_paged_attention_ex (query lengths
+ * from 1, key segments, non-causal mode, sinks, sliding window), with these
+ * differences:
+ *   block_table    rows block_table_stride apart, of which block_table_columns
+ *                  entries are read.  Keys past them, or behind an entry outside
+ *                  [0, num_blocks), are flagged PA_DEV_BAD_BLOCK and left out.
+ *   num_splits     segments apply to every query row, not to single tokens alone:
+ *                  the workspace takes pa_workspace_size(num_tokens, num_q_heads,
+ *                  head_dim, num_splits) bytes.  With 0 a smaller workspace takes
+ *                  fewer segments, down to 256 bytes and one.
+ *   max_query_len  1: a sequence with more query tokens is left unprocessed and
+ *                  flagged PA_DEV_BAD_SEQ.  The time of a long query grows with its
+ *                  blocks of 16 rows (tokens x q heads of a kv head), each of which
+ *                  reads its keys: pa_kv_load_q4 and pa_prompt_attention are the
+ *                  faster way for chunks of hundreds of tokens.
+ *   flags          0 or PA_ATTN_NON_CAUSAL.
+ * Calls that may overlap on the GPU need workspaces of their own.  Numerics: the codes
+ * enter both products exactly; scores are scaled and summed in fp32 (q rounded to
+ * fp16; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale are rounded to fp16;
+ * sums in fp32, output bf16.
+ */
+pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
+                                const void *v_cache, const void *v_scale,
+                                const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                                const int32_t *block_table, int32_t block_table_stride,
+                                int32_t block_table_columns, int32_t num_seqs, int32_t num_tokens,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, int32_t max_query_len,
+                                int32_t max_seq_len, float softmax_scale, int32_t num_splits,
+                                const float *sinks, int32_t sliding_window, void *out, float *lse,
+                                void *workspace, size_t workspace_bytes, uint32_t flags,
+                                void *stream);
+
+/*
  * Synchronizes `stream`, reads the device status word at `status` (a kv_store
  * status word, or the start of an attention workspace), clears it, and maps
  * it to PA_OK / PA_ERR_TIMEOUT (bit 0x8 set) / PA_ERR_DEVICE_CHECK (other

@@ -20,6 +20,7 @@ __all__ = ["kv_store", "kv_store_norm_rope", "kv_store_f8v4", "paged_attention",
            "paged_attention_f8v4", "paged_attention_noalloc", "merge_attn_states",
            "build_block_tables", "BlockTables", "copy_blocks", "copy_blocks_f8v4",
            "paged_attention_shared_prefix", "paged_attention_shared_prefix_f8v4",
+           "kv_store_q4", "kv_load", "kv_load_f8v4", "kv_load_q4", "paged_attention_q4",
            "shared_prefix_workspace_size", "workspace_size", "check_status",
            "auto_num_splits", "Status", "PagedAttentionError", "library_path"]
 

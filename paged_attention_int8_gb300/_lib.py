@@ -112,6 +112,15 @@ def load():
             fn.argtypes = [P] * 8 + table + [P, P] + [i32] * 11 + [
                 ctypes.c_float, P, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
             fn.restype = ctypes.c_int
+        lib.pa_kv_store_q4.argtypes = lib.pa_kv_store.argtypes
+        lib.pa_kv_store_q4.restype = ctypes.c_int
+        for fn in (lib.pa_kv_load, lib.pa_kv_load_f8v4, lib.pa_kv_load_q4):
+            fn.argtypes = [P, i64, P, i64, P, P, i32, i32, P, i32, i32, i32, i32, P, P, P, P, i32,
+                           i32, P, P]
+            fn.restype = ctypes.c_int
+        lib.pa_paged_attention_q4.argtypes = [P] * 8 + [i32] * 11 + [
+            ctypes.c_float, i32, P, i32, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
+        lib.pa_paged_attention_q4.restype = ctypes.c_int
         lib.pa_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.pa_check_status.restype = ctypes.c_int
         lib.pa_status_string.argtypes = [ctypes.c_int]
@@ -842,6 +851,197 @@ def paged_attention_shared_prefix_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_
                           block_table, cu_groups, prefix_lens, max_query_len, max_prefix_len,
                           max_suffix_len, softmax_scale, sinks, out, lse, workspace, stream,
                           return_lse)
+
+
+def _q4_cache(dev, k_cache, k_scale, v_cache, v_scale):
+    """Checks a 4-bit cache on device number `dev`; (num_blocks, Hk, bs, D)."""
+    nb, hk, bs, half = k_cache.shape
+    for t in (k_cache, k_scale, v_cache, v_scale):
+        if t.get_device() != dev or not t.is_contiguous():
+            _refuse(dev, (torch.uint8, torch.float16, torch.int16), k_cache=k_cache,
+                    k_scale=k_scale, v_cache=v_cache, v_scale=v_scale)
+    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
+        raise TypeError("4-bit caches must be uint8")
+    if k_scale.element_size() != 2 or v_scale.element_size() != 2:
+        raise TypeError("k_scale and v_scale must hold 16-bit elements (fp16 scales and zeros)")
+    g = half // 16
+    if k_scale.shape != (nb, hk, 2, bs, g) or v_cache.shape != (nb, hk, bs, half) \
+            or v_scale.shape != (nb, hk, 2, g, bs):
+        raise ValueError(f"cache shapes {tuple(k_scale.shape), tuple(v_cache.shape)}, "
+                         f"{tuple(v_scale.shape)} != {(nb, hk, 2, bs, g), (nb, hk, bs, half)}, "
+                         f"{(nb, hk, 2, g, bs)} (k_scale, v_cache, v_scale)")
+    return nb, hk, bs, 2 * half
+
+
+def _kv_rows(dev, key, value, hk, d):
+    """Checks K/V rows [N, Hk, D] (head and channel dims contiguous); their token
+    strides, those of a single row counting as its width."""
+    n = key.shape[0]
+    for t in (key, value):
+        if t.dtype is not _BF16:
+            raise TypeError("key and value must be bf16")
+        if t.get_device() != dev:
+            raise ValueError(f"all tensors must be CUDA tensors on one device: a row tensor on {t.device}")
+        if t.shape != (n, hk, d):
+            raise ValueError(f"key and value must be [rows, {hk}, {d}], of the same rows")
+        if n and ((d > 1 and t.stride(2) != 1) or (hk > 1 and t.stride(1) != d)):
+            raise ValueError("key/value head and channel dims must be contiguous")
+    return [t.stride(0) if n > 1 else hk * d for t in (key, value)]
+
+
+def kv_store_q4(key, value, slot_mapping, k_cache, k_scale, v_cache, v_scale, status=None,
+                stream=None) -> None:
+    """Store key/value rows [N, Hk, D] (bf16) in the 4-bit format (pa_kv_store_q4):
+    codes 0 .. 15 with an fp16 scale and zero per (token, kv head, 32 channels).
+    ``k_cache`` and ``v_cache`` uint8 [num_blocks, Hk, bs, D/2], ``k_scale`` fp16
+    [num_blocks, Hk, 2, bs, D/32], ``v_scale`` fp16 [num_blocks, Hk, 2, D/32, bs]
+    (scales, then zeros).  Other arguments as kv_store."""
+    dev = key.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    nb, hk, bs, d = _q4_cache(dev, k_cache, k_scale, v_cache, v_scale)
+    ks, vs = _kv_rows(dev, key, value, hk, d)
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.get_device() != dev \
+            or not slot_mapping.is_contiguous():
+        _refuse(dev, (torch.int64,), slot_mapping=slot_mapping)
+    n = key.shape[0]
+    if slot_mapping.shape != (n,):
+        raise ValueError("key/value/slot_mapping shapes differ")
+    if status is not None and (status.dtype is not _I32 or status.get_device() != dev):
+        _refuse(dev, (_I32,), status=status)
+    _call((_lib or load()).pa_kv_store_q4, dev, stream, key.data_ptr(), ks, value.data_ptr(), vs,
+          slot_mapping.data_ptr(), n, hk, d, k_cache.data_ptr(), k_scale.data_ptr(),
+          v_cache.data_ptr(), v_scale.data_ptr(), nb, bs,
+          None if status is None else status.data_ptr())
+
+
+def _kv_load(fn, check, key, value, cu_seqlens_k, block_table, cache, load_lens, status, stream):
+    dev = key.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    nb, hk, bs, d = check(dev, *cache)
+    ks, vs = _kv_rows(dev, key, value, hk, d)
+    for t in (cu_seqlens_k, load_lens, status):
+        if t is not None and (t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous()):
+            _refuse(dev, (_I32,), cu_seqlens_k=cu_seqlens_k, load_lens=load_lens, status=status)
+    s = cu_seqlens_k.numel() - 1
+    if block_table.dtype is not _I32 or block_table.get_device() != dev:
+        raise TypeError("block_table must be an int32 CUDA tensor on the rows' device")
+    rows, columns, table_stride = _table_layout(block_table)
+    if s < 0 or rows != s or (load_lens is not None and load_lens.numel() != s):
+        raise ValueError("cu_seqlens_k [S + 1], block_table [S, ...] and load_lens [S] are wanted")
+    a, b, c, e = cache
+    _call(fn, dev, stream, key.data_ptr(), ks, value.data_ptr(), vs, cu_seqlens_k.data_ptr(),
+          None if load_lens is None else load_lens.data_ptr(), s, key.shape[0],
+          block_table.data_ptr(), table_stride, columns, hk, d, a.data_ptr(), b.data_ptr(),
+          c.data_ptr(), e.data_ptr(), nb, bs, None if status is None else status.data_ptr())
+
+
+def kv_load(key, value, cu_seqlens_k, block_table, k_cache, k_scale, v_cache, v_scale,
+            load_lens=None, status=None, stream=None) -> None:
+    """Read pages of a q8 cache back as packed bf16 rows (pa_kv_load): key j of sequence
+    s, through its row of ``block_table`` int32 [S, max_blocks], into row
+    cu_seqlens_k[s] + j of ``key`` and ``value`` [N, Hk, D] (written).
+    ``cu_seqlens_k`` int32 [S + 1]; ``load_lens`` int32 [S]: load only so many keys of
+    each sequence and leave the rest of its rows as they are (the rows of a
+    prompt's next chunk, behind its cached prefix)."""
+    _kv_load((_lib or load()).pa_kv_load, _q8_cache, key, value, cu_seqlens_k, block_table,
+             (k_cache, k_scale, v_cache, v_scale), load_lens, status, stream)
+
+
+def kv_load_f8v4(key, value, cu_seqlens_k, block_table, k_cache, v_cache, v_scale, v_zero,
+                 load_lens=None, status=None, stream=None) -> None:
+    """kv_load from a cache in the fp8 / 4-bit format (pa_kv_load_f8v4)."""
+    _kv_load((_lib or load()).pa_kv_load_f8v4, _f8v4_cache, key, value, cu_seqlens_k, block_table,
+             (k_cache, v_cache, v_scale, v_zero), load_lens, status, stream)
+
+
+def kv_load_q4(key, value, cu_seqlens_k, block_table, k_cache, k_scale, v_cache, v_scale,
+               load_lens=None, status=None, stream=None) -> None:
+    """kv_load from a cache in the 4-bit format (pa_kv_load_q4)."""
+    _kv_load((_lib or load()).pa_kv_load_q4, _q4_cache, key, value, cu_seqlens_k, block_table,
+             (k_cache, k_scale, v_cache, v_scale), load_lens, status, stream)
+
+
+def _results(dev, q, out, lse, return_lse, stream):
+    """The out and lse of an attention call over q [T, Hq, D]: checked, or allocated."""
+    if out is None:
+        with _allocating(stream, dev):
+            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    else:
+        if out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
+            _refuse(dev, (_BF16,), out=out)
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+    if lse is None:
+        if return_lse:
+            with _allocating(stream, dev):
+                lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    else:
+        if lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
+            _refuse(dev, (_F32,), lse=lse)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [T, Hq]")
+    return out, lse
+
+
+def _workspace(dev, workspace, need, stream):
+    """A call's workspace: checked, or `need()` bytes allocated with its status word zero."""
+    if workspace is None:
+        with _allocating(stream, dev):
+            workspace = torch.empty(need(), dtype=torch.uint8, device=torch.device("cuda", dev))
+            workspace[:4].zero_()
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+    return workspace
+
+
+def _check_sinks(dev, sinks, hq):
+    if sinks is not None:
+        if sinks.dtype is not _F32 or sinks.get_device() != dev or not sinks.is_contiguous():
+            _refuse(dev, (_F32,), sinks=sinks)
+        if sinks.numel() != hq:
+            raise ValueError("sinks must be [num_q_heads]")
+
+
+def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
+                       max_query_len: int, max_seq_len: int, softmax_scale: float | None = None,
+                       num_splits: int = 0, out=None, lse=None, workspace=None, stream=None,
+                       return_lse: bool = True, causal: bool = True, sinks=None,
+                       sliding_window: int = 0):
+    """paged_attention over the 4-bit format (pa_paged_attention_q4): arguments and
+    results as paged_attention, for any query lengths.  ``workspace``: optional uint8
+    CUDA tensor of ``workspace_size(T, Hq, D, num_splits)`` bytes (T query tokens) whose
+    first 4 bytes are zero; a smaller one takes fewer key segments."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    nb, hk, bs, dc = _q4_cache(dev, k_cache, k_scale, v_cache, v_scale)
+    if q.dtype is not _BF16 or not q.is_contiguous():
+        raise TypeError("q must be a contiguous bf16 tensor [T, Hq, D]")
+    t, hq, d = q.shape
+    if dc != d:
+        raise ValueError("cache shape mismatch")
+    for x in (cu_seqlens_q, seq_lens):
+        if x.dtype is not _I32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens)
+    s = seq_lens.numel()
+    if block_table.dtype is not _I32 or block_table.get_device() != dev:
+        raise TypeError("block_table must be an int32 CUDA tensor on q's device")
+    rows, columns, table_stride = _table_layout(block_table)
+    if cu_seqlens_q.numel() != s + 1 or rows != s:
+        raise ValueError("metadata shapes disagree with seq_lens")
+    _check_sinks(dev, sinks, hq)
+    out, lse = _results(dev, q, out, lse, return_lse, stream)
+    workspace = _workspace(dev, workspace, lambda: workspace_size(t, hq, d, num_splits), stream)
+    _call((_lib or load()).pa_paged_attention_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(),
+          k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), cu_seqlens_q.data_ptr(),
+          seq_lens.data_ptr(), block_table.data_ptr(), table_stride, columns, s, t, hq, hk, d, nb,
+          bs, max_query_len, max_seq_len, d ** -0.5 if softmax_scale is None else softmax_scale,
+          num_splits, None if sinks is None else sinks.data_ptr(), sliding_window, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), 0 if causal else ATTN_NON_CAUSAL)
+    return (out, lse) if return_lse else out
 
 
 def check_status(status_tensor, stream=None) -> int:

@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "merge.h"
+#include "q4.h"
 #include "serving.h"
 
 
@@ -814,3 +815,237 @@ extern "C" pa_status pa_paged_attention_noalloc(
   }
   return PA_OK;
 }
+
+// ---------------------------------------------------------------------------
+// The 4-bit cache, and the read-back of all formats.
+namespace {
+
+// What the calls over a cache check of it; false: *st holds the error.
+bool cache_ok(int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
+              std::initializer_list<const void *> arrays, pa_status *st) {
+  *st = PA_ERR_INVALID_ARG;
+  for (const void *p : arrays)
+    if (!p) return fail(*st, "null pointer"), false;
+  if (num_kv_heads <= 0 || num_blocks <= 0)
+    return fail(*st, "num_kv_heads and num_blocks must be positive"), false;
+  if (misaligned(15, arrays)) return fail(*st, "cache pointers must be 16-byte aligned"), false;
+  *st = PA_ERR_UNSUPPORTED;
+  if (!supported_dim(head_dim)) return fail(*st, "head_dim must be 64, 128 or 256"), false;
+  if (!supported_bs(block_size)) return fail(*st, "block_size must be 16 or 32"), false;
+  if (static_cast<int64_t>(num_blocks) * num_kv_heads >= (int64_t{1} << 31) / head_dim)
+    return fail(*st, "num_blocks * num_kv_heads * head_dim must be < 2^31"), false;
+  *st = PA_OK;
+  return true;
+}
+
+// Token strides of the K and V rows of a call.
+bool rows_ok(const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+             int32_t num_kv_heads, int32_t head_dim, pa_status *st) {
+  *st = PA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (!key || !value) return fail(*st, "null pointer"), false;
+  if (key_stride < row || value_stride < row)
+    return fail(*st, "token stride smaller than num_kv_heads * head_dim"), false;
+  if (key_stride % 8 || value_stride % 8 || misaligned(15, {key, value}))
+    return fail(*st, "key/value rows must be 16-byte aligned"), false;
+  *st = PA_OK;
+  return true;
+}
+
+pa_status kv_load(paq8::CacheFormat format, void *key, int64_t key_token_stride, void *value,
+                  int64_t value_token_stride, const int32_t *cu_seqlens_k,
+                  const int32_t *load_lens, int32_t num_seqs, int32_t num_rows,
+                  const int32_t *block_table, int32_t block_table_stride,
+                  int32_t block_table_columns, int32_t num_kv_heads, int32_t head_dim,
+                  const void *a0, const void *a1, const void *a2, const void *a3,
+                  int32_t num_blocks, int32_t block_size, uint32_t *status, void *stream) {
+  g_last_error[0] = '\0';
+  if (num_seqs < 0 || num_rows < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+  if (num_seqs == 0 || num_rows == 0) return PA_OK;
+  if (!cu_seqlens_k || !block_table) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  pa_status st;
+  if (!rows_ok(key, key_token_stride, value, value_token_stride, num_kv_heads, head_dim, &st))
+    return st;
+  if (!cache_ok(num_kv_heads, head_dim, num_blocks, block_size, {a0, a1, a2, a3}, &st)) return st;
+  if (block_table_columns <= 0 || block_table_stride < block_table_columns)
+    return fail(PA_ERR_INVALID_ARG, "the block table's columns must be positive, its row stride no "
+                                    "less than them");
+  if (misaligned(3, {cu_seqlens_k, load_lens, block_table, status}))
+    return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  const int64_t units = (static_cast<int64_t>(num_rows) / block_size + num_seqs) * num_kv_heads;
+  if (static_cast<int64_t>(num_rows) + num_seqs >= (int64_t{1} << 31) || units >= (int64_t{1} << 32))
+    return fail(PA_ERR_UNSUPPORTED, "too many rows in one call: split the sequences");
+  paq8::KvLoad p;
+  p.key = static_cast<uint16_t *>(key);
+  p.value = static_cast<uint16_t *>(value);
+  p.key_stride = key_token_stride;
+  p.value_stride = value_token_stride;
+  p.cu_seqlens_k = cu_seqlens_k;
+  p.load_lens = load_lens;
+  p.num_seqs = num_seqs;
+  p.num_rows = num_rows;
+  p.block_table = block_table;
+  p.table_stride = block_table_stride;
+  p.table_columns = block_table_columns;
+  p.hk = num_kv_heads;
+  p.d = head_dim;
+  p.array[0] = a0;
+  p.array[1] = a1;
+  p.array[2] = a2;
+  p.array[3] = a3;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.status = status;
+  const cudaError_t e = paq8::launch_kv_load(p, format, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_kv_store_q4(const void *key, int64_t key_token_stride, const void *value,
+                         int64_t value_token_stride, const int64_t *slot_mapping,
+                         int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                         void *k_cache, void *k_scale, void *v_cache, void *v_scale,
+                         int32_t num_blocks, int32_t block_size, uint32_t *status, void *stream) {
+  g_last_error[0] = '\0';
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_tokens == 0) return PA_OK;
+  if (!slot_mapping) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  pa_status st;
+  if (!rows_ok(key, key_token_stride, value, value_token_stride, num_kv_heads, head_dim, &st))
+    return st;
+  if (!cache_ok(num_kv_heads, head_dim, num_blocks, block_size, {k_cache, k_scale, v_cache, v_scale},
+                &st))
+    return st;
+  if (misaligned(7, {slot_mapping}))
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
+  if (misaligned(3, {status})) return fail(PA_ERR_INVALID_ARG, "status must be 4-byte aligned");
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads >= (int64_t{1} << 31) / (head_dim / 8) - 4096)
+    return fail(PA_ERR_UNSUPPORTED, "num_tokens * num_kv_heads * head_dim must be < 2^34: split the tokens");
+  paq8::KvStoreQ4 p;
+  p.key = static_cast<const uint16_t *>(key);
+  p.value = static_cast<const uint16_t *>(value);
+  p.key_stride = key_token_stride;
+  p.value_stride = value_token_stride;
+  p.slot_mapping = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.hk = num_kv_heads;
+  p.d = head_dim;
+  p.k_cache = static_cast<uint8_t *>(k_cache);
+  p.v_cache = static_cast<uint8_t *>(v_cache);
+  p.k_scale = static_cast<uint16_t *>(k_scale);
+  p.v_scale = static_cast<uint16_t *>(v_scale);
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.status = status;
+  const cudaError_t e = paq8::launch_kv_store_q4(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+#define PAQ8_KV_LOAD(name, format)                                                                \
+  pa_status name(void *key, int64_t key_token_stride, void *value, int64_t value_token_stride,    \
+                 const int32_t *cu_seqlens_k, const int32_t *load_lens, int32_t num_seqs,         \
+                 int32_t num_rows, const int32_t *block_table, int32_t block_table_stride,        \
+                 int32_t block_table_columns, int32_t num_kv_heads, int32_t head_dim,             \
+                 const void *a0, const void *a1, const void *a2, const void *a3,                  \
+                 int32_t num_blocks, int32_t block_size, uint32_t *status, void *stream) {        \
+    return kv_load(paq8::CacheFormat::format, key, key_token_stride, value, value_token_stride,   \
+                   cu_seqlens_k, load_lens, num_seqs, num_rows, block_table, block_table_stride,  \
+                   block_table_columns, num_kv_heads, head_dim, a0, a1, a2, a3, num_blocks,       \
+                   block_size, status, stream);                                                   \
+  }
+PAQ8_KV_LOAD(pa_kv_load, q8)
+PAQ8_KV_LOAD(pa_kv_load_f8v4, f8v4)
+PAQ8_KV_LOAD(pa_kv_load_q4, q4)
+#undef PAQ8_KV_LOAD
+
+pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
+                                const void *v_cache, const void *v_scale,
+                                const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                                const int32_t *block_table, int32_t block_table_stride,
+                                int32_t block_table_columns, int32_t num_seqs, int32_t num_tokens,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, int32_t max_query_len,
+                                int32_t max_seq_len, float softmax_scale, int32_t num_splits,
+                                const float *sinks, int32_t sliding_window, void *out, float *lse,
+                                void *workspace, size_t workspace_bytes, uint32_t flags,
+                                void *stream) {
+  g_last_error[0] = '\0';
+  if (flags & ~PA_ATTN_NON_CAUSAL) return fail(PA_ERR_INVALID_ARG, "unknown flag bits");
+  const bool causal = !(flags & PA_ATTN_NON_CAUSAL);
+  if (num_seqs < 0 || num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "null workspace");
+  if (sliding_window < 0) return fail(PA_ERR_INVALID_ARG, "sliding_window < 0");
+  if (sliding_window > 0 && !causal)
+    return fail(PA_ERR_INVALID_ARG, "a sliding window needs causal attention");
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!q || !cu_seqlens_q || !seq_lens || !block_table || !out)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  pa_status st;
+  if (!cache_ok(num_kv_heads, head_dim, num_blocks, block_size, {k_cache, k_scale, v_cache, v_scale},
+                &st))
+    return st;
+  if (num_q_heads <= 0 || num_q_heads % num_kv_heads)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (num_q_heads / num_kv_heads > 16)
+    return fail(PA_ERR_UNSUPPORTED, "more than 16 q heads per kv head");
+  if (block_table_columns <= 0 || block_table_stride < block_table_columns)
+    return fail(PA_ERR_INVALID_ARG, "the block table's columns must be positive, its row stride no "
+                                    "less than them");
+  if (max_query_len <= 0 || max_seq_len <= 0 || max_seq_len > 0x7fffffff - 4096)
+    return fail(PA_ERR_INVALID_ARG, "max_query_len and max_seq_len must be positive");
+  if (num_splits < 0 || num_splits > 16) return fail(PA_ERR_INVALID_ARG, "num_splits in [0, 16]");
+  if (misaligned(15, {q, out, workspace}))
+    return fail(PA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned(3, {lse, sinks, cu_seqlens_q, seq_lens, block_table}))
+    return fail(PA_ERR_INVALID_ARG, "lse, sinks and the int32 arrays must be 4-byte aligned");
+  // items of rows, and rows of the join, of all kv heads and segments: one grid
+  if (static_cast<int64_t>(num_tokens) + num_seqs >= (int64_t{1} << 31) ||
+      (static_cast<int64_t>(num_tokens) + num_seqs) * num_q_heads >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "(num_tokens + num_seqs) * num_q_heads must be < 2^31");
+  const int32_t seen = sliding_window > 0 && sliding_window < max_seq_len ? sliding_window : max_seq_len;
+  int32_t ns = num_splits == 0 ? paq8::q4_auto_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                      head_dim, max_query_len, seen)
+                               : num_splits;
+  if (num_splits == 0)
+    while (ns > 1 && workspace_bytes < pa_workspace_size(num_tokens, num_q_heads, head_dim, ns)) --ns;
+  if (workspace_bytes < pa_workspace_size(num_tokens, num_q_heads, head_dim, ns))
+    return fail(PA_ERR_INVALID_ARG, ns > 1 ? "workspace too small for num_splits"
+                                           : "workspace smaller than 256 bytes");
+  if ((static_cast<int64_t>(num_tokens) + num_seqs) * num_kv_heads * ns >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED, "(num_tokens + num_seqs) * num_kv_heads * num_splits must be < 2^31");
+  paq8::AttnQ4 p;
+  p.q = static_cast<const uint16_t *>(q);
+  p.k_cache = static_cast<const uint8_t *>(k_cache);
+  p.v_cache = static_cast<const uint8_t *>(v_cache);
+  p.k_scale = static_cast<const uint16_t *>(k_scale);
+  p.v_scale = static_cast<const uint16_t *>(v_scale);
+  p.cu = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.block_table = block_table;
+  p.table_stride = block_table_stride;
+  p.table_columns = block_table_columns;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.hq = num_q_heads;
+  p.hk = num_kv_heads;
+  p.d = head_dim;
+  p.num_blocks = num_blocks;
+  p.bs = block_size;
+  p.max_query_len = max_query_len;
+  p.max_seq_len = max_seq_len;
+  p.num_splits = ns;
+  p.softmax_scale = softmax_scale;
+  p.sinks = sinks;
+  p.window = sliding_window;
+  p.causal = causal;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.workspace = static_cast<uint8_t *>(workspace);
+  const cudaError_t e = paq8::launch_attention_q4(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,727 @@
+// Attention over the 4-bit cache (q4.cuh): for query row i of a sequence (a token and a
+// q head), over its visible keys j,
+//   s_j = scale * q . k_j,  out = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - m),
+//   lse = m + ln sum_j p_j,   with k_j, v_j = code * scale + zero per 32 channels.
+//
+// Bound by HBM for single tokens: 5/4 D bytes a (key, kv head).  Everything is read
+// once by warps whose lanes hold the codes of their MMA fragments, and no code is
+// turned into a number by arithmetic: a nibble masked out of its word is, as fp16, the
+// subnormal code * 2^-24 (or 16 code * 2^-24 for the upper nibble of a byte), exact in
+// the tensor cores, and the powers of two leave in fp32.
+//   Scores  S^T[16 keys x 8 rows] = K[16 x 16 ch] Q^T[16 ch x 8 rows], keys in the
+//     MMA's M dimension.  Per group s_g sum q c is scaled in fp32; the zeros' part
+//     sum_g z_g (sum q)_g is one more MMA over the groups, with the q sums as two fp16
+//     parts (22 bits; q is a row's, formed once).  No rounding but q to fp16.
+//   Output  O^T[16 ch x 8 rows] += V^T P^T, where the key's scale goes into P: per
+//     group P_g = fp16(p s_g), so that the codes again enter as they are; the zeros'
+//     part is one more MMA (groups in M).  p and p s_g are rounded to fp16 (2^-11);
+//     p is at most 4 and s_g at most 8734, so the product stays inside fp16.
+// The maximum that p is taken against moves only when a score passes it by 2 (p above
+// 4): one vote a block of keys instead of a reduction.
+//
+// A thread block takes 8 NB rows (tokens x the q heads of a kv head) and a segment of
+// the keys; its four warps work on their own 16-key blocks, each with its own ring of
+// asynchronous copies, and join their sums at the end.  Segments leave fp32 triples
+// that q4_join_kernel merges.
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "launch.h"
+#include "programmatic.cuh"
+#include "q4.cuh"
+#include "q4.h"
+
+namespace paq8 {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kMargin = 2.0f;  // log2 of the largest p
+
+struct Q4Args {
+  AttnQ4 p;
+  uint32_t *status;
+  float *part_acc;   // [T * Hq][splits][D]
+  float2 *part_ml;   // [T * Hq][splits]
+  int32_t qpk, block_tokens, num_items, seg_blocks, num_splits;
+  float scale_log2;
+};
+
+// Ring depth by the bytes of a 16-key block (20 D): what keeps about 100 KB an SM in flight.
+template <int D>
+struct Q4Cfg {
+  static constexpr int G = D / 32;
+  static constexpr int kRow = D / 2;                 // bytes of a row's codes
+  static constexpr int kKs = 16 * kRow;              // K scales [16][G], zeros [16][G]
+  static constexpr int kV = kKs + 16 * G * 4;        // V codes
+  static constexpr int kVs = kV + 16 * kRow;         // V scales [G][16], zeros [G][16]
+  static constexpr int kBlock = kVs + 16 * G * 4;    // 20 D bytes
+  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 5 : 4;
+};
+
+// Visible keys of the block of rows that starts at token tok0 of a sequence, in
+// 16-key blocks: what the kernel and the join agree on.
+struct KeyRange {
+  int begin, end;        // keys
+  int first, blocks;     // 16-key blocks
+};
+
+__device__ __forceinline__ KeyRange key_range(const Q4Args &a, int seq_len, int q_len, int tok0) {
+  const int n_tok = min(a.block_tokens, q_len - tok0);
+  const int last0 = a.p.causal ? seq_len - q_len + tok0 : seq_len - 1;
+  const int last1 = a.p.causal ? last0 + n_tok - 1 : last0;
+  KeyRange r;
+  r.end = max(0, last1 + 1);
+  r.begin = a.p.window > 0 ? max(0, last0 - a.p.window + 1) : 0;
+  r.first = r.begin / 16;
+  r.blocks = r.end > r.begin ? (r.end + 15) / 16 - r.first : 0;
+  return r;
+}
+
+__device__ __forceinline__ int segments(const Q4Args &a, int blocks) {
+  return min(a.num_splits, max(1, (blocks + a.seg_blocks - 1) / a.seg_blocks));
+}
+
+// The bounds of a sequence's metadata that the kernels rely on.
+__device__ __forceinline__ bool valid_sequence(const Q4Args &a, int q0, int q_len, int seq_len) {
+  return q0 >= 0 && q_len >= 0 && q0 <= a.p.num_tokens - q_len && seq_len >= (a.p.causal ? q_len : 0) &&
+         (a.p.max_query_len > 1 || q_len <= 1);
+}
+
+// D = A B, m16n8k16, fp16 inputs, fp32 accumulators, no addend.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ float half_lo(uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+}
+__device__ __forceinline__ float half_hi(uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
+}
+
+// N 32-bit words from shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = lds32(addr);
+  } else if constexpr (N == 2) {
+    const uint2 v = lds64(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = lds128(addr + 4 * i);
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    }
+  }
+}
+
+// Where 16-byte chunk c of key r's codes lies in a staged block.  K rows stand in
+// the order of the score MMA's rows, V rows in the order in which the four lanes of
+// a channel row read them, so that the rows of one load are neighbours; chunks of
+// wider rows are exchanged so that the lanes of one phase meet no bank twice.
+template <int D>
+__device__ __forceinline__ uint32_t k_place(int r, int c) {
+  const int row = (r >> 2) * 2 + (r & 1) + ((r >> 1) & 1) * 8;  // inverse of perm16
+  return row * (D / 2) + ((D == 256 ? c ^ (row & 1) : c) * 16);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_place(int r, int c) {
+  const int t = r >> 2, i = r & 3;
+  const int x = D == 256 ? 2 * t : D == 128 ? (t >> 1) * 2 : 0;
+  return (i * 4 + t) * (D / 2) + (c ^ x) * 16;
+}
+
+template <int D, int BS, int NB>
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (NB == 2 ? 3 : 5))
+    attn_q4_kernel(const __grid_constant__ Q4Args a) {
+  using C = Q4Cfg<D>;
+  constexpr int G = C::G;
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  wait_for_predecessor();
+  launch_dependents();  // the join waits for all of this grid
+  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.p.hk));
+  const int rest = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.p.hk));
+  const int item = rest % a.num_items;
+  const int sigma = rest / a.num_items;
+
+  // ---- which rows, which keys
+  int seq = item, tok0 = 0;
+  if (a.p.max_query_len > 1) {
+    seq = find_seq(a.p.cu, a.p.num_seqs, a.block_tokens, item, lane);
+    const int c0 = a.p.cu[seq];
+    tok0 = (item - ((a.block_tokens == 1 ? c0 : c0 / a.block_tokens + seq))) * a.block_tokens;
+  }
+  const int q0 = a.p.cu[seq];
+  const int q_len = a.p.cu[seq + 1] - q0;
+  const int seq_len = a.p.seq_lens[seq];
+  if (tok0 < 0 || tok0 >= q_len) {
+    if (q_len < 0 && sigma == 0 && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+    return;
+  }
+  if (!valid_sequence(a, q0, q_len, seq_len)) {
+    if (sigma == 0 && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+    return;
+  }
+  const KeyRange range = key_range(a, seq_len, q_len, tok0);
+  if (sigma >= segments(a, range.blocks)) return;
+  const int n_rows = min(a.block_tokens, q_len - tok0) * a.qpk;
+  const int seg0 = range.first + sigma * a.seg_blocks;
+  const int seg1 = sigma == a.num_splits - 1 ? range.first + range.blocks
+                                             : min(range.first + range.blocks, seg0 + a.seg_blocks);
+
+  // ---- q as the B operand: lane (g, t) holds row 8 nb + g
+  //   group gr, step e: channels 32 gr + 8 t + 2 e' of the nibbles that step e's words
+  //   hold: step 0 nibbles (0, 4 | 1, 5), step 1 nibbles (2, 6 | 3, 7); the second pair
+  //   of each meets codes of weight 16 and is divided by it (exact down to 2^-13)
+  uint32_t qb[NB][G][2][2];
+  uint32_t qs[NB][2];  // sums over groups 2t, 2t + 1 of row g: fp16 high and low parts
+  int lim[NB][2], lo[NB][2];  // visible keys of rows 8 nb + 2t, + 1
+  int min_lim = 0x7fffffff, max_lo = 0;
+  bool bad_q = false;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = nb * 8 + g;
+    const bool real = row < n_rows;
+    const int tok = q0 + tok0 + (real ? row / a.qpk : 0);
+    const uint16_t *src = a.p.q + (static_cast<int64_t>(tok) * a.p.hq + h * a.qpk + (real ? row % a.qpk : 0)) * D;
+    float sums[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (real) v = *reinterpret_cast<const uint4 *>(src + gr * 32 + t * 8);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+        bad_q |= half2_nonfinite(pack_half2(x[2 * i], x[2 * i + 1]));
+      }
+      qb[nb][gr][0][0] = pack_half2(x[0], x[4]);
+      qb[nb][gr][0][1] = pack_half2(x[1] * 0.0625f, x[5] * 0.0625f);
+      qb[nb][gr][1][0] = pack_half2(x[2], x[6]);
+      qb[nb][gr][1][1] = pack_half2(x[3] * 0.0625f, x[7] * 0.0625f);
+      sums[gr] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    }
+    float mine[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      sums[gr] += __shfl_xor_sync(0xffffffffu, sums[gr], 1);
+      sums[gr] += __shfl_xor_sync(0xffffffffu, sums[gr], 2);
+      // over 32, so that 32 values of the fp16 range stay inside it
+      if (gr >> 1 == t) mine[gr & 1] = sums[gr] * 0.03125f;
+    }
+    const float hi0 = __half2float(__float2half_rn(mine[0])), hi1 = __half2float(__float2half_rn(mine[1]));
+    qs[nb][0] = pack_half2(hi0, hi1);
+    qs[nb][1] = pack_half2(mine[0] - hi0, mine[1] - hi1);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nb * 8 + 2 * t + c;
+      // rows past the last take its keys, so that their arithmetic stays finite
+      const int i = tok0 + (r < n_rows ? r : n_rows - 1) / a.qpk;
+      lim[nb][c] = a.p.causal ? seq_len - q_len + i : seq_len - 1;
+      lo[nb][c] = a.p.window > 0 ? max(0, lim[nb][c] - a.p.window + 1) : 0;
+      min_lim = min(min_lim, lim[nb][c]);
+      max_lo = max(max_lo, lo[nb][c]);
+    }
+  }
+  if (__any_sync(0xffffffffu, bad_q) && warp == 0 && lane == 0 && sigma == 0)
+    flag_status(a.status, PA_DEV_BAD_Q);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
+    max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
+  }
+
+  // ---- this warp's copies: block b of the segment for b % 4 == warp
+  const uint32_t ring = smem_u32(smem_raw) + warp * (C::kStages * C::kBlock);
+  const int n_mine = (seg1 - seg0 - warp + kWarps - 1) / kWarps;  // may be <= 0
+  constexpr int kCodeChunks = 16 * C::kRow / 16;  // of K, and of V
+  constexpr int kScChunks = 16 * G * 2 / 16;      // of one plane of scales or zeros
+  constexpr int kPlane = BS * G * 2;              // bytes of a page's plane
+  const int32_t *table = a.p.block_table + static_cast<int64_t>(seq) * a.p.table_stride;
+  int entries = -1;  // page of this warp's block (32 i + lane), refilled every 32 blocks
+  auto refill = [&](int i) {
+    const int b = seg0 + warp + (i + lane) * kWarps;
+    entries = -1;
+    if (i + lane < n_mine) {
+      const int page = b * 16 / BS;
+      const int e = page < a.p.table_columns ? table[page] : -1;
+      if (e >= 0 && e < a.p.num_blocks) entries = e;
+      else flag_status(a.status, PA_DEV_BAD_BLOCK);
+    }
+  };
+  uint32_t live = 0;  // bit s: stage s holds a block of a valid page
+  auto issue = [&](int i) {  // copies of this warp's i-th block
+    if ((i & 31) == 0 && i < n_mine) refill(i);
+    const int e = __shfl_sync(0xffffffffu, entries, i & 31);
+    const int stage = i % C::kStages;
+    live &= ~(1u << stage);
+    if (i < n_mine && e >= 0) {
+      live |= 1u << stage;
+      const uint32_t st = ring + stage * C::kBlock;
+      const int64_t page = static_cast<int64_t>(e) * a.p.hk + h;
+      const int off = BS == 32 ? ((seg0 + warp + i * kWarps) & 1) * 16 : 0;  // first key in the page
+      const uint8_t *kc = a.p.k_cache + (page * BS + off) * C::kRow;
+      const uint8_t *vc = a.p.v_cache + (page * BS + off) * C::kRow;
+#pragma unroll
+      for (int k = 0; k < kCodeChunks; k += 32) {
+        const int c = k + lane;
+        cp_async_16(st + k_place<D>(c / (C::kRow / 16), c % (C::kRow / 16)), kc + c * 16);
+      }
+#pragma unroll
+      for (int k = 0; k < kCodeChunks; k += 32) {
+        const int c = k + lane;
+        cp_async_16(st + C::kV + v_place<D>(c / (C::kRow / 16), c % (C::kRow / 16)), vc + c * 16);
+      }
+      const uint8_t *ks = reinterpret_cast<const uint8_t *>(a.p.k_scale) + page * (2 * kPlane);
+      const uint8_t *vs = reinterpret_cast<const uint8_t *>(a.p.v_scale) + page * (2 * kPlane);
+#pragma unroll
+      for (int k = 0; k < 4 * kScChunks; k += 32) {
+        const int c = k + lane;  // planes: K scales, K zeros, V scales, V zeros
+        if (c < 4 * kScChunks) {
+          const int plane = (c / kScChunks) & 1, x = c % kScChunks;
+          if (c < 2 * kScChunks)
+            cp_async_16(st + C::kKs + c * 16, ks + plane * kPlane + off * (G * 2) + x * 16);
+          else  // rows of BS keys: two chunks of 16 keys each
+            cp_async_16(st + C::kVs + (c - 2 * kScChunks) * 16,
+                        vs + plane * kPlane + (x >> 1) * (BS * 2) + off * 2 + (x & 1) * 16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+
+  float m_used[NB][2], l[NB][2];  // rows 2t, 2t + 1 (log2 units; l: this lane's share)
+  float o[NB][G][2][4], oz[NB][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      m_used[nb][c] = -INFINITY;
+      l[nb][c] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      oz[nb][e] = 0.0f;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) o[nb][gr][0][e] = o[nb][gr][1][e] = 0.0f;
+    }
+  }
+  const float c1 = a.scale_log2 * 0x1p24f;  // of sum_g s_g (q c 2^-24)
+  const float c2 = a.scale_log2 * 32.0f;    // of sum_g z_g (q sum / 32)
+  const int key_r0 = perm16(g), key_r1 = perm16(g + 8);
+
+  for (int i = 0; i < n_mine; ++i) {
+    cp_async_wait<C::kStages - 2>();
+    __syncwarp();
+    issue(i + C::kStages - 1);  // into the stage that the last block left
+    const int stage = i % C::kStages;
+    if (!((live >> stage) & 1u)) continue;  // no such page: its keys are left out
+    const uint32_t st = ring + stage * C::kBlock;
+    const int key0 = (seg0 + warp + i * kWarps) * 16;
+
+    // ---- scores
+    float s[NB][4];
+    {
+      uint32_t w0[G], w1[G];  // codes of key rows g and g + 8, one word a group
+      if constexpr (D == 256) {
+        const int x = g & 1;  // rows g and g + 8: the same parity
+        const uint32_t r0 = st + g * C::kRow + t * 32, r1 = r0 + 8 * C::kRow;
+        const uint4 a0 = lds128(r0 + x * 16), a1 = lds128(r0 + (x ^ 1) * 16);
+        const uint4 b0 = lds128(r1 + x * 16), b1 = lds128(r1 + (x ^ 1) * 16);
+        w0[0] = a0.x; w0[1] = a0.y; w0[2] = a0.z; w0[3] = a0.w;
+        w0[4] = a1.x; w0[5] = a1.y; w0[6] = a1.z; w0[7] = a1.w;
+        w1[0] = b0.x; w1[1] = b0.y; w1[2] = b0.z; w1[3] = b0.w;
+        w1[4] = b1.x; w1[5] = b1.y; w1[6] = b1.z; w1[7] = b1.w;
+      } else {
+        lds_words(st + g * C::kRow + t * (G * 4), w0);
+        lds_words(st + (g + 8) * C::kRow + t * (G * 4), w1);
+      }
+      uint32_t sw0[G / 2], sw1[G / 2];  // scales of the two keys, two groups a word
+      lds_words(st + C::kKs + key_r0 * (G * 2), sw0);
+      lds_words(st + C::kKs + key_r1 * (G * 2), sw1);
+      const bool has = 2 * t < G;
+      const uint32_t zk = st + C::kKs + 16 * G * 2 + (has ? 4 * t : 0);
+      uint32_t z0 = lds32(zk + key_r0 * (G * 2)), z1 = lds32(zk + key_r1 * (G * 2));
+      if (!has) z0 = z1 = 0u;
+      float acc[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nb][e] = 0.0f;
+      }
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const uint32_t lo4 = 0x000f000fu, hi4 = 0x00f000f0u;
+        const uint32_t u0 = w0[gr] >> 8, u1 = w1[gr] >> 8;
+        const float s0 = gr & 1 ? half_hi(sw0[gr >> 1]) : half_lo(sw0[gr >> 1]);
+        const float s1 = gr & 1 ? half_hi(sw1[gr >> 1]) : half_lo(sw1[gr >> 1]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float part[4];
+          mma_first(part, w0[gr] & lo4, w1[gr] & lo4, w0[gr] & hi4, w1[gr] & hi4, qb[nb][gr][0][0],
+                    qb[nb][gr][0][1]);
+          mma_f16_16816(part, u0 & lo4, u1 & lo4, u0 & hi4, u1 & hi4, qb[nb][gr][1][0],
+                        qb[nb][gr][1][1]);
+          acc[nb][0] = fmaf(s0, part[0], acc[nb][0]);
+          acc[nb][1] = fmaf(s0, part[1], acc[nb][1]);
+          acc[nb][2] = fmaf(s1, part[2], acc[nb][2]);
+          acc[nb][3] = fmaf(s1, part[3], acc[nb][3]);
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float zp[4];
+        mma_first(zp, z0, z1, z0, z1, qs[nb][0], qs[nb][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nb][e] = fmaf(acc[nb][e], c1, zp[e] * c2);
+      }
+    }
+    // keys that a row does not see (and stale ones: whatever stands there)
+    if (key0 + 15 > min_lim || key0 < max_lo) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + (e < 2 ? key_r0 : key_r1);
+          if (key > lim[nb][e & 1] || key < lo[nb][e & 1]) s[nb][e] = -INFINITY;
+        }
+    }
+
+    // ---- softmax against m_used, which moves only when a score passes it by kMargin
+    bool over = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) over = over || s[nb][e] > m_used[nb][e & 1] + kMargin;
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(s[nb][c], s[nb][2 + c]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          const float mn = fmaxf(m_used[nb][c], mx);
+          const float f = mn == -INFINITY ? 1.0f : fast_exp2(m_used[nb][c] - mn);
+          m_used[nb][c] = mn;
+          l[nb][c] *= f;
+          oz[nb][c] *= f;
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            o[nb][gr][0][c] *= f;
+            o[nb][gr][0][2 + c] *= f;
+            o[nb][gr][1][c] *= f;
+            o[nb][gr][1][2 + c] *= f;
+          }
+        }
+    }
+    uint32_t pb[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float m = m_used[nb][e & 1];
+        p[e] = fast_exp2(s[nb][e] - (m == -INFINITY ? 0.0f : m));
+      }
+      l[nb][0] += p[0] + p[2];
+      l[nb][1] += p[1] + p[3];
+      pb[nb][0] = movmatrix_trans(pack_half2(p[0], p[1]));
+      pb[nb][1] = movmatrix_trans(pack_half2(p[2], p[3]));
+    }
+
+    // ---- output: keys 4t .. 4t + 3
+    const bool tail = key0 + 16 > range.end || key0 < range.begin;
+    uint2 keep = make_uint2(0xffffffffu, 0xffffffffu);  // keys that no row sees may hold anything
+    if (tail) {
+      const auto in = [&](int k) { return k >= range.begin && k < range.end; };
+      const int k = key0 + 4 * t;
+      keep.x = (in(k) ? 0x0000ffffu : 0u) | (in(k + 1) ? 0xffff0000u : 0u);
+      keep.y = (in(k + 2) ? 0x0000ffffu : 0u) | (in(k + 3) ? 0xffff0000u : 0u);
+    }
+    {
+      uint2 z = lds64(st + C::kVs + (G + (g < G ? g : 0)) * 32 + t * 8);
+      if (g >= G) z = make_uint2(0u, 0u);
+      z.x &= keep.x;
+      z.y &= keep.y;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) mma_f16_16816(oz[nb], z.x, 0u, z.y, 0u, pb[nb][0], pb[nb][1]);
+    }
+    constexpr int W = G / 2;  // words of a lane's codes of one key: 16 bits a group
+    uint32_t vw[4][W];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = D == 256 ? 2 * t : D == 128 ? (t >> 1) * 2 : 0;
+      const int byte = g * (G * 2);
+      lds_words(st + C::kV + (k * 4 + t) * C::kRow + (((byte >> 4) ^ x) << 4) + (byte & 15), vw[k]);
+    }
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      uint2 sc = lds64(st + C::kVs + gr * 32 + t * 8);
+      sc.x &= keep.x;
+      sc.y &= keep.y;
+      const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
+      const uint32_t x01 = __byte_perm(vw[0][gr >> 1], vw[1][gr >> 1], sel);
+      const uint32_t x23 = __byte_perm(vw[2][gr >> 1], vw[3][gr >> 1], sel);
+      const uint32_t lo4 = 0x000f000fu, hi4 = 0x00f000f0u;
+      const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint32_t p0 = hmul2_u32(pb[nb][0], sc.x), p1 = hmul2_u32(pb[nb][1], sc.y);
+        mma_f16_16816(o[nb][gr][0], x01 & lo4, y01 & lo4, x23 & lo4, y23 & lo4, p0, p1);
+        mma_f16_16816(o[nb][gr][1], x01 & hi4, y01 & hi4, x23 & hi4, y23 & hi4, p0, p1);
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // ---- O^T of this warp as numbers: channels 32 gr + 4 g + i of rows 2t, 2t + 1
+  // (nibble i: o[gr][i & 1][(i & 2) + row]), the zeros' part from the lane of its group
+  float out[NB][2][G][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float z = __shfl_sync(0xffffffffu, oz[nb][c], gr * 4 + t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          out[nb][c][gr][i] = fmaf(o[nb][gr][i & 1][(i & 2) + c], i & 1 ? 0x1p20f : 0x1p24f, z);
+      }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], off);
+
+  // ---- the four warps' sums joined by warp 0 (the rings are no longer read)
+  constexpr int kFields = NB * (4 + 8 * G);
+  float *area = reinterpret_cast<float *>(smem_raw);
+  __syncthreads();
+  if (warp > 0) {
+    float *dst = area + (warp - 1) * kFields * 32 + lane;
+    int f = 0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        dst[32 * f++] = m_used[nb][c];
+        dst[32 * f++] = l[nb][c];
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[32 * f++] = out[nb][c][gr][i];
+      }
+  }
+  __syncthreads();
+  if (warp > 0) return;
+#pragma unroll 1
+  for (int k = 0; k < kWarps - 1; ++k) {
+    const float *src = area + k * kFields * 32 + lane;
+    int f = 0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mo = src[32 * f++];
+        const float mn = fmaxf(m_used[nb][c], mo);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        const float wa = fast_exp2(m_used[nb][c] - mu), wb = fast_exp2(mo - mu);
+        m_used[nb][c] = mn;
+        l[nb][c] = l[nb][c] * wa + src[32 * f++] * wb;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[nb][c][gr][i] = out[nb][c][gr][i] * wa + src[32 * f++] * wb;
+      }
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = nb * 8 + 2 * t + c;
+      if (row >= n_rows) continue;
+      const int64_t tok = q0 + tok0 + row / a.qpk;
+      const int head = h * a.qpk + row % a.qpk;
+      const int64_t at = tok * a.p.hq + head;
+      float m = m_used[nb][c], sum = l[nb][c];
+      if (a.num_splits > 1) {
+        const int64_t prow = at * a.num_splits + sigma;
+        if (g == 0) a.part_ml[prow] = make_float2(m, sum);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+          *reinterpret_cast<float4 *>(a.part_acc + prow * D + gr * 32 + g * 4) =
+              make_float4(out[nb][c][gr][0], out[nb][c][gr][1], out[nb][c][gr][2], out[nb][c][gr][3]);
+        continue;
+      }
+      float w = 1.0f;
+      if (a.p.sinks) {
+        const float sk = a.p.sinks[head] * kLog2e;
+        const float mn = fmaxf(m, sk);
+        if (mn > -INFINITY) {
+          w = fast_exp2(m - mn);
+          sum = sum * w + fast_exp2(sk - mn);
+          m = mn;
+        }
+      }
+      const float inv = sum > 0.0f ? w / sum : 0.0f;  // a row that sees no key: 0
+      uint16_t *dst = a.p.out + at * D + g * 4;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr)
+        *reinterpret_cast<uint2 *>(dst + gr * 32) =
+            make_uint2(pack_bf162(out[nb][c][gr][0] * inv, out[nb][c][gr][1] * inv),
+                       pack_bf162(out[nb][c][gr][2] * inv, out[nb][c][gr][3] * inv));
+      if (g == 0 && a.p.lse) a.p.lse[at] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    }
+}
+
+// Joins a row's triples: M = max m_k, w_k = 2^(m_k - M), out = sum w_k acc_k / sum w_k l_k,
+// the sink as one term more of the sum.  One warp a row (token, q head).
+template <int D>
+__global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4Args a) {
+  constexpr int V = D / 32;  // channels a lane
+  wait_for_predecessor();
+  const int lane = threadIdx.x & 31;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (at >= static_cast<int64_t>(a.p.num_tokens) * a.p.hq) return;
+  const int tok = static_cast<int>(at / a.p.hq);
+  const int head = static_cast<int>(at % a.p.hq);
+  const int seq = find_seq(a.p.cu, a.p.num_seqs, 1, tok, lane);
+  const int q0 = a.p.cu[seq], q_len = a.p.cu[seq + 1] - q0, seq_len = a.p.seq_lens[seq];
+  if (tok < q0 || tok - q0 >= q_len || !valid_sequence(a, q0, q_len, seq_len)) return;
+  const int tok0 = (tok - q0) / a.block_tokens * a.block_tokens;
+  const int n = segments(a, key_range(a, seq_len, q_len, tok0).blocks);
+  const int64_t prow = at * a.num_splits;
+  float m = -INFINITY, l = 0.0f;
+  if (lane < n) {
+    const float2 ml = a.part_ml[prow + lane];
+    m = ml.x;
+    l = ml.y;
+  }
+  const float sink = a.p.sinks ? a.p.sinks[head] * kLog2e : -INFINITY;
+  float top = fmaxf(m, sink);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float mu = top == -INFINITY ? 0.0f : top;
+  const float w = fast_exp2(m - mu);
+  float sum = w * l;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  sum += fast_exp2(sink - mu);
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float wk = __shfl_sync(0xffffffffu, w, k);
+    const float *src = a.part_acc + (prow + k) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      const float2 x = *reinterpret_cast<const float2 *>(src + v);
+      acc[v] = fmaf(wk, x.x, acc[v]);
+      acc[v + 1] = fmaf(wk, x.y, acc[v + 1]);
+    }
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  uint16_t *dst = a.p.out + at * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2)
+    *reinterpret_cast<uint32_t *>(dst + v) = pack_bf162(acc[v] * inv, acc[v + 1] * inv);
+  if (lane == 0 && a.p.lse) a.p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int D, int BS, int NB>
+cudaError_t launch_rows(const Q4Args &a, cudaStream_t stream) {
+  using C = Q4Cfg<D>;
+  constexpr int kRing = kWarps * C::kStages * C::kBlock;
+  constexpr int kMerge = (kWarps - 1) * 32 * NB * (4 + 8 * C::G) * 4;
+  constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static DeviceOnce configured;
+  cudaError_t e = configured.get(nullptr, [](int, int *) {
+    return cudaFuncSetAttribute(attn_q4_kernel<D, BS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = static_cast<int64_t>(a.num_items) * a.p.hk * a.num_splits;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  return launch_kernel(attn_q4_kernel<D, BS, NB>, dim3(static_cast<unsigned>(blocks)), kWarps * 32,
+                       kSmem, stream, a);
+}
+
+template <int D>
+cudaError_t launch_d(const Q4Args &a, cudaStream_t stream) {
+  const bool wide = a.block_tokens * a.qpk > 8;
+  const bool big = a.p.bs == 32;
+  cudaError_t e = wide ? (big ? launch_rows<D, 32, 2>(a, stream) : launch_rows<D, 16, 2>(a, stream))
+                       : (big ? launch_rows<D, 32, 1>(a, stream) : launch_rows<D, 16, 1>(a, stream));
+  if (e != cudaSuccess || a.num_splits == 1) return e;
+  const int64_t rows = static_cast<int64_t>(a.p.num_tokens) * a.p.hq;
+  return launch_kernel(q4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, a);
+}
+
+}  // namespace
+
+// Rows a block: 8 where a single token's q heads fit, else 16.
+int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len) {
+  return max_query_len <= 1 ? 1 : std::max(1, 16 / qpk);
+}
+
+int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
+                       int32_t max_query_len, int32_t max_seq_len) {
+  (void)hq;
+  (void)d;
+  (void)num_tokens;
+  (void)max_query_len;
+  int32_t ns = (max_seq_len + 1023) / 1024;
+  const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(num_seqs) * hk);
+  const int64_t cap = (8192 + units - 1) / units;
+  if (ns > cap) ns = static_cast<int32_t>(cap);
+  return std::max(1, std::min(ns, kMaxSplits));
+}
+
+cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {
+  Q4Args a;
+  a.p = p;
+  a.status = reinterpret_cast<uint32_t *>(p.workspace);
+  a.num_splits = p.num_splits;
+  a.part_acc = reinterpret_cast<float *>(p.workspace + 256);
+  a.part_ml = reinterpret_cast<float2 *>(a.part_acc + static_cast<int64_t>(p.num_tokens) * p.hq *
+                                                          p.num_splits * p.d);
+  a.qpk = p.hq / p.hk;
+  a.block_tokens = q4_block_tokens(a.qpk, p.max_query_len);
+  a.num_items = p.max_query_len <= 1 ? p.num_seqs
+                : a.block_tokens == 1 ? p.num_tokens
+                                      : p.num_tokens / a.block_tokens + p.num_seqs;
+  a.scale_log2 = p.softmax_scale * kLog2e;
+  int blocks = (p.max_seq_len + 15) / 16;
+  if (p.window > 0) blocks = std::min(blocks, (p.window + a.block_tokens + 15) / 16 + 1);
+  a.seg_blocks = std::max(1, (blocks + p.num_splits - 1) / p.num_splits);
+  switch (p.d) {
+    case 64: return launch_d<64>(a, stream);
+    case 128: return launch_d<128>(a, stream);
+    case 256: return launch_d<256>(a, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace paq8

@@ -1,0 +1,201 @@
+// kv_load: pages of a cache read back as packed bf16 rows, for each of the three
+// formats.  Row j of sequence s (j below its length) is
+//   q8    code * scale                    of the row's 32-channel group
+//   f8v4  K: the e4m3 value;  V: code * scale + zero of the token
+//   q4    code * scale + zero             of the row's 32-channel group
+// in fp32 (the products are exact), rounded once more to bf16.
+//
+// Bound by HBM: the page bytes read and 4 D bytes written a (key, kv head).  One warp
+// a (page, kv head): a page's arrays are contiguous for a head, and a lane writes
+// 8 channels (16 bytes) of a row, D / 8 neighbouring lanes a row.  Values that lie
+// channel-major (q8, f8v4) are transposed in registers: a lane takes 4 keys of 8
+// channels, one word a channel (a half word of nibbles), and writes 4 pieces.
+#include "attn_common.cuh"
+#include "attn_f8v4.cuh"
+#include "programmatic.cuh"
+#include "q4.cuh"
+#include "q4.h"
+
+namespace paq8 {
+
+constexpr int kLoadWarps = 4;
+
+__device__ __forceinline__ float half_at(const uint16_t *p) { return __half2float(__ushort_as_half(*p)); }
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
+  return make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]), pack_bf162(x[4], x[5]),
+                    pack_bf162(x[6], x[7]));
+}
+
+// Values of byte b of w, signed.
+__device__ __forceinline__ float byte_code(uint32_t w, int b) {
+  return static_cast<float>(static_cast<int8_t>((w >> (8 * b)) & 0xffu));
+}
+
+template <CacheFormat F, int D, int BS>
+__global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_constant__ KvLoad p) {
+  constexpr int G = D / 32;
+  constexpr int kOctets = D / 8;
+  wait_for_predecessor();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kLoadWarps + (threadIdx.x >> 5);
+  const int h = static_cast<int>(unit % p.hk);
+  const int64_t item = unit / p.hk;
+  if (item >= p.num_rows / BS + p.num_seqs) return;
+  const int seq = find_seq(p.cu_seqlens_k, p.num_seqs, BS, static_cast<int>(item), lane);
+  const int row0 = p.cu_seqlens_k[seq], room = p.cu_seqlens_k[seq + 1] - row0;
+  const int page = static_cast<int>(item) - (row0 / BS + seq);
+  const bool first = page == 0 && h == 0 && lane == 0;
+  if (row0 < 0 || room < 0 || row0 > p.num_rows - room) {
+    if (first) flag_status(p.status, PA_DEV_BAD_SEQ);
+    return;
+  }
+  int n = room;
+  if (p.load_lens) {
+    n = p.load_lens[seq];
+    if (n < 0 || n > room) {
+      if (first) flag_status(p.status, PA_DEV_BAD_SEQ);
+      return;
+    }
+  }
+  if (page < 0 || page * BS >= n) return;
+  const int block = page < p.table_columns
+                        ? p.block_table[static_cast<int64_t>(seq) * p.table_stride + page]
+                        : -1;
+  if (block < 0 || block >= p.num_blocks) {
+    if (lane == 0) flag_status(p.status, PA_DEV_BAD_BLOCK);
+    return;
+  }
+  const int keys = min(BS, n - page * BS);
+  const int64_t at = static_cast<int64_t>(block) * p.hk + h;
+  const int64_t out0 = static_cast<int64_t>(row0) + page * BS;
+  uint16_t *kout = p.key + out0 * p.key_stride + h * D;
+  uint16_t *vout = p.value + out0 * p.value_stride + h * D;
+
+  // ---- keys: every format is token-major
+#pragma unroll
+  for (int i0 = 0; i0 < BS * kOctets; i0 += 32) {
+    const int r = (i0 + lane) / kOctets, o = (i0 + lane) % kOctets;
+    if (r >= keys) continue;
+    float x[8];
+    if constexpr (F == CacheFormat::q4) {
+      const uint8_t *codes = static_cast<const uint8_t *>(p.array[0]) + (at * BS + r) * (D / 2);
+      const uint16_t *sc = static_cast<const uint16_t *>(p.array[1]) + at * (2 * BS * G) + r * G + (o >> 2);
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + q4_k_word(o, G));
+      const float s = half_at(sc), z = half_at(sc + BS * G);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 0xfu), s, z);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.array[0]) +
+                                                       (at * BS + r) * D + o * 8);
+      if constexpr (F == CacheFormat::q8) {
+        const float s = half_at(static_cast<const uint16_t *>(p.array[1]) + (at * BS + r) * G + (o >> 2));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = byte_code(i < 4 ? w.x : w.y, i & 3) * s;
+      } else {
+        const uint32_t v[4] = {e4m3x2_to_half2(w.x), e4m3x2_to_half2(w.x >> 16),
+                               e4m3x2_to_half2(w.y), e4m3x2_to_half2(w.y >> 16)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        }
+      }
+    }
+    *reinterpret_cast<uint4 *>(kout + r * p.key_stride + o * 8) = pack_bf16x8(x);
+  }
+
+  // ---- values
+  if constexpr (F == CacheFormat::q4) {
+#pragma unroll
+    for (int i0 = 0; i0 < BS * kOctets; i0 += 32) {
+      const int r = (i0 + lane) / kOctets, o = (i0 + lane) % kOctets;
+      if (r >= keys) continue;
+      const uint8_t *codes = static_cast<const uint8_t *>(p.array[2]) + (at * BS + r) * (D / 2);
+      const uint16_t *sc = static_cast<const uint16_t *>(p.array[3]) + at * (2 * BS * G) + (o >> 2) * BS + r;
+      const uint32_t w0 = *reinterpret_cast<const uint16_t *>(codes + q4_v_half(o, 0, G));
+      const uint32_t w1 = *reinterpret_cast<const uint16_t *>(codes + q4_v_half(o, 1, G));
+      const float s = half_at(sc), z = half_at(sc + BS * G);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = fmaf(static_cast<float>(((i < 4 ? w0 : w1) >> (4 * (i & 3))) & 0xfu), s, z);
+      *reinterpret_cast<uint4 *>(vout + r * p.value_stride + o * 8) = pack_bf16x8(x);
+    }
+  } else {
+#pragma unroll
+    for (int i0 = 0; i0 < BS / 4 * kOctets; i0 += 32) {
+      const int r = (i0 + lane) / kOctets * 4, o = (i0 + lane) % kOctets;  // keys r .. r + 3
+      if (r >= keys) continue;
+      float x[4][8];
+      if constexpr (F == CacheFormat::q8) {
+        const uint8_t *codes = static_cast<const uint8_t *>(p.array[2]) + (at * D + o * 8) * BS + r;
+        const uint2 sw = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.array[3]) +
+                                                          (at * G + (o >> 2)) * BS + r);
+        const float2 s01 = __half22float2(*reinterpret_cast<const __half2 *>(&sw.x));
+        const float2 s23 = __half22float2(*reinterpret_cast<const __half2 *>(&sw.y));
+        const float s[4] = {s01.x, s01.y, s23.x, s23.y};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + c * BS);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j][c] = byte_code(w, j) * s[j];
+        }
+      } else {
+        const uint8_t *codes = static_cast<const uint8_t *>(p.array[1]) + ((at * D + o * 8) * BS + r) / 2;
+        const uint16_t *sc = static_cast<const uint16_t *>(p.array[2]) + at * BS + r;
+        const uint16_t *zr = static_cast<const uint16_t *>(p.array[3]) + at * BS + r;
+        float s[4], z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[j] = half_at(sc + j);
+          z[j] = half_at(zr + j);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t w = *reinterpret_cast<const uint16_t *>(codes + c * (BS / 2));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[j][c] = fmaf(static_cast<float>((w >> (4 * j)) & 0xfu), s[j], z[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r + j < keys)
+          *reinterpret_cast<uint4 *>(vout + (r + j) * p.value_stride + o * 8) = pack_bf16x8(x[j]);
+    }
+  }
+}
+
+template <CacheFormat F, int D>
+static cudaError_t launch_load_d(const KvLoad &p, dim3 grid, cudaStream_t stream) {
+  return p.block_size == 32
+             ? launch_kernel(kv_load_kernel<F, D, 32>, grid, 32 * kLoadWarps, 0, stream, p)
+             : launch_kernel(kv_load_kernel<F, D, 16>, grid, 32 * kLoadWarps, 0, stream, p);
+}
+
+template <CacheFormat F>
+static cudaError_t launch_load_f(const KvLoad &p, dim3 grid, cudaStream_t stream) {
+  switch (p.d) {
+    case 64: return launch_load_d<F, 64>(p, grid, stream);
+    case 128: return launch_load_d<F, 128>(p, grid, stream);
+    case 256: return launch_load_d<F, 256>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_kv_load(const KvLoad &p, CacheFormat format, cudaStream_t stream) {
+  // pages of sequence s start at item cu[s] / bs + s: at most rows / bs + seqs items
+  const int64_t units =
+      (static_cast<int64_t>(p.num_rows) / p.block_size + p.num_seqs) * p.hk;
+  const dim3 grid(static_cast<unsigned>((units + kLoadWarps - 1) / kLoadWarps));
+  switch (format) {
+    case CacheFormat::q8: return launch_load_f<CacheFormat::q8>(p, grid, stream);
+    case CacheFormat::f8v4: return launch_load_f<CacheFormat::f8v4>(p, grid, stream);
+    case CacheFormat::q4: return launch_load_f<CacheFormat::q4>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace paq8
