@@ -648,6 +648,62 @@ pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *
                                 void *stream);
 
 /*
+ * Bytes of workspace pa_prompt_attention uses for these bounds: 256 bytes of header
+ * (the status word at offset 0) plus the fp32 triples of its key segments, where
+ * few query rows meet many keys.
+ */
+size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_keys,
+                                          int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t max_query_len,
+                                          int32_t max_key_len);
+
+/*
+ * prompt_attention -- attention of packed prompts over their own bf16 K/V rows, before
+ * or beside any cache: the "new keys" pass of a prefix merged by pa_merge_attn_states,
+ * a whole prompt, or a chunk behind rows that pa_kv_load read back.
+ * Passage: "attention_impl.py" (the varlen prefill over query_start_loc, key_offset =
+ * k_len - q_len); "shared/attention_kit.py" (`_attend_with_prefix`: the new keys).
+ *
+ *   q              bf16 [num_tokens][num_q_heads][head_dim], token stride in elements
+ *                  (a multiple of 8); head and channel dims contiguous.
+ *   k, v           bf16 [num_keys][num_kv_heads][head_dim], the same.  Slices of one
+ *                  projection's rows are fine.
+ *   cu_seqlens_q   int32 [num_seqs + 1]: sequence s owns query tokens cu[s] .. cu[s + 1]
+ *                  - 1; non-decreasing, within num_tokens.
+ *   cu_seqlens_k   int32 [num_seqs + 1]: and key rows, likewise (the same array where
+ *                  every query has its own key).  Query i of s sees keys 0 .. k_len -
+ *                  q_len + i of its sequence (bottom-right causal); with q_len above k_len
+ *                  the first queries see none.
+ *   max_query_len, max_key_len
+ *                  host hints of the longest sequence: they size the key segments; any
+ *                  positive value (max_key_len: not negative) gives correct results.
+ *   sinks, sliding_window, out, lse
+ *                  as pa_paged_attention_ex.  A query that sees no key gets out = 0 and
+ *                  lse = -inf (its sink, where there is one).
+ *   workspace      device buffer, 16-byte aligned, its first 4 bytes the status word (zero
+ *                  it once); pa_prompt_attention_workspace_size bytes, a smaller one takes
+ *                  fewer key segments, down to 256 bytes.  Calls that may overlap on the
+ *                  GPU need workspaces of their own.
+ *   flags          0 or PA_ATTN_NON_CAUSAL (every query sees all keys of its sequence).
+ * head_dim 64, 128, 256; num_q_heads a multiple of num_kv_heads, at most 128 times.
+ * A sequence whose bounds are out of range is not written and flagged PA_DEV_BAD_SEQ;
+ * rows of tokens no sequence owns are not written.  What other sequences' rows hold never
+ * reaches a result; an infinity or NaN in a value row may reach queries of its own
+ * sequence up to 15 keys before the first that sees it.  Asynchronous.
+ * Numerics: exact products summed in fp32, softmax in fp32, p rounded to bf16 for its
+ * product with V (fp32 sums), the output rounded to bf16.
+ */
+pa_status pa_prompt_attention(const void *q, int64_t q_token_stride, const void *k,
+                              int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                              const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                              int32_t num_seqs, int32_t num_tokens, int32_t num_keys,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_query_len, int32_t max_key_len, float softmax_scale,
+                              const float *sinks, int32_t sliding_window, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, uint32_t flags,
+                              void *stream);
+
+/*
  * Synchronizes `stream`, reads the device status word at `status` (a kv_store
  * status word, or the start of an attention workspace), clears it, and maps
  * it to PA_OK / PA_ERR_TIMEOUT (bit 0x8 set) / PA_ERR_DEVICE_CHECK (other

@@ -121,6 +121,11 @@ def load():
         lib.pa_paged_attention_q4.argtypes = [P] * 8 + [i32] * 11 + [
             ctypes.c_float, i32, P, i32, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
         lib.pa_paged_attention_q4.restype = ctypes.c_int
+        lib.pa_prompt_attention_workspace_size.argtypes = [i32] * 8
+        lib.pa_prompt_attention_workspace_size.restype = ctypes.c_size_t
+        lib.pa_prompt_attention.argtypes = [P, i64, P, i64, P, i64, P, P] + [i32] * 8 + [
+            ctypes.c_float, P, i32, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
+        lib.pa_prompt_attention.restype = ctypes.c_int
         lib.pa_check_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.pa_check_status.restype = ctypes.c_int
         lib.pa_status_string.argtypes = [ctypes.c_int]
@@ -1039,6 +1044,67 @@ def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_
           seq_lens.data_ptr(), block_table.data_ptr(), table_stride, columns, s, t, hq, hk, d, nb,
           bs, max_query_len, max_seq_len, d ** -0.5 if softmax_scale is None else softmax_scale,
           num_splits, None if sinks is None else sinks.data_ptr(), sliding_window, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), 0 if causal else ATTN_NON_CAUSAL)
+    return (out, lse) if return_lse else out
+
+
+def prompt_attention_workspace_size(num_seqs: int, num_tokens: int, num_keys: int,
+                                    num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                    max_query_len: int, max_key_len: int) -> int:
+    """Bytes of workspace prompt_attention uses for these bounds."""
+    return int(load().pa_prompt_attention_workspace_size(
+        num_seqs, num_tokens, num_keys, num_q_heads, num_kv_heads, head_dim, max_query_len,
+        max_key_len))
+
+
+def prompt_attention(q, k, v, cu_seqlens_q, max_query_len: int, cu_seqlens_k=None,
+                     max_key_len: int | None = None, softmax_scale: float | None = None,
+                     causal: bool = True, sinks=None, sliding_window: int = 0, out=None, lse=None,
+                     workspace=None, stream=None, return_lse: bool = True):
+    """Attention of packed prompts over their own K/V rows, no cache
+    (pa_prompt_attention).
+
+    q [T, Hq, D], k and v [N, Hk, D] bf16, slices of wider rows allowed; cu_seqlens_q int32
+    [S + 1]; ``cu_seqlens_k`` int32 [S + 1] where the keys of a sequence are not one to a
+    query (a prefix before a chunk's own keys).  Query i of a sequence sees keys 0 ..
+    k_len - q_len + i of it.  ``max_query_len`` / ``max_key_len``: host hints of the longest
+    sequence (max_key_len: max_query_len when omitted).  ``workspace``: optional uint8
+    CUDA tensor of ``prompt_attention_workspace_size`` bytes whose first 4 bytes are zero.
+    Other arguments and results as paged_attention."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    if q.dtype is not _BF16:
+        raise TypeError("q must be bf16")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, Hq, D], k and v [N, Hk, D]")
+    t, hq, d = q.shape
+    n, hk, dk = k.shape
+    if dk != d:
+        raise ValueError("q and k must have the same head_dim")
+    ks, vs = _kv_rows(dev, k, v, hk, d)
+    if t and ((d > 1 and q.stride(2) != 1) or (hq > 1 and q.stride(1) != d)):
+        raise ValueError("q's head and channel dims must be contiguous")
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    for x in (cu_seqlens_q, cu_seqlens_k):
+        if x.dtype is not _I32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    s = cu_seqlens_q.numel() - 1
+    if s < 0 or cu_seqlens_k.numel() != s + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must be [S + 1]")
+    if max_key_len is None:
+        max_key_len = max_query_len
+    _check_sinks(dev, sinks, hq)
+    out, lse = _results(dev, q, out, lse, return_lse, stream)
+    workspace = _workspace(dev, workspace, lambda: prompt_attention_workspace_size(
+        s, t, n, hq, hk, d, max_query_len, max_key_len), stream)
+    _call((_lib or load()).pa_prompt_attention, dev, stream, q.data_ptr(),
+          q.stride(0) if t > 1 else hq * d, k.data_ptr(), ks, v.data_ptr(), vs,
+          cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), s, t, n, hq, hk, d, max_query_len,
+          max_key_len, d ** -0.5 if softmax_scale is None else softmax_scale,
+          None if sinks is None else sinks.data_ptr(), sliding_window, out.data_ptr(),
           None if lse is None else lse.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), 0 if causal else ATTN_NON_CAUSAL)
     return (out, lse) if return_lse else out

@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "merge.h"
+#include "prompt.h"
 #include "q4.h"
 #include "serving.h"
 
@@ -1045,6 +1046,95 @@ pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *
   p.lse = lse;
   p.workspace = static_cast<uint8_t *>(workspace);
   const cudaError_t e = paq8::launch_attention_q4(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Attention over whole prompts.
+extern "C" {
+
+size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_keys,
+                                          int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t max_query_len,
+                                          int32_t max_key_len) {
+  (void)num_seqs, (void)num_tokens, (void)num_keys, (void)num_q_heads, (void)num_kv_heads;
+  (void)head_dim, (void)max_query_len, (void)max_key_len;
+  return 256;
+}
+
+pa_status pa_prompt_attention(const void *q, int64_t q_token_stride, const void *k,
+                              int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                              const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                              int32_t num_seqs, int32_t num_tokens, int32_t num_keys,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_query_len, int32_t max_key_len, float softmax_scale,
+                              const float *sinks, int32_t sliding_window, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, uint32_t flags,
+                              void *stream) {
+  g_last_error[0] = '\0';
+  if (flags & ~PA_ATTN_NON_CAUSAL) return fail(PA_ERR_INVALID_ARG, "unknown flag bits");
+  const bool causal = !(flags & PA_ATTN_NON_CAUSAL);
+  if (num_seqs < 0 || num_tokens < 0 || num_keys < 0)
+    return fail(PA_ERR_INVALID_ARG, "negative size");
+  if (!workspace || workspace_bytes < 256)
+    return fail(PA_ERR_INVALID_ARG, "workspace smaller than 256 bytes");
+  if (sliding_window < 0) return fail(PA_ERR_INVALID_ARG, "sliding_window < 0");
+  if (sliding_window > 0 && !causal)
+    return fail(PA_ERR_INVALID_ARG, "a sliding window needs causal attention");
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!q || (num_keys > 0 && (!k || !v)) || !cu_seqlens_q || !cu_seqlens_k || !out)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (num_q_heads / num_kv_heads > 128)
+    return fail(PA_ERR_UNSUPPORTED, "more than 128 q heads per kv head");
+  if (!supported_dim(head_dim)) return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  if (max_query_len <= 0 || max_key_len < 0)
+    return fail(PA_ERR_INVALID_ARG, "max_query_len must be positive, max_key_len not negative");
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t k_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_token_stride < q_row || (num_keys > 0 && (k_token_stride < k_row || v_token_stride < k_row)))
+    return fail(PA_ERR_INVALID_ARG, "token stride smaller than a row");
+  if (q_token_stride % 8 || k_token_stride % 8 || v_token_stride % 8 ||
+      misaligned(15, {q, k, v, out, workspace}))
+    return fail(PA_ERR_INVALID_ARG, "rows, out and workspace must be 16-byte aligned");
+  if (q_token_stride >= (int64_t{1} << 36) || k_token_stride >= (int64_t{1} << 36) ||
+      v_token_stride >= (int64_t{1} << 36))
+    return fail(PA_ERR_UNSUPPORTED, "token stride of 2^36 elements or more");
+  if (misaligned(3, {lse, sinks, cu_seqlens_q, cu_seqlens_k}))
+    return fail(PA_ERR_INVALID_ARG, "lse, sinks and the int32 arrays must be 4-byte aligned");
+  if (num_keys > 0x7fffffff - 4096 ||
+      (static_cast<int64_t>(num_tokens) + num_seqs) * num_q_heads >= (int64_t{1} << 31))
+    return fail(PA_ERR_UNSUPPORTED,
+                "(num_tokens + num_seqs) * num_q_heads and num_keys must be < 2^31 (less 4096)");
+  paq8::PromptAttention p;
+  p.q = static_cast<const uint16_t *>(q);
+  p.k = static_cast<const uint16_t *>(k);
+  p.v = static_cast<const uint16_t *>(v);
+  p.q_stride = q_token_stride;
+  p.k_stride = k_token_stride;
+  p.v_stride = v_token_stride;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_keys = num_keys;
+  p.hq = num_q_heads;
+  p.hk = num_kv_heads;
+  p.d = head_dim;
+  p.max_query_len = max_query_len;
+  p.max_key_len = max_key_len;
+  p.softmax_scale = softmax_scale;
+  p.sinks = sinks;
+  p.window = sliding_window;
+  p.causal = causal;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.workspace = static_cast<uint8_t *>(workspace);
+  p.workspace_bytes = workspace_bytes;
+  const cudaError_t e = paq8::launch_prompt_attention(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

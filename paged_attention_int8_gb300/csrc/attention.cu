@@ -109,12 +109,7 @@ __global__ void __launch_bounds__(128) reduce_kernel(const float *__restrict__ p
 
 // ---------------------------------------------------------------------- host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
+EncodeTiledFn encode_tiled_fn() {
   static EncodeTiledFn fn = []() -> EncodeTiledFn {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -130,7 +125,7 @@ static EncodeTiledFn encode_fn() {
 // 2-D byte map: `rows` rows of `row_bytes`, boxes of box_x bytes x box_y rows.
 static bool encode_map(CUtensorMap *map, const void *base, int64_t rows, int row_bytes, int box_x,
                        int box_y, CUtensorMapSwizzle sw) {
-  EncodeTiledFn fn = encode_fn();
+  EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};

@@ -1,0 +1,557 @@
+// Attention over whole prompts: packed bf16 rows q [T, Hq, D], k, v [Tk, Hk, D] of
+// sequences of different lengths, no cache.  For query i of a sequence of q_len
+// queries and k_len keys, row (i, q head):
+//   out = sum_j p_j v_j / sum_j p_j,  lse = ln sum_j exp(scale q . k_j),
+//   p_j = exp(scale q . k_j - m), over keys j <= k_len - q_len + i (causal; the last
+//   `window` of them with a sliding window) or all keys.
+//
+// Bound by the tensor cores: 4 D Hq flops a query-key pair, on tcgen05 with fp32
+// accumulators in TMEM.  128-row tiles (128 / qpk tokens x the qpk q heads of a kv head)
+// against 128-key tiles:
+//   S = Q K^T   both operands in shared memory, as TMA brings them (bf16, exact products)
+//   P = 2^(S scale - m) by one thread a row, bf16, back into S's TMEM columns
+//   O += P V    P from TMEM, V as it lies in memory (channels contiguous: the MMA's
+//               N-major form)
+// D 64 / 128: two row tiles a block share every K/V tile; while one's softmax runs the
+// tensor core works on the other's products (TMEM: S/P 128 columns and O D columns
+// each).  D 256: one row tile, whose S alternates between two buffers (O takes 256
+// columns): QK(j + 1) runs behind the softmax of j.
+// K and V pass through one ring of 16 KB slots: 64 channels of 128 keys, or 8192 / D keys
+// of all channels, each freed by the commit of its last MMA.
+// The maximum that P is taken against moves only when a tile's sum passes 2^12 (no row
+// maximum on the common path); O in TMEM is then rescaled by the softmax warps.  P is
+// rounded to bf16 (the MMA's operands are of one type); sums and O are fp32.
+// Warps: 4 softmax warps a row tile (one a TMEM lane quarter), one that issues the MMAs
+// from one elected thread, one that issues the copies.
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "launch.h"
+#include "programmatic.cuh"
+#include "prompt.h"
+#include "tcgen05.cuh"
+
+namespace paq8 {
+
+namespace {
+
+struct PromptArgs {
+  PromptAttention p;
+  uint32_t *status;
+  int32_t qpk, tile_tokens, block_tokens;  // tokens a row tile, a block
+  int32_t num_items;
+  float scale_log2;
+};
+
+template <int D>
+struct PromptCfg {
+  static constexpr int kTiles = D == 256 ? 1 : 2;      // row tiles a block
+  static constexpr int kKeys = 128;                    // keys a tile
+  static constexpr int kChunks = D / 64;               // slots of a K tile, and of a V tile
+  static constexpr int kVKeys = kKeys / kChunks;       // keys of a V slot
+  static constexpr int kSlotBytes = 16384;
+  static constexpr int kSlots = 10;
+  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kQOff = kSlots * kSlotBytes;
+  static constexpr int kBarOff = kQOff + kTiles * kQBytes;
+  static constexpr int kSmem = kBarOff + 512 + 1024;
+  static constexpr int kSoftmaxWarps = 4 * kTiles;
+  static constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+  static constexpr float kMaxTileSum = 4096.0f;
+  // TMEM columns of S/P and of O, by row tile (D 64, 128) or by S buffer (D 256)
+  __device__ static __forceinline__ uint32_t s_col(int i) { return D == 256 ? 256 + 128 * i : 256 * i; }
+  __device__ static __forceinline__ uint32_t o_col(int i) { return D == 256 ? 0 : 256 * i + 128; }
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// barriers (8 bytes each)
+constexpr int kBarFull = 0;    // [slots] copy -> MMA
+constexpr int kBarEmpty = 10;  // [slots] commit of a slot's last MMA -> copy
+constexpr int kBarQ = 20;      // [2] copies of a row tile's q -> MMA
+constexpr int kBarS = 22;      // [2] commit of QK -> softmax
+constexpr int kBarP = 24;      // [2] P in TMEM (4 warps) -> MMA
+constexpr int kBarO = 26;      // [2] commit of every PV (D 256: one) -> rescale, epilogue
+constexpr int kBarDrain = 28;  // commit of all that was issued, before an early end
+constexpr int kNumBars = 29;
+
+// kind::f16 with bf16 operands, fp32 accumulator; n_major: B's N dimension contiguous.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool n_major) {
+  return tc::idesc_f16(m, n) | (1u << 7) | (1u << 10) | (n_major ? 1u << 16 : 0u);
+}
+
+// Matrix descriptor of an N-major operand in the 128-byte swizzle: 64 channels (128 bytes)
+// of a key are a row, 8 keys 1024 bytes, the next 64 channels `next` bytes further.
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t next) {
+  uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(next >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// A box of a tiled map at (x, y, z[, w]) into shared memory.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// The tiles of a row tile: keys [begin, end) that some row of it sees, in 128-key tiles
+// counted from the block's first.
+struct TileRange {
+  int tiles, end;
+};
+
+template <int D>
+__global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
+    prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  using C = PromptCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (smem_base - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kMmaWarp = C::kSoftmaxWarps, kCopyWarp = C::kSoftmaxWarps + 1;
+
+  const uint32_t bars = smem_base + C::kBarOff;
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  const uint32_t tmem_slot = bars + 8 * kNumBars;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(bar(kBarFull + s), 1);
+      mbar_init(bar(kBarEmpty + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kBarQ + s), 1);
+      mbar_init(bar(kBarS + s), 1);
+      mbar_init(bar(kBarP + s), 4);
+      mbar_init(bar(kBarO + s), 1);
+    }
+    mbar_init(bar(kBarDrain), 1);
+    fence_barrier_init();
+  }
+  wait_for_predecessor();
+
+  // ---- which rows, which keys; the heaviest blocks first (later queries see more keys)
+  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.p.hk));
+  const int item = a.num_items - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(a.p.hk));
+  const int seq = find_seq(a.p.cu_q, a.p.num_seqs, a.block_tokens, item, lane);
+  const int q0 = a.p.cu_q[seq], q_len = a.p.cu_q[seq + 1] - q0;
+  const int k0 = a.p.cu_k[seq], k_len = a.p.cu_k[seq + 1] - k0;
+  const int tok0 = (item - (a.block_tokens == 1 ? q0 : q0 / a.block_tokens + seq)) * a.block_tokens;
+  if (tok0 < 0 || tok0 >= q_len) return;
+  if (q0 < 0 || q0 > a.p.num_tokens - q_len || k0 < 0 || k_len < 0 || k0 > a.p.num_keys - k_len) {
+    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+    return;
+  }
+  const int shift = a.p.causal ? k_len - q_len : k_len - 1;  // last key of query i: shift (+ i)
+  auto last_of = [&](int i) { return a.p.causal ? shift + i : shift; };
+  auto first_of = [&](int last) { return a.p.window > 0 ? max(0, last - a.p.window + 1) : 0; };
+  const int n_tok = min(a.block_tokens, q_len - tok0);
+  // keys below k_end are seen by some row of the block; a row with last < 0 sees none
+  const int k_begin = min(first_of(last_of(tok0)), max(0, last_of(tok0 + n_tok - 1)));
+  const int t0 = k_begin / C::kKeys;
+  TileRange range[C::kTiles];
+#pragma unroll
+  for (int i = 0; i < C::kTiles; ++i) {
+    const int n = min(a.tile_tokens, n_tok - i * a.tile_tokens);  // tokens of the row tile
+    range[i].end = n > 0 ? max(0, last_of(tok0 + i * a.tile_tokens + n - 1) + 1) : 0;
+    range[i].tiles = max(0, (range[i].end + C::kKeys - 1) / C::kKeys - t0);
+  }
+  int nt = range[0].tiles;
+  if constexpr (C::kTiles == 2) nt = max(nt, range[1].tiles);
+
+  if (warp == kMmaWarp) tc::alloc(tmem_slot, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kBarOff + 8 * kNumBars);
+  bool ok = true;
+
+  // Slots in the order of use: K(0), then (D 256: K(1)), then V(j), K(j + 1 or 2), ...
+  constexpr int kAhead = D == 256 ? 2 : 1;
+  auto slot_of_k = [&](int j) {  // first of the tile's kChunks slots
+    return (j < kAhead ? j : kAhead + 2 * (j - kAhead) + 1) * C::kChunks;
+  };
+  auto slot_of_v = [&](int j) { return (j + kAhead <= nt ? kAhead + 2 * j : nt + j) * C::kChunks; };
+
+  if (warp == kCopyWarp) {
+    // ============================================================ copies
+    if (lane == 0 && nt > 0) {
+      prefetch_tensormap(&map_q);
+      prefetch_tensormap(&map_k);
+      prefetch_tensormap(&map_v);
+      int used = 0;  // slots filled so far
+      auto take = [&]() -> int {
+        const int s = used % C::kSlots;
+        if (used >= C::kSlots && !mbar_wait(bar(kBarEmpty + s), ((used / C::kSlots) - 1) & 1)) return -1;
+        ++used;
+        mbar_arrive_expect_tx(bar(kBarFull + s), C::kSlotBytes);
+        return s;
+      };
+      auto load_q = [&](int i) {
+        mbar_arrive_expect_tx(bar(kBarQ + i), a.tile_tokens * a.qpk * D * 2);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(smem_base + C::kQOff + i * C::kQBytes + c * (128 * 128), &map_q, c * 64, h * a.qpk,
+                      q0 + tok0 + i * a.tile_tokens, bar(kBarQ + i));
+      };
+      auto load_k = [&](int j) -> bool {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          const int s = take();
+          if (s < 0) return false;
+          tma_load_4d(smem_base + s * C::kSlotBytes, &map_k, 0, k0 + (t0 + j) * C::kKeys, c, h,
+                      bar(kBarFull + s));
+        }
+        return true;
+      };
+      auto load_v = [&](int j) -> bool {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          const int s = take();
+          if (s < 0) return false;
+          tma_load_4d(smem_base + s * C::kSlotBytes, &map_v, 0,
+                      k0 + (t0 + j) * C::kKeys + c * C::kVKeys, 0, h, bar(kBarFull + s));
+        }
+        return true;
+      };
+      load_q(0);
+      ok = load_k(0);
+      if (C::kTiles == 2) load_q(1);
+      if (kAhead == 2 && ok && nt > 1) ok = load_k(1);
+      for (int j = 0; ok && j < nt; ++j) {
+        ok = load_v(j);
+        if (ok && j + kAhead < nt) ok = load_k(j + kAhead);
+      }
+      // no block gives up its shared memory before its own copies have landed
+      for (int i = max(0, used - C::kSlots); i < used; ++i)
+        mbar_wait(bar(kBarFull + i % C::kSlots), (i / C::kSlots) & 1);
+      for (int i = 0; i < C::kTiles; ++i) mbar_wait(bar(kBarQ + i), 0);
+    }
+  } else if (warp == kMmaWarp) {
+    // ============================================================ MMA issue
+    if (tc::elect_one() && nt > 0) {
+      constexpr uint32_t id_qk = idesc_bf16(128, C::kKeys, false);
+      constexpr uint32_t id_pv = idesc_bf16(128, D, true);
+      auto wait = [&](int i, uint32_t parity) { return ok = mbar_wait(bar(i), parity); };
+      // S(buffer i) = Q K(j)^T; free: the tile's slots have no later use
+      auto issue_qk = [&](int j, int tile, int i, bool free) -> bool {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          const int u = slot_of_k(j) + c, s = u % C::kSlots;
+          if (!wait(kBarFull + s, (u / C::kSlots) & 1)) return false;
+          tc::fence_after();
+          const uint64_t q_desc = tc::desc_sw128(smem_base + C::kQOff + tile * C::kQBytes + c * (128 * 128));
+          const uint64_t k_desc = tc::desc_sw128(smem_base + s * C::kSlotBytes);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_f16(tmem + C::s_col(i), q_desc + 2 * ks, k_desc + 2 * ks, id_qk,
+                        (c > 0 || ks > 0) ? 1u : 0u);
+          if (free) tc::commit(bar(kBarEmpty + s));
+        }
+        tc::commit(bar(kBarS + i));
+        return true;
+      };
+      // O(tile) += P(buffer i) V(j), over the 16-key steps below `end`
+      auto issue_pv = [&](int j, int tile, int i, uint32_t p_parity, int end, bool free) -> bool {
+        const int keys = min(C::kKeys, end - (t0 + j) * C::kKeys);
+        const int past = k_len - (t0 + j) * C::kKeys;  // keys from here on are another sequence's
+        if (!wait(kBarP + i, p_parity)) return false;
+        tc::fence_after();
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          const int u = slot_of_v(j) + c, s = u % C::kSlots;
+          if (!wait(kBarFull + s, (u / C::kSlots) & 1)) return false;
+          tc::fence_after();
+          const uint32_t v = smem_base + s * C::kSlotBytes;
+          // rows of the last step that lie past the sequence meet P = 0, but may hold
+          // infinities: zeros in their place
+          if (past < keys + 15 && past % 16 && past / 16 * 16 / C::kVKeys == c) {
+            const int r0 = past - c * C::kVKeys, r1 = (past / 16 + 1) * 16 - c * C::kVKeys;
+#pragma unroll 1
+            for (int r = r0; r < r1; ++r)
+#pragma unroll 1
+              for (int b = 0; b < D * 2; b += 16)
+                sts128(v + (b >> 7) * (C::kVKeys * 128) + r * 128 + (b & 127), make_uint4(0u, 0u, 0u, 0u));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+#pragma unroll
+          for (int ks = 0; ks < C::kVKeys / 16; ++ks) {
+            const int step = c * (C::kVKeys / 16) + ks;
+            if (step * 16 < keys)
+              tc::mma_f16_ts(tmem + C::o_col(tile), tmem + C::s_col(i) + step * 8,
+                             desc_n_major(v + ks * 2048, C::kVKeys * 128), id_pv,
+                             (j > 0 || step > 0) ? 1u : 0u);
+          }
+          if (free) tc::commit(bar(kBarEmpty + s));
+        }
+        tc::commit(bar(kBarO + tile));
+        return true;
+      };
+      if constexpr (C::kTiles == 2) {
+        const int n0 = range[0].tiles, n1 = range[1].tiles;
+        for (int j = 0; ok && j <= nt; ++j) {
+          // the row tile's S buffer is free once its PV is issued: MMAs of one thread
+          // execute in order.  A slot is freed by the last row tile that uses it.
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int n = i ? n1 : n0, other = i ? 0 : n1;
+            if (ok && j >= 1 && j - 1 < n)
+              issue_pv(j - 1, i, i, (j - 1) & 1, range[i].end, i == 1 || j - 1 >= other);
+            if (ok && j < n && (j > 0 || wait(kBarQ + i, 0)))
+              issue_qk(j, i, i, i == 1 || j >= other);
+          }
+        }
+      } else {
+        ok = wait(kBarQ, 0) && issue_qk(0, 0, 0, true) && (nt < 2 || issue_qk(1, 0, 1, true));
+        for (int j = 0; ok && j < nt; ++j) {
+          ok = issue_pv(j, 0, j & 1, (j >> 1) & 1, range[0].end, true) &&
+               (j + 2 >= nt || issue_qk(j + 2, 0, j & 1, true));
+        }
+      }
+      // nor before the MMAs that it issued have ended
+      tc::commit(bar(kBarDrain));
+      mbar_wait(bar(kBarDrain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ softmax
+    const int tile = warp >> 2;
+    const int quarter = warp & 3;  // TMEM lanes of this warp
+    const int row = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int tok = tok0 + tile * a.tile_tokens + row / a.qpk;
+    const bool valid = row < a.tile_tokens * a.qpk && tok < tok0 + n_tok;
+    const int head = h * a.qpk + row % a.qpk;
+    // visible keys [lo, limit]; rows that are not written take all, unmasked
+    const int limit = valid ? last_of(tok) : 0x7fffffff;
+    const int lo = valid ? first_of(limit) : 0;
+    const float sl2 = a.scale_log2;
+    const int n = range[tile].tiles;
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)) != 0; };
+    float m_used = -INFINITY;  // the maximum O is scaled to (log2 units)
+    float l = 0.0f;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int i = C::kTiles == 2 ? tile : j & 1;  // S buffer
+      const uint32_t use = C::kTiles == 2 ? j : j >> 1;
+      if (!wait(kBarS + i, use & 1)) { ok = false; break; }
+      tc::fence_after();
+      const uint32_t t_s = t_lane + C::s_col(i);
+      const int key0 = (t0 + j) * C::kKeys;
+      const bool need_mask = key0 + C::kKeys - 1 > limit || key0 < lo;
+      uint32_t pw[64];
+      float ts;
+      const float neg_inf = -INFINITY;
+      const float mul = need_mask ? 1.0f : sl2;  // masked tiles are scaled as they are masked
+      // P of the tile against m_used as bf16 pairs, and its sum in fp32
+      auto exp_tile = [&]() {
+        const float neg_m = m_used == neg_inf ? 0.0f : -m_used;
+        const uint64_t mul2 = f32x2_pack(mul, mul), neg_m2 = f32x2_pack(neg_m, neg_m);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t sr[32];
+          tc::ld32(t_s + cb * 32, sr);
+          tc::wait_ld();
+          if (need_mask) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int key = key0 + cb * 32 + c;
+              sr[c] = __float_as_uint(key > limit || key < lo ? neg_inf : __uint_as_float(sr[c]) * sl2);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), mul2,
+                                   neg_m2),
+                         x0, x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            sum[(c >> 1) & 1] = f32x2_add(sum[(c >> 1) & 1], f32x2_pack(p0, p1));
+            pw[cb * 16 + (c >> 1)] = pack_bf162(p0, p1);
+          }
+        }
+        float s0, s1, s2, s3;
+        f32x2_unpack(sum[0], s0, s1);
+        f32x2_unpack(sum[1], s2, s3);
+        ts = (s0 + s1) + (s2 + s3);
+      };
+      exp_tile();
+      // PV(j - 1) is done (D 64, 128: it was before S(j)): every phase is waited for, in
+      // order, and PV(j) waits for this tile's P
+      if (j > 0) {
+        if (!wait(kBarO + tile, (j - 1) & 1)) { ok = false; break; }
+        tc::fence_after();
+      }
+      const bool grow = valid && (!(ts <= C::kMaxTileSum) || m_used == neg_inf);
+      if (__any_sync(0xffffffffu, grow)) {
+        float f = 1.0f;  // factor of what O and l hold
+        float mx = neg_inf;
+#pragma unroll 1
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t sr[32];
+          tc::ld32(t_s + cb * 32, sr);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int key = key0 + cb * 32 + c;
+            const float x = __uint_as_float(sr[c]) * sl2;
+            if (key <= limit && key >= lo) mx = fmaxf(mx, x);
+          }
+        }
+        if (grow) {
+          const float m_new = fmaxf(m_used, mx);
+          if (m_new > neg_inf) {  // else nothing visible yet: P stays 0
+            f = fast_exp2(m_used - m_new);
+            l *= f;
+            m_used = m_new;
+          }
+        }
+        exp_tile();
+        if (j > 0) {
+          // O holds the tiles before this one
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t orr[32];
+            tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
+            tc::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * f);
+            tc::st32(t_lane + C::o_col(tile) + cb * 32, orr);
+          }
+          tc::wait_st();
+        }
+      }
+      l += ts;
+      tc::st32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&pw[0]));
+      tc::st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[32]));
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarP + i));
+    }
+    // ---- epilogue: O / l as bf16, lse; the sink as one term more of the sum
+    if (ok && n > 0) ok = wait(kBarO + tile, (n - 1) & 1);
+    if (ok) {
+      tc::fence_after();
+      float o_mul = 1.0f;
+      if (a.p.sinks && valid) {
+        const float sk = a.p.sinks[head] * kLog2e;
+        const float mn = fmaxf(m_used, sk);
+        if (mn > -INFINITY) {
+          o_mul = fast_exp2(m_used - mn);
+          l = l * o_mul + fast_exp2(sk - mn);
+          m_used = mn;
+        }
+      }
+      const int64_t at = static_cast<int64_t>(q0 + tok) * a.p.hq + head;
+      const bool seen = valid && limit >= 0 && n > 0;  // else no key: out = 0
+      const float inv = seen ? o_mul / l : 0.0f;
+      uint16_t *dst = a.p.out + at * D;
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t orr[32];
+        if (n > 0) {
+          tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
+          tc::wait_ld();
+        }
+        if (valid) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (seen) {
+              w.x = pack_bf162(__uint_as_float(orr[c]) * inv, __uint_as_float(orr[c + 1]) * inv);
+              w.y = pack_bf162(__uint_as_float(orr[c + 2]) * inv, __uint_as_float(orr[c + 3]) * inv);
+              w.z = pack_bf162(__uint_as_float(orr[c + 4]) * inv, __uint_as_float(orr[c + 5]) * inv);
+              w.w = pack_bf162(__uint_as_float(orr[c + 6]) * inv, __uint_as_float(orr[c + 7]) * inv);
+            }
+            *reinterpret_cast<uint4 *>(dst + cb * 32 + c) = w;
+          }
+        }
+      }
+      if (valid && a.p.lse) a.p.lse[at] = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+    }
+  }
+  if (!ok) flag_status(a.status, PA_DEV_TIMEOUT);
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+// Rows x heads x channels of bf16 as a tiled map with 128-byte swizzle.
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box,
+                  step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_d(const PromptAttention &p, cudaStream_t stream) {
+  using C = PromptCfg<D>;
+  PromptArgs a;
+  a.p = p;
+  a.status = reinterpret_cast<uint32_t *>(p.workspace);
+  a.qpk = p.hq / p.hk;
+  a.tile_tokens = 128 / a.qpk;
+  a.block_tokens = a.tile_tokens * C::kTiles;
+  a.num_items = a.block_tokens == 1 ? p.num_tokens : p.num_tokens / a.block_tokens + p.num_seqs;
+  a.scale_log2 = p.softmax_scale * kLog2e;
+  CUtensorMap mq, mk, mv;
+  const cuuint64_t qd[3] = {D, static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(p.num_tokens)};
+  const cuuint64_t qs[2] = {D * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+  const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(a.qpk), static_cast<cuuint32_t>(a.tile_tokens)};
+  // K and V rows as [kv head][64-channel chunk][key][64 channels]
+  // (without keys no copy is made: any valid map)
+  const bool none = p.num_keys == 0;
+  const cuuint64_t kd[4] = {64, static_cast<cuuint64_t>(none ? 1 : p.num_keys), D / 64, static_cast<cuuint64_t>(p.hk)};
+  const cuuint64_t ks[3] = {static_cast<cuuint64_t>(none ? p.q_stride : p.k_stride) * 2, 128, D * 2};
+  const cuuint64_t vs[3] = {static_cast<cuuint64_t>(none ? p.q_stride : p.v_stride) * 2, 128, D * 2};
+  const cuuint32_t kb[4] = {64, C::kKeys, 1, 1};
+  const cuuint32_t vb[4] = {64, C::kVKeys, D / 64, 1};
+  if (!encode(&mq, p.q, 3, qd, qs, qb) || !encode(&mk, none ? p.q : p.k, 4, kd, ks, kb) ||
+      !encode(&mv, none ? p.q : p.v, 4, kd, vs, vb))
+    return cudaErrorInvalidValue;
+  static DeviceOnce configured;
+  const cudaError_t e = configured.get(nullptr, [](int, int *) {
+    return cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = static_cast<int64_t>(a.num_items) * p.hk;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  return launch_kernel(prompt_kernel<D>, dim3(static_cast<unsigned>(blocks)), C::kThreads, C::kSmem, stream,
+                       a, mq, mk, mv);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptAttention &p, cudaStream_t stream) {
+  switch (p.d) {
+    case 64: return launch_d<64>(p, stream);
+    case 128: return launch_d<128>(p, stream);
+    case 256: return launch_d<256>(p, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace paq8

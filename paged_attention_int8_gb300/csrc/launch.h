@@ -1,6 +1,7 @@
 // Internal launch interface between the C ABI (api.cu) and the kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -39,6 +40,13 @@ class DeviceOnce {
   bool done_[kMaxDevices] = {};
   int value_[kMaxDevices] = {};
 };
+
+// cuTensorMapEncodeTiled of the driver, or null.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();
 
 cudaError_t launch_kv_store(const uint16_t *key, int64_t key_stride, const uint16_t *value,
                             int64_t value_stride, const int64_t *slot_mapping,
