@@ -22,7 +22,8 @@
 // maximum on the common path); O in TMEM is then rescaled by the softmax warps.  P is
 // rounded to bf16 (the MMA's operands are of one type); sums and O are fp32.
 // Warps: 4 softmax warps a row tile (one a TMEM lane quarter), one that issues the MMAs
-// from one elected thread, one that issues the copies.
+// from one elected thread (one a row tile lost the alternation of the two and 20 %), one
+// that issues the copies.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -70,8 +71,8 @@ constexpr int kBarEmpty = 10;  // [slots] commit of a slot's last MMA -> copy
 constexpr int kBarQ = 20;      // [2] copies of a row tile's q -> MMA
 constexpr int kBarS = 22;      // [2] commit of QK -> softmax
 constexpr int kBarP = 24;      // [2] P in TMEM (4 warps) -> MMA
-constexpr int kBarO = 26;      // [2] commit of every PV (D 256: one) -> rescale, epilogue
-constexpr int kBarDrain = 28;  // commit of all that was issued, before an early end
+constexpr int kBarO = 26;      // [2] commit of the last PV -> epilogue (D 256: [1], of every PV -> rescale)
+constexpr int kBarDrain = 28;  // commit of all that was issued, before the end
 constexpr int kNumBars = 29;
 
 // kind::f16 with bf16 operands, fp32 accumulator; n_major: B's N dimension contiguous.
@@ -106,6 +107,19 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// The wait for this thread's TMEM loads, bound to the registers of one of them, so that
+// no use of them can be moved in front of it.
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // The tiles of a row tile: keys [begin, end) that some row of it sees, in 128-key tiles
@@ -246,19 +260,32 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     if (tc::elect_one() && nt > 0) {
       constexpr uint32_t id_qk = idesc_bf16(128, C::kKeys, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
+      const uint64_t q_desc = tc::desc_sw128(smem_base + C::kQOff);
+      const uint64_t k_desc = tc::desc_sw128(smem_base);
+      const uint64_t v_desc = desc_n_major(smem_base, C::kVKeys * 128);
       auto wait = [&](int i, uint32_t parity) { return ok = mbar_wait(bar(i), parity); };
+      auto wait_slot = [&](int u) { return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1); };
+      auto wait_slots = [&](int u) {  // of a tile
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          if (!wait_slot(u + c)) return false;
+        return true;
+      };
       // S(buffer i) = Q K(j)^T; free: the tile's slots have no later use
       auto issue_qk = [&](int j, int tile, int i, bool free) -> bool {
+        const uint32_t s_tmem = tmem + C::s_col(i);
+        const uint64_t qd = q_desc + tile * (C::kQBytes >> 4);
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
           const int u = slot_of_k(j) + c, s = u % C::kSlots;
-          if (!wait(kBarFull + s, (u / C::kSlots) & 1)) return false;
-          tc::fence_after();
-          const uint64_t q_desc = tc::desc_sw128(smem_base + C::kQOff + tile * C::kQBytes + c * (128 * 128));
-          const uint64_t k_desc = tc::desc_sw128(smem_base + s * C::kSlotBytes);
+          if (C::kTiles == 1) {
+            if (!wait_slot(u)) return false;
+            tc::fence_after();
+          }
+          const uint64_t kd = k_desc + s * (C::kSlotBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc::mma_f16(tmem + C::s_col(i), q_desc + 2 * ks, k_desc + 2 * ks, id_qk,
+            tc::mma_f16(s_tmem, qd + (c * (128 * 128 >> 4) + 2 * ks), kd + 2 * ks, id_qk,
                         (c > 0 || ks > 0) ? 1u : 0u);
           if (free) tc::commit(bar(kBarEmpty + s));
         }
@@ -266,51 +293,66 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         return true;
       };
       // O(tile) += P(buffer i) V(j), over the 16-key steps below `end`
-      auto issue_pv = [&](int j, int tile, int i, uint32_t p_parity, int end, bool free) -> bool {
-        const int keys = min(C::kKeys, end - (t0 + j) * C::kKeys);
+      auto issue_pv = [&](int j, int tile, int i, uint32_t p_parity, int end, bool free,
+                          bool last) -> bool {
+        const uint32_t p_tmem = tmem + C::s_col(i), o_tmem = tmem + C::o_col(tile);
+        const int keys = end - (t0 + j) * C::kKeys;
         const int past = k_len - (t0 + j) * C::kKeys;  // keys from here on are another sequence's
         if (!wait(kBarP + i, p_parity)) return false;
         tc::fence_after();
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
           const int u = slot_of_v(j) + c, s = u % C::kSlots;
-          if (!wait(kBarFull + s, (u / C::kSlots) & 1)) return false;
-          tc::fence_after();
-          const uint32_t v = smem_base + s * C::kSlotBytes;
-          // rows of the last step that lie past the sequence meet P = 0, but may hold
-          // infinities: zeros in their place
-          if (past < keys + 15 && past % 16 && past / 16 * 16 / C::kVKeys == c) {
-            const int r0 = past - c * C::kVKeys, r1 = (past / 16 + 1) * 16 - c * C::kVKeys;
-#pragma unroll 1
-            for (int r = r0; r < r1; ++r)
-#pragma unroll 1
-              for (int b = 0; b < D * 2; b += 16)
-                sts128(v + (b >> 7) * (C::kVKeys * 128) + r * 128 + (b & 127), make_uint4(0u, 0u, 0u, 0u));
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (C::kTiles == 1) {
+            if (!wait_slot(u)) return false;
+            tc::fence_after();
           }
+          const uint64_t vd = v_desc + s * (C::kSlotBytes >> 4);
+          if (keys >= C::kKeys) {
 #pragma unroll
-          for (int ks = 0; ks < C::kVKeys / 16; ++ks) {
-            const int step = c * (C::kVKeys / 16) + ks;
-            if (step * 16 < keys)
-              tc::mma_f16_ts(tmem + C::o_col(tile), tmem + C::s_col(i) + step * 8,
-                             desc_n_major(v + ks * 2048, C::kVKeys * 128), id_pv,
-                             (j > 0 || step > 0) ? 1u : 0u);
+            for (int ks = 0; ks < C::kVKeys / 16; ++ks) {
+              const int step = c * (C::kVKeys / 16) + ks;
+              tc::mma_f16_ts(o_tmem, p_tmem + step * 8, vd + ks * 128, id_pv, (j > 0 || step > 0) ? 1u : 0u);
+            }
+          } else {
+            // rows of the last step that lie past the sequence meet P = 0, but may hold
+            // infinities: zeros in their place
+            if (past < keys + 15 && past % 16 && past / 16 * 16 / C::kVKeys == c) {
+              const uint32_t v = smem_base + s * C::kSlotBytes;
+              const int r0 = past - c * C::kVKeys, r1 = (past / 16 + 1) * 16 - c * C::kVKeys;
+#pragma unroll 1
+              for (int r = r0; r < r1; ++r)
+#pragma unroll 1
+                for (int b = 0; b < D * 2; b += 16)
+                  sts128(v + (b >> 7) * (C::kVKeys * 128) + r * 128 + (b & 127), make_uint4(0u, 0u, 0u, 0u));
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+#pragma unroll 1
+            for (int ks = 0; ks < C::kVKeys / 16; ++ks) {
+              const int step = c * (C::kVKeys / 16) + ks;
+              if (step * 16 < keys)
+                tc::mma_f16_ts(o_tmem, p_tmem + step * 8, vd + ks * 128, id_pv, (j > 0 || step > 0) ? 1u : 0u);
+            }
           }
           if (free) tc::commit(bar(kBarEmpty + s));
         }
-        tc::commit(bar(kBarO + tile));
+        if (C::kTiles == 1 || last) tc::commit(bar(kBarO + tile));
         return true;
       };
       if constexpr (C::kTiles == 2) {
         const int n0 = range[0].tiles, n1 = range[1].tiles;
         for (int j = 0; ok && j <= nt; ++j) {
+          // what both row tiles need is waited for before their P, so that nothing stands
+          // between a P and its MMAs
+          if (j >= 1) ok = wait_slots(slot_of_v(j - 1));
+          if (ok && j < nt) ok = wait_slots(slot_of_k(j));
           // the row tile's S buffer is free once its PV is issued: MMAs of one thread
           // execute in order.  A slot is freed by the last row tile that uses it.
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int n = i ? n1 : n0, other = i ? 0 : n1;
             if (ok && j >= 1 && j - 1 < n)
-              issue_pv(j - 1, i, i, (j - 1) & 1, range[i].end, i == 1 || j - 1 >= other);
+              issue_pv(j - 1, i, i, (j - 1) & 1, range[i].end, i == 1 || j - 1 >= other, j == n);
             if (ok && j < n && (j > 0 || wait(kBarQ + i, 0)))
               issue_qk(j, i, i, i == 1 || j >= other);
           }
@@ -318,11 +360,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       } else {
         ok = wait(kBarQ, 0) && issue_qk(0, 0, 0, true) && (nt < 2 || issue_qk(1, 0, 1, true));
         for (int j = 0; ok && j < nt; ++j) {
-          ok = issue_pv(j, 0, j & 1, (j >> 1) & 1, range[0].end, true) &&
+          ok = issue_pv(j, 0, j & 1, (j >> 1) & 1, range[0].end, true, j == nt - 1) &&
                (j + 2 >= nt || issue_qk(j + 2, 0, j & 1, true));
         }
       }
-      // nor before the MMAs that it issued have ended
+      // no block gives up its shared memory and TMEM before its own MMAs have ended
       tc::commit(bar(kBarDrain));
       mbar_wait(bar(kBarDrain), 0);
     }
@@ -362,11 +404,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const float neg_m = m_used == neg_inf ? 0.0f : -m_used;
         const uint64_t mul2 = f32x2_pack(mul, mul), neg_m2 = f32x2_pack(neg_m, neg_m);
         uint64_t sum[2] = {0, 0};
+        uint32_t buf[2][32];  // 32 columns in work, the next on their way
+        tc::ld32(t_s, buf[0]);
+        wait_loaded(buf[0]);
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) {
-          uint32_t sr[32];
-          tc::ld32(t_s + cb * 32, sr);
-          tc::wait_ld();
+          uint32_t(&sr)[32] = buf[cb & 1];
+          if (cb < 3) tc::ld32(t_s + (cb + 1) * 32, buf[(cb + 1) & 1]);
           if (need_mask) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
@@ -384,6 +428,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             sum[(c >> 1) & 1] = f32x2_add(sum[(c >> 1) & 1], f32x2_pack(p0, p1));
             pw[cb * 16 + (c >> 1)] = pack_bf162(p0, p1);
           }
+          if (cb < 3) wait_loaded(buf[(cb + 1) & 1]);
         }
         float s0, s1, s2, s3;
         f32x2_unpack(sum[0], s0, s1);
@@ -391,9 +436,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         ts = (s0 + s1) + (s2 + s3);
       };
       exp_tile();
-      // PV(j - 1) is done (D 64, 128: it was before S(j)): every phase is waited for, in
-      // order, and PV(j) waits for this tile's P
-      if (j > 0) {
+      // PV(j - 1) is done; D 64, 128: it was before S(j).  (Every phase is waited for, in
+      // order: PV(j) waits for this tile's P.)
+      if (C::kTiles == 1 && j > 0) {
         if (!wait(kBarO + tile, (j - 1) & 1)) { ok = false; break; }
         tc::fence_after();
       }
@@ -405,7 +450,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         for (int cb = 0; cb < 4; ++cb) {
           uint32_t sr[32];
           tc::ld32(t_s + cb * 32, sr);
-          tc::wait_ld();
+          wait_loaded(sr);
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int key = key0 + cb * 32 + c;
@@ -428,7 +473,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           for (int cb = 0; cb < D / 32; ++cb) {
             uint32_t orr[32];
             tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
-            tc::wait_ld();
+            wait_loaded(orr);
 #pragma unroll
             for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * f);
             tc::st32(t_lane + C::o_col(tile) + cb * 32, orr);
@@ -445,7 +490,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBarP + i));
     }
     // ---- epilogue: O / l as bf16, lse; the sink as one term more of the sum
-    if (ok && n > 0) ok = wait(kBarO + tile, (n - 1) & 1);
+    if (ok && n > 0) ok = wait(kBarO + tile, C::kTiles == 1 ? (n - 1) & 1 : 0);
     if (ok) {
       tc::fence_after();
       float o_mul = 1.0f;
@@ -467,7 +512,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         uint32_t orr[32];
         if (n > 0) {
           tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
-          tc::wait_ld();
+          wait_loaded(orr);
         }
         if (valid) {
 #pragma unroll
