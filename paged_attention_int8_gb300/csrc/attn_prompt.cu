@@ -18,9 +18,10 @@
 // columns): QK(j + 1) runs behind the softmax of j.
 // K and V pass through one ring of 16 KB slots: 64 channels of 128 keys, or 8192 / D keys
 // of all channels, each freed by the commit of its last MMA.
-// The maximum that P is taken against moves only when a tile's sum passes 2^12 (no row
-// maximum on the common path); O in TMEM is then rescaled by the softmax warps.  P is
-// rounded to bf16 (the MMA's operands are of one type); sums and O are fp32.
+// The maximum that P is taken against moves only when a tile's passes it by 2^8; O in TMEM
+// is then rescaled by the softmax warps.  P is handed over in two halves, so that its
+// product begins while the second is formed.  P is rounded to bf16 (the MMA's operands
+// are of one type); sums and O are fp32.
 // Warps: 4 softmax warps a row tile (one a TMEM lane quarter), one that issues the MMAs
 // from one elected thread (one a row tile lost the alternation of the two and 20 %), one
 // that issues the copies.
@@ -57,8 +58,10 @@ struct PromptCfg {
   static constexpr int kBarOff = kQOff + kTiles * kQBytes;
   static constexpr int kSmem = kBarOff + 512 + 1024;
   static constexpr int kSoftmaxWarps = 4 * kTiles;
-  static constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
-  static constexpr float kMaxTileSum = 4096.0f;
+  // two row tiles: warps in whole groups of four, so that registers can move from the
+  // last group (168 a thread at launch, 88 after) to the softmax (208: no spills)
+  static constexpr int kThreads = kTiles == 2 ? 384 : (kSoftmaxWarps + 2) * 32;
+  static constexpr float kMargin = 8.0f;  // log2 of the largest p
   // TMEM columns of S/P and of O, by row tile (D 64, 128) or by S buffer (D 256)
   __device__ static __forceinline__ uint32_t s_col(int i) { return D == 256 ? 256 + 128 * i : 256 * i; }
   __device__ static __forceinline__ uint32_t o_col(int i) { return D == 256 ? 0 : 256 * i + 128; }
@@ -70,10 +73,10 @@ constexpr int kBarFull = 0;    // [slots] copy -> MMA
 constexpr int kBarEmpty = 10;  // [slots] commit of a slot's last MMA -> copy
 constexpr int kBarQ = 20;      // [2] copies of a row tile's q -> MMA
 constexpr int kBarS = 22;      // [2] commit of QK -> softmax
-constexpr int kBarP = 24;      // [2] P in TMEM (4 warps) -> MMA
-constexpr int kBarO = 26;      // [2] commit of the last PV -> epilogue (D 256: [1], of every PV -> rescale)
-constexpr int kBarDrain = 28;  // commit of all that was issued, before the end
-constexpr int kNumBars = 29;
+constexpr int kBarP = 24;      // [2][half] 64 columns of P in TMEM (4 warps) -> MMA
+constexpr int kBarO = 28;      // [2] commit of the last PV -> epilogue (D 256: [1], of every PV -> rescale)
+constexpr int kBarDrain = 30;  // commit of all that was issued, before the end
+constexpr int kNumBars = 31;
 
 // kind::f16 with bf16 operands, fp32 accumulator; n_major: B's N dimension contiguous.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool n_major) {
@@ -150,7 +153,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(kBarQ + s), 1);
       mbar_init(bar(kBarS + s), 1);
-      mbar_init(bar(kBarP + s), 4);
+      mbar_init(bar(kBarP + 2 * s), 4);
+      mbar_init(bar(kBarP + 2 * s + 1), 4);
       mbar_init(bar(kBarO + s), 1);
     }
     mbar_init(bar(kBarDrain), 1);
@@ -203,6 +207,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 
   if (warp == kCopyWarp) {
     // ============================================================ copies
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (lane == 0 && nt > 0) {
       prefetch_tensormap(&map_q);
       prefetch_tensormap(&map_k);
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ============================================================ MMA issue
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (tc::elect_one() && nt > 0) {
       constexpr uint32_t id_qk = idesc_bf16(128, C::kKeys, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
@@ -298,10 +304,16 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const uint32_t p_tmem = tmem + C::s_col(i), o_tmem = tmem + C::o_col(tile);
         const int keys = end - (t0 + j) * C::kKeys;
         const int past = k_len - (t0 + j) * C::kKeys;  // keys from here on are another sequence's
-        if (!wait(kBarP + i, p_parity)) return false;
+        if (!wait(kBarP + 2 * i, p_parity)) return false;
         tc::fence_after();
+        auto second_half = [&]() {
+          if (!wait(kBarP + 2 * i + 1, p_parity)) return false;
+          tc::fence_after();
+          return true;
+        };
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
+          if (C::kChunks > 1 && c == C::kChunks / 2 && !second_half()) return false;
           const int u = slot_of_v(j) + c, s = u % C::kSlots;
           if (C::kTiles == 1) {
             if (!wait_slot(u)) return false;
@@ -312,9 +324,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < C::kVKeys / 16; ++ks) {
               const int step = c * (C::kVKeys / 16) + ks;
+              if (C::kChunks == 1 && ks == 4 && !second_half()) return false;
               tc::mma_f16_ts(o_tmem, p_tmem + step * 8, vd + ks * 128, id_pv, (j > 0 || step > 0) ? 1u : 0u);
             }
           } else {
+            if (C::kChunks == 1 && !second_half()) return false;
             // rows of the last step that lie past the sequence meet P = 0, but may hold
             // infinities: zeros in their place
             if (past < keys + 15 && past % 16 && past / 16 * 16 / C::kVKeys == c) {
@@ -369,8 +383,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       mbar_wait(bar(kBarDrain), 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp < C::kSoftmaxWarps) {
     // ============================================================ softmax
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int tile = warp >> 2;
     const int quarter = warp & 3;  // TMEM lanes of this warp
     const int row = quarter * 32 + lane;
@@ -394,81 +409,48 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       tc::fence_after();
       const uint32_t t_s = t_lane + C::s_col(i);
       const int key0 = (t0 + j) * C::kKeys;
-      const bool need_mask = key0 + C::kKeys - 1 > limit || key0 < lo;
-      uint32_t pw[64];
-      float ts;
-      const float neg_inf = -INFINITY;
-      const float mul = need_mask ? 1.0f : sl2;  // masked tiles are scaled as they are masked
-      // P of the tile against m_used as bf16 pairs, and its sum in fp32
-      auto exp_tile = [&]() {
-        const float neg_m = m_used == neg_inf ? 0.0f : -m_used;
-        const uint64_t mul2 = f32x2_pack(mul, mul), neg_m2 = f32x2_pack(neg_m, neg_m);
-        uint64_t sum[2] = {0, 0};
-        uint32_t buf[2][32];  // 32 columns in work, the next on their way
-        tc::ld32(t_s, buf[0]);
-        wait_loaded(buf[0]);
+      // scores that are masked, or whose factor would turn the order around, are scaled first
+      const bool first_scaled = key0 + C::kKeys - 1 > limit || key0 < lo || sl2 <= 0.0f;
+      const float mul = first_scaled ? 1.0f : sl2;
+      uint32_t sr[4][32];
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t(&sr)[32] = buf[cb & 1];
-          if (cb < 3) tc::ld32(t_s + (cb + 1) * 32, buf[(cb + 1) & 1]);
-          if (need_mask) {
+      for (int cb = 0; cb < 4; ++cb) tc::ld32(t_s + cb * 32, sr[cb]);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int key = key0 + cb * 32 + c;
-              sr[c] = __float_as_uint(key > limit || key < lo ? neg_inf : __uint_as_float(sr[c]) * sl2);
-            }
-          }
+      for (int cb = 0; cb < 4; ++cb) wait_loaded(sr[cb]);
+      if (first_scaled) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float x0, x1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), mul2,
-                                   neg_m2),
-                         x0, x1);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            sum[(c >> 1) & 1] = f32x2_add(sum[(c >> 1) & 1], f32x2_pack(p0, p1));
-            pw[cb * 16 + (c >> 1)] = pack_bf162(p0, p1);
-          }
-          if (cb < 3) wait_loaded(buf[(cb + 1) & 1]);
-        }
-        float s0, s1, s2, s3;
-        f32x2_unpack(sum[0], s0, s1);
-        f32x2_unpack(sum[1], s2, s3);
-        ts = (s0 + s1) + (s2 + s3);
-      };
-      exp_tile();
-      // PV(j - 1) is done; D 64, 128: it was before S(j).  (Every phase is waited for, in
-      // order: PV(j) waits for this tile's P.)
-      if (C::kTiles == 1 && j > 0) {
-        if (!wait(kBarO + tile, (j - 1) & 1)) { ok = false; break; }
-        tc::fence_after();
-      }
-      const bool grow = valid && (!(ts <= C::kMaxTileSum) || m_used == neg_inf);
-      if (__any_sync(0xffffffffu, grow)) {
-        float f = 1.0f;  // factor of what O and l hold
-        float mx = neg_inf;
-#pragma unroll 1
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t sr[32];
-          tc::ld32(t_s + cb * 32, sr);
-          wait_loaded(sr);
+        for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int key = key0 + cb * 32 + c;
-            const float x = __uint_as_float(sr[c]) * sl2;
-            if (key <= limit && key >= lo) mx = fmaxf(mx, x);
+            sr[cb][c] = __float_as_uint(key > limit || key < lo ? -INFINITY
+                                                                : __uint_as_float(sr[cb][c]) * sl2);
           }
-        }
+      }
+      float mx4[4];
+#pragma unroll
+      for (int cb = 0; cb < 4; ++cb) {
+        mx4[cb] = fmaxf(__uint_as_float(sr[cb][0]), __uint_as_float(sr[cb][1]));
+#pragma unroll
+        for (int c = 2; c < 32; c += 2)
+          mx4[cb] = fmax3(mx4[cb], __uint_as_float(sr[cb][c]), __uint_as_float(sr[cb][c + 1]));
+      }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
+      // PV(j - 1) is done; D 64, 128: it was before S(j).  (Every phase is waited for, in
+      // order: PV(j) waits for this tile's P.)
+      if (C::kTiles == 1 && j > 0) {
+        if (!wait(kBarO, (j - 1) & 1)) { ok = false; break; }
+        tc::fence_after();
+      }
+      const bool grow = valid && mx > m_used + C::kMargin;
+      if (__any_sync(0xffffffffu, grow)) {
+        float f = 1.0f;  // factor of what O and l hold
         if (grow) {
-          const float m_new = fmaxf(m_used, mx);
-          if (m_new > neg_inf) {  // else nothing visible yet: P stays 0
-            f = fast_exp2(m_used - m_new);
-            l *= f;
-            m_used = m_new;
-          }
+          f = fast_exp2(m_used - mx);
+          l *= f;
+          m_used = mx;
         }
-        exp_tile();
         if (j > 0) {
-          // O holds the tiles before this one
 #pragma unroll 1
           for (int cb = 0; cb < D / 32; ++cb) {
             uint32_t orr[32];
@@ -481,13 +463,34 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           tc::wait_st();
         }
       }
-      l += ts;
-      tc::st32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&pw[0]));
-      tc::st32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[32]));
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarP + i));
+      // P against m_used as bf16 pairs, and its sum in fp32, 64 columns at a time
+      const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;  // (no key yet: all masked)
+      const uint64_t mul2 = f32x2_pack(mul, mul), neg_m2 = f32x2_pack(neg_m, neg_m);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pw[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const uint32_t(&x)[32] = sr[2 * half + (c >> 5)];
+          float x0, x1;
+          f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[c & 31]), __uint_as_float(x[(c & 31) + 1])),
+                                 mul2, neg_m2),
+                       x0, x1);
+          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+          sum[(c >> 1) & 1] = f32x2_add(sum[(c >> 1) & 1], f32x2_pack(p0, p1));
+          pw[c >> 1] = pack_bf162(p0, p1);
+        }
+        tc::st32(t_s + half * 32, pw);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + 2 * i + half));
+      }
+      float s0, s1, s2, s3;
+      f32x2_unpack(sum[0], s0, s1);
+      f32x2_unpack(sum[1], s2, s3);
+      l += (s0 + s1) + (s2 + s3);
     }
     // ---- epilogue: O / l as bf16, lse; the sink as one term more of the sum
     if (ok && n > 0) ok = wait(kBarO + tile, C::kTiles == 1 ? (n - 1) & 1 : 0);
@@ -530,6 +533,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
       if (valid && a.p.lse) a.p.lse[at] = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * kLn2;
     }
+  } else {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   }
   if (!ok) flag_status(a.status, PA_DEV_TIMEOUT);
 
