@@ -391,10 +391,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           }
         }
       } else {
-        ok = wait(kBarQ, 0) && issue_qk(0, 0, 0, true) && (nt < 2 || issue_qk(1, 0, 1, true));
-        for (int j = 0; ok && j < nt; ++j) {
-          ok = issue_pv(j, 0, j & 1, (j >> 1) & 1, range[0].end, true, j == nt - 1) &&
-               (j + 2 >= nt || issue_qk(j + 2, 0, j & 1, true));
+        ok = wait(kBarQ, 0);
+#pragma unroll 1
+        for (int j = 0; ok && j < nt + 2; ++j) {
+          if (j >= 2) ok = issue_pv(j - 2, 0, j & 1, ((j - 2) >> 1) & 1, range[0].end, true, true);
+          if (ok && j < nt) ok = issue_qk(j, 0, j & 1, true);
         }
       }
       // no block gives up its shared memory and TMEM before its own MMAs have ended
@@ -455,12 +456,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           mx4[cb] = fmax3(mx4[cb], __uint_as_float(sr[cb][c]), __uint_as_float(sr[cb][c + 1]));
       }
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
-      // PV(j - 1) is done; D 64, 128: it was before S(j).  (Every phase is waited for, in
-      // order: PV(j) waits for this tile's P.)
-      if (C::kTiles == 1 && j > 0) {
-        if (!wait(kBarO, (j - 1) & 1)) { ok = false; break; }
-        tc::fence_after();
-      }
+      // D 256: every PV's phase is waited for, in order, before O is rescaled or behind this
+      // tile's P; D 64, 128: PV(j - 1) was before S(j)
+      bool await_pv = C::kTiles == 1 && j > 0;
       const bool grow = valid && mx > m_used + C::kMargin;
       if (__any_sync(0xffffffffu, grow)) {
         float f = 1.0f;  // factor of what O and l hold
@@ -468,6 +466,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           f = fast_exp2(m_used - mx);
           l *= f;
           m_used = mx;
+        }
+        if (await_pv) {
+          if (!wait(kBarO, (j - 1) & 1)) { ok = false; break; }
+          tc::fence_after();
+          await_pv = false;
         }
         if (j > 0) {
 #pragma unroll 1
@@ -510,6 +513,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       f32x2_unpack(sum[0], s0, s1);
       f32x2_unpack(sum[1], s2, s3);
       l += (s0 + s1) + (s2 + s3);
+      if (await_pv && !wait(kBarO, (j - 1) & 1)) { ok = false; break; }
     }
     // ---- epilogue: O / l as bf16, lse; the sink as one term more of the sum
     if (ok && n > 0) ok = wait(kBarO + tile, C::kTiles == 1 ? (n - 1) & 1 : 0);
