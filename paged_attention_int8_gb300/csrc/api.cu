@@ -1002,6 +1002,7 @@ pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *
     return fail(PA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   if (misaligned(3, {lse, sinks, cu_seqlens_q, seq_lens, block_table}))
     return fail(PA_ERR_INVALID_ARG, "lse, sinks and the int32 arrays must be 4-byte aligned");
+  if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 kv heads");
   // items of rows, and rows of the join, of all kv heads and segments: one grid
   if (static_cast<int64_t>(num_tokens) + num_seqs >= (int64_t{1} << 31) ||
       (static_cast<int64_t>(num_tokens) + num_seqs) * num_q_heads >= (int64_t{1} << 31))
@@ -1015,8 +1016,6 @@ pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *
   if (workspace_bytes < pa_workspace_size(num_tokens, num_q_heads, head_dim, ns))
     return fail(PA_ERR_INVALID_ARG, ns > 1 ? "workspace too small for num_splits"
                                            : "workspace smaller than 256 bytes");
-  if ((static_cast<int64_t>(num_tokens) + num_seqs) * num_kv_heads * ns >= (int64_t{1} << 31))
-    return fail(PA_ERR_UNSUPPORTED, "(num_tokens + num_seqs) * num_kv_heads * num_splits must be < 2^31");
   paq8::AttnQ4 p;
   p.q = static_cast<const uint16_t *>(q);
   p.k_cache = static_cast<const uint8_t *>(k_cache);

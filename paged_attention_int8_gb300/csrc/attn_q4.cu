@@ -43,7 +43,7 @@ struct Q4Args {
   uint32_t *status;
   float *part_acc;   // [T * Hq][splits][D]
   float2 *part_ml;   // [T * Hq][splits]
-  int32_t qpk, block_tokens, num_items, seg_blocks, num_splits;
+  int32_t qpk, qpk_inverse, block_tokens, num_items, seg_blocks, num_splits;
   float scale_log2;
 };
 
@@ -105,6 +105,10 @@ __device__ __forceinline__ float half_hi(uint32_t w) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16)));
 }
 
+__device__ __forceinline__ void sts16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
 // N 32-bit words from shared memory.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
@@ -143,7 +147,7 @@ __device__ __forceinline__ uint32_t v_place(int r, int c) {
 }
 
 template <int D, int BS, int NB>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (NB == 2 ? 3 : 5))
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (NB == 2 ? 3 : D == 128 ? 4 : 5))
     attn_q4_kernel(const __grid_constant__ Q4Args a) {
   using C = Q4Cfg<D>;
   constexpr int G = C::G;
@@ -153,10 +157,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
 
   wait_for_predecessor();
   launch_dependents();  // the join waits for all of this grid
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.p.hk));
-  const int rest = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.p.hk));
-  const int item = rest % a.num_items;
-  const int sigma = rest / a.num_items;
+  const int item = blockIdx.x, h = blockIdx.y, sigma = blockIdx.z;
+  // r / qpk of a row r < 128 of the block
+  const auto token_of = [&](int r) { return (r * a.qpk_inverse) >> 16; };
 
   // ---- which rows, which keys
   int seq = item, tok0 = 0;
@@ -196,8 +199,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
   for (int nb = 0; nb < NB; ++nb) {
     const int row = nb * 8 + g;
     const bool real = row < n_rows;
-    const int tok = q0 + tok0 + (real ? row / a.qpk : 0);
-    const uint16_t *src = a.p.q + (static_cast<int64_t>(tok) * a.p.hq + h * a.qpk + (real ? row % a.qpk : 0)) * D;
+    const int tr = real ? token_of(row) : 0;
+    const uint16_t *src = a.p.q + (static_cast<int64_t>(q0 + tok0 + tr) * a.p.hq + h * a.qpk +
+                                   (real ? row - tr * a.qpk : 0)) * D;
     float sums[G];
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     for (int c = 0; c < 2; ++c) {
       const int r = nb * 8 + 2 * t + c;
       // rows past the last take its keys, so that their arithmetic stays finite
-      const int i = tok0 + (r < n_rows ? r : n_rows - 1) / a.qpk;
+      const int i = tok0 + token_of(r < n_rows ? r : n_rows - 1);
       lim[nb][c] = a.p.causal ? seq_len - q_len + i : seq_len - 1;
       lo[nb][c] = a.p.window > 0 ? max(0, lim[nb][c] - a.p.window + 1) : 0;
       min_lim = min(min_lim, lim[nb][c]);
@@ -250,10 +254,36 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
   // ---- this warp's copies: block b of the segment for b % 4 == warp
   const uint32_t ring = smem_u32(smem_raw) + warp * (C::kStages * C::kBlock);
   const int n_mine = (seg1 - seg0 - warp + kWarps - 1) / kWarps;  // may be <= 0
-  constexpr int kCodeChunks = 16 * C::kRow / 16;  // of K, and of V
+  constexpr int kPer = 16 * C::kRow / 16 / 32;    // code chunks a lane, of K and of V
   constexpr int kScChunks = 16 * G * 2 / 16;      // of one plane of scales or zeros
+  constexpr int kScPer = (4 * kScChunks + 31) / 32;
   constexpr int kPlane = BS * G * 2;              // bytes of a page's plane
+  constexpr int kRowChunks = C::kRow / 16;
   const int32_t *table = a.p.block_table + static_cast<int64_t>(seq) * a.p.table_stride;
+  // this lane's chunks: where they stand in a page, and where they go in a stage
+  const uint8_t *k_src = a.p.k_cache + static_cast<int64_t>(h) * BS * C::kRow + lane * 16;
+  const uint8_t *v_src = a.p.v_cache + static_cast<int64_t>(h) * BS * C::kRow + lane * 16;
+  const int64_t code_page = static_cast<int64_t>(a.p.hk) * BS * C::kRow;
+  const int64_t scale_page = static_cast<int64_t>(a.p.hk) * 2 * kPlane;
+  uint32_t k_dst[kPer], v_dst[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int c = k * 32 + lane;
+    k_dst[k] = k_place<D>(c / kRowChunks, c % kRowChunks);
+    v_dst[k] = C::kV + v_place<D>(c / kRowChunks, c % kRowChunks);
+  }
+  const uint8_t *sc_src[kScPer];  // planes: K scales, K zeros, V scales, V zeros
+  uint32_t sc_dst[kScPer], sc_half[kScPer];  // sc_half: to the page's second 16 keys
+#pragma unroll
+  for (int k = 0; k < kScPer; ++k) {
+    const int c = k * 32 + lane, plane = (c / kScChunks) & 1, x = c % kScChunks;
+    const bool keys = c < 2 * kScChunks;
+    sc_src[k] = reinterpret_cast<const uint8_t *>(keys ? a.p.k_scale : a.p.v_scale) +
+                static_cast<int64_t>(h) * 2 * kPlane + plane * kPlane +
+                (keys ? x * 16 : (x >> 1) * (BS * 2) + (x & 1) * 16);
+    sc_dst[k] = keys ? C::kKs + c * 16 : C::kVs + (c - 2 * kScChunks) * 16;
+    sc_half[k] = keys ? 16 * G * 2 : 32;
+  }
   int entries = -1;  // page of this warp's block (32 i + lane), refilled every 32 blocks
   auto refill = [&](int i) {
     const int b = seg0 + warp + (i + lane) * kWarps;
@@ -274,34 +304,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     if (i < n_mine && e >= 0) {
       live |= 1u << stage;
       const uint32_t st = ring + stage * C::kBlock;
-      const int64_t page = static_cast<int64_t>(e) * a.p.hk + h;
-      const int off = BS == 32 ? ((seg0 + warp + i * kWarps) & 1) * 16 : 0;  // first key in the page
-      const uint8_t *kc = a.p.k_cache + (page * BS + off) * C::kRow;
-      const uint8_t *vc = a.p.v_cache + (page * BS + off) * C::kRow;
+      const int second = BS == 32 ? (seg0 + warp + i * kWarps) & 1 : 0;  // half of the page
+      const int64_t code = e * code_page + second * (16 * C::kRow), scale = e * scale_page;
 #pragma unroll
-      for (int k = 0; k < kCodeChunks; k += 32) {
-        const int c = k + lane;
-        cp_async_16(st + k_place<D>(c / (C::kRow / 16), c % (C::kRow / 16)), kc + c * 16);
-      }
+      for (int k = 0; k < kPer; ++k) cp_async_16(st + k_dst[k], k_src + code + k * 512);
 #pragma unroll
-      for (int k = 0; k < kCodeChunks; k += 32) {
-        const int c = k + lane;
-        cp_async_16(st + C::kV + v_place<D>(c / (C::kRow / 16), c % (C::kRow / 16)), vc + c * 16);
-      }
-      const uint8_t *ks = reinterpret_cast<const uint8_t *>(a.p.k_scale) + page * (2 * kPlane);
-      const uint8_t *vs = reinterpret_cast<const uint8_t *>(a.p.v_scale) + page * (2 * kPlane);
+      for (int k = 0; k < kPer; ++k) cp_async_16(st + v_dst[k], v_src + code + k * 512);
 #pragma unroll
-      for (int k = 0; k < 4 * kScChunks; k += 32) {
-        const int c = k + lane;  // planes: K scales, K zeros, V scales, V zeros
-        if (c < 4 * kScChunks) {
-          const int plane = (c / kScChunks) & 1, x = c % kScChunks;
-          if (c < 2 * kScChunks)
-            cp_async_16(st + C::kKs + c * 16, ks + plane * kPlane + off * (G * 2) + x * 16);
-          else  // rows of BS keys: two chunks of 16 keys each
-            cp_async_16(st + C::kVs + (c - 2 * kScChunks) * 16,
-                        vs + plane * kPlane + (x >> 1) * (BS * 2) + off * 2 + (x & 1) * 16);
-        }
-      }
+      for (int k = 0; k < kScPer; ++k)
+        if (4 * kScChunks % 32 == 0 || k * 32 + lane < 4 * kScChunks)
+          cp_async_16(st + sc_dst[k], sc_src[k] + scale + second * sc_half[k]);
     }
     cp_async_commit();
   };
@@ -326,7 +338,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
   }
   const float c1 = a.scale_log2 * 0x1p24f;  // of sum_g s_g (q c 2^-24)
   const float c2 = a.scale_log2 * 32.0f;    // of sum_g z_g (q sum / 32)
+  float m_safe[NB][2];  // m_used, 0 before the first key
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) m_safe[nb][0] = m_safe[nb][1] = 0.0f;
   const int key_r0 = perm16(g), key_r1 = perm16(g + 8);
+  bool started = false;
 
   for (int i = 0; i < n_mine; ++i) {
     cp_async_wait<C::kStages - 2>();
@@ -391,7 +407,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
         float zp[4];
         mma_first(zp, z0, z1, z0, z1, qs[nb][0], qs[nb][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nb][e] = fmaf(acc[nb][e], c1, zp[e] * c2);
+        for (int e = 0; e < 4; ++e)  // scores less m_safe, log2 units
+          s[nb][e] = fmaf(acc[nb][e], c1, fmaf(zp[e], c2, -m_safe[nb][e & 1]));
       }
     }
     // keys that a row does not see (and stale ones: whatever stands there)
@@ -406,12 +423,15 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     }
 
     // ---- softmax against m_used, which moves only when a score passes it by kMargin
-    bool over = false;
+    float top = s[0][0];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) over = over || s[nb][e] > m_used[nb][e & 1] + kMargin;
-    if (__any_sync(0xffffffffu, over)) {
+      for (int e = 0; e < 4; e += 2) top = fmax3(top, s[nb][e], s[nb][e + 1]);
+    }
+    // (before a row's first key any score moves it: it stands at -inf)
+    if (__any_sync(0xffffffffu, top > (started ? kMargin : -INFINITY))) {
+      bool all = true;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -419,19 +439,26 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
           float mx = fmaxf(s[nb][c], s[nb][2 + c]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          const float mn = fmaxf(m_used[nb][c], mx);
-          const float f = mn == -INFINITY ? 1.0f : fast_exp2(m_used[nb][c] - mn);
-          m_used[nb][c] = mn;
-          l[nb][c] *= f;
-          oz[nb][c] *= f;
+          const float mn = fmaxf(m_used[nb][c], mx + m_safe[nb][c]);
+          if (mn > -INFINITY) {
+            const float d = m_safe[nb][c] - mn, f = fast_exp2(m_used[nb][c] - mn);
+            s[nb][c] += d;
+            s[nb][2 + c] += d;
+            m_used[nb][c] = m_safe[nb][c] = mn;
+            l[nb][c] *= f;
+            oz[nb][c] *= f;
 #pragma unroll
-          for (int gr = 0; gr < G; ++gr) {
-            o[nb][gr][0][c] *= f;
-            o[nb][gr][0][2 + c] *= f;
-            o[nb][gr][1][c] *= f;
-            o[nb][gr][1][2 + c] *= f;
+            for (int gr = 0; gr < G; ++gr) {
+              o[nb][gr][0][c] *= f;
+              o[nb][gr][0][2 + c] *= f;
+              o[nb][gr][1][c] *= f;
+              o[nb][gr][1][2 + c] *= f;
+            }
+          } else {
+            all = false;
           }
         }
+      started = __all_sync(0xffffffffu, all);  // every row of the warp has a maximum
     }
     uint32_t pb[NB][2];
 #pragma unroll
@@ -439,8 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float m = m_used[nb][e & 1];
-        p[e] = fast_exp2(s[nb][e] - (m == -INFINITY ? 0.0f : m));
+        p[e] = fast_exp2(s[nb][e]);
       }
       l[nb][0] += p[0] + p[2];
       l[nb][1] += p[1] + p[3];
@@ -449,19 +475,19 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     }
 
     // ---- output: keys 4t .. 4t + 3
-    const bool tail = key0 + 16 > range.end || key0 < range.begin;
-    uint2 keep = make_uint2(0xffffffffu, 0xffffffffu);  // keys that no row sees may hold anything
-    if (tail) {
-      const auto in = [&](int k) { return k >= range.begin && k < range.end; };
-      const int k = key0 + 4 * t;
-      keep.x = (in(k) ? 0x0000ffffu : 0u) | (in(k + 1) ? 0xffff0000u : 0u);
-      keep.y = (in(k + 2) ? 0x0000ffffu : 0u) | (in(k + 3) ? 0xffff0000u : 0u);
+    // keys that no row sees may hold anything: zeros for their scales and zeros
+    if (key0 + 16 > range.end || key0 < range.begin) {
+#pragma unroll
+      for (int k = 0; k < 16 * G * 2 / 32; ++k) {
+        const int key = key0 + (lane & 15);
+        if (key >= range.end || key < range.begin)
+          sts16(st + C::kVs + (2 * k + (lane >> 4)) * 32 + (lane & 15) * 2, 0);
+      }
+      __syncwarp();
     }
     {
       uint2 z = lds64(st + C::kVs + (G + (g < G ? g : 0)) * 32 + t * 8);
       if (g >= G) z = make_uint2(0u, 0u);
-      z.x &= keep.x;
-      z.y &= keep.y;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) mma_f16_16816(oz[nb], z.x, 0u, z.y, 0u, pb[nb][0], pb[nb][1]);
     }
@@ -475,9 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     }
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
-      uint2 sc = lds64(st + C::kVs + gr * 32 + t * 8);
-      sc.x &= keep.x;
-      sc.y &= keep.y;
+      const uint2 sc = lds64(st + C::kVs + gr * 32 + t * 8);
       const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
       const uint32_t x01 = __byte_perm(vw[0][gr >> 1], vw[1][gr >> 1], sel);
       const uint32_t x23 = __byte_perm(vw[2][gr >> 1], vw[3][gr >> 1], sel);
@@ -561,9 +585,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     for (int c = 0; c < 2; ++c) {
       const int row = nb * 8 + 2 * t + c;
       if (row >= n_rows) continue;
-      const int64_t tok = q0 + tok0 + row / a.qpk;
-      const int head = h * a.qpk + row % a.qpk;
-      const int64_t at = tok * a.p.hq + head;
+      const int tr = token_of(row);
+      const int head = h * a.qpk + row - tr * a.qpk;
+      const int64_t at = static_cast<int64_t>(q0 + tok0 + tr) * a.p.hq + head;
       float m = m_used[nb][c], sum = l[nb][c];
       if (a.num_splits > 1) {
         const int64_t prow = at * a.num_splits + sigma;
@@ -662,10 +686,9 @@ cudaError_t launch_rows(const Q4Args &a, cudaStream_t stream) {
                                 kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(a.num_items) * a.p.hk * a.num_splits;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_kernel(attn_q4_kernel<D, BS, NB>, dim3(static_cast<unsigned>(blocks)), kWarps * 32,
-                       kSmem, stream, a);
+  const dim3 grid(static_cast<unsigned>(a.num_items), static_cast<unsigned>(a.p.hk),
+                  static_cast<unsigned>(a.num_splits));
+  return launch_kernel(attn_q4_kernel<D, BS, NB>, grid, kWarps * 32, kSmem, stream, a);
 }
 
 template <int D>
@@ -708,6 +731,7 @@ cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {
   a.part_ml = reinterpret_cast<float2 *>(a.part_acc + static_cast<int64_t>(p.num_tokens) * p.hq *
                                                           p.num_splits * p.d);
   a.qpk = p.hq / p.hk;
+  a.qpk_inverse = 65536 / a.qpk + 1;
   a.block_tokens = q4_block_tokens(a.qpk, p.max_query_len);
   a.num_items = p.max_query_len <= 1 ? p.num_seqs
                 : a.block_tokens == 1 ? p.num_tokens
