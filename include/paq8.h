@@ -614,16 +614,27 @@ pa_status pa_kv_load_q4(void *key, int64_t key_token_stride, void *value,
                         uint32_t *status, void *stream);
 
 /*
+ * Bytes of workspace pa_paged_attention_q4 uses for these bounds: 256 bytes of header
+ * (the status word at offset 0) plus an fp32 triple of head_dim + 2 for every query row
+ * (num_tokens * num_q_heads) and key segment, where there are several (num_splits, 0:
+ * the automatic number).  256 for sizes out of range.
+ */
+size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens,
+                                            int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_query_len,
+                                            int32_t max_seq_len, int32_t num_splits);
+
+/*
  * paged_attention over the 4-bit format: as pa_paged_attention_ex (query lengths
  * from 1, key segments, non-causal mode, sinks, sliding window), with these
  * differences:
  *   block_table    rows block_table_stride apart, of which block_table_columns
  *                  entries are read.  Keys past them, or behind an entry outside
  *                  [0, num_blocks), are flagged PA_DEV_BAD_BLOCK and left out.
- *   num_splits     segments apply to every query row, not to single tokens alone:
- *                  the workspace takes pa_workspace_size(num_tokens, num_q_heads,
- *                  head_dim, num_splits) bytes.  With 0 a smaller workspace takes
- *                  fewer segments, down to 256 bytes and one.
+ *   num_splits     0 .. 64; segments apply to every query row, not to single tokens
+ *                  alone.  With 0 (automatic) a workspace smaller than
+ *                  pa_paged_attention_q4_workspace_size takes fewer segments, down to
+ *                  256 bytes and one.
  *   max_query_len  1: a sequence with more query tokens is left unprocessed and
  *                  flagged PA_DEV_BAD_SEQ.  The time of a long query grows with its
  *                  blocks of 16 rows (tokens x q heads of a kv head), each of which

@@ -21,6 +21,7 @@ __all__ = ["kv_store", "kv_store_norm_rope", "kv_store_f8v4", "paged_attention",
            "build_block_tables", "BlockTables", "copy_blocks", "copy_blocks_f8v4",
            "paged_attention_shared_prefix", "paged_attention_shared_prefix_f8v4",
            "kv_store_q4", "kv_load", "kv_load_f8v4", "kv_load_q4", "paged_attention_q4",
+           "paged_attention_q4_workspace_size",
            "prompt_attention", "prompt_attention_workspace_size",
            "shared_prefix_workspace_size", "workspace_size", "check_status",
            "auto_num_splits", "Status", "PagedAttentionError", "library_path"]

@@ -121,6 +121,8 @@ def load():
         lib.pa_paged_attention_q4.argtypes = [P] * 8 + [i32] * 11 + [
             ctypes.c_float, i32, P, i32, P, P, P, ctypes.c_size_t, ctypes.c_uint32, P]
         lib.pa_paged_attention_q4.restype = ctypes.c_int
+        lib.pa_paged_attention_q4_workspace_size.argtypes = [i32] * 8
+        lib.pa_paged_attention_q4_workspace_size.restype = ctypes.c_size_t
         lib.pa_prompt_attention_workspace_size.argtypes = [i32] * 8
         lib.pa_prompt_attention_workspace_size.restype = ctypes.c_size_t
         lib.pa_prompt_attention.argtypes = [P, i64, P, i64, P, i64, P, P] + [i32] * 8 + [
@@ -1009,6 +1011,15 @@ def _check_sinks(dev, sinks, hq):
             raise ValueError("sinks must be [num_q_heads]")
 
 
+def paged_attention_q4_workspace_size(num_seqs: int, num_tokens: int, num_q_heads: int,
+                                      num_kv_heads: int, head_dim: int, max_query_len: int,
+                                      max_seq_len: int, num_splits: int = 0) -> int:
+    """Bytes of workspace paged_attention_q4 uses for these bounds."""
+    return int(load().pa_paged_attention_q4_workspace_size(
+        num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_query_len, max_seq_len,
+        num_splits))
+
+
 def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_lens, block_table,
                        max_query_len: int, max_seq_len: int, softmax_scale: float | None = None,
                        num_splits: int = 0, out=None, lse=None, workspace=None, stream=None,
@@ -1016,8 +1027,8 @@ def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_
                        sliding_window: int = 0):
     """paged_attention over the 4-bit format (pa_paged_attention_q4): arguments and
     results as paged_attention, for any query lengths.  ``workspace``: optional uint8
-    CUDA tensor of ``workspace_size(T, Hq, D, num_splits)`` bytes (T query tokens) whose
-    first 4 bytes are zero; a smaller one takes fewer key segments."""
+    CUDA tensor of ``paged_attention_q4_workspace_size`` bytes whose first 4 bytes are zero; a
+    smaller one takes fewer key segments."""
     dev = q.get_device()
     if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
@@ -1038,7 +1049,8 @@ def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_
         raise ValueError("metadata shapes disagree with seq_lens")
     _check_sinks(dev, sinks, hq)
     out, lse = _results(dev, q, out, lse, return_lse, stream)
-    workspace = _workspace(dev, workspace, lambda: workspace_size(t, hq, d, num_splits), stream)
+    workspace = _workspace(dev, workspace, lambda: paged_attention_q4_workspace_size(
+        s, t, hq, hk, d, max_query_len, max_seq_len, num_splits), stream)
     _call((_lib or load()).pa_paged_attention_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(),
           k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), cu_seqlens_q.data_ptr(),
           seq_lens.data_ptr(), block_table.data_ptr(), table_stride, columns, s, t, hq, hk, d, nb,

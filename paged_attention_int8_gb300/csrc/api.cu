@@ -962,6 +962,20 @@ PAQ8_KV_LOAD(pa_kv_load_f8v4, f8v4)
 PAQ8_KV_LOAD(pa_kv_load_q4, q4)
 #undef PAQ8_KV_LOAD
 
+size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens,
+                                            int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t max_query_len,
+                                            int32_t max_seq_len, int32_t num_splits) {
+  if (num_seqs <= 0 || num_tokens <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads ||
+      num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16 || !supported_dim(head_dim) ||
+      max_query_len <= 0 || max_seq_len <= 0 || num_splits < 0 || num_splits > 64)
+    return 256;
+  const int32_t ns = num_splits ? num_splits
+                                : paq8::q4_auto_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                       head_dim, max_query_len, max_seq_len);
+  return ns == 1 ? 256 : shared_bytes(num_tokens, num_q_heads, head_dim, ns);
+}
+
 pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
                                 const void *v_cache, const void *v_scale,
                                 const int32_t *cu_seqlens_q, const int32_t *seq_lens,
@@ -997,7 +1011,7 @@ pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *
                                     "less than them");
   if (max_query_len <= 0 || max_seq_len <= 0 || max_seq_len > 0x7fffffff - 4096)
     return fail(PA_ERR_INVALID_ARG, "max_query_len and max_seq_len must be positive");
-  if (num_splits < 0 || num_splits > 16) return fail(PA_ERR_INVALID_ARG, "num_splits in [0, 16]");
+  if (num_splits < 0 || num_splits > 64) return fail(PA_ERR_INVALID_ARG, "num_splits in [0, 64]");
   if (misaligned(15, {q, out, workspace}))
     return fail(PA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   if (misaligned(3, {lse, sinks, cu_seqlens_q, seq_lens, block_table}))
@@ -1011,9 +1025,12 @@ pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *
   int32_t ns = num_splits == 0 ? paq8::q4_auto_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
                                                       head_dim, max_query_len, seen)
                                : num_splits;
+  const auto need = [&](int32_t n) {
+    return n == 1 ? size_t{256} : shared_bytes(num_tokens, num_q_heads, head_dim, n);
+  };
   if (num_splits == 0)
-    while (ns > 1 && workspace_bytes < pa_workspace_size(num_tokens, num_q_heads, head_dim, ns)) --ns;
-  if (workspace_bytes < pa_workspace_size(num_tokens, num_q_heads, head_dim, ns))
+    while (ns > 1 && workspace_bytes < need(ns)) --ns;
+  if (workspace_bytes < need(ns))
     return fail(PA_ERR_INVALID_ARG, ns > 1 ? "workspace too small for num_splits"
                                            : "workspace smaller than 256 bytes");
   paq8::AttnQ4 p;

@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr float kMargin = 2.0f;  // log2 of the largest p
+constexpr int kMaxSegments = 64;
 
 struct Q4Args {
   AttnQ4 p;
@@ -56,7 +57,7 @@ struct Q4Cfg {
   static constexpr int kV = kKs + 16 * G * 4;        // V codes
   static constexpr int kVs = kV + 16 * kRow;         // V scales [G][16], zeros [G][16]
   static constexpr int kBlock = kVs + 16 * G * 4;    // 20 D bytes
-  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 5 : 4;
+  static constexpr int kStages = D == 256 ? 4 : 6;
 };
 
 // Visible keys of the block of rows that starts at token tok0 of a sequence, in
@@ -146,11 +147,17 @@ __device__ __forceinline__ uint32_t v_place(int r, int c) {
   return (i * 4 + t) * (D / 2) + (c ^ x) * 16;
 }
 
+// Thread blocks an SM, by registers and by the rings.
+constexpr int resident_blocks(int d, bool wide) { return d == 256 ? (wide ? 2 : 3) : wide || d == 128 ? 3 : 5; }
+// Two blocks of keys at a time where their registers fit: the chain from a block's scores to
+// its products is long, and a second one fills its gaps.
+constexpr int keys_blocks(int d, bool wide) { return d <= 128 && !wide ? 2 : 1; }
+
 template <int D, int BS, int NB>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (NB == 2 ? 3 : D == 128 ? 4 : 5))
-    attn_q4_kernel(const __grid_constant__ Q4Args a) {
+__global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn_q4_kernel(const __grid_constant__ Q4Args a) {
   using C = Q4Cfg<D>;
   constexpr int G = C::G;
+  constexpr int KB = keys_blocks(D, NB == 2);  // blocks of keys in work together
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+  for (int i = 0; i < C::kStages - KB; ++i) issue(i);
 
   float m_used[NB][2], l[NB][2];  // rows 2t, 2t + 1 (log2 units; l: this lane's share)
   float o[NB][G][2][4], oz[NB][4];
@@ -344,22 +351,33 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
   const int key_r0 = perm16(g), key_r1 = perm16(g + 8);
   bool started = false;
 
-  for (int i = 0; i < n_mine; ++i) {
-    cp_async_wait<C::kStages - 2>();
+  for (int i = 0; i < n_mine; i += KB) {
+    cp_async_wait<C::kStages - 2 * KB>();
     __syncwarp();
-    issue(i + C::kStages - 1);  // into the stage that the last block left
-    const int stage = i % C::kStages;
-    if (!((live >> stage) & 1u)) continue;  // no such page: its keys are left out
-    const uint32_t st = ring + stage * C::kBlock;
-    const int key0 = (seg0 + warp + i * kWarps) * 16;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) issue(i + kb + C::kStages - KB);  // where the last blocks stood
+    uint32_t st[KB];
+    int key0[KB];
+    bool dead[KB];  // no block, or no such page: its keys are left out
+    bool edge = false;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int stage = (i + kb) % C::kStages;
+      st[kb] = ring + stage * C::kBlock;
+      key0[kb] = (seg0 + warp + (i + kb) * kWarps) * 16;
+      dead[kb] = !((live >> stage) & 1u);
+      edge = edge || dead[kb] || key0[kb] + 15 > min_lim || key0[kb] < max_lo;
+    }
+    if (KB == 1 && dead[0]) continue;
 
     // ---- scores
-    float s[NB][4];
-    {
+    float s[KB][NB][4];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
       uint32_t w0[G], w1[G];  // codes of key rows g and g + 8, one word a group
       if constexpr (D == 256) {
         const int x = g & 1;  // rows g and g + 8: the same parity
-        const uint32_t r0 = st + g * C::kRow + t * 32, r1 = r0 + 8 * C::kRow;
+        const uint32_t r0 = st[kb] + g * C::kRow + t * 32, r1 = r0 + 8 * C::kRow;
         const uint4 a0 = lds128(r0 + x * 16), a1 = lds128(r0 + (x ^ 1) * 16);
         const uint4 b0 = lds128(r1 + x * 16), b1 = lds128(r1 + (x ^ 1) * 16);
         w0[0] = a0.x; w0[1] = a0.y; w0[2] = a0.z; w0[3] = a0.w;
@@ -367,14 +385,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
         w1[0] = b0.x; w1[1] = b0.y; w1[2] = b0.z; w1[3] = b0.w;
         w1[4] = b1.x; w1[5] = b1.y; w1[6] = b1.z; w1[7] = b1.w;
       } else {
-        lds_words(st + g * C::kRow + t * (G * 4), w0);
-        lds_words(st + (g + 8) * C::kRow + t * (G * 4), w1);
+        lds_words(st[kb] + g * C::kRow + t * (G * 4), w0);
+        lds_words(st[kb] + (g + 8) * C::kRow + t * (G * 4), w1);
       }
       uint32_t sw0[G / 2], sw1[G / 2];  // scales of the two keys, two groups a word
-      lds_words(st + C::kKs + key_r0 * (G * 2), sw0);
-      lds_words(st + C::kKs + key_r1 * (G * 2), sw1);
+      lds_words(st[kb] + C::kKs + key_r0 * (G * 2), sw0);
+      lds_words(st[kb] + C::kKs + key_r1 * (G * 2), sw1);
       const bool has = 2 * t < G;
-      const uint32_t zk = st + C::kKs + 16 * G * 2 + (has ? 4 * t : 0);
+      const uint32_t zk = st[kb] + C::kKs + 16 * G * 2 + (has ? 4 * t : 0);
       uint32_t z0 = lds32(zk + key_r0 * (G * 2)), z1 = lds32(zk + key_r1 * (G * 2));
       if (!has) z0 = z1 = 0u;
       float acc[NB][4];
@@ -408,27 +426,41 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
         mma_first(zp, z0, z1, z0, z1, qs[nb][0], qs[nb][1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)  // scores less m_safe, log2 units
-          s[nb][e] = fmaf(acc[nb][e], c1, fmaf(zp[e], c2, -m_safe[nb][e & 1]));
+          s[kb][nb][e] = fmaf(acc[nb][e], c1, fmaf(zp[e], c2, -m_safe[nb][e & 1]));
       }
     }
-    // keys that a row does not see (and stale ones: whatever stands there)
-    if (key0 + 15 > min_lim || key0 < max_lo) {
+    if (edge) {
+      // keys that a row does not see (and stale ones: whatever stands there)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + (e < 2 ? key_r0 : key_r1);
-          if (key > lim[nb][e & 1] || key < lo[nb][e & 1]) s[nb][e] = -INFINITY;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0[kb] + (e < 2 ? key_r0 : key_r1);
+            if (dead[kb] || key > lim[nb][e & 1] || key < lo[nb][e & 1]) s[kb][nb][e] = -INFINITY;
+          }
+      // keys that no row sees may hold anything: zeros for their values' scales and zeros
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int key = key0[kb] + (lane & 15);
+        if (dead[kb] || key >= range.end || key < range.begin) {
+#pragma unroll
+          for (int k = 0; k < 16 * G * 2 / 32; ++k)
+            sts16(st[kb] + C::kVs + (2 * k + (lane >> 4)) * 32 + (lane & 15) * 2, 0);
         }
+      }
+      __syncwarp();
     }
 
     // ---- softmax against m_used, which moves only when a score passes it by kMargin
-    float top = s[0][0];
+    float top = s[0][0][0];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) top = fmax3(top, s[nb][e], s[nb][e + 1]);
-    }
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) top = fmax3(top, s[kb][nb][e], s[kb][nb][e + 1]);
     // (before a row's first key any score moves it: it stands at -inf)
     if (__any_sync(0xffffffffu, top > (started ? kMargin : -INFINITY))) {
       bool all = true;
@@ -436,14 +468,19 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(s[nb][c], s[nb][2 + c]);
+          float mx = fmaxf(s[0][nb][c], s[0][nb][2 + c]);
+#pragma unroll
+          for (int kb = 1; kb < KB; ++kb) mx = fmax3(mx, s[kb][nb][c], s[kb][nb][2 + c]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
           const float mn = fmaxf(m_used[nb][c], mx + m_safe[nb][c]);
           if (mn > -INFINITY) {
             const float d = m_safe[nb][c] - mn, f = fast_exp2(m_used[nb][c] - mn);
-            s[nb][c] += d;
-            s[nb][2 + c] += d;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+              s[kb][nb][c] += d;
+              s[kb][nb][2 + c] += d;
+            }
             m_used[nb][c] = m_safe[nb][c] = mn;
             l[nb][c] *= f;
             oz[nb][c] *= f;
@@ -460,58 +497,50 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? (NB == 2 ? 2 : 3) : (N
         }
       started = __all_sync(0xffffffffu, all);  // every row of the warp has a maximum
     }
-    uint32_t pb[NB][2];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[e] = fast_exp2(s[nb][e]);
-      }
-      l[nb][0] += p[0] + p[2];
-      l[nb][1] += p[1] + p[3];
-      pb[nb][0] = movmatrix_trans(pack_half2(p[0], p[1]));
-      pb[nb][1] = movmatrix_trans(pack_half2(p[2], p[3]));
-    }
 
-    // ---- output: keys 4t .. 4t + 3
-    // keys that no row sees may hold anything: zeros for their scales and zeros
-    if (key0 + 16 > range.end || key0 < range.begin) {
+    // ---- output: keys 4t .. 4t + 3 of each block
 #pragma unroll
-      for (int k = 0; k < 16 * G * 2 / 32; ++k) {
-        const int key = key0 + (lane & 15);
-        if (key >= range.end || key < range.begin)
-          sts16(st + C::kVs + (2 * k + (lane >> 4)) * 32 + (lane & 15) * 2, 0);
-      }
-      __syncwarp();
-    }
-    {
-      uint2 z = lds64(st + C::kVs + (G + (g < G ? g : 0)) * 32 + t * 8);
-      if (g >= G) z = make_uint2(0u, 0u);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) mma_f16_16816(oz[nb], z.x, 0u, z.y, 0u, pb[nb][0], pb[nb][1]);
-    }
-    constexpr int W = G / 2;  // words of a lane's codes of one key: 16 bits a group
-    uint32_t vw[4][W];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int x = D == 256 ? 2 * t : D == 128 ? (t >> 1) * 2 : 0;
-      const int byte = g * (G * 2);
-      lds_words(st + C::kV + (k * 4 + t) * C::kRow + (((byte >> 4) ^ x) << 4) + (byte & 15), vw[k]);
-    }
-#pragma unroll
-    for (int gr = 0; gr < G; ++gr) {
-      const uint2 sc = lds64(st + C::kVs + gr * 32 + t * 8);
-      const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
-      const uint32_t x01 = __byte_perm(vw[0][gr >> 1], vw[1][gr >> 1], sel);
-      const uint32_t x23 = __byte_perm(vw[2][gr >> 1], vw[3][gr >> 1], sel);
-      const uint32_t lo4 = 0x000f000fu, hi4 = 0x00f000f0u;
-      const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+    for (int kb = 0; kb < KB; ++kb) {
+      uint32_t pb[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const uint32_t p0 = hmul2_u32(pb[nb][0], sc.x), p1 = hmul2_u32(pb[nb][1], sc.y);
-        mma_f16_16816(o[nb][gr][0], x01 & lo4, y01 & lo4, x23 & lo4, y23 & lo4, p0, p1);
-        mma_f16_16816(o[nb][gr][1], x01 & hi4, y01 & hi4, x23 & hi4, y23 & hi4, p0, p1);
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = fast_exp2(s[kb][nb][e]);
+        l[nb][0] += p[0] + p[2];
+        l[nb][1] += p[1] + p[3];
+        pb[nb][0] = movmatrix_trans(pack_half2(p[0], p[1]));
+        pb[nb][1] = movmatrix_trans(pack_half2(p[2], p[3]));
+      }
+      {
+        uint2 z = lds64(st[kb] + C::kVs + (G + (g < G ? g : 0)) * 32 + t * 8);
+        if (g >= G) z = make_uint2(0u, 0u);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          mma_f16_16816(oz[nb], z.x, 0u, z.y, 0u, pb[nb][0], pb[nb][1]);
+      }
+      constexpr int W = G / 2;  // words of a lane's codes of one key: 16 bits a group
+      uint32_t vw[4][W];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = D == 256 ? 2 * t : D == 128 ? (t >> 1) * 2 : 0;
+        const int byte = g * (G * 2);
+        lds_words(st[kb] + C::kV + (k * 4 + t) * C::kRow + (((byte >> 4) ^ x) << 4) + (byte & 15), vw[k]);
+      }
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const uint2 sc = lds64(st[kb] + C::kVs + gr * 32 + t * 8);
+        const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
+        const uint32_t x01 = __byte_perm(vw[0][gr >> 1], vw[1][gr >> 1], sel);
+        const uint32_t x23 = __byte_perm(vw[2][gr >> 1], vw[3][gr >> 1], sel);
+        const uint32_t lo4 = 0x000f000fu, hi4 = 0x00f000f0u;
+        const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const uint32_t p0 = hmul2_u32(pb[nb][0], sc.x), p1 = hmul2_u32(pb[nb][1], sc.y);
+          mma_f16_16816(o[nb][gr][0], x01 & lo4, y01 & lo4, x23 & lo4, y23 & lo4, p0, p1);
+          mma_f16_16816(o[nb][gr][1], x01 & hi4, y01 & hi4, x23 & hi4, y23 & hi4, p0, p1);
+        }
       }
     }
   }
@@ -636,19 +665,22 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4
   const int tok0 = (tok - q0) / a.block_tokens * a.block_tokens;
   const int n = segments(a, key_range(a, seq_len, q_len, tok0).blocks);
   const int64_t prow = at * a.num_splits;
-  float m = -INFINITY, l = 0.0f;
-  if (lane < n) {
-    const float2 ml = a.part_ml[prow + lane];
-    m = ml.x;
-    l = ml.y;
-  }
+  static_assert(kMaxSegments <= 64, "two segments a lane");
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (lane + 32 * k < n) {
+      const float2 ml = a.part_ml[prow + lane + 32 * k];
+      m[k] = ml.x;
+      l[k] = ml.y;
+    }
   const float sink = a.p.sinks ? a.p.sinks[head] * kLog2e : -INFINITY;
-  float top = fmaxf(m, sink);
+  float top = fmax3(m[0], m[1], sink);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   const float mu = top == -INFINITY ? 0.0f : top;
-  const float w = fast_exp2(m - mu);
-  float sum = w * l;
+  const float w[2] = {fast_exp2(m[0] - mu), fast_exp2(m[1] - mu)};
+  float sum = w[0] * l[0] + w[1] * l[1];
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   sum += fast_exp2(sink - mu);
@@ -657,7 +689,7 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
 #pragma unroll 4
   for (int k = 0; k < n; ++k) {
-    const float wk = __shfl_sync(0xffffffffu, w, k);
+    const float wk = __shfl_sync(0xffffffffu, k < 32 ? w[0] : w[1], k & 31);
     const float *src = a.part_acc + (prow + k) * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
@@ -709,17 +741,26 @@ int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len) {
   return max_query_len <= 1 ? 1 : std::max(1, 16 / qpk);
 }
 
+// Key segments.  Blocks that do not fill the GPU's places (three quarters of what is
+// resident) are split until about twice as many stand in line, in segments of at least
+// 512 keys (256 where very few stand): 1 x 131072 keys (8 kv heads, D 128) takes 85 us in
+// 16 segments, 551 in 2.  Blocks that fill it are split at 2048 keys, so that the last of
+// long sequences do not run alone: 64 x up to 8192 keys 97 us in 4 segments, 134 in one; 128
+// x up to 2048 keys 60 us in one, 66 in 4 (the join is another launch and trip to memory).
 int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
                        int32_t max_query_len, int32_t max_seq_len) {
-  (void)hq;
-  (void)d;
-  (void)num_tokens;
-  (void)max_query_len;
-  int32_t ns = (max_seq_len + 1023) / 1024;
-  const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(num_seqs) * hk);
-  const int64_t cap = (8192 + units - 1) / units;
-  if (ns > cap) ns = static_cast<int32_t>(cap);
-  return std::max(1, std::min(ns, kMaxSplits));
+  const int32_t tokens = q4_block_tokens(hq / hk, max_query_len);
+  const int64_t items = max_query_len <= 1 ? std::min(num_seqs, num_tokens)
+                                           : std::min<int64_t>(num_tokens, num_tokens / tokens + num_seqs);
+  const int64_t blocks = std::max<int64_t>(1, items * hk);
+  const int64_t places = int64_t{152} * resident_blocks(d, tokens * (hq / hk) > 8);
+  const int64_t keys = std::max<int64_t>(1, max_seq_len);
+  int64_t ns = (keys + 2047) / 2048;
+  if (4 * blocks < 3 * places)
+    ns = std::min((2 * places + blocks - 1) / blocks, keys / (8 * blocks < places ? 256 : 512));
+  else
+    ns = std::min(ns, (16 * places + blocks - 1) / blocks);
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(ns, kMaxSegments)));
 }
 
 cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {

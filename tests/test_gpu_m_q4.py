@@ -229,7 +229,8 @@ def _run(device, hq, hk, d, bs, lens, q_lens, seed=0, pad=0, table_extra=0, **kw
     if sinks is not None:
         sinks = (torch.randn(hq, generator=g) * 3).to(device)
         sinks[0] = -math.inf
-    ws = torch.full((_lib.workspace_size(t, hq, d, kw.get("num_splits", 0)),), 0xFF,
+    ws = torch.full((_lib.paged_attention_q4_workspace_size(len(lens), t, hq, hk, d, max(q_lens), max(lens) or 1,
+                                                                kw.get("num_splits", 0)),), 0xFF,
                     dtype=torch.uint8, device=device)
     ws[:4] = 0
     _lib.paged_attention_q4(q, *cache, torch.tensor(cu, dtype=torch.int32, device=device),
