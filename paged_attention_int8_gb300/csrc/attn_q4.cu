@@ -653,18 +653,22 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
 template <int D>
 __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4Args a) {
   constexpr int V = D / 32;  // channels a lane
-  wait_for_predecessor();
   const int lane = threadIdx.x & 31;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (at >= static_cast<int64_t>(a.p.num_tokens) * a.p.hq) return;
+  if (at >= static_cast<int64_t>(a.p.num_tokens) * a.p.hq) return wait_for_predecessor();
+  // The row's sequence and its segments, while the kernel before still runs: what this
+  // reads was there before that kernel let this one start.
   const int tok = static_cast<int>(at / a.p.hq);
   const int head = static_cast<int>(at % a.p.hq);
   const int seq = find_seq(a.p.cu, a.p.num_seqs, 1, tok, lane);
   const int q0 = a.p.cu[seq], q_len = a.p.cu[seq + 1] - q0, seq_len = a.p.seq_lens[seq];
-  if (tok < q0 || tok - q0 >= q_len || !valid_sequence(a, q0, q_len, seq_len)) return;
-  const int tok0 = (tok - q0) / a.block_tokens * a.block_tokens;
-  const int n = segments(a, key_range(a, seq_len, q_len, tok0).blocks);
+  const bool owned = tok >= q0 && tok - q0 < q_len && valid_sequence(a, q0, q_len, seq_len);
+  const int tok0 = owned ? (tok - q0) / a.block_tokens * a.block_tokens : 0;
+  const int n = owned ? segments(a, key_range(a, seq_len, q_len, tok0).blocks) : 0;
+  const float sink = a.p.sinks ? a.p.sinks[head] * kLog2e : -INFINITY;
   const int64_t prow = at * a.num_splits;
+  wait_for_predecessor();
+  if (!owned) return;
   static_assert(kMaxSegments <= 64, "two segments a lane");
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -674,7 +678,15 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4
       m[k] = ml.x;
       l[k] = ml.y;
     }
-  const float sink = a.p.sinks ? a.p.sinks[head] * kLog2e : -INFINITY;
+  // the first segments' rows come along with their weights
+  constexpr int kEarly = 8;
+  float2 x[kEarly][V / 2];
+  const float *src = a.part_acc + prow * D + lane * V;
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v)
+      x[k][v] = k < n ? *reinterpret_cast<const float2 *>(src + k * D + 2 * v) : make_float2(0.0f, 0.0f);
   float top = fmax3(m[0], m[1], sink);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -687,15 +699,23 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float wk = __shfl_sync(0xffffffffu, k < 32 ? w[0] : w[1], k & 31);
-    const float *src = a.part_acc + (prow + k) * D + lane * V;
 #pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      const float2 x = *reinterpret_cast<const float2 *>(src + v);
-      acc[v] = fmaf(wk, x.x, acc[v]);
-      acc[v + 1] = fmaf(wk, x.y, acc[v + 1]);
+  for (int k = 0; k < kEarly; ++k) {
+    const float wk = __shfl_sync(0xffffffffu, w[0], k);
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) {
+      acc[2 * v] = fmaf(wk, x[k][v].x, acc[2 * v]);
+      acc[2 * v + 1] = fmaf(wk, x[k][v].y, acc[2 * v + 1]);
+    }
+  }
+#pragma unroll 4
+  for (int k = kEarly; k < n; ++k) {
+    const float wk = __shfl_sync(0xffffffffu, k < 32 ? w[0] : w[1], k & 31);
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) {
+      const float2 y = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(k) * D + 2 * v);
+      acc[2 * v] = fmaf(wk, y.x, acc[2 * v]);
+      acc[2 * v + 1] = fmaf(wk, y.y, acc[2 * v + 1]);
     }
   }
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;

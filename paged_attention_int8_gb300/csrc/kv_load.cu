@@ -7,7 +7,7 @@
 //
 // Bound by HBM: the page bytes read and 4 D bytes written a (key, kv head).  One warp
 // a (page, kv head): a page's arrays are contiguous for a head, and a lane writes
-// 8 channels (16 bytes) of a row, D / 8 neighbouring lanes a row.  Values that lie
+// 8 channels (16 bytes) of a row at a time.  Values that lie
 // channel-major (q8, f8v4) are transposed in registers: a lane takes 4 keys of 8
 // channels, one word a channel (a half word of nibbles), and writes 4 pieces.
 #include "attn_common.cuh"
@@ -21,11 +21,37 @@ namespace paq8 {
 constexpr int kLoadWarps = 4;
 
 __device__ __forceinline__ float half_at(const uint16_t *p) { return __half2float(__ushort_as_half(*p)); }
+__device__ __forceinline__ float half_of(uint32_t w, int i) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(w >> (16 * i))));
+}
+
+// N 32-bit words from memory, in loads as wide as they are aligned.
+template <int N>
+__device__ __forceinline__ void load_words(const void *src, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *static_cast<const uint32_t *>(src);
+  } else if constexpr (N == 2) {
+    const uint2 v = *static_cast<const uint2 *>(src);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) + 4 * i);
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    }
+  }
+}
 
 __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
   return make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]), pack_bf162(x[4], x[5]),
                     pack_bf162(x[6], x[7]));
 }
+
+__device__ __forceinline__ void store_row(uint16_t *dst, uint4 v) { *reinterpret_cast<uint4 *>(dst) = v; }
 
 // Values of byte b of w, signed.
 __device__ __forceinline__ float byte_code(uint32_t w, int b) {
@@ -72,20 +98,60 @@ __global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_c
   uint16_t *kout = p.key + out0 * p.key_stride + h * D;
   uint16_t *vout = p.value + out0 * p.value_stride + h * D;
 
-  // ---- keys: every format is token-major
+  if constexpr (F == CacheFormat::q4) {
+    // a lane takes the codes that stand together: of key row r, words 8 t .. 8 t + 7 of every
+    // group; of value row r, the halves 2 t and 2 t + 1.  Four lanes write whole groups.
 #pragma unroll
-  for (int i0 = 0; i0 < BS * kOctets; i0 += 32) {
-    const int r = (i0 + lane) / kOctets, o = (i0 + lane) % kOctets;
-    if (r >= keys) continue;
-    float x[8];
-    if constexpr (F == CacheFormat::q4) {
-      const uint8_t *codes = static_cast<const uint8_t *>(p.array[0]) + (at * BS + r) * (D / 2);
-      const uint16_t *sc = static_cast<const uint16_t *>(p.array[1]) + at * (2 * BS * G) + r * G + (o >> 2);
-      const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + q4_k_word(o, G));
-      const float s = half_at(sc), z = half_at(sc + BS * G);
+    for (int i0 = 0; i0 < BS * 4; i0 += 32) {
+      const int r = (i0 + lane) >> 2, t = lane & 3;
+      if (r >= keys) continue;
+      const uint8_t *codes = static_cast<const uint8_t *>(p.array[0]) + (at * BS + r) * (D / 2) + t * (4 * G);
+      const uint16_t *sc = static_cast<const uint16_t *>(p.array[1]) + at * (2 * BS * G) + r * G;
+      uint32_t w[G], s[G / 2], z[G / 2];
+      load_words(codes, w);
+      load_words(sc, s);
+      load_words(sc + BS * G, z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 0xfu), s, z);
-    } else {
+      for (int gr = 0; gr < G; ++gr) {
+        const float sf = half_of(s[gr >> 1], gr & 1), zf = half_of(z[gr >> 1], gr & 1);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((w[gr] >> (4 * i)) & 0xfu), sf, zf);
+        store_row(kout + r * p.key_stride + gr * 32 + t * 8, pack_bf16x8(x));
+      }
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < BS * 4; i0 += 32) {
+      const int r = (i0 + lane) >> 2, t = lane & 3;
+      if (r >= keys) continue;
+      const uint8_t *codes = static_cast<const uint8_t *>(p.array[2]) + (at * BS + r) * (D / 2) + t * (4 * G);
+      const uint16_t *sc = static_cast<const uint16_t *>(p.array[3]) + at * (2 * BS * G) + r;
+      uint32_t w[G];
+      load_words(codes, w);
+      float sf[G], zf[G];
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        sf[gr] = half_at(sc + gr * BS);
+        zf[gr] = half_at(sc + (G + gr) * BS);
+      }
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        const uint32_t lo = w[gr >> 1] >> (16 * (gr & 1)), hi = w[(G + gr) >> 1] >> (16 * (gr & 1));
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = fmaf(static_cast<float>(((i < 4 ? lo : hi) >> (4 * (i & 3))) & 0xfu), sf[gr], zf[gr]);
+        store_row(vout + r * p.value_stride + gr * 32 + t * 8, pack_bf16x8(x));
+      }
+    }
+    return;
+  } else {
+    // ---- keys, token-major: 8 channels a lane and step
+#pragma unroll
+    for (int i0 = 0; i0 < BS * kOctets; i0 += 32) {
+      const int r = (i0 + lane) / kOctets, o = (i0 + lane) % kOctets;
+      if (r >= keys) continue;
+      float x[8];
       const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.array[0]) +
                                                        (at * BS + r) * D + o * 8);
       if constexpr (F == CacheFormat::q8) {
@@ -97,33 +163,13 @@ __global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_c
                                e4m3x2_to_half2(w.y), e4m3x2_to_half2(w.y >> 16)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
+          x[2 * i] = half_of(v[i], 0);
+          x[2 * i + 1] = half_of(v[i], 1);
         }
       }
+      store_row(kout + r * p.key_stride + o * 8, pack_bf16x8(x));
     }
-    *reinterpret_cast<uint4 *>(kout + r * p.key_stride + o * 8) = pack_bf16x8(x);
-  }
-
-  // ---- values
-  if constexpr (F == CacheFormat::q4) {
-#pragma unroll
-    for (int i0 = 0; i0 < BS * kOctets; i0 += 32) {
-      const int r = (i0 + lane) / kOctets, o = (i0 + lane) % kOctets;
-      if (r >= keys) continue;
-      const uint8_t *codes = static_cast<const uint8_t *>(p.array[2]) + (at * BS + r) * (D / 2);
-      const uint16_t *sc = static_cast<const uint16_t *>(p.array[3]) + at * (2 * BS * G) + (o >> 2) * BS + r;
-      const uint32_t w0 = *reinterpret_cast<const uint16_t *>(codes + q4_v_half(o, 0, G));
-      const uint32_t w1 = *reinterpret_cast<const uint16_t *>(codes + q4_v_half(o, 1, G));
-      const float s = half_at(sc), z = half_at(sc + BS * G);
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = fmaf(static_cast<float>(((i < 4 ? w0 : w1) >> (4 * (i & 3))) & 0xfu), s, z);
-      *reinterpret_cast<uint4 *>(vout + r * p.value_stride + o * 8) = pack_bf16x8(x);
-    }
-  } else {
+    // ---- values, channel-major: 4 keys of 8 channels a lane and step
 #pragma unroll
     for (int i0 = 0; i0 < BS / 4 * kOctets; i0 += 32) {
       const int r = (i0 + lane) / kOctets * 4, o = (i0 + lane) % kOctets;  // keys r .. r + 3
@@ -133,9 +179,7 @@ __global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_c
         const uint8_t *codes = static_cast<const uint8_t *>(p.array[2]) + (at * D + o * 8) * BS + r;
         const uint2 sw = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.array[3]) +
                                                           (at * G + (o >> 2)) * BS + r);
-        const float2 s01 = __half22float2(*reinterpret_cast<const __half2 *>(&sw.x));
-        const float2 s23 = __half22float2(*reinterpret_cast<const __half2 *>(&sw.y));
-        const float s[4] = {s01.x, s01.y, s23.x, s23.y};
+        const float s[4] = {half_of(sw.x, 0), half_of(sw.x, 1), half_of(sw.y, 0), half_of(sw.y, 1)};
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + c * BS);
@@ -144,14 +188,10 @@ __global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_c
         }
       } else {
         const uint8_t *codes = static_cast<const uint8_t *>(p.array[1]) + ((at * D + o * 8) * BS + r) / 2;
-        const uint16_t *sc = static_cast<const uint16_t *>(p.array[2]) + at * BS + r;
-        const uint16_t *zr = static_cast<const uint16_t *>(p.array[3]) + at * BS + r;
-        float s[4], z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[j] = half_at(sc + j);
-          z[j] = half_at(zr + j);
-        }
+        const uint2 sw = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.array[2]) + at * BS + r);
+        const uint2 zw = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.array[3]) + at * BS + r);
+        const float s[4] = {half_of(sw.x, 0), half_of(sw.x, 1), half_of(sw.y, 0), half_of(sw.y, 1)};
+        const float z[4] = {half_of(zw.x, 0), half_of(zw.x, 1), half_of(zw.y, 0), half_of(zw.y, 1)};
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint32_t w = *reinterpret_cast<const uint16_t *>(codes + c * (BS / 2));
@@ -162,8 +202,7 @@ __global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_c
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (r + j < keys)
-          *reinterpret_cast<uint4 *>(vout + (r + j) * p.value_stride + o * 8) = pack_bf16x8(x[j]);
+        if (r + j < keys) store_row(vout + (r + j) * p.value_stride + o * 8, pack_bf16x8(x[j]));
     }
   }
 }
