@@ -8,8 +8,9 @@
 // thread takes 16 channels (two 16-byte loads), two neighbouring lanes a group (one
 // exchange for its extremes); its codes are two words of a K row or four halves of a V row.
 // Several pieces a thread keep their loads in flight together.
-// Measured on 17,296 tokens (8 kv heads, D 128): with 8 channels a thread 29.5 us; with the
-// scales of 8 to 32 tokens gathered in shared memory and written side by side 36 to 38.
+// Measured on 17,296 tokens (8 kv heads, D 128): 23.8 us; with 8 channels a thread 29.5, with a
+// whole group a thread 26 to 29; with 8 channels and the scales of 8 to 32 tokens gathered in
+// shared memory and written side by side 36 to 38.
 #include "launch.h"
 #include "programmatic.cuh"
 #include "q4.cuh"
