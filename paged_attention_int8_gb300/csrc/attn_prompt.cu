@@ -57,10 +57,11 @@ struct PromptCfg {
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kQOff = kSlots * kSlotBytes;
   static constexpr int kBarOff = kQOff + kTiles * kQBytes;
-  static constexpr int kSmem = kBarOff + 512 + 1024;
+  static constexpr int kItemOff = kBarOff + 384;       // two items, the answer
+  static constexpr int kSmem = kItemOff + 256 + 1024;
   static constexpr int kSoftmaxWarps = 4 * kTiles;
   // two row tiles: warps in whole groups of four, so that registers can move from the
-  // last group (168 a thread at launch, 88 after) to the softmax (208: no spills)
+  // last group (168 a thread at launch, 72 after) to the softmax (216)
   static constexpr int kThreads = kTiles == 2 ? 384 : (kSoftmaxWarps + 2) * 32;
   static constexpr float kMargin = 8.0f;  // log2 of the largest p
   // TMEM columns of S/P and of O, by row tile (D 64, 128) or by S buffer (D 256)
@@ -77,7 +78,11 @@ constexpr int kBarS = 22;      // [2] commit of QK -> softmax
 constexpr int kBarP = 24;      // [2][half] 64 columns of P in TMEM (4 warps) -> MMA
 constexpr int kBarO = 28;      // [2] commit of the last PV -> epilogue (D 256: [1], of every PV -> rescale)
 constexpr int kBarDrain = 30;  // commit of all that was issued, before the end
-constexpr int kNumBars = 31;
+constexpr int kBarQFree = 31;  // [2] commit of a row tile's last QK -> copy
+constexpr int kBarItem = 33;   // [2] an item's bounds stand in shared memory -> MMA, softmax
+constexpr int kBarItemFree = 35;  // [2] they were read (MMA, softmax warps) -> copy
+constexpr int kBarNext = 37;   // the answer to the request for another block's work -> copy
+constexpr int kNumBars = 38;
 
 // kind::f16 with bf16 operands, fp32 accumulator; n_major: B's N dimension contiguous.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool n_major) {
@@ -139,11 +144,42 @@ __device__ __forceinline__ void wait_loaded(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// The tiles of a row tile: keys [begin, end) that some row of it sees, in 128-key tiles
-// counted from the block's first.
-struct TileRange {
-  int tiles, end;
+// What a block works on: two row tiles (D 256: one) of a sequence and kv head.
+struct alignas(64) Item {
+  int nt;              // 128-key tiles from t0 on, of the row tile that sees most; -1: no more items
+  int tiles[2];        // of each row tile
+  int end[2];          // keys before it are seen by some row of the row tile
+  int t0, k0, k_len;
+  int shift;           // last key of query i: shift (causal: + i)
+  int q0, tok0, n_tok;
+  int h;
 };
+static_assert(sizeof(Item) == 64, "two of them, and the answer on a 16-byte boundary");
+
+// Asks for the work of a block of this grid that has not started: its number (or none) is
+// written to 16 bytes of shared memory, completing on bar.
+__device__ __forceinline__ void ask_for_block(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          answer),
+      "r"(bar)
+      : "memory");
+}
+// The answer: false where no block was left.
+__device__ __forceinline__ bool answered_block(uint32_t answer, uint32_t &block) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
+      : "=r"(block), "=r"(got)
+      : "r"(answer)
+      : "memory");
+  return got != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
@@ -159,6 +195,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const uint32_t bars = smem_base + C::kBarOff;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const uint32_t tmem_slot = bars + 8 * kNumBars;
+  volatile Item *items = reinterpret_cast<volatile Item *>(smem + C::kItemOff);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(bar(kBarFull + s), 1);
@@ -170,41 +207,15 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       mbar_init(bar(kBarP + 2 * s), 4);
       mbar_init(bar(kBarP + 2 * s + 1), 4);
       mbar_init(bar(kBarO + s), 1);
+      mbar_init(bar(kBarQFree + s), 1);
+      mbar_init(bar(kBarItem + s), 1);
+      mbar_init(bar(kBarItemFree + s), C::kSoftmaxWarps + 1);
     }
     mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(kBarNext), 1);
     fence_barrier_init();
   }
   wait_for_predecessor();
-
-  // ---- which rows, which keys; the heaviest blocks first (later queries see more keys)
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.p.hk));
-  const int item = a.num_items - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(a.p.hk));
-  const int seq = find_seq(a.p.cu_q, a.p.num_seqs, a.block_tokens, item, lane);
-  const int q0 = a.p.cu_q[seq], q_len = a.p.cu_q[seq + 1] - q0;
-  const int k0 = a.p.cu_k[seq], k_len = a.p.cu_k[seq + 1] - k0;
-  const int tok0 = (item - (a.block_tokens == 1 ? q0 : q0 / a.block_tokens + seq)) * a.block_tokens;
-  if (tok0 < 0 || tok0 >= q_len) return;
-  if (q0 < 0 || q0 > a.p.num_tokens - q_len || k0 < 0 || k_len < 0 || k0 > a.p.num_keys - k_len) {
-    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
-    return;
-  }
-  const int shift = a.p.causal ? k_len - q_len : k_len - 1;  // last key of query i: shift (+ i)
-  auto last_of = [&](int i) { return a.p.causal ? shift + i : shift; };
-  auto first_of = [&](int last) { return a.p.window > 0 ? max(0, last - a.p.window + 1) : 0; };
-  const int n_tok = min(a.block_tokens, q_len - tok0);
-  // keys below k_end are seen by some row of the block; a row with last < 0 sees none
-  const int k_begin = min(first_of(last_of(tok0)), max(0, last_of(tok0 + n_tok - 1)));
-  const int t0 = k_begin / C::kKeys;
-  TileRange range[C::kTiles];
-#pragma unroll
-  for (int i = 0; i < C::kTiles; ++i) {
-    const int n = min(a.tile_tokens, n_tok - i * a.tile_tokens);  // tokens of the row tile
-    range[i].end = n > 0 ? max(0, last_of(tok0 + i * a.tile_tokens + n - 1) + 1) : 0;
-    range[i].tiles = max(0, (range[i].end + C::kKeys - 1) / C::kKeys - t0);
-  }
-  int nt = range[0].tiles;
-  if constexpr (C::kTiles == 2) nt = max(nt, range[1].tiles);
-
   if (warp == kMmaWarp) tc::alloc(tmem_slot, 512);
   tc::fence_before();
   __syncthreads();
@@ -212,72 +223,147 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kBarOff + 8 * kNumBars);
   bool ok = true;
 
-  // Slots in the order of use: K(0), then (D 256: K(1)), then V(j), K(j + 1 or 2), ...
+  // Slots of an item in the order of use: K(0), then (D 256: K(1)), then V(j), K(j + 1 or 2), ...
   constexpr int kAhead = D == 256 ? 2 : 1;
   auto slot_of_k = [&](int j) {  // first of the tile's kParts slots
     return (j < kAhead ? j : kAhead + 2 * (j - kAhead) + 1) * C::kParts;
   };
-  auto slot_of_v = [&](int j) { return (j + kAhead <= nt ? kAhead + 2 * j : nt + j) * C::kParts; };
+  auto slot_of_v = [&](int j, int nt) { return (j + kAhead <= nt ? kAhead + 2 * j : nt + j) * C::kParts; };
 
   if (warp == kCopyWarp) {
     // ============================================================ copies
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (lane == 0 && nt > 0) {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (lane == 0) {
       prefetch_tensormap(&map_q);
       prefetch_tensormap(&map_k);
       prefetch_tensormap(&map_v);
-      int used = 0;  // slots filled so far
-      auto take = [&]() -> int {
-        const int s = used % C::kSlots;
-        if (used >= C::kSlots && !mbar_wait(bar(kBarEmpty + s), ((used / C::kSlots) - 1) & 1)) return -1;
-        ++used;
-        mbar_arrive_expect_tx(bar(kBarFull + s), C::kSlotBytes);
-        return s;
-      };
-      auto load_q = [&](int i) {
-        mbar_arrive_expect_tx(bar(kBarQ + i), a.tile_tokens * a.qpk * D * 2);
+    }
+    const uint32_t answer = smem_base + C::kItemOff + 2 * sizeof(Item);
+    int used = 0;        // slots filled so far
+    int q_used[2] = {0, 0};
+    int count = 0, asked = 0;
+    uint32_t block = blockIdx.x;
+    for (bool more = true; more && ok;) {
+      // ---- which rows, which keys; the heaviest first (later queries see more keys)
+      Item it;
+      it.h = static_cast<int>(block % static_cast<uint32_t>(a.p.hk));
+      const int item = a.num_items - 1 - static_cast<int>(block / static_cast<uint32_t>(a.p.hk));
+      const int seq = find_seq(a.p.cu_q, a.p.num_seqs, a.block_tokens, item, lane);
+      it.q0 = a.p.cu_q[seq];
+      it.k0 = a.p.cu_k[seq];
+      const int q_len = a.p.cu_q[seq + 1] - it.q0;
+      it.k_len = a.p.cu_k[seq + 1] - it.k0;
+      it.tok0 = (item - (a.block_tokens == 1 ? it.q0 : it.q0 / a.block_tokens + seq)) * a.block_tokens;
+      bool valid = it.tok0 >= 0 && it.tok0 < q_len;
+      if (valid && (it.q0 < 0 || it.q0 > a.p.num_tokens - q_len || it.k0 < 0 || it.k_len < 0 ||
+                    it.k0 > a.p.num_keys - it.k_len)) {
+        if (lane == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+        valid = false;
+      }
+      if (valid) {
+        it.shift = a.p.causal ? it.k_len - q_len : it.k_len - 1;
+        it.n_tok = min(a.block_tokens, q_len - it.tok0);
+        const auto last_of = [&](int i) { return a.p.causal ? it.shift + i : it.shift; };
+        const int last0 = last_of(it.tok0);
+        const int first0 = a.p.window > 0 ? max(0, last0 - a.p.window + 1) : 0;
+        // (a row whose last key is negative sees none)
+        it.t0 = min(first0, max(0, last_of(it.tok0 + it.n_tok - 1))) / C::kKeys;
+        it.tiles[1] = it.end[1] = 0;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(smem_base + C::kQOff + i * C::kQBytes + c * (128 * 128), &map_q, c * 64, h * a.qpk,
-                      q0 + tok0 + i * a.tile_tokens, bar(kBarQ + i));
-      };
-      auto load_k = [&](int j) -> bool {
-#pragma unroll
-        for (int c = 0; c < C::kParts; ++c) {
-          const int s = take();
-          if (s < 0) return false;
-          tma_load_4d(smem_base + s * C::kSlotBytes, &map_k, 0, k0 + (t0 + j) * C::kKeys,
-                      c * C::kKChunks, h, bar(kBarFull + s));
+        for (int i = 0; i < C::kTiles; ++i) {
+          const int n = min(a.tile_tokens, it.n_tok - i * a.tile_tokens);  // tokens of the row tile
+          it.end[i] = n > 0 ? max(0, last_of(it.tok0 + i * a.tile_tokens + n - 1) + 1) : 0;
+          it.tiles[i] = max(0, (it.end[i] + C::kKeys - 1) / C::kKeys - it.t0);
         }
-        return true;
-      };
-      auto load_v = [&](int j) -> bool {
+        it.nt = max(it.tiles[0], it.tiles[1]);
+        const int b = count & 1;
+        if (lane == 0) {
+          if (count >= 2) ok = mbar_wait(bar(kBarItemFree + b), ((count >> 1) - 1) & 1);
+          if (ok) {
+            volatile int *dst = reinterpret_cast<volatile int *>(items + b);
+            const int *src = reinterpret_cast<const int *>(&it);
 #pragma unroll
-        for (int c = 0; c < C::kParts; ++c) {
-          const int s = take();
-          if (s < 0) return false;
-          tma_load_4d(smem_base + s * C::kSlotBytes, &map_v, 0,
-                      k0 + (t0 + j) * C::kKeys + c * C::kVKeys, 0, h, bar(kBarFull + s));
+            for (int i = 0; i < static_cast<int>(sizeof(Item) / 4); ++i) dst[i] = src[i];
+            mbar_arrive(bar(kBarItem + b));
+          }
+          auto take = [&]() -> int {
+            const int s = used % C::kSlots;
+            if (used >= C::kSlots && !mbar_wait(bar(kBarEmpty + s), ((used / C::kSlots) - 1) & 1)) return -1;
+            ++used;
+            mbar_arrive_expect_tx(bar(kBarFull + s), C::kSlotBytes);
+            return s;
+          };
+          auto load_q = [&](int i) -> bool {
+            if (it.tiles[i] == 0) return true;
+            if (q_used[i] > 0 && !mbar_wait(bar(kBarQFree + i), (q_used[i] - 1) & 1)) return false;
+            ++q_used[i];
+            mbar_arrive_expect_tx(bar(kBarQ + i), a.tile_tokens * a.qpk * D * 2);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem_base + C::kQOff + i * C::kQBytes + c * (128 * 128), &map_q, c * 64,
+                          it.h * a.qpk, it.q0 + it.tok0 + i * a.tile_tokens, bar(kBarQ + i));
+            return true;
+          };
+          auto load_k = [&](int j) -> bool {
+#pragma unroll
+            for (int c = 0; c < C::kParts; ++c) {
+              const int s = take();
+              if (s < 0) return false;
+              tma_load_4d(smem_base + s * C::kSlotBytes, &map_k, 0, it.k0 + (it.t0 + j) * C::kKeys,
+                          c * C::kKChunks, it.h, bar(kBarFull + s));
+            }
+            return true;
+          };
+          auto load_v = [&](int j) -> bool {
+#pragma unroll
+            for (int c = 0; c < C::kParts; ++c) {
+              const int s = take();
+              if (s < 0) return false;
+              tma_load_4d(smem_base + s * C::kSlotBytes, &map_v, 0,
+                          it.k0 + (it.t0 + j) * C::kKeys + c * C::kVKeys, 0, it.h, bar(kBarFull + s));
+            }
+            return true;
+          };
+          // K(0), K(1) before V(0) at D 256; V(j), K(j + 1 or 2) then
+          if (ok) ok = load_q(0);
+          if (ok && C::kTiles == 2) ok = load_q(1);
+#pragma unroll 1
+          for (int j = -kAhead; ok && j < it.nt; ++j) {
+            if (j >= 0) ok = load_v(j);
+            if (ok && j + kAhead < it.nt) ok = load_k(j + kAhead);
+          }
         }
-        return true;
-      };
-      load_q(0);
-      ok = load_k(0);
-      if (C::kTiles == 2) load_q(1);
-      if (kAhead == 2 && ok && nt > 1) ok = load_k(1);
-      for (int j = 0; ok && j < nt; ++j) {
-        ok = load_v(j);
-        if (ok && j + kAhead < nt) ok = load_k(j + kAhead);
+        ++count;
+      }
+      // ---- the next block's number: asked for when this item's copies are on their way (at its
+      // start a block would hold the next while others are idle)
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(kBarNext), 16);
+        ask_for_block(answer, bar(kBarNext));
+      }
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(kBarNext), asked & 1));
+      ++asked;
+      more = ok && answered_block(answer, block);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    }
+    if (lane == 0) {
+      const int b = count & 1;
+      if (ok && count >= 2) ok = mbar_wait(bar(kBarItemFree + b), ((count >> 1) - 1) & 1);
+      if (ok) {
+        items[b].nt = -1;
+        mbar_arrive(bar(kBarItem + b));
       }
       // no block gives up its shared memory before its own copies have landed
       for (int i = max(0, used - C::kSlots); i < used; ++i)
         mbar_wait(bar(kBarFull + i % C::kSlots), (i / C::kSlots) & 1);
-      for (int i = 0; i < C::kTiles; ++i) mbar_wait(bar(kBarQ + i), 0);
+      for (int i = 0; i < C::kTiles; ++i)
+        if (q_used[i] > 0) mbar_wait(bar(kBarQ + i), (q_used[i] - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
     // ============================================================ MMA issue
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (tc::elect_one() && nt > 0) {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (tc::elect_one()) {
       constexpr uint32_t id_qk = idesc_bf16(128, C::kKeys, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
       const uint64_t q_desc = tc::desc_sw128(smem_base + C::kQOff);
@@ -288,14 +374,21 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       auto wait = [&](int i, uint32_t parity) {
         return mbar_test(bar(i), parity) || (ok = mbar_wait(bar(i), parity));
       };
-      auto wait_slot = [&](int u) { return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1); };
+      int slot0 = 0;               // slots of the items before
+      int nt, t0, k_len;           // of the item
+      int tile_count[2] = {0, 0};  // tiles of the items before, by row tile
+      int q_count[2] = {0, 0};
+      auto wait_slot = [&](int u) {
+        u += slot0;
+        return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1);
+      };
       // S(buffer i) = Q K(j)^T; free: the tile's slots have no later use
       auto issue_qk = [&](int j, int tile, int i, bool free) -> bool {
         const uint32_t s_tmem = tmem + C::s_col(i);
         const uint64_t qd = q_desc + tile * (C::kQBytes >> 4);
 #pragma unroll
         for (int c = 0; c < C::kParts; ++c) {
-          const int u = slot_of_k(j) + c, s = u % C::kSlots;
+          const int u = slot_of_k(j) + c, s = (slot0 + u) % C::kSlots;
           if (C::kTiles == 1) {
             if (!wait_slot(u)) return false;
             tc::fence_after();
@@ -328,7 +421,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C::kParts; ++c) {
           if (C::kParts > 1 && c == C::kParts / 2 && !second_half()) return false;
-          const int u = slot_of_v(j) + c, s = u % C::kSlots;
+          const int u = slot_of_v(j, nt) + c, s = (slot0 + u) % C::kSlots;
           if (C::kTiles == 1) {
             if (!wait_slot(u)) return false;
             tc::fence_after();
@@ -367,36 +460,58 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         if (C::kTiles == 1 || last) tc::commit(bar(kBarO + tile));
         return true;
       };
-      if constexpr (C::kTiles == 2) {
-        const int n0 = range[0].tiles, n1 = range[1].tiles;
-        // What both row tiles need is waited for while the queue is full, so that nothing
-        // stands between a P and its MMAs: V(j) behind QK(j) of the first tile, K(j + 1)
-        // behind PV(j - 1) of the second.  A row tile's S buffer is free once its PV is
-        // issued: MMAs of one thread execute in order.  A slot is freed by the last row
-        // tile that uses it.
-        ok = wait_slot(slot_of_k(0));
 #pragma unroll 1
-        for (int j = 0; ok && j <= nt; ++j) {
+      for (int count = 0;; ++count) {
+        const int b = count & 1;
+        if (!wait(kBarItem + b, (count >> 1) & 1)) break;
+        nt = items[b].nt;
+        t0 = items[b].t0;
+        k_len = items[b].k_len;
+        const int n0 = items[b].tiles[0], n1 = items[b].tiles[1];
+        const int end0 = items[b].end[0], end1 = items[b].end[1];
+        mbar_arrive(bar(kBarItemFree + b));
+        if (nt < 0) break;
+        if (nt == 0) continue;
+        if constexpr (C::kTiles == 2) {
+          // What both row tiles need is waited for while the queue is full, so that nothing
+          // stands between a P and its MMAs: V(j) behind QK(j) of the first tile, K(j + 1)
+          // behind PV(j - 1) of the second.  A row tile's S buffer is free once its PV is
+          // issued: MMAs of one thread execute in order.  A slot is freed by the last row
+          // tile that uses it.
+          wait_slot(slot_of_k(0));
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int n = i ? n1 : n0, other = i ? 0 : n1, end = i ? range[1].end : range[0].end;
-            if (ok && j >= 1 && j - 1 < n)
-              issue_pv(j - 1, i, i, (j - 1) & 1, end, i == 1 || j - 1 >= other, j == n);
-            if (i == 1 && ok && j + 1 < nt) wait_slot(slot_of_k(j + 1));
-            if (ok && j < n && (j > 0 || wait(kBarQ + i, 0))) {
-              tc::fence_after();
-              issue_qk(j, i, i, i == 1 || j >= other);
+          for (int j = 0; ok && j <= nt; ++j) {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              const int n = i ? n1 : n0, other = i ? 0 : n1, end = i ? end1 : end0;
+              const int before = i ? tile_count[1] : tile_count[0];
+              if (ok && j >= 1 && j - 1 < n)
+                issue_pv(j - 1, i, i, (before + j - 1) & 1, end, i == 1 || j - 1 >= other, j == n);
+              if (i == 1 && ok && j + 1 < nt) wait_slot(slot_of_k(j + 1));
+              if (ok && j < n && (j > 0 || wait(kBarQ + i, (i ? q_count[1] : q_count[0]) & 1))) {
+                tc::fence_after();
+                issue_qk(j, i, i, i == 1 || j >= other);
+                if (j == n - 1) tc::commit(bar(kBarQFree + i));
+              }
+              if (i == 0 && ok && j < nt) wait_slot(slot_of_v(j, nt));
             }
-            if (i == 0 && ok && j < nt) wait_slot(slot_of_v(j));
+          }
+          tile_count[1] += n1;
+          q_count[1] += n1 > 0;
+        } else {
+          if (wait(kBarQ, q_count[0] & 1)) tc::fence_after();
+#pragma unroll 1
+          for (int j = 0; ok && j < nt + 2; ++j) {
+            const int g = tile_count[0] + j;  // S buffers alternate from item to item
+            if (j >= 2) issue_pv(j - 2, 0, g & 1, ((g - 2) >> 1) & 1, end0, true, true);
+            if (ok && j < nt) issue_qk(j, 0, g & 1, true);
+            if (ok && j == nt - 1) tc::commit(bar(kBarQFree));
           }
         }
-      } else {
-        ok = wait(kBarQ, 0);
-#pragma unroll 1
-        for (int j = 0; ok && j < nt + 2; ++j) {
-          if (j >= 2) ok = issue_pv(j - 2, 0, j & 1, ((j - 2) >> 1) & 1, range[0].end, true, true);
-          if (ok && j < nt) ok = issue_qk(j, 0, j & 1, true);
-        }
+        tile_count[0] += n0;
+        q_count[0] += n0 > 0;
+        slot0 += 2 * nt * C::kParts;
+        if (!ok) break;
       }
       // no block gives up its shared memory and TMEM before its own MMAs have ended
       tc::commit(bar(kBarDrain));
@@ -405,159 +520,173 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     __syncwarp();
   } else if (warp < C::kSoftmaxWarps) {
     // ============================================================ softmax
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int tile = warp >> 2;
     const int quarter = warp & 3;  // TMEM lanes of this warp
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int tok = tok0 + tile * a.tile_tokens + row / a.qpk;
-    const bool valid = row < a.tile_tokens * a.qpk && tok < tok0 + n_tok;
-    const int head = h * a.qpk + row % a.qpk;
-    // visible keys [lo, limit]; rows that are not written take all, unmasked
-    const int limit = valid ? last_of(tok) : 0x7fffffff;
-    const int lo = valid ? first_of(limit) : 0;
+    const int row_tok = row / a.qpk, row_head = row % a.qpk;
     const float sl2 = a.scale_log2;
-    const int n = range[tile].tiles;
     auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)) != 0; };
-    float m_used = -INFINITY;  // the maximum O is scaled to (log2 units)
-    float l = 0.0f;
+    int before = 0, with_tiles = 0;  // tiles, and items with tiles, of this row tile so far
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const int i = C::kTiles == 2 ? tile : j & 1;  // S buffer
-      const uint32_t use = C::kTiles == 2 ? j : j >> 1;
-      if (!wait(kBarS + i, use & 1)) { ok = false; break; }
-      tc::fence_after();
-      const uint32_t t_s = t_lane + C::s_col(i);
-      const int key0 = (t0 + j) * C::kKeys;
-      // scores that are masked, or whose factor would turn the order around, are scaled first
-      const bool first_scaled = key0 + C::kKeys - 1 > limit || key0 < lo || sl2 <= 0.0f;
-      const float mul = first_scaled ? 1.0f : sl2;
-      uint32_t sr[4][32];
+    for (int count = 0;; ++count) {
+      const int b = count & 1;
+      if (!wait(kBarItem + b, (count >> 1) & 1)) { ok = false; break; }
+      const int nt = items[b].nt, t0 = items[b].t0, n = items[b].tiles[tile], shift = items[b].shift;
+      const int tok = items[b].tok0 + tile * a.tile_tokens + row_tok;
+      const bool valid = row < a.tile_tokens * a.qpk && tok < items[b].tok0 + items[b].n_tok;
+      const int head = items[b].h * a.qpk + row_head;
+      const int64_t at = static_cast<int64_t>(items[b].q0 + tok) * a.p.hq + head;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarItemFree + b));
+      if (nt < 0) break;
+      // visible keys [lo, limit]; rows that are not written take all, unmasked
+      const int limit = !valid ? 0x7fffffff : a.p.causal ? shift + tok : shift;
+      const int lo = valid && a.p.window > 0 ? max(0, limit - a.p.window + 1) : 0;
+      float m_used = -INFINITY;  // the maximum O is scaled to (log2 units)
+      float l = 0.0f;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int g = before + j;
+        const int i = C::kTiles == 2 ? tile : g & 1;  // S buffer
+        const uint32_t use = C::kTiles == 2 ? g : g >> 1;
+        if (!wait(kBarS + i, use & 1)) { ok = false; break; }
+        tc::fence_after();
+        const uint32_t t_s = t_lane + C::s_col(i);
+        const int key0 = (t0 + j) * C::kKeys;
+        // scores that are masked, or whose factor would turn the order around, are scaled first
+        const bool first_scaled = key0 + C::kKeys - 1 > limit || key0 < lo || sl2 <= 0.0f;
+        const float mul = first_scaled ? 1.0f : sl2;
+        uint32_t sr[4][32];
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) tc::ld32(t_s + cb * 32, sr[cb]);
+        for (int cb = 0; cb < 4; ++cb) tc::ld32(t_s + cb * 32, sr[cb]);
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) wait_loaded(sr[cb]);
-      if (first_scaled) {
+        for (int cb = 0; cb < 4; ++cb) wait_loaded(sr[cb]);
+        if (first_scaled) {
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb)
+          for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int key = key0 + cb * 32 + c;
-            sr[cb][c] = __float_as_uint(key > limit || key < lo ? -INFINITY
-                                                                : __uint_as_float(sr[cb][c]) * sl2);
+            for (int c = 0; c < 32; ++c) {
+              const int key = key0 + cb * 32 + c;
+              sr[cb][c] = __float_as_uint(key > limit || key < lo ? -INFINITY
+                                                                  : __uint_as_float(sr[cb][c]) * sl2);
+            }
+        }
+        float mx4[4];
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+          mx4[cb] = fmaxf(__uint_as_float(sr[cb][0]), __uint_as_float(sr[cb][1]));
+#pragma unroll
+          for (int c = 2; c < 32; c += 2)
+            mx4[cb] = fmax3(mx4[cb], __uint_as_float(sr[cb][c]), __uint_as_float(sr[cb][c + 1]));
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
+        // D 256: every PV's phase is waited for, in order, before O is rescaled or behind this
+        // tile's P; D 64, 128: PV(j - 1) was before S(j)
+        bool await_pv = C::kTiles == 1 && j > 0;
+        const bool grow = valid && mx > m_used + C::kMargin;
+        if (__any_sync(0xffffffffu, grow)) {
+          float f = 1.0f;  // factor of what O and l hold
+          if (grow) {
+            f = fast_exp2(m_used - mx);
+            l *= f;
+            m_used = mx;
           }
-      }
-      float mx4[4];
-#pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
-        mx4[cb] = fmaxf(__uint_as_float(sr[cb][0]), __uint_as_float(sr[cb][1]));
-#pragma unroll
-        for (int c = 2; c < 32; c += 2)
-          mx4[cb] = fmax3(mx4[cb], __uint_as_float(sr[cb][c]), __uint_as_float(sr[cb][c + 1]));
-      }
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul;
-      // D 256: every PV's phase is waited for, in order, before O is rescaled or behind this
-      // tile's P; D 64, 128: PV(j - 1) was before S(j)
-      bool await_pv = C::kTiles == 1 && j > 0;
-      const bool grow = valid && mx > m_used + C::kMargin;
-      if (__any_sync(0xffffffffu, grow)) {
-        float f = 1.0f;  // factor of what O and l hold
-        if (grow) {
-          f = fast_exp2(m_used - mx);
-          l *= f;
-          m_used = mx;
-        }
-        if (await_pv) {
-          if (!wait(kBarO, (j - 1) & 1)) { ok = false; break; }
-          tc::fence_after();
-          await_pv = false;
-        }
-        if (j > 0) {
+          if (await_pv) {
+            if (!wait(kBarO, (g - 1) & 1)) { ok = false; break; }
+            tc::fence_after();
+            await_pv = false;
+          }
+          if (j > 0) {
 #pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t orr[32];
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t orr[32];
+              tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
+              wait_loaded(orr);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * f);
+              tc::st32(t_lane + C::o_col(tile) + cb * 32, orr);
+            }
+            tc::wait_st();
+          }
+        }
+        // P against m_used as bf16 pairs, and its sum in fp32, 64 columns at a time
+        const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;  // (no key yet: all masked)
+        const uint64_t mul2 = f32x2_pack(mul, mul), neg_m2 = f32x2_pack(neg_m, neg_m);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const uint32_t(&x)[32] = sr[2 * half + (c >> 5)];
+            float x0, x1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[c & 31]), __uint_as_float(x[(c & 31) + 1])),
+                                   mul2, neg_m2),
+                         x0, x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            sum[(c >> 1) & 1] = f32x2_add(sum[(c >> 1) & 1], f32x2_pack(p0, p1));
+            pw[c >> 1] = pack_bf162(p0, p1);
+          }
+          tc::st32(t_s + half * 32, pw);
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarP + 2 * i + half));
+        }
+        float s0, s1, s2, s3;
+        f32x2_unpack(sum[0], s0, s1);
+        f32x2_unpack(sum[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+        if (await_pv && !wait(kBarO, (g - 1) & 1)) { ok = false; break; }
+      }
+      // ---- epilogue: O / l as bf16, lse; the sink as one term more of the sum
+      if (ok && n > 0) ok = wait(kBarO + tile, C::kTiles == 1 ? (before + n - 1) & 1 : with_tiles & 1);
+      before += n;
+      with_tiles += n > 0;
+      if (!ok) break;
+      {
+        tc::fence_after();
+        float o_mul = 1.0f;
+        if (a.p.sinks && valid) {
+          const float sk = a.p.sinks[head] * kLog2e;
+          const float mn = fmaxf(m_used, sk);
+          if (mn > -INFINITY) {
+            o_mul = fast_exp2(m_used - mn);
+            l = l * o_mul + fast_exp2(sk - mn);
+            m_used = mn;
+          }
+        }
+        const bool seen = valid && limit >= 0 && n > 0;  // else no key: out = 0
+        const float inv = seen ? o_mul / l : 0.0f;
+        uint16_t *dst = a.p.out + at * D;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t orr[32];
+          if (n > 0) {
             tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
             wait_loaded(orr);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * f);
-            tc::st32(t_lane + C::o_col(tile) + cb * 32, orr);
           }
-          tc::wait_st();
-        }
-      }
-      // P against m_used as bf16 pairs, and its sum in fp32, 64 columns at a time
-      const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;  // (no key yet: all masked)
-      const uint64_t mul2 = f32x2_pack(mul, mul), neg_m2 = f32x2_pack(neg_m, neg_m);
-      uint64_t sum[2] = {0, 0};
+          if (valid) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pw[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const uint32_t(&x)[32] = sr[2 * half + (c >> 5)];
-          float x0, x1;
-          f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[c & 31]), __uint_as_float(x[(c & 31) + 1])),
-                                 mul2, neg_m2),
-                       x0, x1);
-          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-          sum[(c >> 1) & 1] = f32x2_add(sum[(c >> 1) & 1], f32x2_pack(p0, p1));
-          pw[c >> 1] = pack_bf162(p0, p1);
-        }
-        tc::st32(t_s + half * 32, pw);
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + 2 * i + half));
-      }
-      float s0, s1, s2, s3;
-      f32x2_unpack(sum[0], s0, s1);
-      f32x2_unpack(sum[1], s2, s3);
-      l += (s0 + s1) + (s2 + s3);
-      if (await_pv && !wait(kBarO, (j - 1) & 1)) { ok = false; break; }
-    }
-    // ---- epilogue: O / l as bf16, lse; the sink as one term more of the sum
-    if (ok && n > 0) ok = wait(kBarO + tile, C::kTiles == 1 ? (n - 1) & 1 : 0);
-    if (ok) {
-      tc::fence_after();
-      float o_mul = 1.0f;
-      if (a.p.sinks && valid) {
-        const float sk = a.p.sinks[head] * kLog2e;
-        const float mn = fmaxf(m_used, sk);
-        if (mn > -INFINITY) {
-          o_mul = fast_exp2(m_used - mn);
-          l = l * o_mul + fast_exp2(sk - mn);
-          m_used = mn;
-        }
-      }
-      const int64_t at = static_cast<int64_t>(q0 + tok) * a.p.hq + head;
-      const bool seen = valid && limit >= 0 && n > 0;  // else no key: out = 0
-      const float inv = seen ? o_mul / l : 0.0f;
-      uint16_t *dst = a.p.out + at * D;
-#pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t orr[32];
-        if (n > 0) {
-          tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
-          wait_loaded(orr);
-        }
-        if (valid) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (seen) {
-              w.x = pack_bf162(__uint_as_float(orr[c]) * inv, __uint_as_float(orr[c + 1]) * inv);
-              w.y = pack_bf162(__uint_as_float(orr[c + 2]) * inv, __uint_as_float(orr[c + 3]) * inv);
-              w.z = pack_bf162(__uint_as_float(orr[c + 4]) * inv, __uint_as_float(orr[c + 5]) * inv);
-              w.w = pack_bf162(__uint_as_float(orr[c + 6]) * inv, __uint_as_float(orr[c + 7]) * inv);
+            for (int c = 0; c < 32; c += 8) {
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              if (seen) {
+                w.x = pack_bf162(__uint_as_float(orr[c]) * inv, __uint_as_float(orr[c + 1]) * inv);
+                w.y = pack_bf162(__uint_as_float(orr[c + 2]) * inv, __uint_as_float(orr[c + 3]) * inv);
+                w.z = pack_bf162(__uint_as_float(orr[c + 4]) * inv, __uint_as_float(orr[c + 5]) * inv);
+                w.w = pack_bf162(__uint_as_float(orr[c + 6]) * inv, __uint_as_float(orr[c + 7]) * inv);
+              }
+              *reinterpret_cast<uint4 *>(dst + cb * 32 + c) = w;
             }
-            *reinterpret_cast<uint4 *>(dst + cb * 32 + c) = w;
           }
         }
+        if (valid && a.p.lse) a.p.lse[at] = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * kLn2;
       }
-      if (valid && a.p.lse) a.p.lse[at] = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * kLn2;
     }
   } else {
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   }
   if (!ok) flag_status(a.status, PA_DEV_TIMEOUT);
 
