@@ -61,7 +61,7 @@ struct PromptCfg {
   static constexpr int kSmem = kItemOff + 256 + 1024;
   static constexpr int kSoftmaxWarps = 4 * kTiles;
   // two row tiles: warps in whole groups of four, so that registers can move from the
-  // last group (168 a thread at launch, 72 after) to the softmax (216)
+  // last group (168 a thread at launch, 88 after) to the softmax (208)
   static constexpr int kThreads = kTiles == 2 ? 384 : (kSoftmaxWarps + 2) * 32;
   static constexpr float kMargin = 8.0f;  // log2 of the largest p
   // TMEM columns of S/P and of O, by row tile (D 64, 128) or by S buffer (D 256)
@@ -223,16 +223,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::kBarOff + 8 * kNumBars);
   bool ok = true;
 
-  // Slots of an item in the order of use: K(0), then (D 256: K(1)), then V(j), K(j + 1 or 2), ...
+  // An item's slots in the order of use: K(0), then (D 256: K(1)), then V(j), K(j + 1 or 2), ...
   constexpr int kAhead = D == 256 ? 2 : 1;
-  auto slot_of_k = [&](int j) {  // first of the tile's kParts slots
-    return (j < kAhead ? j : kAhead + 2 * (j - kAhead) + 1) * C::kParts;
-  };
-  auto slot_of_v = [&](int j, int nt) { return (j + kAhead <= nt ? kAhead + 2 * j : nt + j) * C::kParts; };
 
   if (warp == kCopyWarp) {
     // ============================================================ copies
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (lane == 0) {
       prefetch_tensormap(&map_q);
       prefetch_tensormap(&map_k);
@@ -362,7 +358,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ============================================================ MMA issue
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (tc::elect_one()) {
       constexpr uint32_t id_qk = idesc_bf16(128, C::kKeys, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
@@ -374,43 +370,49 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       auto wait = [&](int i, uint32_t parity) {
         return mbar_test(bar(i), parity) || (ok = mbar_wait(bar(i), parity));
       };
-      int slot0 = 0;               // slots of the items before
       int nt, t0, k_len;           // of the item
       int tile_count[2] = {0, 0};  // tiles of the items before, by row tile
       int q_count[2] = {0, 0};
-      auto wait_slot = [&](int u) {
-        u += slot0;
-        return wait(kBarFull + u % C::kSlots, (u / C::kSlots) & 1);
+      struct Place {  // in the ring
+        int slot;
+        uint32_t parity;
+        __device__ __forceinline__ Place next() const {
+          return slot + 1 == C::kSlots ? Place{0, parity ^ 1u} : Place{slot + 1, parity};
+        }
       };
-      // S(buffer i) = Q K(j)^T; free: the tile's slots have no later use
-      auto issue_qk = [&](int j, int tile, int i, bool free) -> bool {
+      Place place = {0, 0u};  // of the next slot that comes into use
+      auto wait_slot = [&](const Place &at) { return wait(kBarFull + at.slot, at.parity); };
+      // S(buffer i) = Q K(j)^T, K(j) at `at` (D 256: and the three slots after it, waited for
+      // here); free: the tile's slots have no later use
+      auto issue_qk = [&](int tile, int i, Place &at, bool free) -> bool {
         const uint32_t s_tmem = tmem + C::s_col(i);
         const uint64_t qd = q_desc + tile * (C::kQBytes >> 4);
 #pragma unroll
         for (int c = 0; c < C::kParts; ++c) {
-          const int u = slot_of_k(j) + c, s = (slot0 + u) % C::kSlots;
           if (C::kTiles == 1) {
-            if (!wait_slot(u)) return false;
+            if (!wait_slot(at)) return false;
             tc::fence_after();
           }
-          const uint64_t kd = k_desc + s * (C::kSlotBytes >> 4);
+          const uint64_t kd = k_desc + at.slot * (C::kSlotBytes >> 4);
 #pragma unroll
           for (int ks = 0; ks < 4 * C::kKChunks; ++ks) {  // 64 channels: 16 KB of Q and of K
             const int step = c * 4 * C::kKChunks + ks;
             tc::mma_f16(s_tmem, qd + ((step >> 2) * 1024 + 2 * (step & 3)),
                         kd + ((ks >> 2) * 1024 + 2 * (ks & 3)), id_qk, step > 0 ? 1u : 0u);
           }
-          if (free) tc::commit(bar(kBarEmpty + s));
+          if (free) tc::commit(bar(kBarEmpty + at.slot));
+          if (C::kTiles == 1) at = at.next();
         }
         tc::commit(bar(kBarS + i));
         return true;
       };
-      // O(tile) += P(buffer i) V(j), over the 16-key steps below `end`
-      auto issue_pv = [&](int j, int tile, int i, uint32_t p_parity, int end, bool free,
+      // O(tile) += P(buffer i) V(j), over the 16-key steps below `end`, V(j) at `at`
+      auto issue_pv = [&](int j, int tile, int i, uint32_t p_parity, int end, Place &at, bool free,
                           bool last) -> bool {
         const uint32_t p_tmem = tmem + C::s_col(i), o_tmem = tmem + C::o_col(tile);
         const int keys = end - (t0 + j) * C::kKeys;
         const int past = k_len - (t0 + j) * C::kKeys;  // keys from here on are another sequence's
+        uint64_t vd = v_desc + at.slot * (C::kSlotBytes >> 4);
         if (!wait(kBarP + 2 * i, p_parity)) return false;
         tc::fence_after();
         auto second_half = [&]() {
@@ -421,12 +423,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C::kParts; ++c) {
           if (C::kParts > 1 && c == C::kParts / 2 && !second_half()) return false;
-          const int u = slot_of_v(j, nt) + c, s = (slot0 + u) % C::kSlots;
           if (C::kTiles == 1) {
-            if (!wait_slot(u)) return false;
+            if (!wait_slot(at)) return false;
             tc::fence_after();
+            vd = v_desc + at.slot * (C::kSlotBytes >> 4);
           }
-          const uint64_t vd = v_desc + s * (C::kSlotBytes >> 4);
           if (keys >= C::kKeys) {
 #pragma unroll
             for (int ks = 0; ks < C::kVKeys / 16; ++ks) {
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             // rows of the last step that lie past the sequence meet P = 0, but may hold
             // infinities: zeros in their place
             if (past < keys + 15 && past % 16 && past / 16 * 16 / C::kVKeys == c) {
-              const uint32_t v = smem_base + s * C::kSlotBytes;
+              const uint32_t v = smem_base + at.slot * C::kSlotBytes;
               const int r0 = past - c * C::kVKeys, r1 = (past / 16 + 1) * 16 - c * C::kVKeys;
 #pragma unroll 1
               for (int r = r0; r < r1; ++r)
@@ -455,7 +456,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
                 tc::mma_f16_ts(o_tmem, p_tmem + step * 8, vd + ks * 128, id_pv, (j > 0 || step > 0) ? 1u : 0u);
             }
           }
-          if (free) tc::commit(bar(kBarEmpty + s));
+          if (free) tc::commit(bar(kBarEmpty + at.slot));
+          if (C::kTiles == 1) at = at.next();
         }
         if (C::kTiles == 1 || last) tc::commit(bar(kBarO + tile));
         return true;
@@ -478,23 +480,27 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           // behind PV(j - 1) of the second.  A row tile's S buffer is free once its PV is
           // issued: MMAs of one thread execute in order.  A slot is freed by the last row
           // tile that uses it.
-          wait_slot(slot_of_k(0));
+          Place k_at = place, v_at = place;  // of K(j), V(j - 1)
+          wait_slot(k_at);
 #pragma unroll 1
           for (int j = 0; ok && j <= nt; ++j) {
+            const Place v_next = k_at.next(), k_next = v_next.next();
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
               const int n = i ? n1 : n0, other = i ? 0 : n1, end = i ? end1 : end0;
               const int before = i ? tile_count[1] : tile_count[0];
               if (ok && j >= 1 && j - 1 < n)
-                issue_pv(j - 1, i, i, (before + j - 1) & 1, end, i == 1 || j - 1 >= other, j == n);
-              if (i == 1 && ok && j + 1 < nt) wait_slot(slot_of_k(j + 1));
+                issue_pv(j - 1, i, i, (before + j - 1) & 1, end, v_at, i == 1 || j - 1 >= other, j == n);
+              if (i == 1 && ok && j + 1 < nt) wait_slot(k_next);
               if (ok && j < n && (j > 0 || wait(kBarQ + i, (i ? q_count[1] : q_count[0]) & 1))) {
                 tc::fence_after();
-                issue_qk(j, i, i, i == 1 || j >= other);
+                issue_qk(i, i, k_at, i == 1 || j >= other);
                 if (j == n - 1) tc::commit(bar(kBarQFree + i));
               }
-              if (i == 0 && ok && j < nt) wait_slot(slot_of_v(j, nt));
+              if (i == 0 && ok && j < nt) wait_slot(v_next);
             }
+            v_at = v_next;
+            if (j < nt) place = k_at = k_next;  // (two slots a tile)
           }
           tile_count[1] += n1;
           q_count[1] += n1 > 0;
@@ -503,14 +509,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 #pragma unroll 1
           for (int j = 0; ok && j < nt + 2; ++j) {
             const int g = tile_count[0] + j;  // S buffers alternate from item to item
-            if (j >= 2) issue_pv(j - 2, 0, g & 1, ((g - 2) >> 1) & 1, end0, true, true);
-            if (ok && j < nt) issue_qk(j, 0, g & 1, true);
+            if (j >= 2) issue_pv(j - 2, 0, g & 1, ((g - 2) >> 1) & 1, end0, place, true, true);
+            if (ok && j < nt) issue_qk(0, g & 1, place, true);
             if (ok && j == nt - 1) tc::commit(bar(kBarQFree));
           }
         }
         tile_count[0] += n0;
         q_count[0] += n0 > 0;
-        slot0 += 2 * nt * C::kParts;
         if (!ok) break;
       }
       // no block gives up its shared memory and TMEM before its own MMAs have ended
@@ -520,12 +525,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     __syncwarp();
   } else if (warp < C::kSoftmaxWarps) {
     // ============================================================ softmax
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int tile = warp >> 2;
     const int quarter = warp & 3;  // TMEM lanes of this warp
     const int row = quarter * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int row_tok = row / a.qpk, row_head = row % a.qpk;
     const float sl2 = a.scale_log2;
     auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)) != 0; };
     int before = 0, with_tiles = 0;  // tiles, and items with tiles, of this row tile so far
@@ -534,10 +538,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       const int b = count & 1;
       if (!wait(kBarItem + b, (count >> 1) & 1)) { ok = false; break; }
       const int nt = items[b].nt, t0 = items[b].t0, n = items[b].tiles[tile], shift = items[b].shift;
+      const int row_tok = row / a.qpk;
       const int tok = items[b].tok0 + tile * a.tile_tokens + row_tok;
       const bool valid = row < a.tile_tokens * a.qpk && tok < items[b].tok0 + items[b].n_tok;
-      const int head = items[b].h * a.qpk + row_head;
-      const int64_t at = static_cast<int64_t>(items[b].q0 + tok) * a.p.hq + head;
+      const int head = items[b].h * a.qpk + row - row_tok * a.qpk, out_tok = items[b].q0 + tok;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarItemFree + b));
       if (nt < 0) break;
@@ -563,15 +567,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         for (int cb = 0; cb < 4; ++cb) tc::ld32(t_s + cb * 32, sr[cb]);
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) wait_loaded(sr[cb]);
+        const auto scale_first = [&](uint32_t(&x)[32], int first) {  // keys from `first` on
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            x[c] = __float_as_uint(first + c > limit || first + c < lo ? -INFINITY : __uint_as_float(x[c]) * sl2);
+        };
         if (first_scaled) {
 #pragma unroll
-          for (int cb = 0; cb < 4; ++cb)
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int key = key0 + cb * 32 + c;
-              sr[cb][c] = __float_as_uint(key > limit || key < lo ? -INFINITY
-                                                                  : __uint_as_float(sr[cb][c]) * sl2);
-            }
+          for (int cb = 0; cb < 4; ++cb) scale_first(sr[cb], key0 + cb * 32);
         }
         float mx4[4];
 #pragma unroll
@@ -658,6 +661,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             m_used = mn;
           }
         }
+        const int64_t at = static_cast<int64_t>(out_tok) * a.p.hq + head;
         const bool seen = valid && limit >= 0 && n > 0;  // else no key: out = 0
         const float inv = seen ? o_mul / l : 0.0f;
         uint16_t *dst = a.p.out + at * D;
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   }
   if (!ok) flag_status(a.status, PA_DEV_TIMEOUT);
 
