@@ -1075,9 +1075,14 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
                                           int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t head_dim, int32_t max_query_len,
                                           int32_t max_key_len) {
-  (void)num_seqs, (void)num_tokens, (void)num_keys, (void)num_q_heads, (void)num_kv_heads;
-  (void)head_dim, (void)max_query_len, (void)max_key_len;
-  return 256;
+  (void)num_keys, (void)max_query_len;
+  if (num_seqs <= 0 || num_tokens <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads ||
+      num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 128 || !supported_dim(head_dim) ||
+      max_key_len < 0)
+    return 256;
+  const int32_t ns =
+      paq8::prompt_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_key_len);
+  return ns == 1 ? 256 : shared_bytes(num_tokens, num_q_heads, head_dim, ns);
 }
 
 pa_status pa_prompt_attention(const void *q, int64_t q_token_stride, const void *k,

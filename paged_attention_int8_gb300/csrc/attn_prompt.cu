@@ -31,6 +31,7 @@
 #include "launch.h"
 #include "programmatic.cuh"
 #include "prompt.h"
+#include "segments.cuh"
 #include "tcgen05.cuh"
 
 namespace paq8 {
@@ -41,8 +42,10 @@ struct PromptArgs {
   PromptAttention p;
   uint32_t *status;
   int32_t qpk, tile_tokens, block_tokens;  // tokens a row tile, a block
-  int32_t num_items;
+  int32_t num_items, num_splits;
   float scale_log2;
+  float *part_acc;   // [T * Hq][splits][D]
+  float2 *part_ml;   // [T * Hq][splits]
 };
 
 template <int D>
@@ -152,9 +155,43 @@ struct alignas(64) Item {
   int t0, k0, k_len;
   int shift;           // last key of query i: shift (causal: + i)
   int q0, tok0, n_tok;
-  int h;
+  int h, segment;
 };
 static_assert(sizeof(Item) == 64, "two of them, and the answer on a 16-byte boundary");
+
+// The tiles and keys of the row tiles of a block that starts at token tok0 of a sequence:
+// what the kernel and the join agree on.
+struct Rows {
+  int first_tile, tiles[2], end[2], nt;
+};
+template <int TILES>
+__device__ __forceinline__ Rows rows_of(const PromptArgs &a, int q_len, int k_len, int tok0) {
+  Rows r;
+  const int shift = a.p.causal ? k_len - q_len : k_len - 1;
+  const auto last_of = [&](int i) { return a.p.causal ? shift + i : shift; };
+  const int n_tok = min(a.block_tokens, q_len - tok0);
+  const int last0 = last_of(tok0);
+  const int first0 = a.p.window > 0 ? max(0, last0 - a.p.window + 1) : 0;
+  // (a row whose last key is negative sees none)
+  r.first_tile = min(first0, max(0, last_of(tok0 + n_tok - 1))) / 128;
+  r.tiles[1] = r.end[1] = 0;
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) {
+    const int n = min(a.tile_tokens, n_tok - i * a.tile_tokens);  // tokens of the row tile
+    r.end[i] = n > 0 ? max(0, last_of(tok0 + i * a.tile_tokens + n - 1) + 1) : 0;
+    r.tiles[i] = max(0, (r.end[i] + 127) / 128 - r.first_tile);
+  }
+  r.nt = max(r.tiles[0], r.tiles[1]);
+  return r;
+}
+// Tiles a segment of a block of nt tiles, and how many segments that makes.
+__device__ __forceinline__ int segment_tiles(const PromptArgs &a, int nt) {
+  return max(1, (nt + a.num_splits - 1) / a.num_splits);
+}
+__device__ __forceinline__ int segment_count(const PromptArgs &a, int nt) {
+  const int t = segment_tiles(a, nt);
+  return max(1, (nt + t - 1) / t);
+}
 
 // Asks for the work of a block of this grid that has not started: its number (or none) is
 // written to 16 bytes of shared memory, completing on bar.
@@ -243,7 +280,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       // ---- which rows, which keys; the heaviest first (later queries see more keys)
       Item it;
       it.h = static_cast<int>(block % static_cast<uint32_t>(a.p.hk));
-      const int item = a.num_items - 1 - static_cast<int>(block / static_cast<uint32_t>(a.p.hk));
+      const int rest = static_cast<int>(block / static_cast<uint32_t>(a.p.hk));
+      it.segment = rest / a.num_items;
+      const int item = a.num_items - 1 - rest % a.num_items;
       const int seq = find_seq(a.p.cu_q, a.p.num_seqs, a.block_tokens, item, lane);
       it.q0 = a.p.cu_q[seq];
       it.k0 = a.p.cu_k[seq];
@@ -256,20 +295,20 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         if (lane == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
         valid = false;
       }
+      Rows rows;
+      if (valid) {
+        rows = rows_of<C::kTiles>(a, q_len, it.k_len, it.tok0);
+        valid = it.segment < segment_count(a, rows.nt);
+      }
       if (valid) {
         it.shift = a.p.causal ? it.k_len - q_len : it.k_len - 1;
         it.n_tok = min(a.block_tokens, q_len - it.tok0);
-        const auto last_of = [&](int i) { return a.p.causal ? it.shift + i : it.shift; };
-        const int last0 = last_of(it.tok0);
-        const int first0 = a.p.window > 0 ? max(0, last0 - a.p.window + 1) : 0;
-        // (a row whose last key is negative sees none)
-        it.t0 = min(first0, max(0, last_of(it.tok0 + it.n_tok - 1))) / C::kKeys;
-        it.tiles[1] = it.end[1] = 0;
+        const int most = segment_tiles(a, rows.nt), skipped = it.segment * most;
+        it.t0 = rows.first_tile + skipped;
 #pragma unroll
-        for (int i = 0; i < C::kTiles; ++i) {
-          const int n = min(a.tile_tokens, it.n_tok - i * a.tile_tokens);  // tokens of the row tile
-          it.end[i] = n > 0 ? max(0, last_of(it.tok0 + i * a.tile_tokens + n - 1) + 1) : 0;
-          it.tiles[i] = max(0, (it.end[i] + C::kKeys - 1) / C::kKeys - it.t0);
+        for (int i = 0; i < 2; ++i) {
+          it.end[i] = rows.end[i];
+          it.tiles[i] = min(most, max(0, rows.tiles[i] - skipped));
         }
         it.nt = max(it.tiles[0], it.tiles[1]);
         const int b = count & 1;
@@ -542,6 +581,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       const int tok = items[b].tok0 + tile * a.tile_tokens + row_tok;
       const bool valid = row < a.tile_tokens * a.qpk && tok < items[b].tok0 + items[b].n_tok;
       const int head = items[b].h * a.qpk + row - row_tok * a.qpk, out_tok = items[b].q0 + tok;
+      const int segment = items[b].segment;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarItemFree + b));
       if (nt < 0) break;
@@ -651,6 +691,25 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       if (!ok) break;
       {
         tc::fence_after();
+        const int64_t at = static_cast<int64_t>(out_tok) * a.p.hq + head;
+        const bool seen = valid && limit >= 0 && n > 0;  // else no key: out = 0
+        if (a.num_splits > 1) {
+          const int64_t prow = at * a.num_splits + segment;
+          float *dst = a.part_acc + prow * D;
+#pragma unroll 1
+          for (int cb = 0; n > 0 && cb < D / 32; ++cb) {
+            uint32_t orr[32];
+            tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
+            wait_loaded(orr);
+            if (seen) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 4)
+                *reinterpret_cast<uint4 *>(dst + cb * 32 + c) = make_uint4(orr[c], orr[c + 1], orr[c + 2], orr[c + 3]);
+            }
+          }
+          if (valid) a.part_ml[prow] = seen ? make_float2(m_used, l) : make_float2(-INFINITY, 0.0f);
+          continue;
+        }
         float o_mul = 1.0f;
         if (a.p.sinks && valid) {
           const float sk = a.p.sinks[head] * kLog2e;
@@ -661,8 +720,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             m_used = mn;
           }
         }
-        const int64_t at = static_cast<int64_t>(out_tok) * a.p.hq + head;
-        const bool seen = valid && limit >= 0 && n > 0;  // else no key: out = 0
         const float inv = seen ? o_mul / l : 0.0f;
         uint16_t *dst = a.p.out + at * D;
 #pragma unroll 1
@@ -700,6 +757,30 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     tc::fence_after();
     tc::dealloc(tmem, 512);
   }
+}
+
+// Joins the triples of a row (token, q head), one warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  // (the prompt kernel lets nothing start early)
+  wait_for_predecessor();
+  if (at >= static_cast<int64_t>(a.p.num_tokens) * a.p.hq) return;
+  const int tok = static_cast<int>(at / a.p.hq);
+  const int head = static_cast<int>(at % a.p.hq);
+  const int seq = find_seq(a.p.cu_q, a.p.num_seqs, 1, tok, lane);
+  const int q0 = a.p.cu_q[seq], q_len = a.p.cu_q[seq + 1] - q0;
+  const int k0 = a.p.cu_k[seq], k_len = a.p.cu_k[seq + 1] - k0;
+  if (tok < q0 || tok - q0 >= q_len || q0 < 0 || q0 > a.p.num_tokens - q_len || k0 < 0 || k_len < 0 ||
+      k0 > a.p.num_keys - k_len)
+    return;
+  const int tok0 = (tok - q0) / a.block_tokens * a.block_tokens;
+  const int n = segment_count(a, rows_of<PromptCfg<D>::kTiles>(a, q_len, k_len, tok0).nt);
+  const float sink = a.p.sinks ? a.p.sinks[head] * kLog2e : -INFINITY;
+  const int64_t prow = at * a.num_splits;
+  join_row<D>(a.part_acc + prow * D, a.part_ml + prow, n, sink, a.p.out + at * D,
+              a.p.lse ? a.p.lse + at : nullptr, lane);
 }
 
 // Rows x heads x channels of bf16 as a tiled map with 128-byte swizzle.
@@ -743,13 +824,33 @@ cudaError_t launch_d(const PromptAttention &p, cudaStream_t stream) {
     return cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(a.num_items) * p.hk;
+  a.num_splits = prompt_splits(p.num_seqs, p.num_tokens, p.hq, p.hk, p.d, p.max_key_len);
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.hq;
+  while (a.num_splits > 1 &&
+         p.workspace_bytes < 256 + static_cast<size_t>(rows) * a.num_splits * (D + 2) * sizeof(float))
+    --a.num_splits;
+  a.part_acc = reinterpret_cast<float *>(p.workspace + 256);
+  a.part_ml = reinterpret_cast<float2 *>(a.part_acc + rows * a.num_splits * D);
+  const int64_t blocks = static_cast<int64_t>(a.num_items) * p.hk * a.num_splits;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_kernel(prompt_kernel<D>, dim3(static_cast<unsigned>(blocks)), C::kThreads, C::kSmem, stream,
-                       a, mq, mk, mv);
+  const cudaError_t launched = launch_kernel(prompt_kernel<D>, dim3(static_cast<unsigned>(blocks)), C::kThreads,
+                                             C::kSmem, stream, a, mq, mk, mv);
+  if (launched != cudaSuccess || a.num_splits == 1) return launched;
+  return launch_kernel(prompt_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, a);
 }
 
 }  // namespace
+
+// Key segments: blocks that leave a quarter of the SMs idle, and more, are split until about
+// two stand in line for each, in segments of 512 keys at least.
+int32_t prompt_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
+                      int32_t max_key_len) {
+  const int64_t block_tokens = 128 / (hq / hk) * (d == 256 ? 1 : 2);
+  const int64_t blocks = std::max<int64_t>(num_seqs, (num_tokens + block_tokens - 1) / block_tokens) * hk;
+  if (4 * blocks >= 3 * 152) return 1;
+  const int64_t ns = std::min<int64_t>((2 * 152 + blocks - 1) / blocks, max_key_len / 512);
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(ns, kMaxSegments)));
+}
 
 cudaError_t launch_prompt_attention(const PromptAttention &p, cudaStream_t stream) {
   switch (p.d) {

@@ -30,6 +30,7 @@
 #include "programmatic.cuh"
 #include "q4.cuh"
 #include "q4.h"
+#include "segments.cuh"
 
 namespace paq8 {
 
@@ -37,7 +38,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr float kMargin = 2.0f;  // log2 of the largest p
-constexpr int kMaxSegments = 64;
 
 struct Q4Args {
   AttnQ4 p;
@@ -648,11 +648,9 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     }
 }
 
-// Joins a row's triples: M = max m_k, w_k = 2^(m_k - M), out = sum w_k acc_k / sum w_k l_k,
-// the sink as one term more of the sum.  One warp a row (token, q head).
+// Joins the triples of a row (token, q head), one warp a row.
 template <int D>
 __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4Args a) {
-  constexpr int V = D / 32;  // channels a lane
   const int lane = threadIdx.x & 31;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (at >= static_cast<int64_t>(a.p.num_tokens) * a.p.hq) return wait_for_predecessor();
@@ -668,62 +666,9 @@ __global__ void __launch_bounds__(128) q4_join_kernel(const __grid_constant__ Q4
   const float sink = a.p.sinks ? a.p.sinks[head] * kLog2e : -INFINITY;
   const int64_t prow = at * a.num_splits;
   wait_for_predecessor();
-  if (!owned) return;
-  static_assert(kMaxSegments <= 64, "two segments a lane");
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (lane + 32 * k < n) {
-      const float2 ml = a.part_ml[prow + lane + 32 * k];
-      m[k] = ml.x;
-      l[k] = ml.y;
-    }
-  // the first segments' rows come along with their weights
-  constexpr int kEarly = 8;
-  float2 x[kEarly][V / 2];
-  const float *src = a.part_acc + prow * D + lane * V;
-#pragma unroll
-  for (int k = 0; k < kEarly; ++k)
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v)
-      x[k][v] = k < n ? *reinterpret_cast<const float2 *>(src + k * D + 2 * v) : make_float2(0.0f, 0.0f);
-  float top = fmax3(m[0], m[1], sink);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  const float mu = top == -INFINITY ? 0.0f : top;
-  const float w[2] = {fast_exp2(m[0] - mu), fast_exp2(m[1] - mu)};
-  float sum = w[0] * l[0] + w[1] * l[1];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  sum += fast_exp2(sink - mu);
-  float acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kEarly; ++k) {
-    const float wk = __shfl_sync(0xffffffffu, w[0], k);
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) {
-      acc[2 * v] = fmaf(wk, x[k][v].x, acc[2 * v]);
-      acc[2 * v + 1] = fmaf(wk, x[k][v].y, acc[2 * v + 1]);
-    }
-  }
-#pragma unroll 4
-  for (int k = kEarly; k < n; ++k) {
-    const float wk = __shfl_sync(0xffffffffu, k < 32 ? w[0] : w[1], k & 31);
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) {
-      const float2 y = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(k) * D + 2 * v);
-      acc[2 * v] = fmaf(wk, y.x, acc[2 * v]);
-      acc[2 * v + 1] = fmaf(wk, y.y, acc[2 * v + 1]);
-    }
-  }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  uint16_t *dst = a.p.out + at * D + lane * V;
-#pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<uint32_t *>(dst + v) = pack_bf162(acc[v] * inv, acc[v + 1] * inv);
-  if (lane == 0 && a.p.lse) a.p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (owned)
+    join_row<D>(a.part_acc + prow * D, a.part_ml + prow, n, sink, a.p.out + at * D,
+                a.p.lse ? a.p.lse + at : nullptr, lane);
 }
 
 template <int D, int BS, int NB>

@@ -23,6 +23,9 @@ struct PromptAttention {
   size_t workspace_bytes;
 };
 
+// Key segments that a call of these sizes takes.
+int32_t prompt_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
+                      int32_t max_key_len);
 cudaError_t launch_prompt_attention(const PromptAttention &p, cudaStream_t stream);
 
 }  // namespace paq8

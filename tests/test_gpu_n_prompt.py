@@ -112,6 +112,30 @@ def test_non_causal(cuda_device, hq, hk, d, sinks):
     run(cuda_device, hq, hk, d, [130, 3, 40, 1], [300, 0, 17, 1], causal=False, sinks=sinks)
 
 
+@pytest.mark.parametrize("hq,hk,d", HEADS)
+@pytest.mark.parametrize("q_lens,k_lens", [([40], [5000]), ([1], [3001]), ([3, 70, 1], [9000, 2000, 40]),
+                                           ([200], [200])])
+def test_few_rows_over_many_keys(cuda_device, hq, hk, d, q_lens, k_lens):
+    # key segments, joined; rows that some segments hold nothing for (the window, the sinks)
+    for kw in ({}, dict(sinks=True), dict(sliding_window=700), dict(causal=False, sinks=True)):
+        run(cuda_device, hq, hk, d, q_lens, k_lens, seed=d, pad=1, hint=(max(q_lens), 100000), **kw)
+
+
+def test_a_small_workspace_takes_fewer_segments(cuda_device):
+    H.ensure_built()
+    q = torch.randn((20, 8, 128), device=cuda_device).bfloat16()
+    k = torch.randn((8000, 2, 128), device=cuda_device).bfloat16()
+    cu = torch.tensor([0, 20], dtype=torch.int32, device=cuda_device)
+    cuk = torch.tensor([0, 8000], dtype=torch.int32, device=cuda_device)
+    need = _lib.prompt_attention_workspace_size(1, 20, 8000, 8, 2, 128, 20, 8000)
+    assert need > 256 + 20 * 8 * 8 * 130 * 4
+    for size in (need, need // 2, 256 + 20 * 8 * 2 * 130 * 4, 256 + 20 * 8 * 2 * 130 * 4 - 4, 256):
+        ws = torch.zeros(size, dtype=torch.uint8, device=cuda_device)
+        out, lse = _lib.prompt_attention(q, k, k, cu, 20, cu_seqlens_k=cuk, max_key_len=8000, workspace=ws)
+        assert _lib.check_status(ws) == 0
+        check(q, k, k, [20], [8000], out, lse)
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.0, -0.25])
 @pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 2, 128), (6, 2, 256)])
 def test_scales_and_growing_scores(cuda_device, hq, hk, d, scale):
