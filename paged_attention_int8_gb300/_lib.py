@@ -555,6 +555,7 @@ def merge_attn_states(out_a, lse_a, out_b, lse_b, out=None, lse=None, stream=Non
 # device numbers, and enter the tensors' device only when another one is current.
 
 _I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_I64, _U8, _F16 = torch.int64, torch.uint8, torch.float16
 
 
 def _call(fn, dev, stream, *args):
@@ -862,38 +863,63 @@ def paged_attention_shared_prefix_f8v4(q, k_cache, v_cache, v_scale, v_zero, cu_
 
 def _q4_cache(dev, k_cache, k_scale, v_cache, v_scale):
     """Checks a 4-bit cache on device number `dev`; (num_blocks, Hk, bs, D)."""
-    nb, hk, bs, half = k_cache.shape
-    for t in (k_cache, k_scale, v_cache, v_scale):
-        if t.get_device() != dev or not t.is_contiguous():
-            _refuse(dev, (torch.uint8, torch.float16, torch.int16), k_cache=k_cache,
-                    k_scale=k_scale, v_cache=v_cache, v_scale=v_scale)
-    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
+    shape = k_cache.shape
+    nb, hk, bs, half = shape
+    g = half // 16
+    if (k_cache.dtype is _U8 and v_cache.dtype is _U8 and k_scale.dtype is _F16
+            and v_scale.dtype is _F16 and v_cache.shape == shape
+            and k_scale.shape == (nb, hk, 2, bs, g) and v_scale.shape == (nb, hk, 2, g, bs)
+            and k_cache.get_device() == dev and k_scale.get_device() == dev
+            and v_cache.get_device() == dev and v_scale.get_device() == dev
+            and k_cache.is_contiguous() and k_scale.is_contiguous() and v_cache.is_contiguous()
+            and v_scale.is_contiguous()):
+        return nb, hk, bs, 2 * half
+    _refuse(dev, (_U8, _F16, torch.int16), k_cache=k_cache, k_scale=k_scale, v_cache=v_cache,
+            v_scale=v_scale)
+    if k_cache.dtype is not _U8 or v_cache.dtype is not _U8:
         raise TypeError("4-bit caches must be uint8")
     if k_scale.element_size() != 2 or v_scale.element_size() != 2:
         raise TypeError("k_scale and v_scale must hold 16-bit elements (fp16 scales and zeros)")
-    g = half // 16
-    if k_scale.shape != (nb, hk, 2, bs, g) or v_cache.shape != (nb, hk, bs, half) \
+    if k_scale.shape != (nb, hk, 2, bs, g) or v_cache.shape != shape \
             or v_scale.shape != (nb, hk, 2, g, bs):
         raise ValueError(f"cache shapes {tuple(k_scale.shape), tuple(v_cache.shape)}, "
                          f"{tuple(v_scale.shape)} != {(nb, hk, 2, bs, g), (nb, hk, bs, half)}, "
                          f"{(nb, hk, 2, g, bs)} (k_scale, v_cache, v_scale)")
-    return nb, hk, bs, 2 * half
+    return nb, hk, bs, 2 * half  # scales as their bits
 
 
 def _kv_rows(dev, key, value, hk, d):
-    """Checks K/V rows [N, Hk, D] (head and channel dims contiguous); their token
+    """Checks K/V rows [N, Hk, D] (head and channel dims contiguous); N and their token
     strides, those of a single row counting as its width."""
-    n = key.shape[0]
-    for t in (key, value):
-        if t.dtype is not _BF16:
-            raise TypeError("key and value must be bf16")
-        if t.get_device() != dev:
-            raise ValueError(f"all tensors must be CUDA tensors on one device: a row tensor on {t.device}")
-        if t.shape != (n, hk, d):
-            raise ValueError(f"key and value must be [rows, {hk}, {d}], of the same rows")
-        if n and ((d > 1 and t.stride(2) != 1) or (hk > 1 and t.stride(1) != d)):
-            raise ValueError("key/value head and channel dims must be contiguous")
-    return [t.stride(0) if n > 1 else hk * d for t in (key, value)]
+    shape = key.shape
+    n = shape[0]
+    if key.dtype is not _BF16 or value.dtype is not _BF16:
+        raise TypeError("key and value must be bf16")
+    if key.get_device() != dev or value.get_device() != dev:
+        raise ValueError("all tensors must be CUDA tensors on one device: the rows are on "
+                         f"{key.device} and {value.device}")
+    if shape != (n, hk, d) or value.shape != shape:
+        raise ValueError(f"key and value must be [rows, {hk}, {d}], of the same rows")
+    a, b = key.stride(), value.stride()
+    if n and (a[2] != 1 or b[2] != 1 or (hk > 1 and (a[1] != d or b[1] != d))):
+        raise ValueError("key/value head and channel dims must be contiguous")
+    return (n, a[0], b[0]) if n > 1 else (n, hk * d, hk * d)
+
+
+def _int_table(dev, block_table):
+    """Checks an int32 block table on device number `dev`: its rows, columns and row stride."""
+    if block_table.dtype is not _I32 or block_table.get_device() != dev:
+        raise TypeError("block_table must be an int32 CUDA tensor on the other tensors' device")
+    shape = block_table.shape
+    if len(shape) == 2 and shape[0] > 1 and block_table.is_contiguous():
+        return shape[0], shape[1], shape[1]
+    return _table_layout(block_table)
+
+
+def _ints(dev, t, n=None):
+    """Whether t is a contiguous int32 tensor on device number `dev` (of n elements)."""
+    return (t.dtype is _I32 and t.get_device() == dev and t.is_contiguous()
+            and (n is None or t.numel() == n))
 
 
 def kv_store_q4(key, value, slot_mapping, k_cache, k_scale, v_cache, v_scale, status=None,
@@ -907,14 +933,13 @@ def kv_store_q4(key, value, slot_mapping, k_cache, k_scale, v_cache, v_scale, st
     if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
     nb, hk, bs, d = _q4_cache(dev, k_cache, k_scale, v_cache, v_scale)
-    ks, vs = _kv_rows(dev, key, value, hk, d)
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.get_device() != dev \
+    n, ks, vs = _kv_rows(dev, key, value, hk, d)
+    if slot_mapping.dtype is not _I64 or slot_mapping.get_device() != dev \
             or not slot_mapping.is_contiguous():
-        _refuse(dev, (torch.int64,), slot_mapping=slot_mapping)
-    n = key.shape[0]
+        _refuse(dev, (_I64,), slot_mapping=slot_mapping)
     if slot_mapping.shape != (n,):
         raise ValueError("key/value/slot_mapping shapes differ")
-    if status is not None and (status.dtype is not _I32 or status.get_device() != dev):
+    if status is not None and not _ints(dev, status):
         _refuse(dev, (_I32,), status=status)
     _call((_lib or load()).pa_kv_store_q4, dev, stream, key.data_ptr(), ks, value.data_ptr(), vs,
           slot_mapping.data_ptr(), n, hk, d, k_cache.data_ptr(), k_scale.data_ptr(),
@@ -927,21 +952,18 @@ def _kv_load(fn, check, key, value, cu_seqlens_k, block_table, cache, load_lens,
     if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
     nb, hk, bs, d = check(dev, *cache)
-    ks, vs = _kv_rows(dev, key, value, hk, d)
-    for t in (cu_seqlens_k, load_lens, status):
-        if t is not None and (t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous()):
-            _refuse(dev, (_I32,), cu_seqlens_k=cu_seqlens_k, load_lens=load_lens, status=status)
-    s = cu_seqlens_k.numel() - 1
-    if block_table.dtype is not _I32 or block_table.get_device() != dev:
-        raise TypeError("block_table must be an int32 CUDA tensor on the rows' device")
-    rows, columns, table_stride = _table_layout(block_table)
-    if s < 0 or rows != s or (load_lens is not None and load_lens.numel() != s):
+    n, ks, vs = _kv_rows(dev, key, value, hk, d)
+    rows, columns, table_stride = _int_table(dev, block_table)
+    if not _ints(dev, cu_seqlens_k, rows + 1) \
+            or (load_lens is not None and not _ints(dev, load_lens, rows)) \
+            or (status is not None and not _ints(dev, status)):
+        _refuse(dev, (_I32,), cu_seqlens_k=cu_seqlens_k, load_lens=load_lens, status=status)
         raise ValueError("cu_seqlens_k [S + 1], block_table [S, ...] and load_lens [S] are wanted")
     a, b, c, e = cache
     _call(fn, dev, stream, key.data_ptr(), ks, value.data_ptr(), vs, cu_seqlens_k.data_ptr(),
-          None if load_lens is None else load_lens.data_ptr(), s, key.shape[0],
-          block_table.data_ptr(), table_stride, columns, hk, d, a.data_ptr(), b.data_ptr(),
-          c.data_ptr(), e.data_ptr(), nb, bs, None if status is None else status.data_ptr())
+          None if load_lens is None else load_lens.data_ptr(), rows, n, block_table.data_ptr(),
+          table_stride, columns, hk, d, a.data_ptr(), b.data_ptr(), c.data_ptr(), e.data_ptr(), nb,
+          bs, None if status is None else status.data_ptr())
 
 
 def kv_load(key, value, cu_seqlens_k, block_table, k_cache, k_scale, v_cache, v_scale,
@@ -970,45 +992,43 @@ def kv_load_q4(key, value, cu_seqlens_k, block_table, k_cache, k_scale, v_cache,
              (k_cache, k_scale, v_cache, v_scale), load_lens, status, stream)
 
 
-def _results(dev, q, out, lse, return_lse, stream):
+def _results(dev, q, shape, out, lse, return_lse, stream):
     """The out and lse of an attention call over q [T, Hq, D]: checked, or allocated."""
     if out is None:
         with _allocating(stream, dev):
-            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-    else:
-        if out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous():
-            _refuse(dev, (_BF16,), out=out)
-        if out.shape != q.shape:
-            raise ValueError("out must be shaped like q")
+            out = torch.empty(shape, dtype=_BF16, device=q.device)
+    elif out.dtype is not _BF16 or out.shape != shape or out.get_device() != dev \
+            or not out.is_contiguous():
+        _refuse(dev, (_BF16,), out=out)
+        raise ValueError("out must be shaped like q")
     if lse is None:
         if return_lse:
             with _allocating(stream, dev):
-                lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
-    else:
-        if lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
-            _refuse(dev, (_F32,), lse=lse)
-        if lse.shape != q.shape[:2]:
-            raise ValueError("lse must be [T, Hq]")
+                lse = torch.empty(shape[:2], dtype=_F32, device=q.device)
+    elif lse.dtype is not _F32 or lse.shape != shape[:2] or lse.get_device() != dev \
+            or not lse.is_contiguous():
+        _refuse(dev, (_F32,), lse=lse)
+        raise ValueError("lse must be [T, Hq]")
     return out, lse
 
 
 def _workspace(dev, workspace, need, stream):
-    """A call's workspace: checked, or `need()` bytes allocated with its status word zero."""
+    """A call's workspace and its bytes: checked, or `need()` bytes allocated with the status
+    word zero."""
     if workspace is None:
         with _allocating(stream, dev):
             workspace = torch.empty(need(), dtype=torch.uint8, device=torch.device("cuda", dev))
             workspace[:4].zero_()
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
-    return workspace
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _check_sinks(dev, sinks, hq):
-    if sinks is not None:
-        if sinks.dtype is not _F32 or sinks.get_device() != dev or not sinks.is_contiguous():
-            _refuse(dev, (_F32,), sinks=sinks)
-        if sinks.numel() != hq:
-            raise ValueError("sinks must be [num_q_heads]")
+    if sinks.dtype is not _F32 or sinks.get_device() != dev or not sinks.is_contiguous():
+        _refuse(dev, (_F32,), sinks=sinks)
+    if sinks.numel() != hq:
+        raise ValueError("sinks must be [num_q_heads]")
 
 
 def paged_attention_q4_workspace_size(num_seqs: int, num_tokens: int, num_q_heads: int,
@@ -1035,29 +1055,26 @@ def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_
     nb, hk, bs, dc = _q4_cache(dev, k_cache, k_scale, v_cache, v_scale)
     if q.dtype is not _BF16 or not q.is_contiguous():
         raise TypeError("q must be a contiguous bf16 tensor [T, Hq, D]")
-    t, hq, d = q.shape
+    shape = q.shape
+    t, hq, d = shape
     if dc != d:
         raise ValueError("cache shape mismatch")
-    for x in (cu_seqlens_q, seq_lens):
-        if x.dtype is not _I32 or x.get_device() != dev or not x.is_contiguous():
-            _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens)
-    s = seq_lens.numel()
-    if block_table.dtype is not _I32 or block_table.get_device() != dev:
-        raise TypeError("block_table must be an int32 CUDA tensor on q's device")
-    rows, columns, table_stride = _table_layout(block_table)
-    if cu_seqlens_q.numel() != s + 1 or rows != s:
+    s, columns, table_stride = _int_table(dev, block_table)
+    if not _ints(dev, cu_seqlens_q, s + 1) or not _ints(dev, seq_lens, s):
+        _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, seq_lens=seq_lens)
         raise ValueError("metadata shapes disagree with seq_lens")
-    _check_sinks(dev, sinks, hq)
-    out, lse = _results(dev, q, out, lse, return_lse, stream)
-    workspace = _workspace(dev, workspace, lambda: paged_attention_q4_workspace_size(
+    if sinks is not None:
+        _check_sinks(dev, sinks, hq)
+    out, lse = _results(dev, q, shape, out, lse, return_lse, stream)
+    workspace, size = _workspace(dev, workspace, lambda: paged_attention_q4_workspace_size(
         s, t, hq, hk, d, max_query_len, max_seq_len, num_splits), stream)
     _call((_lib or load()).pa_paged_attention_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(),
           k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), cu_seqlens_q.data_ptr(),
           seq_lens.data_ptr(), block_table.data_ptr(), table_stride, columns, s, t, hq, hk, d, nb,
           bs, max_query_len, max_seq_len, d ** -0.5 if softmax_scale is None else softmax_scale,
           num_splits, None if sinks is None else sinks.data_ptr(), sliding_window, out.data_ptr(),
-          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), 0 if causal else ATTN_NON_CAUSAL)
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), size,
+          0 if causal else ATTN_NON_CAUSAL)
     return (out, lse) if return_lse else out
 
 
@@ -1089,36 +1106,37 @@ def prompt_attention(q, k, v, cu_seqlens_q, max_query_len: int, cu_seqlens_k=Non
         raise ValueError("all tensors must be CUDA tensors")
     if q.dtype is not _BF16:
         raise TypeError("q must be bf16")
-    if q.dim() != 3 or k.dim() != 3:
+    shape, k_shape = q.shape, k.shape
+    if len(shape) != 3 or len(k_shape) != 3:
         raise ValueError("q must be [T, Hq, D], k and v [N, Hk, D]")
-    t, hq, d = q.shape
-    n, hk, dk = k.shape
-    if dk != d:
+    t, hq, d = shape
+    hk = k_shape[1]
+    if k_shape[2] != d:
         raise ValueError("q and k must have the same head_dim")
-    ks, vs = _kv_rows(dev, k, v, hk, d)
-    if t and ((d > 1 and q.stride(2) != 1) or (hq > 1 and q.stride(1) != d)):
+    n, ks, vs = _kv_rows(dev, k, v, hk, d)
+    qs = q.stride()
+    if t and (qs[2] != 1 or (hq > 1 and qs[1] != d)):
         raise ValueError("q's head and channel dims must be contiguous")
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
-    for x in (cu_seqlens_q, cu_seqlens_k):
-        if x.dtype is not _I32 or x.get_device() != dev or not x.is_contiguous():
-            _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
     s = cu_seqlens_q.numel() - 1
-    if s < 0 or cu_seqlens_k.numel() != s + 1:
+    if s < 0 or not _ints(dev, cu_seqlens_q) or not _ints(dev, cu_seqlens_k, s + 1):
+        _refuse(dev, (_I32,), cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
         raise ValueError("cu_seqlens_q and cu_seqlens_k must be [S + 1]")
     if max_key_len is None:
         max_key_len = max_query_len
-    _check_sinks(dev, sinks, hq)
-    out, lse = _results(dev, q, out, lse, return_lse, stream)
-    workspace = _workspace(dev, workspace, lambda: prompt_attention_workspace_size(
+    if sinks is not None:
+        _check_sinks(dev, sinks, hq)
+    out, lse = _results(dev, q, shape, out, lse, return_lse, stream)
+    workspace, size = _workspace(dev, workspace, lambda: prompt_attention_workspace_size(
         s, t, n, hq, hk, d, max_query_len, max_key_len), stream)
     _call((_lib or load()).pa_prompt_attention, dev, stream, q.data_ptr(),
-          q.stride(0) if t > 1 else hq * d, k.data_ptr(), ks, v.data_ptr(), vs,
+          qs[0] if t > 1 else hq * d, k.data_ptr(), ks, v.data_ptr(), vs,
           cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), s, t, n, hq, hk, d, max_query_len,
           max_key_len, d ** -0.5 if softmax_scale is None else softmax_scale,
           None if sinks is None else sinks.data_ptr(), sliding_window, out.data_ptr(),
-          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), 0 if causal else ATTN_NON_CAUSAL)
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), size,
+          0 if causal else ATTN_NON_CAUSAL)
     return (out, lse) if return_lse else out
 
 
