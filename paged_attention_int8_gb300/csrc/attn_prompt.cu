@@ -721,7 +721,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           }
         }
         const float inv = seen ? o_mul / l : 0.0f;
-        uint16_t *dst = a.p.out + at * D;
+        // Four neighbouring lanes exchange 16-byte pieces, so that they write 64 bytes of one row
+        // after another (a lane writing its own row kept the memory pipe for 3000 cycles and more,
+        // and the waits behind it).
+        int out_row[4];  // rows of this lane's four, -1: not written
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          out_row[r] = __shfl_sync(0xffffffffu, valid ? static_cast<int>(at) : -1, (lane & ~3) + r);
+        const bool odd = lane & 1, high = lane & 2;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t orr[32];
@@ -729,19 +736,31 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
             wait_loaded(orr);
           }
-          if (valid) {
+          uint32_t piece[4][4];  // [row of the four][word] of piece lane & 3
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
-              if (seen) {
-                w.x = pack_bf162(__uint_as_float(orr[c]) * inv, __uint_as_float(orr[c + 1]) * inv);
-                w.y = pack_bf162(__uint_as_float(orr[c + 2]) * inv, __uint_as_float(orr[c + 3]) * inv);
-                w.z = pack_bf162(__uint_as_float(orr[c + 4]) * inv, __uint_as_float(orr[c + 5]) * inv);
-                w.w = pack_bf162(__uint_as_float(orr[c + 6]) * inv, __uint_as_float(orr[c + 7]) * inv);
-              }
-              *reinterpret_cast<uint4 *>(dst + cb * 32 + c) = w;
-            }
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[4];  // word k of this row's pieces
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x[i] = seen ? pack_bf162(__uint_as_float(orr[8 * i + 2 * k]) * inv,
+                                       __uint_as_float(orr[8 * i + 2 * k + 1]) * inv)
+                          : 0u;
+            const uint32_t a01 = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], 1);
+            const uint32_t a23 = __shfl_xor_sync(0xffffffffu, odd ? x[2] : x[3], 1);
+            const uint32_t e0 = odd ? a01 : x[0], o0 = odd ? x[1] : a01;  // even and odd rows
+            const uint32_t e1 = odd ? a23 : x[2], o1 = odd ? x[3] : a23;
+            const uint32_t be = __shfl_xor_sync(0xffffffffu, high ? e0 : e1, 2);
+            const uint32_t bo = __shfl_xor_sync(0xffffffffu, high ? o0 : o1, 2);
+            piece[0][k] = high ? be : e0;
+            piece[1][k] = high ? bo : o0;
+            piece[2][k] = high ? e1 : be;
+            piece[3][k] = high ? o1 : bo;
           }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (out_row[r] >= 0)
+              *reinterpret_cast<uint4 *>(a.p.out + static_cast<int64_t>(out_row[r]) * D + cb * 32 + (lane & 3) * 8) =
+                  make_uint4(piece[r][0], piece[r][1], piece[r][2], piece[r][3]);
         }
         if (valid && a.p.lse) a.p.lse[at] = l == 0.0f ? -INFINITY : (m_used + log2f(l)) * kLn2;
       }
