@@ -148,10 +148,12 @@ __device__ __forceinline__ uint32_t v_place(int r, int c) {
 }
 
 // Thread blocks an SM, by registers and by the rings.
-constexpr int resident_blocks(int d, bool wide) { return d == 256 ? (wide ? 2 : 3) : wide || d == 128 ? 3 : 5; }
-// Two blocks of keys at a time where their registers fit: the chain from a block's scores to
-// its products is long, and a second one fills its gaps.
-constexpr int keys_blocks(int d, bool wide) { return d <= 128 && !wide ? 2 : 1; }
+constexpr int resident_blocks(int d, bool wide) { return wide ? 2 : d == 64 ? 5 : 3; }
+// Two blocks of keys at a time where that pays: the chain from a block's scores to its products
+// is long, and a second one fills its gaps (D 128, 32 sequences x 6000 keys, 3 x 4 rows: 39 us, 50
+// with one at three thread blocks an SM).  At D 64 the registers of 16 rows are better spent
+// otherwise (64 x 4096 keys, 16 q heads a kv head: 23 us, 27 with two), D 256 has none left.
+constexpr int keys_blocks(int d, bool wide) { return d == 128 || (d == 64 && !wide) ? 2 : 1; }
 
 template <int D, int BS, int NB>
 __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn_q4_kernel(const __grid_constant__ Q4Args a) {
@@ -701,9 +703,15 @@ cudaError_t launch_d(const Q4Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-// Rows a block: 8 where a single token's q heads fit, else 16.
-int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len) {
-  return max_query_len <= 1 ? 1 : std::max(1, 16 / qpk);
+// Rows a block.  16 rows read each key once for twice the rows, 8 leave more blocks an SM: at D
+// 64 and 256 a sequence of few rows is faster in eights (16 sequences x 4096 keys, D 256, 3
+// tokens x 4 heads: 50 us, 58 in sixteens; 8 x 4096, D 64, 8 x 4: 21 and 27), one of many in
+// sixteens (D 256, 40 tokens x 7 heads: 146 and 166).  At D 128 sixteens hold two blocks of keys
+// in work as eights do, and neither wins by more than a tenth.
+int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len, int32_t d) {
+  if (max_query_len <= 1) return 1;
+  const bool eights = d != 128 && int64_t{max_query_len} * qpk <= 64;
+  return std::max(1, (eights ? 8 : 16) / qpk);
 }
 
 // Key segments.  Blocks that do not fill the GPU's places (three quarters of what is
@@ -714,7 +722,7 @@ int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len) {
 // x up to 2048 keys 60 us in one, 66 in 4 (the join is another launch and trip to memory).
 int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
                        int32_t max_query_len, int32_t max_seq_len) {
-  const int32_t tokens = q4_block_tokens(hq / hk, max_query_len);
+  const int32_t tokens = q4_block_tokens(hq / hk, max_query_len, d);
   const int64_t items = max_query_len <= 1 ? std::min(num_seqs, num_tokens)
                                            : std::min<int64_t>(num_tokens, num_tokens / tokens + num_seqs);
   const int64_t blocks = std::max<int64_t>(1, items * hk);
@@ -738,7 +746,7 @@ cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {
                                                           p.num_splits * p.d);
   a.qpk = p.hq / p.hk;
   a.qpk_inverse = 65536 / a.qpk + 1;
-  a.block_tokens = q4_block_tokens(a.qpk, p.max_query_len);
+  a.block_tokens = q4_block_tokens(a.qpk, p.max_query_len, p.d);
   a.num_items = p.max_query_len <= 1 ? p.num_seqs
                 : a.block_tokens == 1 ? p.num_tokens
                                       : p.num_tokens / a.block_tokens + p.num_seqs;

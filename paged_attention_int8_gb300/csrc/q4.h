@@ -57,7 +57,7 @@ struct AttnQ4 {
 };
 
 // Query tokens that a row block takes, and the automatic number of key segments.
-int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len);
+int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len, int32_t d);
 int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
                        int32_t max_query_len, int32_t max_seq_len);
 cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream);
