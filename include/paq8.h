@@ -554,8 +554,9 @@ pa_status pa_paged_attention_shared_prefix_f8v4_view(
 
 /*
  * kv_store in the 4-bit format.  Arguments as pa_kv_store.  Every token writes bytes
- * of its own.  Values beyond +-65504, or whose range is, leave the fp16 of scale and
- * zero (infinities).  num_tokens * num_kv_heads * head_dim below 2^34.  Asynchronous.
+ * of its own: real slots of a call must differ.  Values beyond +-65504, or a range 15 times
+ * that, leave the fp16 of zero or scale (infinities); a group that holds a NaN reads
+ * back as NaN, the groups beside it as they are.  num_tokens * num_kv_heads * head_dim below 2^34.  Asynchronous.
  */
 pa_status pa_kv_store_q4(const void *key, int64_t key_token_stride,
                          const void *value, int64_t value_token_stride,
@@ -643,8 +644,10 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  *   flags          0 or PA_ATTN_NON_CAUSAL.
  * Calls that may overlap on the GPU need workspaces of their own.  Numerics: the codes
  * enter both products exactly; scores are scaled and summed in fp32 (q rounded to
- * fp16; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale are rounded to fp16;
- * sums in fp32, output bf16.
+ * fp16; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale are rounded to fp16
+ * (2^-11 each; p * scale below 6e-8 of the largest p to steps of 6e-11, below 6e-5 to
+ * steps of 6e-8 where scales of 16 and more stand among the keys); sums in fp32,
+ * output bf16.
  */
 pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
                                 const void *v_cache, const void *v_scale,

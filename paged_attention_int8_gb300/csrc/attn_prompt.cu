@@ -822,6 +822,7 @@ cudaError_t launch_d(const PromptAttention &p, cudaStream_t stream) {
   a.tile_tokens = 128 / a.qpk;
   a.block_tokens = a.tile_tokens * C::kTiles;
   a.num_items = a.block_tokens == 1 ? p.num_tokens : p.num_tokens / a.block_tokens + p.num_seqs;
+  if (p.window >= p.num_keys) a.p.window = 0;  // no query leaves a key out
   a.scale_log2 = p.softmax_scale * kLog2e;
   CUtensorMap mq, mk, mv;
   const cuuint64_t qd[3] = {D, static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(p.num_tokens)};

@@ -14,10 +14,13 @@
 //     parts (22 bits; q is a row's, formed once).  No rounding but q to fp16.
 //   Output  O^T[16 ch x 8 rows] += V^T P^T, where the key's scale goes into P: per
 //     group P_g = fp16(p s_g), so that the codes again enter as they are; the zeros'
-//     part is one more MMA (groups in M).  p and p s_g are rounded to fp16 (2^-11);
-//     p is at most 4 and s_g at most 8734, so the product stays inside fp16.
-// The maximum that p is taken against moves only when a score passes it by 2 (p above
-// 4): one vote a block of keys instead of a reduction.
+//     part is one more MMA (groups in M).  p and p s_g are rounded to fp16 (2^-11).
+// The maximum that p is taken against moves only when a score passes it by 2^2: one
+// vote a block of keys instead of a reduction.  p is lifted by 2^10, so that small
+// weights of small scales stay out of fp16's subnormals (p s_g is normal from 6e-8
+// on); with s_g of 16 and more, ranges above 240, the product can leave fp16, whose
+// infinity then stands in the sums: such a warp goes over its keys again without the
+// lift (4 s_g is at most 34936).
 //
 // A thread block takes 8 NB rows (tokens x the q heads of a kv head) and a segment of
 // the keys; its four warps work on their own 16-key blocks, each with its own ring of
@@ -37,7 +40,8 @@ namespace paq8 {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr float kMargin = 2.0f;  // log2 of the largest p
+constexpr float kMargin = 2.0f;  // log2 of the largest p over that of the maximum
+constexpr float kLift = 10.0f;   // log2 of p at the maximum
 
 struct Q4Args {
   AttnQ4 p;
@@ -72,10 +76,11 @@ __device__ __forceinline__ KeyRange key_range(const Q4Args &a, int seq_len, int 
   const int last0 = a.p.causal ? seq_len - q_len + tok0 : seq_len - 1;
   const int last1 = a.p.causal ? last0 + n_tok - 1 : last0;
   KeyRange r;
-  r.end = max(0, last1 + 1);
+  // (keys past the table's columns have no page: left out here, flagged by the kernel)
+  r.end = static_cast<int>(min(static_cast<int64_t>(last1) + 1, int64_t{a.p.table_columns} * a.p.bs));
   r.begin = a.p.window > 0 ? max(0, last0 - a.p.window + 1) : 0;
   r.first = r.begin / 16;
-  r.blocks = r.end > r.begin ? (r.end + 15) / 16 - r.first : 0;
+  r.blocks = r.end > r.begin ? (r.end - 1) / 16 + 1 - r.first : 0;
   return r;
 }
 
@@ -189,6 +194,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     return;
   }
   const KeyRange range = key_range(a, seq_len, q_len, tok0);
+  if (seq_len > int64_t{a.p.table_columns} * BS && sigma == 0 && threadIdx.x == 0)
+    flag_status(a.status, PA_DEV_BAD_BLOCK);
   if (sigma >= segments(a, range.blocks)) return;
   const int n_rows = min(a.block_tokens, q_len - tok0) * a.qpk;
   const int seg0 = range.first + sigma * a.seg_blocks;
@@ -298,8 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     const int b = seg0 + warp + (i + lane) * kWarps;
     entries = -1;
     if (i + lane < n_mine) {
-      const int page = b * 16 / BS;
-      const int e = page < a.p.table_columns ? table[page] : -1;
+      const int e = table[b * 16 / BS];
       if (e >= 0 && e < a.p.num_blocks) entries = e;
       else flag_status(a.status, PA_DEV_BAD_BLOCK);
     }
@@ -326,15 +332,22 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < C::kStages - KB; ++i) issue(i);
-
   float m_used[NB][2], l[NB][2];  // rows 2t, 2t + 1 (log2 units; l: this lane's share)
   float o[NB][G][2][4], oz[NB][4];
+  const float c1 = a.scale_log2 * 0x1p24f;  // of sum_g s_g (q c 2^-24)
+  const float c2 = a.scale_log2 * 32.0f;    // of sum_g z_g (q sum / 32)
+  float m_safe[NB][2];  // m_used, 0 before the first key
+  const int key_r0 = perm16(g), key_r1 = perm16(g + 8);
+  // (m_used: the maximum less the lift, which p, l and o are taken against)
+  float lift = kLift;
+again:
+#pragma unroll
+  for (int i = 0; i < C::kStages - KB; ++i) issue(i);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      m_safe[nb][c] = 0.0f;
       m_used[nb][c] = -INFINITY;
       l[nb][c] = 0.0f;
     }
@@ -345,12 +358,6 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
       for (int gr = 0; gr < G; ++gr) o[nb][gr][0][e] = o[nb][gr][1][e] = 0.0f;
     }
   }
-  const float c1 = a.scale_log2 * 0x1p24f;  // of sum_g s_g (q c 2^-24)
-  const float c2 = a.scale_log2 * 32.0f;    // of sum_g z_g (q sum / 32)
-  float m_safe[NB][2];  // m_used, 0 before the first key
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) m_safe[nb][0] = m_safe[nb][1] = 0.0f;
-  const int key_r0 = perm16(g), key_r1 = perm16(g + 8);
   bool started = false;
 
   for (int i = 0; i < n_mine; i += KB) {
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
 #pragma unroll
         for (int e = 0; e < 4; e += 2) top = fmax3(top, s[kb][nb][e], s[kb][nb][e + 1]);
     // (before a row's first key any score moves it: it stands at -inf)
-    if (__any_sync(0xffffffffu, top > (started ? kMargin : -INFINITY))) {
+    if (__any_sync(0xffffffffu, top > (started ? kMargin + lift : -INFINITY))) {
       bool all = true;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
           for (int kb = 1; kb < KB; ++kb) mx = fmax3(mx, s[kb][nb][c], s[kb][nb][2 + c]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          const float mn = fmaxf(m_used[nb][c], mx + m_safe[nb][c]);
+          const float mn = fmaxf(m_used[nb][c], mx + m_safe[nb][c] - lift);
           if (mn > -INFINITY) {
             const float d = m_safe[nb][c] - mn, f = fast_exp2(m_used[nb][c] - mn);
 #pragma unroll
@@ -547,6 +554,20 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     }
   }
   cp_async_wait<0>();
+  if (lift > 0.0f) {
+    float nan = 0.0f;  // NaN where a sum is infinite, or NaN
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) nan = fmaf(o[nb][gr][0][e], 0.0f, fmaf(o[nb][gr][1][e], 0.0f, nan));
+    if (__any_sync(0xffffffffu, nan != nan)) {
+      lift = 0.0f;
+      __syncwarp();
+      goto again;
+    }
+  }
 
   // ---- O^T of this warp as numbers: channels 32 gr + 4 g + i of rows 2t, 2t + 1
   // (nibble i: o[gr][i & 1][(i & 2) + row]), the zeros' part from the lane of its group
@@ -752,7 +773,7 @@ cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {
                                       : p.num_tokens / a.block_tokens + p.num_seqs;
   a.scale_log2 = p.softmax_scale * kLog2e;
   int blocks = (p.max_seq_len + 15) / 16;
-  if (p.window > 0) blocks = std::min(blocks, (p.window + a.block_tokens + 15) / 16 + 1);
+  if (p.window > 0 && p.window < p.max_seq_len) blocks = std::min(blocks, (p.window + a.block_tokens + 15) / 16 + 1);
   a.seg_blocks = std::max(1, (blocks + p.num_splits - 1) / p.num_splits);
   switch (p.d) {
     case 64: return launch_d<64>(a, stream);

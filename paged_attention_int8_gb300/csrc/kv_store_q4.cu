@@ -61,6 +61,18 @@ __device__ __forceinline__ uint32_t q4_codes(const uint64_t *x, float lo, float 
   return word - (0x4b400000u + 0xb4000000u + 0x40000000u);
 }
 
+// The least of the arguments, NaN where one of them is (fminf passes it over).
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float fmin3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kStoreThreads)
     kv_store_q4_kernel(const __grid_constant__ KvStoreQ4 p, const FastDiv per_token,
@@ -101,12 +113,12 @@ __global__ void __launch_bounds__(kStoreThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = bf16_lo(w[i]), b = bf16_hi(w[i]);
-        lo = fmin3(lo, a, b);
+        lo = fmin3_nan(lo, a, b);  // a NaN becomes its group's zero, and its scale
         hi = fmax3(hi, a, b);
         x[4 * half + i] = f32x2_pack(a, b);
       }
     }
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    lo = fmin_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     if (slot[k] < 0) continue;  // the same for the two lanes of a group
     if (slot[k] >= num_slots) {
