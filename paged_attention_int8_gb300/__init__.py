@@ -9,7 +9,9 @@ causal prefill + decode over that cache and returns bf16 output and fp32 LSE;
 LSEs.  For batches whose requests share prompts, ``build_block_tables`` forms
 a step's tables and slot map on the device, ``copy_blocks`` fills the pages a
 fork made private, and ``paged_attention_shared_prefix`` computes each shared
-prefix once.
+prefix once.  ``kv_store_q4`` and ``paged_attention_q4`` keep and read a cache in 4 bits;
+``prompt_attention`` computes prompts over their own bf16 rows, and ``kv_load`` (one
+a format) reads a cached prefix back as such rows.
 
 Importing the package does not load the CUDA library; the first call does, and
 fails loudly if it has not been built.
