@@ -737,10 +737,12 @@ int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len, int32_t d) {
 
 // Key segments.  Blocks that do not fill the GPU's places (three quarters of what is
 // resident) are split until about twice as many stand in line, in segments of at least
-// 512 keys (256 where very few stand): 1 x 131072 keys (8 kv heads, D 128) takes 85 us in
-// 16 segments, 551 in 2.  Blocks that fill it are split at 2048 keys, so that the last of
-// long sequences do not run alone: 64 x up to 8192 keys 97 us in 4 segments, 134 in one; 128
-// x up to 2048 keys 60 us in one, 66 in 4 (the join is another launch and trip to memory).
+// 512 keys (256 where very few stand); where that limit leaves fewer than two rounds, one
+// full round: 1 x 131072 keys (8 kv heads, D 128, caches cold) takes 379 us in 2 segments, 60 in
+// 16, 54 in 57 (456 blocks on 456 places), 65 in 64.  Blocks that fill it are split at 2048 keys,
+// so that the last of long sequences do not run alone: 64 x up to 8192 keys 93 us in 4 segments,
+// 108 in one; 128 x up to 2048 keys 56 us in one, 64 in 4 (the join is another launch and trip
+// to memory).
 int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
                        int32_t max_query_len, int32_t max_seq_len) {
   const int32_t tokens = q4_block_tokens(hq / hk, max_query_len, d);
@@ -750,10 +752,13 @@ int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t
   const int64_t places = int64_t{152} * resident_blocks(d, tokens * (hq / hk) > 8);
   const int64_t keys = std::max<int64_t>(1, max_seq_len);
   int64_t ns = (keys + 2047) / 2048;
-  if (4 * blocks < 3 * places)
-    ns = std::min((2 * places + blocks - 1) / blocks, keys / (8 * blocks < places ? 256 : 512));
-  else
+  if (4 * blocks < 3 * places) {
+    const int64_t two = (2 * places + blocks - 1) / blocks;
+    ns = std::min<int64_t>({two, keys / (8 * blocks < places ? 256 : 512), kMaxSegments});
+    if (ns < two && ns * blocks > places) ns = places / blocks;
+  } else {
     ns = std::min(ns, (16 * places + blocks - 1) / blocks);
+  }
   return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(ns, kMaxSegments)));
 }
 
