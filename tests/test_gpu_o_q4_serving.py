@@ -507,3 +507,26 @@ def test_prompts_of_which_some_are_empty(cuda_device, hq, hk, d):
             _compare(out[span], lse[span], q[span], (kk, 0 * kk, vv, 0 * vv), b - (a - none), p_bits=8)
         at, ak = at + a, ak + b
     assert (out[at:] == 7).all() and (lse[at:] == 7).all()
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 2, 128), (6, 2, 256)])
+@pytest.mark.parametrize("count", [2, 31, 32, 33, 70])
+def test_many_prompts_of_uneven_lengths(cuda_device, hq, hk, d, count):
+    H.ensure_built()
+    dev = cuda_device
+    g = torch.Generator().manual_seed(count + d)
+    q_lens = torch.randint(0, 90, (count,), generator=g).tolist()
+    k_lens = [a + int(b) for a, b in zip(q_lens, torch.randint(0, 300, (count,), generator=g))]
+    t, n = sum(q_lens), sum(k_lens)
+    q = torch.randn((t, hq, d), generator=g).bfloat16().to(dev)
+    k, v = (torch.randn((n, hk, d), generator=g).bfloat16().to(dev) for _ in range(2))
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+    out, lse = _lib.prompt_attention(q, k, v, _starts(q_lens, dev), 90, cu_seqlens_k=_starts(k_lens, dev),
+                                     max_key_len=390, workspace=ws)
+    assert _lib.check_status(ws) == 0
+    at = ak = 0
+    for a, b in zip(q_lens, k_lens):
+        kk, vv = k[ak:ak + b].double(), v[ak:ak + b].double()
+        if a:
+            _compare(out[at:at + a], lse[at:at + a], q[at:at + a], (kk, 0 * kk, vv, 0 * vv), b - a, p_bits=8)
+        at, ak = at + a, ak + b
