@@ -27,6 +27,7 @@
 // asynchronous copies, and join their sums at the end.  Segments leave fp32 triples
 // that q4_join_kernel merges.
 #include <algorithm>
+#include <utility>
 
 #include "attn_common.cuh"
 #include "launch.h"
@@ -48,8 +49,9 @@ struct Q4Args {
   uint32_t *status;
   float *part_acc;   // [T * Hq][splits][D]
   float2 *part_ml;   // [T * Hq][splits]
-  int32_t qpk, qpk_inverse, block_tokens, num_items, seg_blocks, num_splits;
+  int32_t qpk, qpk_inverse, block_tokens, num_items, num_splits;
   float scale_log2;
+  int32_t seg_start[kMaxSegments];  // 16-key blocks of a range before each segment
 };
 
 // Ring depth by the bytes of a 16-key block (20 D): what keeps about 100 KB an SM in flight.
@@ -85,7 +87,9 @@ __device__ __forceinline__ KeyRange key_range(const Q4Args &a, int seq_len, int 
 }
 
 __device__ __forceinline__ int segments(const Q4Args &a, int blocks) {
-  return min(a.num_splits, max(1, (blocks + a.seg_blocks - 1) / a.seg_blocks));
+  int n = 1;
+  while (n < a.num_splits && a.seg_start[n] < blocks) ++n;
+  return n;
 }
 
 // The bounds of a sequence's metadata that the kernels rely on.
@@ -196,11 +200,11 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
   const KeyRange range = key_range(a, seq_len, q_len, tok0);
   if (seq_len > int64_t{a.p.table_columns} * BS && sigma == 0 && threadIdx.x == 0)
     flag_status(a.status, PA_DEV_BAD_BLOCK);
-  if (sigma >= segments(a, range.blocks)) return;
+  if (sigma > 0 && a.seg_start[sigma] >= range.blocks) return;  // (as segments() counts)
   const int n_rows = min(a.block_tokens, q_len - tok0) * a.qpk;
-  const int seg0 = range.first + sigma * a.seg_blocks;
+  const int seg0 = range.first + a.seg_start[sigma];
   const int seg1 = sigma == a.num_splits - 1 ? range.first + range.blocks
-                                             : min(range.first + range.blocks, seg0 + a.seg_blocks);
+                                             : min(range.first + range.blocks, range.first + a.seg_start[sigma + 1]);
 
   // ---- q as the B operand: lane (g, t) holds row 8 nb + g
   //   group gr, step e: channels 32 gr + 8 t + 2 e' of the nibbles that step e's words
@@ -735,27 +739,38 @@ int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len, int32_t d) {
   return std::max(1, (eights ? 8 : 16) / qpk);
 }
 
-// Key segments.  Blocks that do not fill the GPU's places (three quarters of what is
-// resident) are split until about twice as many stand in line, in segments of at least
-// 512 keys (256 where very few stand); where that limit leaves fewer than two rounds, one
-// full round: 1 x 131072 keys (8 kv heads, D 128, caches cold) takes 379 us in 2 segments, 60 in
-// 16, 54 in 57 (456 blocks on 456 places), 65 in 64.  Blocks that fill it are split at 2048 keys,
-// so that the last of long sequences do not run alone: 64 x up to 8192 keys 93 us in 4 segments,
-// 108 in one; 128 x up to 2048 keys 56 us in one, 64 in 4 (the join is another launch and trip
-// to memory).
-int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
-                       int32_t max_query_len, int32_t max_seq_len) {
+namespace {
+// Blocks of rows of a call (at most), and how many stand on the GPU at once.
+std::pair<int64_t, int64_t> blocks_and_places(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk,
+                                              int32_t d, int32_t max_query_len) {
   const int32_t tokens = q4_block_tokens(hq / hk, max_query_len, d);
   const int64_t items = max_query_len <= 1 ? std::min(num_seqs, num_tokens)
                                            : std::min<int64_t>(num_tokens, num_tokens / tokens + num_seqs);
-  const int64_t blocks = std::max<int64_t>(1, items * hk);
-  const int64_t places = int64_t{152} * resident_blocks(d, tokens * (hq / hk) > 8);
+  return {std::max<int64_t>(1, items * hk), int64_t{152} * resident_blocks(d, tokens * (hq / hk) > 8)};
+}
+}  // namespace
+
+// Key segments.  Blocks that do not fill the GPU's places (three quarters of what is
+// resident) are split until about three times as many stand in line, in segments of at least
+// 512 keys (256 where very few stand); where that limit leaves fewer than three rounds, one
+// full round: 1 x 131072 keys (8 kv heads, D 128, caches cold) takes 379 us in 2 segments, 60 in
+// 16, 54 in 57 (456 blocks on 456 places), 65 in 64.  Blocks that fill it are split at 2048 keys,
+// so that the last of long sequences do not run alone: 64 x up to 8192 keys 87 us in 4 segments,
+// 105 in one; 128 x up to 2048 keys 56 us in one, 62 in 4 (the join is another launch and trip
+// to memory).
+// Where segments stand in line, those that start first are the longest (n - i parts of n (n + 1) /
+// 2 each), so that the last ones to run are short: 64 x up to 8192 keys 93 us in equal
+// segments, 87 so; 48 x 5 tokens x 8 heads on up to 6001 keys 127 and 117; 16 x up to 32768 keys 105
+// and 97; 6 x up to 131072 keys at D 256, five drawings of lengths, 1268 and 1133 together.
+int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk, int32_t d,
+                       int32_t max_query_len, int32_t max_seq_len) {
+  const auto [blocks, places] = blocks_and_places(num_seqs, num_tokens, hq, hk, d, max_query_len);
   const int64_t keys = std::max<int64_t>(1, max_seq_len);
   int64_t ns = (keys + 2047) / 2048;
   if (4 * blocks < 3 * places) {
-    const int64_t two = (2 * places + blocks - 1) / blocks;
-    ns = std::min<int64_t>({two, keys / (8 * blocks < places ? 256 : 512), kMaxSegments});
-    if (ns < two && ns * blocks > places) ns = places / blocks;
+    const int64_t three = (3 * places + blocks - 1) / blocks;
+    ns = std::min<int64_t>({three, keys / (8 * blocks < places ? 256 : 512), kMaxSegments});
+    if (ns < three && ns * blocks > places) ns = places / blocks;
   } else {
     ns = std::min(ns, (16 * places + blocks - 1) / blocks);
   }
@@ -779,7 +794,12 @@ cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {
   a.scale_log2 = p.softmax_scale * kLog2e;
   int blocks = (p.max_seq_len + 15) / 16;
   if (p.window > 0 && p.window < p.max_seq_len) blocks = std::min(blocks, (p.window + a.block_tokens + 15) / 16 + 1);
-  a.seg_blocks = std::max(1, (blocks + p.num_splits - 1) / p.num_splits);
+  const auto [row_blocks, places] = blocks_and_places(p.num_seqs, p.num_tokens, p.hq, p.hk, p.d, p.max_query_len);
+  const bool falling = p.num_splits * row_blocks > places;
+  const int64_t n = p.num_splits;
+  for (int64_t i = 0; i < n; ++i)
+    a.seg_start[i] = static_cast<int32_t>(
+        falling ? blocks * i * (2 * n + 1 - i) / (n * (n + 1)) : i * std::max<int64_t>(1, (blocks + n - 1) / n));
   switch (p.d) {
     case 64: return launch_d<64>(a, stream);
     case 128: return launch_d<128>(a, stream);

@@ -530,3 +530,21 @@ def test_many_prompts_of_uneven_lengths(cuda_device, hq, hk, d, count):
         if a:
             _compare(out[at:at + a], lse[at:at + a], q[at:at + a], (kk, 0 * kk, vv, 0 * vv), b - a, p_bits=8)
         at, ak = at + a, ak + b
+
+
+@pytest.mark.parametrize("count,most,splits", [(3, 9, 64), (200, 40, 7), (40, 700, 3), (6, 5000, 0), (300, 100, 2)])
+@pytest.mark.parametrize("d,bs,q_len", [(64, 16, 1), (128, 32, 1), (128, 16, 3), (256, 16, 1)])
+def test_segments_of_all_sizes(cuda_device, count, most, splits, d, bs, q_len):
+    """More segments than keys, more blocks than places, segments that hold nothing."""
+    H.ensure_built()
+    dev, hq, hk = cuda_device, 8, 2
+    lens = torch.randint(q_len, most, (count,), generator=torch.Generator().manual_seed(count)).tolist()
+    _, cache, cpu, table, _, sl = _decode_inputs(dev, lens, hq, hk, d, bs, count)
+    g = torch.Generator().manual_seed(d)
+    q = torch.randn((count * q_len, hq, d), generator=g).bfloat16().to(dev)
+    out, lse = _lib.paged_attention_q4(q, *cache, _starts([q_len] * count, dev), sl, table.to(dev), q_len, most,
+                                       num_splits=splits)
+    for s in sorted({0, 1, 2, count // 2, count - 1}):
+        span = slice(s * q_len, (s + 1) * q_len)
+        _compare(out[span], lse[span], q[span], [x.to(dev) for x in _q4.rows64(cpu, table[s], lens[s])],
+                 lens[s] - q_len)
