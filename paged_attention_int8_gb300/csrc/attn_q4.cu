@@ -740,19 +740,20 @@ int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len, int32_t d) {
 }
 
 namespace {
-// Blocks of rows of a call (at most), and how many stand on the GPU at once.
+// Blocks of rows of a call (at most, by the hint of its longest query), and how many stand on
+// the GPU at once.
 std::pair<int64_t, int64_t> blocks_and_places(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t hk,
                                               int32_t d, int32_t max_query_len) {
   const int32_t tokens = q4_block_tokens(hq / hk, max_query_len, d);
-  const int64_t items = max_query_len <= 1 ? std::min(num_seqs, num_tokens)
-                                           : std::min<int64_t>(num_tokens, num_tokens / tokens + num_seqs);
+  const int64_t items = std::min<int64_t>({num_tokens, num_tokens / tokens + num_seqs,
+                                           (int64_t{max_query_len} + tokens - 1) / tokens * num_seqs});
   return {std::max<int64_t>(1, items * hk), int64_t{152} * resident_blocks(d, tokens * (hq / hk) > 8)};
 }
 }  // namespace
 
 // Key segments.  Blocks that do not fill the GPU's places (three quarters of what is
 // resident) are split until about three times as many stand in line, in segments of at least
-// 512 keys (256 where very few stand); where that limit leaves fewer than three rounds, one
+// 512 keys (256 where very few stand); where that limit leaves fewer than 2.5 rounds, one
 // full round: 1 x 131072 keys (8 kv heads, D 128, caches cold) takes 379 us in 2 segments, 60 in
 // 16, 54 in 57 (456 blocks on 456 places), 65 in 64.  Blocks that fill it are split at 2048 keys,
 // so that the last of long sequences do not run alone: 64 x up to 8192 keys 87 us in 4 segments,
@@ -768,9 +769,8 @@ int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t
   const int64_t keys = std::max<int64_t>(1, max_seq_len);
   int64_t ns = (keys + 2047) / 2048;
   if (4 * blocks < 3 * places) {
-    const int64_t three = (3 * places + blocks - 1) / blocks;
-    ns = std::min<int64_t>({three, keys / (8 * blocks < places ? 256 : 512), kMaxSegments});
-    if (ns < three && ns * blocks > places) ns = places / blocks;
+    ns = std::min<int64_t>({(3 * places + blocks - 1) / blocks, keys / (8 * blocks < places ? 256 : 512), kMaxSegments});
+    if (ns * blocks > places && 2 * ns * blocks < 5 * places) ns = places / blocks;
   } else {
     ns = std::min(ns, (16 * places + blocks - 1) / blocks);
   }
