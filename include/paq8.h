@@ -638,9 +638,9 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  *                  256 bytes and one.
  *   max_query_len  1: a sequence with more query tokens is left unprocessed and
  *                  flagged PA_DEV_BAD_SEQ.  The time of a long query grows with its
- *                  blocks of 16 rows (tokens x q heads of a kv head), each of which
- *                  reads its keys: pa_kv_load_q4 and pa_prompt_attention are the
- *                  faster way for chunks of hundreds of tokens.
+ *                  blocks of 16 rows (tokens x q heads of a kv head; head_dim 128 above 64
+ *                  rows: of 64), each of which reads its keys: pa_kv_load_q4 and
+ *                  pa_prompt_attention are the faster way for chunks of hundreds of tokens.
  *   flags          0 or PA_ATTN_NON_CAUSAL.
  * An infinity or NaN in a value row may reach the results of its own sequence's other
  * queries in the call.  Calls that may overlap on the GPU need workspaces of their own.
@@ -648,7 +648,9 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  * fp32 (q rounded to fp16; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale are
  * rounded to fp16 (2^-11 each; p * scale below 6e-8 of the largest p to steps of 6e-11,
  * below 6e-5 to steps of 6e-8 where scales of 16 and more stand among the keys); sums
- * in fp32, output bf16.
+ * in fp32, output bf16.  At head_dim 128 with more than 64 rows (max_query_len times the
+ * q heads of a kv head) p and the values code * scale + zero are rounded to fp16 instead
+ * (a value past 65504 to an infinity).
  */
 pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
                                 const void *v_cache, const void *v_scale,

@@ -25,11 +25,12 @@
 // A thread block takes 8 NB rows (tokens x the q heads of a kv head) and a segment of
 // the keys; its four warps work on their own 16-key blocks, each with its own ring of
 // asynchronous copies, and join their sums at the end.  Segments leave fp32 triples
-// that q4_join_kernel merges.
+// that q4_join_kernel merges.  Long queries go to attn_q4_tc.cu (on_tc below).
 #include <algorithm>
 #include <utility>
 
 #include "attn_common.cuh"
+#include "attn_q4.cuh"
 #include "launch.h"
 #include "programmatic.cuh"
 #include "q4.cuh"
@@ -40,19 +41,11 @@ namespace paq8 {
 
 namespace {
 
+using namespace q4;
+
 constexpr int kWarps = 4;
 constexpr float kMargin = 2.0f;  // log2 of the largest p over that of the maximum
 constexpr float kLift = 10.0f;   // log2 of p at the maximum
-
-struct Q4Args {
-  AttnQ4 p;
-  uint32_t *status;
-  float *part_acc;   // [T * Hq][splits][D]
-  float2 *part_ml;   // [T * Hq][splits]
-  int32_t qpk, qpk_inverse, block_tokens, num_items, num_splits;
-  float scale_log2;
-  int32_t seg_start[kMaxSegments];  // 16-key blocks of a range before each segment
-};
 
 // Ring depth by the bytes of a 16-key block (20 D): what keeps about 100 KB an SM in flight.
 template <int D>
@@ -65,38 +58,6 @@ struct Q4Cfg {
   static constexpr int kBlock = kVs + 16 * G * 4;    // 20 D bytes
   static constexpr int kStages = D == 256 ? 4 : 6;
 };
-
-// Visible keys of the block of rows that starts at token tok0 of a sequence, in
-// 16-key blocks: what the kernel and the join agree on.
-struct KeyRange {
-  int begin, end;        // keys
-  int first, blocks;     // 16-key blocks
-};
-
-__device__ __forceinline__ KeyRange key_range(const Q4Args &a, int seq_len, int q_len, int tok0) {
-  const int n_tok = min(a.block_tokens, q_len - tok0);
-  const int last0 = a.p.causal ? seq_len - q_len + tok0 : seq_len - 1;
-  const int last1 = a.p.causal ? last0 + n_tok - 1 : last0;
-  KeyRange r;
-  // (keys past the table's columns have no page: left out here, flagged by the kernel)
-  r.end = static_cast<int>(min(static_cast<int64_t>(last1) + 1, int64_t{a.p.table_columns} * a.p.bs));
-  r.begin = a.p.window > 0 ? max(0, last0 - a.p.window + 1) : 0;
-  r.first = r.begin / 16;
-  r.blocks = r.end > r.begin ? (r.end - 1) / 16 + 1 - r.first : 0;
-  return r;
-}
-
-__device__ __forceinline__ int segments(const Q4Args &a, int blocks) {
-  int n = 1;
-  while (n < a.num_splits && a.seg_start[n] < blocks) ++n;
-  return n;
-}
-
-// The bounds of a sequence's metadata that the kernels rely on.
-__device__ __forceinline__ bool valid_sequence(const Q4Args &a, int q0, int q_len, int seq_len) {
-  return q0 >= 0 && q_len >= 0 && q0 <= a.p.num_tokens - q_len && seq_len >= (a.p.causal ? q_len : 0) &&
-         (a.p.max_query_len > 1 || q_len <= 1);
-}
 
 // D = A B, m16n8k16, fp16 inputs, fp32 accumulators, no addend.
 __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -716,16 +677,30 @@ cudaError_t launch_rows(const Q4Args &a, cudaStream_t stream) {
 }
 
 template <int D>
+cudaError_t launch_join(const Q4Args &a, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.p.num_tokens) * a.p.hq;
+  return launch_kernel(q4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, a);
+}
+
+template <int D>
 cudaError_t launch_d(const Q4Args &a, cudaStream_t stream) {
   const bool wide = a.block_tokens * a.qpk > 8;
   const bool big = a.p.bs == 32;
   cudaError_t e = wide ? (big ? launch_rows<D, 32, 2>(a, stream) : launch_rows<D, 16, 2>(a, stream))
                        : (big ? launch_rows<D, 32, 1>(a, stream) : launch_rows<D, 16, 1>(a, stream));
-  if (e != cudaSuccess || a.num_splits == 1) return e;
-  const int64_t rows = static_cast<int64_t>(a.p.num_tokens) * a.p.hq;
-  return launch_kernel(q4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, a);
+  return e != cudaSuccess || a.num_splits == 1 ? e : launch_join<D>(a, stream);
 }
 
+}  // namespace
+
+namespace {
+// Long queries go to the tcgen05 kernel (attn_q4_tc.cu), which turns a key's codes into
+// operands once per 64 rows: from more than 64 rows a sequence and kv head on it is ahead at D 128
+// (16 sequences x 4096 keys: 32 rows 44 us here, 55 there, 64 rows 61 and 54, 128 rows 97 and 77, 1200
+// rows 695 and 509; 4 x 8192: 56 rows 36 and 42, 112 rows 45 and 40, 2100 rows 470 and 258).
+bool on_tc(int32_t qpk, int32_t max_query_len, int32_t d) {
+  return d == 128 && max_query_len > 1 && int64_t{max_query_len} * qpk > 64;
+}
 }  // namespace
 
 // Rows a block.  16 rows read each key once for twice the rows, 8 leave more blocks an SM: at D
@@ -735,6 +710,7 @@ cudaError_t launch_d(const Q4Args &a, cudaStream_t stream) {
 // in work as eights do, and neither wins by more than a tenth.
 int32_t q4_block_tokens(int32_t qpk, int32_t max_query_len, int32_t d) {
   if (max_query_len <= 1) return 1;
+  if (on_tc(qpk, max_query_len, d)) return kTcRows / qpk;
   const bool eights = d != 128 && int64_t{max_query_len} * qpk <= 64;
   return std::max(1, (eights ? 8 : 16) / qpk);
 }
@@ -747,7 +723,8 @@ std::pair<int64_t, int64_t> blocks_and_places(int32_t num_seqs, int32_t num_toke
   const int32_t tokens = q4_block_tokens(hq / hk, max_query_len, d);
   const int64_t items = std::min<int64_t>({num_tokens, num_tokens / tokens + num_seqs,
                                            (int64_t{max_query_len} + tokens - 1) / tokens * num_seqs});
-  return {std::max<int64_t>(1, items * hk), int64_t{152} * resident_blocks(d, tokens * (hq / hk) > 8)};
+  const int resident = on_tc(hq / hk, max_query_len, d) ? 1 : resident_blocks(d, tokens * (hq / hk) > 8);
+  return {std::max<int64_t>(1, items * hk), int64_t{152} * resident};
 }
 }  // namespace
 
@@ -800,6 +777,11 @@ cudaError_t launch_attention_q4(const AttnQ4 &p, cudaStream_t stream) {
   for (int64_t i = 0; i < n; ++i)
     a.seg_start[i] = static_cast<int32_t>(
         falling ? blocks * i * (2 * n + 1 - i) / (n * (n + 1)) : i * std::max<int64_t>(1, (blocks + n - 1) / n));
+  if (on_tc(a.qpk, p.max_query_len, p.d)) {
+    for (int64_t i = 0; i < n; ++i) a.seg_start[i] = (a.seg_start[i] + 7) / 8 * 8;  // whole tiles of 128 keys
+    const cudaError_t e = launch_attention_tc(a, stream);
+    return e != cudaSuccess || a.num_splits == 1 ? e : launch_join<128>(a, stream);
+  }
   switch (p.d) {
     case 64: return launch_d<64>(a, stream);
     case 128: return launch_d<128>(a, stream);

@@ -548,3 +548,148 @@ def test_segments_of_all_sizes(cuda_device, count, most, splits, d, bs, q_len):
         span = slice(s * q_len, (s + 1) * q_len)
         _compare(out[span], lse[span], q[span], [x.to(dev) for x in _q4.rows64(cpu, table[s], lens[s])],
                  lens[s] - q_len)
+
+
+# ------------------------------------------- long queries (D 128: another kernel above 64 rows)
+# p and the values are rounded to fp16 there: 2^-11 each of p |v|
+
+def _long(cpu, table, q, cu, lens, q_lens, out, lse, dev, causal=True, window=0, sinks=None, bits=10):
+    at = 0
+    for s, (n, a) in enumerate(zip(lens, q_lens)):
+        if a:
+            parts = [x.to(dev) for x in _q4.rows64(cpu, table[s], n)]
+            span = slice(at, at + a)
+            ref, z, vc, vz, va, reach = _q4.attention64(q[span], parts, n - a, causal, window, sinks)
+            d = q.shape[-1]
+            eps = 2.0 ** -16 * reach + d ** -0.5 * 2.0 ** -21 * (float(parts[0].abs().amax()) * d if n else 0.0)
+            tol = (2.0 ** -8 * ref.abs() + (1.01 * 2.0 ** -bits + 2 * eps[..., None] + 2.0 ** -20) * (vc + vz)
+                   + n * 2.0 ** -35 * (float((parts[2].abs() + parts[3].abs()).max()) if n else 0.0) + 1e-30)
+            assert not torch.isnan(out[span]).any()
+            err = (out[span].double() - ref).abs()
+            assert (err <= tol).all(), (s, float((err - tol).max()), float(err.max()))
+            none = torch.isinf(z)
+            assert torch.equal(torch.isinf(lse[span]), none)
+            e = torch.where(none, torch.zeros_like(z), (lse[span].double() - z).abs())
+            assert (e <= eps + 2.0 ** -20 * (1 + torch.where(none, torch.zeros_like(z), z.abs()))).all()
+        at += a
+
+
+def _long_batch(lens, hk, bs, seed, value_scale=1.0):
+    table, blocks = _table(lens, bs, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    cpu = _q4.empty_cache(blocks, hk, 128, bs)
+    n = sum(lens)
+    key = torch.randn((n, hk, 128), generator=g)
+    value = torch.randn((n, hk, 128), generator=g) * value_scale
+    _q4.store(cpu, key.bfloat16(), value.bfloat16(), _slots(table, bs, [(0, x) for x in lens]))
+    return cpu, table
+
+
+@pytest.mark.parametrize("hq,hk", [(4, 4), (8, 2), (28, 4), (16, 1), (10, 2)])
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("splits", [1, 3, 0, 64])
+@pytest.mark.parametrize("window,causal", [(0, True), (1, True), (100, True), (0, False)])
+def test_long_queries(cuda_device, hq, hk, bs, splits, window, causal):
+    H.ensure_built()
+    dev = cuda_device
+    lens, q_lens = [130, 700, 66, 1025, 90, 0 if not causal else 3], [130, 33, 66, 70, 1, 3]
+    cpu, table = _long_batch(lens, hk, bs, hq + bs)
+    cache = [x.to(dev) for x in cpu]
+    g = torch.Generator().manual_seed(hq)
+    t = sum(q_lens)
+    q = torch.randn((t + 2, hq, 128), generator=g).bfloat16().to(dev)
+    sinks = (torch.randn(hq, generator=g) * 3).to(dev)
+    sinks[0] = -math.inf
+    cu = _starts(q_lens, dev)
+    for sk in (None, sinks):
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((t + 2, hq), 7.0, device=dev)
+        ws = torch.zeros(_lib.paged_attention_q4_workspace_size(6, t + 2, hq, hk, 128, 130, 1025, splits),
+                         dtype=torch.uint8, device=dev)
+        ws[256:] = 0xFF
+        _lib.paged_attention_q4(q, *cache, cu, _i32(lens, dev), table.to(dev), 130, 1025, out=out, lse=lse,
+                                workspace=ws, num_splits=splits, sliding_window=window, causal=causal, sinks=sk)
+        assert _lib.check_status(ws) == 0
+        _long(cpu, table, q, cu, lens, q_lens, out, lse, dev, causal, window, sk)
+        assert (out[t:] == 7).all() and (lse[t:] == 7).all()
+
+
+@pytest.mark.parametrize("spread", [1e-3, 1.0, 3000.0])
+def test_long_queries_over_small_and_large_values(cuda_device, spread):
+    H.ensure_built()
+    dev, hq, hk = cuda_device, 8, 2
+    lens, q_lens = [3000, 200], [40, 100]
+    cpu, table = _long_batch(lens, hk, 16, 3, spread)
+    g = torch.Generator().manual_seed(4)
+    q = (torch.randn((140, hq, 128), generator=g) * 2).bfloat16().to(dev)
+    cu = _starts(q_lens, dev)
+    out, lse = _lib.paged_attention_q4(q, *[x.to(dev) for x in cpu], cu, _i32(lens, dev), table.to(dev), 100, 3000)
+    _long(cpu, table, q, cu, lens, q_lens, out, lse, dev)
+
+
+def test_long_queries_without_some_pages(cuda_device):
+    """Entries out of range, a table that ends early, pages before a window, q out of range."""
+    H.ensure_built()
+    dev, hq, hk, bs, n, a = cuda_device, 8, 2, 16, 900, 80
+    cpu, table = _long_batch([n], hk, bs, 8)
+    cache = [x.to(dev) for x in cpu]
+    q = torch.randn((a, hq, 128), generator=torch.Generator().manual_seed(1)).bfloat16().to(dev)
+    cu, sl = _i32([0, a], dev), _i32([n], dev)
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device=dev)
+    bad = table.clone()
+    bad[0, 9], bad[0, 20] = 1 << 30, -5
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[9 * bs:10 * bs] = keep[20 * bs:21 * bs] = False
+    for tab, k in ((bad.to(dev), keep), (table.to(dev)[:, :40], torch.arange(n) < 40 * bs)):
+        out, lse = _lib.paged_attention_q4(q, *cache, cu, sl, tab, a, n, workspace=ws, causal=False)
+        with pytest.raises(_lib.PagedAttentionError) as e:
+            _lib.check_status(ws)
+        assert e.value.bits == _lib.DEV_BAD_BLOCK
+        ws.zero_()
+        parts = [x[k].to(dev) for x in _q4.rows64(cpu, table[0], n)]
+        _compare(out, lse, q, parts, 0, causal=False, p_bits=10)
+    stale = table.clone()
+    stale[0, :(n - a - 100) // bs] = -1
+    out, lse = _lib.paged_attention_q4(q, *cache, cu, sl, stale.to(dev), a, n, workspace=ws, sliding_window=100)
+    assert _lib.check_status(ws) == 0
+    _long(cpu, table, q, cu, [n], [a], out, lse, dev, window=100)
+    q[3, 1, 7] = 1e5
+    _lib.paged_attention_q4(q, *cache, cu, sl, table.to(dev), a, n, workspace=ws)
+    with pytest.raises(_lib.PagedAttentionError) as e:
+        _lib.check_status(ws)
+    assert e.value.bits == _lib.DEV_BAD_Q
+    ws.zero_()
+    _lib.paged_attention_q4(q, *cache, _i32([0, a + 1], dev), sl, table.to(dev), a + 1, n, workspace=ws)
+    with pytest.raises(_lib.PagedAttentionError) as e:
+        _lib.check_status(ws)
+    assert e.value.bits == _lib.DEV_BAD_SEQ
+
+
+def test_long_queries_captured(cuda_device):
+    H.ensure_built()
+    dev, hq, hk = cuda_device, 8, 2
+    lens, q_lens = [2000, 300], [50, 90]
+    cpu, table = _long_batch(lens, hk, 32, 12)
+    cache, tab, cu, sl = [x.to(dev) for x in cpu], table.to(dev), _starts(q_lens, dev), _i32(lens, dev)
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn((140, hq, 128), generator=g).bfloat16().to(dev)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=dev)
+    out, lse = torch.zeros_like(q), torch.zeros((140, hq), device=dev)
+
+    def call():
+        _lib.paged_attention_q4(q, *cache, cu, sl, tab, 90, 2000, out=out, lse=lse, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        q.copy_(torch.randn(q.shape, generator=g).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        have = out.clone(), lse.clone()
+        out.fill_(0)
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, have[0]) and torch.equal(lse, have[1])
+        _long(cpu, table, q, cu, lens, q_lens, out, lse, dev)
