@@ -880,6 +880,9 @@ cudaError_t launch_d(const PromptAttention &p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   static DeviceOnce configured;
   const cudaError_t e = configured.get(nullptr, [](int, int *) {
+    const cudaError_t r = registers_cover(reinterpret_cast<const void *>(prompt_kernel<D>), C::kThreads,
+                                          C::kTiles == 2 ? 256 * 208 + 128 * 88 : 0);
+    if (r != cudaSuccess) return r;
     return cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;

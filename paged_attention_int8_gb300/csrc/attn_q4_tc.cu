@@ -704,6 +704,9 @@ template <int BS>
 cudaError_t launch(const Q4Args &a, cudaStream_t stream) {
   static DeviceOnce configured;
   const cudaError_t e = configured.get(nullptr, [](int, int *) {
+    const cudaError_t r = registers_cover(reinterpret_cast<const void *>(attn_q4_tc_kernel<BS>), kThreads,
+                                          256 * 144 + 256 * 80 + 128 * 32);
+    if (r != cudaSuccess) return r;
     return cudaFuncSetAttribute(attn_q4_tc_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (e != cudaSuccess) return e;

@@ -41,6 +41,15 @@ class DeviceOnce {
   int value_[kMaxDevices] = {};
 };
 
+// Whether the registers that a block of `threads` is launched with cover what its warps then take
+// between them (setmaxnreg waits for registers that are not there).
+inline cudaError_t registers_cover(const void *kernel, int threads, int taken) {
+  cudaFuncAttributes f;
+  const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+  if (e != cudaSuccess) return e;
+  return (f.numRegs + 7) / 8 * 8 * threads >= taken ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 // cuTensorMapEncodeTiled of the driver, or null.
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
