@@ -625,14 +625,14 @@ again:
           m = mn;
         }
       }
-      const float inv = sum > 0.0f ? w / sum : 0.0f;  // a row that sees no key: 0
+      const float inv = sum == 0.0f ? 0.0f : w / sum;  // a row that sees no key: 0 (a NaN stays one)
       uint16_t *dst = a.p.out + at * D + g * 4;
 #pragma unroll
       for (int gr = 0; gr < G; ++gr)
         *reinterpret_cast<uint2 *>(dst + gr * 32) =
             make_uint2(pack_bf162(out[nb][c][gr][0] * inv, out[nb][c][gr][1] * inv),
                        pack_bf162(out[nb][c][gr][2] * inv, out[nb][c][gr][3] * inv));
-      if (g == 0 && a.p.lse) a.p.lse[at] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+      if (g == 0 && a.p.lse) a.p.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
 }
 

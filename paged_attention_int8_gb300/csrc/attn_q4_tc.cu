@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
               m = mn;
             }
           }
-          inv = sum > 0.0f ? w / sum : 0.0f;  // a row that sees no key: 0
-          if (a.p.lse) a.p.lse[at] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+          inv = sum == 0.0f ? 0.0f : w / sum;  // a row that sees no key: 0 (a NaN stays one)
+          if (a.p.lse) a.p.lse[at] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
         }
       }
       sts_f32(m_at + tid * 4, inv);

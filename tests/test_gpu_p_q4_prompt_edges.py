@@ -1,0 +1,79 @@
+"""The 4-bit cache and prompt_attention where their documentation makes a promise that larger
+tests do not reach: keys that are no numbers, values past what fp16 holds next to their
+weights, queries far from 1, sequences whose bounds fall, and which outputs a value that is no
+number can reach."""
+import math
+
+import pytest
+import torch
+
+from paged_attention_int8_gb300 import _lib
+from tests import _harness as H
+from tests import _q4
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x, device):
+    return torch.tensor(x, dtype=torch.int32, device=device)
+
+
+def _starts(lens, device):
+    return torch.tensor([0] + list(lens)).cumsum(0).int().to(device)
+
+
+def _filled(lens, hk, d, bs, key, value):
+    """A cache that holds rows key, value [sum(lens), Hk, D], on the CPU, and its table."""
+    pages = [-(-n // bs) for n in lens]
+    perm = torch.randperm(sum(pages) + 1, generator=torch.Generator().manual_seed(d)).int()
+    table = torch.full((len(lens), max(pages)), -1, dtype=torch.int32)
+    at = 0
+    for s, c in enumerate(pages):
+        table[s, :c] = perm[at:at + c]
+        at += c
+    pos = torch.cat([torch.arange(n) for n in lens])
+    seq = torch.cat([torch.full((n,), s) for s, n in enumerate(lens)])
+    cpu = _q4.empty_cache(sum(pages) + 1, hk, d, bs)
+    _q4.store(cpu, key.bfloat16(), value.bfloat16(), table[seq, pos // bs].long() * bs + pos % bs)
+    return cpu, table
+
+
+def _flagged(status, bits):
+    with pytest.raises(_lib.PagedAttentionError) as e:
+        _lib.check_status(status)
+    assert e.value.bits == bits
+
+
+# --------------------------------------------------- keys and values that are no numbers
+
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (8, 2, 128), (6, 2, 256)])
+@pytest.mark.parametrize("count", [1, 3, 70])
+@pytest.mark.parametrize("splits", [1, 4])
+@pytest.mark.parametrize("sink", [False, True])
+def test_a_key_that_is_no_number(cuda_device, hq, hk, d, count, splits, sink):
+    """Rows that see it have neither an output nor an lse, whatever the segments; the rows
+    before it and the other sequences are what they are without it."""
+    H.ensure_built()
+    dev, lens, bad = cuda_device, [400, 350, 77], 400 - 1 - count // 2
+    g = torch.Generator().manual_seed(d)
+    key, value = (torch.randn((sum(lens), hk, d), generator=g) for _ in range(2))
+    q = torch.randn((3 * count, hq, d), generator=g).bfloat16().to(dev)
+    sinks = torch.randn(hq, generator=g).to(dev) if sink else None
+    got = []
+    for nan in (False, True):
+        key[bad, 0, 5] = float("nan") if nan else 0.5
+        cpu, table = _filled(lens, hk, d, 16, key, value)
+        got.append(_lib.paged_attention_q4(q, *[x.to(dev) for x in cpu], _starts([count] * 3, dev), _i32(lens, dev),
+                                           table.to(dev), count, 400, num_splits=splits, sinks=sinks))
+    (want, want_lse), (out, lse) = got
+    first = bad - (400 - count)  # query that sees it first
+    heads = slice(0, hq // hk)   # of kv head 0
+    assert torch.isnan(out[first:count, heads]).all() and torch.isnan(lse[first:count, heads]).all()
+    assert torch.equal(lse[count:], want_lse[count:]) and torch.equal(out[count:], want[count:])
+    assert torch.equal(lse[:, heads.stop:], want_lse[:, heads.stop:])
+    assert torch.equal(out[:, heads.stop:], want[:, heads.stop:])
+    # queries before it share a block with those that see it, and so where its maxima move: each of the
+    # two results is within half a bf16 step and 2^-10 of sum p |c s| + 2^-11 of sum p |z| (under 9)
+    a, b = out[:first, heads].float(), want[:first, heads].float()
+    assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -9 * 9).all()
+    assert ((lse[:first, heads] - want_lse[:first, heads]).abs() <= 2e-3).all()
