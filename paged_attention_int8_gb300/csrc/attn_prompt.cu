@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             m_used = mn;
           }
         }
-        const float inv = seen ? o_mul / l : 0.0f;
+        const float inv = seen && l != 0.0f ? o_mul / l : 0.0f;  // (l is 0 where every score is -inf)
         // Four neighbouring lanes exchange 16-byte pieces, so that they write 64 bytes of one row
         // after another (a lane writing its own row kept the memory pipe for 3000 cycles and more,
         // and the waits behind it).

@@ -77,3 +77,21 @@ def test_a_key_that_is_no_number(cuda_device, hq, hk, d, count, splits, sink):
     a, b = out[:first, heads].float(), want[:first, heads].float()
     assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -9 * 9).all()
     assert ((lse[:first, heads] - want_lse[:first, heads]).abs() <= 2e-3).all()
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 2, 128), (6, 2, 256)])
+def test_scores_of_minus_infinity(cuda_device, hq, hk, d):
+    """Weights that are all zero give 0 and -inf in one segment as in several."""
+    H.ensure_built()
+    dev = cuda_device
+    q = torch.ones((5, hq, d), device=dev).bfloat16()
+    k = torch.full((4000, hk, d), -float("inf"), device=dev).bfloat16()
+    v = torch.randn((4000, hk, d), device=dev).bfloat16()
+    need = _lib.prompt_attention_workspace_size(1, 5, 4000, hq, hk, d, 5, 4000)
+    assert need > 256
+    for size in (256, need):
+        ws = torch.zeros(size, dtype=torch.uint8, device=dev)
+        out, lse = _lib.prompt_attention(q, k, v, _i32([0, 5], dev), 5, cu_seqlens_k=_i32([0, 4000], dev),
+                                         max_key_len=4000, workspace=ws)
+        assert _lib.check_status(ws) == 0
+        assert (out == 0).all() and (lse == -math.inf).all()
