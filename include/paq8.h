@@ -647,8 +647,8 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  * Numerics: the codes enter both products exactly; scores are scaled and summed in
  * fp32 (q rounded to fp16; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale are
  * rounded to fp16 (2^-11 each; p * scale below 6e-8 of the largest p to steps of 6e-11,
- * below 6e-5 to steps of 6e-8 where scales of 16 and more stand among the keys); sums
- * in fp32, output bf16.  At head_dim 128 with more than 64 rows (max_query_len times the
+ * below 6e-5 to steps of 6e-8 where scales of 16 and more stand among the keys, below
+ * 2.4e-4 to steps of 2.4e-7 where they pass 16376); sums in fp32, output bf16.  At head_dim 128 with more than 64 rows (max_query_len times the
  * q heads of a kv head) p and the values code * scale + zero are rounded to fp16 instead
  * (a value past 65504 to an infinity).
  */

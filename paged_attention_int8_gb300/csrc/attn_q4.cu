@@ -20,7 +20,8 @@
 // weights of small scales stay out of fp16's subnormals (p s_g is normal from 6e-8
 // on); with s_g of 16 and more, ranges above 240, the product can leave fp16, whose
 // infinity then stands in the sums: such a warp goes over its keys again without the
-// lift (4 s_g is at most 34936).
+// lift (p s_g is at most 4 s_g), and where that is too much, from s_g 16376 on, a third
+// time with p at most 1.
 //
 // A thread block takes 8 NB rows (tokens x the q heads of a kv head) and a segment of
 // the keys; its four warps work on their own 16-key blocks, each with its own ring of
@@ -519,7 +520,7 @@ again:
     }
   }
   cp_async_wait<0>();
-  if (lift > 0.0f) {
+  if (lift > -kMargin) {
     float nan = 0.0f;  // NaN where a sum is infinite, or NaN
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -528,7 +529,7 @@ again:
 #pragma unroll
         for (int e = 0; e < 4; ++e) nan = fmaf(o[nb][gr][0][e], 0.0f, fmaf(o[nb][gr][1][e], 0.0f, nan));
     if (__any_sync(0xffffffffu, nan != nan)) {
-      lift = 0.0f;
+      lift = lift > 0.0f ? 0.0f : -kMargin;
       __syncwarp();
       goto again;
     }

@@ -95,3 +95,37 @@ def test_scores_of_minus_infinity(cuda_device, hq, hk, d):
                                          max_key_len=4000, workspace=ws)
         assert _lib.check_status(ws) == 0
         assert (out == 0).all() and (lse == -math.inf).all()
+
+
+# ----------------------------------------------------------------- values and queries of all sizes
+
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (8, 2, 128), (6, 2, 256), (32, 2, 128)])
+@pytest.mark.parametrize("count", [1, 3])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_the_largest_scales(cuda_device, hq, hk, d, count, splits):
+    """Values up to 9e5 over zeros that fp16 holds: steps of up to 6e4, near its largest number.
+
+    p and p * scale are rounded to fp16, 2^-11 each; p below its normal range to 2^-25 against a
+    largest p of at least 1 / 4: 2^-23 a key of its largest value."""
+    H.ensure_built()
+    dev, n = cuda_device, 1000
+    g = torch.Generator().manual_seed(d + count)
+    key = torch.randn((n, hk, d), generator=g)
+    value = torch.rand((n, hk, d), generator=g) * 9e5
+    value[..., ::32] = 0  # a group's lowest
+    q = (torch.randn((count, hq, d), generator=g) * 0.5).bfloat16().to(dev)
+    cpu, table = _filled([n], hk, d, 16, key, value)
+    held = [x[table[0].long()][:n // 16] for x in cpu[1::2]]
+    assert all(torch.isfinite(x).all() for x in held) and float(held[1][:, :, 0].max()) > 5e4
+    out, lse = _lib.paged_attention_q4(q, *[x.to(dev) for x in cpu], _i32([0, count], dev), _i32([n], dev),
+                                       table.to(dev), count, n, num_splits=splits)
+    parts = [x.to(dev) for x in _q4.rows64(cpu, table[0], n)]
+    ref, z, vc, vz, _, reach = _q4.attention64(q, parts, n - count)
+    eps = 2.0 ** -17 * reach
+    tol = (2.0 ** -8 * ref.abs() + 1.01 * (2.0 ** -10 * vc + 2.0 ** -11 * vz)
+           + (2 * eps[..., None] + 2.0 ** -20) * (vc + vz)
+           + n * 2.0 ** -23 * float((parts[2].abs() + parts[3].abs()).max()))
+    err = (out.double() - ref).abs()
+    assert torch.isfinite(out).all()
+    assert (err <= tol).all(), float((err - tol).max())
+    assert ((lse.double() - z).abs() <= eps + 2.0 ** -20 * (1 + z.abs())).all()
