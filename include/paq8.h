@@ -703,8 +703,9 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
  *                  GPU need workspaces of their own.
  *   flags          0 or PA_ATTN_NON_CAUSAL (every query sees all keys of its sequence).
  * head_dim 64, 128, 256; num_q_heads a multiple of num_kv_heads, at most 128 times.
- * A sequence whose bounds are out of range is not written and flagged PA_DEV_BAD_SEQ;
- * rows of tokens no sequence owns are not written.  What other sequences' rows hold never
+ * A sequence whose bounds fall or are out of range is not written and flagged PA_DEV_BAD_SEQ
+ * (one without query tokens asks for nothing); rows of tokens no sequence owns are not
+ * written.  What other sequences' rows hold never
  * reaches a result; an infinity or NaN in a value row may reach queries of its own
  * sequence up to 15 keys before the first that sees it.  Asynchronous.
  * Numerics: exact products summed in fp32, softmax in fp32, p rounded to bf16 for its

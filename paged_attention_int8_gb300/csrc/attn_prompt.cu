@@ -276,9 +276,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     int q_used[2] = {0, 0};
     int count = 0, asked = 0;
     uint32_t block = blockIdx.x;
+    const auto fits = [&](int q0, int q_len, int k0, int k_len) {
+      return q_len > 0 && q0 >= 0 && q0 <= a.p.num_tokens - q_len && k0 >= 0 && k_len >= 0 &&
+             k0 <= a.p.num_keys - k_len;
+    };
     // 2 to 32 sequences: the one with most keys first, lane s holding sequence s and where its
     // items stand in that order (4 chunks behind prefixes of 1 to 6000 keys, D 256: 124 us, 133 in
-    // the order of the batch).  A sequence whose bounds are out of range has one item, to be flagged.
+    // the order of the batch).  A sequence whose bounds are out of range has none, and is flagged.
     const bool ranked = a.p.num_seqs > 1 && a.p.num_seqs <= 32;
     int start = 0, items_of = 0, q0_of = 0, k0_of = 0, q_len_of = 0, k_len_of = 0;
     if (ranked) {
@@ -288,11 +292,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         k0_of = a.p.cu_k[lane];
         q_len_of = a.p.cu_q[lane + 1] - q0_of;
         k_len_of = a.p.cu_k[lane + 1] - k0_of;
-        if (q_len_of > 0) {
-          const bool fits = q0_of >= 0 && q0_of <= a.p.num_tokens - q_len_of && k0_of >= 0 && k_len_of >= 0 &&
-                            k0_of <= a.p.num_keys - k_len_of;
-          items_of = fits ? (q_len_of - 1) / a.block_tokens + 1 : 1;
-          keys = fits ? k_len_of : 0;
+        if (fits(q0_of, q_len_of, k0_of, k_len_of)) {
+          items_of = (q_len_of - 1) / a.block_tokens + 1;
+          keys = k_len_of;
+        } else if (q_len_of != 0) {
+          flag_status(a.status, PA_DEV_BAD_SEQ);
         }
       }
 #pragma unroll 1
@@ -328,12 +332,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         it.k_len = a.p.cu_k[seq + 1] - it.k0;
         it.tok0 = (item - (a.block_tokens == 1 ? it.q0 : it.q0 / a.block_tokens + seq)) * a.block_tokens;
       }
-      bool valid = it.tok0 >= 0 && it.tok0 < q_len;
-      if (valid && (it.q0 < 0 || it.q0 > a.p.num_tokens - q_len || it.k0 < 0 || it.k_len < 0 ||
-                    it.k0 > a.p.num_keys - it.k_len)) {
-        if (lane == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
-        valid = false;
-      }
+      bool valid = it.tok0 >= 0 && it.tok0 < q_len && fits(it.q0, q_len, it.k0, it.k_len);
       Rows rows;
       if (valid) {
         rows = rows_of<C::kTiles>(a, q_len, it.k_len, it.tok0);
@@ -408,6 +407,16 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           }
         }
         ++count;
+      }
+      // in the batch's order no item need be that of a sequence with bad bounds: item n looks at
+      // sequence n (and n + num_items, ...)
+      if (!ranked && it.h == 0 && it.segment == 0) {
+        const int64_t n = rest % a.num_items;
+        for (int64_t s = n + int64_t{lane} * a.num_items; s < a.p.num_seqs; s += int64_t{32} * a.num_items) {
+          const int q0 = a.p.cu_q[s], k0 = a.p.cu_k[s];
+          const int len = a.p.cu_q[s + 1] - q0;
+          if (len != 0 && !fits(q0, len, k0, a.p.cu_k[s + 1] - k0)) flag_status(a.status, PA_DEV_BAD_SEQ);
+        }
       }
       // ---- the next block's number: asked for when this item's copies are on their way (at its
       // start a block would hold the next while others are idle)

@@ -129,3 +129,43 @@ def test_the_largest_scales(cuda_device, hq, hk, d, count, splits):
     assert torch.isfinite(out).all()
     assert (err <= tol).all(), float((err - tol).max())
     assert ((lse.double() - z).abs() <= eps + 2.0 ** -20 * (1 + z.abs())).all()
+
+
+# ---------------------------------------------------------------- bounds out of range
+
+# starts of sequences over 40 rows: a falling one last, in the middle, beside many, and none within
+BAD_STARTS = [[0, 40, 20], [0, 20, 10, 40], list(range(30)) + [25, 30, 31, 32, 33, 40],
+              list(range(20)) + [10] + list(range(20, 40)), [100, 120], [-50, -20, 40]]
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 2, 128), (6, 2, 256), (128, 1, 256)])
+@pytest.mark.parametrize("starts", BAD_STARTS)
+def test_prompt_bounds_that_are_flagged(cuda_device, hq, hk, d, starts):
+    H.ensure_built()
+    dev = cuda_device
+    q = torch.randn((40, hq, d), device=dev).bfloat16()
+    k = torch.randn((40, hk, d), device=dev).bfloat16()
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device=dev)
+    cu = _i32(starts, dev)
+    flat = _i32([0] * len(starts), dev)
+    for cu_k in (cu, flat):
+        _lib.prompt_attention(q, k, k, cu, 40, cu_seqlens_k=cu_k, max_key_len=40, workspace=ws)
+        _flagged(ws, _lib.DEV_BAD_SEQ)
+        assert _lib.check_status(ws) == 0
+
+
+def test_a_bad_prompt_keeps_no_other_from_its_rows(cuda_device):
+    """Tiles of one token: as many items as tokens, whatever the sequences that are left out."""
+    H.ensure_built()
+    dev = cuda_device
+    q = torch.randn((4, 128, 256), device=dev).bfloat16()
+    k = torch.randn((4, 1, 256), device=dev).bfloat16()
+    for starts, own in (([0, 9, 2, 4], [2, 3]), ([0, 2, 4, 9], [0, 1, 2, 3]), ([-1, 0, 2, 4], [0, 1, 2, 3])):
+        ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((4, 128), 7.0, device=dev)
+        _lib.prompt_attention(q, k, k, _i32(starts, dev), 9, cu_seqlens_k=_i32([0] * 4, dev), max_key_len=9, out=out,
+                              lse=lse, workspace=ws)
+        _flagged(ws, _lib.DEV_BAD_SEQ)
+        for i in range(4):  # the queries see no key
+            assert (out[i] == (0 if i in own else 7)).all() and (lse[i] == (-math.inf if i in own else 7)).all()
