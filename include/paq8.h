@@ -581,8 +581,8 @@ pa_status pa_kv_store_q4(const void *key, int64_t key_token_stride,
  *   block_table    int32: rows block_table_stride apart, of which
  *                  block_table_columns entries are read.
  * Each value is code * scale (+ zero) in fp32, rounded once to bf16.  Device checks
- * (status, or NULL): rows out of range or a bad load_lens (PA_DEV_BAD_SEQ, the
- * sequence is not loaded); an entry outside [0, num_blocks) or past the table's
+ * (status, or NULL): rows that fall or are out of range or a bad load_lens (PA_DEV_BAD_SEQ,
+ * the sequence is not loaded); an entry outside [0, num_blocks) or past the table's
  * columns (PA_DEV_BAD_BLOCK, the rows of that page are not written).
  * num_seqs == 0 or num_rows == 0 is a no-op.  Asynchronous.
  */

@@ -69,22 +69,27 @@ __global__ void __launch_bounds__(32 * kLoadWarps) kv_load_kernel(const __grid_c
   const int h = static_cast<int>(unit % p.hk);
   const int64_t item = unit / p.hk;
   if (item >= p.num_rows / BS + p.num_seqs) return;
+  // row0, room and length of a sequence; whether they fit
+  struct Bounds {
+    int row0, room, n;
+  };
+  const auto bounds_of = [&](int seq) {
+    const int row0 = p.cu_seqlens_k[seq], room = p.cu_seqlens_k[seq + 1] - row0;
+    return Bounds{row0, room, p.load_lens ? p.load_lens[seq] : room};
+  };
+  const auto fit = [&](const Bounds &b) {
+    return b.row0 >= 0 && b.room >= 0 && b.row0 <= p.num_rows - b.room && b.n >= 0 && b.n <= b.room;
+  };
+  // No item need be that of a sequence whose bounds are bad: item i looks at sequence i (there are
+  // no fewer items than sequences), on its way to its own.
+  Bounds other{0, 0, 0};
+  if (h == 0 && item < p.num_seqs) other = bounds_of(static_cast<int>(item));
   const int seq = find_seq(p.cu_seqlens_k, p.num_seqs, BS, static_cast<int>(item), lane);
-  const int row0 = p.cu_seqlens_k[seq], room = p.cu_seqlens_k[seq + 1] - row0;
+  const Bounds own = bounds_of(seq);
+  if (!fit(other) && lane == 0) flag_status(p.status, PA_DEV_BAD_SEQ);
+  if (!fit(own)) return;
+  const int row0 = own.row0, n = own.n;
   const int page = static_cast<int>(item) - (row0 / BS + seq);
-  const bool first = page == 0 && h == 0 && lane == 0;
-  if (row0 < 0 || room < 0 || row0 > p.num_rows - room) {
-    if (first) flag_status(p.status, PA_DEV_BAD_SEQ);
-    return;
-  }
-  int n = room;
-  if (p.load_lens) {
-    n = p.load_lens[seq];
-    if (n < 0 || n > room) {
-      if (first) flag_status(p.status, PA_DEV_BAD_SEQ);
-      return;
-    }
-  }
   if (page < 0 || page * BS >= n) return;
   const int block = page < p.table_columns
                         ? p.block_table[static_cast<int64_t>(seq) * p.table_stride + page]

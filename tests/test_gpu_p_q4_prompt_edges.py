@@ -169,3 +169,20 @@ def test_a_bad_prompt_keeps_no_other_from_its_rows(cuda_device):
         _flagged(ws, _lib.DEV_BAD_SEQ)
         for i in range(4):  # the queries see no key
             assert (out[i] == (0 if i in own else 7)).all() and (lse[i] == (-math.inf if i in own else 7)).all()
+
+
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 32), (256, 16)])
+@pytest.mark.parametrize("starts", BAD_STARTS)
+def test_read_back_bounds_that_are_flagged(cuda_device, d, bs, starts):
+    H.ensure_built()
+    dev, hk = cuda_device, 2
+    cache = [x.to(dev) for x in _q4.empty_cache(3, hk, d, bs, fill=0)]
+    rows = torch.full((2, 40, hk, d), 7.0, dtype=torch.bfloat16, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    table = torch.arange(3, dtype=torch.int32, device=dev).repeat(len(starts) - 1, 1)
+    for lens in (None, _i32([0] * (len(starts) - 1), dev)):
+        _lib.kv_load_q4(rows[0], rows[1], _i32(starts, dev), table, *cache, load_lens=lens, status=status)
+        _flagged(status, _lib.DEV_BAD_SEQ)
+    _lib.kv_load_q4(rows[0], rows[1], _i32([0, 3, 6], dev), table[:1].repeat(2, 1), *cache,
+                    load_lens=_i32([0, 4], dev), status=status)
+    _flagged(status, _lib.DEV_BAD_SEQ)
