@@ -151,12 +151,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
   const int q0 = a.p.cu[seq];
   const int q_len = a.p.cu[seq + 1] - q0;
   const int seq_len = a.p.seq_lens[seq];
-  if (tok0 < 0 || tok0 >= q_len) {
-    if (q_len < 0 && sigma == 0 && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
-    return;
-  }
-  if (!valid_sequence(a, q0, q_len, seq_len)) {
-    if (sigma == 0 && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+  if (tok0 < 0 || tok0 >= q_len || !valid_sequence(a, q0, q_len, seq_len)) {
+    if (threadIdx.x == 0) flag_bad_sequences(a, item, h, sigma);
     return;
   }
   const KeyRange range = key_range(a, seq_len, q_len, tok0);
@@ -576,7 +572,10 @@ again:
       }
   }
   __syncthreads();
-  if (warp > 0) return;
+  if (warp > 0) {
+    if (threadIdx.x == 32 && a.p.max_query_len > 1) flag_bad_sequences(a, item, h, sigma);
+    return;
+  }
 #pragma unroll 1
   for (int k = 0; k < kWarps - 1; ++k) {
     const float *src = area + k * kFields * 32 + lane;

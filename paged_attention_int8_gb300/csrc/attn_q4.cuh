@@ -51,6 +51,16 @@ __device__ __forceinline__ bool valid_sequence(const Q4Args &a, int q0, int q_le
          (a.p.max_query_len > 1 || q_len <= 1);
 }
 
+// No item need be that of a sequence whose bounds are bad: item i looks at sequences i, i +
+// num_items, ... (single tokens: its own), by one thread of one block.
+__device__ __forceinline__ void flag_bad_sequences(const Q4Args &a, int item, int h, int sigma) {
+  if (h != 0 || sigma != 0) return;
+  for (int64_t s = item; s < a.p.num_seqs; s += a.num_items) {
+    const int q0 = a.p.cu[s], q_len = a.p.cu[s + 1] - q0;
+    if (q_len != 0 && !valid_sequence(a, q0, q_len, a.p.seq_lens[s])) flag_status(a.status, PA_DEV_BAD_SEQ);
+  }
+}
+
 // The tcgen05 kernel of a call (D 128, blocks of up to kTcRows rows); its triples and results are
 // those of the mma.sync kernel.
 constexpr int kTcRows = 64;

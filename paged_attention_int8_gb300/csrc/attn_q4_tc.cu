@@ -199,12 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
   const int q_len = a.p.cu[seq + 1] - q0;
   const int seq_len = a.p.seq_lens[seq];
   const int tok0 = (item - ((a.block_tokens == 1 ? q0 : q0 / a.block_tokens + seq))) * a.block_tokens;
-  if (tok0 < 0 || tok0 >= q_len) {
-    if (q_len < 0 && sigma == 0 && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
-    return;
-  }
-  if (!valid_sequence(a, q0, q_len, seq_len)) {
-    if (sigma == 0 && threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_SEQ);
+  if (tok0 < 0 || tok0 >= q_len || !valid_sequence(a, q0, q_len, seq_len)) {
+    if (threadIdx.x == 0) flag_bad_sequences(a, item, h, sigma);
     return;
   }
   const KeyRange range = key_range(a, seq_len, q_len, tok0);
@@ -688,6 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
         mbar_wait(bar(kBarDrain), 0);
       }
       __syncwarp();
+    } else if (warp == kMmaWarp + 1 && lane == 0) {
+      flag_bad_sequences(a, item, h, sigma);
     }
   }
   if (!ok) flag_status(a.status, PA_DEV_TIMEOUT);

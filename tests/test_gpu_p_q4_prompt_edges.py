@@ -186,3 +186,26 @@ def test_read_back_bounds_that_are_flagged(cuda_device, d, bs, starts):
     _lib.kv_load_q4(rows[0], rows[1], _i32([0, 3, 6], dev), table[:1].repeat(2, 1), *cache,
                     load_lens=_i32([0, 4], dev), status=status)
     _flagged(status, _lib.DEV_BAD_SEQ)
+
+
+@pytest.mark.parametrize("hq,hk,d,most", [(4, 2, 64, 40), (16, 1, 64, 40), (8, 2, 128, 10), (8, 2, 128, 40),
+                                          (6, 2, 256, 40), (16, 1, 256, 2)])
+@pytest.mark.parametrize("starts", BAD_STARTS)
+def test_cached_bounds_that_are_flagged(cuda_device, hq, hk, d, most, starts):
+    H.ensure_built()
+    dev = cuda_device
+    cache = [x.to(dev) for x in _q4.empty_cache(4, hk, d, 16, fill=0)]
+    for x in cache[1::2]:
+        x.fill_(1.0)
+    q = torch.randn((40, hq, d), device=dev).bfloat16()
+    n = len(starts) - 1
+    table = torch.arange(4, dtype=torch.int32, device=dev).repeat(n, 1)
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device=dev)
+    for splits in (1, 3):
+        _lib.paged_attention_q4(q, *cache, _i32(starts, dev), _i32([60] * n, dev), table, most, 60, workspace=ws,
+                                num_splits=splits)
+        _flagged(ws, _lib.DEV_BAD_SEQ)
+    # a sequence without queries asks for nothing
+    _lib.paged_attention_q4(q, *cache, _i32([0, 0, 2, 2], dev), _i32([-5, 60, 0], dev), table[:1].repeat(3, 1), most,
+                            60, workspace=ws)
+    assert _lib.check_status(ws) == 0
