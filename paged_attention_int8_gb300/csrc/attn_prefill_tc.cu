@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(512, 1)
         auto load_s = [&]() {
           tc::ld32(t_lane, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
           tc::ld32(t_lane + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-          tc::wait_ld();
+          tc::wait_loaded(*reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tc::wait_loaded(*reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
           if (need_mask) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(512, 1)
             for (int cb = 0; cb < D / 32; ++cb) {
               uint32_t orr[32];
               tc::ld32(t_lane + C::kOCol + cb * 32, orr);
-              tc::wait_ld();
+              tc::wait_loaded(orr);
 #pragma unroll
               for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * f);
               tc::st32(t_lane + C::kOCol + cb * 32, orr);
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t orr[32];
           tc::ld32(t_lane + C::kOCol + cb * 32, orr);
-          tc::wait_ld();
+          tc::wait_loaded(orr);
           if (valid) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {

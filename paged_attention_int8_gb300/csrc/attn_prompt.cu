@@ -134,19 +134,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// The wait for this thread's TMEM loads, bound to the registers of one of them, so that
-// no use of them can be moved in front of it.
-__device__ __forceinline__ void wait_loaded(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
 // What a block works on: two row tiles (D 256: one) of a sequence and kv head.
 struct alignas(64) Item {
   int nt;              // 128-key tiles from t0 on, of the row tile that sees most; -1: no more items
@@ -654,7 +641,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) tc::ld32(t_s + cb * 32, sr[cb]);
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) wait_loaded(sr[cb]);
+        for (int cb = 0; cb < 4; ++cb) tc::wait_loaded(sr[cb]);
         const auto scale_first = [&](uint32_t(&x)[32], int first) {  // keys from `first` on
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -694,7 +681,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             for (int cb = 0; cb < D / 32; ++cb) {
               uint32_t orr[32];
               tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
-              wait_loaded(orr);
+              tc::wait_loaded(orr);
 #pragma unroll
               for (int c = 0; c < 32; ++c) orr[c] = __float_as_uint(__uint_as_float(orr[c]) * f);
               tc::st32(t_lane + C::o_col(tile) + cb * 32, orr);
@@ -748,7 +735,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           for (int cb = 0; n > 0 && cb < D / 32; ++cb) {
             uint32_t orr[32];
             tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
-            wait_loaded(orr);
+            tc::wait_loaded(orr);
             if (seen) {
 #pragma unroll
               for (int c = 0; c < 32; c += 4)
@@ -782,7 +769,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           uint32_t orr[32];
           if (n > 0) {
             tc::ld32(t_lane + C::o_col(tile) + cb * 32, orr);
-            wait_loaded(orr);
+            tc::wait_loaded(orr);
           }
           uint32_t piece[4][4];  // [row of the four][word] of piece lane & 3
 #pragma unroll

@@ -340,16 +340,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
           for (int i = 0; i < 16; ++i)
             x2[i] = f32x2_fma(f32x2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f, x2[i]);
         };
-        tc::wait_ld();
+        tc::wait_loaded(r0);
+        tc::wait_loaded(r1);
         add(r0, z2);
         add(r1, sc2[0]);
         tc::ld32(t_lane + kSCol + 1 * kN, r0);
         tc::ld32(t_lane + kSCol + 2 * kN, r1);
-        tc::wait_ld();
+        tc::wait_loaded(r0);
+        tc::wait_loaded(r1);
         add(r0, sc2[1]);
         add(r1, sc2[2]);
         tc::ld32(t_lane + kSCol + 3 * kN, r0);
-        tc::wait_ld();
+        tc::wait_loaded(r0);
         add(r0, sc2[3]);
       }
       tc::fence_before();
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
           tc::fence_after();
           uint32_t o[32];
           tc::ld32(t_lane + kOCol, o);
-          tc::wait_ld();
+          tc::wait_loaded(o);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             o[c] = __float_as_uint(__uint_as_float(o[c]) * lds_f32(m_mine + (2 * kN + c) * 4));
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
     for (int c = 0; c < 32; ++c) o[c] = 0u;
     if (nt > 0) {
       tc::ld32(t_lane + kOCol, o);
-      tc::wait_ld();
+      tc::wait_loaded(o);
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
