@@ -645,12 +645,14 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  * An infinity or NaN in a value row may reach the results of its own sequence's other
  * queries in the call.  Calls that may overlap on the GPU need workspaces of their own.
  * Numerics: the codes enter both products exactly; scores are scaled and summed in
- * fp32 (q rounded to fp16; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale are
- * rounded to fp16 (2^-11 each; p * scale below 6e-8 of the largest p to steps of 6e-11,
- * below 6e-5 to steps of 6e-8 where scales of 16 and more stand among the keys, below
- * 2.4e-4 to steps of 2.4e-7 where they pass 16376); sums in fp32, output bf16.  At head_dim 128 with more than 64 rows (max_query_len times the
- * q heads of a kv head) p and the values code * scale + zero are rounded to fp16 instead
- * (a value past 65504 to an infinity).
+ * fp32 (q in fp16, times a power of two by the largest of its block of rows: bf16 values
+ * from 2^-28 of that on are exact; |q| >= 65520 is flagged PA_DEV_BAD_Q); p and p * scale
+ * are rounded to fp16 (2^-11 each; p * scale below 6e-8 of the largest p to steps of
+ * 6e-11, below 6e-5 to steps of 6e-8 where scales of 16 and more stand among the keys,
+ * below 2.4e-4 to steps of 2.4e-7 where they pass 16376); sums in fp32, output bf16.  At
+ * head_dim 128 with more than 64 rows (max_query_len times the q heads of a kv head) p
+ * and the values code * scale + zero are rounded to fp16 instead (a value past 65504 to
+ * an infinity).
  */
 pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
                                 const void *v_cache, const void *v_scale,

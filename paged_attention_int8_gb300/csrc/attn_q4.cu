@@ -11,7 +11,8 @@
 //   Scores  S^T[16 keys x 8 rows] = K[16 x 16 ch] Q^T[16 ch x 8 rows], keys in the
 //     MMA's M dimension.  Per group s_g sum q c is scaled in fp32; the zeros' part
 //     sum_g z_g (sum q)_g is one more MMA over the groups, with the q sums as two fp16
-//     parts (22 bits; q is a row's, formed once).  No rounding but q to fp16.
+//     parts (22 bits; q is a row's, formed once).  No rounding but q's to fp16, in a power of
+//     two of a block's largest (query_scale).
 //   Output  O^T[16 ch x 8 rows] += V^T P^T, where the key's scale goes into P: per
 //     group P_g = fp16(p s_g), so that the codes again enter as they are; the zeros'
 //     part is one more MMA (groups in M).  p and p s_g are rounded to fp16 (2^-11).
@@ -167,12 +168,14 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
   // ---- q as the B operand: lane (g, t) holds row 8 nb + g
   //   group gr, step e: channels 32 gr + 8 t + 2 e' of the nibbles that step e's words
   //   hold: step 0 nibbles (0, 4 | 1, 5), step 1 nibbles (2, 6 | 3, 7); the second pair
-  //   of each meets codes of weight 16 and is divided by it (exact down to 2^-13)
+  //   of each meets codes of weight 16 and is divided by it
   uint32_t qb[NB][G][2][2];
   uint32_t qs[NB][2];  // sums over groups 2t, 2t + 1 of row g: fp16 high and low parts
   int lim[NB][2], lo[NB][2];  // visible keys of rows 8 nb + 2t, + 1
   int min_lim = 0x7fffffff, max_lo = 0;
   bool bad_q = false;
+  uint4 raw[NB][G];
+  float largest = 0.0f;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int row = nb * 8 + g;
@@ -180,53 +183,11 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     const int tr = real ? token_of(row) : 0;
     const uint16_t *src = a.p.q + (static_cast<int64_t>(q0 + tok0 + tr) * a.p.hq + h * a.qpk +
                                    (real ? row - tr * a.qpk : 0)) * D;
-    float sums[G];
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (real) v = *reinterpret_cast<const uint4 *>(src + gr * 32 + t * 8);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-        bad_q |= half2_nonfinite(pack_half2(x[2 * i], x[2 * i + 1]));
-      }
-      qb[nb][gr][0][0] = pack_half2(x[0], x[4]);
-      qb[nb][gr][0][1] = pack_half2(x[1] * 0.0625f, x[5] * 0.0625f);
-      qb[nb][gr][1][0] = pack_half2(x[2], x[6]);
-      qb[nb][gr][1][1] = pack_half2(x[3] * 0.0625f, x[7] * 0.0625f);
-      sums[gr] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+      raw[nb][gr] = make_uint4(0u, 0u, 0u, 0u);
+      if (real) raw[nb][gr] = *reinterpret_cast<const uint4 *>(src + gr * 32 + t * 8);
     }
-    float mine[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int gr = 0; gr < G; ++gr) {
-      sums[gr] += __shfl_xor_sync(0xffffffffu, sums[gr], 1);
-      sums[gr] += __shfl_xor_sync(0xffffffffu, sums[gr], 2);
-      // over 32, so that 32 values of the fp16 range stay inside it
-      if (gr >> 1 == t) mine[gr & 1] = sums[gr] * 0.03125f;
-    }
-    const float hi0 = __half2float(__float2half_rn(mine[0])), hi1 = __half2float(__float2half_rn(mine[1]));
-    qs[nb][0] = pack_half2(hi0, hi1);
-    qs[nb][1] = pack_half2(mine[0] - hi0, mine[1] - hi1);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = nb * 8 + 2 * t + c;
-      // rows past the last take its keys, so that their arithmetic stays finite
-      const int i = tok0 + token_of(r < n_rows ? r : n_rows - 1);
-      lim[nb][c] = a.p.causal ? seq_len - q_len + i : seq_len - 1;
-      lo[nb][c] = a.p.window > 0 ? max(0, lim[nb][c] - a.p.window + 1) : 0;
-      min_lim = min(min_lim, lim[nb][c]);
-      max_lo = max(max_lo, lo[nb][c]);
-    }
-  }
-  if (__any_sync(0xffffffffu, bad_q) && warp == 0 && lane == 0 && sigma == 0)
-    flag_status(a.status, PA_DEV_BAD_Q);
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
-    max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
   }
 
   // ---- this warp's copies: block b of the segment for b % 4 == warp
@@ -294,17 +255,73 @@ __global__ void __launch_bounds__(kWarps * 32, resident_blocks(D, NB == 2)) attn
     }
     cp_async_commit();
   };
+  // the first copies go out while q is on its way
+#pragma unroll
+  for (int i = 0; i < C::kStages - KB; ++i) issue(i);
+
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) largest = fmaxf(largest, largest_of(raw[nb][gr]));
+  const QueryScale by = query_scale(warp_largest(largest), a.scale_log2);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float sums[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      const uint4 v = raw[nb][gr];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]) * by.up;
+        x[2 * i + 1] = bf16_hi(w[i]) * by.up;
+        bad_q |= half2_nonfinite(pack_half2(x[2 * i], x[2 * i + 1]));
+      }
+      qb[nb][gr][0][0] = pack_half2(x[0], x[4]);
+      qb[nb][gr][0][1] = pack_half2(x[1] * 0.0625f, x[5] * 0.0625f);
+      qb[nb][gr][1][0] = pack_half2(x[2], x[6]);
+      qb[nb][gr][1][1] = pack_half2(x[3] * 0.0625f, x[7] * 0.0625f);
+      sums[gr] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    }
+    float mine[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+      sums[gr] += __shfl_xor_sync(0xffffffffu, sums[gr], 1);
+      sums[gr] += __shfl_xor_sync(0xffffffffu, sums[gr], 2);
+      // over 32, so that 32 values of the fp16 range stay inside it
+      if (gr >> 1 == t) mine[gr & 1] = sums[gr] * 0.03125f;
+    }
+    const float hi0 = __half2float(__float2half_rn(mine[0])), hi1 = __half2float(__float2half_rn(mine[1]));
+    qs[nb][0] = pack_half2(hi0, hi1);
+    qs[nb][1] = pack_half2(mine[0] - hi0, mine[1] - hi1);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nb * 8 + 2 * t + c;
+      // rows past the last take its keys, so that their arithmetic stays finite
+      const int i = tok0 + token_of(r < n_rows ? r : n_rows - 1);
+      lim[nb][c] = a.p.causal ? seq_len - q_len + i : seq_len - 1;
+      lo[nb][c] = a.p.window > 0 ? max(0, lim[nb][c] - a.p.window + 1) : 0;
+      min_lim = min(min_lim, lim[nb][c]);
+      max_lo = max(max_lo, lo[nb][c]);
+    }
+  }
+  if (__any_sync(0xffffffffu, bad_q) && warp == 0 && lane == 0 && sigma == 0)
+    flag_status(a.status, PA_DEV_BAD_Q);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
+    max_lo = max(max_lo, __shfl_xor_sync(0xffffffffu, max_lo, o));
+  }
+
   float m_used[NB][2], l[NB][2];  // rows 2t, 2t + 1 (log2 units; l: this lane's share)
   float o[NB][G][2][4], oz[NB][4];
-  const float c1 = a.scale_log2 * 0x1p24f;  // of sum_g s_g (q c 2^-24)
-  const float c2 = a.scale_log2 * 32.0f;    // of sum_g z_g (q sum / 32)
+  const float c1 = by.codes, c2 = by.zeros;
   float m_safe[NB][2];  // m_used, 0 before the first key
   const int key_r0 = perm16(g), key_r1 = perm16(g + 8);
   // (m_used: the maximum less the lift, which p, l and o are taken against)
   float lift = kLift;
 again:
-#pragma unroll
-  for (int i = 0; i < C::kStages - KB; ++i) issue(i);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -527,6 +544,8 @@ again:
     if (__any_sync(0xffffffffu, nan != nan)) {
       lift = lift > 0.0f ? 0.0f : -kMargin;
       __syncwarp();
+#pragma unroll
+      for (int i = 0; i < C::kStages - KB; ++i) issue(i);
       goto again;
     }
   }

@@ -61,6 +61,33 @@ __device__ __forceinline__ void flag_bad_sequences(const Q4Args &a, int item, in
   }
 }
 
+// Queries enter the products as fp16.  They are multiplied by the power of two that brings the
+// largest of a block to 2^15 .. 2^16 (32 of them over 32 stay within fp16), which the scores'
+// factors take back: bf16 values down to 2^-28 of the largest keep their bits, as q and as q / 16.
+// Of a block with values from 65520 on (flagged) the power is 1.
+struct QueryScale {
+  float up, codes, zeros;  // of q; of sum_g s_g (q c 2^-24) and of sum_g z_g (q sum / 32)
+};
+__device__ __forceinline__ QueryScale query_scale(float largest, float scale_log2) {
+  const int e = static_cast<int>(__float_as_uint(fminf(largest, 65504.0f)) >> 23) - 127;
+  const int f = min(15 - e, 120);
+  const auto power = [](int x) { return __uint_as_float(static_cast<uint32_t>(x + 127) << 23); };
+  return {power(f), scale_log2 * power(24 - f), scale_log2 * power(5 - f)};
+}
+// The largest |x| of eight bf16 values (a NaN is passed over).
+__device__ __forceinline__ float largest_of(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmax3(m, fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i])));
+  return m;
+}
+
+// The largest of a warp's values >= 0, whose bits are in their order.
+__device__ __forceinline__ float warp_largest(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+
 // The tcgen05 kernel of a call (D 128, blocks of up to kTcRows rows); its triples and results are
 // those of the mma.sync kernel.
 constexpr int kTcRows = 64;

@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
       if (ok && !__all_sync(0xffffffffu, mbar_test(bar(b), parity)))
         ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity));
     };
+    QueryScale by;
     // ---- q: a row's group a thread, octets as the codes' words have them: 0, 4, 1, 5, 2, 6, 3, 7
     {
       const int row = tid & 63, g = tid >> 6;
@@ -258,18 +259,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
       const int tr = real ? (row * a.qpk_inverse) >> 16 : 0;
       const uint16_t *src = a.p.q + (static_cast<int64_t>(q0 + tok0 + tr) * a.p.hq + h * a.qpk +
                                      (real ? row - tr * a.qpk : 0)) * kD + g * 32;
+      uint4 v[4];
+      float largest = 0.0f;
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        v[o] = make_uint4(0u, 0u, 0u, 0u);
+        if (real) v[o] = *reinterpret_cast<const uint4 *>(src + o * 8);
+      }
+#pragma unroll
+      for (int o = 0; o < 4; ++o) largest = fmaxf(largest, largest_of(v[o]));
+      largest = warp_largest(largest);
+      if (lane == 0) sts_f32(smem + kPartOff + warp * 4, largest);
+      softmax_sync();
+      largest = warp_largest(lds_f32(smem + kPartOff + (lane % kSoftmaxWarps) * 4));
+      by = query_scale(largest, a.scale_log2);
       bool bad_q = false;
       float sum = 0.0f;
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (real) v = *reinterpret_cast<const uint4 *>(src + o * 8);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {v[o].x, v[o].y, v[o].z, v[o].w};
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[2 * i] = bf16_lo(w[i]);
-          x[2 * i + 1] = bf16_hi(w[i]);
+          x[2 * i] = bf16_lo(w[i]) * by.up;
+          x[2 * i + 1] = bf16_hi(w[i]) * by.up;
           bad_q |= half2_nonfinite(pack_half2(x[2 * i], x[2 * i + 1]));
         }
         sts128(smem + kQOff + tc::sw128_chunk(row, g * 4 + o, kN),
@@ -293,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
     softmax_sync();
 
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + r_first;
-    const float c1 = a.scale_log2 * 0x1p24f, c2 = a.scale_log2 * 32.0f;
+    const float c1 = by.codes, c2 = by.zeros;
     uint64_t l2[kHalf / 2];
 #pragma unroll
     for (int i = 0; i < kHalf / 2; ++i) l2[i] = 0;

@@ -131,6 +131,38 @@ def test_the_largest_scales(cuda_device, hq, hk, d, count, splits):
     assert ((lse.double() - z).abs() <= eps + 2.0 ** -20 * (1 + z.abs())).all()
 
 
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (8, 2, 128), (6, 2, 256), (16, 1, 128)])
+@pytest.mark.parametrize("count", [1, 3, 70])
+@pytest.mark.parametrize("size", [1e-30, 1e-5, 1e-3, 1.0, 1e4])
+def test_queries_of_all_sizes(cuda_device, hq, hk, d, count, size):
+    """Queries whose size a softmax_scale takes back: no bit of theirs is lost.
+
+    A score: exact products summed in fp32 (32 of a group on the tensor core, then the groups): under
+    2^-16 of scale * sum |q| (|c s| + |z|).  The rest as in the other tests, p and the values
+    in fp16 (2^-11 each)."""
+    H.ensure_built()
+    dev, lens = cuda_device, [300, 90]
+    g = torch.Generator().manual_seed(d + count)
+    key, value = (torch.randn((sum(lens), hk, d), generator=g) for _ in range(2))
+    q = (torch.randn((2 * count, hq, d), generator=g) * size).bfloat16().to(dev)
+    scale = d ** -0.5 / size
+    cpu, table = _filled(lens, hk, d, 16, key, value)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=dev)
+    out, lse = _lib.paged_attention_q4(q, *[x.to(dev) for x in cpu], _starts([count] * 2, dev), _i32(lens, dev),
+                                       table.to(dev), count, 300, softmax_scale=scale, workspace=ws)
+    assert _lib.check_status(ws) == 0
+    for s, n in enumerate(lens):
+        span = slice(s * count, (s + 1) * count)
+        parts = [x.to(dev) for x in _q4.rows64(cpu, table[s], n)]
+        ref, z, vc, vz, _, reach = _q4.attention64(q[span], parts, n - count, scale=scale)
+        eps = 2.0 ** -16 * reach
+        tol = (2.0 ** -8 * ref.abs() + (1.01 * 2.0 ** -10 + 2 * eps[..., None] + 2.0 ** -20) * (vc + vz)
+               + n * 2.0 ** -35 * (15 + float((parts[2].abs() + parts[3].abs()).max())))
+        err = (out[span].double() - ref).abs()
+        assert (err <= tol).all(), (s, float((err - tol).max()), float(err.max()))
+        assert ((lse[span].double() - z).abs() <= eps + 2.0 ** -20 * (1 + z.abs())).all(), s
+
+
 # ---------------------------------------------------------------- bounds out of range
 
 # starts of sequences over 40 rows: a falling one last, in the middle, beside many, and none within
