@@ -50,6 +50,7 @@ constexpr float kMargin = 2.0f;  // log2 of the largest p over that of the maxim
 constexpr float kLift = 10.0f;   // log2 of p at the maximum
 
 // Ring depth by the bytes of a 16-key block (20 D): what keeps about 100 KB an SM in flight.
+constexpr int ring_stages(int d) { return d == 256 ? 4 : 6; }
 template <int D>
 struct Q4Cfg {
   static constexpr int G = D / 32;
@@ -58,7 +59,7 @@ struct Q4Cfg {
   static constexpr int kV = kKs + 16 * G * 4;        // V codes
   static constexpr int kVs = kV + 16 * kRow;         // V scales [G][16], zeros [G][16]
   static constexpr int kBlock = kVs + 16 * G * 4;    // 20 D bytes
-  static constexpr int kStages = D == 256 ? 4 : 6;
+  static constexpr int kStages = ring_stages(D);
 };
 
 // D = A B, m16n8k16, fp16 inputs, fp32 accumulators, no addend.
@@ -119,12 +120,18 @@ __device__ __forceinline__ uint32_t v_place(int r, int c) {
   return (i * 4 + t) * (D / 2) + (c ^ x) * 16;
 }
 
-// Thread blocks an SM, by registers and by the rings.
-constexpr int resident_blocks(int d, bool wide) { return wide ? 2 : d == 64 ? 5 : 3; }
+// Thread blocks an SM: what the registers allow, and the rings (of the 228 KB of an SM's shared
+// memory, of which a block takes 1 KB more than its own): two at D 256.
+constexpr int resident_blocks(int d, bool wide) {
+  const int by_registers = wide ? 2 : d == 64 ? 5 : 3;
+  const int by_rings = 228 * 1024 / (kWarps * ring_stages(d) * 20 * d + 1024);
+  return by_registers < by_rings ? by_registers : by_rings;
+}
 // Two blocks of keys at a time where that pays: the chain from a block's scores to its products
 // is long, and a second one fills its gaps (D 128, 32 sequences x 6000 keys, 3 x 4 rows: 39 us, 50
 // with one at three thread blocks an SM).  At D 64 the registers of 16 rows are better spent
-// otherwise (64 x 4096 keys, 16 q heads a kv head: 23 us, 27 with two), D 256 has none left.
+// otherwise (64 x 4096 keys, 16 q heads a kv head: 23 us, 27 with two); at D 256 one block of keys
+// takes 232 of 255.
 constexpr int keys_blocks(int d, bool wide) { return d == 128 || (d == 64 && !wide) ? 2 : 1; }
 
 template <int D, int BS, int NB>
@@ -751,7 +758,10 @@ std::pair<int64_t, int64_t> blocks_and_places(int32_t num_seqs, int32_t num_toke
 // resident) are split until about three times as many stand in line, in segments of at least
 // 512 keys (256 where very few stand); where that limit leaves fewer than 2.5 rounds, one
 // full round: 1 x 131072 keys (8 kv heads, D 128, caches cold) takes 379 us in 2 segments, 60 in
-// 16, 54 in 57 (456 blocks on 456 places), 65 in 64.  Blocks that fill it are split at 2048 keys,
+// 16, 54 in 57 (456 blocks on 456 places), 65 in 64.  Eights at D 256 stand two an SM: 4.5 times the
+// places in line, 512 keys at least (1 x 131072 keys 84 us in 38 segments, 304 blocks on 304 places,
+// and 103 in 57; 24 x up to 32768 keys 210 us in 8 segments, 231 in 5; 1 x 8192 keys 18 us in 16
+// segments, 22 in 32; 8 x 8192 would be 36 us in 7, 41 as it is).  Blocks that fill it are split at 2048 keys,
 // so that the last of long sequences do not run alone: 64 x up to 8192 keys 87 us in 4 segments,
 // 105 in one; 128 x up to 2048 keys 56 us in one, 62 in 4 (the join is another launch and trip
 // to memory).
@@ -765,7 +775,10 @@ int32_t q4_auto_splits(int32_t num_seqs, int32_t num_tokens, int32_t hq, int32_t
   const int64_t keys = std::max<int64_t>(1, max_seq_len);
   int64_t ns = (keys + 2047) / 2048;
   if (4 * blocks < 3 * places) {
-    ns = std::min<int64_t>({(3 * places + blocks - 1) / blocks, keys / (8 * blocks < places ? 256 : 512), kMaxSegments});
+    const bool eights = d == 256 && q4_block_tokens(hq / hk, max_query_len, d) * (hq / hk) <= 8;
+    const int64_t line = eights ? 9 * places / 2 : 3 * places;
+    const int64_t least = 8 * blocks < places && !eights ? 256 : 512;
+    ns = std::min<int64_t>({(line + blocks - 1) / blocks, keys / least, kMaxSegments});
     if (ns * blocks > places && 2 * ns * blocks < 5 * places) ns = places / blocks;
   } else {
     ns = std::min(ns, (16 * places + blocks - 1) / blocks);
