@@ -707,9 +707,11 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
  * head_dim 64, 128, 256; num_q_heads a multiple of num_kv_heads, at most 128 times.
  * A sequence whose bounds fall or are out of range is not written and flagged PA_DEV_BAD_SEQ
  * (one without query tokens asks for nothing); rows of tokens no sequence owns are not
- * written.  What other sequences' rows hold never
- * reaches a result; an infinity or NaN in a value row may reach queries of its own
- * sequence up to 15 keys before the first that sees it.  Asynchronous.
+ * written.  What other sequences' rows hold never reaches a result.  An infinity or NaN
+ * in a value row may reach queries of its own sequence that do not see its key (their
+ * weight is a zero, but 0 times infinity is not): with n = 128 / (q heads a kv head) query
+ * tokens a tile, rounded down, up to n + 14 keys behind a query's last key, and with a
+ * window up to 2 n + 126 (head_dim 256: n + 126) in front of its first.  Asynchronous.
  * Numerics: exact products summed in fp32, softmax in fp32, p rounded to bf16 for its
  * product with V (fp32 sums), the output rounded to bf16.
  */

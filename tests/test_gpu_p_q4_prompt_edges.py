@@ -241,3 +241,50 @@ def test_cached_bounds_that_are_flagged(cuda_device, hq, hk, d, most, starts):
     _lib.paged_attention_q4(q, *cache, _i32([0, 0, 2, 2], dev), _i32([-5, 60, 0], dev), table[:1].repeat(3, 1), most,
                             60, workspace=ws)
     assert _lib.check_status(ws) == 0
+
+
+# ----------------------------------------------------------------- what reaches what
+
+@pytest.mark.parametrize("hq,hk,d", [(2, 2, 64), (4, 1, 64), (3, 3, 128), (8, 2, 128), (16, 1, 128), (2, 2, 256),
+                                     (6, 1, 256), (100, 1, 128)])
+@pytest.mark.parametrize("window", [0, 70, 200])
+@pytest.mark.parametrize("prefix", [0, 77])
+def test_which_outputs_a_value_reaches(cuda_device, hq, hk, d, window, prefix):
+    """A value row that holds no number reaches the queries that see its key, and of those that do
+    not only queries of the same tile of 128 / (q heads a kv head) query tokens, up to 15
+    keys in front of what its last query sees, and (with a window) of the same one or two
+    tiles, back to the 128 keys in which the window of their first query begins."""
+    H.ensure_built()
+    dev, n = cuda_device, 600
+    g = torch.Generator().manual_seed(d + hq)
+    q = torch.randn((n, hq, d), generator=g).bfloat16().to(dev)
+    k, v = (torch.randn((n + prefix, hk, d), generator=g).bfloat16().to(dev) for _ in range(2))
+    cu_q, cu_k = _i32([0, n], dev), _i32([0, n + prefix], dev)
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev)  # one segment
+
+    def call(values):
+        r = _lib.prompt_attention(q, k, values, cu_q, n, cu_seqlens_k=cu_k, max_key_len=n + prefix,
+                                  sliding_window=window, workspace=ws)
+        assert _lib.check_status(ws) == 0
+        return r
+
+    want, want_lse = call(v)
+    tile = 128 // (hq // hk)
+    block = tile * (1 if d == 256 else 2)
+    for j in (0, 130, 301, 447, n + prefix - 1):
+        for bad in (float("nan"), float("inf")):
+            values = v.clone()
+            values[j] = bad
+            out, lse = call(values)
+            assert torch.equal(lse, want_lse)
+            finite = torch.isfinite(out).flatten(1).any(1).tolist()
+            same = (out == want).flatten(1).all(1).tolist()
+            for i in range(n):
+                at = prefix + i  # the last key of query i
+                if j <= at and (not window or j > at - window):
+                    assert not finite[i], (j, i)
+                    continue
+                end = prefix + min(i // tile * tile + tile, n)  # behind the last key of its tile
+                first = max(0, prefix + i // block * block - window + 1) if window else 0
+                if j >= -(-end // 16) * 16 or j < first // 128 * 128:
+                    assert same[i], (j, i)
