@@ -288,3 +288,60 @@ def test_which_outputs_a_value_reaches(cuda_device, hq, hk, d, window, prefix):
                 first = max(0, prefix + i // block * block - window + 1) if window else 0
                 if j >= -(-end // 16) * 16 or j < first // 128 * 128:
                     assert same[i], (j, i)
+
+
+# ----------------------------------------------------------------- large groups
+
+def _prompts(device, hq, hk, d, q_lens, k_lens, sinks=None, window=0, room=None):
+    g = torch.Generator().manual_seed(hq + d)
+    t, n = sum(q_lens), sum(k_lens)
+    q = torch.randn((t, hq, d), generator=g).bfloat16().to(device)
+    k, v = (torch.randn((n, hk, d), generator=g).bfloat16().to(device) for _ in range(2))
+    most = max(q_lens), max(k_lens)
+    size = _lib.prompt_attention_workspace_size(len(q_lens), t, n, hq, hk, d, *most)
+    ws = torch.full((size if room is None else room,), 0xFF, dtype=torch.uint8, device=device)
+    ws[:4] = 0
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full((t, hq), float("nan"), device=device)
+    _lib.prompt_attention(q, k, v, _starts(q_lens, device), most[0], cu_seqlens_k=_starts(k_lens, device),
+                          max_key_len=most[1], sinks=sinks, sliding_window=window, out=out, lse=lse, workspace=ws)
+    assert _lib.check_status(ws) == 0
+    at = ak = 0
+    for a, b in zip(q_lens, k_lens):
+        kk, vv = k[ak:ak + b].double(), v[ak:ak + b].double()
+        ref, z, va, _, _, reach = _q4.attention64(q[at:at + a], (kk, 0 * kk, vv, 0 * vv), b - a, True, window, sinks)
+        eps = d * 2.0 ** -23 * reach  # D exact products summed in fp32
+        tol = 2.0 ** -8 * ref.abs() + (1.01 * 2.0 ** -8 + 2 * eps[..., None] + 2.0 ** -20) * va + 1e-30
+        got = out[at:at + a].double()
+        assert ((got - ref).abs() <= tol).all(), (a, b)
+        empty = torch.isinf(z)
+        assert torch.equal(torch.isinf(lse[at:at + a]), empty)
+        e = torch.where(empty, torch.zeros_like(z), (lse[at:at + a].double() - z).abs())
+        assert (e <= eps + 2.0 ** -20 * (1 + torch.where(empty, torch.zeros_like(z), z.abs()))).all(), (a, b)
+        at, ak = at + a, ak + b
+    return size
+
+
+@pytest.mark.parametrize("hq,hk", [(32, 2), (65, 1), (100, 1), (128, 1)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("count", [1, 5, 32, 33])
+def test_prompts_of_large_groups(cuda_device, hq, hk, d, count):
+    """Tiles of 8 tokens down to one, sequences in order of their keys and (33) in their own."""
+    H.ensure_built()
+    dev = cuda_device
+    g = torch.Generator().manual_seed(count + hq)
+    q_lens = [70] if count == 1 else torch.randint(0, 9, (count,), generator=g).tolist()
+    k_lens = [90] if count == 1 else [max(0, a + int(b)) for a, b in zip(q_lens, torch.randint(-2, 200, (count,),
+                                                                                              generator=g))]
+    sinks = (torch.randn(hq, generator=g) * 2).to(dev)
+    for kw in ({}, dict(sinks=sinks, window=40)):
+        _prompts(dev, hq, hk, d, q_lens, k_lens, room=256, **kw)
+
+
+@pytest.mark.parametrize("hq,hk", [(16, 1), (65, 1), (100, 1), (128, 1)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompts_of_large_groups_in_segments(cuda_device, hq, hk, d):
+    H.ensure_built()
+    for q_lens, k_lens, window in (([3], [3000], 0), ([2, 0, 1], [2500, 7, 1300], 0), ([4, 1], [3001, 2], 700)):
+        size = _prompts(cuda_device, hq, hk, d, q_lens, k_lens, window=window)
+        assert size > 256 + sum(q_lens) * hq * (d + 2) * 4  # more than one segment
