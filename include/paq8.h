@@ -641,6 +641,9 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  *                  blocks of 16 rows (tokens x q heads of a kv head; head_dim 128 above 64
  *                  rows: of 64), each of which reads its keys: pa_kv_load_q4 and
  *                  pa_prompt_attention are the faster way for chunks of hundreds of tokens.
+ *                  It picks the kernel for every sequence of the call: single tokens beside
+ *                  a long query take its blocks, at its time and with its roundings (below);
+ *                  they are better off in a call of their own.
  *   flags          0 or PA_ATTN_NON_CAUSAL.
  * An infinity or NaN in a value row may reach the results of its own sequence's other
  * queries in the call.  Calls that may overlap on the GPU need workspaces of their own.
@@ -652,7 +655,7 @@ size_t pa_paged_attention_q4_workspace_size(int32_t num_seqs, int32_t num_tokens
  * below 2.4e-4 to steps of 2.4e-7 where they pass 16376); sums in fp32, output bf16.  At
  * head_dim 128 with more than 64 rows (max_query_len times the q heads of a kv head) p
  * and the values code * scale + zero are rounded to fp16 instead (a value past 65504 to
- * an infinity).
+ * an infinity), of all sequences of the call.
  */
 pa_status pa_paged_attention_q4(const void *q, const void *k_cache, const void *k_scale,
                                 const void *v_cache, const void *v_scale,

@@ -1046,7 +1046,9 @@ def paged_attention_q4(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, seq_
                        return_lse: bool = True, causal: bool = True, sinks=None,
                        sliding_window: int = 0):
     """paged_attention over the 4-bit format (pa_paged_attention_q4): arguments and
-    results as paged_attention, for any query lengths.  ``workspace``: optional uint8
+    results as paged_attention, for any query lengths.  ``max_query_len`` picks the kernel
+    for all sequences: keep single tokens and long queries in calls of their own (they are
+    faster there, and keep the codes exact).  ``workspace``: optional uint8
     CUDA tensor of ``paged_attention_q4_workspace_size`` bytes whose first 4 bytes are zero; a
     smaller one takes fewer key segments."""
     dev = q.get_device()
