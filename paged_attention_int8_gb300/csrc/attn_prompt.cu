@@ -92,30 +92,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool n_major) {
   return tc::idesc_f16(m, n) | (1u << 7) | (1u << 10) | (n_major ? 1u << 16 : 0u);
 }
 
-// Matrix descriptor of an N-major operand in the 128-byte swizzle: 64 channels (128 bytes)
-// of a key are a row, 8 keys 1024 bytes, the next 64 channels `next` bytes further.
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t next) {
-  uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(next >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// One test of a barrier's phase, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // A box of a tiled map at (x, y, z[, w]) into shared memory.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
                                             uint32_t bar) {
@@ -438,7 +414,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
       const uint64_t q_desc = tc::desc_sw128(smem_base + C::kQOff);
       const uint64_t k_desc = tc::desc_sw128(smem_base);
-      const uint64_t v_desc = desc_n_major(smem_base, C::kVKeys * 128);
+      const uint64_t v_desc = tc::desc_mn_major(smem_base, C::kVKeys * 128);
       // (a phase that is complete, the common case, costs a test half of what a waiting test
       // does; the tensor core's queue holds five MMAs, 320 cycles, to hide it behind)
       auto wait = [&](int i, uint32_t parity) {

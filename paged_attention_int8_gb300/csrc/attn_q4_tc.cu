@@ -89,30 +89,8 @@ static_assert(kKCol + 2 * (kD / 2) <= 512, "TMEM");
 __host__ __device__ constexpr uint32_t idesc(int n, bool a_m, bool b_n) {
   return tc::idesc_f16(128, n) | (a_m ? 1u << 15 : 0u) | (b_n ? 1u << 16 : 0u);
 }
-// Matrix descriptor of such an operand in the 128-byte swizzle: 64 elements (128 bytes) of a key
-// are a row, 8 keys 1024 bytes, the next 64 elements `next` bytes further.
-__device__ __forceinline__ uint64_t desc_contiguous(uint32_t addr, uint32_t next) {
-  uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(next >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// One test of a barrier's phase, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t b, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(b), "r"(parity)
-      : "memory");
-  return done != 0;
-}
 // The softmax warps' own barrier, and their vote.
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
@@ -657,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q4_tc_kernel(const __grid_co
         constexpr uint32_t id_qk = idesc(kN, false, false), id_pv = idesc(kN, true, true);
         const uint64_t q_desc = tc::desc_sw128(smem + kQOff), qs_desc = tc::desc_sw128(smem + kQsOff);
         const uint64_t z_desc = tc::desc_sw128(smem + kZOff);
-        const uint64_t v_desc = desc_contiguous(smem + kVOff, kKeys * 128);
-        const uint64_t p_desc = desc_contiguous(smem + kPOff, kPBytes);
+        const uint64_t v_desc = tc::desc_mn_major(smem + kVOff, kKeys * 128);
+        const uint64_t p_desc = tc::desc_mn_major(smem + kPOff, kPBytes);
         auto wait = [&](int i, uint32_t parity) {
           return mbar_test(bar(i), parity) || (ok = mbar_wait(bar(i), parity));
         };

@@ -23,6 +23,18 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t smem_addr) {
   return d;
 }
 
+// Matrix descriptor of an operand whose M or N dimension is the contiguous one, in the 128-byte
+// swizzle: 64 of its 16-bit elements (128 bytes) of one k are a row, 8 k 1024 bytes, the next 64
+// elements `next` bytes further (the leading byte offset).
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t smem_addr, uint32_t next) {
+  uint64_t d = static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(next >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
 // Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, both
 // operands K-major, M x N.  Fields: D format [4,6) (1 = f32), A/B format
 // [7,10)/[10,13) (0 = f16), A/B major [15]/[16] (0 = K), N >> 3 [17,23),
