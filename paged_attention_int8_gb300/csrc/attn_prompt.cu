@@ -371,8 +371,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         }
         ++count;
       }
-      // in the batch's order no item need be that of a sequence with bad bounds: item n looks at
-      // sequence n (and n + num_items, ...)
+      // ---- the next block's number: asked for when this item's copies are on their way (at its
+      // start a block would hold the next while others are idle)
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(kBarNext), 16);
+        ask_for_block(answer, bar(kBarNext));
+      }
+      // (in the batch's order no item need be that of a sequence with bad bounds: item n looks at
+      // sequence n (and n + num_items, ...))
       if (!ranked && it.h == 0 && it.segment == 0) {
         const int64_t n = rest % a.num_items;
         for (int64_t s = n + int64_t{lane} * a.num_items; s < a.p.num_seqs; s += int64_t{32} * a.num_items) {
@@ -380,12 +386,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           const int len = a.p.cu_q[s + 1] - q0;
           if (len != 0 && !fits(q0, len, k0, a.p.cu_k[s + 1] - k0)) flag_status(a.status, PA_DEV_BAD_SEQ);
         }
-      }
-      // ---- the next block's number: asked for when this item's copies are on their way (at its
-      // start a block would hold the next while others are idle)
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(kBarNext), 16);
-        ask_for_block(answer, bar(kBarNext));
       }
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(kBarNext), asked & 1));
       ++asked;

@@ -308,12 +308,21 @@ def _prompts(device, hq, hk, d, q_lens, k_lens, sinks=None, window=0, room=None)
     assert _lib.check_status(ws) == 0
     at = ak = 0
     for a, b in zip(q_lens, k_lens):
-        kk, vv = k[ak:ak + b].double(), v[ak:ak + b].double()
-        ref, z, va, _, _, reach = _q4.attention64(q[at:at + a], (kk, 0 * kk, vv, 0 * vv), b - a, True, window, sinks)
+        # in 64 bits, all heads at once
+        qq = q[at:at + a].double()
+        kk, vv = (x[ak:ak + b].double().repeat_interleave(hq // hk, 1) for x in (k, v))
+        key, pos = torch.arange(b, device=device)[None], b - a + torch.arange(a, device=device)[:, None]
+        seen = (key <= pos) & (key > pos - (window or b + 1))
+        x = torch.einsum("ihd,jhd->hij", qq, kk) * d ** -0.5
+        reach = torch.einsum("ihd,jhd->hij", qq.abs(), kk.abs()).masked_fill(~seen, 0) * d ** -0.5
+        reach = torch.cat([reach, reach.new_zeros((hq, a, 1))], 2).amax(2).T
+        extra = x.new_full((hq, a, 1), -math.inf) if sinks is None else sinks.double().view(hq, 1, 1).expand(hq, a, 1)
+        z = torch.logsumexp(torch.cat([x.masked_fill(~seen, -math.inf), extra], 2), 2).T
+        p = torch.exp(x - z.T[..., None]).masked_fill(~seen, 0)
+        ref, va = (torch.einsum("hij,jhd->ihd", p, y) for y in (vv, vv.abs()))
         eps = d * 2.0 ** -23 * reach  # D exact products summed in fp32
         tol = 2.0 ** -8 * ref.abs() + (1.01 * 2.0 ** -8 + 2 * eps[..., None] + 2.0 ** -20) * va + 1e-30
-        got = out[at:at + a].double()
-        assert ((got - ref).abs() <= tol).all(), (a, b)
+        assert ((out[at:at + a].double() - ref).abs() <= tol).all(), (a, b)
         empty = torch.isinf(z)
         assert torch.equal(torch.isinf(lse[at:at + a]), empty)
         e = torch.where(empty, torch.zeros_like(z), (lse[at:at + a].double() - z).abs())
