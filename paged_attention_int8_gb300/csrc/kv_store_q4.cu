@@ -3,8 +3,9 @@
 //   code = clamp(round_half_away((x - lo) / s), 0, 15)   (the IEEE fp32 quotient)
 //   scale = fp16(s), zero = fp16(lo), to nearest even.
 //
-// Bound by HBM: 4 D bytes read and D + D / 4 written a (token, kv head); in practice by
-// the issue of instructions (packed fp32, one reciprocal of 23 bits a half group).  A
+// Bound by HBM: 4 D bytes read and D + D / 4 written a (token, kv head); in practice by its
+// latencies (55 % of the issue slots, 39 % of HBM: loads, arithmetic and small writes one
+// behind another at half the warps of an SM).  Packed fp32, one reciprocal of 23 bits a half group.  A
 // thread takes 16 channels (two 16-byte loads), two neighbouring lanes a group (one
 // exchange for its extremes); its codes are two words of a K row or four halves of a V row.
 // Several pieces a thread keep their loads in flight together.
