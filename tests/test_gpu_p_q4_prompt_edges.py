@@ -80,6 +80,35 @@ def test_a_key_that_is_no_number(cuda_device, hq, hk, d, count, splits, sink):
 
 
 @pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 2, 128), (6, 2, 256)])
+@pytest.mark.parametrize("q_len,k_len", [(300, 300), (9, 3000)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_key_of_a_prompt_that_is_no_number(cuda_device, hq, hk, d, q_len, k_len, bad):
+    """As test_a_key_that_is_no_number; the second sizes go in segments.  (Infinite keys: the queries
+    have both signs, so that their scores are inf - inf.)"""
+    H.ensure_built()
+    dev = cuda_device
+    g = torch.Generator().manual_seed(d)
+    q = torch.randn((q_len, hq, d), generator=g).bfloat16().to(dev)
+    k, v = (torch.randn((k_len, hk, d), generator=g).bfloat16().to(dev) for _ in range(2))
+    assert _lib.prompt_attention_workspace_size(1, q_len, k_len, hq, hk, d, q_len, k_len) > 256 or q_len == k_len
+
+    def call(keys):
+        return _lib.prompt_attention(q, keys, v, _i32([0, q_len], dev), q_len, cu_seqlens_k=_i32([0, k_len], dev),
+                                     max_key_len=k_len)
+
+    want, want_lse = call(k)
+    assert torch.isfinite(want).all() and torch.isfinite(want_lse).all()
+    at = k_len - 5
+    k[at, 0] = bad
+    out, lse = call(k)
+    first, heads = q_len - 5, slice(0, hq // hk)
+    assert torch.isnan(out[first:, heads]).all() and torch.isnan(lse[first:, heads]).all()
+    assert torch.equal(out[:first], want[:first]) and torch.equal(lse[:first], want_lse[:first])
+    assert torch.equal(out[:, heads.stop:], want[:, heads.stop:])
+    assert torch.equal(lse[:, heads.stop:], want_lse[:, heads.stop:])
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (8, 2, 128), (6, 2, 256)])
 def test_scores_of_minus_infinity(cuda_device, hq, hk, d):
     """Weights that are all zero give 0 and -inf in one segment as in several."""
     H.ensure_built()
