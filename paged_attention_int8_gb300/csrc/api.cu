@@ -923,7 +923,8 @@ pa_status pa_kv_store_q4(const void *key, int64_t key_token_stride, const void *
   if (misaligned(7, {slot_mapping}))
     return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
   if (misaligned(3, {status})) return fail(PA_ERR_INVALID_ARG, "status must be 4-byte aligned");
-  if (static_cast<int64_t>(num_tokens) * num_kv_heads >= (int64_t{1} << 31) / (head_dim / 8) - 4096)
+  // (16 channels a piece: the kernel's piece numbers stay below 2^30)
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads >= (int64_t{1} << 34) / head_dim)
     return fail(PA_ERR_UNSUPPORTED, "num_tokens * num_kv_heads * head_dim must be < 2^34: split the tokens");
   paq8::KvStoreQ4 p;
   p.key = static_cast<const uint16_t *>(key);
